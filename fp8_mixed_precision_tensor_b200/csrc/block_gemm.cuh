@@ -1,0 +1,437 @@
+// block_gemm.cuh -- FP8 products whose operands carry one power-of-two scale
+// per block of 128 along the reduction, on the 5th-generation tensor cores.
+//
+//   C[r, c] = sum_b 2^(sa[r,b] + sb[c,b] - 254) sum_{k in block b} A(r, k) B(c, k)   (+ bias)
+//
+// tcgen05.mma kind::mxf8f6f4 takes a scale byte per row and 32 elements of
+// the reduction from tensor memory and applies it while it multiplies, at the
+// rate of the unscaled FP8 product.  A block of 128 is four such groups with
+// the same byte: the packed scale words (see block_scale.cuh) are copied to
+// tensor memory once per four blocks, and the four MMAs of a block name the
+// block's byte (the instruction descriptor's scale ids).  The accumulator
+// therefore holds the finished product: no partial sums leave the tensor
+// core, and the epilogue only rounds.  Operand layouts, TMA rings, bounded
+// waits and the abort protocol are those of gemm.cuh.
+//
+// "Training and inference of large language models using 8-bit floating
+// point", 제안 방법 (scale, cast, multiply, undo the scale), per block.
+#pragma once
+
+#include "block_scale.cuh"
+#include "gemm.cuh"
+
+namespace fp8lib {
+namespace bgemm {
+
+using namespace gemm;
+
+struct BArgs {
+  int rows, cols;              // output extent along A's and B's outer indices
+  int num_m_blocks, num_n_blocks, num_tiles, num_k_blocks, group_m;
+  int bn;                      // output columns per tile (a multiple of 32, at most 256)
+  int stages, sf_atoms_b;      // ring depth; 512-byte scale groups loaded per tile for B
+  uint32_t stage_bytes, tmem_cols;
+  uint32_t idesc;
+  const void *bias;            // per output feature, or null
+  int bias_dtype;
+  void *out;
+  int out_dtype;
+  size_t ld_out;               // elements
+  int swap;                    // 0: out[r, c]; 1: out[c, r] (A holds the features, B the tokens)
+  int vec_out;                 // rows of `out` start on 16-byte boundaries
+  // tokens form: B is cast from x [cols, x_cols] inside the kernel
+  const void *x;
+  size_t ldx;
+  int x_cols, x_vec, margin;
+};
+
+// A block-scaled MMA, one CTA: D[tmem] (+)= A B with scales at sfa, sfb.
+__device__ __forceinline__ void tc_mma_bs(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+
+// 512 bytes of scales (32 rows x 16 bytes) to the four columns at `taddr` of
+// every lane quarter.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Descriptor of such a group in shared memory: no swizzle, 8-row cores 128 B apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(128 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// Scale ids of block kb: byte kb % 4 of the packed words of both operands.
+__device__ __forceinline__ uint32_t with_scale_ids(uint32_t idesc, int kb) {
+  const uint32_t id = (uint32_t)kb & 3u;
+  return idesc | (id << 4) | (id << 29);
+}
+
+constexpr int kSfSlot = 2048;   // per stage: A's 512 bytes, then up to 3 x 512 of B
+constexpr int kSfCols = 16;     // tensor-memory columns of one set of scales (4 + up to 12)
+constexpr int kSfSets = 3;
+// Sets of scale columns: a group of four blocks writes its set once and the
+// next three groups write others.  A set is rewritten at the earliest nine
+// blocks after its last block was multiplied; a ring of at most nine stages
+// has by then seen those MMAs complete (its slot was refilled), so the copy
+// cannot overtake a reader.
+constexpr int kMaxStages = 9;
+constexpr int kNoCast = -1;     // B comes as codes; otherwise the element type of x
+constexpr int kTokens = 32;     // tokens form: columns of its tile
+
+// One stage of the tokens form, by one warp: the 1x128 blocks of x[0..M, k0..
+// k0+127] as E4M3 codes in the K-major 128-byte-swizzled tile at `tile`, and
+// their scale bytes at byte kb % 4 of the words at `sf`.  16 lanes per token,
+// 8 elements each; four pairs of tokens are loaded before any is used.
+template <int DT>
+__device__ __forceinline__ void cast_tokens_stage(const BArgs &a, int k0, uint32_t tile, uint32_t sf, int lane) {
+  const int c8 = lane & 15, half = lane >> 4;
+#pragma unroll 1
+  for (int t0 = 0; t0 < a.cols; t0 += 8) {
+    float f[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int t = t0 + 2 * i + half;
+      if (a.x_vec) block::load8<DT, true>(a.x, a.ldx, t, k0 + c8 * 8, a.cols, a.x_cols, f[i]);
+      else block::load8<DT, false>(a.x, a.ldx, t, k0 + c8 * 8, a.cols, a.x_cols, f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int t = t0 + 2 * i + half;
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; j++) m = max(m, absbits_f32(f[i][j]));
+      m = block::max16(m);
+      const int k = block::block_exponent(m, kMaxE4M3, a.margin);
+      const float s = pow2f(k);
+      const uint32_t lo = enc4<FP8_E4M3>(f[i][0] * s, f[i][1] * s, f[i][2] * s, f[i][3] * s);
+      const uint32_t hi = enc4<FP8_E4M3>(f[i][4] * s, f[i][5] * s, f[i][6] * s, f[i][7] * s);
+      const uint32_t at = tile + t * 128 + (((c8 >> 1) ^ (t & 7)) << 4) + (c8 & 1) * 8;
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(lo), "r"(hi) : "memory");
+      if (c8 == 0)
+        asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf + t * 16 + ((k0 >> 7) & 3)), "r"((uint32_t)(127 - k))
+                     : "memory");
+    }
+  }
+}
+
+__device__ __forceinline__ void store_one(const BArgs &a, size_t at, float y) {
+  if (a.out_dtype == FP8_DT_F32) reinterpret_cast<float *>(a.out)[at] = y;
+  else if (a.out_dtype == FP8_DT_BF16) reinterpret_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(y);
+  else if (a.out_dtype == FP8_DT_F16) reinterpret_cast<__half *>(a.out)[at] = __float2half_rn(y);
+  else reinterpret_cast<uint16_t *>(a.out)[at] = (uint16_t)(bf16x2_rto(y, y) & 0xffffu);
+}
+
+// Output chunk of 32 accumulator columns of one lane.  Not swapped: out[row,
+// col0...]; swapped: out[col0 + j, row], so that the lanes of a warp write
+// neighbouring features of a token.
+__device__ __forceinline__ void store_out(const BArgs &a, const float (&v)[32], int n, int row, int col0) {
+  if (row >= a.rows) return;
+  if (a.swap) {
+    const float b = a.bias ? load_bias(a.bias, a.bias_dtype, row) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; j++) {
+      if (j < n && col0 + j < a.cols) {
+        store_one(a, (size_t)(col0 + j) * a.ld_out + row, a.bias ? __fadd_rn(v[j], b) : v[j]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 32; c += 8) {
+    if (c >= n || col0 + c >= a.cols) break;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      f[j] = v[c + j];
+      if (a.bias && col0 + c + j < a.cols) f[j] = __fadd_rn(f[j], load_bias(a.bias, a.bias_dtype, col0 + c + j));
+    }
+    const int cols = min(a.cols, col0 + n);
+#define FP8_STORE(DT)                                                                                       \
+  if (a.vec_out) block::store8<DT, true>(a.out, a.ld_out, row, col0 + c, a.rows, cols, f);                  \
+  else block::store8<DT, false>(a.out, a.ld_out, row, col0 + c, a.rows, cols, f)
+    if (a.out_dtype == FP8_DT_F32) { FP8_STORE(FP8_DT_F32); }
+    else if (a.out_dtype == FP8_DT_BF16) { FP8_STORE(FP8_DT_BF16); }
+    else if (a.out_dtype == FP8_DT_F16) { FP8_STORE(FP8_DT_F16); }
+    else { FP8_STORE(FP8_DT_BF16_RTO); }
+#undef FP8_STORE
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One-CTA kernel: a tile of 128 x bn outputs per cluster of S CTAs, each of
+// which reduces its share of the k-blocks (S = 1: no cluster).  The partial
+// tiles are added in rank order through distributed shared memory, each CTA
+// finishing bn / S columns: no workspace, no atomics, the same bits each time.
+//   warp 0 TMA producer, warp 1 TMEM allocation and MMA issue, warps 2-5 epilogue.
+// XDT != kNoCast is the form for few tokens: A holds the weights, and the
+// epilogue warps, idle until the accumulator is complete, cast the tokens'
+// activations into the ring (each every fourth stage, its loads overlapping
+// the other warps'), so that one launch does what the cast and the product do.
+template <bool A_MN, bool B_MN, int XDT>
+__global__ void __launch_bounds__(kThreads)
+    k_bgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+            const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+            const __grid_constant__ BArgs args, const int splits) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *base_ptr = smem_raw + (base - raw);
+  const int S = args.stages;
+  const uint32_t sf0 = base + S * args.stage_bytes;
+  const uint32_t bar0 = sf0 + S * kSfSlot;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * kMaxStages);
+  const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 1);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (bar0 - base) + 8 * (2 * kMaxStages + 2));
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = splits > 1 ? (int)cluster_rank() : 0;
+  const int tile = blockIdx.x / splits;
+  // this CTA's k-blocks
+  const int kb0 = (int)((long long)args.num_k_blocks * rank / splits);
+  const int kb1 = (int)((long long)args.num_k_blocks * (rank + 1) / splits);
+  int mb, nb;
+  {
+    const int per_band = args.group_m * args.num_n_blocks;
+    const int band = tile / per_band, first = band * args.group_m;
+    const int rows_in_band = min(args.num_m_blocks - first, args.group_m);
+    const int r = tile - band * per_band;
+    mb = first + r % rows_in_band;
+    nb = r / rows_in_band;
+  }
+  const int row0 = mb * BM, col0 = nb * args.bn;
+
+  constexpr bool CAST = XDT != kNoCast;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; s++) {
+      mbar_init(full_bar(s), CAST ? 2 : 1);  // the producer's arrive, and the casting warp's
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(tfull_bar, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmSA);
+    if (!CAST) {
+      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&tmSB);
+    }
+  }
+  if constexpr (CAST) {  // token rows the cast never writes are zero
+    for (int i = threadIdx.x; i < S * (kTokens * BK + 512) / 16; i += kThreads) {
+      const int s = i / ((kTokens * BK + 512) / 16), o = (i % ((kTokens * BK + 512) / 16)) * 16;
+      const uint32_t at = o < kTokens * BK ? base + s * args.stage_bytes + BM * BK + o
+                                           : sf0 + s * kSfSlot + 512 + (o - kTokens * BK);
+      st_shared_v4(at, 0u, 0u, 0u, 0u);
+    }
+    fence_async_shared();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(args.tmem_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t sf_bytes = 512u + 512u * args.sf_atoms_b;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; kb++) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
+        const uint32_t sa = base + stage * args.stage_bytes, sb = sa + BM * BK, ss = sf0 + stage * kSfSlot;
+        const bool scales = kb == kb0 || (kb & 3) == 0;
+        mbar_arrive_expect_tx(full_bar(stage), (CAST ? (uint32_t)(BM * BK) : args.stage_bytes) +
+                                                   (scales ? (CAST ? 512u : sf_bytes) : 0u));
+        if (scales) {
+          tma_load_3d(ss, &tmSA, 0, kb >> 2, row0 >> 7, full_bar(stage));
+          if (!CAST) tma_load_3d(ss + 512, &tmSB, 0, kb >> 2, col0 >> 7, full_bar(stage));
+        }
+        if (A_MN) tma_load_2d(sa, &tmA, row0, kb * BK, full_bar(stage));
+        else      tma_load_2d(sa, &tmA, kb * BK, row0, full_bar(stage));
+        if (CAST) {
+        } else if (B_MN) {
+          for (int c = 0; c < args.bn; c += 128)
+            tma_load_2d(sb + c * BK, &tmB, col0 + c, kb * BK, full_bar(stage));
+        } else {
+          tma_load_2d(sb, &tmB, kb * BK, col0, full_bar(stage));
+        }
+        issued_mask |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) {
+        for (int s = 0; s < S; s++)
+          if (issued_mask & (1u << s)) mbar_wait_drain(full_bar(s), (issued_par >> s) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint64_t a_d0 = operand_desc<A_MN>(base, 0), b_d0 = operand_desc<B_MN>(base + BM * BK, 0);
+      constexpr uint64_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
+      constexpr uint64_t b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
+      const uint64_t st_d = args.stage_bytes >> 4;
+      // the scales of a tile that starts inside a 128-row group: skip whole 32-row columns
+      const uint32_t sfb_skip = (uint32_t)(col0 & 127) >> 5;
+      const uint32_t sf_tmem = tmem_base + args.bn;
+      int stage = 0, set = kSfSets - 1;
+      uint32_t phase = 0;
+      bool ok = true, issued_any = false;
+      for (int kb = kb0; kb < kb1; kb++) {
+        if (!stage_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+        if (kb == kb0 || (kb & 3) == 0) {
+          set = set == kSfSets - 1 ? 0 : set + 1;
+          const uint32_t t = sf_tmem + set * kSfCols, ss = sf0 + stage * kSfSlot;
+          tc_cp_scales(t, scale_desc(ss));
+          if (!CAST)
+            for (int i = 0; i < args.sf_atoms_b; i++) tc_cp_scales(t + 4 + 4 * i, scale_desc(ss + 512 + 512 * i));
+        }
+        const uint32_t sfa = sf_tmem + set * kSfCols;
+        uint32_t sfb = sfa + 4 + sfb_skip;
+        if (CAST) {  // every stage brings its own token scales; their columns belong to the ring slot
+          sfb = sf_tmem + kSfSets * kSfCols + 4 * stage;
+          tc_cp_scales(sfb, scale_desc(sf0 + stage * kSfSlot + 512));
+        }
+        const uint64_t so = (uint64_t)stage * st_d;
+        const uint32_t idesc = with_scale_ids(args.idesc, kb);
+#pragma unroll
+        for (int ks = 0; ks < BK / UMMA_K; ks++)
+          tc_mma_bs(tmem_base, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, idesc, sfa, sfb,
+                    (kb != kb0 || ks != 0) ? 1u : 0u);
+        tc_commit(empty_bar(stage));
+        issued_any = true;
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      }
+      if (ok) {
+        tc_commit(tfull_bar);
+      } else if (issued_any) {
+        tc_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    const int row = row0 + q * 32 + lane;
+    if constexpr (CAST) {
+      int stage = q % S;
+      uint32_t phase = (uint32_t)(q / S) & 1u;
+      for (int kb = kb0 + q; kb < kb1; kb += 4) {
+        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag))) break;
+        cast_tokens_stage<XDT>(args, kb * BK, base + stage * args.stage_bytes + BM * BK, sf0 + stage * kSfSlot + 512,
+                               lane);
+        fence_async_shared();  // the MMAs and the scale copy read through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_bar(stage));
+        stage += 4;
+        while (stage >= S) {
+          stage -= S;
+          phase ^= 1u;
+        }
+      }
+      __syncwarp();
+    }
+    const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
+    tc_fence_after();
+    if (got) {
+#pragma unroll 1
+      for (int c = 0; c < args.bn; c += 32) {
+        if (splits == 1 && col0 + c >= args.cols) break;
+        uint32_t r[32];
+        tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; j++) v[j] = __uint_as_float(r[j]);
+        if (splits == 1) {
+          store_out(args, v, 32, row, col0 + c);
+        } else {  // partial tile, column by column: [bn][128] floats over the ring
+#pragma unroll
+          for (int j = 0; j < 32; j++)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c + j) * BM + q * 32 + lane) * 4), "f"(v[j])
+                         : "memory");
+        }
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+  }
+
+  if (splits > 1) {
+    cluster_sync();
+    if (warp >= 2) {
+      const int q = warp & 3, row = row0 + q * 32 + lane;
+      const int per = args.bn / splits;  // a multiple of 4 (bn % 32 == 0, splits <= 8)
+#pragma unroll 1
+      for (int c = rank * per; c < (rank + 1) * per; c += 4) {
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = 0.0f;
+        for (int s = 0; s < splits; s++) {
+          const uint32_t src = map_to_rank(base, (uint32_t)s);
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            float x;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(x)
+                         : "r"(src + ((c + j) * BM + q * 32 + lane) * 4)
+                         : "memory");
+            v[j] = s == 0 ? x : __fadd_rn(v[j], x);
+          }
+        }
+        store_out(args, v, 4, row, col0 + c);
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its partial tile
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(args.tmem_cols)
+                 : "memory");
+  }
+}
+
+// out[r, c] = bias[c] or 0: a product with an empty reduction.
+__global__ void k_bgemm_empty(const BArgs a) {
+  const size_t n = (size_t)a.rows * a.cols, stride = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
+    const int r = (int)(i / a.cols), c = (int)(i % a.cols);
+    store_one(a, (size_t)r * a.ld_out + c, a.bias ? load_bias(a.bias, a.bias_dtype, c) : 0.0f);
+  }
+}
+
+}  // namespace bgemm
+}  // namespace fp8lib

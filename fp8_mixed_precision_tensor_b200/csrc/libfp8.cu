@@ -15,6 +15,9 @@
 #include "adam.cuh"
 #include "allreduce.cuh"
 #include "amax_cast.cuh"
+#include "block_act.cuh"
+#include "block_gemm.cuh"
+#include "block_scale.cuh"
 #include "common.cuh"
 #include "gemm.cuh"
 
@@ -777,6 +780,424 @@ int fp8_selftest_encode(int fmt, unsigned lo_bits, unsigned long long hi_bits, u
     k_encode_selftest<FP8_E4M3><<<d->sms * 8, 256, 0, s>>>(lo_bits, hi_bits, bad_dev, first_dev);
   else
     k_encode_selftest<FP8_E5M2><<<d->sms * 8, 256, 0, s>>>(lo_bits, hi_bits, bad_dev, first_dev);
+  return launch_rc();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Block-scaled operands, products and activation checkpoints.
+
+namespace {
+
+size_t dtype_bytes(int dt) { return dt == FP8_DT_F32 ? 4 : 2; }
+bool fp8_fmt(int f) { return f == FP8_E4M3 || f == FP8_E5M2; }
+bool valid_act(int a) { return a == FP8_ACT_GELU_TANH || a == FP8_ACT_GELU_ERF || a == FP8_ACT_SILU; }
+
+// A high-precision matrix argument: FP8_OK, or what is wrong with it.
+int check_matrix(const void *p, int dtype, int cols, size_t ld) {
+  if (!p || ld < (size_t)cols) return FP8_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(p) % dtype_bytes(dtype) ? FP8_ERR_UNALIGNED : FP8_OK;
+}
+// Whether its rows start on 16-byte boundaries.
+bool wide_rows(const void *p, int dtype, size_t ld) { return aligned16(p) && ld * dtype_bytes(dtype) % 16 == 0; }
+
+int check_blocks(const fp8_blocks *b, int cols) {
+  if (!b || !b->q || !b->s || b->ld < (size_t)cols) return FP8_ERR_INVALID_ARG;
+  return aligned16(b->q) && aligned16(b->s) && b->ld % 16 == 0 ? FP8_OK : FP8_ERR_UNALIGNED;
+}
+
+// f(std::integral_constant<int, dtype>) for a runtime element type.
+template <typename F>
+void with_dtype(int dt, F f) {
+  if (dt == FP8_DT_F32) f(std::integral_constant<int, FP8_DT_F32>());
+  else if (dt == FP8_DT_BF16) f(std::integral_constant<int, FP8_DT_BF16>());
+  else f(std::integral_constant<int, FP8_DT_F16>());
+}
+template <typename F>
+void with_fmt(int fmt, F f) {
+  if (fmt == FP8_E4M3) f(std::integral_constant<int, FP8_E4M3>());
+  else f(std::integral_constant<int, FP8_E5M2>());
+}
+template <typename F>
+void with_bool(bool b, F f) {
+  if (b) f(std::true_type());
+  else f(std::false_type());
+}
+template <typename F>
+void with_act(int act, F f) {
+  if (act == FP8_ACT_GELU_TANH) f(std::integral_constant<int, FP8_ACT_GELU_TANH>());
+  else if (act == FP8_ACT_GELU_ERF) f(std::integral_constant<int, FP8_ACT_GELU_ERF>());
+  else f(std::integral_constant<int, FP8_ACT_SILU>());
+}
+
+// One CTA per 128x128 tile.
+unsigned tile_grid(int rows, int cols) {
+  const unsigned long long t = (unsigned long long)((rows + 127) / 128) * (unsigned long long)((cols + 127) / 128);
+  return (unsigned)(t < 0x7fffffffull ? t : 0x7fffffffull);
+}
+
+block::CastOut cast_out(const fp8_blocks *row, const fp8_blocks *col) {
+  block::CastOut o = {};
+  if (row) { o.q = row->q; o.s = row->s; o.ldq = row->ld; }
+  if (col) { o.qt = col->q; o.st = col->s; o.ldqt = col->ld; }
+  return o;
+}
+
+std::mutex g_block_mu;
+bool g_block_ready[kMaxDevices];
+
+template <typename K>
+int set_max_smem(K kernel) {
+  return set_smem(kernel, 232448);  // 227 KB, the most a CTA can ask for
+}
+
+// One-time per-device attributes of the block-scaled kernels.
+int block_ready() {
+  int dev;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FP8_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(g_block_mu);
+  if (g_block_ready[dev]) return FP8_OK;
+  using bgemm::k_bgemm;
+  constexpr int no = bgemm::kNoCast;
+  int rc = set_max_smem(k_bgemm<false, false, no>) | set_max_smem(k_bgemm<false, true, no>) |
+           set_max_smem(k_bgemm<true, false, no>) | set_max_smem(k_bgemm<true, true, no>) |
+           set_max_smem(k_bgemm<false, false, FP8_DT_F32>) | set_max_smem(k_bgemm<false, false, FP8_DT_BF16>) |
+           set_max_smem(k_bgemm<false, false, FP8_DT_F16>);
+  if (rc) return FP8_ERR_CUDA;
+  g_block_ready[dev] = true;
+  return FP8_OK;
+}
+
+// Codes with `inner` bytes per row, rows `ld` apart -> TMA map, 128 bytes x box_outer, 128-byte swizzle.
+int make_code_map(CUtensorMap *m, const uint8_t *q, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_outer) {
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {ld};
+  cuuint32_t box[2] = {128, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(q), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FP8_OK : FP8_ERR_CUDA;
+}
+
+// Scale groups [ceil(outer/128)][ceil(KB/4)][512 B] -> TMA map, box of `atoms` groups along the outer axis.
+int make_scale_map(CUtensorMap *m, const uint8_t *s, int outer, int red, uint32_t atoms) {
+  const uint64_t kg = ((uint64_t)(red + 127) / 128 + 3) / 4, rb = (uint64_t)(outer + 127) / 128;
+  cuuint64_t dims[3] = {128, kg, rb};  // in 32-bit words
+  cuuint64_t strides[2] = {512, 512 * kg};
+  cuuint32_t box[3] = {128, 1, atoms};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(s), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FP8_OK : FP8_ERR_CUDA;
+}
+
+struct BOperand {
+  const fp8_blocks *b;
+  int fmt;
+};
+
+// C[rows, cols] (or, swapped, C[cols, rows]) on the one-CTA kernel.  XDT: the
+// tokens form, B cast from a.x in the kernel (B.b unused).
+template <bool A_MN, bool B_MN, int XDT = bgemm::kNoCast>
+int launch_bgemm(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, int bn, int splits,
+                 cudaStream_t stream) {
+  using namespace bgemm;
+  const int rows = a.rows, cols = a.cols;
+  a.bn = bn;
+  a.num_m_blocks = (rows + gemm::BM - 1) / gemm::BM;
+  a.num_n_blocks = (cols + bn - 1) / bn;
+  a.num_tiles = a.num_m_blocks * a.num_n_blocks;
+  a.num_k_blocks = (K + gemm::BK - 1) / gemm::BK;
+  a.group_m = 16;
+  a.sf_atoms_b = bn % 128 == 0 ? bn / 128 : (bn < 128 && 128 % bn == 0) ? 1 : (96 + bn + 127) / 128;
+  const int b_rows = B_MN ? (bn + 127) / 128 * 128 : bn;
+  a.stage_bytes = (uint32_t)(gemm::BM + b_rows) * gemm::BK;
+  uint32_t tmem = 32;
+  while (tmem < (uint32_t)(bn + kSfSets * kSfCols + (XDT == kNoCast ? 0 : 4 * kMaxStages))) tmem *= 2;
+  a.tmem_cols = tmem;
+  // two CTAs per SM where the accumulators and a ring of at least three stages of both fit
+  const uint32_t room = (tmem <= 256 ? 114688u : 230400u) - 1024u - 256u;
+  int stages = (int)(room / (a.stage_bytes + kSfSlot));
+  if (stages > kMaxStages) stages = kMaxStages;
+  a.stages = stages;
+  if (splits > 1 && (uint32_t)bn * gemm::BM * 4 > stages * a.stage_bytes) return FP8_ERR_UNSUPPORTED;
+  a.idesc = ((uint32_t)A.fmt << 7) | ((uint32_t)B.fmt << 10) | ((uint32_t)(A_MN ? 1 : 0) << 15) |
+            ((uint32_t)(B_MN ? 1 : 0) << 16) | ((uint32_t)(bn >> 3) << 17) | (1u << 23)  // scales: 8-bit exponents
+            | ((uint32_t)(gemm::BM >> 7) << 27);
+  CUtensorMap ma, mb, msa, msb;
+  int rc = A_MN ? make_code_map(&ma, A.b->q, rows, K, A.b->ld, gemm::BK)
+                : make_code_map(&ma, A.b->q, K, rows, A.b->ld, gemm::BM);
+  if (rc) return rc;
+  if ((rc = make_scale_map(&msa, A.b->s, rows, K, 1))) return rc;
+  if constexpr (XDT == kNoCast) {
+    rc = B_MN ? make_code_map(&mb, B.b->q, cols, K, B.b->ld, gemm::BK)
+              : make_code_map(&mb, B.b->q, K, cols, B.b->ld, (uint32_t)bn);
+    if (rc) return rc;
+    if ((rc = make_scale_map(&msb, B.b->s, cols, K, (uint32_t)a.sf_atoms_b))) return rc;
+  } else {
+    mb = ma;
+    msb = msa;
+  }
+  const size_t smem = (size_t)stages * (a.stage_bytes + kSfSlot) + 256 + 1024;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = splits;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)a.num_tiles * splits);
+  cfg.blockDim = dim3(gemm::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = splits > 1 ? 1 : 0;
+  return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm<A_MN, B_MN, XDT>, ma, mb, msa, msb, a, splits));
+}
+
+// Reduction splits for `tiles` tiles of kblocks blocks on `slots` resident
+// CTAs: doubled while every CTA stays resident and keeps two blocks.
+int pick_splits(long long tiles, int kblocks, int slots) {
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= slots && kblocks >= 4 * s) s *= 2;
+  return s;
+}
+
+// Out[R, C] = sum over `red` of A(r, .) B(c, .) (+ bias[c]).  A_MN / B_MN: the
+// operand's codes are [red, outer] instead of [outer, red].
+template <bool A_MN, bool B_MN>
+int run_bgemm(const BOperand &A, const BOperand &B, const void *bias, int bias_dtype, void *out, int out_dtype,
+              size_t ld_out, int R, int C, int red, cudaStream_t stream) {
+  if (R < 0 || C < 0 || red < 0 || !valid_out_dtype(out_dtype) || (bias && !valid_dtype(bias_dtype)))
+    return FP8_ERR_INVALID_ARG;
+  if (R == 0 || C == 0) return FP8_OK;
+  int rc = check_matrix(out, out_dtype, C, ld_out);
+  if (rc) return rc;
+  if (bias && reinterpret_cast<uintptr_t>(bias) % dtype_bytes(bias_dtype)) return FP8_ERR_UNALIGNED;
+  bgemm::BArgs a = {};
+  a.rows = R;
+  a.cols = C;
+  a.bias = bias;
+  a.bias_dtype = bias_dtype;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.ld_out = ld_out;
+  a.vec_out = wide_rows(out, out_dtype, ld_out);
+  DeviceInfo *d;
+  if (red == 0) {
+    if ((rc = device_info(&d))) return rc;
+    bgemm::k_bgemm_empty<<<d->sms * 4, 256, 0, stream>>>(a);
+    return launch_rc();
+  }
+  if ((rc = check_blocks(A.b, A_MN ? R : red))) return rc;
+  if ((rc = check_blocks(B.b, B_MN ? C : red))) return rc;
+  if ((rc = device_info(&d))) return rc;
+  if ((rc = block_ready())) return rc;
+  const int kblocks = (red + 127) / 128;
+  if constexpr (!A_MN) {
+    if (R <= 128) {  // few tokens: their rows become the tile's columns, the weights its 128 lanes
+      const int bn = (R + 31) / 32 * 32;
+      a.swap = 1;
+      a.rows = C;
+      a.cols = R;
+      return launch_bgemm<B_MN, A_MN>(B, A, a, red, bn, pick_splits((C + 127) / 128, kblocks, 2 * d->sms),
+                                      stream);
+    }
+  }
+  const int bn = C <= 128 ? 128 : (long long)((R + 127) / 128) * ((C + 255) / 256) >= d->sms ? 256 : 128;
+  const long long tiles = (long long)((R + 127) / 128) * ((C + bn - 1) / bn);
+  return launch_bgemm<A_MN, B_MN>(A, B, a, red, bn, pick_splits(tiles, kblocks, bn == 256 ? d->sms : 2 * d->sms),
+                                  stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fp8_block_scale_bytes(int outer, int red) {
+  return outer > 0 && red > 0 ? block::scale_groups(outer, red) * 512 : 0;
+}
+
+int fp8_block_cast(const void *x, int dtype, int rows, int cols, size_t ldx, int fmt, int margin,
+                   const fp8_blocks *row, const fp8_blocks *col, void *stream) {
+  if (!valid_dtype(dtype) || !fp8_fmt(fmt) || rows < 0 || cols < 0 || margin < 0 || margin > 64 || (!row && !col))
+    return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  int rc = check_matrix(x, dtype, cols, ldx);
+  if (rc || (row && (rc = check_blocks(row, cols))) || (col && (rc = check_blocks(col, cols)))) return rc;
+  const block::CastOut o = cast_out(row, col);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  with_dtype(dtype, [&](auto dt) {
+    with_fmt(fmt, [&](auto f) {
+      with_bool(wide_rows(x, dtype, ldx), [&](auto vec) {
+        block::k_block_cast<decltype(dt)::value, decltype(f)::value, decltype(vec)::value>
+            <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(x, rows, cols, ldx, margin, o);
+      });
+    });
+  });
+  return launch_rc();
+}
+
+int fp8_block_cast_square(const void *x, int dtype, int rows, int cols, size_t ldx, int fmt, int margin,
+                          const fp8_blocks *out, uint8_t *s_col, void *stream) {
+  if (!valid_dtype(dtype) || !fp8_fmt(fmt) || rows < 0 || cols < 0 || margin < 0 || margin > 64)
+    return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  int rc = check_matrix(x, dtype, cols, ldx);
+  if (rc || (rc = check_blocks(out, cols))) return rc;
+  if (!s_col) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(s_col)) return FP8_ERR_UNALIGNED;
+  block::CastOut o = cast_out(out, nullptr);
+  o.st = s_col;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  with_dtype(dtype, [&](auto dt) {
+    with_fmt(fmt, [&](auto f) {
+      with_bool(wide_rows(x, dtype, ldx), [&](auto vec) {
+        block::k_block_cast_square<decltype(dt)::value, decltype(f)::value, decltype(vec)::value>
+            <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(x, rows, cols, ldx, margin, o);
+      });
+    });
+  });
+  return launch_rc();
+}
+
+int fp8_block_decode(const fp8_blocks *in, int fmt, int axis, int rows, int cols, void *x, int dtype, size_t ldx,
+                     void *stream) {
+  if (!valid_dtype(dtype) || !fp8_fmt(fmt) || rows < 0 || cols < 0 || (axis != 0 && axis != 1))
+    return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  int rc = check_matrix(x, dtype, cols, ldx);
+  if (rc || (rc = check_blocks(in, cols))) return rc;
+  DeviceInfo *d;
+  if ((rc = device_info(&d))) return rc;
+  const unsigned grid = grid_for((size_t)rows * (((size_t)cols + 7) / 8), block::kCastThreads, d->sms * 8);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  with_dtype(dtype, [&](auto dt) {
+    with_fmt(fmt, [&](auto f) {
+      with_bool(axis == 0, [&](auto colblocks) {
+        with_bool(wide_rows(x, dtype, ldx), [&](auto vec) {
+          block::k_block_decode<decltype(dt)::value, decltype(f)::value, decltype(colblocks)::value, decltype(vec)::value>
+              <<<grid, block::kCastThreads, 0, s>>>(in->q, in->s, rows, cols, in->ld, x, ldx);
+        });
+      });
+    });
+  });
+  return launch_rc();
+}
+
+int fp8_block_linear_fwd(const fp8_blocks *x, const fp8_blocks *w, const void *bias, int bias_dtype, void *y,
+                         int y_dtype, size_t ldy, int M, int N, int K, void *stream) {
+  return run_bgemm<false, false>({x, 0}, {w, 0}, bias, bias_dtype, y, y_dtype, ldy, M, N, K,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+int fp8_block_linear_tokens(const void *x, int x_dtype, size_t ldx, int margin, const fp8_blocks *w, const void *bias,
+                            int bias_dtype, void *y, int y_dtype, size_t ldy, int M, int N, int K, void *stream) {
+  if (M < 0 || M > FP8_BLOCK_TOKENS_MAX || N < 0 || K < 0 || margin < 0 || margin > 64 || !valid_dtype(x_dtype) ||
+      !valid_out_dtype(y_dtype) || (bias && !valid_dtype(bias_dtype)))
+    return FP8_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0 || N == 0 || K == 0)
+    return run_bgemm<false, false>({nullptr, 0}, {w, 0}, bias, bias_dtype, y, y_dtype, ldy, M, N, K, s);
+  int rc = check_matrix(x, x_dtype, K, ldx);
+  if (rc || (rc = check_matrix(y, y_dtype, N, ldy)) || (rc = check_blocks(w, K))) return rc;
+  if (bias && reinterpret_cast<uintptr_t>(bias) % dtype_bytes(bias_dtype)) return FP8_ERR_UNALIGNED;
+  DeviceInfo *d;
+  if ((rc = device_info(&d)) || (rc = block_ready())) return rc;
+  bgemm::BArgs a = {};
+  a.rows = N;
+  a.cols = M;
+  a.bias = bias;
+  a.bias_dtype = bias_dtype;
+  a.out = y;
+  a.out_dtype = y_dtype;
+  a.ld_out = ldy;
+  a.swap = 1;
+  a.x = x;
+  a.ldx = ldx;
+  a.x_cols = K;
+  a.x_vec = wide_rows(x, x_dtype, ldx);
+  a.margin = margin;
+  const int splits = pick_splits((N + 127) / 128, (K + 127) / 128, 2 * d->sms);
+  with_dtype(x_dtype, [&](auto dt) {
+    rc = launch_bgemm<false, false, decltype(dt)::value>({w, 0}, {nullptr, 0}, a, K, bgemm::kTokens, splits, s);
+  });
+  return rc;
+}
+
+int fp8_block_linear_dgrad(const fp8_blocks *dy, int dy_fmt, const fp8_blocks *w, void *dx, int dx_dtype,
+                           size_t lddx, int M, int N, int K, void *stream) {
+  if (!fp8_fmt(dy_fmt)) return FP8_ERR_INVALID_ARG;
+  return run_bgemm<false, true>({dy, dy_fmt}, {w, 0}, nullptr, 0, dx, dx_dtype, lddx, M, K, N,
+                                static_cast<cudaStream_t>(stream));
+}
+
+int fp8_block_linear_wgrad(const fp8_blocks *dy, int dy_fmt, const fp8_blocks *x, void *dw, int dw_dtype,
+                           size_t lddw, int M, int N, int K, void *stream) {
+  if (!fp8_fmt(dy_fmt)) return FP8_ERR_INVALID_ARG;
+  return run_bgemm<true, true>({dy, dy_fmt}, {x, 0}, nullptr, 0, dw, dw_dtype, lddw, N, K, M,
+                               static_cast<cudaStream_t>(stream));
+}
+
+int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int act, int margin,
+                const fp8_blocks *ckpt, const fp8_blocks *a_row, void *a, size_t lda, void *stream) {
+  if (!valid_dtype(dtype) || !valid_act(act) || rows < 0 || cols < 0 || margin < 0 || margin > 64)
+    return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  int rc = check_matrix(h, dtype, cols, ldh);
+  if (rc || (rc = check_blocks(ckpt, cols)) || (a_row && (rc = check_blocks(a_row, cols))) ||
+      (a && (rc = check_matrix(a, dtype, cols, lda))))
+    return rc;
+  block::ActFwd p = {h, rows, cols, ldh, margin, ckpt->q, ckpt->s, ckpt->ld, nullptr, nullptr, 0, a, lda};
+  if (a_row) {
+    p.aq = a_row->q;
+    p.as = a_row->s;
+    p.lda_q = a_row->ld;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  with_dtype(dtype, [&](auto dt) {
+    with_act(act, [&](auto f) {
+      with_bool(wide_rows(h, dtype, ldh) && (!a || wide_rows(a, dtype, lda)), [&](auto vec) {
+        block::k_act_fwd<decltype(dt)::value, decltype(f)::value, decltype(vec)::value>
+            <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(p);
+      });
+    });
+  });
+  return launch_rc();
+}
+
+int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int cols, size_t ldda, int act, int fmt,
+                int margin, const fp8_blocks *dh_row, const fp8_blocks *dh_col, const fp8_blocks *a_col, void *dh,
+                size_t lddh, void *stream) {
+  if (!valid_dtype(dtype) || !valid_act(act) || !fp8_fmt(fmt) || rows < 0 || cols < 0 || margin < 0 || margin > 64 ||
+      (!dh_row && !dh_col && !a_col && !dh))
+    return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  int rc = check_matrix(da, dtype, cols, ldda);
+  if (rc || (rc = check_blocks(ckpt, cols)) || (dh_row && (rc = check_blocks(dh_row, cols))) ||
+      (dh_col && (rc = check_blocks(dh_col, cols))) || (a_col && (rc = check_blocks(a_col, cols))) ||
+      (dh && (rc = check_matrix(dh, dtype, cols, lddh))))
+    return rc;
+  block::ActBwd p = {ckpt->q, ckpt->s, ckpt->ld, da, rows, cols, ldda, margin, cast_out(dh_row, dh_col),
+                     nullptr, nullptr, 0, dh, lddh};
+  if (a_col) {
+    p.aqt = a_col->q;
+    p.ast = a_col->s;
+    p.ldaqt = a_col->ld;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  with_dtype(dtype, [&](auto dt) {
+    with_act(act, [&](auto f) {
+      with_fmt(fmt, [&](auto g) {
+        with_bool(wide_rows(da, dtype, ldda) && (!dh || wide_rows(dh, dtype, lddh)), [&](auto vec) {
+          block::k_act_bwd<decltype(dt)::value, decltype(f)::value, decltype(g)::value, decltype(vec)::value>
+              <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(p);
+        });
+      });
+    });
+  });
   return launch_rc();
 }
 

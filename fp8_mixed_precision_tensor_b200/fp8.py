@@ -25,6 +25,8 @@ FP8_STATUS_NONFINITE, FP8_STATUS_TIMEOUT, FP8_STATUS_INTERNAL, FP8_STATUS_BAD_MU
 FP8_DT_F32, FP8_DT_BF16, FP8_DT_F16 = 0, 1, 2
 FP8_DT_BF16_RTO = 3  # GEMM outputs only: bfloat16 rounded to odd, for a following FP8 cast
 FP8_E4M3, FP8_E5M2, FP8_F16S = 0, 1, 2
+FP8_ACT_GELU_TANH, FP8_ACT_GELU_ERF, FP8_ACT_SILU = 0, 1, 2
+FP8_BLOCK_TOKENS_MAX = 32
 
 _DT = {torch.float32: FP8_DT_F32, torch.bfloat16: FP8_DT_BF16, torch.float16: FP8_DT_F16}
 
@@ -35,6 +37,9 @@ SYMBOLS = ("fp8_amax", "fp8_compute_scale", "fp8_cast", "fp8_scale_cast", "fp8_a
            "fp8_adam_apply", "fp8_adam_step_noalloc", "fp8_adam_step_into", "fp8_adam_step_into_castgrad",
            "fp8_adam_stats_into",
            "fp8_adam_apply_into",
+           "fp8_block_scale_bytes", "fp8_block_cast", "fp8_block_cast_square", "fp8_block_decode",
+           "fp8_block_linear_fwd", "fp8_block_linear_tokens", "fp8_block_linear_dgrad", "fp8_block_linear_wgrad",
+           "fp8_act_fwd", "fp8_act_bwd",
            "fp8_selftest_wait_timeout", "fp8_selftest_step_reciprocal", "fp8_selftest_encode", "fp8_get_status", "fp8_strerror")
 
 
@@ -63,6 +68,10 @@ class _GradCast(ctypes.Structure):
 class _MuRule(ctypes.Structure):
     _fields_ = [("theta", ctypes.c_float), ("interval", ctypes.c_int), ("mu_min", ctypes.c_float),
                 ("mu_max", ctypes.c_float)]
+
+
+class _Blocks(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("ld", ctypes.c_size_t)]
 
 
 class _HParams(ctypes.Structure):
@@ -103,13 +112,24 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in ("fp8_adam_step_into", "fp8_adam_stats_into", "fp8_adam_apply_into"):
         getattr(lib, name).argtypes = [ctypes.POINTER(_Chunk), ctypes.POINTER(_Dest), i,
                                        ctypes.POINTER(_HParams), p, sz, p]
+    b = ctypes.POINTER(_Blocks)
+    lib.fp8_block_scale_bytes.argtypes, lib.fp8_block_scale_bytes.restype = [i, i], sz
+    lib.fp8_block_cast.argtypes = [p, i, i, i, sz, i, i, b, b, p]
+    lib.fp8_block_cast_square.argtypes = [p, i, i, i, sz, i, i, b, p, p]
+    lib.fp8_block_decode.argtypes = [b, i, i, i, i, p, i, sz, p]
+    lib.fp8_block_linear_fwd.argtypes = [b, b, p, i, p, i, sz, i, i, i, p]
+    lib.fp8_block_linear_tokens.argtypes = [p, i, sz, i, b, p, i, p, i, sz, i, i, i, p]
+    lib.fp8_block_linear_dgrad.argtypes = [b, i, b, p, i, sz, i, i, i, p]
+    lib.fp8_block_linear_wgrad.argtypes = [b, i, b, p, i, sz, i, i, i, p]
+    lib.fp8_act_fwd.argtypes = [p, i, i, i, sz, i, i, b, b, p, sz, p]
+    lib.fp8_act_bwd.argtypes = [b, p, i, i, i, sz, i, i, i, b, b, b, p, sz, p]
     lib.fp8_selftest_wait_timeout.argtypes = [ctypes.c_uint, p]
     lib.fp8_selftest_step_reciprocal.argtypes = [ctypes.c_uint, ctypes.c_ulonglong, p, p, p]
     lib.fp8_selftest_encode.argtypes = [i, ctypes.c_uint, ctypes.c_ulonglong, p, p, p]
     lib.fp8_get_status.argtypes = [ctypes.POINTER(ctypes.c_uint), p]
     lib.fp8_strerror.argtypes, lib.fp8_strerror.restype = [i], ctypes.c_char_p
     for name in SYMBOLS:
-        if name not in ("fp8_adam_workspace_bytes", "fp8_strerror"):
+        if name not in ("fp8_adam_workspace_bytes", "fp8_block_scale_bytes", "fp8_strerror"):
             getattr(lib, name).restype = i
     _lib = lib
     return lib
@@ -399,6 +419,182 @@ def fp8_adam_step_noalloc(chunks, lr: float, beta1: float, beta2: float, eps: fl
     hp = _HParams(lr, beta1, beta2, eps, step, margin)
     _check(load_library().fp8_adam_step_noalloc(arr, len(arr), ctypes.byref(hp), _stream(stream)),
            "fp8_adam_step_noalloc")
+
+
+# ---------------------------------------------------------------- block-scaled FP8
+def fp8_block_scale_bytes(outer: int, red: int) -> int:
+    """Bytes of the scales of `outer` rows of `red` blocked elements."""
+    return load_library().fp8_block_scale_bytes(outer, red)
+
+
+def block_codes(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    """An uninitialised [rows, cols] uint8 code matrix whose rows start on
+    16-byte boundaries (its row stride is cols rounded up to 16)."""
+    return torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=device)[:, :cols]
+
+
+def block_scales(outer: int, red: int, device="cuda") -> torch.Tensor:
+    """An uninitialised scale buffer for `outer` rows of `red` blocked elements
+    (a code matrix's (rows, cols) for 1x128 blocks, (cols, rows) for 128x1)."""
+    return torch.empty(fp8_block_scale_bytes(outer, red), dtype=torch.uint8, device=device)
+
+
+def _on_device(t: torch.Tensor, what: str) -> torch.Tensor:
+    if not t.is_cuda:
+        raise ValueError("libfp8 takes device tensors")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t
+
+
+def _matrix(t: torch.Tensor, what: str, shape=None) -> tuple[int, int, int, int]:
+    """(pointer, rows, cols, row stride in elements) of a matrix whose rows are contiguous."""
+    _on_device(t, what)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {'a matrix' if shape is None else tuple(shape)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous (strides {t.stride()})")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{what}: rows overlap (strides {t.stride()})")
+    return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _hp_matrix(t: torch.Tensor, what: str, shape=None):
+    if t.dtype not in _DT:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected float32, bfloat16 or float16")
+    return _matrix(t, what, shape)
+
+
+def _blocks(q, s, what: str, shape, outer: int, red: int):
+    """fp8_blocks of a code matrix and its scale buffer."""
+    if q is None and s is None:
+        return None
+    if q is None or s is None:
+        raise ValueError(f"{what}: codes and scales go together")
+    if q.dtype != torch.uint8 or s.dtype != torch.uint8:
+        raise TypeError(f"{what}: codes and scales are uint8")
+    ptr, rows, _, ld = _matrix(q, what, shape)
+    _on_device(s, f"{what} scales")
+    need = fp8_block_scale_bytes(outer, red)
+    if not s.is_contiguous() or s.numel() < need:
+        raise ValueError(f"{what}: scales are {need} contiguous bytes, got {s.numel()}")
+    return ctypes.byref(_Blocks(ptr, s.data_ptr(), -(-ld // 16) * 16 if rows <= 1 else ld))
+
+
+def _vector(t, what: str, n: int):
+    if t is None:
+        return None, 0
+    if t.dtype not in _DT:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected float32, bfloat16 or float16")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous elements expected")
+    return _on_device(t, what).data_ptr(), _DT[t.dtype]
+
+
+def fp8_block_cast(x, fmt: int, margin: int, q_row=None, s_row=None, q_col=None, s_col=None, stream=None) -> None:
+    """x [rows, cols] to codes of 1x128 blocks (q_row, s_row) and / or of 128x1
+    blocks (q_col, s_col), reading x once."""
+    ptr, rows, cols, ld = _hp_matrix(x, "x")
+    _check(load_library().fp8_block_cast(ptr, _DT[x.dtype], rows, cols, ld, fmt, margin,
+                                         _blocks(q_row, s_row, "row blocks", x.shape, rows, cols),
+                                         _blocks(q_col, s_col, "column blocks", x.shape, cols, rows),
+                                         _stream(stream)), "fp8_block_cast")
+
+
+def fp8_block_cast_square(x, fmt: int, margin: int, q, s_row, s_col, stream=None) -> None:
+    """x to codes of 128x128 blocks, their scales in both orders (s_row for
+    products that reduce over the columns, s_col over the rows)."""
+    ptr, rows, cols, ld = _hp_matrix(x, "x")
+    row = _blocks(q, s_row, "blocks", x.shape, rows, cols)
+    _blocks(q, s_col, "blocks", x.shape, cols, rows)
+    _check(load_library().fp8_block_cast_square(ptr, _DT[x.dtype], rows, cols, ld, fmt, margin, row,
+                                                s_col.data_ptr(), _stream(stream)), "fp8_block_cast_square")
+
+
+def fp8_block_decode(q, s, fmt: int, axis: int, x, stream=None) -> None:
+    """x = the values of blocked codes; axis 1: blocks along the columns
+    (1x128), 0: along the rows (128x1)."""
+    ptr, rows, cols, ld = _hp_matrix(x, "x")
+    b = _blocks(q, s, "blocks", x.shape, *((rows, cols) if axis else (cols, rows)))
+    _check(load_library().fp8_block_decode(b, fmt, axis, rows, cols, ptr, _DT[x.dtype], ld, _stream(stream)),
+           "fp8_block_decode")
+
+
+def fp8_block_linear_fwd(xq, xs, wq, ws, y, bias=None, stream=None, rto=False) -> None:
+    """y[M,N] = x . w^T (+ bias): xq [M,K] with scales of (M, K), wq [N,K] with scales of (N, K)."""
+    (M, K), N = xq.shape, wq.shape[0]
+    yp, _, _, ld = _hp_matrix(y, "y", (M, N))
+    bp, bdt = _vector(bias, "bias", N)
+    _check(load_library().fp8_block_linear_fwd(_blocks(xq, xs, "x", (M, K), M, K), _blocks(wq, ws, "w", (N, K), N, K),
+                                               bp, bdt, yp, _out_dt(y, rto), ld, M, N, K, _stream(stream)),
+           "fp8_block_linear_fwd")
+
+
+def fp8_block_linear_tokens(x, wq, ws, y, bias=None, margin: int = 0, stream=None, rto=False) -> None:
+    """y[M,N] = x . w^T (+ bias) for at most FP8_BLOCK_TOKENS_MAX tokens x [M,K]
+    in float32, bfloat16 or float16: fp8_block_cast and fp8_block_linear_fwd in
+    one launch."""
+    xp, M, K, ldx = _hp_matrix(x, "x")
+    N = wq.shape[0]
+    yp, _, _, ldy = _hp_matrix(y, "y", (M, N))
+    bp, bdt = _vector(bias, "bias", N)
+    _check(load_library().fp8_block_linear_tokens(xp, _DT[x.dtype], ldx, margin, _blocks(wq, ws, "w", (N, K), N, K),
+                                                  bp, bdt, yp, _out_dt(y, rto), ldy, M, N, K, _stream(stream)),
+           "fp8_block_linear_tokens")
+
+
+def fp8_block_linear_dgrad(dyq, dys, dy_fmt: int, wq, ws_col, dx, stream=None, rto=False) -> None:
+    """dx[M,K] = dy . w: dyq [M,N] with scales of (M, N), wq [N,K] with scales of (K, N)."""
+    (M, N), K = dyq.shape, wq.shape[1]
+    xp, _, _, ld = _hp_matrix(dx, "dx", (M, K))
+    _check(load_library().fp8_block_linear_dgrad(_blocks(dyq, dys, "dy", (M, N), M, N), dy_fmt,
+                                                 _blocks(wq, ws_col, "w", (N, K), K, N), xp, _out_dt(dx, rto), ld,
+                                                 M, N, K, _stream(stream)), "fp8_block_linear_dgrad")
+
+
+def fp8_block_linear_wgrad(dyq, dys_col, dy_fmt: int, xq, xs_col, dw, stream=None, rto=False) -> None:
+    """dw[N,K] = dy^T . x: dyq [M,N] with scales of (N, M), xq [M,K] with scales of (K, M)."""
+    (M, N), K = dyq.shape, xq.shape[1]
+    wp, _, _, ld = _hp_matrix(dw, "dw", (N, K))
+    _check(load_library().fp8_block_linear_wgrad(_blocks(dyq, dys_col, "dy", (M, N), N, M), dy_fmt,
+                                                 _blocks(xq, xs_col, "x", (M, K), K, M), wp, _out_dt(dw, rto), ld,
+                                                 M, N, K, _stream(stream)), "fp8_block_linear_wgrad")
+
+
+# ---------------------------------------------------------------- activations with an 8-bit checkpoint
+def fp8_act_fwd(h, act: int, margin: int, ckpt_q, ckpt_s, a_q=None, a_s=None, a=None, stream=None) -> None:
+    """From h: the E4M3 checkpoint (1x128 blocks), and optionally the E4M3
+    codes of act(h)'s 1x128 blocks and act(h) itself (h's dtype)."""
+    ptr, rows, cols, ld = _hp_matrix(h, "h")
+    ap, lda = None, 0
+    if a is not None:
+        if a.dtype != h.dtype:
+            raise TypeError("a has h's dtype")
+        ap, _, _, lda = _hp_matrix(a, "a", h.shape)
+    _check(load_library().fp8_act_fwd(ptr, _DT[h.dtype], rows, cols, ld, act, margin,
+                                      _blocks(ckpt_q, ckpt_s, "checkpoint", h.shape, rows, cols),
+                                      _blocks(a_q, a_s, "a blocks", h.shape, rows, cols), ap, lda, _stream(stream)),
+           "fp8_act_fwd")
+
+
+def fp8_act_bwd(ckpt_q, ckpt_s, da, act: int, fmt: int = FP8_E5M2, margin: int = 0, dh_q=None, dh_s=None,
+                dh_q_col=None, dh_s_col=None, a_q_col=None, a_s_col=None, dh=None, stream=None) -> None:
+    """From the checkpoint and da: codes of dh = da * act'(h') in 1x128 blocks
+    (dh_q, dh_s) and 128x1 blocks (dh_q_col, dh_s_col), E4M3 codes of act(h')
+    in 128x1 blocks (a_q_col, a_s_col), and dh itself (da's dtype); any of them."""
+    ptr, rows, cols, ld = _hp_matrix(da, "da")
+    hp, lddh = None, 0
+    if dh is not None:
+        if dh.dtype != da.dtype:
+            raise TypeError("dh has da's dtype")
+        hp, _, _, lddh = _hp_matrix(dh, "dh", da.shape)
+    _check(load_library().fp8_act_bwd(_blocks(ckpt_q, ckpt_s, "checkpoint", da.shape, rows, cols), ptr,
+                                      _DT[da.dtype], rows, cols, ld, act, fmt, margin,
+                                      _blocks(dh_q, dh_s, "dh row blocks", da.shape, rows, cols),
+                                      _blocks(dh_q_col, dh_s_col, "dh column blocks", da.shape, cols, rows),
+                                      _blocks(a_q_col, a_s_col, "a column blocks", da.shape, cols, rows),
+                                      hp, lddh, _stream(stream)), "fp8_act_bwd")
 
 
 def fp8_selftest_wait_timeout(limit_us: int, stream=None) -> None:

@@ -25,6 +25,7 @@
  *     (amax, scale, inverse scale) stay in device memory as float.
  *   - Bulk tensors are dense and contiguous; their pointers must be 16-byte
  *     aligned (FP8_ERR_UNALIGNED otherwise).  Any element count is allowed.
+ *     (The block-scaled calls take row pitches; their own rules stand there.)
  *   - Errors found on the host are returned at once and nothing is enqueued.
  *     Conditions found on the device (a non-finite amax, a pipeline wait that
  *     ran out of time) set bits of a device status word read by
@@ -533,6 +534,128 @@ int fp8_selftest_step_reciprocal(unsigned lo_bits, unsigned long long hi_bits, u
  */
 int fp8_selftest_encode(int fmt, unsigned lo_bits, unsigned long long hi_bits, unsigned long long *bad_dev,
                         unsigned *first_dev, void *stream);
+
+/*
+ * Block-scaled FP8 ([FP8-AMAX] 제안 방법 per block instead of per tensor): a
+ * tensor's codes with one power-of-two scale per block of 128 elements --
+ * 1x128 (a row's 128 neighbours), 128x1 (a column's) or 128x128 -- so that an
+ * outlier costs only its own block precision.  A block's scale is
+ * 2^(clamp(floor(log2(fmt_max / amax)) - margin, -126, 126)), the rule of
+ * fp8_compute_scale with mu = 1: an all-zero block has scale 1, a block with a
+ * NaN or inf too and sets FP8_STATUS_NONFINITE.
+ *
+ * Scales are stored as one byte per block and row (column): the biased
+ * exponent of the DEscale, value = dec(code) * 2^(byte - 127).  The bytes of
+ * an operand with `outer` rows whose `red` elements are blocked (the columns
+ * for 1x128 blocks; for 128x1 blocks outer = columns, red = rows) stand in
+ * groups of 128 outer indices x 4 blocks, 512 bytes each: the byte of outer
+ * index r, block b is at
+ *   ((r / 128) * ceil(ceil(red / 128) / 4) + b / 4) * 512
+ *       + (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4,
+ * fp8_block_scale_bytes(outer, red) bytes in all; padding bytes are 127.
+ * 128x128 blocks repeat their byte for each of the 128 rows (columns).
+ *
+ * Codes keep the source's row-major order, rows `ld` bytes apart: ld a
+ * multiple of 16 and at least the row's length (any length; bytes behind it
+ * are neither read nor written).  Code and scale pointers are 16-byte aligned.
+ * High-precision matrices have rows `ld` elements apart (ld at least the row's
+ * length) and may start at any element; rows that start on 16-byte boundaries
+ * are read and written with wide accesses.
+ */
+typedef struct {
+  uint8_t *q;  /* dev: codes */
+  uint8_t *s;  /* dev: scale bytes */
+  size_t ld;   /* bytes from one row of codes to the next */
+} fp8_blocks;
+
+/* Bytes of the scales of `outer` rows of `red` blocked elements (0 if either is 0 or negative). */
+size_t fp8_block_scale_bytes(int outer, int red);
+
+/*
+ * fp8_block_cast -- x [rows, cols] to codes of 1x128 blocks (`row`; scales of
+ * outer = rows) and / or of 128x1 blocks (`col`; outer = cols), reading x once.
+ * The first are operands of products that reduce over the columns (forward,
+ * dgrad), the second of those that reduce over the rows (wgrad).
+ *   dtype     FP8_DT_F32, FP8_DT_BF16 or FP8_DT_F16
+ *   fmt       FP8_E4M3 or FP8_E5M2;  margin 0..64
+ *   row, col  HOST structs, or NULL (not both)
+ * rows == 0 or cols == 0 is a no-op.
+ */
+int fp8_block_cast(const void *x, int dtype, int rows, int cols, size_t ldx, int fmt, int margin,
+                   const fp8_blocks *row, const fp8_blocks *col, void *stream);
+
+/*
+ * fp8_block_cast_square -- x to codes of 128x128 blocks (weights): one set of
+ * codes and both orders of its scales, out->s for products that reduce over
+ * the columns (outer = rows) and s_col (outer = cols) for those over the rows.
+ */
+int fp8_block_cast_square(const void *x, int dtype, int rows, int cols, size_t ldx, int fmt, int margin,
+                          const fp8_blocks *out, uint8_t *s_col, void *stream);
+
+/*
+ * fp8_block_decode -- x = dec(q) * 2^(byte - 127), rounded to dtype.
+ *   axis  1: the scales are blocks along the columns (1x128, or out->s of a
+ *         square cast); 0: along the rows (128x1, or its s_col)
+ */
+int fp8_block_decode(const fp8_blocks *in, int fmt, int axis, int rows, int cols, void *x, int dtype, size_t ldx,
+                     void *stream);
+
+/*
+ * Linear-layer products on such operands (shapes as fp8_linear_*; each operand
+ * read in place).  The tensor core applies the scales while it multiplies;
+ * the binary32 accumulator is the finished product, rounded once after the
+ * bias.  Any M, N, K >= 0 (an empty reduction gives the bias or 0).  Output
+ * types as fp8_linear_*.  The result's scale 2^(sum of the two exponents)
+ * must keep the product a binary32 number.
+ *   fwd    Y[M,N]  = X . W^T (+ bias[N])   x [M,K], w [N,K] E4M3, scales along K
+ *   dgrad  dX[M,K] = dY . W                dy [M,N] dy_fmt, scales along N; w [N,K] E4M3
+ *                                          with scales along N (w->s of outer = K)
+ *   wgrad  dW[N,K] = dY^T . X              dy [M,N] dy_fmt, x [M,K] E4M3, scales along M
+ * dy_fmt: FP8_E5M2 or FP8_E4M3.
+ */
+int fp8_block_linear_fwd(const fp8_blocks *x, const fp8_blocks *w, const void *bias, int bias_dtype, void *y,
+                         int y_dtype, size_t ldy, int M, int N, int K, void *stream);
+/* The forward product of at most FP8_BLOCK_TOKENS_MAX tokens from their
+ * high-precision x [M,K] of x_dtype: its cast to E4M3 1x128 blocks (as
+ * fp8_block_cast with this margin) and the product in one launch.  The codes
+ * are the same; the result may differ from the two calls' by the order in
+ * which partial sums of the reduction are added. */
+#define FP8_BLOCK_TOKENS_MAX 32
+int fp8_block_linear_tokens(const void *x, int x_dtype, size_t ldx, int margin, const fp8_blocks *w, const void *bias,
+                            int bias_dtype, void *y, int y_dtype, size_t ldy, int M, int N, int K, void *stream);
+
+int fp8_block_linear_dgrad(const fp8_blocks *dy, int dy_fmt, const fp8_blocks *w, void *dx, int dx_dtype,
+                           size_t lddx, int M, int N, int K, void *stream);
+int fp8_block_linear_wgrad(const fp8_blocks *dy, int dy_fmt, const fp8_blocks *x, void *dw, int dw_dtype,
+                           size_t lddw, int M, int N, int K, void *stream);
+
+/*
+ * Activation functions with an 8-bit checkpoint.  act: FP8_ACT_GELU_TANH
+ * 0.5 h (1 + tanh(sqrt(2/pi) (h + 0.044715 h^3))), FP8_ACT_GELU_ERF
+ * 0.5 h (1 + erf(h / sqrt 2)), FP8_ACT_SILU h / (1 + exp(-h)).
+ *
+ * fp8_act_fwd -- from h [rows, cols] of dtype: `ckpt`, E4M3 codes of h's
+ * 1x128 blocks (what the backward pass needs of this layer); optionally
+ * `a_row`, E4M3 codes of act(h)'s 1x128 blocks (the next product's operand),
+ * and a, act(h) in dtype.
+ */
+#define FP8_ACT_GELU_TANH 0
+#define FP8_ACT_GELU_ERF 1
+#define FP8_ACT_SILU 2
+int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int act, int margin,
+                const fp8_blocks *ckpt, const fp8_blocks *a_row, void *a, size_t lda, void *stream);
+
+/*
+ * fp8_act_bwd -- from the checkpoint's h' = dec(ckpt) and da [rows, cols] of
+ * dtype, dh = da * act'(h') in any of: dh_row / dh_col, codes of fmt of its
+ * 1x128 / 128x1 blocks (the operands of dgrad / wgrad), and dh in dtype; and
+ * a_col, E4M3 codes of the 128x1 blocks of act(h') (the following layer's
+ * wgrad operand, which the forward pass then need not keep).  Outputs not
+ * wanted are NULL (not all).  Codes are cast from the binary32 values.
+ */
+int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int cols, size_t ldda, int act, int fmt,
+                int margin, const fp8_blocks *dh_row, const fp8_blocks *dh_col, const fp8_blocks *a_col, void *dh,
+                size_t lddh, void *stream);
 
 /* Human-readable message of a status code (static string). */
 const char *fp8_strerror(int code);
