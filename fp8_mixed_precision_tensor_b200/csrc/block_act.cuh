@@ -19,67 +19,88 @@ namespace fp8lib {
 namespace block {
 
 // All three functions have the form act(h) = h * g(h) with a gate g that goes
-// from 0 to 1:  SiLU g = s(h);  tanh GELU g = s(2 c (h + 0.044715 h^3)),
-// c = sqrt(2/pi) (since (1 + tanh(u)) / 2 = s(2u));  GELU g = Phi(h).
-// q = 1 - g is computed on its own (not by subtraction), so that the small
-// one of the two keeps its relative accuracy, and dg = g'(h).  __expf: error
-// at most 2 + 1.17 |x| units in the last place of a number that scales a
-// value already far below 1.
-struct Gate {
-  float h;  // the argument, limited to +-110 (where exp(-|h|) is 0 in binary32)
-  float g, q, dg;
-};
+// from 0 to 1 and satisfies g(-h) = 1 - g(h):  SiLU g = s(h);  tanh GELU g =
+// s(2 c (h + 0.044715 h^3)), c = sqrt(2/pi) (since (1 + tanh(u)) / 2 = s(2u));
+// GELU g = Phi(h).  With y = |h| and p = g(-y) = 1 - g(y), the small one of the
+// two, computed on its own so that it keeps its relative accuracy,
+//   act(h)  = max(h, 0) - y p
+//   act'(h) = (h >= 0 ? 1 : 0) + sign(h) r,   r = y g'(y) - p,
+// and for the sigmoid gates g' = p (1 - p) u', so r = p (y (1 - p) u' - 1).
+//
+// For h > 0 act(h) lies below h, possibly by less than binary32 shows.
+// Rounded to nearest it would become h itself, and h, a 16-bit number, sits
+// exactly on an FP8 rounding border one time in sixteen: the tie would then go
+// to the even code where the true value goes to the lower one.  So y p is
+// subtracted rounding toward zero, and da act' = da + da r is rounded to the
+// side of da on which it lies; a p that has underflowed counts as the smallest
+// normal number (r is then positive).
+// ex2.approx and rcp.approx are within 2 units in the last place, and the
+// argument's rounding adds about |u| units to exp(-u).
+constexpr float kTiny = 1.17549435e-38f;
+constexpr float kLog2e = 1.4426950408889634f;
 
-template <int ACT>
-__device__ __forceinline__ Gate gate_of(float h0) {
-  Gate r;
-  const float h = h0 > 110.0f ? 110.0f : (h0 < -110.0f ? -110.0f : h0);  // a NaN stays
-  r.h = h;
-  if constexpr (ACT == FP8_ACT_GELU_ERF) {
-    const float z = fabsf(h) * 0.70710678118654752f;
-    const float small = 0.5f * erfcf(z), big = 1.0f - small;
-    r.g = h > 0.0f ? big : small;
-    r.q = h > 0.0f ? small : big;
-    r.dg = __expf(-z * z) * 0.39894228040143268f;
-  } else {
-    float u = h, du = 1.0f;
-    if constexpr (ACT == FP8_ACT_GELU_TANH) {
-      const float c = 1.5957691216057308f, h2 = h * h;  // 2 sqrt(2/pi)
-      u = c * (h + 0.044715f * h2 * h);
-      du = c + (3.0f * 0.044715f * c) * h2;
-    }
-    const float e = __expf(-fabsf(u));
-    const float big = __fdividef(1.0f, 1.0f + e), small = e * big;
-    r.g = h > 0.0f ? big : small;
-    r.q = h > 0.0f ? small : big;
-    r.dg = big * small * du;
-  }
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
-// act(h).  For h > 0 the value h - h q lies below h, possibly by less than
-// binary32 shows.  Rounded to nearest it would become h itself, and h, a
-// 16-bit number, sits exactly on an FP8 rounding border one time in sixteen:
-// the tie would then go to the even code where the true value goes to the
-// lower one.  Rounding toward zero keeps it below; a q that has underflowed
-// counts as the smallest normal number.
-__device__ __forceinline__ float act_value(const Gate &t, float h) {
-  constexpr float tiny = 1.17549435e-38f;
-  if (h > 0.0f) return __fmaf_rz(-t.h, fmaxf(t.q, tiny), h);
-  return t.h * t.g;
+// The gates of two elements, on the packed binary32 instructions (two results
+// per issue slot): y = |h|, at most 110 (exp(-110) is 0 in binary32; a NaN
+// stays), p and, with GRAD, r.
+template <int ACT, bool GRAD>
+__device__ __forceinline__ void gate2(float2 h, float2 &y, float2 &p, float2 &r) {
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y.x) : "f"(fabsf(h.x)), "f"(110.0f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y.y) : "f"(fabsf(h.y)), "f"(110.0f));
+  const float lx = (__float_as_uint(h.x) >> 31) ? 0.0f : kTiny, ly = (__float_as_uint(h.y) >> 31) ? 0.0f : kTiny;
+  if constexpr (ACT == FP8_ACT_GELU_ERF) {
+    p = make_float2(fmaxf(0.5f * erfcf(y.x * 0.70710678118654752f), lx),
+                    fmaxf(0.5f * erfcf(y.y * 0.70710678118654752f), ly));
+    if constexpr (GRAD) {
+      const float2 a = __fmul2_rn(__fmul2_rn(y, y), both(-0.5f * kLog2e));
+      const float2 s = __fmul2_rn(make_float2(exp2_approx(a.x), exp2_approx(a.y)), both(0.39894228040143268f));
+      r = __ffma2_rn(y, make_float2(fmaxf(s.x, lx), fmaxf(s.y, ly)), make_float2(-p.x, -p.y));
+    }
+  } else {
+    constexpr float c = 1.5957691216057308f;  // 2 sqrt(2/pi)
+    float2 a, du = both(1.0f);
+    if constexpr (ACT == FP8_ACT_GELU_TANH) {
+      const float2 y2 = __fmul2_rn(y, y);
+      a = __fmul2_rn(y, __ffma2_rn(both(-0.044715f * c * kLog2e), y2, both(-c * kLog2e)));
+      du = __ffma2_rn(both(3.0f * 0.044715f * c), y2, both(c));
+    } else {
+      a = __fmul2_rn(y, both(-kLog2e));
+    }
+    const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
+    const float2 o = __fadd2_rn(e, both(1.0f));
+    const float2 big = make_float2(rcp_approx(o.x), rcp_approx(o.y));
+    p = __fmul2_rn(e, big);
+    p = make_float2(fmaxf(p.x, lx), fmaxf(p.y, ly));
+    if constexpr (GRAD) {
+      const float2 yb = __fmul2_rn(y, big);
+      const float2 w = ACT == FP8_ACT_GELU_TANH ? __ffma2_rn(yb, du, both(-1.0f)) : __fadd2_rn(yb, both(-1.0f));
+      r = __fmul2_rn(p, w);
+    }
+  }
 }
 
-// da * act'(h), act' = g + h g' = 1 + r with r = h g' - q.  For h > 0 the
-// product is da + da r, rounded to the side of da on which it lies, for the
-// same reason (r is positive where both its terms have underflowed).
-__device__ __forceinline__ float act_grad(const Gate &t, float h, float da) {
-  constexpr float tiny = 1.17549435e-38f;
-  if (h > 0.0f) {
-    float r = __fmaf_rn(t.h, t.dg, -t.q);
-    if (r == 0.0f) r = tiny;
-    return (da > 0.0f) == (r > 0.0f) ? __fmaf_ru(da, r, da) : __fmaf_rd(da, r, da);
-  }
-  return da * __fmaf_rn(t.h, t.dg, t.g);
+__device__ __forceinline__ float2 act_value2(float2 h, float2 y, float2 p) {
+  return __ffma2_rz(make_float2(-y.x, -y.y), p, make_float2(fmaxf(h.x, 0.0f), fmaxf(h.y, 0.0f)));
+}
+
+__device__ __forceinline__ float2 act_grad2(float2 h, float2 r, float2 da) {
+  // r with the sign of h; da or, for h < 0, 0
+  const uint32_t sx = __float_as_uint(h.x) & 0x80000000u, sy = __float_as_uint(h.y) & 0x80000000u;
+  r = make_float2(__uint_as_float(__float_as_uint(r.x) ^ sx), __uint_as_float(__float_as_uint(r.y) ^ sy));
+  const float2 base = make_float2(sx ? 0.0f : da.x, sy ? 0.0f : da.y);
+  const float2 up = __ffma2_ru(da, r, base), down = __ffma2_rd(da, r, base);
+  return make_float2((int)(__float_as_uint(da.x) ^ __float_as_uint(r.x)) < 0 ? down.x : up.x,
+                     (int)(__float_as_uint(da.y) ^ __float_as_uint(r.y)) < 0 ? down.y : up.y);
 }
 
 struct ActFwd {
@@ -93,42 +114,42 @@ struct ActFwd {
   size_t lda_q;
   void *a;           // a itself in h's type, or null
   size_t lda;
+  int vec_h, vec_a;  // rows of h / a start on 16-byte boundaries
 };
 
 // HBM-bound: h is read once (2 B at 16 bits), one or two code bytes and / or
-// a are written.  A row's 128-block is 16 neighbouring lanes, its amax four
-// shuffles; nothing is shared between rows, so there is no barrier.
-template <int DT, int ACT, bool VEC>
-__global__ void __launch_bounds__(kCastThreads) k_act_fwd(const ActFwd p) {
+// a are written.  512 threads with four rows each: act(h) of a thread's 32
+// elements waits in registers for its rows' amaxes (eight rows each needed
+// 184 registers and ran at a third of the occupancy).
+template <int DT, int ACT>
+__global__ void __launch_bounds__(kActThreads, 2) k_act_fwd(const ActFwd p) {
+  constexpr int RP = 4;
   const int tiles_c = (p.cols + kTile - 1) / kTile;
   const long long tiles = (long long)((p.rows + kTile - 1) / kTile) * tiles_c;
   const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile;
     const int col = col0 + c8 * 8;
-#pragma unroll 2
-    for (int i = 0; i < kRowsPer; i++) {
-      const int row = row0 + r0 + 16 * i;
-      float h[8], a[8];
-      load8<DT, VEC>(p.h, p.ldh, row, col, p.rows, p.cols, h);
-      uint32_t mh = 0, ma = 0;
+    Raw8<DT> raw[RP];
+    load_tile<DT>(p.h, p.ldh, p.vec_h, row0, col0, p.rows, p.cols, raw);
+    cast_raw_rows<DT, FP8_E4M3>(raw, p.cq, p.cs, p.ldc, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
+    if (p.aq || p.a) {
+      float f[RP][8];
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        a[j] = act_value(gate_of<ACT>(h[j]), h[j]);
-        mh = max(mh, absbits_f32(h[j]));
-        ma = max(ma, absbits_f32(a[j]));
+      for (int i = 0; i < RP; i++) {
+        unpack8<DT>(raw[i], f[i]);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float2 h = make_float2(f[i][j], f[i][j + 1]);
+          float2 y, q, r;
+          gate2<ACT, false>(h, y, q, r);
+          const float2 a = act_value2(h, y, q);
+          f[i][j] = a.x;
+          f[i][j + 1] = a.y;
+        }
+        if (p.a) store8<DT>(p.vec_a, p.a, p.lda, row0 + r0 + Geo<RP>::kStep * i, col, p.rows, p.cols, f[i]);
       }
-      mh = max16(mh);
-      const int kh = block_exponent(mh, kMaxE4M3, p.margin);
-      if (c8 == 0) put_scale(p.cs, row, col0 / kTile, tiles_c, kh);
-      cast_row8<FP8_E4M3>(p.cq, p.ldc, row, col, p.rows, p.cols, h, pow2f(kh));
-      if (p.aq) {
-        ma = max16(ma);
-        const int ka = block_exponent(ma, kMaxE4M3, p.margin);
-        if (c8 == 0) put_scale(p.as, row, col0 / kTile, tiles_c, ka);
-        cast_row8<FP8_E4M3>(p.aq, p.lda_q, row, col, p.rows, p.cols, a, pow2f(ka));
-      }
-      if (p.a) store8<DT, VEC>(p.a, p.lda, row, col, p.rows, p.cols, a);
+      if (p.aq) cast_tile_rows<FP8_E4M3>(f, p.aq, p.as, p.lda_q, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
     }
   }
 }
@@ -145,41 +166,113 @@ struct ActBwd {
   size_t ldaqt;
   void *dh_hp;         // dh itself in da's type, or null
   size_t lddh;
+  int vec_da, vec_dh;  // rows of da / dh start on 16-byte boundaries
 };
 
-// One pass over a 128x128 tile: 1 + 2 B read, up to 3 code bytes (or 2 B of
-// dh) written.  dh and act(h') of the tile stay in registers between the
-// amaxes and the encoding.  GFMT: format of dh's codes.
-template <int DT, int ACT, int GFMT, bool VEC>
-__global__ void __launch_bounds__(kCastThreads) k_act_bwd(const ActBwd p) {
-  __shared__ ColScratch sc[2];
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, int bytes, bool in) {
+  const int n = in ? bytes : 0;  // the rest of the destination is zeroed
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// Shared memory of k_act_bwd: two buffers of a tile's codes and da, each
+// thread's own elements at its own places, so that a thread waits for its own
+// copies only.
+template <int DT>
+struct ActBwdSmem {
+  static constexpr int kDaBytes = kTile * kTile * (DT == FP8_DT_F32 ? 4 : 2);
+  static constexpr int kBuffer = kTile * kTile + kDaBytes;
+  static constexpr int kBytes = 2 * kBuffer;
+};
+
+// One pass over 128x128 tiles: 1 + 2 B read, up to 3 code bytes (or 2 B of dh)
+// written.  dh and act(h') of a thread's 32 elements stay in registers between
+// the amaxes and the encoding, which leaves room for one CTA of 16 warps per
+// SM; the next tile's inputs are copied into shared memory meanwhile.  Bound
+// by instruction issue as much as by HBM (about 30 per element).
+// GFMT: format of dh's codes.
+template <int DT, int ACT, int GFMT>
+__global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
+  constexpr int RP = 4, kVecs = Raw8<DT>::kWords / 4;
+  extern __shared__ __align__(16) uint8_t act_smem[];
+  __shared__ ColScratch<RP> sc[2];
   const int tiles_c = (p.cols + kTile - 1) / kTile;
   const long long tiles = (long long)((p.rows + kTile - 1) / kTile) * tiles_c;
   const int kg = (tiles_c + 3) / 4;
   const float gmax = GFMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
   const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
-  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+  const uint32_t smem = smem_u32(act_smem);
+  uint32_t sb[RP];  // scale bytes of the tile in the buffer
+  // Starts the copies of tile t into buffer b (tiles with a ragged or unaligned row are read directly instead).
+  auto prefetch = [&](long long t, int b) {
+    const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile, col = col0 + c8 * 8;
+    if (wide_tile(p.vec_da, col0, p.cols)) {
+      const uint32_t base = smem + b * ActBwdSmem<DT>::kBuffer;
+#pragma unroll
+      for (int i = 0; i < RP; i++) {
+        const int row = row0 + r0 + Geo<RP>::kStep * i;
+        const bool in = row < p.rows && col < p.cols;
+        const size_t r = in ? row : 0, c = in ? col : 0;
+        cp_async(base + (i * kActThreads + threadIdx.x) * 8, p.cq + r * p.ldc + c, 8, in);
+        const uint8_t *src = reinterpret_cast<const uint8_t *>(p.da) + (r * p.ldda + c) * (DT == FP8_DT_F32 ? 4 : 2);
+#pragma unroll
+        for (int v = 0; v < kVecs; v++)
+          cp_async(base + kTile * kTile + ((i * kVecs + v) * kActThreads + threadIdx.x) * 16, src + 16 * v, 16, in);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if ((long long)blockIdx.x < tiles) prefetch(blockIdx.x, 0);
+  int buf = 0;
+  for (long long t = blockIdx.x; t < tiles; t += gridDim.x, buf ^= 1) {
     const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile;
     const int col = col0 + c8 * 8;
-    float a[kRowsPer][8], d[kRowsPer][8];
 #pragma unroll
-    for (int i = 0; i < kRowsPer; i++) {
-      const int row = row0 + r0 + 16 * i;
-      load_codes8<FP8_E4M3>(p.cq, p.ldc, row, col, p.rows, p.cols, a[i]);
-      load8<DT, VEC>(p.da, p.ldda, row, col, p.rows, p.cols, d[i]);
+    for (int i = 0; i < RP; i++)
+      sb[i] = p.cs[scale_at(min(row0 + r0 + Geo<RP>::kStep * i, p.rows - 1), col0 / kTile, kg)];
+    if (t + gridDim.x < tiles) prefetch(t + gridDim.x, buf ^ 1);
+    else asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    float a[RP][8], d[RP][8];
+    if (wide_tile(p.vec_da, col0, p.cols)) {
+      const uint8_t *base = act_smem + buf * ActBwdSmem<DT>::kBuffer;
+#pragma unroll
+      for (int i = 0; i < RP; i++) {
+        decode8<FP8_E4M3>(*reinterpret_cast<const uint2 *>(base + (i * kActThreads + threadIdx.x) * 8), a[i]);
+        Raw8<DT> raw;
+#pragma unroll
+        for (int v = 0; v < kVecs; v++)
+          *reinterpret_cast<uint4 *>(&raw.w[4 * v]) = *reinterpret_cast<const uint4 *>(
+              base + kTile * kTile + ((i * kVecs + v) * kActThreads + threadIdx.x) * 16);
+        unpack8<DT>(raw, d[i]);
+      }
+    } else {
+      Raw8<DT> raw[RP];
+      load_tile<DT>(p.da, p.ldda, p.vec_da, row0, col0, p.rows, p.cols, raw);
+#pragma unroll
+      for (int i = 0; i < RP; i++) {
+        decode8<FP8_E4M3>(load_codes8(p.cq, p.ldc, row0 + r0 + Geo<RP>::kStep * i, col, p.rows, p.cols), a[i]);
+        unpack8<DT>(raw[i], d[i]);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kRowsPer; i++) {
-      const int row = row0 + r0 + 16 * i;
-      const float s = row < p.rows ? descale_of(p.cs[scale_at(row, col0 / kTile, kg)]) : 1.0f;
+    for (int i = 0; i < RP; i++) {
+      const float s = descale_of(sb[i]);
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const float h = a[i][j] * s;
-        const Gate t2 = gate_of<ACT>(h);
-        a[i][j] = act_value(t2, h);
-        d[i][j] = act_grad(t2, h, d[i][j]);
+      for (int j = 0; j < 8; j += 2) {
+        const float2 h = __fmul2_rn(make_float2(a[i][j], a[i][j + 1]), both(s));
+        float2 y, q, r;
+        gate2<ACT, true>(h, y, q, r);
+        const float2 v = act_value2(h, y, q), g = act_grad2(h, r, make_float2(d[i][j], d[i][j + 1]));
+        a[i][j] = v.x;
+        a[i][j + 1] = v.y;
+        d[i][j] = g.x;
+        d[i][j + 1] = g.y;
       }
-      if (p.dh_hp) store8<DT, VEC>(p.dh_hp, p.lddh, row, col, p.rows, p.cols, d[i]);
+      if (p.dh_hp)
+        store8<DT>(p.vec_dh, p.dh_hp, p.lddh, row0 + r0 + Geo<RP>::kStep * i, col, p.rows, p.cols, d[i]);
     }
     if (p.dh.q) cast_tile_rows<GFMT>(d, p.dh.q, p.dh.s, p.dh.ldq, row0, col0, p.rows, p.cols, gmax, p.margin);
     if (p.dh.qt)

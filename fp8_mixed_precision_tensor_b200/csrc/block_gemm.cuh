@@ -108,26 +108,32 @@ __device__ __forceinline__ void cast_tokens_stage(const BArgs &a, int k0, uint32
   const int c8 = lane & 15, half = lane >> 4;
 #pragma unroll 1
   for (int t0 = 0; t0 < a.cols; t0 += 8) {
-    float f[4][8];
+    block::Raw8<DT> raw[4];
+    if (block::wide_tile(a.x_vec, k0, a.x_cols)) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int t = t0 + 2 * i + half;
-      if (a.x_vec) block::load8<DT, true>(a.x, a.ldx, t, k0 + c8 * 8, a.cols, a.x_cols, f[i]);
-      else block::load8<DT, false>(a.x, a.ldx, t, k0 + c8 * 8, a.cols, a.x_cols, f[i]);
+      for (int i = 0; i < 4; i++)
+        raw[i] = block::load_raw8_wide<DT>(a.x, a.ldx, t0 + 2 * i + half, k0 + c8 * 8, a.cols, a.x_cols);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        raw[i] = block::load_raw8_single<DT>(a.x, a.ldx, t0 + 2 * i + half, k0 + c8 * 8, a.cols, a.x_cols);
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int t = t0 + 2 * i + half;
       uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < 8; j++) m = max(m, absbits_f32(f[i][j]));
-      m = block::max16(m);
+      for (int j = 0; j < block::Raw8<DT>::kWords; j++) m = block::max_words<DT>(m, raw[i].w[j]);
+      m = block::max16(block::word_abs<DT>(m));
       const int k = block::block_exponent(m, kMaxE4M3, a.margin);
       const float s = pow2f(k);
-      const uint32_t lo = enc4<FP8_E4M3>(f[i][0] * s, f[i][1] * s, f[i][2] * s, f[i][3] * s);
-      const uint32_t hi = enc4<FP8_E4M3>(f[i][4] * s, f[i][5] * s, f[i][6] * s, f[i][7] * s);
+      float f[8];
+      block::unpack8<DT>(raw[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; j++) f[j] *= s;
+      const uint2 c = block::enc8<FP8_E4M3>(f, m >= 0x7f800000u);
       const uint32_t at = tile + t * 128 + (((c8 >> 1) ^ (t & 7)) << 4) + (c8 & 1) * 8;
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(lo), "r"(hi) : "memory");
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(c.x), "r"(c.y) : "memory");
       if (c8 == 0)
         asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf + t * 16 + ((k0 >> 7) & 3)), "r"((uint32_t)(127 - k))
                      : "memory");
@@ -145,37 +151,40 @@ __device__ __forceinline__ void store_one(const BArgs &a, size_t at, float y) {
 // Output chunk of 32 accumulator columns of one lane.  Not swapped: out[row,
 // col0...]; swapped: out[col0 + j, row], so that the lanes of a warp write
 // neighbouring features of a token.
-__device__ __forceinline__ void store_out(const BArgs &a, const float (&v)[32], int n, int row, int col0) {
-  if (row >= a.rows) return;
+// bias: of feature col0 + lane (not swapped) or of this row's feature (swapped), loaded by the caller.
+__device__ __forceinline__ void store_out(const BArgs &a, float (&v)[32], int n, int row, int col0, float bias) {
   if (a.swap) {
-    const float b = a.bias ? load_bias(a.bias, a.bias_dtype, row) : 0.0f;
+    if (row >= a.rows) return;
 #pragma unroll
-    for (int j = 0; j < 32; j++) {
-      if (j < n && col0 + j < a.cols) {
-        store_one(a, (size_t)(col0 + j) * a.ld_out + row, a.bias ? __fadd_rn(v[j], b) : v[j]);
-      }
-    }
+    for (int j = 0; j < 32; j++)
+      if (j < n && col0 + j < a.cols)
+        store_one(a, (size_t)(col0 + j) * a.ld_out + row, a.bias ? __fadd_rn(v[j], bias) : v[j]);
     return;
   }
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < 32; j++) v[j] = __fadd_rn(v[j], __shfl_sync(0xffffffffu, bias, j));
+  }
+  if (row >= a.rows) return;
 #pragma unroll
   for (int c = 0; c < 32; c += 8) {
     if (c >= n || col0 + c >= a.cols) break;
     float f[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      f[j] = v[c + j];
-      if (a.bias && col0 + c + j < a.cols) f[j] = __fadd_rn(f[j], load_bias(a.bias, a.bias_dtype, col0 + c + j));
-    }
+    for (int j = 0; j < 8; j++) f[j] = v[c + j];
     const int cols = min(a.cols, col0 + n);
-#define FP8_STORE(DT)                                                                                       \
-  if (a.vec_out) block::store8<DT, true>(a.out, a.ld_out, row, col0 + c, a.rows, cols, f);                  \
-  else block::store8<DT, false>(a.out, a.ld_out, row, col0 + c, a.rows, cols, f)
-    if (a.out_dtype == FP8_DT_F32) { FP8_STORE(FP8_DT_F32); }
-    else if (a.out_dtype == FP8_DT_BF16) { FP8_STORE(FP8_DT_BF16); }
-    else if (a.out_dtype == FP8_DT_F16) { FP8_STORE(FP8_DT_F16); }
-    else { FP8_STORE(FP8_DT_BF16_RTO); }
+#define FP8_STORE(DT) block::store8<DT>(a.vec_out, a.out, a.ld_out, row, col0 + c, a.rows, cols, f)
+    if (a.out_dtype == FP8_DT_F32) FP8_STORE(FP8_DT_F32);
+    else if (a.out_dtype == FP8_DT_BF16) FP8_STORE(FP8_DT_BF16);
+    else if (a.out_dtype == FP8_DT_F16) FP8_STORE(FP8_DT_F16);
+    else FP8_STORE(FP8_DT_BF16_RTO);
 #undef FP8_STORE
   }
+}
+
+__device__ __forceinline__ float chunk_bias(const BArgs &a, int row, int col0) {
+  const int i = a.swap ? row : col0 + (int)(threadIdx.x & 31);
+  return a.bias && i < (a.swap ? a.rows : a.cols) ? load_bias(a.bias, a.bias_dtype, i) : 0.0f;
 }
 
 // ---------------------------------------------------------------------------
@@ -368,13 +377,14 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll 1
       for (int c = 0; c < args.bn; c += 32) {
         if (splits == 1 && col0 + c >= args.cols) break;
+        const float bias = splits == 1 ? chunk_bias(args, row, col0 + c) : 0.0f;
         uint32_t r[32];
         tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; j++) v[j] = __uint_as_float(r[j]);
         if (splits == 1) {
-          store_out(args, v, 32, row, col0 + c);
+          store_out(args, v, 32, row, col0 + c, bias);
         } else {  // partial tile, column by column: [bn][128] floats over the ring
 #pragma unroll
           for (int j = 0; j < 32; j++)
@@ -394,9 +404,10 @@ __global__ void __launch_bounds__(kThreads)
       const int per = args.bn / splits;  // a multiple of 4 (bn % 32 == 0, splits <= 8)
 #pragma unroll 1
       for (int c = rank * per; c < (rank + 1) * per; c += 4) {
+        const float bias = chunk_bias(args, row, col0 + c);
         float v[32];
 #pragma unroll
-        for (int j = 0; j < 4; j++) v[j] = 0.0f;
+        for (int j = 0; j < 32; j++) v[j] = 0.0f;
         for (int s = 0; s < splits; s++) {
           const uint32_t src = map_to_rank(base, (uint32_t)s);
 #pragma unroll
@@ -409,7 +420,7 @@ __global__ void __launch_bounds__(kThreads)
             v[j] = s == 0 ? x : __fadd_rn(v[j], x);
           }
         }
-        store_out(args, v, 4, row, col0 + c);
+        store_out(args, v, 4, row, col0 + c, bias);
       }
     }
     cluster_sync();  // no CTA leaves while another reads its partial tile

@@ -1031,10 +1031,9 @@ int fp8_block_cast(const void *x, int dtype, int rows, int cols, size_t ldx, int
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_fmt(fmt, [&](auto f) {
-      with_bool(wide_rows(x, dtype, ldx), [&](auto vec) {
-        block::k_block_cast<decltype(dt)::value, decltype(f)::value, decltype(vec)::value>
-            <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(x, rows, cols, ldx, margin, o);
-      });
+      block::k_block_cast<decltype(dt)::value, decltype(f)::value>
+          <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(x, rows, cols, ldx, wide_rows(x, dtype, ldx), margin,
+                                                                 o);
     });
   });
   return launch_rc();
@@ -1054,10 +1053,9 @@ int fp8_block_cast_square(const void *x, int dtype, int rows, int cols, size_t l
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_fmt(fmt, [&](auto f) {
-      with_bool(wide_rows(x, dtype, ldx), [&](auto vec) {
-        block::k_block_cast_square<decltype(dt)::value, decltype(f)::value, decltype(vec)::value>
-            <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(x, rows, cols, ldx, margin, o);
-      });
+      block::k_block_cast_square<decltype(dt)::value, decltype(f)::value>
+          <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(x, rows, cols, ldx, wide_rows(x, dtype, ldx), margin,
+                                                                 o);
     });
   });
   return launch_rc();
@@ -1077,10 +1075,8 @@ int fp8_block_decode(const fp8_blocks *in, int fmt, int axis, int rows, int cols
   with_dtype(dtype, [&](auto dt) {
     with_fmt(fmt, [&](auto f) {
       with_bool(axis == 0, [&](auto colblocks) {
-        with_bool(wide_rows(x, dtype, ldx), [&](auto vec) {
-          block::k_block_decode<decltype(dt)::value, decltype(f)::value, decltype(colblocks)::value, decltype(vec)::value>
-              <<<grid, block::kCastThreads, 0, s>>>(in->q, in->s, rows, cols, in->ld, x, ldx);
-        });
+        block::k_block_decode<decltype(dt)::value, decltype(f)::value, decltype(colblocks)::value>
+            <<<grid, block::kCastThreads, 0, s>>>(in->q, in->s, rows, cols, in->ld, x, ldx, wide_rows(x, dtype, ldx));
       });
     });
   });
@@ -1150,7 +1146,8 @@ int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int ac
   if (rc || (rc = check_blocks(ckpt, cols)) || (a_row && (rc = check_blocks(a_row, cols))) ||
       (a && (rc = check_matrix(a, dtype, cols, lda))))
     return rc;
-  block::ActFwd p = {h, rows, cols, ldh, margin, ckpt->q, ckpt->s, ckpt->ld, nullptr, nullptr, 0, a, lda};
+  block::ActFwd p = {h, rows, cols, ldh, margin, ckpt->q, ckpt->s, ckpt->ld, nullptr, nullptr, 0, a, lda,
+                     wide_rows(h, dtype, ldh), wide_rows(a, dtype, lda)};
   if (a_row) {
     p.aq = a_row->q;
     p.as = a_row->s;
@@ -1159,10 +1156,8 @@ int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int ac
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_act(act, [&](auto f) {
-      with_bool(wide_rows(h, dtype, ldh) && (!a || wide_rows(a, dtype, lda)), [&](auto vec) {
-        block::k_act_fwd<decltype(dt)::value, decltype(f)::value, decltype(vec)::value>
-            <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(p);
-      });
+      block::k_act_fwd<decltype(dt)::value, decltype(f)::value>
+          <<<tile_grid(rows, cols), block::kActThreads, 0, s>>>(p);
     });
   });
   return launch_rc();
@@ -1180,8 +1175,10 @@ int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int
       (dh_col && (rc = check_blocks(dh_col, cols))) || (a_col && (rc = check_blocks(a_col, cols))) ||
       (dh && (rc = check_matrix(dh, dtype, cols, lddh))))
     return rc;
+  DeviceInfo *d;
+  if ((rc = device_info(&d))) return rc;
   block::ActBwd p = {ckpt->q, ckpt->s, ckpt->ld, da, rows, cols, ldda, margin, cast_out(dh_row, dh_col),
-                     nullptr, nullptr, 0, dh, lddh};
+                     nullptr, nullptr, 0, dh, lddh, wide_rows(da, dtype, ldda), wide_rows(dh, dtype, lddh)};
   if (a_col) {
     p.aqt = a_col->q;
     p.ast = a_col->s;
@@ -1191,14 +1188,16 @@ int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int
   with_dtype(dtype, [&](auto dt) {
     with_act(act, [&](auto f) {
       with_fmt(fmt, [&](auto g) {
-        with_bool(wide_rows(da, dtype, ldda) && (!dh || wide_rows(dh, dtype, lddh)), [&](auto vec) {
-          block::k_act_bwd<decltype(dt)::value, decltype(f)::value, decltype(g)::value, decltype(vec)::value>
-              <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(p);
-        });
+        using K = decltype(dt);
+        const auto kernel = block::k_act_bwd<K::value, decltype(f)::value, decltype(g)::value>;
+        constexpr int smem = block::ActBwdSmem<K::value>::kBytes;
+        if ((rc = set_smem(kernel, smem))) return;
+        const unsigned tiles = tile_grid(rows, cols);
+        kernel<<<tiles < (unsigned)d->sms ? tiles : d->sms, block::kActThreads, smem, s>>>(p);
       });
     });
   });
-  return launch_rc();
+  return rc ? rc : launch_rc();
 }
 
 int fp8_get_status(unsigned *host_out, void *stream) {
