@@ -45,9 +45,19 @@ struct BArgs {
   int x_cols, x_vec, margin;
 };
 
+// Operands of a block-scaled MMA as finished values.  With the descriptors'
+// constant adds folded into unrolled cta_group::2 MMAs, this compiler (ptxas
+// 12.9.86) gave the instruction wrong descriptor words: every row read the
+// first rows' data, with the right scales.  A move that it cannot see through
+// prevents the folding.
+__device__ __forceinline__ void opaque(uint64_t &a, uint64_t &b) {
+  asm volatile("mov.b64 %0, %0;\n\tmov.b64 %1, %1;" : "+l"(a), "+l"(b));
+}
+
 // A block-scaled MMA, one CTA: D[tmem] (+)= A B with scales at sfa, sfb.
 __device__ __forceinline__ void tc_mma_bs(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
+  opaque(ad, bd);
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -432,6 +442,308 @@ __global__ void __launch_bounds__(kThreads)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(args.tmem_cols)
                  : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Pair kernel: a cluster of two CTAs on two SMs computes 256 x 256 tiles with
+// tcgen05.mma.cta_group::2, persistent over the tiles.  Each CTA loads its
+// 128 rows of A, its 128 columns of B (32 KB per stage, 5 stages) and, every
+// fourth block, the scales of its rows and of all 256 columns (each tensor
+// core multiplies 128 rows by all columns).
+//
+// Tensor memory: two 256-column accumulators and the scales do not fit side
+// by side in 512 columns, so the accumulators overlap by 32: the first is
+// columns 0..255, the second 224..479, the scales 480..511.  The epilogue
+// reads the shared 32 columns first and then lets the next tile's MMAs start;
+// by the time a warp says so for one tile it has read all of the tile before,
+// so that one signal covers both accumulators.  The gap between two tiles is
+// one barrier round trip and two TMEM loads.
+//   warp 0 TMA producer (both CTAs), warp 1 TMEM allocation and MMA issue
+//   (leader), warps 2-5 epilogue (both CTAs).
+constexpr int kP2Stages = 5;
+constexpr int kP2SfSlot = 512 + 1024;
+constexpr int kP2Acc1 = 224;    // first column of the second accumulator
+constexpr int kP2Sf = 480;      // two sets of scales, 16 columns each
+constexpr int kP2OutBoxes = 2;  // staging boxes per epilogue warp (stores pipelined)
+constexpr int kP2SmemBytes =
+    kP2Stages * (kPairStageBytes + kP2SfSlot) + 4 * kP2OutBoxes * kWideStageOutBytes + 256 + 1024;
+
+__device__ __forceinline__ void tc_mma_bs_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                               uint32_t sfb, uint32_t accumulate) {
+  opaque(ad, bd);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+
+// The copy of scales in both CTAs of the pair, each from its own shared memory.
+__device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_leader(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                                 uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar)
+      : "memory");
+}
+
+// A row's 32 values of two neighbouring columns each -> 16 packed words.
+template <int OUT>
+__device__ __forceinline__ uint32_t pack_out(float a, float b) {
+  if constexpr (OUT == FP8_DT_BF16_RTO) return bf16x2_rto(a, b);
+  if constexpr (OUT == FP8_DT_F16) return f16x2(a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <bool A_MN, bool B_MN, int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_bgemm2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+             const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+             const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ BArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *base_ptr = smem_raw + (base - raw);
+  const uint32_t out_stage0 = base + kP2Stages * kPairStageBytes;
+  const uint32_t sf0 = out_stage0 + 4 * kP2OutBoxes * kWideStageOutBytes;
+  const uint32_t bar0 = sf0 + kP2Stages * kP2SfSlot;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kP2Stages + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kP2Stages + b); };
+  auto sffree_bar = [&](int b) { return bar0 + 8u * (2 * kP2Stages + 2 + b); };
+  const uint32_t tempty_bar = bar0 + 8u * (2 * kP2Stages + 4);
+  const uint32_t drain_bar = bar0 + 8u * (2 * kP2Stages + 5);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (bar0 - base) + 8 * (2 * kP2Stages + 6));
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  auto coords = [&](int t, int &mb, int &nb) {
+    const int per_band = args.group_m * args.num_n_blocks;
+    const int band = t / per_band, first = band * args.group_m;
+    const int rows_in_band = min(args.num_m_blocks - first, args.group_m);
+    const int r = t - band * per_band;
+    mb = first + r % rows_in_band;
+    nb = r / rows_in_band;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kP2Stages; s++) {
+      mbar_init(full_bar(s), 1);   // leader: its producer's arrive + both CTAs' bytes
+      mbar_init(empty_bar(s), 1);  // one multicast commit per phase
+    }
+    for (int b = 0; b < 2; b++) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(sffree_bar(b), 1);
+    }
+    mbar_init(tempty_bar, 8);  // leader: 4 epilogue warps x 2 CTAs
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+    if (args.vec_out) tma_prefetch_desc(&tmOut);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs initialised before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producers (both CTAs, one thread)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true, issued = false;
+      for (int tile = pair; tile < args.num_tiles && ok; tile += num_pairs) {
+        int mb, nb;
+        coords(tile, mb, nb);
+        const int arow = mb * 256 + (int)rank * 128, bcol = nb * 256 + (int)rank * 128;
+        for (int kb = 0; kb < args.num_k_blocks; kb++) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
+          const uint32_t sa = base + stage * kPairStageBytes, sb = sa + kPairHalf * BK, ss = sf0 + stage * kP2SfSlot;
+          const uint32_t fb = map_to_rank(full_bar(stage), 0);
+          const bool scales = (kb & 3) == 0;
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), 2 * (kPairStageBytes + (scales ? kP2SfSlot : 0)));
+          if (scales) {
+            tma_load_3d_pair(ss, &tmSA, 0, kb >> 2, arow >> 7, fb);
+            tma_load_3d_pair(ss + 512, &tmSB, 0, kb >> 2, nb * 2, fb);
+          }
+          if (A_MN) tma_load_2d_pair(sa, &tmA, arow, kb * BK, fb);
+          else      tma_load_2d_pair(sa, &tmA, kb * BK, arow, fb);
+          if (B_MN) tma_load_2d_pair(sb, &tmB, bcol, kb * BK, fb);
+          else      tma_load_2d_pair(sb, &tmB, kb * BK, bcol, fb);
+          issued = true;
+          if (++stage == kP2Stages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok && issued) sleep_ns_bounded(50000);  // let copies in flight land
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader, one thread)
+    if (leader && lane == 0) {
+      const uint64_t a_d0 = operand_desc<A_MN>(base, 0), b_d0 = operand_desc<B_MN>(base + kPairHalf * BK, 0);
+      constexpr uint64_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
+      constexpr uint64_t b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
+      constexpr uint64_t st_d = kPairStageBytes >> 4;
+      int stage = 0, n = 0;
+      uint32_t phase = 0, group = 0;
+      bool ok = true, issued_any = false;
+      for (int tile = pair; tile < args.num_tiles && ok; tile += num_pairs, n++) {
+        if (n > 0 && !mbar_wait(tempty_bar, (uint32_t)(n - 1) & 1u, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (n & 1) * kP2Acc1;
+        for (int kb = 0; kb < args.num_k_blocks; kb++) {
+          if (!stage_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+          if ((kb & 3) == 0) {  // the set's last readers, two groups ago, have completed
+            const uint32_t set = group & 1u;
+            if (group >= 2 && !stage_ready(sffree_bar(set), ((group >> 1) - 1) & 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            const uint32_t sf = tmem_base + kP2Sf + set * 16, ss = sf0 + stage * kP2SfSlot;
+            tc_cp_scales_pair(sf, scale_desc(ss));
+            tc_cp_scales_pair(sf + 4, scale_desc(ss + 512));
+            tc_cp_scales_pair(sf + 8, scale_desc(ss + 1024));
+            group++;
+          }
+          const uint32_t sfa = tmem_base + kP2Sf + ((group - 1) & 1u) * 16;
+          const uint64_t so = (uint64_t)stage * st_d;
+          const uint32_t idesc = with_scale_ids(args.idesc, kb);
+#pragma unroll
+          for (int ks = 0; ks < BK / UMMA_K; ks++)
+            tc_mma_bs_pair(d_tmem, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, idesc, sfa, sfa + 4,
+                           (kb | ks) != 0 ? 1u : 0u);
+          tc_commit_pair(empty_bar(stage));
+          if ((kb & 3) == 3 || kb == args.num_k_blocks - 1) tc_commit_leader(sffree_bar((group - 1) & 1u));
+          issued_any = true;
+          if (++stage == kP2Stages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit_pair(tfull_bar(n & 1));
+      }
+      if (!ok && issued_any) {
+        tc_commit_leader(drain_bar);
+        mbar_wait_drain(drain_bar, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;
+    const uint32_t stg0 = out_stage0 + (warp - 2) * kP2OutBoxes * kWideStageOutBytes;
+    constexpr int kBox = OUT == FP8_DT_F32 ? 32 : 64;  // columns of one 128-byte box
+    constexpr int kNum = 256 / kBox;
+    uint32_t box = 0;
+    int n = 0;
+    for (int tile = pair; tile < args.num_tiles; tile += num_pairs, n++) {
+      int mb, nb;
+      coords(tile, mb, nb);
+      const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar(n & 1), (uint32_t)(n >> 1) & 1u, abort_flag));
+      if (!got) break;
+      tc_fence_after();
+      const int row0 = mb * 256 + (int)rank * kPairHalf + q * 32;
+      const uint32_t acc = tmem_base + ((uint32_t)(q * 32) << 16) + (n & 1) * kP2Acc1;
+#pragma unroll 1
+      for (int i = 0; i < kNum; i++) {
+        // the first accumulator's last columns, the second's first ones are shared: read them first
+        const int c = ((n & 1) ? i : (i + kNum - 1) % kNum) * kBox;
+        const int col0 = nb * 256 + c;
+        uint32_t w[32];
+        const float bias0 = chunk_bias(args, 0, col0);
+        const float bias1 = OUT == FP8_DT_F32 ? 0.0f : chunk_bias(args, 0, col0 + 32);
+        uint32_t r[32];
+        tmem_ld32(acc + c, r);
+        if (args.bias) {
+#pragma unroll
+          for (int j = 0; j < 32; j++)
+            r[j] = __float_as_uint(__fadd_rn(__uint_as_float(r[j]), __shfl_sync(0xffffffffu, bias0, j)));
+        }
+        if constexpr (OUT == FP8_DT_F32) {
+#pragma unroll
+          for (int j = 0; j < 32; j++) w[j] = r[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; j++) w[j] = pack_out<OUT>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+          tmem_ld32(acc + c + 32, r);
+          if (args.bias) {
+#pragma unroll
+            for (int j = 0; j < 32; j++)
+              r[j] = __float_as_uint(__fadd_rn(__uint_as_float(r[j]), __shfl_sync(0xffffffffu, bias1, j)));
+          }
+#pragma unroll
+          for (int j = 0; j < 16; j++)
+            w[16 + j] = pack_out<OUT>(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        }
+        if (i == 0) {  // the shared columns are read: the next tile may start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(map_to_rank(tempty_bar, 0));
+        }
+        if (!args.vec_out) {  // rows that do not start on 16-byte boundaries: element stores
+          const int row = row0 + lane;
+          if (row < args.rows) {
+            const size_t at = (size_t)row * args.ld_out + col0;
+#pragma unroll
+            for (int j = 0; j < kBox; j++) {
+              if (col0 + j < args.cols) {
+                if constexpr (OUT == FP8_DT_F32) reinterpret_cast<uint32_t *>(args.out)[at + j] = w[j];
+                else reinterpret_cast<uint16_t *>(args.out)[at + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+              }
+            }
+          }
+          continue;
+        }
+        const uint32_t stg = stg0 + box * kWideStageOutBytes;
+        box ^= 1u;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int ch = 0; ch < 8; ch++) {  // 16-byte chunk ch of this row, 128B swizzle
+          const uint32_t addr = stg + lane * 128 + ((ch ^ (lane & 7)) << 4);
+          st_shared_v4(addr, w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (row0 < args.rows && col0 < args.cols) tma_store_2d(&tmOut, stg, col0, row0);
+          bulk_commit();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait0();  // every store has landed before the CTA exits
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // the leader's MMAs no longer read this CTA's smem / TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
   }
 }
 

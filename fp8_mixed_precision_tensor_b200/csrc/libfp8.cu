@@ -844,28 +844,66 @@ block::CastOut cast_out(const fp8_blocks *row, const fp8_blocks *col) {
   return o;
 }
 
+struct BlockInfo {
+  bool ready = false;
+  int pair_clusters = 0;  // co-resident clusters of the pair kernel
+};
 std::mutex g_block_mu;
-bool g_block_ready[kMaxDevices];
+BlockInfo g_block[kMaxDevices];
 
 template <typename K>
 int set_max_smem(K kernel) {
   return set_smem(kernel, 232448);  // 227 KB, the most a CTA can ask for
 }
 
+template <bool A_MN, bool B_MN>
+int set_pair_smem() {
+  using bgemm::k_bgemm2;
+  return set_smem(k_bgemm2<A_MN, B_MN, FP8_DT_F32>, bgemm::kP2SmemBytes) |
+         set_smem(k_bgemm2<A_MN, B_MN, FP8_DT_BF16>, bgemm::kP2SmemBytes) |
+         set_smem(k_bgemm2<A_MN, B_MN, FP8_DT_F16>, bgemm::kP2SmemBytes) |
+         set_smem(k_bgemm2<A_MN, B_MN, FP8_DT_BF16_RTO>, bgemm::kP2SmemBytes);
+}
+
+void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int clusters, cudaStream_t stream) {
+  *cfg = {};
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = 2;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg->gridDim = dim3(2 * clusters);
+  cfg->blockDim = dim3(gemm::kThreads);
+  cfg->dynamicSmemBytes = bgemm::kP2SmemBytes;
+  cfg->stream = stream;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
 // One-time per-device attributes of the block-scaled kernels.
-int block_ready() {
+int block_info(DeviceInfo **d, BlockInfo **out) {
+  int rc0 = device_info(d);
+  if (rc0) return rc0;
   int dev;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FP8_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_block_mu);
-  if (g_block_ready[dev]) return FP8_OK;
+  BlockInfo &b = g_block[dev];
+  *out = &b;
+  if (b.ready) return FP8_OK;
   using bgemm::k_bgemm;
   constexpr int no = bgemm::kNoCast;
   int rc = set_max_smem(k_bgemm<false, false, no>) | set_max_smem(k_bgemm<false, true, no>) |
            set_max_smem(k_bgemm<true, false, no>) | set_max_smem(k_bgemm<true, true, no>) |
            set_max_smem(k_bgemm<false, false, FP8_DT_F32>) | set_max_smem(k_bgemm<false, false, FP8_DT_BF16>) |
            set_max_smem(k_bgemm<false, false, FP8_DT_F16>);
+  rc |= set_pair_smem<false, false>() | set_pair_smem<false, true>() | set_pair_smem<true, true>();
   if (rc) return FP8_ERR_CUDA;
-  g_block_ready[dev] = true;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  pair_config(&cfg, &attr, (*d)->sms / 2, nullptr);
+  if (cudaOccupancyMaxActiveClusters(&b.pair_clusters, bgemm::k_bgemm2<false, false, FP8_DT_BF16>, &cfg) !=
+      cudaSuccess)
+    return FP8_ERR_CUDA;
+  b.ready = true;
   return FP8_OK;
 }
 
@@ -890,6 +928,22 @@ int make_scale_map(CUtensorMap *m, const uint8_t *s, int outer, int red, uint32_
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(s), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FP8_OK : FP8_ERR_CUDA;
+}
+
+// Output rows `ld` elements apart -> TMA map for 32-row boxes of 128 bytes (make_out_map with a pitch).
+int make_pitched_out_map(CUtensorMap *m, void *out, int dtype, uint64_t rows, uint64_t cols, uint64_t ld) {
+  const CUtensorMapDataType t = dtype == FP8_DT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : dtype == FP8_DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t esz = dtype_bytes(dtype);
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld * esz};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / esz), 32};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(m, t, 2, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FP8_OK : FP8_ERR_CUDA;
 }
@@ -957,6 +1011,40 @@ int launch_bgemm(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, in
   return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm<A_MN, B_MN, XDT>, ma, mb, msa, msb, a, splits));
 }
 
+// C[rows, cols] on the pair kernel.
+template <bool A_MN, bool B_MN>
+int launch_bgemm2(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, int clusters, cudaStream_t stream) {
+  using namespace bgemm;
+  const int rows = a.rows, cols = a.cols;
+  a.num_m_blocks = (rows + 255) / 256;
+  a.num_n_blocks = (cols + 255) / 256;
+  a.num_tiles = a.num_m_blocks * a.num_n_blocks;
+  a.num_k_blocks = (K + gemm::BK - 1) / gemm::BK;
+  a.group_m = 8;
+  a.idesc = ((uint32_t)A.fmt << 7) | ((uint32_t)B.fmt << 10) | ((uint32_t)(A_MN ? 1 : 0) << 15) |
+            ((uint32_t)(B_MN ? 1 : 0) << 16) | ((uint32_t)(256 >> 3) << 17) | (1u << 23) | ((uint32_t)(256 >> 7) << 27);
+  CUtensorMap ma, mb, msa, msb, mo;
+  int rc = A_MN ? make_code_map(&ma, A.b->q, rows, K, A.b->ld, gemm::BK)
+                : make_code_map(&ma, A.b->q, K, rows, A.b->ld, 128);
+  if (rc) return rc;
+  rc = B_MN ? make_code_map(&mb, B.b->q, cols, K, B.b->ld, gemm::BK)
+            : make_code_map(&mb, B.b->q, K, cols, B.b->ld, 128);
+  if (rc) return rc;
+  if ((rc = make_scale_map(&msa, A.b->s, rows, K, 1))) return rc;
+  if ((rc = make_scale_map(&msb, B.b->s, cols, K, 2))) return rc;
+  mo = ma;  // unused by the element stores
+  if (a.vec_out && (rc = make_pitched_out_map(&mo, a.out, a.out_dtype, rows, cols, a.ld_out))) return rc;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  pair_config(&cfg, &attr, a.num_tiles < clusters ? a.num_tiles : clusters, stream);
+  switch (a.out_dtype) {
+    case FP8_DT_F32: return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm2<A_MN, B_MN, FP8_DT_F32>, ma, mb, msa, msb, mo, a));
+    case FP8_DT_BF16: return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm2<A_MN, B_MN, FP8_DT_BF16>, ma, mb, msa, msb, mo, a));
+    case FP8_DT_F16: return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm2<A_MN, B_MN, FP8_DT_F16>, ma, mb, msa, msb, mo, a));
+    default: return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm2<A_MN, B_MN, FP8_DT_BF16_RTO>, ma, mb, msa, msb, mo, a));
+  }
+}
+
 // Reduction splits for `tiles` tiles of kblocks blocks on `slots` resident
 // CTAs: doubled while every CTA stays resident and keeps two blocks.
 int pick_splits(long long tiles, int kblocks, int slots) {
@@ -993,8 +1081,8 @@ int run_bgemm(const BOperand &A, const BOperand &B, const void *bias, int bias_d
   }
   if ((rc = check_blocks(A.b, A_MN ? R : red))) return rc;
   if ((rc = check_blocks(B.b, B_MN ? C : red))) return rc;
-  if ((rc = device_info(&d))) return rc;
-  if ((rc = block_ready())) return rc;
+  BlockInfo *bi;
+  if ((rc = block_info(&d, &bi))) return rc;
   const int kblocks = (red + 127) / 128;
   if constexpr (!A_MN) {
     if (R <= 128) {  // few tokens: their rows become the tile's columns, the weights its 128 lanes
@@ -1006,6 +1094,9 @@ int run_bgemm(const BOperand &A, const BOperand &B, const void *bias, int bias_d
                                       stream);
     }
   }
+  const long long pair_tiles = (long long)((R + 255) / 256) * ((C + 255) / 256);
+  if (bi->pair_clusters > 0 && pair_tiles >= bi->pair_clusters)
+    return launch_bgemm2<A_MN, B_MN>(A, B, a, red, bi->pair_clusters, stream);
   const int bn = C <= 128 ? 128 : (long long)((R + 127) / 128) * ((C + 255) / 256) >= d->sms ? 256 : 128;
   const long long tiles = (long long)((R + 127) / 128) * ((C + bn - 1) / bn);
   return launch_bgemm<A_MN, B_MN>(A, B, a, red, bn, pick_splits(tiles, kblocks, bn == 256 ? d->sms : 2 * d->sms),
@@ -1101,7 +1192,8 @@ int fp8_block_linear_tokens(const void *x, int x_dtype, size_t ldx, int margin, 
   if (rc || (rc = check_matrix(y, y_dtype, N, ldy)) || (rc = check_blocks(w, K))) return rc;
   if (bias && reinterpret_cast<uintptr_t>(bias) % dtype_bytes(bias_dtype)) return FP8_ERR_UNALIGNED;
   DeviceInfo *d;
-  if ((rc = device_info(&d)) || (rc = block_ready())) return rc;
+  BlockInfo *bi;
+  if ((rc = block_info(&d, &bi))) return rc;
   bgemm::BArgs a = {};
   a.rows = N;
   a.cols = M;
