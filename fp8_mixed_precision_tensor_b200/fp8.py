@@ -136,8 +136,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the current stream's handle, without making a Stream object for it (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -439,143 +439,182 @@ def block_scales(outer: int, red: int, device="cuda") -> torch.Tensor:
     return torch.empty(fp8_block_scale_bytes(outer, red), dtype=torch.uint8, device=device)
 
 
-def _on_device(t: torch.Tensor, what: str) -> torch.Tensor:
-    if not t.is_cuda:
+# The argument checks below run on every call of a path whose kernels take a
+# few microseconds, so they read each tensor's properties once.
+_U8 = torch.uint8
+
+
+def _device(t: torch.Tensor, what: str) -> int:
+    """The device of a call: its first tensor's, which must be the current one."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("libfp8 takes device tensors")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{what} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _matrix(t: torch.Tensor, what: str, shape=None) -> tuple[int, int, int, int]:
-    """(pointer, rows, cols, row stride in elements) of a matrix whose rows are contiguous."""
-    _on_device(t, what)
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {'a matrix' if shape is None else tuple(shape)}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what}: the elements of a row must be contiguous (strides {t.stride()})")
-    if rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{what}: rows overlap (strides {t.stride()})")
-    return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols
+def _bad_matrix(t: torch.Tensor, what: str, rows: int, cols: int, dev: int) -> None:
+    """Names what _matrix found wrong."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the call's device is cuda:{dev}")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    raise ValueError(f"{what}: strides {t.stride()}; the elements of a row must be contiguous and rows must not overlap")
 
 
-def _hp_matrix(t: torch.Tensor, what: str, shape=None):
-    if t.dtype not in _DT:
+def _matrix(t: torch.Tensor, what: str, rows: int, cols: int, dev: int) -> int:
+    """Row stride in elements of a [rows, cols] matrix whose rows are contiguous."""
+    st = t.stride()
+    if (t.get_device() != dev or t.shape != (rows, cols) or (cols > 1 and st[1] != 1) or
+            (rows > 1 and st[0] < cols)):
+        _bad_matrix(t, what, rows, cols, dev)
+    return st[0] if rows > 1 else cols
+
+
+def _hp(t: torch.Tensor, what: str) -> int:
+    """Element type code of a high-precision tensor."""
+    dt = _DT.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{what}: dtype {t.dtype}, expected float32, bfloat16 or float16")
-    return _matrix(t, what, shape)
+    return dt
 
 
-def _blocks(q, s, what: str, shape, outer: int, red: int):
-    """fp8_blocks of a code matrix and its scale buffer."""
-    if q is None and s is None:
-        return None
+def _input(t: torch.Tensor, what: str):
+    """(dtype code, rows, cols, row stride, device) of a call's high-precision input."""
+    dt, dev = _hp(t, what), _device(t, what)
+    if t.dim() != 2:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected a matrix")
+    rows, cols = t.shape
+    return dt, rows, cols, _matrix(t, what, rows, cols, dev), dev
+
+
+def _blocks(q, s, what: str, rows: int, cols: int, outer: int, red: int, dev: int):
+    """fp8_blocks of a [rows, cols] code matrix and its scale buffer."""
     if q is None or s is None:
+        if q is s:
+            return None
         raise ValueError(f"{what}: codes and scales go together")
-    if q.dtype != torch.uint8 or s.dtype != torch.uint8:
+    if q.dtype is not _U8 or s.dtype is not _U8:
         raise TypeError(f"{what}: codes and scales are uint8")
-    ptr, rows, _, ld = _matrix(q, what, shape)
-    _on_device(s, f"{what} scales")
-    need = fp8_block_scale_bytes(outer, red)
-    if not s.is_contiguous() or s.numel() < need:
-        raise ValueError(f"{what}: scales are {need} contiguous bytes, got {s.numel()}")
-    return ctypes.byref(_Blocks(ptr, s.data_ptr(), -(-ld // 16) * 16 if rows <= 1 else ld))
+    ld = _matrix(q, what, rows, cols, dev)
+    need = -(-outer // 128) * -(-red // 512) * 512  # fp8_block_scale_bytes
+    if s.numel() < need or not s.is_contiguous() or s.get_device() != dev:
+        raise ValueError(f"{what}: scales are {need} contiguous bytes on cuda:{dev}, got {s.numel()} on {s.device}")
+    return ctypes.byref(_Blocks(q.data_ptr(), s.data_ptr(), ld if rows > 1 else (ld + 15) // 16 * 16))
 
 
-def _vector(t, what: str, n: int):
+def _vector(t, what: str, n: int, dev: int):
     if t is None:
         return None, 0
-    if t.dtype not in _DT:
-        raise TypeError(f"{what}: dtype {t.dtype}, expected float32, bfloat16 or float16")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what}: {n} contiguous elements expected")
-    return _on_device(t, what).data_ptr(), _DT[t.dtype]
+    dt = _hp(t, what)
+    if t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{what}: {n} contiguous elements on cuda:{dev} expected")
+    return t.data_ptr(), dt
+
+
+def _codes_shape(q: torch.Tensor, what: str):
+    """(rows, cols, device) of a call's leading code matrix."""
+    dev = _device(q, what)
+    if q.dim() != 2:
+        raise ValueError(f"{what}: shape {tuple(q.shape)}, expected a matrix")
+    rows, cols = q.shape
+    return rows, cols, dev
 
 
 def fp8_block_cast(x, fmt: int, margin: int, q_row=None, s_row=None, q_col=None, s_col=None, stream=None) -> None:
     """x [rows, cols] to codes of 1x128 blocks (q_row, s_row) and / or of 128x1
     blocks (q_col, s_col), reading x once."""
-    ptr, rows, cols, ld = _hp_matrix(x, "x")
-    _check(load_library().fp8_block_cast(ptr, _DT[x.dtype], rows, cols, ld, fmt, margin,
-                                         _blocks(q_row, s_row, "row blocks", x.shape, rows, cols),
-                                         _blocks(q_col, s_col, "column blocks", x.shape, cols, rows),
+    dt, rows, cols, ld, dev = _input(x, "x")
+    _check(load_library().fp8_block_cast(x.data_ptr(), dt, rows, cols, ld, fmt, margin,
+                                         _blocks(q_row, s_row, "row blocks", rows, cols, rows, cols, dev),
+                                         _blocks(q_col, s_col, "column blocks", rows, cols, cols, rows, dev),
                                          _stream(stream)), "fp8_block_cast")
 
 
 def fp8_block_cast_square(x, fmt: int, margin: int, q, s_row, s_col, stream=None) -> None:
     """x to codes of 128x128 blocks, their scales in both orders (s_row for
     products that reduce over the columns, s_col over the rows)."""
-    ptr, rows, cols, ld = _hp_matrix(x, "x")
-    row = _blocks(q, s_row, "blocks", x.shape, rows, cols)
-    _blocks(q, s_col, "blocks", x.shape, cols, rows)
-    _check(load_library().fp8_block_cast_square(ptr, _DT[x.dtype], rows, cols, ld, fmt, margin, row,
+    dt, rows, cols, ld, dev = _input(x, "x")
+    row = _blocks(q, s_row, "blocks", rows, cols, rows, cols, dev)
+    _blocks(q, s_col, "blocks", rows, cols, cols, rows, dev)
+    _check(load_library().fp8_block_cast_square(x.data_ptr(), dt, rows, cols, ld, fmt, margin, row,
                                                 s_col.data_ptr(), _stream(stream)), "fp8_block_cast_square")
 
 
 def fp8_block_decode(q, s, fmt: int, axis: int, x, stream=None) -> None:
     """x = the values of blocked codes; axis 1: blocks along the columns
     (1x128), 0: along the rows (128x1)."""
-    ptr, rows, cols, ld = _hp_matrix(x, "x")
-    b = _blocks(q, s, "blocks", x.shape, *((rows, cols) if axis else (cols, rows)))
-    _check(load_library().fp8_block_decode(b, fmt, axis, rows, cols, ptr, _DT[x.dtype], ld, _stream(stream)),
+    dt, rows, cols, ld, dev = _input(x, "x")
+    b = _blocks(q, s, "blocks", rows, cols, *((rows, cols) if axis else (cols, rows)), dev)
+    _check(load_library().fp8_block_decode(b, fmt, axis, rows, cols, x.data_ptr(), dt, ld, _stream(stream)),
            "fp8_block_decode")
+
+
+def _out(t, what: str, rows: int, cols: int, dev: int, rto: bool) -> tuple[int, int, int]:
+    """(pointer, type code, row stride) of a product's output."""
+    dt = _hp(t, what)
+    return t.data_ptr(), _out_dt(t, True) if rto else dt, _matrix(t, what, rows, cols, dev)
 
 
 def fp8_block_linear_fwd(xq, xs, wq, ws, y, bias=None, stream=None, rto=False) -> None:
     """y[M,N] = x . w^T (+ bias): xq [M,K] with scales of (M, K), wq [N,K] with scales of (N, K)."""
-    (M, K), N = xq.shape, wq.shape[0]
-    yp, _, _, ld = _hp_matrix(y, "y", (M, N))
-    bp, bdt = _vector(bias, "bias", N)
-    _check(load_library().fp8_block_linear_fwd(_blocks(xq, xs, "x", (M, K), M, K), _blocks(wq, ws, "w", (N, K), N, K),
-                                               bp, bdt, yp, _out_dt(y, rto), ld, M, N, K, _stream(stream)),
-           "fp8_block_linear_fwd")
+    M, K, dev = _codes_shape(xq, "x")
+    N = wq.shape[0]
+    yp, ydt, ld = _out(y, "y", M, N, dev, rto)
+    bp, bdt = (None, 0) if bias is None else _vector(bias, "bias", N, dev)
+    _check(load_library().fp8_block_linear_fwd(_blocks(xq, xs, "x", M, K, M, K, dev),
+                                               _blocks(wq, ws, "w", N, K, N, K, dev), bp, bdt, yp, ydt, ld, M, N, K,
+                                               _stream(stream)), "fp8_block_linear_fwd")
 
 
 def fp8_block_linear_tokens(x, wq, ws, y, bias=None, margin: int = 0, stream=None, rto=False) -> None:
     """y[M,N] = x . w^T (+ bias) for at most FP8_BLOCK_TOKENS_MAX tokens x [M,K]
     in float32, bfloat16 or float16: fp8_block_cast and fp8_block_linear_fwd in
     one launch."""
-    xp, M, K, ldx = _hp_matrix(x, "x")
+    dt, M, K, ldx, dev = _input(x, "x")
     N = wq.shape[0]
-    yp, _, _, ldy = _hp_matrix(y, "y", (M, N))
-    bp, bdt = _vector(bias, "bias", N)
-    _check(load_library().fp8_block_linear_tokens(xp, _DT[x.dtype], ldx, margin, _blocks(wq, ws, "w", (N, K), N, K),
-                                                  bp, bdt, yp, _out_dt(y, rto), ldy, M, N, K, _stream(stream)),
-           "fp8_block_linear_tokens")
+    yp, ydt, ldy = _out(y, "y", M, N, dev, rto)
+    bp, bdt = (None, 0) if bias is None else _vector(bias, "bias", N, dev)
+    _check(load_library().fp8_block_linear_tokens(x.data_ptr(), dt, ldx, margin,
+                                                  _blocks(wq, ws, "w", N, K, N, K, dev), bp, bdt, yp, ydt, ldy, M, N,
+                                                  K, _stream(stream)), "fp8_block_linear_tokens")
 
 
 def fp8_block_linear_dgrad(dyq, dys, dy_fmt: int, wq, ws_col, dx, stream=None, rto=False) -> None:
     """dx[M,K] = dy . w: dyq [M,N] with scales of (M, N), wq [N,K] with scales of (K, N)."""
-    (M, N), K = dyq.shape, wq.shape[1]
-    xp, _, _, ld = _hp_matrix(dx, "dx", (M, K))
-    _check(load_library().fp8_block_linear_dgrad(_blocks(dyq, dys, "dy", (M, N), M, N), dy_fmt,
-                                                 _blocks(wq, ws_col, "w", (N, K), K, N), xp, _out_dt(dx, rto), ld,
-                                                 M, N, K, _stream(stream)), "fp8_block_linear_dgrad")
+    M, N, dev = _codes_shape(dyq, "dy")
+    K = wq.shape[1]
+    xp, xdt, ld = _out(dx, "dx", M, K, dev, rto)
+    _check(load_library().fp8_block_linear_dgrad(_blocks(dyq, dys, "dy", M, N, M, N, dev), dy_fmt,
+                                                 _blocks(wq, ws_col, "w", N, K, K, N, dev), xp, xdt, ld, M, N, K,
+                                                 _stream(stream)), "fp8_block_linear_dgrad")
 
 
 def fp8_block_linear_wgrad(dyq, dys_col, dy_fmt: int, xq, xs_col, dw, stream=None, rto=False) -> None:
     """dw[N,K] = dy^T . x: dyq [M,N] with scales of (N, M), xq [M,K] with scales of (K, M)."""
-    (M, N), K = dyq.shape, xq.shape[1]
-    wp, _, _, ld = _hp_matrix(dw, "dw", (N, K))
-    _check(load_library().fp8_block_linear_wgrad(_blocks(dyq, dys_col, "dy", (M, N), N, M), dy_fmt,
-                                                 _blocks(xq, xs_col, "x", (M, K), K, M), wp, _out_dt(dw, rto), ld,
-                                                 M, N, K, _stream(stream)), "fp8_block_linear_wgrad")
+    M, N, dev = _codes_shape(dyq, "dy")
+    K = xq.shape[1]
+    wp, wdt, ld = _out(dw, "dw", N, K, dev, rto)
+    _check(load_library().fp8_block_linear_wgrad(_blocks(dyq, dys_col, "dy", M, N, N, M, dev), dy_fmt,
+                                                 _blocks(xq, xs_col, "x", M, K, K, M, dev), wp, wdt, ld, M, N, K,
+                                                 _stream(stream)), "fp8_block_linear_wgrad")
 
 
 # ---------------------------------------------------------------- activations with an 8-bit checkpoint
 def fp8_act_fwd(h, act: int, margin: int, ckpt_q, ckpt_s, a_q=None, a_s=None, a=None, stream=None) -> None:
     """From h: the E4M3 checkpoint (1x128 blocks), and optionally the E4M3
     codes of act(h)'s 1x128 blocks and act(h) itself (h's dtype)."""
-    ptr, rows, cols, ld = _hp_matrix(h, "h")
+    dt, rows, cols, ld, dev = _input(h, "h")
     ap, lda = None, 0
     if a is not None:
-        if a.dtype != h.dtype:
+        if a.dtype is not h.dtype:
             raise TypeError("a has h's dtype")
-        ap, _, _, lda = _hp_matrix(a, "a", h.shape)
-    _check(load_library().fp8_act_fwd(ptr, _DT[h.dtype], rows, cols, ld, act, margin,
-                                      _blocks(ckpt_q, ckpt_s, "checkpoint", h.shape, rows, cols),
-                                      _blocks(a_q, a_s, "a blocks", h.shape, rows, cols), ap, lda, _stream(stream)),
-           "fp8_act_fwd")
+        ap, lda = a.data_ptr(), _matrix(a, "a", rows, cols, dev)
+    _check(load_library().fp8_act_fwd(h.data_ptr(), dt, rows, cols, ld, act, margin,
+                                      _blocks(ckpt_q, ckpt_s, "checkpoint", rows, cols, rows, cols, dev),
+                                      _blocks(a_q, a_s, "a blocks", rows, cols, rows, cols, dev), ap, lda,
+                                      _stream(stream)), "fp8_act_fwd")
 
 
 def fp8_act_bwd(ckpt_q, ckpt_s, da, act: int, fmt: int = FP8_E5M2, margin: int = 0, dh_q=None, dh_s=None,
@@ -583,17 +622,17 @@ def fp8_act_bwd(ckpt_q, ckpt_s, da, act: int, fmt: int = FP8_E5M2, margin: int =
     """From the checkpoint and da: codes of dh = da * act'(h') in 1x128 blocks
     (dh_q, dh_s) and 128x1 blocks (dh_q_col, dh_s_col), E4M3 codes of act(h')
     in 128x1 blocks (a_q_col, a_s_col), and dh itself (da's dtype); any of them."""
-    ptr, rows, cols, ld = _hp_matrix(da, "da")
+    dt, rows, cols, ld, dev = _input(da, "da")
     hp, lddh = None, 0
     if dh is not None:
-        if dh.dtype != da.dtype:
+        if dh.dtype is not da.dtype:
             raise TypeError("dh has da's dtype")
-        hp, _, _, lddh = _hp_matrix(dh, "dh", da.shape)
-    _check(load_library().fp8_act_bwd(_blocks(ckpt_q, ckpt_s, "checkpoint", da.shape, rows, cols), ptr,
-                                      _DT[da.dtype], rows, cols, ld, act, fmt, margin,
-                                      _blocks(dh_q, dh_s, "dh row blocks", da.shape, rows, cols),
-                                      _blocks(dh_q_col, dh_s_col, "dh column blocks", da.shape, cols, rows),
-                                      _blocks(a_q_col, a_s_col, "a column blocks", da.shape, cols, rows),
+        hp, lddh = dh.data_ptr(), _matrix(dh, "dh", rows, cols, dev)
+    _check(load_library().fp8_act_bwd(_blocks(ckpt_q, ckpt_s, "checkpoint", rows, cols, rows, cols, dev),
+                                      da.data_ptr(), dt, rows, cols, ld, act, fmt, margin,
+                                      _blocks(dh_q, dh_s, "dh row blocks", rows, cols, rows, cols, dev),
+                                      _blocks(dh_q_col, dh_s_col, "dh column blocks", rows, cols, cols, rows, dev),
+                                      _blocks(a_q_col, a_s_col, "a column blocks", rows, cols, cols, rows, dev),
                                       hp, lddh, _stream(stream)), "fp8_act_bwd")
 
 
