@@ -123,6 +123,8 @@ struct ActFwd {
 // 184 registers and ran at a third of the occupancy).
 template <int DT, int ACT>
 __global__ void __launch_bounds__(kActThreads, 2) k_act_fwd(const ActFwd p) {
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr int RP = 4;
   const int tiles_c = (p.cols + kTile - 1) / kTile;
   const long long tiles = (long long)((p.rows + kTile - 1) / kTile) * tiles_c;
@@ -195,6 +197,8 @@ struct ActBwdSmem {
 // GFMT: format of dh's codes.
 template <int DT, int ACT, int GFMT>
 __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr int RP = 4, kVecs = Raw8<DT>::kWords / 4;
   extern __shared__ __align__(16) uint8_t act_smem[];
   __shared__ ColScratch<RP> sc[2];

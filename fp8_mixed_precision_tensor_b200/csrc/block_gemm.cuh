@@ -31,7 +31,7 @@ struct BArgs {
   int bn;                      // output columns per tile (a multiple of 32, at most 256)
   int stages, sf_atoms_b;      // ring depth; 512-byte scale groups loaded per tile for B
   uint32_t stage_bytes, tmem_cols;
-  uint32_t idesc;
+  uint32_t idesc, desc_hi;
   const void *bias;            // per output feature, or null
   int bias_dtype;
   void *out;
@@ -45,24 +45,24 @@ struct BArgs {
   int x_cols, x_vec, margin;
 };
 
-// Operands of a block-scaled MMA as finished values.  With the descriptors'
-// constant adds folded into unrolled cta_group::2 MMAs, this compiler (ptxas
-// 12.9.86) gave the instruction wrong descriptor words: every row read the
-// first rows' data, with the right scales.  A move that it cannot see through
-// prevents the folding.
-__device__ __forceinline__ void opaque(uint64_t &a, uint64_t &b) {
-  asm volatile("mov.b64 %0, %0;\n\tmov.b64 %1, %1;" : "+l"(a), "+l"(b));
-}
+// Shared-memory descriptors of the block-scaled MMAs are passed as two words:
+// the low one (address and leading offset) advances by 32-bit adds that cannot
+// carry, the high one (stride, version, swizzle) comes from the kernel's
+// arguments.  With 64-bit descriptors of constant high part in unrolled
+// cta_group::2 MMAs this compiler (ptxas 12.9.86) gave the instruction wrong
+// descriptors, depending on the code around it: every row was multiplied with
+// the first rows' data, at the right scales.
+constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29);  // 8-row groups 1024 B apart, 128-byte swizzle
 
 // A block-scaled MMA, one CTA: D[tmem] (+)= A B with scales at sfa, sfb.
-__device__ __forceinline__ void tc_mma_bs(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
-                                          uint32_t sfb, uint32_t accumulate) {
-  opaque(ad, bd);
+__device__ __forceinline__ void tc_mma_bs(uint32_t d, uint32_t ad, uint32_t bd, uint32_t hi, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
-      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+      "r"(ad), "r"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(hi)
       : "memory");
 }
 
@@ -109,45 +109,59 @@ constexpr int kMaxStages = 9;
 constexpr int kNoCast = -1;     // B comes as codes; otherwise the element type of x
 constexpr int kTokens = 32;     // tokens form: columns of its tile
 
-// One stage of the tokens form, by one warp: the 1x128 blocks of x[0..M, k0..
-// k0+127] as E4M3 codes in the K-major 128-byte-swizzled tile at `tile`, and
-// their scale bytes at byte kb % 4 of the words at `sf`.  16 lanes per token,
-// 8 elements each; four pairs of tokens are loaded before any is used.
+constexpr int kTokenBatch = 8;  // tokens that one warp casts at a time
+constexpr int kTokenThreads = 64 + 8 * 32;
+constexpr int kTokenStages = 5;  // the least ring depth of the tokens form (see its casting warps)
+
+// Eight tokens' parts of one stage: x[t0 .. t0+7, k0 .. k0+127], 16 lanes per
+// token, 8 elements each, four pairs of tokens.
 template <int DT>
-__device__ __forceinline__ void cast_tokens_stage(const BArgs &a, int k0, uint32_t tile, uint32_t sf, int lane) {
+__device__ __forceinline__ void load_tokens(const BArgs &a, int t0, int k0, int lane, block::Raw8<DT> (&raw)[4]) {
   const int c8 = lane & 15, half = lane >> 4;
-#pragma unroll 1
-  for (int t0 = 0; t0 < a.cols; t0 += 8) {
-    block::Raw8<DT> raw[4];
-    if (block::wide_tile(a.x_vec, k0, a.x_cols)) {
+  if (block::wide_tile(a.x_vec, k0, a.x_cols)) {
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        raw[i] = block::load_raw8_wide<DT>(a.x, a.ldx, t0 + 2 * i + half, k0 + c8 * 8, a.cols, a.x_cols);
-    } else {
+    for (int i = 0; i < 4; i++)
+      raw[i] = block::load_raw8_wide<DT>(a.x, a.ldx, t0 + 2 * i + half, k0 + c8 * 8, a.cols, a.x_cols);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        raw[i] = block::load_raw8_single<DT>(a.x, a.ldx, t0 + 2 * i + half, k0 + c8 * 8, a.cols, a.x_cols);
-    }
+    for (int i = 0; i < 4; i++)
+      raw[i] = block::load_raw8_single<DT>(a.x, a.ldx, t0 + 2 * i + half, k0 + c8 * 8, a.cols, a.x_cols);
+  }
+}
+
+// The same eight tokens as E4M3 codes in the K-major 128-byte-swizzled tile at
+// `tile`, and their scale bytes at byte kb % 4 of the words at `sf`.
+template <int DT>
+__device__ __forceinline__ void cast_tokens(const BArgs &a, int t0, int kb, uint32_t tile, uint32_t sf, int lane,
+                                            const block::Raw8<DT> (&raw)[4]) {
+  const int c8 = lane & 15, half = lane >> 4;
+  uint32_t m[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int t = t0 + 2 * i + half;
-      uint32_t m = 0;
+  for (int i = 0; i < 4; i++) {
+    m[i] = 0;
 #pragma unroll
-      for (int j = 0; j < block::Raw8<DT>::kWords; j++) m = block::max_words<DT>(m, raw[i].w[j]);
-      m = block::max16(block::word_abs<DT>(m));
-      const int k = block::block_exponent(m, kMaxE4M3, a.margin);
-      const float s = pow2f(k);
-      float f[8];
-      block::unpack8<DT>(raw[i], f);
+    for (int j = 0; j < block::Raw8<DT>::kWords; j++) m[i] = block::max_words<DT>(m[i], raw[i].w[j]);
+    m[i] = block::word_abs<DT>(m[i]);
+  }
+  const uint32_t v = block::reduce_rows<4>(m, c8);  // lane c8 holds pair c8 / 4
+  const int k = block::block_exponent(v, kMaxE4M3, a.margin);
+  const float own = pow2f(k);
+  const bool nan = __any_sync(0xffffffffu, v >= 0x7f800000u);
+  if ((c8 & 3) == 0)
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf + (t0 + 2 * (c8 >> 2) + half) * 16 + (kb & 3)),
+                 "r"((uint32_t)(127 - k))
+                 : "memory");
 #pragma unroll
-      for (int j = 0; j < 8; j++) f[j] *= s;
-      const uint2 c = block::enc8<FP8_E4M3>(f, m >= 0x7f800000u);
-      const uint32_t at = tile + t * 128 + (((c8 >> 1) ^ (t & 7)) << 4) + (c8 & 1) * 8;
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(c.x), "r"(c.y) : "memory");
-      if (c8 == 0)
-        asm volatile("st.shared.u8 [%0], %1;" ::"r"(sf + t * 16 + ((k0 >> 7) & 3)), "r"((uint32_t)(127 - k))
-                     : "memory");
-    }
+  for (int i = 0; i < 4; i++) {
+    const int t = t0 + 2 * i + half;
+    const float s = __shfl_sync(0xffffffffu, own, (lane & 16) + 4 * i);
+    float f[8];
+    block::unpack8<DT>(raw[i], f);
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] *= s;
+    const uint2 c = block::enc8<FP8_E4M3>(f, nan);
+    const uint32_t at = tile + t * 128 + (((c8 >> 1) ^ (t & 7)) << 4) + (c8 & 1) * 8;
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(c.x), "r"(c.y) : "memory");
   }
 }
 
@@ -199,16 +213,19 @@ __device__ __forceinline__ float chunk_bias(const BArgs &a, int row, int col0) {
 
 // ---------------------------------------------------------------------------
 // One-CTA kernel: a tile of 128 x bn outputs per cluster of S CTAs, each of
-// which reduces its share of the k-blocks (S = 1: no cluster).  The partial
-// tiles are added in rank order through distributed shared memory, each CTA
-// finishing bn / S columns: no workspace, no atomics, the same bits each time.
+// which reduces its share of the k-blocks (S = 1: no cluster).  Each CTA then
+// sends every other its part of the partial tile through distributed shared
+// memory (posted stores; reading the others' parts instead cost 12 us at 128
+// columns), adds the S partial sums of its own bn / S columns in rank order
+// and stores them: no workspace, no atomics, the same bits each time.
 //   warp 0 TMA producer, warp 1 TMEM allocation and MMA issue, warps 2-5 epilogue.
-// XDT != kNoCast is the form for few tokens: A holds the weights, and the
-// epilogue warps, idle until the accumulator is complete, cast the tokens'
-// activations into the ring (each every fourth stage, its loads overlapping
-// the other warps'), so that one launch does what the cast and the product do.
+// XDT != kNoCast is the form for few tokens: A holds the weights, and eight
+// warps (four of them the epilogue's, idle until the accumulator is complete)
+// cast the tokens' activations into the ring, eight tokens of one stage at a
+// time, the next ones' loads in flight meanwhile, so that one launch does what
+// the cast and the product do.  Bound by the weights' HBM traffic.
 template <bool A_MN, bool B_MN, int XDT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(XDT == kNoCast ? kThreads : kTokenThreads)
     k_bgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
             const __grid_constant__ BArgs args, const int splits) {
@@ -244,9 +261,11 @@ __global__ void __launch_bounds__(kThreads)
   const int row0 = mb * BM, col0 = nb * args.bn;
 
   constexpr bool CAST = XDT != kNoCast;
+  constexpr int kNumThreads = CAST ? kTokenThreads : kThreads;
+  const int batches = (args.cols + kTokenBatch - 1) / kTokenBatch;  // tokens form: casts per stage
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; s++) {
-      mbar_init(full_bar(s), CAST ? 2 : 1);  // the producer's arrive, and the casting warp's
+      mbar_init(full_bar(s), CAST ? 1 + batches : 1);  // the producer's arrive, and the casting warps'
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull_bar, 1);
@@ -261,7 +280,7 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   if constexpr (CAST) {  // token rows the cast never writes are zero
-    for (int i = threadIdx.x; i < S * (kTokens * BK + 512) / 16; i += kThreads) {
+    for (int i = threadIdx.x; i < S * (kTokens * BK + 512) / 16; i += kNumThreads) {
       const int s = i / ((kTokens * BK + 512) / 16), o = (i % ((kTokens * BK + 512) / 16)) * 16;
       const uint32_t at = o < kTokens * BK ? base + s * args.stage_bytes + BM * BK + o
                                            : sf0 + s * kSfSlot + 512 + (o - kTokens * BK);
@@ -279,6 +298,10 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // Not before the allocation: a dependent CTA that took tensor memory first
+  // and then waited for this kernel would wait for good.
+  pdl_launch_dependents();
+  pdl_wait();
   const uint32_t sf_bytes = 512u + 512u * args.sf_atoms_b;
 
   if (warp == 0) {
@@ -317,10 +340,10 @@ __global__ void __launch_bounds__(kThreads)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint64_t a_d0 = operand_desc<A_MN>(base, 0), b_d0 = operand_desc<B_MN>(base + BM * BK, 0);
-      constexpr uint64_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
-      constexpr uint64_t b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
-      const uint64_t st_d = args.stage_bytes >> 4;
+      const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0), b_d0 = (uint32_t)operand_desc<B_MN>(base + BM * BK, 0);
+      constexpr uint32_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
+      constexpr uint32_t b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
+      const uint32_t st_d = args.stage_bytes >> 4;
       // the scales of a tile that starts inside a 128-row group: skip whole 32-row columns
       const uint32_t sfb_skip = (uint32_t)(col0 & 127) >> 5;
       const uint32_t sf_tmem = tmem_base + args.bn;
@@ -342,11 +365,11 @@ __global__ void __launch_bounds__(kThreads)
           sfb = sf_tmem + kSfSets * kSfCols + 4 * stage;
           tc_cp_scales(sfb, scale_desc(sf0 + stage * kSfSlot + 512));
         }
-        const uint64_t so = (uint64_t)stage * st_d;
+        const uint32_t so = (uint32_t)stage * st_d;
         const uint32_t idesc = with_scale_ids(args.idesc, kb);
 #pragma unroll
         for (int ks = 0; ks < BK / UMMA_K; ks++)
-          tc_mma_bs(tmem_base, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, idesc, sfa, sfb,
+          tc_mma_bs(tmem_base, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfb,
                     (kb != kb0 || ks != 0) ? 1u : 0u);
         tc_commit(empty_bar(stage));
         issued_any = true;
@@ -364,76 +387,105 @@ __global__ void __launch_bounds__(kThreads)
     const int q = warp & 3;
     const int row = row0 + q * 32 + lane;
     if constexpr (CAST) {
-      int stage = q % S;
-      uint32_t phase = (uint32_t)(q / S) & 1u;
-      for (int kb = kb0 + q; kb < kb1; kb += 4) {
-        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag))) break;
-        cast_tokens_stage<XDT>(args, kb * BK, base + stage * args.stage_bytes + BM * BK, sf0 + stage * kSfSlot + 512,
-                               lane);
+      // Unit u: batch u % batches of block kb0 + u / batches; the casting warps
+      // take them in turn.  At most 4 * batches warps do, so that a warp's next
+      // unit is at most four blocks on: a parity wait tells only one phase of a
+      // ring slot from the next, and a warp that skipped a whole turn of the
+      // ring (five stages at the least) could take an older phase for its own.
+      const int units = (kb1 - kb0) * batches, step = min(8, 4 * batches);
+      block::Raw8<XDT> raw[4];
+      int u = warp - 2 < step ? warp - 2 : units;
+      if (u < units) load_tokens<XDT>(args, u % batches * kTokenBatch, (kb0 + u / batches) * BK, lane, raw);
+      for (; u < units; u += step) {
+        const int i = u / batches, stage = i % S, t0 = u % batches * kTokenBatch;
+        block::Raw8<XDT> next[4];
+        const int un = min(u + step, units - 1);
+        load_tokens<XDT>(args, un % batches * kTokenBatch, (kb0 + un / batches) * BK, lane, next);
+        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), ((uint32_t)(i / S) & 1u) ^ 1u, abort_flag))) break;
+        cast_tokens<XDT>(args, t0, kb0 + i, base + stage * args.stage_bytes + BM * BK, sf0 + stage * kSfSlot + 512,
+                         lane, raw);
         fence_async_shared();  // the MMAs and the scale copy read through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(full_bar(stage));
-        stage += 4;
-        while (stage >= S) {
-          stage -= S;
-          phase ^= 1u;
-        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) raw[j] = next[j];
       }
       __syncwarp();
     }
-    const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
-    tc_fence_after();
-    if (got) {
+    if (warp < 6) {
+      float bias = args.swap && splits == 1 ? chunk_bias(args, row, 0) : 0.0f;
+      const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
+      tc_fence_after();
+      if (got && splits == 1) {
 #pragma unroll 1
-      for (int c = 0; c < args.bn; c += 32) {
-        if (splits == 1 && col0 + c >= args.cols) break;
-        const float bias = splits == 1 ? chunk_bias(args, row, col0 + c) : 0.0f;
-        uint32_t r[32];
-        tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
-        float v[32];
+        for (int c = 0; c < args.bn && col0 + c < args.cols; c += 32) {
+          if (!args.swap) bias = chunk_bias(args, row, col0 + c);
+          uint32_t r[32];
+          tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
+          float v[32];
 #pragma unroll
-        for (int j = 0; j < 32; j++) v[j] = __uint_as_float(r[j]);
-        if (splits == 1) {
+          for (int j = 0; j < 32; j++) v[j] = __uint_as_float(r[j]);
           store_out(args, v, 32, row, col0 + c, bias);
-        } else {  // partial tile, column by column: [bn][128] floats over the ring
-#pragma unroll
-          for (int j = 0; j < 32; j++)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c + j) * BM + q * 32 + lane) * 4), "f"(v[j])
-                         : "memory");
         }
       }
+      tc_fence_before();
+      __syncwarp();
     }
-    tc_fence_before();
-    __syncwarp();
   }
 
   if (splits > 1) {
-    cluster_sync();
-    if (warp >= 2) {
-      const int q = warp & 3, row = row0 + q * 32 + lane;
-      const int per = args.bn / splits;  // a multiple of 4 (bn % 32 == 0, splits <= 8)
+    // Columns in units of 8 (a vector store), or 4 where the tokens are few;
+    // CTA r finishes units [r * units / S, (r + 1) * units / S).  A partial
+    // tile of CTA s arrives at slot s of the owner's ring, 4 columns x 128
+    // rows (2 KB) apart.
+    const int unit = args.bn >= 128 ? 8 : 4, units = args.bn / unit, per4 = (units + splits - 1) / splits * (unit / 4);
+    cluster_sync();  // every CTA's MMAs have read their ring
+    const int q = warp & 3, row = row0 + q * 32 + lane;
+    if (warp >= 2 && warp < 6) {
+      tc_fence_after();
+      for (int r = 0; r < splits; r++) {
+        const uint32_t dst = map_to_rank(base, (uint32_t)r) + (rank * per4 * BM + q * 32 + lane) * 16;
+        const int c0 = r * units / splits * unit, c1 = (r + 1) * units / splits * unit;
 #pragma unroll 1
-      for (int c = rank * per; c < (rank + 1) * per; c += 4) {
+        for (int c = c0; c < c1; c += 4) {
+          uint32_t v[4];
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                       : "r"(tmem_base + ((uint32_t)(q * 32) << 16) + c));
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c - c0) / 4 * (BM * 16)),
+                       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                       : "memory");
+        }
+      }
+      tc_fence_before();
+    }
+    cluster_sync();  // all parts have arrived
+    if (warp >= 2 && warp < 6) {
+      const int c0 = rank * units / splits * unit, c1 = (rank + 1) * units / splits * unit;
+#pragma unroll 1
+      for (int c = c0; c < c1; c += 8) {
         const float bias = chunk_bias(args, row, col0 + c);
+        const int n = min(8, c1 - c);
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; j++) v[j] = 0.0f;
         for (int s = 0; s < splits; s++) {
-          const uint32_t src = map_to_rank(base, (uint32_t)s);
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            float x;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                         : "=f"(x)
-                         : "r"(src + ((c + j) * BM + q * 32 + lane) * 4)
+          for (int h = 0; h < 2; h++) {
+            if (4 * h >= n) break;
+            float x[4];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                         : "r"(base + ((s * per4 + (c - c0) / 4 + h) * BM + q * 32 + lane) * 16)
                          : "memory");
-            v[j] = s == 0 ? x : __fadd_rn(v[j], x);
+#pragma unroll
+            for (int j = 0; j < 4; j++) v[4 * h + j] = __fadd_rn(v[4 * h + j], x[j]);
           }
         }
-        store_out(args, v, 4, row, col0 + c, bias);
+        store_out(args, v, n, row, col0 + c, bias);
       }
     }
-    cluster_sync();  // no CTA leaves while another reads its partial tile
   }
 
   tc_fence_before();
@@ -469,14 +521,14 @@ constexpr int kP2OutBoxes = 2;  // staging boxes per epilogue warp (stores pipel
 constexpr int kP2SmemBytes =
     kP2Stages * (kPairStageBytes + kP2SfSlot) + 4 * kP2OutBoxes * kWideStageOutBytes + 256 + 1024;
 
-__device__ __forceinline__ void tc_mma_bs_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
-                                               uint32_t sfb, uint32_t accumulate) {
-  opaque(ad, bd);
+__device__ __forceinline__ void tc_mma_bs_pair(uint32_t d, uint32_t ad, uint32_t bd, uint32_t hi, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
-      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+      "r"(ad), "r"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(hi)
       : "memory");
 }
 
@@ -570,6 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // barriers of both CTAs initialised before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // Not before the allocation: a dependent CTA that took tensor memory first
+  // and then waited for this kernel would wait for good.
+  pdl_launch_dependents();
+  pdl_wait();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producers (both CTAs, one thread)
@@ -605,10 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader, one thread)
     if (leader && lane == 0) {
-      const uint64_t a_d0 = operand_desc<A_MN>(base, 0), b_d0 = operand_desc<B_MN>(base + kPairHalf * BK, 0);
-      constexpr uint64_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
-      constexpr uint64_t b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
-      constexpr uint64_t st_d = kPairStageBytes >> 4;
+      const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0);
+      const uint32_t b_d0 = (uint32_t)operand_desc<B_MN>(base + kPairHalf * BK, 0);
+      constexpr uint32_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
+      constexpr uint32_t b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
+      constexpr uint32_t st_d = kPairStageBytes >> 4;
       int stage = 0, n = 0;
       uint32_t phase = 0, group = 0;
       bool ok = true, issued_any = false;
@@ -631,11 +688,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             group++;
           }
           const uint32_t sfa = tmem_base + kP2Sf + ((group - 1) & 1u) * 16;
-          const uint64_t so = (uint64_t)stage * st_d;
+          const uint32_t so = (uint32_t)stage * st_d;
           const uint32_t idesc = with_scale_ids(args.idesc, kb);
 #pragma unroll
           for (int ks = 0; ks < BK / UMMA_K; ks++)
-            tc_mma_bs_pair(d_tmem, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, idesc, sfa, sfa + 4,
+            tc_mma_bs_pair(d_tmem, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfa + 4,
                            (kb | ks) != 0 ? 1u : 0u);
           tc_commit_pair(empty_bar(stage));
           if ((kb & 3) == 3 || kb == args.num_k_blocks - 1) tc_commit_leader(sffree_bar((group - 1) & 1u));
@@ -749,6 +806,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // out[r, c] = bias[c] or 0: a product with an empty reduction.
 __global__ void k_bgemm_empty(const BArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
   const size_t n = (size_t)a.rows * a.cols, stride = (size_t)gridDim.x * blockDim.x;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
     const int r = (int)(i / a.cols), c = (int)(i % a.cols);

@@ -314,10 +314,8 @@ __device__ __forceinline__ void cast_tile_cols(const float (&v)[RP][8], ColScrat
 // the separate form took 139 instead of 95 us for 8192 x 12288 bf16 in both
 // directions.  Returns whether the warp saw an amax that is not finite.
 template <int RP>
-__device__ __forceinline__ bool row_scales(const uint32_t (&m)[RP], uint8_t *s, int row0, int col0, int tiles_c,
-                                           float fmax, int margin, float (&out)[RP]) {
+__device__ __forceinline__ uint32_t reduce_rows(const uint32_t (&m)[RP], int l) {
   static_assert(RP == 8 || RP == 4, "halved down to one row");
-  const int lane = threadIdx.x & 31, l = lane & 15, r0 = threadIdx.x >> 4;
   uint32_t v[RP];
 #pragma unroll
   for (int i = 0; i < RP; i++) v[i] = m[i];
@@ -332,12 +330,20 @@ __device__ __forceinline__ bool row_scales(const uint32_t (&m)[RP], uint8_t *s, 
   }
 #pragma unroll
   for (; bit > 0; bit /= 2) v[0] = max(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
-  const int k = block_exponent(v[0], fmax, margin);
+  return v[0];
+}
+
+template <int RP>
+__device__ __forceinline__ bool row_scales(const uint32_t (&m)[RP], uint8_t *s, int row0, int col0, int tiles_c,
+                                           float fmax, int margin, float (&out)[RP]) {
+  const int lane = threadIdx.x & 31, l = lane & 15, r0 = threadIdx.x >> 4;
+  const uint32_t v = reduce_rows<RP>(m, l);
+  const int k = block_exponent(v, fmax, margin);
   if (l % (16 / RP) == 0) put_scale(s, row0 + r0 + Geo<RP>::kStep * (l * RP / 16), col0 / kTile, tiles_c, k);
   const float own = pow2f(k);
 #pragma unroll
   for (int i = 0; i < RP; i++) out[i] = __shfl_sync(0xffffffffu, own, (lane & 16) + i * (16 / RP));
-  return __any_sync(0xffffffffu, v[0] >= 0x7f800000u);
+  return __any_sync(0xffffffffu, v >= 0x7f800000u);
 }
 
 // The row side of the same tile of floats.
@@ -391,6 +397,8 @@ __device__ __forceinline__ void cast_raw_rows(const Raw8<DT> (&raw)[RP], uint8_t
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kCastThreads)
     k_block_cast(const void *__restrict__ x, int rows, int cols, size_t ldx, int vec, int margin, const CastOut out) {
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr int RP = 8;
   __shared__ ColScratch<RP> sc;
   const float fmax = FMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
@@ -439,6 +447,8 @@ template <int DT, int FMT>
 __global__ void __launch_bounds__(kCastThreads)
     k_block_cast_square(const void *__restrict__ x, int rows, int cols, size_t ldx, int vec, int margin,
                         const CastOut out) {
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr int RP = 8;
   __shared__ uint32_t red[32];
   const float fmax = FMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
@@ -552,6 +562,8 @@ template <int DT, int FMT, bool COLS>
 __global__ void __launch_bounds__(kCastThreads)
     k_block_decode(const uint8_t *__restrict__ q, const uint8_t *__restrict__ s, int rows, int cols, size_t ldq,
                    void *__restrict__ x, size_t ldx, int vec) {
+  pdl_launch_dependents();
+  pdl_wait();
   const long long groups_c = (cols + 7) / 8;
   const long long groups = (long long)rows * groups_c;
   const int kg = COLS ? ((rows + 127) / 128 + 3) / 4 : ((cols + 127) / 128 + 3) / 4;

@@ -217,4 +217,12 @@ __device__ __forceinline__ int device_log2mu(float mu) {
   return e;
 }
 
+// Programmatic dependent launch: a kernel launched with that attribute may
+// start while the stream's previous kernel still runs, once all of its CTAs
+// have said `launch_dependents` (or ended).  Every kernel so launched sets
+// itself up, then waits here -- until the previous kernel has completed and
+// its memory is visible -- before it touches global memory.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 }  // namespace fp8lib

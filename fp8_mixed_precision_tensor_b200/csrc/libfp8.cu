@@ -831,6 +831,28 @@ void with_act(int act, F f) {
   else f(std::integral_constant<int, FP8_ACT_SILU>());
 }
 
+// Launch with programmatic dependence on the stream's previous kernel (see
+// pdl_wait); cluster > 1: clusters of that many CTAs.
+template <typename... P, typename... A>
+int launch_pdl(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, unsigned cluster,
+               A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cuda_rc(cudaLaunchKernelEx(&cfg, kernel, P(args)...));
+}
+
 // One CTA per 128x128 tile.
 unsigned tile_grid(int rows, int cols) {
   const unsigned long long t = (unsigned long long)((rows + 127) / 128) * (unsigned long long)((cols + 127) / 128);
@@ -865,20 +887,6 @@ int set_pair_smem() {
          set_smem(k_bgemm2<A_MN, B_MN, FP8_DT_BF16_RTO>, bgemm::kP2SmemBytes);
 }
 
-void pair_config(cudaLaunchConfig_t *cfg, cudaLaunchAttribute *attr, int clusters, cudaStream_t stream) {
-  *cfg = {};
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = 2;
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
-  cfg->gridDim = dim3(2 * clusters);
-  cfg->blockDim = dim3(gemm::kThreads);
-  cfg->dynamicSmemBytes = bgemm::kP2SmemBytes;
-  cfg->stream = stream;
-  cfg->attrs = attr;
-  cfg->numAttrs = 1;
-}
-
 // One-time per-device attributes of the block-scaled kernels.
 int block_info(DeviceInfo **d, BlockInfo **out) {
   int rc0 = device_info(d);
@@ -897,9 +905,17 @@ int block_info(DeviceInfo **d, BlockInfo **out) {
            set_max_smem(k_bgemm<false, false, FP8_DT_F16>);
   rc |= set_pair_smem<false, false>() | set_pair_smem<false, true>() | set_pair_smem<true, true>();
   if (rc) return FP8_ERR_CUDA;
-  cudaLaunchConfig_t cfg;
+  cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
-  pair_config(&cfg, &attr, (*d)->sms / 2, nullptr);
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2 * ((*d)->sms / 2));
+  cfg.blockDim = dim3(gemm::kThreads);
+  cfg.dynamicSmemBytes = bgemm::kP2SmemBytes;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   if (cudaOccupancyMaxActiveClusters(&b.pair_clusters, bgemm::k_bgemm2<false, false, FP8_DT_BF16>, &cfg) !=
       cudaSuccess)
     return FP8_ERR_CUDA;
@@ -976,8 +992,9 @@ int launch_bgemm(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, in
   const uint32_t room = (tmem <= 256 ? 114688u : 230400u) - 1024u - 256u;
   int stages = (int)(room / (a.stage_bytes + kSfSlot));
   if (stages > kMaxStages) stages = kMaxStages;
+  if (XDT != kNoCast && stages < kTokenStages) return FP8_ERR_UNSUPPORTED;  // (never: a stage is 22 KB)
   a.stages = stages;
-  if (splits > 1 && (uint32_t)bn * gemm::BM * 4 > stages * a.stage_bytes) return FP8_ERR_UNSUPPORTED;
+  a.desc_hi = kDescHi;
   a.idesc = ((uint32_t)A.fmt << 7) | ((uint32_t)B.fmt << 10) | ((uint32_t)(A_MN ? 1 : 0) << 15) |
             ((uint32_t)(B_MN ? 1 : 0) << 16) | ((uint32_t)(bn >> 3) << 17) | (1u << 23)  // scales: 8-bit exponents
             | ((uint32_t)(gemm::BM >> 7) << 27);
@@ -996,19 +1013,9 @@ int launch_bgemm(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, in
     msb = msa;
   }
   const size_t smem = (size_t)stages * (a.stage_bytes + kSfSlot) + 256 + 1024;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = splits;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)a.num_tiles * splits);
-  cfg.blockDim = dim3(gemm::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
-  return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm<A_MN, B_MN, XDT>, ma, mb, msa, msb, a, splits));
+  constexpr int threads = XDT == kNoCast ? gemm::kThreads : kTokenThreads;
+  return launch_pdl(k_bgemm<A_MN, B_MN, XDT>, (unsigned)a.num_tiles * splits, threads, smem, stream, splits, ma, mb,
+                    msa, msb, a, splits);
 }
 
 // C[rows, cols] on the pair kernel.
@@ -1021,6 +1028,7 @@ int launch_bgemm2(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, i
   a.num_tiles = a.num_m_blocks * a.num_n_blocks;
   a.num_k_blocks = (K + gemm::BK - 1) / gemm::BK;
   a.group_m = 8;
+  a.desc_hi = kDescHi;
   a.idesc = ((uint32_t)A.fmt << 7) | ((uint32_t)B.fmt << 10) | ((uint32_t)(A_MN ? 1 : 0) << 15) |
             ((uint32_t)(B_MN ? 1 : 0) << 16) | ((uint32_t)(256 >> 3) << 17) | (1u << 23) | ((uint32_t)(256 >> 7) << 27);
   CUtensorMap ma, mb, msa, msb, mo;
@@ -1034,14 +1042,15 @@ int launch_bgemm2(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, i
   if ((rc = make_scale_map(&msb, B.b->s, cols, K, 2))) return rc;
   mo = ma;  // unused by the element stores
   if (a.vec_out && (rc = make_pitched_out_map(&mo, a.out, a.out_dtype, rows, cols, a.ld_out))) return rc;
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr;
-  pair_config(&cfg, &attr, a.num_tiles < clusters ? a.num_tiles : clusters, stream);
+  const unsigned grid = 2 * (unsigned)(a.num_tiles < clusters ? a.num_tiles : clusters);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, gemm::kThreads, kP2SmemBytes, stream, 2, ma, mb, msa, msb, mo, a);
+  };
   switch (a.out_dtype) {
-    case FP8_DT_F32: return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm2<A_MN, B_MN, FP8_DT_F32>, ma, mb, msa, msb, mo, a));
-    case FP8_DT_BF16: return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm2<A_MN, B_MN, FP8_DT_BF16>, ma, mb, msa, msb, mo, a));
-    case FP8_DT_F16: return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm2<A_MN, B_MN, FP8_DT_F16>, ma, mb, msa, msb, mo, a));
-    default: return cuda_rc(cudaLaunchKernelEx(&cfg, k_bgemm2<A_MN, B_MN, FP8_DT_BF16_RTO>, ma, mb, msa, msb, mo, a));
+    case FP8_DT_F32: return go(k_bgemm2<A_MN, B_MN, FP8_DT_F32>);
+    case FP8_DT_BF16: return go(k_bgemm2<A_MN, B_MN, FP8_DT_BF16>);
+    case FP8_DT_F16: return go(k_bgemm2<A_MN, B_MN, FP8_DT_F16>);
+    default: return go(k_bgemm2<A_MN, B_MN, FP8_DT_BF16_RTO>);
   }
 }
 
@@ -1076,8 +1085,7 @@ int run_bgemm(const BOperand &A, const BOperand &B, const void *bias, int bias_d
   DeviceInfo *d;
   if (red == 0) {
     if ((rc = device_info(&d))) return rc;
-    bgemm::k_bgemm_empty<<<d->sms * 4, 256, 0, stream>>>(a);
-    return launch_rc();
+    return launch_pdl(bgemm::k_bgemm_empty, (unsigned)d->sms * 4, 256, 0, stream, 1, a);
   }
   if ((rc = check_blocks(A.b, A_MN ? R : red))) return rc;
   if ((rc = check_blocks(B.b, B_MN ? C : red))) return rc;
@@ -1122,12 +1130,11 @@ int fp8_block_cast(const void *x, int dtype, int rows, int cols, size_t ldx, int
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_fmt(fmt, [&](auto f) {
-      block::k_block_cast<decltype(dt)::value, decltype(f)::value>
-          <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(x, rows, cols, ldx, wide_rows(x, dtype, ldx), margin,
-                                                                 o);
+      rc = launch_pdl(block::k_block_cast<decltype(dt)::value, decltype(f)::value>, tile_grid(rows, cols),
+                      block::kCastThreads, 0, s, 1, x, rows, cols, ldx, (int)wide_rows(x, dtype, ldx), margin, o);
     });
   });
-  return launch_rc();
+  return rc;
 }
 
 int fp8_block_cast_square(const void *x, int dtype, int rows, int cols, size_t ldx, int fmt, int margin,
@@ -1144,12 +1151,11 @@ int fp8_block_cast_square(const void *x, int dtype, int rows, int cols, size_t l
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_fmt(fmt, [&](auto f) {
-      block::k_block_cast_square<decltype(dt)::value, decltype(f)::value>
-          <<<tile_grid(rows, cols), block::kCastThreads, 0, s>>>(x, rows, cols, ldx, wide_rows(x, dtype, ldx), margin,
-                                                                 o);
+      rc = launch_pdl(block::k_block_cast_square<decltype(dt)::value, decltype(f)::value>, tile_grid(rows, cols),
+                      block::kCastThreads, 0, s, 1, x, rows, cols, ldx, (int)wide_rows(x, dtype, ldx), margin, o);
     });
   });
-  return launch_rc();
+  return rc;
 }
 
 int fp8_block_decode(const fp8_blocks *in, int fmt, int axis, int rows, int cols, void *x, int dtype, size_t ldx,
@@ -1166,12 +1172,13 @@ int fp8_block_decode(const fp8_blocks *in, int fmt, int axis, int rows, int cols
   with_dtype(dtype, [&](auto dt) {
     with_fmt(fmt, [&](auto f) {
       with_bool(axis == 0, [&](auto colblocks) {
-        block::k_block_decode<decltype(dt)::value, decltype(f)::value, decltype(colblocks)::value>
-            <<<grid, block::kCastThreads, 0, s>>>(in->q, in->s, rows, cols, in->ld, x, ldx, wide_rows(x, dtype, ldx));
+        rc = launch_pdl(block::k_block_decode<decltype(dt)::value, decltype(f)::value, decltype(colblocks)::value>,
+                        grid, block::kCastThreads, 0, s, 1, in->q, in->s, rows, cols, in->ld, x, ldx,
+                        (int)wide_rows(x, dtype, ldx));
       });
     });
   });
-  return launch_rc();
+  return rc;
 }
 
 int fp8_block_linear_fwd(const fp8_blocks *x, const fp8_blocks *w, const void *bias, int bias_dtype, void *y,
@@ -1248,11 +1255,11 @@ int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int ac
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_act(act, [&](auto f) {
-      block::k_act_fwd<decltype(dt)::value, decltype(f)::value>
-          <<<tile_grid(rows, cols), block::kActThreads, 0, s>>>(p);
+      rc = launch_pdl(block::k_act_fwd<decltype(dt)::value, decltype(f)::value>, tile_grid(rows, cols),
+                      block::kActThreads, 0, s, 1, p);
     });
   });
-  return launch_rc();
+  return rc;
 }
 
 int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int cols, size_t ldda, int act, int fmt,
@@ -1285,11 +1292,11 @@ int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int
         constexpr int smem = block::ActBwdSmem<K::value>::kBytes;
         if ((rc = set_smem(kernel, smem))) return;
         const unsigned tiles = tile_grid(rows, cols);
-        kernel<<<tiles < (unsigned)d->sms ? tiles : d->sms, block::kActThreads, smem, s>>>(p);
+        rc = launch_pdl(kernel, tiles < (unsigned)d->sms ? tiles : (unsigned)d->sms, block::kActThreads, smem, s, 1, p);
       });
     });
   });
-  return rc ? rc : launch_rc();
+  return rc;
 }
 
 int fp8_get_status(unsigned *host_out, void *stream) {

@@ -344,6 +344,19 @@ def test_tokens_form_against_binary64(M, N, K, dtype):
     assert fp8.fp8_get_status() == 0
 
 
+@pytest.mark.parametrize("M", [1, 8, 9, 17, 32])
+@pytest.mark.parametrize("N,K", [(19000, 3000), (12288, 4096), (300, 33000)])
+def test_tokens_form_runs_its_ring_many_times(M, N, K):
+    """Reductions much longer than the kernel's ring of operand stages, on one CTA per tile and split."""
+    L = Layer(M, N, K, key=("ring",))
+    y = torch.empty((M, N), device="cuda")
+    for _ in range(5):
+        y.fill_(float("nan"))
+        fp8.fp8_block_linear_tokens(L.x, L.wq, L.ws, y)
+        assert_product(y, (L.X @ L.W.T, L.X.abs() @ L.W.abs().T, K))
+    assert fp8.fp8_get_status() == 0
+
+
 def test_tokens_form_reports_a_non_finite_token():
     L = Layer(4, 256, 256)
     x = torch.randn(4, 256, device="cuda")
