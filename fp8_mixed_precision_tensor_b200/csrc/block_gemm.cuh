@@ -82,6 +82,13 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
   return d;
 }
 
+// Bring a box of a tensor map into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
                                             uint32_t bar) {
   asm volatile(
@@ -111,6 +118,7 @@ constexpr int kTokens = 32;     // tokens form: columns of its tile
 
 constexpr int kTokenBatch = 8;  // tokens that one warp casts at a time
 constexpr int kTokenThreads = 64 + 8 * 32;
+constexpr int kTokenPrefetch = 16;  // weight blocks (16 KB each) brought into L2 ahead
 constexpr int kTokenStages = 5;  // the least ring depth of the tokens form (see its casting warps)
 
 // Eight tokens' parts of one stage: x[t0 .. t0+7, k0 .. k0+127], 16 lanes per
@@ -301,6 +309,11 @@ __global__ void __launch_bounds__(XDT == kNoCast ? kThreads : kTokenThreads)
   // Not before the allocation: a dependent CTA that took tensor memory first
   // and then waited for this kernel would wait for good.
   pdl_launch_dependents();
+  // Tokens form: the first weights come into L2 while the stream's previous
+  // kernel ends.  (L2 is where its writes go too, so a weight that it still
+  // writes is read as written by the loads after the wait.)
+  if (CAST && threadIdx.x == 0)
+    for (int kb = kb0; kb < min(kb1, kb0 + kTokenPrefetch); kb++) tma_prefetch_2d(&tmA, kb * BK, row0);
   pdl_wait();
   const uint32_t sf_bytes = 512u + 512u * args.sf_atoms_b;
 
@@ -434,27 +447,31 @@ __global__ void __launch_bounds__(XDT == kNoCast ? kThreads : kTokenThreads)
   }
 
   if (splits > 1) {
-    // Columns in units of 8 (a vector store), or 4 where the tokens are few;
-    // CTA r finishes units [r * units / S, (r + 1) * units / S).  A partial
-    // tile of CTA s arrives at slot s of the owner's ring, 4 columns x 128
-    // rows (2 KB) apart.
-    const int unit = args.bn >= 128 ? 8 : 4, units = args.bn / unit, per4 = (units + splits - 1) / splits * (unit / 4);
+    // Columns in units of 8 (a vector store), or 4 where the columns are
+    // tokens; unit u is finished by CTA u % S, as its unit u / S.  The partial
+    // of CTA s arrives at slot s of the owner's ring: per unit, groups of 4
+    // columns x 128 rows x 16 bytes.
+    const int unit = args.swap ? 4 : 8, groups = unit / 4;
+    const int cols = min(args.bn, args.cols - col0), units = (cols + unit - 1) / unit;
+    const int per = (units + splits - 1) / splits;
     cluster_sync();  // every CTA's MMAs have read their ring
     const int q = warp & 3, row = row0 + q * 32 + lane;
+    float bias = 0.0f;
     if (warp >= 2 && warp < 6) {
+      if (args.swap) bias = chunk_bias(args, row, 0);
       tc_fence_after();
-      for (int r = 0; r < splits; r++) {
-        const uint32_t dst = map_to_rank(base, (uint32_t)r) + (rank * per4 * BM + q * 32 + lane) * 16;
-        const int c0 = r * units / splits * unit, c1 = (r + 1) * units / splits * unit;
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 4) {
-          uint32_t v[4];
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                       : "r"(tmem_base + ((uint32_t)(q * 32) << 16) + c));
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c - c0) / 4 * (BM * 16)),
-                       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
+#pragma unroll
+        for (int g = 0; g < 8; g++) {
+          const int u = (c + 4 * g) / unit;
+          if (c + 4 * g >= cols) break;
+          const uint32_t dst = map_to_rank(base, (uint32_t)(u % splits)) +
+                               (((rank * per + u / splits) * groups + (g & (groups - 1))) * BM + q * 32 + lane) * 16;
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(r[4 * g]),
+                       "r"(r[4 * g + 1]), "r"(r[4 * g + 2]), "r"(r[4 * g + 3])
                        : "memory");
         }
       }
@@ -462,28 +479,27 @@ __global__ void __launch_bounds__(XDT == kNoCast ? kThreads : kTokenThreads)
     }
     cluster_sync();  // all parts have arrived
     if (warp >= 2 && warp < 6) {
-      const int c0 = rank * units / splits * unit, c1 = (rank + 1) * units / splits * unit;
 #pragma unroll 1
-      for (int c = c0; c < c1; c += 8) {
-        const float bias = chunk_bias(args, row, col0 + c);
-        const int n = min(8, c1 - c);
+      for (int i = 0, u = rank; u < units; i++, u += splits) {
+        if (!args.swap) bias = chunk_bias(args, row, col0 + u * unit);
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; j++) v[j] = 0.0f;
+#pragma unroll 2
         for (int s = 0; s < splits; s++) {
 #pragma unroll
           for (int h = 0; h < 2; h++) {
-            if (4 * h >= n) break;
+            if (h >= groups) break;
             float x[4];
             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                          : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
-                         : "r"(base + ((s * per4 + (c - c0) / 4 + h) * BM + q * 32 + lane) * 16)
+                         : "r"(base + (((s * per + i) * groups + h) * BM + q * 32 + lane) * 16)
                          : "memory");
 #pragma unroll
             for (int j = 0; j < 4; j++) v[4 * h + j] = __fadd_rn(v[4 * h + j], x[j]);
           }
         }
-        store_out(args, v, n, row, col0 + c, bias);
+        store_out(args, v, unit, row, col0 + u * unit, bias);
       }
     }
   }
