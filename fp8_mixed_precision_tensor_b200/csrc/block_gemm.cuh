@@ -28,6 +28,7 @@ using namespace gemm;
 struct BArgs {
   int rows, cols;              // output extent along A's and B's outer indices
   int num_m_blocks, num_n_blocks, num_tiles, num_k_blocks, group_m;
+  int whole;                   // pair kernel: tiles from this one on are worked as two halves of 128 columns
   int bn;                      // output columns per tile (a multiple of 32, at most 256)
   int stages, sf_atoms_b;      // ring depth; 512-byte scale groups loaded per tile for B
   uint32_t stage_bytes, tmem_cols;
@@ -527,6 +528,9 @@ __global__ void __launch_bounds__(XDT == kNoCast ? kThreads : kTokenThreads)
 // by the time a warp says so for one tile it has read all of the tile before,
 // so that one signal covers both accumulators.  The gap between two tiles is
 // one barrier round trip and two TMEM loads.
+// Whole tiles fill the clusters in waves.  Where the last wave would leave half
+// of the clusters idle, its tiles are worked as two halves of 128 columns (N =
+// 128, the CTAs loading from columns 64 apart), so that it lasts half as long.
 //   warp 0 TMA producer (both CTAs), warp 1 TMEM allocation and MMA issue
 //   (leader), warps 2-5 epilogue (both CTAs).
 constexpr int kP2Stages = 5;
@@ -575,6 +579,33 @@ __device__ __forceinline__ uint32_t pack_out(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// A staged box (32 rows of 128 bytes, swizzled) to rows at any alignment:
+// neighbouring lanes store neighbouring elements.
+template <int OUT>
+__device__ __forceinline__ void store_box_elements(const BArgs &a, uint32_t stg, int row0, int col0, int lane) {
+  constexpr int esz = OUT == FP8_DT_F32 ? 4 : 2;
+  const int rows = min(32, a.rows - row0);
+  for (int r = 0; r < rows; r++) {
+#pragma unroll
+    for (int h = 0; h < 4 / esz; h++) {
+      const int e = h * 32 + lane;
+      const uint32_t src = stg + r * 128 + (((e * esz >> 4) ^ (r & 7)) << 4) + (e * esz & 15);
+      const size_t at = (size_t)(row0 + r) * a.ld_out + col0 + e;
+      if (col0 + e >= a.cols) continue;
+      if constexpr (esz == 4) {
+        uint32_t v;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(src) : "memory");
+        reinterpret_cast<uint32_t *>(a.out)[at] = v;
+      } else {
+        uint16_t v;
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(src) : "memory");
+        reinterpret_cast<uint16_t *>(a.out)[at] = v;
+      }
+    }
+  }
+  __syncwarp();
+}
+
 template <bool A_MN, bool B_MN, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_bgemm2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -600,13 +631,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  // Item t of the work: its tile, and the half (0, 1) of it or -1 for the whole.
+  const int num_items = args.whole + 2 * (args.num_tiles - args.whole);
   auto coords = [&](int t, int &mb, int &nb) {
+    int half = -1;
+    if (t >= args.whole) {
+      half = (t - args.whole) & 1;
+      t = args.whole + ((t - args.whole) >> 1);
+    }
     const int per_band = args.group_m * args.num_n_blocks;
     const int band = t / per_band, first = band * args.group_m;
     const int rows_in_band = min(args.num_m_blocks - first, args.group_m);
     const int r = t - band * per_band;
     mb = first + r % rows_in_band;
     nb = r / rows_in_band;
+    return half;
   };
 
   if (threadIdx.x == 0) {
@@ -649,10 +688,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true, issued = false;
-      for (int tile = pair; tile < args.num_tiles && ok; tile += num_pairs) {
+      for (int tile = pair; tile < num_items && ok; tile += num_pairs) {
         int mb, nb;
-        coords(tile, mb, nb);
-        const int arow = mb * 256 + (int)rank * 128, bcol = nb * 256 + (int)rank * 128;
+        const int half = coords(tile, mb, nb);
+        const int arow = mb * 256 + (int)rank * 128;
+        const int bcol = nb * 256 + (half < 0 ? (int)rank * 128 : half * 128 + (int)rank * 64);
         for (int kb = 0; kb < args.num_k_blocks; kb++) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t sa = base + stage * kPairStageBytes, sb = sa + kPairHalf * BK, ss = sf0 + stage * kP2SfSlot;
@@ -685,10 +725,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, n = 0;
       uint32_t phase = 0, group = 0;
       bool ok = true, issued_any = false;
-      for (int tile = pair; tile < args.num_tiles && ok; tile += num_pairs, n++) {
+      for (int tile = pair; tile < num_items && ok; tile += num_pairs, n++) {
         if (n > 0 && !mbar_wait(tempty_bar, (uint32_t)(n - 1) & 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (n & 1) * kP2Acc1;
+        const bool split = tile >= args.whole;
+        const uint32_t shape = split ? args.idesc ^ ((256u >> 3) << 17) ^ ((128u >> 3) << 17) : args.idesc;
+        const uint32_t sfb_off = split && ((tile - args.whole) & 1) ? 8u : 4u;
         for (int kb = 0; kb < args.num_k_blocks; kb++) {
           if (!stage_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
           if ((kb & 3) == 0) {  // the set's last readers, two groups ago, have completed
@@ -705,10 +748,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t sfa = tmem_base + kP2Sf + ((group - 1) & 1u) * 16;
           const uint32_t so = (uint32_t)stage * st_d;
-          const uint32_t idesc = with_scale_ids(args.idesc, kb);
+          const uint32_t idesc = with_scale_ids(shape, kb);
 #pragma unroll
           for (int ks = 0; ks < BK / UMMA_K; ks++)
-            tc_mma_bs_pair(d_tmem, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfa + 4,
+            tc_mma_bs_pair(d_tmem, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfa + sfb_off,
                            (kb | ks) != 0 ? 1u : 0u);
           tc_commit_pair(empty_bar(stage));
           if ((kb & 3) == 3 || kb == args.num_k_blocks - 1) tc_commit_leader(sffree_bar((group - 1) & 1u));
@@ -732,19 +775,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kNum = 256 / kBox;
     uint32_t box = 0;
     int n = 0;
-    for (int tile = pair; tile < args.num_tiles; tile += num_pairs, n++) {
+    for (int tile = pair; tile < num_items; tile += num_pairs, n++) {
       int mb, nb;
-      coords(tile, mb, nb);
+      const int half = coords(tile, mb, nb);
       const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar(n & 1), (uint32_t)(n >> 1) & 1u, abort_flag));
       if (!got) break;
       tc_fence_after();
       const int row0 = mb * 256 + (int)rank * kPairHalf + q * 32;
       const uint32_t acc = tmem_base + ((uint32_t)(q * 32) << 16) + (n & 1) * kP2Acc1;
 #pragma unroll 1
-      for (int i = 0; i < kNum; i++) {
+      for (int i = 0; i < (half < 0 ? kNum : kNum / 2); i++) {
         // the first accumulator's last columns, the second's first ones are shared: read them first
-        const int c = ((n & 1) ? i : (i + kNum - 1) % kNum) * kBox;
-        const int col0 = nb * 256 + c;
+        // (a half tile in the first accumulator leaves the shared columns alone)
+        const int c = ((n & 1) || half >= 0 ? i : (i + kNum - 1) % kNum) * kBox;
+        const int col0 = nb * 256 + max(half, 0) * 128 + c;
         uint32_t w[32];
         const float bias0 = chunk_bias(args, 0, col0);
         const float bias1 = OUT == FP8_DT_F32 ? 0.0f : chunk_bias(args, 0, col0 + 32);
@@ -776,20 +820,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(map_to_rank(tempty_bar, 0));
         }
-        if (!args.vec_out) {  // rows that do not start on 16-byte boundaries: element stores
-          const int row = row0 + lane;
-          if (row < args.rows) {
-            const size_t at = (size_t)row * args.ld_out + col0;
-#pragma unroll
-            for (int j = 0; j < kBox; j++) {
-              if (col0 + j < args.cols) {
-                if constexpr (OUT == FP8_DT_F32) reinterpret_cast<uint32_t *>(args.out)[at + j] = w[j];
-                else reinterpret_cast<uint16_t *>(args.out)[at + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-              }
-            }
-          }
-          continue;
-        }
         const uint32_t stg = stg0 + box * kWideStageOutBytes;
         box ^= 1u;
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
@@ -798,6 +828,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ch = 0; ch < 8; ch++) {  // 16-byte chunk ch of this row, 128B swizzle
           const uint32_t addr = stg + lane * 128 + ((ch ^ (lane & 7)) << 4);
           st_shared_v4(addr, w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+        }
+        if (!args.vec_out) {
+          // Rows that do not start on 16-byte boundaries: element stores, a warp
+          // per row (a lane per row took five times as long, 32 sectors a store).
+          __syncwarp();
+          store_box_elements<OUT>(args, stg, row0, col0, lane);
+          continue;
         }
         fence_async_shared();
         __syncwarp();

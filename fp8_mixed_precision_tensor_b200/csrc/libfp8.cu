@@ -899,8 +899,7 @@ int block_info(DeviceInfo **d, BlockInfo **out) {
   if (b.ready) return FP8_OK;
   using bgemm::k_bgemm;
   constexpr int no = bgemm::kNoCast;
-  int rc = set_max_smem(k_bgemm<false, false, no>) | set_max_smem(k_bgemm<false, true, no>) |
-           set_max_smem(k_bgemm<true, false, no>) | set_max_smem(k_bgemm<true, true, no>) |
+  int rc = set_max_smem(k_bgemm<false, false, no>) | set_max_smem(k_bgemm<true, false, no>) |
            set_max_smem(k_bgemm<false, false, FP8_DT_F32>) | set_max_smem(k_bgemm<false, false, FP8_DT_BF16>) |
            set_max_smem(k_bgemm<false, false, FP8_DT_F16>);
   rc |= set_pair_smem<false, false>() | set_pair_smem<false, true>() | set_pair_smem<true, true>();
@@ -917,7 +916,8 @@ int block_info(DeviceInfo **d, BlockInfo **out) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (cudaOccupancyMaxActiveClusters(&b.pair_clusters, bgemm::k_bgemm2<false, false, FP8_DT_BF16>, &cfg) !=
-      cudaSuccess)
+          cudaSuccess ||
+      b.pair_clusters < 1)
     return FP8_ERR_CUDA;
   b.ready = true;
   return FP8_OK;
@@ -1042,7 +1042,11 @@ int launch_bgemm2(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, i
   if ((rc = make_scale_map(&msb, B.b->s, cols, K, 2))) return rc;
   mo = ma;  // unused by the element stores
   if (a.vec_out && (rc = make_pitched_out_map(&mo, a.out, a.out_dtype, rows, cols, a.ld_out))) return rc;
-  const unsigned grid = 2 * (unsigned)(a.num_tiles < clusters ? a.num_tiles : clusters);
+  // the last wave's tiles in halves where the halves fit one wave
+  const int last = a.num_tiles % clusters;
+  a.whole = a.num_tiles - (2 * last <= clusters ? last : 0);
+  const int items = a.whole + 2 * (a.num_tiles - a.whole);
+  const unsigned grid = 2 * (unsigned)(items < clusters ? items : clusters);
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, gemm::kThreads, kP2SmemBytes, stream, 2, ma, mb, msa, msb, mo, a);
   };
@@ -1102,13 +1106,7 @@ int run_bgemm(const BOperand &A, const BOperand &B, const void *bias, int bias_d
                                       stream);
     }
   }
-  const long long pair_tiles = (long long)((R + 255) / 256) * ((C + 255) / 256);
-  if (bi->pair_clusters > 0 && pair_tiles >= bi->pair_clusters)
-    return launch_bgemm2<A_MN, B_MN>(A, B, a, red, bi->pair_clusters, stream);
-  const int bn = C <= 128 ? 128 : (long long)((R + 127) / 128) * ((C + 255) / 256) >= d->sms ? 256 : 128;
-  const long long tiles = (long long)((R + 127) / 128) * ((C + bn - 1) / bn);
-  return launch_bgemm<A_MN, B_MN>(A, B, a, red, bn, pick_splits(tiles, kblocks, bn == 256 ? d->sms : 2 * d->sms),
-                                  stream);
+  return launch_bgemm2<A_MN, B_MN>(A, B, a, red, bi->pair_clusters, stream);
 }
 
 }  // namespace
