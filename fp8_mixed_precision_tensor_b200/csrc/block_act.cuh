@@ -32,39 +32,45 @@ namespace block {
 // exactly on an FP8 rounding border one time in sixteen: the tie would then go
 // to the even code where the true value goes to the lower one.  So y p is
 // subtracted rounding toward zero, and da act' = da + da r is rounded to the
-// side of da on which it lies; a p that has underflowed counts as the smallest
-// normal number (r is then positive).
+// side of da on which it lies.  p never reaches 0 (the smallest subnormal is
+// added to it, which shows in nothing else), and r is then positive.
+//
+// These kernels were bound by the ALU pipe (minima, selects, logic: half the
+// rate of FMA), so the arithmetic is on the packed binary32 instructions and
+// the rest as little as it can be: 43 -> 20 instructions per element forward,
+// 63 -> 35 backward.
 // ex2.approx and rcp.approx are within 2 units in the last place, and the
-// argument's rounding adds about |u| units to exp(-u).
-constexpr float kTiny = 1.17549435e-38f;
+// argument's rounding adds about |u| units to exp(-u); exp(-u) below 2^-126
+// counts as 0.
+constexpr float kLeast = 1.4012984643e-45f;  // 2^-149
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+__device__ __forceinline__ float2 exp2_approx(float2 x) {
+  float2 r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
   return r;
 }
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+__device__ __forceinline__ float2 rcp_approx(float2 x) {
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
   return r;
 }
 
-// The gates of two elements, on the packed binary32 instructions (two results
-// per issue slot): y = |h|, at most 110 (exp(-110) is 0 in binary32; a NaN
-// stays), p and, with GRAD, r.
+// The gates of two elements: y = |h|, at most 110 (exp(-110) is 0 in binary32;
+// a NaN stays), p and, with GRAD, r.
 template <int ACT, bool GRAD>
 __device__ __forceinline__ void gate2(float2 h, float2 &y, float2 &p, float2 &r) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y.x) : "f"(fabsf(h.x)), "f"(110.0f));
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y.y) : "f"(fabsf(h.y)), "f"(110.0f));
-  const float lx = (__float_as_uint(h.x) >> 31) ? 0.0f : kTiny, ly = (__float_as_uint(h.y) >> 31) ? 0.0f : kTiny;
   if constexpr (ACT == FP8_ACT_GELU_ERF) {
-    p = make_float2(fmaxf(0.5f * erfcf(y.x * 0.70710678118654752f), lx),
-                    fmaxf(0.5f * erfcf(y.y * 0.70710678118654752f), ly));
+    const float2 e = make_float2(erfcf(y.x * 0.70710678118654752f), erfcf(y.y * 0.70710678118654752f));
+    p = __ffma2_rn(e, both(0.5f), both(kLeast));
     if constexpr (GRAD) {
-      const float2 a = __fmul2_rn(__fmul2_rn(y, y), both(-0.5f * kLog2e));
-      const float2 s = __fmul2_rn(make_float2(exp2_approx(a.x), exp2_approx(a.y)), both(0.39894228040143268f));
-      r = __ffma2_rn(y, make_float2(fmaxf(s.x, lx), fmaxf(s.y, ly)), make_float2(-p.x, -p.y));
+      const float2 s = exp2_approx(__fmul2_rn(__fmul2_rn(y, y), both(-0.5f * kLog2e)));
+      // (where both have underflowed: y 2^-149 - 2^-149 > 0)
+      r = __ffma2_rn(y, __ffma2_rn(s, both(0.39894228040143268f), both(kLeast)), make_float2(-p.x, -p.y));
     }
   } else {
     constexpr float c = 1.5957691216057308f;  // 2 sqrt(2/pi)
@@ -76,11 +82,9 @@ __device__ __forceinline__ void gate2(float2 h, float2 &y, float2 &p, float2 &r)
     } else {
       a = __fmul2_rn(y, both(-kLog2e));
     }
-    const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
-    const float2 o = __fadd2_rn(e, both(1.0f));
-    const float2 big = make_float2(rcp_approx(o.x), rcp_approx(o.y));
-    p = __fmul2_rn(e, big);
-    p = make_float2(fmaxf(p.x, lx), fmaxf(p.y, ly));
+    const float2 e = exp2_approx(a);
+    const float2 big = rcp_approx(__fadd2_rn(e, both(1.0f)));
+    p = __ffma2_rn(e, big, both(kLeast));
     if constexpr (GRAD) {
       const float2 yb = __fmul2_rn(y, big);
       const float2 w = ACT == FP8_ACT_GELU_TANH ? __ffma2_rn(yb, du, both(-1.0f)) : __fadd2_rn(yb, both(-1.0f));
@@ -99,8 +103,9 @@ __device__ __forceinline__ float2 act_grad2(float2 h, float2 r, float2 da) {
   r = make_float2(__uint_as_float(__float_as_uint(r.x) ^ sx), __uint_as_float(__float_as_uint(r.y) ^ sy));
   const float2 base = make_float2(sx ? 0.0f : da.x, sy ? 0.0f : da.y);
   const float2 up = __ffma2_ru(da, r, base), down = __ffma2_rd(da, r, base);
-  return make_float2((int)(__float_as_uint(da.x) ^ __float_as_uint(r.x)) < 0 ? down.x : up.x,
-                     (int)(__float_as_uint(da.y) ^ __float_as_uint(r.y)) < 0 ? down.y : up.y);
+  // the side: the sign of da r, kept from underflowing
+  const float2 side = __fmul2_rn(__fmul2_rn(r, both(1.2676506e30f)), da);
+  return make_float2(side.x > 0.0f ? up.x : down.x, side.y > 0.0f ? up.y : down.y);
 }
 
 struct ActFwd {
@@ -128,10 +133,8 @@ __global__ void __launch_bounds__(kActThreads, 2) k_act_fwd(const ActFwd p) {
   constexpr int RP = 4;
   const int tiles_c = (p.cols + kTile - 1) / kTile;
   const long long tiles = (long long)((p.rows + kTile - 1) / kTile) * tiles_c;
-  const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile;
-    const int col = col0 + c8 * 8;
     Raw8<DT> raw[RP];
     load_tile<DT>(p.h, p.ldh, p.vec_h, row0, col0, p.rows, p.cols, raw);
     cast_raw_rows<DT, FP8_E4M3>(raw, p.cq, p.cs, p.ldc, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
@@ -149,8 +152,8 @@ __global__ void __launch_bounds__(kActThreads, 2) k_act_fwd(const ActFwd p) {
           f[i][j] = a.x;
           f[i][j + 1] = a.y;
         }
-        if (p.a) store8<DT>(p.vec_a, p.a, p.lda, row0 + r0 + Geo<RP>::kStep * i, col, p.rows, p.cols, f[i]);
       }
+      if (p.a) store_tile<DT>(p.vec_a, p.a, p.lda, row0, col0, p.rows, p.cols, f);
       if (p.aq) cast_tile_rows<FP8_E4M3>(f, p.aq, p.as, p.lda_q, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
     }
   }
@@ -193,7 +196,7 @@ struct ActBwdSmem {
 // written.  dh and act(h') of a thread's 32 elements stay in registers between
 // the amaxes and the encoding, which leaves room for one CTA of 16 warps per
 // SM; the next tile's inputs are copied into shared memory meanwhile.  Bound
-// by instruction issue as much as by HBM (about 30 per element).
+// by instruction issue as much as by HBM.
 // GFMT: format of dh's codes.
 template <int DT, int ACT, int GFMT>
 __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
@@ -275,9 +278,8 @@ __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
         d[i][j] = g.x;
         d[i][j + 1] = g.y;
       }
-      if (p.dh_hp)
-        store8<DT>(p.vec_dh, p.dh_hp, p.lddh, row0 + r0 + Geo<RP>::kStep * i, col, p.rows, p.cols, d[i]);
     }
+    if (p.dh_hp) store_tile<DT>(p.vec_dh, p.dh_hp, p.lddh, row0, col0, p.rows, p.cols, d);
     if (p.dh.q) cast_tile_rows<GFMT>(d, p.dh.q, p.dh.s, p.dh.ldq, row0, col0, p.rows, p.cols, gmax, p.margin);
     if (p.dh.qt)
       cast_tile_cols<GFMT>(d, sc[0], p.dh.qt, p.dh.st, p.dh.ldqt, row0, col0, p.rows, p.cols, gmax, p.margin);

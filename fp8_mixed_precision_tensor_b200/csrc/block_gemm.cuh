@@ -165,10 +165,11 @@ __device__ __forceinline__ void cast_tokens(const BArgs &a, int t0, int kb, uint
     const int t = t0 + 2 * i + half;
     const float s = __shfl_sync(0xffffffffu, own, (lane & 16) + 4 * i);
     float f[8];
+    float2 s4[4];
     block::unpack8<DT>(raw[i], f);
-#pragma unroll
-    for (int j = 0; j < 8; j++) f[j] *= s;
-    const uint2 c = block::enc8<FP8_E4M3>(f, nan);
+    block::spread_scale(s, s4);
+    uint2 c = block::enc8<FP8_E4M3>(f, s4);
+    if (nan) c = block::enc8_any<FP8_E4M3>(f, s4);
     const uint32_t at = tile + t * 128 + (((c8 >> 1) ^ (t & 7)) << 4) + (c8 & 1) * 8;
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(c.x), "r"(c.y) : "memory");
   }

@@ -146,10 +146,18 @@ __device__ __forceinline__ void load_tile(const void *x, size_t ld, bool vec, in
 }
 
 // Running maxima of magnitudes on the stored words: two 16-bit magnitudes per
-// word (their bits order like the values, NaN on top), or one of 32 bits.
+// word, or one of 32 bits.  A NaN anywhere stays one.
 template <int DT>
 __device__ __forceinline__ uint32_t max_words(uint32_t m, uint32_t w) {
-  return DT == FP8_DT_F32 ? max(m, w & 0x7fffffffu) : __vmaxu2(m, w & 0x7fff7fffu);
+  uint32_t r;
+  if constexpr (DT == FP8_DT_F32) {
+    asm("{\n\t.reg .f32 t0;\n\tabs.f32 t0, %2;\n\tmax.NaN.f32 %0, %1, t0;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  } else if constexpr (DT == FP8_DT_BF16) {
+    asm("{\n\t.reg .b32 t0;\n\tabs.bf16x2 t0, %2;\n\tmax.NaN.bf16x2 %0, %1, t0;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  } else {
+    asm("{\n\t.reg .b32 t0;\n\tabs.f16x2 t0, %2;\n\tmax.NaN.f16x2 %0, %1, t0;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  }
+  return r;
 }
 
 // The binary32 bit pattern of a 16-bit magnitude.
@@ -165,10 +173,12 @@ __device__ __forceinline__ uint32_t word_abs(uint32_t m) {
   return widen_abs<DT>(max(m & 0xffffu, m >> 16));
 }
 
-// Running maximum |x| over floats; a NaN anywhere stays one and orders above inf as bits.
-__device__ __forceinline__ float absmax(float acc, float x) {
+// Running maximum of magnitudes over two floats; a NaN anywhere stays one and orders above inf as bits.
+__device__ __forceinline__ float absmax2(float acc, float x, float y) {
   float r;
-  asm("{\n\t.reg .f32 t0;\n\tabs.f32 t0, %2;\n\tmax.NaN.f32 %0, %1, t0;\n\t}" : "=f"(r) : "f"(acc), "f"(x));
+  asm("{\n\t.reg .f32 t0, t1;\n\tabs.f32 t0, %2;\n\tabs.f32 t1, %3;\n\tmax.NaN.f32 %0, %1, t0, t1;\n\t}"
+      : "=f"(r)
+      : "f"(acc), "f"(x), "f"(y));
   return r;
 }
 
@@ -181,42 +191,42 @@ __device__ __forceinline__ uint32_t enc4_no_nan(float a, float b, float c, float
          ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, F) << 16);
 }
 
+// f * s as codes, none of them NaN / any value.
 template <int FMT>
-__device__ __forceinline__ uint2 enc8(const float (&f)[8], bool nan) {
-  if (nan) return make_uint2(enc4<FMT>(f[0], f[1], f[2], f[3]), enc4<FMT>(f[4], f[5], f[6], f[7]));
-  return make_uint2(enc4_no_nan<FMT>(f[0], f[1], f[2], f[3]), enc4_no_nan<FMT>(f[4], f[5], f[6], f[7]));
+__device__ __forceinline__ uint2 enc8(const float (&f)[8], const float2 (&s)[4]) {
+  float2 y[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) y[j] = __fmul2_rn(make_float2(f[2 * j], f[2 * j + 1]), s[j]);
+  return make_uint2(enc4_no_nan<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), enc4_no_nan<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
+}
+template <int FMT>
+__device__ __forceinline__ uint2 enc8_any(const float (&f)[8], const float2 (&s)[4]) {
+  float2 y[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) y[j] = __fmul2_rn(make_float2(f[2 * j], f[2 * j + 1]), s[j]);
+  return make_uint2(enc4<FMT>(y[0].x, y[0].y, y[1].x, y[1].y), enc4<FMT>(y[2].x, y[2].y, y[3].x, y[3].y));
 }
 
-// Eight code bytes to q[row, col...] (rows of ldq bytes, a multiple of 16;
-// col a multiple of 8, so an 8-byte store is aligned).
-__device__ __forceinline__ void store_codes8(uint8_t *q, size_t ldq, int row, int col, int rows, int cols, uint2 v) {
-  if (row >= rows || col >= cols) return;
+// A thread's RP groups of eight codes to q (rows of ldq bytes, a multiple of
+// 16; col a multiple of 8, so an 8-byte store is aligned).  One predicate per
+// row; the group that straddles the row's end is stored apart.
+template <int RP>
+__device__ __forceinline__ void store_codes(uint8_t *q, size_t ldq, int row0, int col, int rows, int cols,
+                                            const uint2 (&o)[RP]) {
+  const int row = row0 + (threadIdx.x >> 4);
   uint8_t *p = q + (size_t)row * ldq + col;
-  if (col + 8 <= cols) {
-    __stcs(reinterpret_cast<uint2 *>(p), v);
-    return;
+  const int left = col + 8 <= cols ? rows - row : 0;  // rows that take whole groups
+#pragma unroll
+  for (int i = 0; i < RP; i++)
+    if (i * Geo<RP>::kStep < left) __stcs(reinterpret_cast<uint2 *>(p + (size_t)(i * Geo<RP>::kStep) * ldq), o[i]);
+  if (col < cols && col + 8 > cols) {
+#pragma unroll 1
+    for (int j = 0; j < cols - col; j++)
+#pragma unroll
+      for (int i = 0; i < RP; i++)
+        if (row + i * Geo<RP>::kStep < rows)
+          p[(size_t)(i * Geo<RP>::kStep) * ldq + j] = (uint8_t)((j < 4 ? o[i].x : o[i].y) >> (8 * (j & 3)));
   }
-  const unsigned long long w = ((unsigned long long)v.y << 32) | v.x;
-  for (int j = 0; j < cols - col; j++) p[j] = (uint8_t)(w >> (8 * j));
-}
-
-// f * s (one scale) and f * s (a scale per column) as codes.  nan: whether a
-// value may be NaN.
-template <int FMT>
-__device__ __forceinline__ void cast_row8(uint8_t *q, size_t ldq, int row, int col, int rows, int cols,
-                                          const float (&f)[8], float s, bool nan) {
-  float y[8];
-#pragma unroll
-  for (int j = 0; j < 8; j++) y[j] = f[j] * s;
-  store_codes8(q, ldq, row, col, rows, cols, enc8<FMT>(y, nan));
-}
-template <int FMT>
-__device__ __forceinline__ void cast_col8(uint8_t *q, size_t ldq, int row, int col, int rows, int cols,
-                                          const float (&f)[8], const float (&s)[8], bool nan) {
-  float y[8];
-#pragma unroll
-  for (int j = 0; j < 8; j++) y[j] = f[j] * s[j];
-  store_codes8(q, ldq, row, col, rows, cols, enc8<FMT>(y, nan));
 }
 
 // Scale byte of (r, b) plus, behind the last block, the padding of its group of four.
@@ -253,7 +263,7 @@ struct ColScratch {
 // some amax is not finite.  Called by all threads.
 template <int RP>
 __device__ __forceinline__ bool column_scales(ColScratch<RP> &sc, uint8_t *st, int row0, int col0, int rows, float fmax,
-                                              int margin, float (&s)[8]) {
+                                              int margin, float2 (&s)[4]) {
   const int c8 = threadIdx.x & 15;
   uint32_t a = 0;
   __syncthreads();
@@ -266,7 +276,7 @@ __device__ __forceinline__ bool column_scales(ColScratch<RP> &sc, uint8_t *st, i
   }
   const bool bad = __syncthreads_or(a >= 0x7f800000u);
   *reinterpret_cast<float4 *>(&s[0]) = *reinterpret_cast<const float4 *>(&sc.scale[c8 * 8]);
-  *reinterpret_cast<float4 *>(&s[4]) = *reinterpret_cast<const float4 *>(&sc.scale[c8 * 8 + 4]);
+  *reinterpret_cast<float4 *>(&s[2]) = *reinterpret_cast<const float4 *>(&sc.scale[c8 * 8 + 4]);
   return bad;
 }
 
@@ -288,21 +298,25 @@ template <int FMT, int RP>
 __device__ __forceinline__ void cast_tile_cols(const float (&v)[RP][8], ColScratch<RP> &sc, uint8_t *qt,
                                                uint8_t *st, size_t ldq, int row0, int col0, int rows, int cols,
                                                float fmax, int margin) {
-  const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   uint32_t m[8];
 #pragma unroll
   for (int j = 0; j < 8; j++) {
     float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < RP; i++) a = absmax(a, v[i][j]);
+    for (int i = 0; i < RP; i += 2) a = absmax2(a, v[i][j], v[i + 1][j]);
     m[j] = __float_as_uint(a);
   }
   put_column_maxima(sc, m);
-  float s[8];
+  float2 s[4];
   const bool bad = column_scales(sc, st, row0, col0, rows, fmax, margin, s);
+  uint2 o[RP];
 #pragma unroll
-  for (int i = 0; i < RP; i++)
-    cast_col8<FMT>(qt, ldq, row0 + r0 + Geo<RP>::kStep * i, col0 + c8 * 8, rows, cols, v[i], s, bad);
+  for (int i = 0; i < RP; i++) o[i] = enc8<FMT>(v[i], s);
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < RP; i++) o[i] = enc8_any<FMT>(v[i], s);
+  }
+  store_codes(qt, ldq, row0, col0 + (threadIdx.x & 15) * 8, rows, cols, o);
 }
 
 // The scales of a thread's RP row blocks: m[i] is the thread's maximum of its
@@ -346,31 +360,74 @@ __device__ __forceinline__ bool row_scales(const uint32_t (&m)[RP], uint8_t *s, 
   return __any_sync(0xffffffffu, v >= 0x7f800000u);
 }
 
+// One scale as the four pairs of a group.
+__device__ __forceinline__ void spread_scale(float s, float2 (&o)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; j++) o[j] = both(s);
+}
+
 // The row side of the same tile of floats.
 template <int FMT, int RP>
 __device__ __forceinline__ void cast_tile_rows(const float (&v)[RP][8], uint8_t *q, uint8_t *s, size_t ldq,
                                                int row0, int col0, int rows, int cols, float fmax, int margin) {
-  const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   uint32_t m[RP];
 #pragma unroll
   for (int i = 0; i < RP; i++) {
     float a = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; j++) a = absmax(a, v[i][j]);
+    for (int j = 0; j < 8; j += 2) a = absmax2(a, v[i][j], v[i][j + 1]);
     m[i] = __float_as_uint(a);
   }
   float sc[RP];
   const bool nan = row_scales(m, s, row0, col0, (cols + kTile - 1) / kTile, fmax, margin, sc);
+  uint2 o[RP];
 #pragma unroll
-  for (int i = 0; i < RP; i++)
-    cast_row8<FMT>(q, ldq, row0 + r0 + Geo<RP>::kStep * i, col0 + c8 * 8, rows, cols, v[i], sc[i], nan);
+  for (int i = 0; i < RP; i++) {
+    float2 s4[4];
+    spread_scale(sc[i], s4);
+    o[i] = enc8<FMT>(v[i], s4);
+  }
+  if (nan) {
+#pragma unroll
+    for (int i = 0; i < RP; i++) {
+      float2 s4[4];
+      spread_scale(sc[i], s4);
+      o[i] = enc8_any<FMT>(v[i], s4);
+    }
+  }
+  store_codes(q, ldq, row0, col0 + (threadIdx.x & 15) * 8, rows, cols, o);
+}
+
+// A tile of elements as stored, encoded with one scale per row (sc) or per column pair (s4).
+template <int DT, int FMT, int RP>
+__device__ __forceinline__ void store_raw_rows(const Raw8<DT> (&raw)[RP], const float (&sc)[RP], bool nan, uint8_t *q,
+                                               size_t ldq, int row0, int col, int rows, int cols) {
+  uint2 o[RP];
+#pragma unroll
+  for (int i = 0; i < RP; i++) {
+    float f[8];
+    float2 s4[4];
+    unpack8<DT>(raw[i], f);
+    spread_scale(sc[i], s4);
+    o[i] = enc8<FMT>(f, s4);
+  }
+  if (nan) {
+#pragma unroll
+    for (int i = 0; i < RP; i++) {
+      float f[8];
+      float2 s4[4];
+      unpack8<DT>(raw[i], f);
+      spread_scale(sc[i], s4);
+      o[i] = enc8_any<FMT>(f, s4);
+    }
+  }
+  store_codes(q, ldq, row0, col, rows, cols, o);
 }
 
 // The row side of a tile of elements as stored.
 template <int DT, int FMT, int RP>
 __device__ __forceinline__ void cast_raw_rows(const Raw8<DT> (&raw)[RP], uint8_t *q, uint8_t *s, size_t ldq,
                                               int row0, int col0, int rows, int cols, float fmax, int margin) {
-  const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   uint32_t m[RP];
 #pragma unroll
   for (int i = 0; i < RP; i++) {
@@ -381,12 +438,7 @@ __device__ __forceinline__ void cast_raw_rows(const Raw8<DT> (&raw)[RP], uint8_t
   }
   float sc[RP];
   const bool nan = row_scales(m, s, row0, col0, (cols + kTile - 1) / kTile, fmax, margin, sc);
-#pragma unroll
-  for (int i = 0; i < RP; i++) {
-    float f[8];
-    unpack8<DT>(raw[i], f);
-    cast_row8<FMT>(q, ldq, row0 + r0 + Geo<RP>::kStep * i, col0 + c8 * 8, rows, cols, f, sc[i], nan);
-  }
+  store_raw_rows<DT, FMT>(raw, sc, nan, q, ldq, row0, col0 + (threadIdx.x & 15) * 8, rows, cols);
 }
 
 // Cast of x [rows, cols] to 1x128 blocks and / or 128x1 blocks, x read once.
@@ -395,7 +447,7 @@ __device__ __forceinline__ void cast_raw_rows(const Raw8<DT> (&raw)[RP], uint8_t
 // over the thread's 8 rows and then through shared memory.  HBM-bound: 2 B
 // read and 1 B written per direction and 16-bit element.
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kCastThreads)
+__global__ void __launch_bounds__(kCastThreads, DT == FP8_DT_F32 ? 2 : 3)
     k_block_cast(const void *__restrict__ x, int rows, int cols, size_t ldx, int vec, int margin, const CastOut out) {
   pdl_launch_dependents();
   pdl_wait();
@@ -404,7 +456,7 @@ __global__ void __launch_bounds__(kCastThreads)
   const float fmax = FMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
   const int tiles_c = (cols + kTile - 1) / kTile;
   const long long tiles = (long long)((rows + kTile - 1) / kTile) * tiles_c;
-  const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  const int c8 = threadIdx.x & 15;
   for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile;
     const int col = col0 + c8 * 8;
@@ -428,14 +480,24 @@ __global__ void __launch_bounds__(kCastThreads)
     }
     if (out.q) cast_raw_rows<DT, FMT>(raw, out.q, out.s, out.ldq, row0, col0, rows, cols, fmax, margin);
     if (out.qt) {
-      float s[8];
+      float2 s[4];
       const bool bad = column_scales(sc, out.st, row0, col0, rows, fmax, margin, s);
+      uint2 o[RP];
 #pragma unroll
       for (int i = 0; i < RP; i++) {
         float f[8];
         unpack8<DT>(raw[i], f);
-        cast_col8<FMT>(out.qt, out.ldqt, row0 + r0 + Geo<RP>::kStep * i, col, rows, cols, f, s, bad);
+        o[i] = enc8<FMT>(f, s);
       }
+      if (bad) {
+#pragma unroll
+        for (int i = 0; i < RP; i++) {
+          float f[8];
+          unpack8<DT>(raw[i], f);
+          o[i] = enc8_any<FMT>(f, s);
+        }
+      }
+      store_codes(out.qt, out.ldqt, row0, col, rows, cols, o);
     }
   }
 }
@@ -444,7 +506,7 @@ __global__ void __launch_bounds__(kCastThreads)
 // for each of its rows (out.s) and each of its columns (out.st), so that the
 // codes serve products that reduce along either axis.
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kCastThreads)
+__global__ void __launch_bounds__(kCastThreads, DT == FP8_DT_F32 ? 2 : 3)
     k_block_cast_square(const void *__restrict__ x, int rows, int cols, size_t ldx, int vec, int margin,
                         const CastOut out) {
   pdl_launch_dependents();
@@ -454,7 +516,7 @@ __global__ void __launch_bounds__(kCastThreads)
   const float fmax = FMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
   const int tiles_c = (cols + kTile - 1) / kTile, tiles_r = (rows + kTile - 1) / kTile;
   const long long tiles = (long long)tiles_r * tiles_c;
-  const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  const int c8 = threadIdx.x & 15;
   for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile;
     const int col = col0 + c8 * 8;
@@ -472,14 +534,10 @@ __global__ void __launch_bounds__(kCastThreads)
       put_scale(out.s, r, col0 / kTile, tiles_c, r < rows ? k : 0);
       put_scale(out.st, c, row0 / kTile, tiles_r, c < cols ? k : 0);
     }
-    const float s = pow2f(k);
-    const bool nan = m >= 0x7f800000u;
+    float sc[RP];
 #pragma unroll
-    for (int i = 0; i < RP; i++) {
-      float f[8];
-      unpack8<DT>(raw[i], f);
-      cast_row8<FMT>(out.q, out.ldq, row0 + r0 + Geo<RP>::kStep * i, col, rows, cols, f, s, nan);
-    }
+    for (int i = 0; i < RP; i++) sc[i] = pow2f(k);
+    store_raw_rows<DT, FMT>(raw, sc, m >= 0x7f800000u, out.q, out.ldq, row0, col, rows, cols);
   }
 }
 
@@ -554,6 +612,52 @@ __device__ __forceinline__ void store8(bool vec, void *out, size_t ld, int row, 
     for (int j = 0; j < 8; j++)
       if (col + j < cols) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
   }
+}
+
+// Eight floats rounded to DT as 16-byte words.
+template <int DT>
+__device__ __forceinline__ void pack8(const float (&f)[8], uint4 (&w)[DT == FP8_DT_F32 ? 2 : 1]) {
+  if constexpr (DT == FP8_DT_F32) {
+    w[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    w[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+  } else {
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      if constexpr (DT == FP8_DT_BF16) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+        h[k] = *reinterpret_cast<const uint32_t *>(&b);
+      } else {
+        h[k] = f16x2(f[2 * k], f[2 * k + 1]);
+      }
+    }
+    w[0] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+
+// A thread's part of a tile of floats, rounded to DT.
+template <int DT, int RP>
+__device__ __forceinline__ void store_tile(bool vec, void *out, size_t ld, int row0, int col0, int rows, int cols,
+                                           const float (&f)[RP][8]) {
+  const int row = row0 + (threadIdx.x >> 4), col = col0 + (threadIdx.x & 15) * 8;
+  if (wide_tile(vec, col0, cols)) {
+    constexpr int esz = DT == FP8_DT_F32 ? 4 : 2;
+    uint8_t *p = reinterpret_cast<uint8_t *>(out) + ((size_t)row * ld + col) * esz;
+    const int left = col < cols ? rows - row : 0;
+#pragma unroll
+    for (int i = 0; i < RP; i++) {
+      uint4 w[DT == FP8_DT_F32 ? 2 : 1];
+      pack8<DT>(f[i], w);
+      if (i * Geo<RP>::kStep < left) {
+        uint4 *q = reinterpret_cast<uint4 *>(p + (size_t)(i * Geo<RP>::kStep) * ld * esz);
+        __stcs(q, w[0]);
+        if constexpr (DT == FP8_DT_F32) __stcs(q + 1, w[1]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < RP; i++) store8<DT>(false, out, ld, row + i * Geo<RP>::kStep, col, rows, cols, f[i]);
 }
 
 // Decode of blocked codes: x = dec(q) * 2^(byte - 127).  COLS: 128x1 blocks
