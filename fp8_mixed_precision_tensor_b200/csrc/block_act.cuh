@@ -132,9 +132,8 @@ __global__ void __launch_bounds__(kActThreads, 2) k_act_fwd(const ActFwd p) {
   pdl_wait();
   constexpr int RP = 4;
   const int tiles_c = (p.cols + kTile - 1) / kTile;
-  const long long tiles = (long long)((p.rows + kTile - 1) / kTile) * tiles_c;
-  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile;
+  {
+    const auto [row0, col0] = tile_at(blockIdx.x, tiles_c);
     Raw8<DT> raw[RP];
     load_tile<DT>(p.h, p.ldh, p.vec_h, row0, col0, p.rows, p.cols, raw);
     cast_raw_rows<DT, FP8_E4M3>(raw, p.cq, p.cs, p.ldc, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
@@ -206,17 +205,32 @@ __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
   extern __shared__ __align__(16) uint8_t act_smem[];
   __shared__ ColScratch<RP> sc[2];
   const int tiles_c = (p.cols + kTile - 1) / kTile;
-  const long long tiles = (long long)((p.rows + kTile - 1) / kTile) * tiles_c;
+  const unsigned tiles = (unsigned)((p.rows + kTile - 1) / kTile) * (unsigned)tiles_c;
   const int kg = (tiles_c + 3) / 4;
   const float gmax = GFMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
   const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   const uint32_t smem = smem_u32(act_smem);
   uint32_t sb[RP];  // scale bytes of the tile in the buffer
   // Starts the copies of tile t into buffer b (tiles with a ragged or unaligned row are read directly instead).
-  auto prefetch = [&](long long t, int b) {
-    const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile, col = col0 + c8 * 8;
+  auto prefetch = [&](TileAt at, int b) {
+    const int row0 = at.row0, col0 = at.col0, col = col0 + c8 * 8;
     if (wide_tile(p.vec_da, col0, p.cols)) {
       const uint32_t base = smem + b * ActBwdSmem<DT>::kBuffer;
+      if (row0 + kTile <= p.rows && col0 + kTile <= p.cols) {  // inside: nothing to leave out
+        const uint8_t *cq = p.cq + (size_t)(row0 + r0) * p.ldc + col;
+        const size_t esz = DT == FP8_DT_F32 ? 4 : 2;
+        const uint8_t *da = reinterpret_cast<const uint8_t *>(p.da) + ((size_t)(row0 + r0) * p.ldda + col) * esz;
+        const size_t cstep = Geo<RP>::kStep * p.ldc, dstep = Geo<RP>::kStep * p.ldda * esz;
+#pragma unroll
+        for (int i = 0; i < RP; i++, cq += cstep, da += dstep) {
+          cp_async(base + (i * kActThreads + threadIdx.x) * 8, cq, 8, true);
+#pragma unroll
+          for (int v = 0; v < kVecs; v++)
+            cp_async(base + kTile * kTile + ((i * kVecs + v) * kActThreads + threadIdx.x) * 16, da + 16 * v, 16, true);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < RP; i++) {
         const int row = row0 + r0 + Geo<RP>::kStep * i;
@@ -231,16 +245,19 @@ __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if ((long long)blockIdx.x < tiles) prefetch(blockIdx.x, 0);
+  TileAt next = tile_at(blockIdx.x, tiles_c);  // (the grid has at most one CTA per tile)
+  prefetch(next, 0);
   int buf = 0;
-  for (long long t = blockIdx.x; t < tiles; t += gridDim.x, buf ^= 1) {
-    const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile;
+  for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x, buf ^= 1) {
+    const int row0 = next.row0, col0 = next.col0;
     const int col = col0 + c8 * 8;
 #pragma unroll
     for (int i = 0; i < RP; i++)
       sb[i] = p.cs[scale_at(min(row0 + r0 + Geo<RP>::kStep * i, p.rows - 1), col0 / kTile, kg)];
-    if (t + gridDim.x < tiles) prefetch(t + gridDim.x, buf ^ 1);
-    else asm volatile("cp.async.commit_group;" ::: "memory");
+    if (t + gridDim.x < tiles) {
+      next = tile_at(t + gridDim.x, tiles_c);
+      prefetch(next, buf ^ 1);
+    } else asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     float a[RP][8], d[RP][8];
     if (wide_tile(p.vec_da, col0, p.cols)) {

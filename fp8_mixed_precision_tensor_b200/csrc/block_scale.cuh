@@ -40,11 +40,20 @@ __device__ __forceinline__ size_t scale_at(int r, int b, int kgroups) {
   return ((size_t)(r >> 7) * kgroups + (b >> 2)) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (b & 3);
 }
 
-// Exponent k of the scale 2^k of a block with this amax (bit pattern).
-__device__ __forceinline__ int block_exponent(uint32_t amax_bits, float fmax, int margin) {
+// Exponent k of the scale 2^k of a block with this amax (bit pattern).  For a
+// normal amax 1.f 2^e and fmt_max = 1.75 2^E the rule's floor is E - e, less
+// one where 1.f > 1.75: adding 2^23 - 1 - 0.75 2^23 to the bits carries into
+// the exponent exactly then.  The rest (zero, subnormal, not finite) is rare
+// and goes to the general rule.
+__device__ __noinline__ int block_exponent_rare(uint32_t amax_bits, float fmax, int margin) {
   int k;
   if (!scale_exponent(__uint_as_float(amax_bits), fmax, margin, 0, k)) atomicOr(&g_status, FP8_STATUS_NONFINITE);
   return k;
+}
+__device__ __forceinline__ int block_exponent(uint32_t amax_bits, float fmax, int margin) {
+  if (amax_bits - 0x00800000u >= 0x7f000000u) return block_exponent_rare(amax_bits, fmax, margin);
+  const int top = (fmax == kMaxE4M3 ? 8 : 15) + 127;
+  return clamp_exp(top - (int)((amax_bits + 0x1fffffu) >> 23) - margin);
 }
 
 // A cast tile is 128 x 128 elements: 16 threads across (8 elements each), RP
@@ -59,9 +68,18 @@ struct Geo {
   static constexpr int kWarps = kThreads / 32;
 };
 
+// First row and column of tile t (row-major over tiles_c tiles across).
+struct TileAt {
+  int row0, col0;
+};
+__device__ __forceinline__ TileAt tile_at(unsigned t, unsigned tiles_c) {
+  const unsigned r = t / tiles_c;
+  return {(int)(r * kTile), (int)((t - r * tiles_c) * kTile)};
+}
+
 // Eight consecutive elements of a high-precision row as they are stored.
 template <int DT>
-struct Raw8 {
+struct __align__(16) Raw8 {
   static constexpr int kWords = DT == FP8_DT_F32 ? 8 : 4;
   uint32_t w[kWords];
 };
@@ -136,7 +154,16 @@ template <int DT, int RP>
 __device__ __forceinline__ void load_tile(const void *x, size_t ld, bool vec, int row0, int col0, int rows, int cols,
                                           Raw8<DT> (&raw)[RP]) {
   const int row = row0 + (threadIdx.x >> 4), col = col0 + (threadIdx.x & 15) * 8;
-  if (wide_tile(vec, col0, cols)) {
+  if (vec && row0 + kTile <= rows && col0 + kTile <= cols) {  // inside: nothing to clamp
+    constexpr int esz = DT == FP8_DT_F32 ? 4 : 2;
+    const uint8_t *p = reinterpret_cast<const uint8_t *>(x) + ((size_t)row * ld + col) * esz;
+    const size_t step = (size_t)Geo<RP>::kStep * ld * esz;
+#pragma unroll
+    for (int i = 0; i < RP; i++, p += step)
+#pragma unroll
+      for (int h = 0; h < Raw8<DT>::kWords / 4; h++)
+        *reinterpret_cast<uint4 *>(&raw[i].w[4 * h]) = __ldcs(reinterpret_cast<const uint4 *>(p) + h);
+  } else if (wide_tile(vec, col0, cols)) {
 #pragma unroll
     for (int i = 0; i < RP; i++) raw[i] = load_raw8_wide<DT>(x, ld, row + Geo<RP>::kStep * i, col, rows, cols);
   } else {
@@ -184,11 +211,41 @@ __device__ __forceinline__ float absmax2(float acc, float x, float y) {
 
 // enc4 for values none of which is NaN (a block with a finite amax): the
 // saturating conversion alone.
+// (Written out, so that the second pair is converted into the upper half of
+// the first one's register: through cuda_fp8.h's 16-bit result each pair cost
+// three more logic instructions.)
 template <int FMT>
 __device__ __forceinline__ uint32_t enc4_no_nan(float a, float b, float c, float d) {
-  constexpr __nv_fp8_interpretation_t F = FMT == FP8_E4M3 ? __NV_E4M3 : __NV_E5M2;
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, F) |
-         ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, F) << 16);
+  uint32_t r;
+  if constexpr (FMT == FP8_E4M3)
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+  else
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// Four codes as floats.
+template <int FMT>
+__device__ __forceinline__ void dec4(uint32_t w, float2 &a, float2 &b) {
+  uint32_t x, y;
+  if constexpr (FMT == FP8_E4M3)
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(x), "=r"(y)
+        : "r"(w));
+  else
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e5m2x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e5m2x2 %1, hi;\n\t}"
+        : "=r"(x), "=r"(y)
+        : "r"(w));
+  a = h2f2(x);
+  b = h2f2(y);
 }
 
 // f * s as codes, none of them NaN / any value.
@@ -216,16 +273,18 @@ __device__ __forceinline__ void store_codes(uint8_t *q, size_t ldq, int row0, in
   const int row = row0 + (threadIdx.x >> 4);
   uint8_t *p = q + (size_t)row * ldq + col;
   const int left = col + 8 <= cols ? rows - row : 0;  // rows that take whole groups
+  const size_t step = (size_t)Geo<RP>::kStep * ldq;
+  uint8_t *w = p;
 #pragma unroll
-  for (int i = 0; i < RP; i++)
-    if (i * Geo<RP>::kStep < left) __stcs(reinterpret_cast<uint2 *>(p + (size_t)(i * Geo<RP>::kStep) * ldq), o[i]);
+  for (int i = 0; i < RP; i++, w += step)
+    if (i * Geo<RP>::kStep < left) __stcs(reinterpret_cast<uint2 *>(w), o[i]);
   if (col < cols && col + 8 > cols) {
 #pragma unroll 1
     for (int j = 0; j < cols - col; j++)
 #pragma unroll
       for (int i = 0; i < RP; i++)
         if (row + i * Geo<RP>::kStep < rows)
-          p[(size_t)(i * Geo<RP>::kStep) * ldq + j] = (uint8_t)((j < 4 ? o[i].x : o[i].y) >> (8 * (j & 3)));
+          p[i * step + j] = (uint8_t)((j < 4 ? o[i].x : o[i].y) >> (8 * (j & 3)));
   }
 }
 
@@ -442,7 +501,7 @@ __device__ __forceinline__ void cast_raw_rows(const Raw8<DT> (&raw)[RP], uint8_t
 }
 
 // Cast of x [rows, cols] to 1x128 blocks and / or 128x1 blocks, x read once.
-// Each CTA takes 128x128 tiles: the tile sits in registers as stored (64
+// Each CTA takes one 128x128 tile: it sits in registers as stored (64
 // elements per thread), a row's amax is reduced over its 16 lanes, a column's
 // over the thread's 8 rows and then through shared memory.  HBM-bound: 2 B
 // read and 1 B written per direction and 16-bit element.
@@ -455,10 +514,9 @@ __global__ void __launch_bounds__(kCastThreads, DT == FP8_DT_F32 ? 2 : 3)
   __shared__ ColScratch<RP> sc;
   const float fmax = FMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
   const int tiles_c = (cols + kTile - 1) / kTile;
-  const long long tiles = (long long)((rows + kTile - 1) / kTile) * tiles_c;
   const int c8 = threadIdx.x & 15;
-  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile;
+  {
+    const auto [row0, col0] = tile_at(blockIdx.x, tiles_c);
     const int col = col0 + c8 * 8;
     Raw8<DT> raw[RP];
     load_tile<DT>(x, ldx, vec, row0, col0, rows, cols, raw);
@@ -515,10 +573,9 @@ __global__ void __launch_bounds__(kCastThreads, DT == FP8_DT_F32 ? 2 : 3)
   __shared__ uint32_t red[32];
   const float fmax = FMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
   const int tiles_c = (cols + kTile - 1) / kTile, tiles_r = (rows + kTile - 1) / kTile;
-  const long long tiles = (long long)tiles_r * tiles_c;
   const int c8 = threadIdx.x & 15;
-  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int row0 = (int)(t / tiles_c) * kTile, col0 = (int)(t % tiles_c) * kTile;
+  {
+    const auto [row0, col0] = tile_at(blockIdx.x, tiles_c);
     const int col = col0 + c8 * 8;
     Raw8<DT> raw[RP];
     load_tile<DT>(x, ldx, vec, row0, col0, rows, cols, raw);
@@ -561,7 +618,8 @@ __device__ __forceinline__ void decode8(uint2 v, float (&f)[8]) {
   const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
   for (int h = 0; h < 2; h++) {
-    const float2 a = dec2<FMT>(w[h]), b = dec2<FMT>(w[h] >> 16);
+    float2 a, b;
+    dec4<FMT>(w[h], a, b);
     f[4 * h] = a.x;
     f[4 * h + 1] = a.y;
     f[4 * h + 2] = b.x;

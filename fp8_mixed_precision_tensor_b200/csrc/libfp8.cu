@@ -836,6 +836,7 @@ void with_act(int act, F f) {
 template <typename... P, typename... A>
 int launch_pdl(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, unsigned cluster,
                A... args) {
+  if (grid == 0) return FP8_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -853,10 +854,10 @@ int launch_pdl(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
   return cuda_rc(cudaLaunchKernelEx(&cfg, kernel, P(args)...));
 }
 
-// One CTA per 128x128 tile.
+// One CTA per 128x128 tile; 0 for more tiles than a grid can have (codes of 32 TB).
 unsigned tile_grid(int rows, int cols) {
-  const unsigned long long t = (unsigned long long)((rows + 127) / 128) * (unsigned long long)((cols + 127) / 128);
-  return (unsigned)(t < 0x7fffffffull ? t : 0x7fffffffull);
+  const unsigned long long t = (unsigned long long)((rows + 127LL) / 128) * (unsigned long long)((cols + 127LL) / 128);
+  return t <= 0x7fffffffull ? (unsigned)t : 0u;
 }
 
 block::CastOut cast_out(const fp8_blocks *row, const fp8_blocks *col) {
