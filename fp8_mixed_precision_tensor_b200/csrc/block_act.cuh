@@ -194,16 +194,19 @@ struct ActBwdSmem {
 // One pass over 128x128 tiles: 1 + 2 B read, up to 3 code bytes (or 2 B of dh)
 // written.  dh and act(h') of a thread's 32 elements stay in registers between
 // the amaxes and the encoding, which leaves room for one CTA of 16 warps per
-// SM; the next tile's inputs are copied into shared memory meanwhile.  Bound
-// by instruction issue as much as by HBM.
-// GFMT: format of dh's codes.
-template <int DT, int ACT, int GFMT>
-__global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
+// SM (two where only a bfloat16 dh is wanted); the next tile's inputs are copied into
+// shared memory meanwhile.  Bound by instruction issue as much as by HBM.
+// OUT: the format of dh's codes, or kActPlain where no codes are wanted.
+constexpr int kActPlain = -1;
+template <int DT, int ACT, int OUT>
+__global__ void __launch_bounds__(kActThreads, OUT == kActPlain && DT == FP8_DT_BF16 ? 2 : 1) k_act_bwd(const ActBwd p) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int RP = 4, kVecs = Raw8<DT>::kWords / 4;
   extern __shared__ __align__(16) uint8_t act_smem[];
-  __shared__ ColScratch<RP> sc[2];
+  constexpr bool kCodes = OUT != kActPlain;
+  constexpr int GFMT = kCodes ? OUT : FP8_E5M2;
+  __shared__ ColScratch<RP> sc[kCodes ? 2 : 1];
   const int tiles_c = (p.cols + kTile - 1) / kTile;
   const unsigned tiles = (unsigned)((p.rows + kTile - 1) / kTile) * (unsigned)tiles_c;
   const int kg = (tiles_c + 3) / 4;
@@ -289,19 +292,35 @@ __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
         const float2 h = __fmul2_rn(make_float2(a[i][j], a[i][j + 1]), both(s));
         float2 y, q, r;
         gate2<ACT, true>(h, y, q, r);
-        const float2 v = act_value2(h, y, q), g = act_grad2(h, r, make_float2(d[i][j], d[i][j + 1]));
-        a[i][j] = v.x;
-        a[i][j + 1] = v.y;
+        const float2 g = act_grad2(h, r, make_float2(d[i][j], d[i][j + 1]));
         d[i][j] = g.x;
         d[i][j + 1] = g.y;
+        if constexpr (kCodes) {
+          const float2 v = act_value2(h, y, q);
+          a[i][j] = v.x;
+          a[i][j + 1] = v.y;
+        }
       }
     }
     if (p.dh_hp) store_tile<DT>(p.vec_dh, p.dh_hp, p.lddh, row0, col0, p.rows, p.cols, d);
-    if (p.dh.q) cast_tile_rows<GFMT>(d, p.dh.q, p.dh.s, p.dh.ldq, row0, col0, p.rows, p.cols, gmax, p.margin);
-    if (p.dh.qt)
-      cast_tile_cols<GFMT>(d, sc[0], p.dh.qt, p.dh.st, p.dh.ldqt, row0, col0, p.rows, p.cols, gmax, p.margin);
-    if (p.aqt)
-      cast_tile_cols<FP8_E4M3>(a, sc[1], p.aqt, p.ast, p.ldaqt, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
+    if constexpr (kCodes) {
+      // the two column reductions share their barriers
+      const bool dcols = p.dh.qt != nullptr, acols = p.aqt != nullptr;
+      if (dcols) put_tile_maxima(d, sc[0]);
+      if (acols) put_tile_maxima(a, sc[1]);
+      if (p.dh.q) cast_tile_rows<GFMT>(d, p.dh.q, p.dh.s, p.dh.ldq, row0, col0, p.rows, p.cols, gmax, p.margin);
+      if (dcols || acols) {
+        __syncthreads();
+        bool bad = false;
+        const int c = threadIdx.x & (kTile - 1);
+        if (dcols && threadIdx.x < kTile) bad = finish_column(sc[0], c, p.dh.st, row0, col0, p.rows, gmax, p.margin);
+        if (acols && threadIdx.x / kTile == 1)
+          bad = finish_column(sc[1], c, p.ast, row0, col0, p.rows, kMaxE4M3, p.margin);
+        bad = __syncthreads_or(bad);
+        if (dcols) store_tile_cols<GFMT>(d, sc[0], bad, p.dh.qt, p.dh.ldqt, row0, col0, p.rows, p.cols);
+        if (acols) store_tile_cols<FP8_E4M3>(a, sc[1], bad, p.aqt, p.ldaqt, row0, col0, p.rows, p.cols);
+      }
+    }
   }
 }
 

@@ -318,25 +318,37 @@ struct ColScratch {
 };
 
 // From the warps' maxima (binary32 bit patterns in sc.part) to the tile's 128
-// column scales: written to st, and the thread's eight to s.  Returns whether
-// some amax is not finite.  Called by all threads.
+// column scales: written to st, and to sc.scale.  Called by 128 threads, c the
+// column of each; returns whether its amax is not finite.
+template <int RP>
+__device__ __forceinline__ bool finish_column(ColScratch<RP> &sc, int c, uint8_t *st, int row0, int col0, int rows,
+                                              float fmax, int margin) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int w = 0; w < Geo<RP>::kWarps; w++) a = max(a, sc.part[w][c]);
+  const int k = block_exponent(a, fmax, margin);
+  sc.scale[c] = pow2f(k);
+  put_scale(st, col0 + c, row0 / kTile, (rows + kTile - 1) / kTile, k);
+  return a >= 0x7f800000u;
+}
+
+// The thread's eight column scales.
+template <int RP>
+__device__ __forceinline__ void get_column_scales(const ColScratch<RP> &sc, float2 (&s)[4]) {
+  const int c8 = threadIdx.x & 15;
+  *reinterpret_cast<float4 *>(&s[0]) = *reinterpret_cast<const float4 *>(&sc.scale[c8 * 8]);
+  *reinterpret_cast<float4 *>(&s[2]) = *reinterpret_cast<const float4 *>(&sc.scale[c8 * 8 + 4]);
+}
+
+// The same for one tile, by all threads: the thread's scales to s.
 template <int RP>
 __device__ __forceinline__ bool column_scales(ColScratch<RP> &sc, uint8_t *st, int row0, int col0, int rows, float fmax,
                                               int margin, float2 (&s)[4]) {
-  const int c8 = threadIdx.x & 15;
-  uint32_t a = 0;
   __syncthreads();
-  if (threadIdx.x < kTile) {
-#pragma unroll
-    for (int w = 0; w < Geo<RP>::kWarps; w++) a = max(a, sc.part[w][threadIdx.x]);
-    const int k = block_exponent(a, fmax, margin);
-    sc.scale[threadIdx.x] = pow2f(k);
-    put_scale(st, col0 + threadIdx.x, row0 / kTile, (rows + kTile - 1) / kTile, k);
-  }
-  const bool bad = __syncthreads_or(a >= 0x7f800000u);
-  *reinterpret_cast<float4 *>(&s[0]) = *reinterpret_cast<const float4 *>(&sc.scale[c8 * 8]);
-  *reinterpret_cast<float4 *>(&s[2]) = *reinterpret_cast<const float4 *>(&sc.scale[c8 * 8 + 4]);
-  return bad;
+  const bool bad = threadIdx.x < kTile && finish_column(sc, threadIdx.x, st, row0, col0, rows, fmax, margin);
+  const bool any = __syncthreads_or(bad);
+  get_column_scales(sc, s);
+  return any;
 }
 
 // A warp's eight column maxima per thread (lanes l and l + 16 hold the same columns) to sc.part.
@@ -351,12 +363,11 @@ __device__ __forceinline__ void put_column_maxima(ColScratch<RP> &sc, uint32_t (
   }
 }
 
-// The column side of a tile of floats held in registers: v[i] = row r0 + i *
-// Geo<RP>::kStep, columns c8*8 .. +7 of the tile at (row0, col0).
-template <int FMT, int RP>
-__device__ __forceinline__ void cast_tile_cols(const float (&v)[RP][8], ColScratch<RP> &sc, uint8_t *qt,
-                                               uint8_t *st, size_t ldq, int row0, int col0, int rows, int cols,
-                                               float fmax, int margin) {
+// The column side of a tile of floats held in registers (v[i] = row r0 + i *
+// Geo<RP>::kStep, columns c8*8 .. +7 of the tile at (row0, col0)): the maxima,
+// and, once the scales are there, the codes.
+template <int RP>
+__device__ __forceinline__ void put_tile_maxima(const float (&v)[RP][8], ColScratch<RP> &sc) {
   uint32_t m[8];
 #pragma unroll
   for (int j = 0; j < 8; j++) {
@@ -366,8 +377,12 @@ __device__ __forceinline__ void cast_tile_cols(const float (&v)[RP][8], ColScrat
     m[j] = __float_as_uint(a);
   }
   put_column_maxima(sc, m);
+}
+template <int FMT, int RP>
+__device__ __forceinline__ void store_tile_cols(const float (&v)[RP][8], const ColScratch<RP> &sc, bool bad,
+                                                uint8_t *qt, size_t ldq, int row0, int col0, int rows, int cols) {
   float2 s[4];
-  const bool bad = column_scales(sc, st, row0, col0, rows, fmax, margin, s);
+  get_column_scales(sc, s);
   uint2 o[RP];
 #pragma unroll
   for (int i = 0; i < RP; i++) o[i] = enc8<FMT>(v[i], s);

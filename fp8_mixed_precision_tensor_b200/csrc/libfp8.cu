@@ -1285,14 +1285,19 @@ int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_act(act, [&](auto f) {
-      with_fmt(fmt, [&](auto g) {
+      auto go = [&](auto out) {
         using K = decltype(dt);
-        const auto kernel = block::k_act_bwd<K::value, decltype(f)::value, decltype(g)::value>;
+        constexpr int kOut = decltype(out)::value;
+        const auto kernel = block::k_act_bwd<K::value, decltype(f)::value, kOut>;
         constexpr int smem = block::ActBwdSmem<K::value>::kBytes;
         if ((rc = set_smem(kernel, smem))) return;
+        // resident CTAs (the kernel's launch bounds)
+        const unsigned cap = (unsigned)d->sms * (kOut == block::kActPlain && K::value == FP8_DT_BF16 ? 2u : 1u);
         const unsigned tiles = tile_grid(rows, cols);
-        rc = launch_pdl(kernel, tiles < (unsigned)d->sms ? tiles : (unsigned)d->sms, block::kActThreads, smem, s, 1, p);
-      });
+        rc = launch_pdl(kernel, tiles < cap ? tiles : cap, block::kActThreads, smem, s, 1, p);
+      };
+      if (dh_row || dh_col || a_col) with_fmt(fmt, go);
+      else go(std::integral_constant<int, block::kActPlain>());
     });
   });
   return rc;
