@@ -29,18 +29,17 @@ struct BArgs {
   int rows, cols;              // output extent along A's and B's outer indices
   int num_m_blocks, num_n_blocks, num_tiles, num_k_blocks, group_m;
   int whole;                   // pair kernel: tiles from this one on are worked as two halves of 128 columns
-  int bn;                      // output columns per tile (a multiple of 32, at most 256)
-  int stages, sf_atoms_b;      // ring depth; 512-byte scale groups loaded per tile for B
+  int bn;                      // token kernels: tokens of the tile (a multiple of 16)
+  int stages;                  // token kernels: ring depth
   uint32_t stage_bytes, tmem_cols;
   uint32_t idesc, desc_hi;
   const void *bias;            // per output feature, or null
   int bias_dtype;
-  void *out;
+  void *out;                   // pair kernel: [rows, cols]; token kernels: [cols, rows] (A holds the features)
   int out_dtype;
   size_t ld_out;               // elements
-  int swap;                    // 0: out[r, c]; 1: out[c, r] (A holds the features, B the tokens)
   int vec_out;                 // rows of `out` start on 16-byte boundaries
-  // tokens form: B is cast from x [cols, x_cols] inside the kernel
+  // tokens cast in the kernel: x [cols, x_cols]
   const void *x;
   size_t ldx;
   int x_cols, x_vec, margin;
@@ -65,6 +64,20 @@ __device__ __forceinline__ void tc_mma_bs(uint32_t d, uint32_t ad, uint32_t bd, 
       "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %3, [%5], [%6], p;\n\t}" ::"r"(d),
       "r"(ad), "r"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(hi)
       : "memory");
+}
+
+// The MMA issuers' loops run in the whole warp with one elected lane issuing:
+// their many operands then stay in uniform registers, where the MMAs take them
+// from.  In a loop of one lane every operand is moved there for each MMA,
+// about 190 cycles a block-scaled MMA instead of its 128.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ bool warp_ready(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+         __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
 // 512 bytes of scales (32 rows x 16 bytes) to the four columns at `taddr` of
@@ -105,24 +118,290 @@ __device__ __forceinline__ uint32_t with_scale_ids(uint32_t idesc, int kb) {
   return idesc | (id << 4) | (id << 29);
 }
 
-constexpr int kSfSlot = 2048;   // per stage: A's 512 bytes, then up to 3 x 512 of B
-constexpr int kSfCols = 16;     // tensor-memory columns of one set of scales (4 + up to 12)
+__device__ __forceinline__ void store_one(const BArgs &a, size_t at, float y) {
+  if (a.out_dtype == FP8_DT_F32) reinterpret_cast<float *>(a.out)[at] = y;
+  else if (a.out_dtype == FP8_DT_BF16) reinterpret_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(y);
+  else if (a.out_dtype == FP8_DT_F16) reinterpret_cast<__half *>(a.out)[at] = __float2half_rn(y);
+  else reinterpret_cast<uint16_t *>(a.out)[at] = (uint16_t)(bf16x2_rto(y, y) & 0xffffu);
+}
+
+// ---------------------------------------------------------------------------
+// Kernels for few tokens (at most 128).  The weights are the MMA's 128-row
+// operand, the tokens its columns, so that a tile streams 128 rows of weights
+// and wastes no multiplication on absent tokens.  A cluster of S CTAs takes a
+// tile, each its share of the k-blocks (S = 1: no cluster).  The CTAs then
+// exchange their partial tiles through distributed shared memory (posted
+// stores; reading the others' parts instead cost 12 us at 128 columns), and
+// each adds the S parts of its own tokens in rank order and stores them: no
+// workspace, no atomics, the same bits each time.
+//   warp 0 TMA producer, warp 1 TMEM allocation and MMA issue, warps 2-5 epilogue.
+constexpr int kSfCols = 8;      // tensor-memory columns of one set of scales: 4 of A, 4 of B
 constexpr int kSfSets = 3;
-// Sets of scale columns: a group of four blocks writes its set once and the
-// next three groups write others.  A set is rewritten at the earliest nine
-// blocks after its last block was multiplied; a ring of at most nine stages
-// has by then seen those MMAs complete (its slot was refilled), so the copy
-// cannot overtake a reader.
+// A group of four blocks writes a set of A's scales once and the next two
+// groups write others.  A set is rewritten at the earliest nine blocks after
+// its last block was multiplied; a ring of at most nine stages has by then
+// seen those MMAs complete (its slot was refilled), so the copy cannot
+// overtake a reader.
 constexpr int kMaxStages = 9;
-constexpr int kNoCast = -1;     // B comes as codes; otherwise the element type of x
-constexpr int kTokens = 32;     // tokens form: columns of its tile
 
-constexpr int kTokenBatch = 8;  // tokens that one warp casts at a time
-constexpr int kTokenThreads = 64 + 8 * 32;
-constexpr int kTokenPrefetch = 16;  // weight blocks (16 KB each) brought into L2 ahead
-constexpr int kTokenStages = 5;  // the least ring depth of the tokens form (see its casting warps)
+// This lane's feature: the tile's accumulator to out[token, feature];
+// neighbouring lanes write neighbouring features.
+__device__ __forceinline__ void store_tokens(const BArgs &a, int row, uint32_t tmem) {
+  const float bias = a.bias && row < a.rows ? load_bias(a.bias, a.bias_dtype, row) : 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < a.cols; c += 32) {
+    uint32_t r[32];
+    tmem_ld32(tmem + c, r);
+    if (row < a.rows) {
+#pragma unroll
+      for (int j = 0; j < 32; j++) {
+        const float v = __uint_as_float(r[j]);
+        if (c + j < a.cols) store_one(a, (size_t)(c + j) * a.ld_out + row, a.bias ? __fadd_rn(v, bias) : v);
+      }
+    }
+  }
+}
 
-// Eight tokens' parts of one stage: x[t0 .. t0+7, k0 .. k0+127], 16 lanes per
+// The exchange: tokens in units of four, unit u finished by CTA u % S as its
+// unit u / S.  The part of CTA s arrives in the owner's ring (free by then),
+// slot s, per unit 128 rows x 16 bytes.  All threads of the CTA call it.
+__device__ __forceinline__ void exchange_tokens(const BArgs &a, int splits, int rank, int row0, uint32_t base,
+                                                uint32_t tmem_base) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, row = row0 + q * 32 + lane;
+  const int units = (a.cols + 3) / 4, per = (units + splits - 1) / splits;
+  const bool mine = warp >= 2 && warp < 6;
+  const float bias = mine && a.bias && row < a.rows ? load_bias(a.bias, a.bias_dtype, row) : 0.0f;
+  cluster_sync();  // every CTA's MMAs have read their ring
+  if (mine) {
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < a.cols; c += 32) {
+      uint32_t r[32];
+      tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
+#pragma unroll
+      for (int g = 0; g < 8; g++) {
+        const int u = c / 4 + g;
+        if (u >= units) break;
+        const uint32_t dst = map_to_rank(base, (uint32_t)(u % splits)) +
+                             ((rank * per + u / splits) * BM + q * 32 + lane) * 16;
+        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(r[4 * g]), "r"(r[4 * g + 1]),
+                     "r"(r[4 * g + 2]), "r"(r[4 * g + 3])
+                     : "memory");
+      }
+    }
+    tc_fence_before();
+  }
+  cluster_sync();  // all parts have arrived
+  if (mine) {
+#pragma unroll 1
+    for (int i = 0, u = rank; u < units; i++, u += splits) {
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+      for (int s = 0; s < splits; s++) {
+        float x[4];
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                     : "r"(base + ((s * per + i) * BM + q * 32 + lane) * 16)
+                     : "memory");
+#pragma unroll
+        for (int j = 0; j < 4; j++) v[j] = __fadd_rn(v[j], x[j]);
+      }
+      if (row < a.rows) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          if (u * 4 + j < a.cols)
+            store_one(a, (size_t)(u * 4 + j) * a.ld_out + row, a.bias ? __fadd_rn(v[j], bias) : v[j]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+
+// Tokens that come as codes (forward and dgrad; in dgrad the weights are read
+// along their rows: A_MN).  Ring stage: A 16 KB, B bn x 128 B; scales of both
+// (1 KB) with every fourth block.
+constexpr int kSfSlot = 1024;
+
+template <bool A_MN>
+__global__ void __launch_bounds__(kThreads)
+    k_bgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+            const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+            const __grid_constant__ BArgs args, const int splits) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *base_ptr = smem_raw + (base - raw);
+  const int S = args.stages;
+  const uint32_t sf0 = base + S * args.stage_bytes;
+  const uint32_t bar0 = sf0 + S * kSfSlot;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * kMaxStages);
+  const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 1);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (bar0 - base) + 8 * (2 * kMaxStages + 2));
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = splits > 1 ? (int)cluster_rank() : 0;
+  const int row0 = (int)(blockIdx.x / splits) * BM;
+  // this CTA's k-blocks
+  const int kb0 = (int)((long long)args.num_k_blocks * rank / splits);
+  const int kb1 = (int)((long long)args.num_k_blocks * (rank + 1) / splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; s++) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(tfull_bar, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), args.tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  // Not before the allocation: a dependent CTA that took tensor memory first
+  // and then waited for this kernel would wait for good.
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; kb++) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
+        const uint32_t sa = base + stage * args.stage_bytes, ss = sf0 + stage * kSfSlot;
+        const bool scales = kb == kb0 || (kb & 3) == 0;
+        mbar_arrive_expect_tx(full_bar(stage), args.stage_bytes + (scales ? kSfSlot : 0));
+        if (scales) {
+          tma_load_3d(ss, &tmSA, 0, kb >> 2, row0 >> 7, full_bar(stage));
+          tma_load_3d(ss + 512, &tmSB, 0, kb >> 2, 0, full_bar(stage));
+        }
+        if (A_MN) tma_load_2d(sa, &tmA, row0, kb * BK, full_bar(stage));
+        else      tma_load_2d(sa, &tmA, kb * BK, row0, full_bar(stage));
+        tma_load_2d(sa + BM * BK, &tmB, kb * BK, 0, full_bar(stage));
+        issued_mask |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) {
+        for (int s = 0; s < S; s++)
+          if (issued_mask & (1u << s)) mbar_wait_drain(full_bar(s), (issued_par >> s) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    {
+      const bool elected = elect_one();
+      const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0), b_d0 = (uint32_t)operand_desc<false>(base + BM * BK, 0);
+      constexpr uint32_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4, b_ks = UMMA_K >> 4;
+      const uint32_t st_d = args.stage_bytes >> 4, sf_tmem = tmem_base + args.bn;
+      int stage = 0, set = kSfSets - 1;
+      uint32_t phase = 0;
+      bool ok = true, issued_any = false;
+      for (int kb = kb0; kb < kb1; kb++) {
+        if (!warp_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+        if (kb == kb0 || (kb & 3) == 0) {
+          set = set == kSfSets - 1 ? 0 : set + 1;
+          if (elected) {
+            tc_cp_scales(sf_tmem + set * kSfCols, scale_desc(sf0 + stage * kSfSlot));
+            tc_cp_scales(sf_tmem + set * kSfCols + 4, scale_desc(sf0 + stage * kSfSlot + 512));
+          }
+        }
+        const uint32_t sfa = sf_tmem + set * kSfCols, so = (uint32_t)stage * st_d;
+        const uint32_t idesc = with_scale_ids(args.idesc, kb);
+        if (elected) {
+#pragma unroll
+          for (int ks = 0; ks < BK / UMMA_K; ks++)
+            tc_mma_bs(tmem_base, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfa + 4,
+                      (kb != kb0 || ks != 0) ? 1u : 0u);
+          tc_commit(empty_bar(stage));
+        }
+        issued_any = true;
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+      }
+      if (ok) {
+        if (elected) tc_commit(tfull_bar);
+      } else if (issued_any) {
+        if (elected) tc_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0);
+      }
+    }
+    __syncwarp();
+  } else {
+    const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
+    tc_fence_after();
+    if (got && splits == 1)
+      store_tokens(args, row0 + (warp & 3) * 32 + lane, tmem_base + ((uint32_t)((warp & 3) * 32) << 16));
+    tc_fence_before();
+    __syncwarp();
+  }
+  if (splits > 1) exchange_tokens(args, splits, rank, row0, base, tmem_base);
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free(tmem_base, args.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tokens that come as x itself (at most 32): the cast and the product in one
+// launch.  Here the tokens are the MMA's rows and 256 weight rows its columns:
+// an MMA takes some 128 cycles whether it has 16 columns or 256, so with the
+// weights as rows a CTA could not multiply more than 32 bytes of them a cycle
+// (12288 x 4096 at one token: 18 us).  The rows of absent tokens need not exist:
+// the A descriptor's 16 KB window runs over whatever lies behind the tokens'
+// codes in shared memory, and what it makes of that lands in accumulator rows
+// that nothing reads.
+//   warp 0 TMA producer: 256 x 128-byte tiles of the weights, a ring of 5
+//   warp 1 TMEM allocation and MMA issue
+//   warps 2-17 cast x, a block of eight tokens at a time: a chain of some 1300
+//   cycles behind a round trip to L2, so it takes many warps to keep ahead.
+//   The codes live in a second ring, four blocks (a group of scale bytes) a
+//   slot.  (Casting into the weights' own ring held a CTA to 45 GB/s.)
+//   warps 4, 8, 12, 16 (accumulator rows 0..31) then finish, 64 columns each:
+//   a cluster of S CTAs shares a tile's reduction and exchanges its parts as
+//   above, in units of eight features.
+// Bound by the weights' HBM traffic, and below about 30 MB by the latencies of
+// start, cast and exchange.
+constexpr int kTokStages = 5;
+constexpr int kTokBN = 256;    // weight rows per tile
+constexpr int kTokBatch = 8;   // tokens that one cast takes
+constexpr int kTokWarps = 16;
+constexpr int kTokThreads = 64 + 32 * kTokWarps;
+constexpr int kTokPrefetch = 8;  // weight blocks (32 KB) brought into L2 ahead of the dependency wait
+constexpr int kTokCodes = 48 * 1024;
+// Slots of the code ring.  A parity wait tells only one phase of a slot from
+// the next, so a casting warp must not be able to skip a whole turn of the
+// ring: its next unit is kTokWarps units on, 4 / batches groups.
+__host__ __device__ constexpr int tok_groups(int batches) { return 12 / batches; }
+constexpr int kTokMaxGroups = 12;
+constexpr int kTokStageBytes = kTokBN * BK;
+constexpr int kTokSmem =
+    kTokCodes + kTokStages * (kTokStageBytes + 1024) + kTokMaxGroups * 512 + 512 + 1024;
+constexpr int kTokSfA = kTokBN;              // tensor-memory columns: 12 x 4 of the tokens' scales,
+constexpr int kTokSfB = kTokBN + 48;         // 3 x 8 of the weights'
+constexpr uint32_t kTokTmem = 512;
+
+// Eight tokens' parts of one block: x[t0 .. t0+7, k0 .. k0+127], 16 lanes per
 // token, 8 elements each, four pairs of tokens.
 template <int DT>
 __device__ __forceinline__ void load_tokens(const BArgs &a, int t0, int k0, int lane, block::Raw8<DT> (&raw)[4]) {
@@ -175,149 +454,84 @@ __device__ __forceinline__ void cast_tokens(const BArgs &a, int t0, int kb, uint
   }
 }
 
-__device__ __forceinline__ void store_one(const BArgs &a, size_t at, float y) {
-  if (a.out_dtype == FP8_DT_F32) reinterpret_cast<float *>(a.out)[at] = y;
-  else if (a.out_dtype == FP8_DT_BF16) reinterpret_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(y);
-  else if (a.out_dtype == FP8_DT_F16) reinterpret_cast<__half *>(a.out)[at] = __float2half_rn(y);
-  else reinterpret_cast<uint16_t *>(a.out)[at] = (uint16_t)(bf16x2_rto(y, y) & 0xffffu);
+// Eight features of this lane's token (and, with n < 8, fewer) to out.
+__device__ __forceinline__ void store_features(const BArgs &a, int token, int col, const float (&v)[8]) {
+  if (a.out_dtype == FP8_DT_F32) block::store8<FP8_DT_F32>(a.vec_out, a.out, a.ld_out, token, col, a.cols, a.rows, v);
+  else if (a.out_dtype == FP8_DT_BF16) block::store8<FP8_DT_BF16>(a.vec_out, a.out, a.ld_out, token, col, a.cols, a.rows, v);
+  else if (a.out_dtype == FP8_DT_F16) block::store8<FP8_DT_F16>(a.vec_out, a.out, a.ld_out, token, col, a.cols, a.rows, v);
+  else block::store8<FP8_DT_BF16_RTO>(a.vec_out, a.out, a.ld_out, token, col, a.cols, a.rows, v);
 }
 
-// Output chunk of 32 accumulator columns of one lane.  Not swapped: out[row,
-// col0...]; swapped: out[col0 + j, row], so that the lanes of a warp write
-// neighbouring features of a token.
-// bias: of feature col0 + lane (not swapped) or of this row's feature (swapped), loaded by the caller.
-__device__ __forceinline__ void store_out(const BArgs &a, float (&v)[32], int n, int row, int col0, float bias) {
-  if (a.swap) {
-    if (row >= a.rows) return;
-#pragma unroll
-    for (int j = 0; j < 32; j++)
-      if (j < n && col0 + j < a.cols)
-        store_one(a, (size_t)(col0 + j) * a.ld_out + row, a.bias ? __fadd_rn(v[j], bias) : v[j]);
-    return;
-  }
-  if (a.bias) {
-#pragma unroll
-    for (int j = 0; j < 32; j++) v[j] = __fadd_rn(v[j], __shfl_sync(0xffffffffu, bias, j));
-  }
-  if (row >= a.rows) return;
-#pragma unroll
-  for (int c = 0; c < 32; c += 8) {
-    if (c >= n || col0 + c >= a.cols) break;
-    float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) f[j] = v[c + j];
-    const int cols = min(a.cols, col0 + n);
-#define FP8_STORE(DT) block::store8<DT>(a.vec_out, a.out, a.ld_out, row, col0 + c, a.rows, cols, f)
-    if (a.out_dtype == FP8_DT_F32) FP8_STORE(FP8_DT_F32);
-    else if (a.out_dtype == FP8_DT_BF16) FP8_STORE(FP8_DT_BF16);
-    else if (a.out_dtype == FP8_DT_F16) FP8_STORE(FP8_DT_F16);
-    else FP8_STORE(FP8_DT_BF16_RTO);
-#undef FP8_STORE
-  }
-}
-
-__device__ __forceinline__ float chunk_bias(const BArgs &a, int row, int col0) {
-  const int i = a.swap ? row : col0 + (int)(threadIdx.x & 31);
-  return a.bias && i < (a.swap ? a.rows : a.cols) ? load_bias(a.bias, a.bias_dtype, i) : 0.0f;
-}
-
-// ---------------------------------------------------------------------------
-// One-CTA kernel: a tile of 128 x bn outputs per cluster of S CTAs, each of
-// which reduces its share of the k-blocks (S = 1: no cluster).  Each CTA then
-// sends every other its part of the partial tile through distributed shared
-// memory (posted stores; reading the others' parts instead cost 12 us at 128
-// columns), adds the S partial sums of its own bn / S columns in rank order
-// and stores them: no workspace, no atomics, the same bits each time.
-//   warp 0 TMA producer, warp 1 TMEM allocation and MMA issue, warps 2-5 epilogue.
-// XDT != kNoCast is the form for few tokens: A holds the weights, and eight
-// warps (four of them the epilogue's, idle until the accumulator is complete)
-// cast the tokens' activations into the ring, eight tokens of one stage at a
-// time, the next ones' loads in flight meanwhile, so that one launch does what
-// the cast and the product do.  Bound by the weights' HBM traffic.
-template <bool A_MN, bool B_MN, int XDT>
-__global__ void __launch_bounds__(XDT == kNoCast ? kThreads : kTokenThreads)
-    k_bgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-            const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-            const __grid_constant__ BArgs args, const int splits) {
+template <int DT>
+__global__ void __launch_bounds__(kTokThreads, 1)
+    k_btokens(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSW,
+              const __grid_constant__ BArgs args, const int splits) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *base_ptr = smem_raw + (base - raw);
-  const int S = args.stages;
-  const uint32_t sf0 = base + S * args.stage_bytes;
-  const uint32_t bar0 = sf0 + S * kSfSlot;
+  const int batches = (args.cols + kTokBatch - 1) / kTokBatch, G = tok_groups(batches);
+  const uint32_t tile_bytes = (uint32_t)batches * 1024, group_bytes = 4 * tile_bytes;  // codes of a block, of a group
+  const uint32_t ring0 = base + kTokCodes;
+  const uint32_t sfw0 = ring0 + kTokStages * kTokStageBytes;  // weights' scales, per stage
+  const uint32_t sfx0 = sfw0 + kTokStages * 1024;             // tokens' scales, per slot
+  const uint32_t bar0 = sfx0 + kTokMaxGroups * 512;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
-  const uint32_t tfull_bar = bar0 + 8u * (2 * kMaxStages);
-  const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 1);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (bar0 - base) + 8 * (2 * kMaxStages + 2));
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kTokStages + s); };
+  auto cfull_bar = [&](int g) { return bar0 + 8u * (2 * kTokStages + g); };
+  auto cempty_bar = [&](int g) { return bar0 + 8u * (2 * kTokStages + kTokMaxGroups + g); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * kTokStages + 2 * kTokMaxGroups);
+  const uint32_t drain_bar = tfull_bar + 8u;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (drain_bar + 8u - base));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = splits > 1 ? (int)cluster_rank() : 0;
-  const int tile = blockIdx.x / splits;
-  // this CTA's k-blocks
+  const int row0 = (int)(blockIdx.x / splits) * kTokBN;  // first weight row
   const int kb0 = (int)((long long)args.num_k_blocks * rank / splits);
   const int kb1 = (int)((long long)args.num_k_blocks * (rank + 1) / splits);
-  int mb, nb;
-  {
-    const int per_band = args.group_m * args.num_n_blocks;
-    const int band = tile / per_band, first = band * args.group_m;
-    const int rows_in_band = min(args.num_m_blocks - first, args.group_m);
-    const int r = tile - band * per_band;
-    mb = first + r % rows_in_band;
-    nb = r / rows_in_band;
-  }
-  const int row0 = mb * BM, col0 = nb * args.bn;
+  const int g0 = kb0 >> 2, groups = ((kb1 + 3) >> 2) - g0;  // groups of four blocks, by their scale bytes
 
-  constexpr bool CAST = XDT != kNoCast;
-  constexpr int kNumThreads = CAST ? kTokenThreads : kThreads;
-  const int batches = (args.cols + kTokenBatch - 1) / kTokenBatch;  // tokens form: casts per stage
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; s++) {
-      mbar_init(full_bar(s), CAST ? 1 + batches : 1);  // the producer's arrive, and the casting warps'
+    for (int s = 0; s < kTokStages; s++) {
+      mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
+    }
+    for (int g = 0; g < G; g++) {
+      mbar_init(cfull_bar(g), 4 * batches);
+      mbar_init(cempty_bar(g), 1);
     }
     mbar_init(tfull_bar, 1);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmSA);
-    if (!CAST) {
-      tma_prefetch_desc(&tmB);
-      tma_prefetch_desc(&tmSB);
-    }
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmSW);
   }
-  if constexpr (CAST) {  // token rows the cast never writes are zero
-    for (int i = threadIdx.x; i < S * (kTokens * BK + 512) / 16; i += kNumThreads) {
-      const int s = i / ((kTokens * BK + 512) / 16), o = (i % ((kTokens * BK + 512) / 16)) * 16;
-      const uint32_t at = o < kTokens * BK ? base + s * args.stage_bytes + BM * BK + o
-                                           : sf0 + s * kSfSlot + 512 + (o - kTokens * BK);
-      st_shared_v4(at, 0u, 0u, 0u, 0u);
-    }
-    fence_async_shared();
-  }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(args.tmem_cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kTokTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  // Not before the allocation: a dependent CTA that took tensor memory first
-  // and then waited for this kernel would wait for good.
-  pdl_launch_dependents();
-  // Tokens form: the first weights come into L2 while the stream's previous
-  // kernel ends.  (L2 is where its writes go too, so a weight that it still
-  // writes is read as written by the loads after the wait.)
-  if (CAST && threadIdx.x == 0)
-    for (int kb = kb0; kb < min(kb1, kb0 + kTokenPrefetch); kb++) tma_prefetch_2d(&tmA, kb * BK, row0);
+  pdl_launch_dependents();  // (not before the allocation: see k_bgemm)
+  // x and the first weights come into L2 while the stream's previous kernel
+  // ends.  (L2 is where its writes go too, so what it still writes is read as
+  // written by the loads after the wait.)  x first: behind 25 MB of weights
+  // its loads took 2.5 us.
+  {
+    const int esz = DT == FP8_DT_F32 ? 4 : 2;
+    const int c0 = g0 * 512, c1 = min((g0 + groups) * 512, args.x_cols), lines = ((c1 - c0) * esz + 127) / 128;
+    for (int i = threadIdx.x; i < lines * args.cols; i += kTokThreads) {
+      const int r = i / lines, c = c0 + (i - r * lines) * (128 / esz);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t *>(args.x) +
+                                                   ((size_t)r * args.ldx + c) * esz)
+                   : "memory");
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int kb = kb0; kb < min(kb1, kb0 + kTokPrefetch); kb++) tma_prefetch_2d(&tmW, kb * BK, row0);
   pdl_wait();
-  const uint32_t sf_bytes = 512u + 512u * args.sf_atoms_b;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -326,192 +540,172 @@ __global__ void __launch_bounds__(XDT == kNoCast ? kThreads : kTokenThreads)
       bool ok = true;
       for (int kb = kb0; kb < kb1; kb++) {
         if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
-        const uint32_t sa = base + stage * args.stage_bytes, sb = sa + BM * BK, ss = sf0 + stage * kSfSlot;
         const bool scales = kb == kb0 || (kb & 3) == 0;
-        mbar_arrive_expect_tx(full_bar(stage), (CAST ? (uint32_t)(BM * BK) : args.stage_bytes) +
-                                                   (scales ? (CAST ? 512u : sf_bytes) : 0u));
-        if (scales) {
-          tma_load_3d(ss, &tmSA, 0, kb >> 2, row0 >> 7, full_bar(stage));
-          if (!CAST) tma_load_3d(ss + 512, &tmSB, 0, kb >> 2, col0 >> 7, full_bar(stage));
-        }
-        if (A_MN) tma_load_2d(sa, &tmA, row0, kb * BK, full_bar(stage));
-        else      tma_load_2d(sa, &tmA, kb * BK, row0, full_bar(stage));
-        if (CAST) {
-        } else if (B_MN) {
-          for (int c = 0; c < args.bn; c += 128)
-            tma_load_2d(sb + c * BK, &tmB, col0 + c, kb * BK, full_bar(stage));
-        } else {
-          tma_load_2d(sb, &tmB, kb * BK, col0, full_bar(stage));
-        }
+        mbar_arrive_expect_tx(full_bar(stage), kTokStageBytes + (scales ? 1024 : 0));
+        if (scales) tma_load_3d(sfw0 + stage * 1024, &tmSW, 0, kb >> 2, row0 >> 7, full_bar(stage));
+        tma_load_2d(ring0 + stage * kTokStageBytes, &tmW, kb * BK, row0, full_bar(stage));
         issued_mask |= 1u << stage;
         issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-        if (++stage == S) { stage = 0; phase ^= 1u; }
+        if (++stage == kTokStages) { stage = 0; phase ^= 1u; }
       }
       if (!ok) {
-        for (int s = 0; s < S; s++)
+        for (int s = 0; s < kTokStages; s++)
           if (issued_mask & (1u << s)) mbar_wait_drain(full_bar(s), (issued_par >> s) & 1u);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0), b_d0 = (uint32_t)operand_desc<B_MN>(base + BM * BK, 0);
-      constexpr uint32_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
-      constexpr uint32_t b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
-      const uint32_t st_d = args.stage_bytes >> 4;
-      // the scales of a tile that starts inside a 128-row group: skip whole 32-row columns
-      const uint32_t sfb_skip = (uint32_t)(col0 & 127) >> 5;
-      const uint32_t sf_tmem = tmem_base + args.bn;
-      int stage = 0, set = kSfSets - 1;
-      uint32_t phase = 0;
-      bool ok = true, issued_any = false;
-      for (int kb = kb0; kb < kb1; kb++) {
-        if (!stage_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
-        if (kb == kb0 || (kb & 3) == 0) {
-          set = set == kSfSets - 1 ? 0 : set + 1;
-          const uint32_t t = sf_tmem + set * kSfCols, ss = sf0 + stage * kSfSlot;
-          tc_cp_scales(t, scale_desc(ss));
-          if (!CAST)
-            for (int i = 0; i < args.sf_atoms_b; i++) tc_cp_scales(t + 4 + 4 * i, scale_desc(ss + 512 + 512 * i));
+    const bool elected = elect_one();
+    const uint32_t a_d0 = (uint32_t)operand_desc<false>(base, 0), b_d0 = (uint32_t)operand_desc<false>(ring0, 0);
+    constexpr uint32_t ks_d = UMMA_K >> 4, st_d = kTokStageBytes >> 4;
+    const uint32_t grp_d = group_bytes >> 4, tile_d = tile_bytes >> 4;
+    int stage = 0, set = kSfSets - 1, slot = 0;
+    uint32_t phase = 0, cphase = 0;
+    bool ok = true, issued_any = false;
+    for (int kb = kb0; kb < kb1; kb++) {
+      const uint32_t sfa = tmem_base + kTokSfA + slot * 4;
+      if (!warp_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+      if (kb == kb0 || (kb & 3) == 0) {
+        if (!warp_ready(cfull_bar(slot), cphase, abort_flag)) { ok = false; break; }
+        set = set == kSfSets - 1 ? 0 : set + 1;
+        if (elected) {
+          tc_cp_scales(sfa, scale_desc(sfx0 + slot * 512));
+          tc_cp_scales(tmem_base + kTokSfB + set * 8, scale_desc(sfw0 + stage * 1024));
+          tc_cp_scales(tmem_base + kTokSfB + set * 8 + 4, scale_desc(sfw0 + stage * 1024 + 512));
         }
-        const uint32_t sfa = sf_tmem + set * kSfCols;
-        uint32_t sfb = sfa + 4 + sfb_skip;
-        if (CAST) {  // every stage brings its own token scales; their columns belong to the ring slot
-          sfb = sf_tmem + kSfSets * kSfCols + 4 * stage;
-          tc_cp_scales(sfb, scale_desc(sf0 + stage * kSfSlot + 512));
-        }
-        const uint32_t so = (uint32_t)stage * st_d;
-        const uint32_t idesc = with_scale_ids(args.idesc, kb);
+      }
+      const uint32_t sfb = tmem_base + kTokSfB + set * 8;
+      const uint32_t idesc = with_scale_ids(args.idesc, kb);
+      const uint32_t ad = a_d0 + slot * grp_d + (kb & 3) * tile_d, bd = b_d0 + stage * st_d;
+      if (elected) {
 #pragma unroll
         for (int ks = 0; ks < BK / UMMA_K; ks++)
-          tc_mma_bs(tmem_base, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfb,
+          tc_mma_bs(tmem_base, ad + ks * ks_d, bd + ks * ks_d, args.desc_hi, idesc, sfa, sfb,
                     (kb != kb0 || ks != 0) ? 1u : 0u);
         tc_commit(empty_bar(stage));
-        issued_any = true;
-        if (++stage == S) { stage = 0; phase ^= 1u; }
+        if ((kb & 3) == 3) tc_commit(cempty_bar(slot));
       }
-      if (ok) {
-        tc_commit(tfull_bar);
-      } else if (issued_any) {
-        tc_commit(drain_bar);
-        mbar_wait_drain(drain_bar, 0);
+      if ((kb & 3) == 3 && ++slot == G) {
+        slot = 0;
+        cphase ^= 1u;
       }
+      issued_any = true;
+      if (++stage == kTokStages) { stage = 0; phase ^= 1u; }
+    }
+    if (ok) {
+      if (elected) tc_commit(tfull_bar);
+    } else if (issued_any) {
+      if (elected) tc_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0);
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;
-    const int row = row0 + q * 32 + lane;
-    if constexpr (CAST) {
-      // Unit u: batch u % batches of block kb0 + u / batches; the casting warps
-      // take them in turn.  At most 4 * batches warps do, so that a warp's next
-      // unit is at most four blocks on: a parity wait tells only one phase of a
-      // ring slot from the next, and a warp that skipped a whole turn of the
-      // ring (five stages at the least) could take an older phase for its own.
-      const int units = (kb1 - kb0) * batches, step = min(8, 4 * batches);
-      block::Raw8<XDT> raw[4];
-      int u = warp - 2 < step ? warp - 2 : units;
-      if (u < units) load_tokens<XDT>(args, u % batches * kTokenBatch, (kb0 + u / batches) * BK, lane, raw);
-      for (; u < units; u += step) {
-        const int i = u / batches, stage = i % S, t0 = u % batches * kTokenBatch;
-        block::Raw8<XDT> next[4];
-        const int un = min(u + step, units - 1);
-        load_tokens<XDT>(args, un % batches * kTokenBatch, (kb0 + un / batches) * BK, lane, next);
-        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), ((uint32_t)(i / S) & 1u) ^ 1u, abort_flag))) break;
-        cast_tokens<XDT>(args, t0, kb0 + i, base + stage * args.stage_bytes + BM * BK, sf0 + stage * kSfSlot + 512,
-                         lane, raw);
-        fence_async_shared();  // the MMAs and the scale copy read through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full_bar(stage));
-#pragma unroll
-        for (int j = 0; j < 4; j++) raw[j] = next[j];
-      }
+    // Unit u: tokens of batch u % batches, block u / batches (counted from the
+    // first group's first block; blocks of a group that another CTA multiplies
+    // are cast too, so that every group has the same number of units).
+    const int units = groups * 4 * batches;
+    block::Raw8<DT> x[4];
+    int u = warp - 2;
+    if (u < units) load_tokens<DT>(args, u % batches * kTokBatch, (g0 * 4 + u / batches) * BK, lane, x);
+    for (; u < units; u += kTokWarps) {
+      const int i = u / batches, t0 = (u - i * batches) * kTokBatch, g = i >> 2, slot = g % G;
+      block::Raw8<DT> next[4];
+      const int un = min(u + kTokWarps, units - 1);
+      load_tokens<DT>(args, un % batches * kTokBatch, (g0 * 4 + un / batches) * BK, lane, next);
+      if (!__all_sync(0xffffffffu, mbar_wait(cempty_bar(slot), ((uint32_t)(g / G) & 1u) ^ 1u, abort_flag))) break;
+      cast_tokens<DT>(args, t0, i & 3, base + slot * group_bytes + (i & 3) * tile_bytes, sfx0 + slot * 512, lane, x);
+      fence_async_shared();  // the MMAs and the scale copy read through the async proxy
       __syncwarp();
-    }
-    if (warp < 6) {
-      float bias = args.swap && splits == 1 ? chunk_bias(args, row, 0) : 0.0f;
-      const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
-      tc_fence_after();
-      if (got && splits == 1) {
-#pragma unroll 1
-        for (int c = 0; c < args.bn && col0 + c < args.cols; c += 32) {
-          if (!args.swap) bias = chunk_bias(args, row, col0 + c);
-          uint32_t r[32];
-          tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
-          float v[32];
+      if (lane == 0) mbar_arrive(cfull_bar(slot));
 #pragma unroll
-          for (int j = 0; j < 32; j++) v[j] = __uint_as_float(r[j]);
-          store_out(args, v, 32, row, col0 + c, bias);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
+      for (int j = 0; j < 4; j++) x[j] = next[j];
     }
+    __syncwarp();
   }
 
-  if (splits > 1) {
-    // Columns in units of 8 (a vector store), or 4 where the columns are
-    // tokens; unit u is finished by CTA u % S, as its unit u / S.  The partial
-    // of CTA s arrives at slot s of the owner's ring: per unit, groups of 4
-    // columns x 128 rows x 16 bytes.
-    const int unit = args.swap ? 4 : 8, groups = unit / 4;
-    const int cols = min(args.bn, args.cols - col0), units = (cols + unit - 1) / unit;
-    const int per = (units + splits - 1) / splits;
-    cluster_sync();  // every CTA's MMAs have read their ring
-    const int q = warp & 3, row = row0 + q * 32 + lane;
-    float bias = 0.0f;
-    if (warp >= 2 && warp < 6) {
-      if (args.swap) bias = chunk_bias(args, row, 0);
-      tc_fence_after();
+  // ------------------------------------------------------------ finish
+  const bool mine = warp >= 4 && (warp & 3) == 0;  // accumulator rows 0..31
+  const int c0 = ((warp >> 2) - 1) * 64;           // of these 64 columns
+  bool got = false;
+  if (mine) {
+    got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
+    tc_fence_after();
+  }
+  const int units = (min(kTokBN, args.rows - row0) + 7) / 8, per = (units + splits - 1) / splits;
+  if (splits > 1) cluster_sync();  // every CTA's MMAs have read their rings
+  if (mine && got) {
 #pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
+    for (int c = c0; c < c0 + 64 && c / 8 < units; c += 32) {
+      const int bcol = row0 + c + lane;
+      const float bias = splits == 1 && args.bias && bcol < args.rows ? load_bias(args.bias, args.bias_dtype, bcol) : 0.0f;
+      uint32_t r[32];
+      tmem_ld32(tmem_base + c, r);
 #pragma unroll
-        for (int g = 0; g < 8; g++) {
-          const int u = (c + 4 * g) / unit;
-          if (c + 4 * g >= cols) break;
-          const uint32_t dst = map_to_rank(base, (uint32_t)(u % splits)) +
-                               (((rank * per + u / splits) * groups + (g & (groups - 1))) * BM + q * 32 + lane) * 16;
-          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(r[4 * g]),
-                       "r"(r[4 * g + 1]), "r"(r[4 * g + 2]), "r"(r[4 * g + 3])
-                       : "memory");
+      for (int g = 0; g < 4; g++) {
+        const int u = c / 8 + g;
+        if (splits == 1) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            v[j] = __uint_as_float(r[8 * g + j]);
+            if (args.bias) v[j] = __fadd_rn(v[j], __shfl_sync(0xffffffffu, bias, 8 * g + j));
+          }
+          store_features(args, lane, row0 + u * 8, v);
+        } else if (u < units && lane < args.cols) {  // to slot `rank` of the owner, 32 lanes x 16 bytes per half
+          const uint32_t dst = map_to_rank(base, (uint32_t)(u % splits)) + (((rank * per + u / splits) * 2) * 32 + lane) * 16;
+#pragma unroll
+          for (int h = 0; h < 2; h++)
+            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + h * 512), "r"(r[8 * g + 4 * h]),
+                         "r"(r[8 * g + 4 * h + 1]), "r"(r[8 * g + 4 * h + 2]), "r"(r[8 * g + 4 * h + 3])
+                         : "memory");
         }
       }
-      tc_fence_before();
     }
+  }
+  tc_fence_before();
+  if (splits > 1) {
     cluster_sync();  // all parts have arrived
-    if (warp >= 2 && warp < 6) {
-#pragma unroll 1
-      for (int i = 0, u = rank; u < units; i++, u += splits) {
-        if (!args.swap) bias = chunk_bias(args, row, col0 + u * unit);
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; j++) v[j] = 0.0f;
-#pragma unroll 2
+    if (warp >= 2) {
+      for (int i = warp - 2; i * splits + rank < units; i += kTokWarps) {
+        const int col = row0 + (i * splits + rank) * 8;
+        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         for (int s = 0; s < splits; s++) {
 #pragma unroll
           for (int h = 0; h < 2; h++) {
-            if (h >= groups) break;
-            float x[4];
+            float p[4];
             asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
-                         : "r"(base + (((s * per + i) * groups + h) * BM + q * 32 + lane) * 16)
+                         : "=f"(p[0]), "=f"(p[1]), "=f"(p[2]), "=f"(p[3])
+                         : "r"(base + (((s * per + i) * 2 + h) * 32 + lane) * 16)
                          : "memory");
 #pragma unroll
-            for (int j = 0; j < 4; j++) v[4 * h + j] = __fadd_rn(v[4 * h + j], x[j]);
+            for (int j = 0; j < 4; j++) v[4 * h + j] = __fadd_rn(v[4 * h + j], p[j]);
           }
         }
-        store_out(args, v, unit, row, col0 + u * unit, bias);
+        if (args.bias) {
+#pragma unroll
+          for (int j = 0; j < 8; j++)
+            if (col + j < args.rows) v[j] = __fadd_rn(v[j], load_bias(args.bias, args.bias_dtype, col + j));
+        }
+        store_features(args, lane, col, v);
       }
     }
   }
 
-  tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(args.tmem_cols)
-                 : "memory");
+    tmem_free(tmem_base, kTokTmem);
+  }
+}
+
+// out[r, c] = bias[c] or 0: a product with an empty reduction.
+__global__ void k_bgemm_empty(const BArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const size_t n = (size_t)a.rows * a.cols, stride = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
+    const int r = (int)(i / a.cols), c = (int)(i % a.cols);
+    store_one(a, (size_t)r * a.ld_out + c, a.bias ? load_bias(a.bias, a.bias_dtype, c) : 0.0f);
   }
 }
 
@@ -605,6 +799,12 @@ __device__ __forceinline__ void store_box_elements(const BArgs &a, uint32_t stg,
     }
   }
   __syncwarp();
+}
+
+// The bias of feature col0 + lane, handed out by shuffles.
+__device__ __forceinline__ float chunk_bias(const BArgs &a, int col0) {
+  const int i = col0 + (int)(threadIdx.x & 31);
+  return a.bias && i < a.cols ? load_bias(a.bias, a.bias_dtype, i) : 0.0f;
 }
 
 template <bool A_MN, bool B_MN, int OUT>
@@ -716,8 +916,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (leader, one thread)
-    if (leader && lane == 0) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (leader) {
+      const bool elected = elect_one();
       const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0);
       const uint32_t b_d0 = (uint32_t)operand_desc<B_MN>(base + kPairHalf * BK, 0);
       constexpr uint32_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
@@ -727,43 +928,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, group = 0;
       bool ok = true, issued_any = false;
       for (int tile = pair; tile < num_items && ok; tile += num_pairs, n++) {
-        if (n > 0 && !mbar_wait(tempty_bar, (uint32_t)(n - 1) & 1u, abort_flag)) { ok = false; break; }
+        if (n > 0 && !warp_ready(tempty_bar, (uint32_t)(n - 1) & 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (n & 1) * kP2Acc1;
         const bool split = tile >= args.whole;
         const uint32_t shape = split ? args.idesc ^ ((256u >> 3) << 17) ^ ((128u >> 3) << 17) : args.idesc;
         const uint32_t sfb_off = split && ((tile - args.whole) & 1) ? 8u : 4u;
         for (int kb = 0; kb < args.num_k_blocks; kb++) {
-          if (!stage_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+          if (!warp_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
           if ((kb & 3) == 0) {  // the set's last readers, two groups ago, have completed
             const uint32_t set = group & 1u;
-            if (group >= 2 && !stage_ready(sffree_bar(set), ((group >> 1) - 1) & 1u, abort_flag)) {
+            if (group >= 2 && !warp_ready(sffree_bar(set), ((group >> 1) - 1) & 1u, abort_flag)) {
               ok = false;
               break;
             }
             const uint32_t sf = tmem_base + kP2Sf + set * 16, ss = sf0 + stage * kP2SfSlot;
-            tc_cp_scales_pair(sf, scale_desc(ss));
-            tc_cp_scales_pair(sf + 4, scale_desc(ss + 512));
-            tc_cp_scales_pair(sf + 8, scale_desc(ss + 1024));
+            if (elected) {
+              tc_cp_scales_pair(sf, scale_desc(ss));
+              tc_cp_scales_pair(sf + 4, scale_desc(ss + 512));
+              tc_cp_scales_pair(sf + 8, scale_desc(ss + 1024));
+            }
             group++;
           }
           const uint32_t sfa = tmem_base + kP2Sf + ((group - 1) & 1u) * 16;
           const uint32_t so = (uint32_t)stage * st_d;
           const uint32_t idesc = with_scale_ids(shape, kb);
+          if (elected) {
 #pragma unroll
-          for (int ks = 0; ks < BK / UMMA_K; ks++)
-            tc_mma_bs_pair(d_tmem, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfa + sfb_off,
-                           (kb | ks) != 0 ? 1u : 0u);
-          tc_commit_pair(empty_bar(stage));
-          if ((kb & 3) == 3 || kb == args.num_k_blocks - 1) tc_commit_leader(sffree_bar((group - 1) & 1u));
+            for (int ks = 0; ks < BK / UMMA_K; ks++)
+              tc_mma_bs_pair(d_tmem, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfa + sfb_off,
+                             (kb | ks) != 0 ? 1u : 0u);
+            tc_commit_pair(empty_bar(stage));
+            if ((kb & 3) == 3 || kb == args.num_k_blocks - 1) tc_commit_leader(sffree_bar((group - 1) & 1u));
+          }
           issued_any = true;
           if (++stage == kP2Stages) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        tc_commit_pair(tfull_bar(n & 1));
+        if (elected) tc_commit_pair(tfull_bar(n & 1));
       }
       if (!ok && issued_any) {
-        tc_commit_leader(drain_bar);
+        if (elected) tc_commit_leader(drain_bar);
         mbar_wait_drain(drain_bar, 0);
       }
     }
@@ -791,8 +996,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = ((n & 1) || half >= 0 ? i : (i + kNum - 1) % kNum) * kBox;
         const int col0 = nb * 256 + max(half, 0) * 128 + c;
         uint32_t w[32];
-        const float bias0 = chunk_bias(args, 0, col0);
-        const float bias1 = OUT == FP8_DT_F32 ? 0.0f : chunk_bias(args, 0, col0 + 32);
+        const float bias0 = chunk_bias(args, col0);
+        const float bias1 = OUT == FP8_DT_F32 ? 0.0f : chunk_bias(args, col0 + 32);
         uint32_t r[32];
         tmem_ld32(acc + c, r);
         if (args.bias) {
@@ -855,17 +1060,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
-  }
-}
-
-// out[r, c] = bias[c] or 0: a product with an empty reduction.
-__global__ void k_bgemm_empty(const BArgs a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const size_t n = (size_t)a.rows * a.cols, stride = (size_t)gridDim.x * blockDim.x;
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
-    const int r = (int)(i / a.cols), c = (int)(i % a.cols);
-    store_one(a, (size_t)r * a.ld_out + c, a.bias ? load_bias(a.bias, a.bias_dtype, c) : 0.0f);
   }
 }
 

@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kCastThreads, DT == FP8_DT_F32 ? 2 : 3)
 // for each of its rows (out.s) and each of its columns (out.st), so that the
 // codes serve products that reduce along either axis.
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kCastThreads, DT == FP8_DT_F32 ? 2 : 3)
+__global__ void __launch_bounds__(kCastThreads)
     k_block_cast_square(const void *__restrict__ x, int rows, int cols, size_t ldx, int vec, int margin,
                         const CastOut out) {
   pdl_launch_dependents();

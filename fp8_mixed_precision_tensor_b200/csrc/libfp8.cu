@@ -869,7 +869,8 @@ block::CastOut cast_out(const fp8_blocks *row, const fp8_blocks *col) {
 
 struct BlockInfo {
   bool ready = false;
-  int pair_clusters = 0;  // co-resident clusters of the pair kernel
+  int pair_clusters = 0;         // co-resident clusters of the pair kernel
+  int token_clusters[9] = {0};   // co-resident clusters of 2..8 CTAs of the tokens kernel
 };
 std::mutex g_block_mu;
 BlockInfo g_block[kMaxDevices];
@@ -898,11 +899,9 @@ int block_info(DeviceInfo **d, BlockInfo **out) {
   BlockInfo &b = g_block[dev];
   *out = &b;
   if (b.ready) return FP8_OK;
-  using bgemm::k_bgemm;
-  constexpr int no = bgemm::kNoCast;
-  int rc = set_max_smem(k_bgemm<false, false, no>) | set_max_smem(k_bgemm<true, false, no>) |
-           set_max_smem(k_bgemm<false, false, FP8_DT_F32>) | set_max_smem(k_bgemm<false, false, FP8_DT_BF16>) |
-           set_max_smem(k_bgemm<false, false, FP8_DT_F16>);
+  using namespace bgemm;
+  int rc = set_max_smem(k_bgemm<false>) | set_max_smem(k_bgemm<true>) | set_max_smem(k_btokens<FP8_DT_F32>) |
+           set_max_smem(k_btokens<FP8_DT_BF16>) | set_max_smem(k_btokens<FP8_DT_F16>);
   rc |= set_pair_smem<false, false>() | set_pair_smem<false, true>() | set_pair_smem<true, true>();
   if (rc) return FP8_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -920,6 +919,14 @@ int block_info(DeviceInfo **d, BlockInfo **out) {
           cudaSuccess ||
       b.pair_clusters < 1)
     return FP8_ERR_CUDA;
+  cfg.blockDim = dim3(kTokThreads);
+  cfg.dynamicSmemBytes = kTokSmem;
+  for (int s = 2; s <= 8; s++) {
+    attr.val.clusterDim.x = s;
+    cfg.gridDim = dim3(s * ((*d)->sms / s));
+    if (cudaOccupancyMaxActiveClusters(&b.token_clusters[s], k_btokens<FP8_DT_BF16>, &cfg) != cudaSuccess)
+      return FP8_ERR_CUDA;
+  }
   b.ready = true;
   return FP8_OK;
 }
@@ -970,53 +977,64 @@ struct BOperand {
   int fmt;
 };
 
-// C[rows, cols] (or, swapped, C[cols, rows]) on the one-CTA kernel.  XDT: the
-// tokens form, B cast from a.x in the kernel (B.b unused).
-template <bool A_MN, bool B_MN, int XDT = bgemm::kNoCast>
-int launch_bgemm(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, int bn, int splits,
-                 cudaStream_t stream) {
+// Instruction descriptor: operand formats, majorness, 8-bit exponent scales, N and M.
+uint32_t block_idesc(int fmt_a, int fmt_b, bool a_mn, bool b_mn, int n, int m) {
+  return ((uint32_t)fmt_a << 7) | ((uint32_t)fmt_b << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27);
+}
+
+// Reduction splits for `tiles` tiles of kblocks blocks on `slots` resident
+// CTAs: as many as stay resident, each with two blocks at the least.
+int pick_splits(long long tiles, int kblocks, int slots) {
+  int s = 1;
+  while (s < 8 && tiles * (s + 1) <= slots && kblocks >= 2 * (s + 1)) s++;
+  return s;
+}
+
+// Out[tokens, features] for at most 128 tokens as codes (B [tokens, K]); A
+// holds the features, A_MN: read along its rows.
+template <bool A_MN>
+int launch_bgemm(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, int sms, cudaStream_t stream) {
   using namespace bgemm;
-  const int rows = a.rows, cols = a.cols;
-  a.bn = bn;
-  a.num_m_blocks = (rows + gemm::BM - 1) / gemm::BM;
-  a.num_n_blocks = (cols + bn - 1) / bn;
-  a.num_tiles = a.num_m_blocks * a.num_n_blocks;
+  a.bn = (a.cols + 31) / 32 * 32;
   a.num_k_blocks = (K + gemm::BK - 1) / gemm::BK;
-  a.group_m = 16;
-  a.sf_atoms_b = bn % 128 == 0 ? bn / 128 : (bn < 128 && 128 % bn == 0) ? 1 : (96 + bn + 127) / 128;
-  const int b_rows = B_MN ? (bn + 127) / 128 * 128 : bn;
-  a.stage_bytes = (uint32_t)(gemm::BM + b_rows) * gemm::BK;
-  uint32_t tmem = 32;
-  while (tmem < (uint32_t)(bn + kSfSets * kSfCols + (XDT == kNoCast ? 0 : 4 * kMaxStages))) tmem *= 2;
-  a.tmem_cols = tmem;
-  // two CTAs per SM where the accumulators and a ring of at least three stages of both fit
-  const uint32_t room = (tmem <= 256 ? 114688u : 230400u) - 1024u - 256u;
-  int stages = (int)(room / (a.stage_bytes + kSfSlot));
-  if (stages > kMaxStages) stages = kMaxStages;
-  if (XDT != kNoCast && stages < kTokenStages) return FP8_ERR_UNSUPPORTED;  // (never: a stage is 22 KB)
-  a.stages = stages;
+  a.stage_bytes = (uint32_t)(gemm::BM + a.bn) * gemm::BK;
+  a.tmem_cols = a.bn + kSfSets * kSfCols <= 64 ? 64 : a.bn + kSfSets * kSfCols <= 128 ? 128 : 256;
+  // two CTAs per SM
+  const int fit = (int)((114688u - 1024u - 256u) / (a.stage_bytes + kSfSlot));
+  a.stages = fit < kMaxStages ? fit : kMaxStages;
   a.desc_hi = kDescHi;
-  a.idesc = ((uint32_t)A.fmt << 7) | ((uint32_t)B.fmt << 10) | ((uint32_t)(A_MN ? 1 : 0) << 15) |
-            ((uint32_t)(B_MN ? 1 : 0) << 16) | ((uint32_t)(bn >> 3) << 17) | (1u << 23)  // scales: 8-bit exponents
-            | ((uint32_t)(gemm::BM >> 7) << 27);
+  a.idesc = block_idesc(A.fmt, B.fmt, A_MN, false, a.bn, gemm::BM);
   CUtensorMap ma, mb, msa, msb;
-  int rc = A_MN ? make_code_map(&ma, A.b->q, rows, K, A.b->ld, gemm::BK)
-                : make_code_map(&ma, A.b->q, K, rows, A.b->ld, gemm::BM);
-  if (rc) return rc;
-  if ((rc = make_scale_map(&msa, A.b->s, rows, K, 1))) return rc;
-  if constexpr (XDT == kNoCast) {
-    rc = B_MN ? make_code_map(&mb, B.b->q, cols, K, B.b->ld, gemm::BK)
-              : make_code_map(&mb, B.b->q, K, cols, B.b->ld, (uint32_t)bn);
-    if (rc) return rc;
-    if ((rc = make_scale_map(&msb, B.b->s, cols, K, (uint32_t)a.sf_atoms_b))) return rc;
-  } else {
-    mb = ma;
-    msb = msa;
-  }
-  const size_t smem = (size_t)stages * (a.stage_bytes + kSfSlot) + 256 + 1024;
-  constexpr int threads = XDT == kNoCast ? gemm::kThreads : kTokenThreads;
-  return launch_pdl(k_bgemm<A_MN, B_MN, XDT>, (unsigned)a.num_tiles * splits, threads, smem, stream, splits, ma, mb,
-                    msa, msb, a, splits);
+  int rc = A_MN ? make_code_map(&ma, A.b->q, a.rows, K, A.b->ld, gemm::BK)
+                : make_code_map(&ma, A.b->q, K, a.rows, A.b->ld, gemm::BM);
+  if (rc || (rc = make_code_map(&mb, B.b->q, K, a.cols, B.b->ld, (uint32_t)a.bn)) ||
+      (rc = make_scale_map(&msa, A.b->s, a.rows, K, 1)) || (rc = make_scale_map(&msb, B.b->s, a.cols, K, 1)))
+    return rc;
+  const long long tiles = ((long long)a.rows + gemm::BM - 1) / gemm::BM;
+  const int splits = pick_splits(tiles, a.num_k_blocks, 2 * sms);
+  const size_t smem = (size_t)a.stages * (a.stage_bytes + kSfSlot) + 256 + 1024;
+  return launch_pdl(k_bgemm<A_MN>, (unsigned)(tiles * splits), gemm::kThreads, smem, stream, splits, ma, mb, msa, msb,
+                    a, splits);
+}
+
+// The same from x (a.x) for at most 32 tokens, in splits that keep every
+// cluster resident.
+template <int DT>
+int launch_btokens(const BOperand &W, bgemm::BArgs a, int K, const BlockInfo &bi, cudaStream_t stream) {
+  using namespace bgemm;
+  a.num_k_blocks = (K + gemm::BK - 1) / gemm::BK;
+  a.desc_hi = kDescHi;
+  a.idesc = block_idesc(FP8_E4M3, W.fmt, false, false, kTokBN, gemm::BM);
+  CUtensorMap mw, msw;
+  int rc = make_code_map(&mw, W.b->q, K, a.rows, W.b->ld, kTokBN);
+  if (rc || (rc = make_scale_map(&msw, W.b->s, a.rows, K, kTokBN / 128))) return rc;
+  const long long tiles = ((long long)a.rows + kTokBN - 1) / kTokBN;
+  int splits = 1;
+  for (int s = 2; s <= 8; s++)
+    if (tiles <= bi.token_clusters[s] && a.num_k_blocks >= 2 * s) splits = s;
+  return launch_pdl(k_btokens<DT>, (unsigned)(tiles * splits), kTokThreads, (size_t)kTokSmem, stream, splits, mw, msw, a,
+                    splits);
 }
 
 // C[rows, cols] on the pair kernel.
@@ -1030,8 +1048,7 @@ int launch_bgemm2(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, i
   a.num_k_blocks = (K + gemm::BK - 1) / gemm::BK;
   a.group_m = 8;
   a.desc_hi = kDescHi;
-  a.idesc = ((uint32_t)A.fmt << 7) | ((uint32_t)B.fmt << 10) | ((uint32_t)(A_MN ? 1 : 0) << 15) |
-            ((uint32_t)(B_MN ? 1 : 0) << 16) | ((uint32_t)(256 >> 3) << 17) | (1u << 23) | ((uint32_t)(256 >> 7) << 27);
+  a.idesc = block_idesc(A.fmt, B.fmt, A_MN, B_MN, 256, 256);
   CUtensorMap ma, mb, msa, msb, mo;
   int rc = A_MN ? make_code_map(&ma, A.b->q, rows, K, A.b->ld, gemm::BK)
                 : make_code_map(&ma, A.b->q, K, rows, A.b->ld, 128);
@@ -1057,14 +1074,6 @@ int launch_bgemm2(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, i
     case FP8_DT_F16: return go(k_bgemm2<A_MN, B_MN, FP8_DT_F16>);
     default: return go(k_bgemm2<A_MN, B_MN, FP8_DT_BF16_RTO>);
   }
-}
-
-// Reduction splits for `tiles` tiles of kblocks blocks on `slots` resident
-// CTAs: doubled while every CTA stays resident and keeps two blocks.
-int pick_splits(long long tiles, int kblocks, int slots) {
-  int s = 1;
-  while (s < 8 && tiles * s * 2 <= slots && kblocks >= 4 * s) s *= 2;
-  return s;
 }
 
 // Out[R, C] = sum over `red` of A(r, .) B(c, .) (+ bias[c]).  A_MN / B_MN: the
@@ -1096,15 +1105,11 @@ int run_bgemm(const BOperand &A, const BOperand &B, const void *bias, int bias_d
   if ((rc = check_blocks(B.b, B_MN ? C : red))) return rc;
   BlockInfo *bi;
   if ((rc = block_info(&d, &bi))) return rc;
-  const int kblocks = (red + 127) / 128;
   if constexpr (!A_MN) {
-    if (R <= 128) {  // few tokens: their rows become the tile's columns, the weights its 128 lanes
-      const int bn = (R + 31) / 32 * 32;
-      a.swap = 1;
+    if (R <= 128) {  // few tokens: the weights become the row operand
       a.rows = C;
       a.cols = R;
-      return launch_bgemm<B_MN, A_MN>(B, A, a, red, bn, pick_splits((C + 127) / 128, kblocks, 2 * d->sms),
-                                      stream);
+      return launch_bgemm<B_MN>(B, A, a, red, d->sms, stream);
     }
   }
   return launch_bgemm2<A_MN, B_MN>(A, B, a, red, bi->pair_clusters, stream);
@@ -1208,16 +1213,13 @@ int fp8_block_linear_tokens(const void *x, int x_dtype, size_t ldx, int margin, 
   a.out = y;
   a.out_dtype = y_dtype;
   a.ld_out = ldy;
-  a.swap = 1;
+  a.vec_out = wide_rows(y, y_dtype, ldy);
   a.x = x;
   a.ldx = ldx;
   a.x_cols = K;
   a.x_vec = wide_rows(x, x_dtype, ldx);
   a.margin = margin;
-  const int splits = pick_splits((N + 127) / 128, (K + 127) / 128, 2 * d->sms);
-  with_dtype(x_dtype, [&](auto dt) {
-    rc = launch_bgemm<false, false, decltype(dt)::value>({w, 0}, {nullptr, 0}, a, K, bgemm::kTokens, splits, s);
-  });
+  with_dtype(x_dtype, [&](auto dt) { rc = launch_btokens<decltype(dt)::value>({w, 0}, a, K, *bi, s); });
   return rc;
 }
 

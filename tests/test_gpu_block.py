@@ -345,7 +345,7 @@ def test_tokens_form_against_binary64(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("M", [1, 8, 9, 17, 32])
-@pytest.mark.parametrize("N,K", [(19000, 3000), (12288, 4096), (300, 33000)])
+@pytest.mark.parametrize("N,K", [(19000, 3000), (12288, 4096), (300, 33000), (128, 70000)])
 def test_tokens_form_runs_its_ring_many_times(M, N, K):
     """Reductions much longer than the kernel's ring of operand stages, on one CTA per tile and split."""
     L = Layer(M, N, K, key=("ring",))
