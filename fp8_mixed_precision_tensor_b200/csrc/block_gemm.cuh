@@ -371,34 +371,46 @@ __global__ void __launch_bounds__(kThreads)
 // the A descriptor's 16 KB window runs over whatever lies behind the tokens'
 // codes in shared memory, and what it makes of that lands in accumulator rows
 // that nothing reads.
-//   warp 0 TMA producer: 256 x 128-byte tiles of the weights, a ring of 5
+//   warp 0 TMA producer: 256 x 128-byte tiles of the weights, a ring of 4 to 6
 //   warp 1 TMEM allocation and MMA issue
 //   warps 2-17 cast x, a block of eight tokens at a time: a chain of some 1300
 //   cycles behind a round trip to L2, so it takes many warps to keep ahead.
 //   The codes live in a second ring, four blocks (a group of scale bytes) a
 //   slot.  (Casting into the weights' own ring held a CTA to 45 GB/s.)
-//   warps 4, 8, 12, 16 (accumulator rows 0..31) then finish, 64 columns each:
-//   a cluster of S CTAs shares a tile's reduction and exchanges its parts as
-//   above, in units of eight features.
+//   warps 4, 8, 12, 16 (accumulator rows 0..31) then finish, 64 columns each.
+// A cluster of S CTAs shares a tile's reduction: unit u of eight features is
+// finished by CTA u % S.  The parts go to the owner as asynchronous stores that
+// count their bytes on a barrier of the owner's, into memory kept for them, so
+// that the end of the reduction needs no cluster-wide barrier (two of them and
+// the exchange took 2.7 us).
 // Bound by the weights' HBM traffic, and below about 30 MB by the latencies of
 // start, cast and exchange.
-constexpr int kTokStages = 5;
+constexpr int kTokMaxStages = 6;
 constexpr int kTokBN = 256;    // weight rows per tile
 constexpr int kTokBatch = 8;   // tokens that one cast takes
 constexpr int kTokWarps = 16;
 constexpr int kTokThreads = 64 + 32 * kTokWarps;
 constexpr int kTokPrefetch = 8;  // weight blocks (32 KB) brought into L2 ahead of the dependency wait
-constexpr int kTokCodes = 48 * 1024;
-// Slots of the code ring.  A parity wait tells only one phase of a slot from
-// the next, so a casting warp must not be able to skip a whole turn of the
-// ring: its next unit is kTokWarps units on, 4 / batches groups.
-__host__ __device__ constexpr int tok_groups(int batches) { return 12 / batches; }
-constexpr int kTokMaxGroups = 12;
 constexpr int kTokStageBytes = kTokBN * BK;
-constexpr int kTokSmem =
-    kTokCodes + kTokStages * (kTokStageBytes + 1024) + kTokMaxGroups * 512 + 512 + 1024;
-constexpr int kTokSfA = kTokBN;              // tensor-memory columns: 12 x 4 of the tokens' scales,
-constexpr int kTokSfB = kTokBN + 48;         // 3 x 8 of the weights'
+// Slots of the code ring, by the number of batches of eight tokens.  A parity
+// wait tells only one phase of a slot from the next, so a casting warp must
+// not be able to skip a whole turn of the ring: its next unit is kTokWarps
+// units on, 4 / batches groups (4, 2, 2, 1).
+__host__ __device__ constexpr int tok_groups(int batches) { return batches == 1 ? 4 : 3; }
+constexpr int kTokMaxGroups = 4;
+// Parts of a CTA's units of eight features: S * ceil(32 / S) <= 36 of them, 32 bytes per token.
+__host__ __device__ constexpr int tok_parts(int batches) { return 36 * 32 * 8 * batches; }
+__host__ __device__ constexpr int tok_fixed(int batches) {
+  return tok_groups(batches) * (4096 * batches + 512) + tok_parts(batches) + 512 + 1024;
+}
+// What is left of the SM's shared memory holds weights in flight: it is their
+// latency that bounds a CTA (16 blocks of 32 KB: 11 us with four stages).
+__host__ __device__ constexpr int tok_stages(int batches) {
+  const int n = (232448 - tok_fixed(batches)) / (kTokStageBytes + 1024);
+  return n < kTokMaxStages ? n : kTokMaxStages;
+}
+constexpr int kTokSfA = kTokBN;       // tensor-memory columns: 4 x 4 of the tokens' scales,
+constexpr int kTokSfB = kTokBN + 16;  // 3 x 8 of the weights'
 constexpr uint32_t kTokTmem = 512;
 
 // Eight tokens' parts of one block: x[t0 .. t0+7, k0 .. k0+127], 16 lanes per
@@ -470,19 +482,21 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *base_ptr = smem_raw + (base - raw);
-  const int batches = (args.cols + kTokBatch - 1) / kTokBatch, G = tok_groups(batches);
+  const int batches = (args.cols + kTokBatch - 1) / kTokBatch, G = tok_groups(batches), S = tok_stages(batches);
   const uint32_t tile_bytes = (uint32_t)batches * 1024, group_bytes = 4 * tile_bytes;  // codes of a block, of a group
-  const uint32_t ring0 = base + kTokCodes;
-  const uint32_t sfw0 = ring0 + kTokStages * kTokStageBytes;  // weights' scales, per stage
-  const uint32_t sfx0 = sfw0 + kTokStages * 1024;             // tokens' scales, per slot
-  const uint32_t bar0 = sfx0 + kTokMaxGroups * 512;
+  const uint32_t ring0 = base + G * group_bytes;
+  const uint32_t sfw0 = ring0 + S * kTokStageBytes;  // weights' scales, per stage
+  const uint32_t sfx0 = sfw0 + S * 1024;             // tokens' scales, per slot
+  const uint32_t parts0 = sfx0 + G * 512;
+  const uint32_t bar0 = parts0 + tok_parts(batches);
+  const int lanes = kTokBatch * batches;             // lanes of a part
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (kTokStages + s); };
-  auto cfull_bar = [&](int g) { return bar0 + 8u * (2 * kTokStages + g); };
-  auto cempty_bar = [&](int g) { return bar0 + 8u * (2 * kTokStages + kTokMaxGroups + g); };
-  const uint32_t tfull_bar = bar0 + 8u * (2 * kTokStages + 2 * kTokMaxGroups);
-  const uint32_t drain_bar = tfull_bar + 8u;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (drain_bar + 8u - base));
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kTokMaxStages + s); };
+  auto cfull_bar = [&](int g) { return bar0 + 8u * (2 * kTokMaxStages + g); };
+  auto cempty_bar = [&](int g) { return bar0 + 8u * (2 * kTokMaxStages + kTokMaxGroups + g); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * kTokMaxStages + 2 * kTokMaxGroups);
+  const uint32_t drain_bar = tfull_bar + 8u, parts_bar = tfull_bar + 16u, loaded_bar = tfull_bar + 24u;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (loaded_bar + 8u - base));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -491,9 +505,12 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   const int kb0 = (int)((long long)args.num_k_blocks * rank / splits);
   const int kb1 = (int)((long long)args.num_k_blocks * (rank + 1) / splits);
   const int g0 = kb0 >> 2, groups = ((kb1 + 3) >> 2) - g0;  // groups of four blocks, by their scale bytes
+  const int units_x = groups * 4 * batches;                 // casts
+  const int units = (min(kTokBN, args.rows - row0) + 7) / 8, per = (units + splits - 1) / splits;
+  const int owned = (units - rank + splits - 1) / splits;   // of this CTA
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kTokStages; s++) {
+    for (int s = 0; s < S; s++) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
@@ -503,14 +520,18 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     }
     mbar_init(tfull_bar, 1);
     mbar_init(drain_bar, 1);
+    mbar_init(parts_bar, 1);
+    mbar_init(loaded_bar, min(kTokWarps, units_x));
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (splits > 1 && owned > 0) mbar_arrive_expect_tx(parts_bar, (uint32_t)(owned * splits * args.cols * 32));
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmSW);
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), kTokTmem);
   tc_fence_before();
-  __syncthreads();
+  if (splits > 1) cluster_sync();  // no CTA sends a part before its owner's barrier is set up
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_launch_dependents();  // (not before the allocation: see k_bgemm)
@@ -539,6 +560,9 @@ __global__ void __launch_bounds__(kTokThreads, 1)
       uint32_t phase = 0, issued_mask = 0, issued_par = 0;
       bool ok = true;
       for (int kb = kb0; kb < kb1; kb++) {
+        // the ring's first fill waits for x: its 128 KB in front of the first
+        // loads of x delayed them, and the casts behind them, by over 1 us
+        if (kb == kb0 + 1 && !mbar_wait(loaded_bar, 0, abort_flag)) { ok = false; break; }
         if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) { ok = false; break; }
         const bool scales = kb == kb0 || (kb & 3) == 0;
         mbar_arrive_expect_tx(full_bar(stage), kTokStageBytes + (scales ? 1024 : 0));
@@ -546,10 +570,10 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         tma_load_2d(ring0 + stage * kTokStageBytes, &tmW, kb * BK, row0, full_bar(stage));
         issued_mask |= 1u << stage;
         issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-        if (++stage == kTokStages) { stage = 0; phase ^= 1u; }
+        if (++stage == S) { stage = 0; phase ^= 1u; }
       }
       if (!ok) {
-        for (int s = 0; s < kTokStages; s++)
+        for (int s = 0; s < S; s++)
           if (issued_mask & (1u << s)) mbar_wait_drain(full_bar(s), (issued_par >> s) & 1u);
       }
     }
@@ -590,7 +614,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         cphase ^= 1u;
       }
       issued_any = true;
-      if (++stage == kTokStages) { stage = 0; phase ^= 1u; }
+      if (++stage == S) { stage = 0; phase ^= 1u; }
     }
     if (ok) {
       if (elected) tc_commit(tfull_bar);
@@ -603,14 +627,24 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     // Unit u: tokens of batch u % batches, block u / batches (counted from the
     // first group's first block; blocks of a group that another CTA multiplies
     // are cast too, so that every group has the same number of units).
-    const int units = groups * 4 * batches;
     block::Raw8<DT> x[4];
     int u = warp - 2;
-    if (u < units) load_tokens<DT>(args, u % batches * kTokBatch, (g0 * 4 + u / batches) * BK, lane, x);
-    for (; u < units; u += kTokWarps) {
+    if (u < units_x) load_tokens<DT>(args, u % batches * kTokBatch, (g0 * 4 + u / batches) * BK, lane, x);
+    if (u < units_x) {
+      uint32_t seen = 0;
+#pragma unroll
+      for (int j = 0; j < 4; j++) seen |= x[j].w[0];
+      uint32_t any;  // (0 or 1: makes the arrive wait for the loads)
+      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tvote.sync.any.pred p, p, 0xffffffff;\n\t"
+                   "selp.u32 %0, 1, 0, p;\n\t}"
+                   : "=r"(any)
+                   : "r"(seen));
+      if (lane == 0 && any <= 1u) mbar_arrive(loaded_bar);
+    }
+    for (; u < units_x; u += kTokWarps) {
       const int i = u / batches, t0 = (u - i * batches) * kTokBatch, g = i >> 2, slot = g % G;
       block::Raw8<DT> next[4];
-      const int un = min(u + kTokWarps, units - 1);
+      const int un = min(u + kTokWarps, units_x - 1);
       load_tokens<DT>(args, un % batches * kTokBatch, (g0 * 4 + un / batches) * BK, lane, next);
       if (!__all_sync(0xffffffffu, mbar_wait(cempty_bar(slot), ((uint32_t)(g / G) & 1u) ^ 1u, abort_flag))) break;
       cast_tokens<DT>(args, t0, i & 3, base + slot * group_bytes + (i & 3) * tile_bytes, sfx0 + slot * 512, lane, x);
@@ -624,16 +658,11 @@ __global__ void __launch_bounds__(kTokThreads, 1)
   }
 
   // ------------------------------------------------------------ finish
-  const bool mine = warp >= 4 && (warp & 3) == 0;  // accumulator rows 0..31
-  const int c0 = ((warp >> 2) - 1) * 64;           // of these 64 columns
-  bool got = false;
-  if (mine) {
-    got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
+  if (warp >= 4 && (warp & 3) == 0) {     // accumulator rows 0..31
+    const int c0 = ((warp >> 2) - 1) * 64;  // of these 64 columns
+    const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
     tc_fence_after();
-  }
-  const int units = (min(kTokBN, args.rows - row0) + 7) / 8, per = (units + splits - 1) / splits;
-  if (splits > 1) cluster_sync();  // every CTA's MMAs have read their rings
-  if (mine && got) {
+    // (after a timeout the parts are sent all the same: their owners count on them)
 #pragma unroll 1
     for (int c = c0; c < c0 + 64 && c / 8 < units; c += 32) {
       const int bcol = row0 + c + lane;
@@ -650,46 +679,54 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             v[j] = __uint_as_float(r[8 * g + j]);
             if (args.bias) v[j] = __fadd_rn(v[j], __shfl_sync(0xffffffffu, bias, 8 * g + j));
           }
-          store_features(args, lane, row0 + u * 8, v);
-        } else if (u < units && lane < args.cols) {  // to slot `rank` of the owner, 32 lanes x 16 bytes per half
-          const uint32_t dst = map_to_rank(base, (uint32_t)(u % splits)) + (((rank * per + u / splits) * 2) * 32 + lane) * 16;
+          if (got) store_features(args, lane, row0 + u * 8, v);
+        } else if (u < units && lane < args.cols) {  // to part `rank` of the owner's unit, `lanes` x 16 bytes per half
+          const uint32_t owner = (uint32_t)(u % splits), bar = map_to_rank(parts_bar, owner);
+          const uint32_t dst = map_to_rank(parts0, owner) + (((rank * per + u / splits) * 2) * lanes + lane) * 16;
 #pragma unroll
           for (int h = 0; h < 2; h++)
-            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + h * 512), "r"(r[8 * g + 4 * h]),
-                         "r"(r[8 * g + 4 * h + 1]), "r"(r[8 * g + 4 * h + 2]), "r"(r[8 * g + 4 * h + 3])
+            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                             dst + h * lanes * 16),
+                         "r"(r[8 * g + 4 * h]), "r"(r[8 * g + 4 * h + 1]), "r"(r[8 * g + 4 * h + 2]),
+                         "r"(r[8 * g + 4 * h + 3]), "r"(bar)
                          : "memory");
         }
       }
     }
+    tc_fence_before();
   }
-  tc_fence_before();
-  if (splits > 1) {
-    cluster_sync();  // all parts have arrived
-    if (warp >= 2) {
-      for (int i = warp - 2; i * splits + rank < units; i += kTokWarps) {
-        const int col = row0 + (i * splits + rank) * 8;
-        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < splits; s++) {
+  __syncwarp();
+  // No CTA leaves before every other has sent its parts (normally long since).
+  if (splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (splits > 1 && owned > 0 && warp >= 2) {
+    const bool got = __all_sync(0xffffffffu, mbar_wait(parts_bar, 0, abort_flag));
+    for (int i = warp - 2; got && i < owned; i += kTokWarps) {
+      const int col = row0 + (i * splits + rank) * 8;
+      float bias = 0.0f;
+      if (args.bias && lane < 8 && col + lane < args.rows) bias = load_bias(args.bias, args.bias_dtype, col + lane);
+      float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+      for (int s = 0; s < splits; s++) {
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            float p[4];
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(p[0]), "=f"(p[1]), "=f"(p[2]), "=f"(p[3])
-                         : "r"(base + (((s * per + i) * 2 + h) * 32 + lane) * 16)
-                         : "memory");
+        for (int h = 0; h < 2; h++) {
+          float p[4];
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(p[0]), "=f"(p[1]), "=f"(p[2]), "=f"(p[3])
+                       : "r"(parts0 + (((s * per + i) * 2 + h) * lanes + min(lane, lanes - 1)) * 16)
+                       : "memory");
 #pragma unroll
-            for (int j = 0; j < 4; j++) v[4 * h + j] = __fadd_rn(v[4 * h + j], p[j]);
-          }
+          for (int j = 0; j < 4; j++) v[4 * h + j] = __fadd_rn(v[4 * h + j], p[j]);
         }
-        if (args.bias) {
-#pragma unroll
-          for (int j = 0; j < 8; j++)
-            if (col + j < args.rows) v[j] = __fadd_rn(v[j], load_bias(args.bias, args.bias_dtype, col + j));
-        }
-        store_features(args, lane, col, v);
       }
+      if (args.bias) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = __fadd_rn(v[j], __shfl_sync(0xffffffffu, bias, j));
+      }
+      store_features(args, lane, col, v);
     }
+    __syncwarp();
   }
+  if (splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
   __syncthreads();
   if (warp == 1) {

@@ -920,7 +920,7 @@ int block_info(DeviceInfo **d, BlockInfo **out) {
       b.pair_clusters < 1)
     return FP8_ERR_CUDA;
   cfg.blockDim = dim3(kTokThreads);
-  cfg.dynamicSmemBytes = kTokSmem;
+  cfg.dynamicSmemBytes = 232448;
   for (int s = 2; s <= 8; s++) {
     attr.val.clusterDim.x = s;
     cfg.gridDim = dim3(s * ((*d)->sms / s));
@@ -1033,8 +1033,9 @@ int launch_btokens(const BOperand &W, bgemm::BArgs a, int K, const BlockInfo &bi
   int splits = 1;
   for (int s = 2; s <= 8; s++)
     if (tiles <= bi.token_clusters[s] && a.num_k_blocks >= 2 * s) splits = s;
-  return launch_pdl(k_btokens<DT>, (unsigned)(tiles * splits), kTokThreads, (size_t)kTokSmem, stream, splits, mw, msw, a,
-                    splits);
+  const int batches = (a.cols + kTokBatch - 1) / kTokBatch;
+  const size_t smem = (size_t)tok_fixed(batches) + tok_stages(batches) * (kTokStageBytes + 1024);
+  return launch_pdl(k_btokens<DT>, (unsigned)(tiles * splits), kTokThreads, smem, stream, splits, mw, msw, a, splits);
 }
 
 // C[rows, cols] on the pair kernel.
