@@ -80,6 +80,10 @@ class _HParams(ctypes.Structure):
 
 
 _lib = None
+# The C functions behind torch.cuda.current_device() and current_stream(), where this torch has them.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -137,7 +141,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 def _stream(stream) -> int:
     if stream is None:  # the current stream's handle, without making a Stream object for it (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -440,7 +444,8 @@ def block_scales(outer: int, red: int, device="cuda") -> torch.Tensor:
 
 
 # The argument checks below run on every call of a path whose kernels take a
-# few microseconds, so they read each tensor's properties once.
+# few microseconds: each reads a tensor's properties once and decides by one
+# expression; what was wrong is found out afterwards.
 _U8 = torch.uint8
 
 
@@ -449,7 +454,7 @@ def _device(t: torch.Tensor, what: str) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError("libfp8 takes device tensors")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{what} is on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
@@ -465,11 +470,12 @@ def _bad_matrix(t: torch.Tensor, what: str, rows: int, cols: int, dev: int) -> N
 
 def _matrix(t: torch.Tensor, what: str, rows: int, cols: int, dev: int) -> int:
     """Row stride in elements of a [rows, cols] matrix whose rows are contiguous."""
-    st = t.stride()
-    if (t.get_device() != dev or t.shape != (rows, cols) or (cols > 1 and st[1] != 1) or
-            (rows > 1 and st[0] < cols)):
+    if t.get_device() != dev or t.shape != (rows, cols):
         _bad_matrix(t, what, rows, cols, dev)
-    return st[0] if rows > 1 else cols
+    ld, inner = t.stride()
+    if (inner != 1 and cols > 1) or (ld < cols and rows > 1):
+        _bad_matrix(t, what, rows, cols, dev)
+    return ld if rows > 1 else cols
 
 
 def _hp(t: torch.Tensor, what: str) -> int:
@@ -482,26 +488,36 @@ def _hp(t: torch.Tensor, what: str) -> int:
 
 def _input(t: torch.Tensor, what: str):
     """(dtype code, rows, cols, row stride, device) of a call's high-precision input."""
-    dt, dev = _hp(t, what), _device(t, what)
-    if t.dim() != 2:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected a matrix")
-    rows, cols = t.shape
-    return dt, rows, cols, _matrix(t, what, rows, cols, dev), dev
+    dt, dev, shape = _hp(t, what), _device(t, what), t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: shape {tuple(shape)}, expected a matrix")
+    rows, cols = shape
+    ld, inner = t.stride()
+    if (inner != 1 and cols > 1) or (ld < cols and rows > 1):
+        _bad_matrix(t, what, rows, cols, dev)
+    return dt, rows, cols, ld if rows > 1 else cols, dev
+
+
+def _bad_blocks(q, s, what: str, rows: int, cols: int, need: int, dev: int) -> None:
+    """Names what _blocks found wrong."""
+    if q is None or s is None:
+        raise ValueError(f"{what}: codes and scales go together")
+    if q.dtype is not _U8 or s.dtype is not _U8:
+        raise TypeError(f"{what}: codes and scales are uint8")
+    _matrix(q, what, rows, cols, dev)
+    raise ValueError(f"{what}: scales are {need} contiguous bytes on cuda:{dev}, got {s.numel()} on {s.device}")
 
 
 def _blocks(q, s, what: str, rows: int, cols: int, outer: int, red: int, dev: int):
     """fp8_blocks of a [rows, cols] code matrix and its scale buffer."""
-    if q is None or s is None:
-        if q is s:
-            return None
-        raise ValueError(f"{what}: codes and scales go together")
-    if q.dtype is not _U8 or s.dtype is not _U8:
-        raise TypeError(f"{what}: codes and scales are uint8")
+    if q is None and s is None:
+        return None
+    need = (outer + 127) // 128 * ((red + 511) // 512) * 512  # fp8_block_scale_bytes
+    if (q is None or s is None or q.dtype is not _U8 or s.dtype is not _U8 or s.numel() < need or
+            s.get_device() != dev or not s.is_contiguous()):
+        _bad_blocks(q, s, what, rows, cols, need, dev)
     ld = _matrix(q, what, rows, cols, dev)
-    need = -(-outer // 128) * -(-red // 512) * 512  # fp8_block_scale_bytes
-    if s.numel() < need or not s.is_contiguous() or s.get_device() != dev:
-        raise ValueError(f"{what}: scales are {need} contiguous bytes on cuda:{dev}, got {s.numel()} on {s.device}")
-    return ctypes.byref(_Blocks(q.data_ptr(), s.data_ptr(), ld if rows > 1 else (ld + 15) // 16 * 16))
+    return _Blocks(q.data_ptr(), s.data_ptr(), ld if rows > 1 else (ld + 15) // 16 * 16)
 
 
 def _vector(t, what: str, n: int, dev: int):
@@ -515,10 +531,10 @@ def _vector(t, what: str, n: int, dev: int):
 
 def _codes_shape(q: torch.Tensor, what: str):
     """(rows, cols, device) of a call's leading code matrix."""
-    dev = _device(q, what)
-    if q.dim() != 2:
-        raise ValueError(f"{what}: shape {tuple(q.shape)}, expected a matrix")
-    rows, cols = q.shape
+    dev, shape = _device(q, what), q.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: shape {tuple(shape)}, expected a matrix")
+    rows, cols = shape
     return rows, cols, dev
 
 
