@@ -126,10 +126,12 @@ __device__ __forceinline__ void store_one(const BArgs &a, size_t at, float y) {
 }
 
 // ---------------------------------------------------------------------------
-// Kernels for few tokens (at most 128).  The weights are the MMA's 128-row
-// operand, the tokens its columns, so that a tile streams 128 rows of weights
-// and wastes no multiplication on absent tokens.  A cluster of S CTAs takes a
-// tile, each its share of the k-blocks (S = 1: no cluster).  The CTAs then
+// The kernel for few tiles: few tokens, or a long reduction behind a small
+// output.  The operand whose rows are neighbours in the output's memory (the
+// weights; in wgrad x) is the MMA's 128-row operand, the other (the tokens; in
+// wgrad dy) its columns, up to 128 of them, so that a batch below that wastes
+// no multiplication on absent tokens.  A cluster of S CTAs takes a tile, each
+// its share of the k-blocks (S = 1: no cluster).  The CTAs then
 // exchange their partial tiles through distributed shared memory (posted
 // stores; reading the others' parts instead cost 12 us at 128 columns), and
 // each adds the S parts of its own tokens in rank order and stores them: no
@@ -144,75 +146,124 @@ constexpr int kSfSets = 3;
 // overtake a reader.
 constexpr int kMaxStages = 9;
 
+// One value to an output element where `p`; OUT as out_dtype.  Predicated, not
+// branched around: with a branch per element 128 tokens took twice as long.
+template <int OUT>
+__device__ __forceinline__ void store_as(void *at, float y, bool p) {
+  if constexpr (OUT == FP8_DT_F32) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q st.global.f32 [%0], %1;\n\t}" ::"l"(at), "f"(y),
+                 "r"((int)p)
+                 : "memory");
+  } else {
+    const uint16_t h = (uint16_t)(OUT == FP8_DT_BF16_RTO ? bf16x2_rto(y, y)
+                                  : OUT == FP8_DT_F16    ? (uint32_t)__half_as_ushort(__float2half_rn(y))
+                                                         : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y)));
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q st.global.b16 [%0], %1;\n\t}" ::"l"(at), "h"(h),
+                 "r"((int)p)
+                 : "memory");
+  }
+}
+template <typename F>
+__device__ __forceinline__ void with_out(int dtype, F f) {
+  if (dtype == FP8_DT_BF16) f(std::integral_constant<int, FP8_DT_BF16>());
+  else if (dtype == FP8_DT_F16) f(std::integral_constant<int, FP8_DT_F16>());
+  else if (dtype == FP8_DT_F32) f(std::integral_constant<int, FP8_DT_F32>());
+  else f(std::integral_constant<int, FP8_DT_BF16_RTO>());
+}
+
+// 16 columns of this lane's accumulator row.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15},"
+      " [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // This lane's feature: the tile's accumulator to out[token, feature];
 // neighbouring lanes write neighbouring features.
-__device__ __forceinline__ void store_tokens(const BArgs &a, int row, uint32_t tmem) {
+__device__ __forceinline__ void store_tokens(const BArgs &a, int row, int col0, uint32_t tmem) {
   const float bias = a.bias && row < a.rows ? load_bias(a.bias, a.bias_dtype, row) : 0.0f;
+  const int cols = min(a.cols - col0, a.bn);
+  with_out(a.out_dtype, [&](auto out) {
+    constexpr int OUT = decltype(out)::value, esz = OUT == FP8_DT_F32 ? 4 : 2;
+    const size_t step = a.ld_out * esz;
+    char *at = static_cast<char *>(a.out) + col0 * step + (size_t)row * esz;
 #pragma unroll 1
-  for (int c = 0; c < a.cols; c += 32) {
-    uint32_t r[32];
-    tmem_ld32(tmem + c, r);
-    if (row < a.rows) {
+    for (int c = 0; c < cols; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(tmem + c, r);
 #pragma unroll
-      for (int j = 0; j < 32; j++) {
-        const float v = __uint_as_float(r[j]);
-        if (c + j < a.cols) store_one(a, (size_t)(c + j) * a.ld_out + row, a.bias ? __fadd_rn(v, bias) : v);
+      for (int j = 0; j < 16; j++) {
+        store_as<OUT>(at, __fadd_rn(__uint_as_float(r[j]), bias), row < a.rows && c + j < cols);
+        at += step;
       }
     }
-  }
+  });
 }
 
 // The exchange: tokens in units of four, unit u finished by CTA u % S as its
 // unit u / S.  The part of CTA s arrives in the owner's ring (free by then),
 // slot s, per unit 128 rows x 16 bytes.  All threads of the CTA call it.
-__device__ __forceinline__ void exchange_tokens(const BArgs &a, int splits, int rank, int row0, uint32_t base,
-                                                uint32_t tmem_base) {
+__device__ __forceinline__ void exchange_tokens(const BArgs &a, int splits, int rank, int row0, int col0,
+                                                uint32_t base, uint32_t tmem_base) {
+  const int cols = min(a.cols - col0, a.bn);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, row = row0 + q * 32 + lane;
-  const int units = (a.cols + 3) / 4, per = (units + splits - 1) / splits;
+  const int units = (cols + 3) / 4, per = (units + splits - 1) / splits;
   const bool mine = warp >= 2 && warp < 6;
   const float bias = mine && a.bias && row < a.rows ? load_bias(a.bias, a.bias_dtype, row) : 0.0f;
   cluster_sync();  // every CTA's MMAs have read their ring
   if (mine) {
     tc_fence_after();
+    uint32_t at = base + (rank * per * BM + q * 32 + lane) * 16;
+    uint32_t tmem = tmem_base + ((uint32_t)(q * 32) << 16);
+    int owner = 0;
 #pragma unroll 1
-    for (int c = 0; c < a.cols; c += 32) {
-      uint32_t r[32];
-      tmem_ld32(tmem_base + ((uint32_t)(q * 32) << 16) + c, r);
+    for (int c = 0; c < cols; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(tmem + c, r);
 #pragma unroll
-      for (int g = 0; g < 8; g++) {
-        const int u = c / 4 + g;
-        if (u >= units) break;
-        const uint32_t dst = map_to_rank(base, (uint32_t)(u % splits)) +
-                             ((rank * per + u / splits) * BM + q * 32 + lane) * 16;
-        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(r[4 * g]), "r"(r[4 * g + 1]),
-                     "r"(r[4 * g + 2]), "r"(r[4 * g + 3])
-                     : "memory");
+      for (int g = 0; g < 4; g++) {
+        if (c + 4 * g < cols)
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(map_to_rank(at, (uint32_t)owner)),
+                       "r"(r[4 * g]), "r"(r[4 * g + 1]), "r"(r[4 * g + 2]), "r"(r[4 * g + 3])
+                       : "memory");
+        if (++owner == splits) {
+          owner = 0;
+          at += BM * 16;
+        }
       }
     }
     tc_fence_before();
   }
   cluster_sync();  // all parts have arrived
   if (mine) {
+    with_out(a.out_dtype, [&](auto out) {
+      constexpr int OUT = decltype(out)::value, esz = OUT == FP8_DT_F32 ? 4 : 2;
+      const size_t step = a.ld_out * esz;
+      char *at = static_cast<char *>(a.out) + (col0 + rank * 4) * step + (size_t)row * esz;
+      uint32_t first = base + (q * 32 + lane) * 16;
 #pragma unroll 1
-    for (int i = 0, u = rank; u < units; i++, u += splits) {
-      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int c = rank * 4; c < cols; c += splits * 4, at += splits * 4 * step, first += BM * 16) {
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t src = first;
 #pragma unroll 2
-      for (int s = 0; s < splits; s++) {
-        float x[4];
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
-                     : "r"(base + ((s * per + i) * BM + q * 32 + lane) * 16)
-                     : "memory");
+        for (int s = 0; s < splits; s++, src += per * BM * 16) {
+          float x[4];
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                       : "r"(src)
+                       : "memory");
 #pragma unroll
-        for (int j = 0; j < 4; j++) v[j] = __fadd_rn(v[j], x[j]);
-      }
-      if (row < a.rows) {
+          for (int j = 0; j < 4; j++) v[j] = __fadd_rn(v[j], x[j]);
+        }
 #pragma unroll
         for (int j = 0; j < 4; j++)
-          if (u * 4 + j < a.cols)
-            store_one(a, (size_t)(u * 4 + j) * a.ld_out + row, a.bias ? __fadd_rn(v[j], bias) : v[j]);
+          store_as<OUT>(at + j * step, __fadd_rn(v[j], bias), row < a.rows && c + j < cols);
       }
-    }
+    });
   }
 }
 
@@ -224,12 +275,13 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
 }
 
-// Tokens that come as codes (forward and dgrad; in dgrad the weights are read
-// along their rows: A_MN).  Ring stage: A 16 KB, B bn x 128 B; scales of both
+// A_MN, B_MN: the operand's codes are read along their rows (the weights in
+// dgrad, both in wgrad).  Ring stage: A 16 KB, B bn x 128 B; scales of both
 // (1 KB) with every fourth block.
 constexpr int kSfSlot = 1024;
+constexpr int kFewSmemBytes = 112 * 1024;  // at most: two CTAs per SM
 
-template <bool A_MN>
+template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads)
     k_bgemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
@@ -250,7 +302,8 @@ __global__ void __launch_bounds__(kThreads)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = splits > 1 ? (int)cluster_rank() : 0;
-  const int row0 = (int)(blockIdx.x / splits) * BM;
+  const int tile = (int)(blockIdx.x / splits);
+  const int row0 = tile / args.num_n_blocks * BM, col0 = tile % args.num_n_blocks * 128;
   // this CTA's k-blocks
   const int kb0 = (int)((long long)args.num_k_blocks * rank / splits);
   const int kb1 = (int)((long long)args.num_k_blocks * (rank + 1) / splits);
@@ -291,11 +344,12 @@ __global__ void __launch_bounds__(kThreads)
         mbar_arrive_expect_tx(full_bar(stage), args.stage_bytes + (scales ? kSfSlot : 0));
         if (scales) {
           tma_load_3d(ss, &tmSA, 0, kb >> 2, row0 >> 7, full_bar(stage));
-          tma_load_3d(ss + 512, &tmSB, 0, kb >> 2, 0, full_bar(stage));
+          tma_load_3d(ss + 512, &tmSB, 0, kb >> 2, col0 >> 7, full_bar(stage));
         }
         if (A_MN) tma_load_2d(sa, &tmA, row0, kb * BK, full_bar(stage));
         else      tma_load_2d(sa, &tmA, kb * BK, row0, full_bar(stage));
-        tma_load_2d(sa + BM * BK, &tmB, kb * BK, 0, full_bar(stage));
+        if (B_MN) tma_load_2d(sa + BM * BK, &tmB, col0, kb * BK, full_bar(stage));
+        else      tma_load_2d(sa + BM * BK, &tmB, kb * BK, col0, full_bar(stage));
         issued_mask |= 1u << stage;
         issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
         if (++stage == S) { stage = 0; phase ^= 1u; }
@@ -309,8 +363,8 @@ __global__ void __launch_bounds__(kThreads)
   } else if (warp == 1) {
     {
       const bool elected = elect_one();
-      const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0), b_d0 = (uint32_t)operand_desc<false>(base + BM * BK, 0);
-      constexpr uint32_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4, b_ks = UMMA_K >> 4;
+      const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0), b_d0 = (uint32_t)operand_desc<B_MN>(base + BM * BK, 0);
+      constexpr uint32_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4, b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
       const uint32_t st_d = args.stage_bytes >> 4, sf_tmem = tmem_base + args.bn;
       int stage = 0, set = kSfSets - 1;
       uint32_t phase = 0;
@@ -348,11 +402,11 @@ __global__ void __launch_bounds__(kThreads)
     const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
     tc_fence_after();
     if (got && splits == 1)
-      store_tokens(args, row0 + (warp & 3) * 32 + lane, tmem_base + ((uint32_t)((warp & 3) * 32) << 16));
+      store_tokens(args, row0 + (warp & 3) * 32 + lane, col0, tmem_base + ((uint32_t)((warp & 3) * 32) << 16));
     tc_fence_before();
     __syncwarp();
   }
-  if (splits > 1) exchange_tokens(args, splits, rank, row0, base, tmem_base);
+  if (splits > 1) exchange_tokens(args, splits, rank, row0, col0, base, tmem_base);
 
   tc_fence_before();
   __syncthreads();

@@ -871,6 +871,7 @@ struct BlockInfo {
   bool ready = false;
   int pair_clusters = 0;         // co-resident clusters of the pair kernel
   int token_clusters[9] = {0};   // co-resident clusters of 2..8 CTAs of the tokens kernel
+  int few_clusters[9] = {0};     // the same of the kernel for few tiles, at one CTA per SM
 };
 std::mutex g_block_mu;
 BlockInfo g_block[kMaxDevices];
@@ -900,7 +901,8 @@ int block_info(DeviceInfo **d, BlockInfo **out) {
   *out = &b;
   if (b.ready) return FP8_OK;
   using namespace bgemm;
-  int rc = set_max_smem(k_bgemm<false>) | set_max_smem(k_bgemm<true>) | set_max_smem(k_btokens<FP8_DT_F32>) |
+  int rc = set_max_smem(k_bgemm<false, false>) | set_max_smem(k_bgemm<true, false>) |
+           set_max_smem(k_bgemm<true, true>) | set_max_smem(k_btokens<FP8_DT_F32>) |
            set_max_smem(k_btokens<FP8_DT_BF16>) | set_max_smem(k_btokens<FP8_DT_F16>);
   rc |= set_pair_smem<false, false>() | set_pair_smem<false, true>() | set_pair_smem<true, true>();
   if (rc) return FP8_ERR_CUDA;
@@ -919,12 +921,16 @@ int block_info(DeviceInfo **d, BlockInfo **out) {
           cudaSuccess ||
       b.pair_clusters < 1)
     return FP8_ERR_CUDA;
-  cfg.blockDim = dim3(kTokThreads);
-  cfg.dynamicSmemBytes = 232448;
   for (int s = 2; s <= 8; s++) {
     attr.val.clusterDim.x = s;
+    cfg.blockDim = dim3(kTokThreads);
+    cfg.dynamicSmemBytes = 232448;
     cfg.gridDim = dim3(s * ((*d)->sms / s));
     if (cudaOccupancyMaxActiveClusters(&b.token_clusters[s], k_btokens<FP8_DT_BF16>, &cfg) != cudaSuccess)
+      return FP8_ERR_CUDA;
+    cfg.blockDim = dim3(gemm::kThreads);
+    cfg.dynamicSmemBytes = kFewSmemBytes;
+    if (cudaOccupancyMaxActiveClusters(&b.few_clusters[s], k_bgemm<false, false>, &cfg) != cudaSuccess)
       return FP8_ERR_CUDA;
   }
   b.ready = true;
@@ -983,38 +989,73 @@ uint32_t block_idesc(int fmt_a, int fmt_b, bool a_mn, bool b_mn, int n, int m) {
          ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27);
 }
 
-// Reduction splits for `tiles` tiles of kblocks blocks on `slots` resident
-// CTAs: as many as stay resident, each with two blocks at the least.
-int pick_splits(long long tiles, int kblocks, int slots) {
-  int s = 1;
-  while (s < 8 && tiles * (s + 1) <= slots && kblocks >= 2 * (s + 1)) s++;
-  return s;
+// Reduction splits for `tiles` tiles of kblocks blocks: as many as leave every
+// cluster resident, each CTA two blocks at the least.
+int pick_splits(long long tiles, int kblocks, const int (&clusters)[9]) {
+  int splits = 1;
+  for (int s = 2; s <= 8; s++)
+    if (tiles <= clusters[s] && kblocks >= 2 * s) splits = s;
+  return splits;
 }
 
-// Out[tokens, features] for at most 128 tokens as codes (B [tokens, K]); A
-// holds the features, A_MN: read along its rows.
-template <bool A_MN>
-int launch_bgemm(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, int sms, cudaStream_t stream) {
+// The same for the kernel for few tiles, of which an SM holds two CTAs (the
+// runtime's count of resident clusters says one, for any kernel that allocates
+// tensor memory; twice its count are resident in any case).  The second CTA of
+// an SM slows the first one's exchange, so it has to bring enough blocks: 64
+// tiles of 32 blocks took 11.8 us in two splits and 11.4 in four, of 16 blocks
+// 9.3 and 9.7, of 64 blocks 16.8 and 14.8.
+int few_splits(long long tiles, int kblocks, const BlockInfo &bi) {
+  int splits = pick_splits(tiles, kblocks, bi.few_clusters);
+  for (int s = splits + 1; s <= 8; s++)
+    if (tiles <= 2 * bi.few_clusters[s] && kblocks >= 10 * s) splits = s;
+  return splits;
+}
+
+// Whether Out[R, C] goes to the kernel for few tiles (128 x 128, 1.1 to 3 MMAs'
+// time of the pair kernel's for the same product, but on more SMs).  Up to 64
+// rows always: the pair kernel would multiply 256.  Else, measured against the
+// pair kernel: one split wins 5 to 25 % for up to 96 tiles of at most 32 blocks
+// (777 x 1305 x 1024: 7.5 us on pairs, 6.2 here; 128 x 12288 x 8192: 27.8 and
+// 32.6), but not where code rows straddle 32-byte sectors (the same at K = 1001
+// in rows of 1008 bytes: 8.0 and 8.8), since here every operand byte is fetched
+// twice as often; with splits the exchange (3 us) has to pay: from 16 blocks on
+// with four splits (256 x 2048 x 2048: 8.7 and 8.3; x 16384: 45 and 17), from
+// 24 on with fewer (1024 x 1024 x 2048: 8.8 and 9.3; x 4096: 14.0 and 11.8).
+bool few_tiles(int R, int C, int red, bool sectors, const BlockInfo &bi) {
+  if (R <= 64) return true;
+  const long long tiles = ((R + 127LL) / 128) * ((C + 127LL) / 128);
+  const int kblocks = (red + 127) / 128, splits = few_splits(tiles, kblocks, bi);
+  if (splits == 1) return tiles <= 96 && kblocks <= 32 && sectors;
+  return kblocks >= (splits >= 4 ? 16 : 24);
+}
+
+// Out[columns, rows] in 128-row tiles whose reduction is shared by a cluster;
+// A holds the rows (features), B the columns (tokens).
+template <bool A_MN, bool B_MN>
+int launch_bgemm(const BOperand &A, const BOperand &B, bgemm::BArgs a, int K, const BlockInfo &bi,
+                 cudaStream_t stream) {
   using namespace bgemm;
-  a.bn = (a.cols + 31) / 32 * 32;
+  a.bn = B_MN || a.cols > 128 ? 128 : (a.cols + 31) / 32 * 32;
+  a.num_n_blocks = (a.cols + 127) / 128;
   a.num_k_blocks = (K + gemm::BK - 1) / gemm::BK;
   a.stage_bytes = (uint32_t)(gemm::BM + a.bn) * gemm::BK;
   a.tmem_cols = a.bn + kSfSets * kSfCols <= 64 ? 64 : a.bn + kSfSets * kSfCols <= 128 ? 128 : 256;
-  // two CTAs per SM
-  const int fit = (int)((114688u - 1024u - 256u) / (a.stage_bytes + kSfSlot));
+  const int fit = (kFewSmemBytes - 1024 - 256) / (int)(a.stage_bytes + kSfSlot);
   a.stages = fit < kMaxStages ? fit : kMaxStages;
   a.desc_hi = kDescHi;
-  a.idesc = block_idesc(A.fmt, B.fmt, A_MN, false, a.bn, gemm::BM);
+  a.idesc = block_idesc(A.fmt, B.fmt, A_MN, B_MN, a.bn, gemm::BM);
   CUtensorMap ma, mb, msa, msb;
   int rc = A_MN ? make_code_map(&ma, A.b->q, a.rows, K, A.b->ld, gemm::BK)
                 : make_code_map(&ma, A.b->q, K, a.rows, A.b->ld, gemm::BM);
-  if (rc || (rc = make_code_map(&mb, B.b->q, K, a.cols, B.b->ld, (uint32_t)a.bn)) ||
-      (rc = make_scale_map(&msa, A.b->s, a.rows, K, 1)) || (rc = make_scale_map(&msb, B.b->s, a.cols, K, 1)))
+  if (rc) return rc;
+  rc = B_MN ? make_code_map(&mb, B.b->q, a.cols, K, B.b->ld, gemm::BK)
+            : make_code_map(&mb, B.b->q, K, a.cols, B.b->ld, (uint32_t)a.bn);
+  if (rc || (rc = make_scale_map(&msa, A.b->s, a.rows, K, 1)) || (rc = make_scale_map(&msb, B.b->s, a.cols, K, 1)))
     return rc;
-  const long long tiles = ((long long)a.rows + gemm::BM - 1) / gemm::BM;
-  const int splits = pick_splits(tiles, a.num_k_blocks, 2 * sms);
+  const long long tiles = ((long long)a.rows + gemm::BM - 1) / gemm::BM * a.num_n_blocks;
+  const int splits = few_splits(tiles, a.num_k_blocks, bi);
   const size_t smem = (size_t)a.stages * (a.stage_bytes + kSfSlot) + 256 + 1024;
-  return launch_pdl(k_bgemm<A_MN>, (unsigned)(tiles * splits), gemm::kThreads, smem, stream, splits, ma, mb, msa, msb,
+  return launch_pdl(k_bgemm<A_MN, B_MN>, (unsigned)(tiles * splits), gemm::kThreads, smem, stream, splits, ma, mb, msa, msb,
                     a, splits);
 }
 
@@ -1030,9 +1071,7 @@ int launch_btokens(const BOperand &W, bgemm::BArgs a, int K, const BlockInfo &bi
   int rc = make_code_map(&mw, W.b->q, K, a.rows, W.b->ld, kTokBN);
   if (rc || (rc = make_scale_map(&msw, W.b->s, a.rows, K, kTokBN / 128))) return rc;
   const long long tiles = ((long long)a.rows + kTokBN - 1) / kTokBN;
-  int splits = 1;
-  for (int s = 2; s <= 8; s++)
-    if (tiles <= bi.token_clusters[s] && a.num_k_blocks >= 2 * s) splits = s;
+  const int splits = pick_splits(tiles, a.num_k_blocks, bi.token_clusters);
   const int batches = (a.cols + kTokBatch - 1) / kTokBatch;
   const size_t smem = (size_t)tok_fixed(batches) + tok_stages(batches) * (kTokStageBytes + 1024);
   return launch_pdl(k_btokens<DT>, (unsigned)(tiles * splits), kTokThreads, smem, stream, splits, mw, msw, a, splits);
@@ -1106,12 +1145,10 @@ int run_bgemm(const BOperand &A, const BOperand &B, const void *bias, int bias_d
   if ((rc = check_blocks(B.b, B_MN ? C : red))) return rc;
   BlockInfo *bi;
   if ((rc = block_info(&d, &bi))) return rc;
-  if constexpr (!A_MN) {
-    if (R <= 128) {  // few tokens: the weights become the row operand
-      a.rows = C;
-      a.cols = R;
-      return launch_bgemm<B_MN>(B, A, a, red, d->sms, stream);
-    }
+  if (few_tiles(R, C, red, A.b->ld % 32 == 0 && B.b->ld % 32 == 0, *bi)) {  // the weights (x in wgrad) become the row operand
+    a.rows = C;
+    a.cols = R;
+    return launch_bgemm<B_MN, A_MN>(B, A, a, red, *bi, stream);
   }
   return launch_bgemm2<A_MN, B_MN>(A, B, a, red, bi->pair_clusters, stream);
 }

@@ -432,9 +432,11 @@ def fp8_block_scale_bytes(outer: int, red: int) -> int:
 
 
 def block_codes(rows: int, cols: int, device="cuda") -> torch.Tensor:
-    """An uninitialised [rows, cols] uint8 code matrix whose rows start on
-    16-byte boundaries (its row stride is cols rounded up to 16)."""
-    return torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=device)[:, :cols]
+    """An uninitialised [rows, cols] uint8 code matrix whose row stride is cols
+    rounded up to 128.  The products take any multiple of 16; rows that straddle
+    no cache lines cost them less (4000 x 4000 x 4104: 52 us, 60 with a stride
+    of 4112)."""
+    return torch.empty((rows, -(-cols // 128) * 128), dtype=torch.uint8, device=device)[:, :cols]
 
 
 def block_scales(outer: int, red: int, device="cuda") -> torch.Tensor:

@@ -285,6 +285,30 @@ def test_products_against_binary64(shape, grad):
     assert fp8.fp8_get_status() == 0
 
 
+# A long reduction behind few output tiles, in turn in y, dx and dw: one to
+# eight CTAs share a tile, with the last tiles and blocks cut short.
+FEW_TILES = [(65, 100, 1100), (130, 260, 9000), (200, 9000, 136), (8200, 130, 257), (65, 7000, 12300), (777, 1305, 4100),
+             (1024, 1024, 4096), (1500, 1100, 8200), (129, 12000, 300)]
+
+
+@pytest.mark.parametrize("shape", FEW_TILES)
+def test_long_reductions_of_few_tiles(shape):
+    M, N, K = shape
+    L = Layer(M, N, K)
+    bias = torch.randn(N, device="cuda")
+    ref = L.references(bias)
+    for dtype, pad in ((BF16, 0), (F16, 3), (F32, 1)):
+        y, dx, dw = (torch.full((r, c + pad), 7.0, dtype=dtype, device="cuda") for r, c in ((M, N), (M, K), (N, K)))
+        for _ in range(2):
+            fp8.fp8_block_linear_fwd(L.xq, L.xs, L.wq, L.ws, y[:, :N], bias=bias)
+            fp8.fp8_block_linear_dgrad(L.gq, L.gs, L.grad, L.wq, L.wsc, dx[:, :K])
+            fp8.fp8_block_linear_wgrad(L.gqc, L.gsc, L.grad, L.xqc, L.xsc, dw[:, :K])
+        for name, out, n in (("y", y, N), ("dx", dx, K), ("dw", dw, K)):
+            assert_product(out[:, :n], ref[name], (name, dtype))
+            assert bool((out[:, n:] == 7.0).all()), name
+    assert fp8.fp8_get_status() == 0
+
+
 @pytest.mark.parametrize("shape", [(5, 260, 200), (200, 260, 200), (2309, 4871, 256)])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16, "rto"])
 @pytest.mark.parametrize("pad,offset", [(0, 0), (8, 0), (3, 0), (0, 1)])
