@@ -513,10 +513,23 @@ __device__ __forceinline__ void cast_tokens(const BArgs &a, int t0, int kb, uint
     float2 s4[4];
     block::unpack8<DT>(raw[i], f);
     block::spread_scale(s, s4);
-    uint2 c = block::enc8<FP8_E4M3>(f, s4);
-    if (nan) c = block::enc8_any<FP8_E4M3>(f, s4);
+    const uint2 c = block::enc8<FP8_E4M3>(f, s4);
     const uint32_t at = tile + t * 128 + (((c8 >> 1) ^ (t & 7)) << 4) + (c8 & 1) * 8;
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(c.x), "r"(c.y) : "memory");
+  }
+  if (nan) {  // behind the common code, which a CTA mostly runs once, from a cold instruction cache
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int t = t0 + 2 * i + half;
+      const float s = __shfl_sync(0xffffffffu, own, (lane & 16) + 4 * i);
+      float f[8];
+      float2 s4[4];
+      block::unpack8<DT>(raw[i], f);
+      block::spread_scale(s, s4);
+      const uint2 c = block::enc8_any<FP8_E4M3>(f, s4);
+      const uint32_t at = tile + t * 128 + (((c8 >> 1) ^ (t & 7)) << 4) + (c8 & 1) * 8;
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(c.x), "r"(c.y) : "memory");
+    }
   }
 }
 
@@ -681,30 +694,45 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     // Unit u: tokens of batch u % batches, block u / batches (counted from the
     // first group's first block; blocks of a group that another CTA multiplies
     // are cast too, so that every group has the same number of units).
+    // The first turn only loads; one load and one cast site keep the code short.
     block::Raw8<DT> x[4];
-    int u = warp - 2;
-    if (u < units_x) load_tokens<DT>(args, u % batches * kTokBatch, (g0 * 4 + u / batches) * BK, lane, x);
-    if (u < units_x) {
-      uint32_t seen = 0;
-#pragma unroll
-      for (int j = 0; j < 4; j++) seen |= x[j].w[0];
-      uint32_t any;  // (0 or 1: makes the arrive wait for the loads)
-      asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tvote.sync.any.pred p, p, 0xffffffff;\n\t"
-                   "selp.u32 %0, 1, 0, p;\n\t}"
-                   : "=r"(any)
-                   : "r"(seen));
-      if (lane == 0 && any <= 1u) mbar_arrive(loaded_bar);
-    }
-    for (; u < units_x; u += kTokWarps) {
-      const int i = u / batches, t0 = (u - i * batches) * kTokBatch, g = i >> 2, slot = g % G;
+    const int step_i = kTokWarps / batches, step_b = kTokWarps - step_i * batches;
+    int i = (warp - 2) / batches, b = (warp - 2) - i * batches;  // the unit to load: block, batch
+    int ci = -1, cb = 0, cg = 0, slot = 0;                       // the one to cast; its group, slot and the slot's turn
+    uint32_t turn = 1;
+    const int blocks = groups * 4;
+    while (i < blocks || ci >= 0) {
       block::Raw8<DT> next[4];
-      const int un = min(u + kTokWarps, units_x - 1);
-      load_tokens<DT>(args, un % batches * kTokBatch, (g0 * 4 + un / batches) * BK, lane, next);
-      if (!__all_sync(0xffffffffu, mbar_wait(cempty_bar(slot), ((uint32_t)(g / G) & 1u) ^ 1u, abort_flag))) break;
-      cast_tokens<DT>(args, t0, i & 3, base + slot * group_bytes + (i & 3) * tile_bytes, sfx0 + slot * 512, lane, x);
-      fence_async_shared();  // the MMAs and the scale copy read through the async proxy
-      __syncwarp();
-      if (lane == 0) mbar_arrive(cfull_bar(slot));
+      const bool more = i < blocks;
+      if (more) load_tokens<DT>(args, b * kTokBatch, (g0 * 4 + i) * BK, lane, next);
+      if (ci < 0) {
+        uint32_t seen = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j++) seen |= next[j].w[0];
+        uint32_t any;  // (0 or 1: makes the arrive wait for the loads)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tvote.sync.any.pred p, p, 0xffffffff;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(any)
+                     : "r"(seen));
+        if (lane == 0 && any <= 1u) mbar_arrive(loaded_bar);
+      } else {
+        for (slot += (ci >> 2) - cg, cg = ci >> 2; slot >= G; slot -= G) turn ^= 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait(cempty_bar(slot), turn, abort_flag))) break;
+        cast_tokens<DT>(args, cb * kTokBatch, ci & 3, base + slot * group_bytes + (ci & 3) * tile_bytes,
+                        sfx0 + slot * 512, lane, x);
+        fence_async_shared();  // the MMAs and the scale copy read through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cfull_bar(slot));
+      }
+      ci = more ? i : -1;
+      if (!more) break;
+      cb = b;
+      i += step_i;
+      b += step_b;
+      if (b >= batches) {
+        b -= batches;
+        i++;
+      }
 #pragma unroll
       for (int j = 0; j < 4; j++) x[j] = next[j];
     }
@@ -717,33 +745,43 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     const bool got = __all_sync(0xffffffffu, mbar_wait(tfull_bar, 0, abort_flag));
     tc_fence_after();
     // (after a timeout the parts are sent all the same: their owners count on them)
+    int owner = splits > 1 ? (c0 / 8) % splits : 0;
+    uint32_t part = parts0 + (uint32_t)((rank * per + c0 / 8 / splits) * 2 * lanes + lane) * 16;
 #pragma unroll 1
-    for (int c = c0; c < c0 + 64 && c / 8 < units; c += 32) {
-      const int bcol = row0 + c + lane;
-      const float bias = splits == 1 && args.bias && bcol < args.rows ? load_bias(args.bias, args.bias_dtype, bcol) : 0.0f;
-      uint32_t r[32];
-      tmem_ld32(tmem_base + c, r);
+    for (int c = c0; c < c0 + 64 && c / 8 < units; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(tmem_base + c, r);
+      if (splits == 1) {
+        const int bcol = row0 + c + lane;
+        const float bias = args.bias && lane < 16 && bcol < args.rows ? load_bias(args.bias, args.bias_dtype, bcol) : 0.0f;
 #pragma unroll
-      for (int g = 0; g < 4; g++) {
-        const int u = c / 8 + g;
-        if (splits == 1) {
+        for (int j = 0; j < 16; j++)
+          r[j] = __float_as_uint(__fadd_rn(__uint_as_float(r[j]), __shfl_sync(0xffffffffu, bias, j)));
+#pragma unroll
+        for (int g = 0; g < 2; g++) {
           float v[8];
 #pragma unroll
-          for (int j = 0; j < 8; j++) {
-            v[j] = __uint_as_float(r[8 * g + j]);
-            if (args.bias) v[j] = __fadd_rn(v[j], __shfl_sync(0xffffffffu, bias, 8 * g + j));
-          }
-          if (got) store_features(args, lane, row0 + u * 8, v);
-        } else if (u < units && lane < args.cols) {  // to part `rank` of the owner's unit, `lanes` x 16 bytes per half
-          const uint32_t owner = (uint32_t)(u % splits), bar = map_to_rank(parts_bar, owner);
-          const uint32_t dst = map_to_rank(parts0, owner) + (((rank * per + u / splits) * 2) * lanes + lane) * 16;
+          for (int j = 0; j < 8; j++) v[j] = __uint_as_float(r[8 * g + j]);
+          if (got) store_features(args, lane, row0 + c + 8 * g, v);
+        }
+      } else {  // to part `rank` of the owner's unit, `lanes` x 16 bytes per half
 #pragma unroll
-          for (int h = 0; h < 2; h++)
-            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                             dst + h * lanes * 16),
-                         "r"(r[8 * g + 4 * h]), "r"(r[8 * g + 4 * h + 1]), "r"(r[8 * g + 4 * h + 2]),
-                         "r"(r[8 * g + 4 * h + 3]), "r"(bar)
-                         : "memory");
+        for (int g = 0; g < 2; g++) {
+          if (c / 8 + g < units && lane < args.cols) {
+            const uint32_t bar = map_to_rank(parts_bar, (uint32_t)owner), dst = map_to_rank(part, (uint32_t)owner);
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+              asm volatile(
+                  "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                      dst + h * lanes * 16),
+                  "r"(r[8 * g + 4 * h]), "r"(r[8 * g + 4 * h + 1]), "r"(r[8 * g + 4 * h + 2]), "r"(r[8 * g + 4 * h + 3]),
+                  "r"(bar)
+                  : "memory");
+          }
+          if (++owner == splits) {
+            owner = 0;
+            part += 2 * lanes * 16;
+          }
         }
       }
     }
