@@ -17,7 +17,6 @@ MAIN = os.path.join(HERE, "csrc", "libfp8.cu")
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "--split-compile=0",  # optimise the kernels in parallel
     "-Xcompiler", "-fPIC", "-shared",
 ]
 
