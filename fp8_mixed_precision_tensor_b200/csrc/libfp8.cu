@@ -860,6 +860,9 @@ unsigned tile_grid(int rows, int cols) {
   return t <= 0x7fffffffull ? (unsigned)t : 0u;
 }
 
+// Whether an elementwise kernel takes its form for few tiles: one CTA or less per SM.
+bool few_tiles_of(unsigned tiles, int sms) { return tiles != 0 && tiles <= (unsigned)sms; }
+
 block::CastOut cast_out(const fp8_blocks *row, const fp8_blocks *col) {
   block::CastOut o = {};
   if (row) { o.q = row->q; o.s = row->s; o.ldq = row->ld; }
@@ -1169,11 +1172,18 @@ int fp8_block_cast(const void *x, int dtype, int rows, int cols, size_t ldx, int
   int rc = check_matrix(x, dtype, cols, ldx);
   if (rc || (row && (rc = check_blocks(row, cols))) || (col && (rc = check_blocks(col, cols)))) return rc;
   const block::CastOut o = cast_out(row, col);
+  DeviceInfo *d;
+  if ((rc = device_info(&d))) return rc;
+  const unsigned tiles = tile_grid(rows, cols);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_fmt(fmt, [&](auto f) {
-      rc = launch_pdl(block::k_block_cast<decltype(dt)::value, decltype(f)::value>, tile_grid(rows, cols),
-                      block::kCastThreads, 0, s, 1, x, rows, cols, ldx, (int)wide_rows(x, dtype, ldx), margin, o);
+      constexpr int DT = decltype(dt)::value, FMT = decltype(f)::value;
+      const int vec = (int)wide_rows(x, dtype, ldx);
+      if (few_tiles_of(tiles, d->sms))
+        rc = launch_pdl(block::k_block_cast<DT, FMT, 2>, tiles, 1024, 0, s, 1, x, rows, cols, ldx, vec, margin, o);
+      else
+        rc = launch_pdl(block::k_block_cast<DT, FMT, 8>, tiles, block::kCastThreads, 0, s, 1, x, rows, cols, ldx, vec, margin, o);
     });
   });
   return rc;
@@ -1190,11 +1200,18 @@ int fp8_block_cast_square(const void *x, int dtype, int rows, int cols, size_t l
   if (!aligned16(s_col)) return FP8_ERR_UNALIGNED;
   block::CastOut o = cast_out(out, nullptr);
   o.st = s_col;
+  DeviceInfo *d;
+  if ((rc = device_info(&d))) return rc;
+  const unsigned tiles = tile_grid(rows, cols);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_fmt(fmt, [&](auto f) {
-      rc = launch_pdl(block::k_block_cast_square<decltype(dt)::value, decltype(f)::value>, tile_grid(rows, cols),
-                      block::kCastThreads, 0, s, 1, x, rows, cols, ldx, (int)wide_rows(x, dtype, ldx), margin, o);
+      constexpr int DT = decltype(dt)::value, FMT = decltype(f)::value;
+      const int vec = (int)wide_rows(x, dtype, ldx);
+      if (few_tiles_of(tiles, d->sms))
+        rc = launch_pdl(block::k_block_cast_square<DT, FMT, 2>, tiles, 1024, 0, s, 1, x, rows, cols, ldx, vec, margin, o);
+      else
+        rc = launch_pdl(block::k_block_cast_square<DT, FMT, 8>, tiles, block::kCastThreads, 0, s, 1, x, rows, cols, ldx, vec, margin, o);
     });
   });
   return rc;
@@ -1291,11 +1308,15 @@ int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int ac
     p.as = a_row->s;
     p.lda_q = a_row->ld;
   }
+  DeviceInfo *d;
+  if ((rc = device_info(&d))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_act(act, [&](auto f) {
-      rc = launch_pdl(block::k_act_fwd<decltype(dt)::value, decltype(f)::value>, tile_grid(rows, cols),
-                      block::kActThreads, 0, s, 1, p);
+      constexpr int DT = decltype(dt)::value, ACT = decltype(f)::value;
+      const unsigned tiles = tile_grid(rows, cols);
+      if (few_tiles_of(tiles, d->sms)) rc = launch_pdl(block::k_act_fwd<DT, ACT, 1>, tiles * 4, block::kActThreads, 0, s, 1, p);
+      else rc = launch_pdl(block::k_act_fwd<DT, ACT, 4>, tiles, block::kActThreads, 0, s, 1, p);
     });
   });
   return rc;
@@ -1315,6 +1336,7 @@ int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int
     return rc;
   DeviceInfo *d;
   if ((rc = device_info(&d))) return rc;
+  const unsigned tiles = tile_grid(rows, cols);
   block::ActBwd p = {ckpt->q, ckpt->s, ckpt->ld, da, rows, cols, ldda, margin, cast_out(dh_row, dh_col),
                      nullptr, nullptr, 0, dh, lddh, wide_rows(da, dtype, ldda), wide_rows(dh, dtype, lddh)};
   if (a_col) {
@@ -1325,19 +1347,22 @@ int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {
     with_act(act, [&](auto f) {
-      auto go = [&](auto out) {
-        using K = decltype(dt);
-        constexpr int kOut = decltype(out)::value;
-        const auto kernel = block::k_act_bwd<K::value, decltype(f)::value, kOut>;
-        constexpr int smem = block::ActBwdSmem<K::value>::kBytes;
+      constexpr int DT = decltype(dt)::value, ACT = decltype(f)::value;
+      auto go = [&](auto out, auto rows_per_thread) {
+        constexpr int OUT = decltype(out)::value, RP = decltype(rows_per_thread)::value;
+        const auto kernel = block::k_act_bwd<DT, ACT, OUT, RP>;
+        constexpr int smem = block::ActBwdSmem<DT, RP>::kBytes;
         if ((rc = set_smem(kernel, smem))) return;
-        // resident CTAs (the kernel's launch bounds)
-        const unsigned cap = (unsigned)d->sms * (kOut == block::kActPlain && K::value == FP8_DT_BF16 ? 2u : 1u);
-        const unsigned tiles = tile_grid(rows, cols);
-        rc = launch_pdl(kernel, tiles < cap ? tiles : cap, block::kActThreads, smem, s, 1, p);
+        const unsigned cap = (unsigned)(d->sms * block::kActBwdPerSm<DT, RP, OUT>);  // resident CTAs
+        const unsigned slabs = RP == 1 ? (rows + 31) / 32u * ((cols + 127) / 128u) : tiles;
+        rc = launch_pdl(kernel, slabs < cap ? slabs : cap, block::kActThreads, smem, s, 1, p);
       };
-      if (dh_row || dh_col || a_col) with_fmt(fmt, go);
-      else go(std::integral_constant<int, block::kActPlain>());
+      using Plain = std::integral_constant<int, block::kActPlain>;
+      using One = std::integral_constant<int, 1>;
+      using Four = std::integral_constant<int, 4>;
+      if (dh_row || dh_col || a_col) with_fmt(fmt, [&](auto out) { go(out, Four()); });
+      else if (few_tiles_of(tiles, d->sms)) go(Plain(), One());
+      else go(Plain(), Four());
     });
   });
   return rc;
