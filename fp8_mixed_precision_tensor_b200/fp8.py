@@ -10,6 +10,8 @@ has not been built.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -17,6 +19,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8.so")
+CALLS_PATH = os.path.join(_HERE, "_calls.so")
 
 # status codes / enums (include/fp8.h)
 FP8_OK, FP8_ERR_INVALID_ARG, FP8_ERR_UNALIGNED, FP8_ERR_UNSUPPORTED = 0, 1, 2, 3
@@ -80,15 +83,35 @@ class _HParams(ctypes.Structure):
 
 
 _lib = None
+_calls = None  # _calls.so, bound to _lib
 # The C functions behind torch.cuda.current_device() and current_stream(), where this torch has them.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
+def _bound_calls(lib: ctypes.CDLL):
+    """_calls.so with the addresses of lib's block-scaled operators."""
+    if not os.path.exists(CALLS_PATH):
+        raise ImportError(f"_calls.so not built ({CALLS_PATH}); run python -m fp8_mixed_precision_tensor_b200.build")
+    name = __package__ + "._calls"
+    loader = importlib.machinery.ExtensionFileLoader(name, CALLS_PATH)
+    calls = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, CALLS_PATH, loader=loader))
+    loader.exec_module(calls)
+    calls.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+        "fp8_block_cast", "fp8_block_cast_square", "fp8_block_linear_fwd", "fp8_block_linear_tokens",
+        "fp8_block_linear_dgrad", "fp8_block_linear_wgrad", "fp8_act_fwd", "fp8_act_bwd")))
+    return calls
+
+
+def _load_calls():
+    load_library()
+    return _calls
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libfp8.so and declare the signatures of every entry point."""
-    global _lib
+    global _lib, _calls
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -135,6 +158,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in SYMBOLS:
         if name not in ("fp8_adam_workspace_bytes", "fp8_block_scale_bytes", "fp8_strerror"):
             getattr(lib, name).restype = i
+    _calls = _bound_calls(lib)
     _lib = lib
     return lib
 
@@ -445,9 +469,10 @@ def block_scales(outer: int, red: int, device="cuda") -> torch.Tensor:
     return torch.empty(fp8_block_scale_bytes(outer, red), dtype=torch.uint8, device=device)
 
 
-# The argument checks below run on every call of a path whose kernels take a
-# few microseconds: each reads a tensor's properties once and decides by one
-# expression; what was wrong is found out afterwards.
+# The block-scaled operators go through _calls.so, which enqueues a plainly valid
+# call (device tensors of the right kinds and shapes, the current device and
+# stream) in 3 us.  What it leaves is checked here: made all the same, or refused
+# with what is wrong about it.
 _U8 = torch.uint8
 
 
@@ -543,6 +568,8 @@ def _codes_shape(q: torch.Tensor, what: str):
 def fp8_block_cast(x, fmt: int, margin: int, q_row=None, s_row=None, q_col=None, s_col=None, stream=None) -> None:
     """x [rows, cols] to codes of 1x128 blocks (q_row, s_row) and / or of 128x1
     blocks (q_col, s_col), reading x once."""
+    if (_calls or _load_calls()).block_cast(x, fmt, margin, q_row, s_row, q_col, s_col, stream):
+        return
     dt, rows, cols, ld, dev = _input(x, "x")
     _check(load_library().fp8_block_cast(x.data_ptr(), dt, rows, cols, ld, fmt, margin,
                                          _blocks(q_row, s_row, "row blocks", rows, cols, rows, cols, dev),
@@ -553,6 +580,8 @@ def fp8_block_cast(x, fmt: int, margin: int, q_row=None, s_row=None, q_col=None,
 def fp8_block_cast_square(x, fmt: int, margin: int, q, s_row, s_col, stream=None) -> None:
     """x to codes of 128x128 blocks, their scales in both orders (s_row for
     products that reduce over the columns, s_col over the rows)."""
+    if (_calls or _load_calls()).block_cast_square(x, fmt, margin, q, s_row, s_col, stream):
+        return
     dt, rows, cols, ld, dev = _input(x, "x")
     row = _blocks(q, s_row, "blocks", rows, cols, rows, cols, dev)
     _blocks(q, s_col, "blocks", rows, cols, cols, rows, dev)
@@ -577,6 +606,8 @@ def _out(t, what: str, rows: int, cols: int, dev: int, rto: bool) -> tuple[int, 
 
 def fp8_block_linear_fwd(xq, xs, wq, ws, y, bias=None, stream=None, rto=False) -> None:
     """y[M,N] = x . w^T (+ bias): xq [M,K] with scales of (M, K), wq [N,K] with scales of (N, K)."""
+    if (_calls or _load_calls()).linear_fwd(xq, xs, wq, ws, y, bias, stream, rto):
+        return
     M, K, dev = _codes_shape(xq, "x")
     N = wq.shape[0]
     yp, ydt, ld = _out(y, "y", M, N, dev, rto)
@@ -590,6 +621,8 @@ def fp8_block_linear_tokens(x, wq, ws, y, bias=None, margin: int = 0, stream=Non
     """y[M,N] = x . w^T (+ bias) for at most FP8_BLOCK_TOKENS_MAX tokens x [M,K]
     in float32, bfloat16 or float16: fp8_block_cast and fp8_block_linear_fwd in
     one launch."""
+    if (_calls or _load_calls()).linear_tokens(x, wq, ws, y, bias, margin, stream, rto):
+        return
     dt, M, K, ldx, dev = _input(x, "x")
     N = wq.shape[0]
     yp, ydt, ldy = _out(y, "y", M, N, dev, rto)
@@ -601,6 +634,8 @@ def fp8_block_linear_tokens(x, wq, ws, y, bias=None, margin: int = 0, stream=Non
 
 def fp8_block_linear_dgrad(dyq, dys, dy_fmt: int, wq, ws_col, dx, stream=None, rto=False) -> None:
     """dx[M,K] = dy . w: dyq [M,N] with scales of (M, N), wq [N,K] with scales of (K, N)."""
+    if (_calls or _load_calls()).linear_dgrad(dyq, dys, dy_fmt, wq, ws_col, dx, stream, rto):
+        return
     M, N, dev = _codes_shape(dyq, "dy")
     K = wq.shape[1]
     xp, xdt, ld = _out(dx, "dx", M, K, dev, rto)
@@ -611,6 +646,8 @@ def fp8_block_linear_dgrad(dyq, dys, dy_fmt: int, wq, ws_col, dx, stream=None, r
 
 def fp8_block_linear_wgrad(dyq, dys_col, dy_fmt: int, xq, xs_col, dw, stream=None, rto=False) -> None:
     """dw[N,K] = dy^T . x: dyq [M,N] with scales of (N, M), xq [M,K] with scales of (K, M)."""
+    if (_calls or _load_calls()).linear_wgrad(dyq, dys_col, dy_fmt, xq, xs_col, dw, stream, rto):
+        return
     M, N, dev = _codes_shape(dyq, "dy")
     K = xq.shape[1]
     wp, wdt, ld = _out(dw, "dw", N, K, dev, rto)
@@ -623,6 +660,8 @@ def fp8_block_linear_wgrad(dyq, dys_col, dy_fmt: int, xq, xs_col, dw, stream=Non
 def fp8_act_fwd(h, act: int, margin: int, ckpt_q, ckpt_s, a_q=None, a_s=None, a=None, stream=None) -> None:
     """From h: the E4M3 checkpoint (1x128 blocks), and optionally the E4M3
     codes of act(h)'s 1x128 blocks and act(h) itself (h's dtype)."""
+    if (_calls or _load_calls()).act_fwd(h, act, margin, ckpt_q, ckpt_s, a_q, a_s, a, stream):
+        return
     dt, rows, cols, ld, dev = _input(h, "h")
     ap, lda = None, 0
     if a is not None:
@@ -640,6 +679,9 @@ def fp8_act_bwd(ckpt_q, ckpt_s, da, act: int, fmt: int = FP8_E5M2, margin: int =
     """From the checkpoint and da: codes of dh = da * act'(h') in 1x128 blocks
     (dh_q, dh_s) and 128x1 blocks (dh_q_col, dh_s_col), E4M3 codes of act(h')
     in 128x1 blocks (a_q_col, a_s_col), and dh itself (da's dtype); any of them."""
+    if (_calls or _load_calls()).act_bwd(ckpt_q, ckpt_s, da, act, fmt, margin, dh_q, dh_s, dh_q_col,
+                                         dh_s_col, a_q_col, a_s_col, dh, stream):
+        return
     dt, rows, cols, ld, dev = _input(da, "da")
     hp, lddh = None, 0
     if dh is not None:

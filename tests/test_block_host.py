@@ -176,3 +176,14 @@ def test_binding_takes_device_tensors_only(fp8):
         fp8.fp8_act_fwd(x, fp8.FP8_ACT_SILU, 0, q, s)
     with pytest.raises(TypeError):
         fp8.fp8_block_cast(x.double(), fp8.FP8_E4M3, 0, q, s)
+
+
+def test_short_route_leaves_host_tensors_and_wrong_arguments(fp8):
+    x, q, s = torch.zeros(4, 128), torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    assert fp8._calls.block_cast(x, 0, 0, q, s, None, None, None) is False
+    assert fp8._calls.block_cast(x, 0, 0) is False and fp8._calls.linear_fwd(*range(8)) is False
+    assert fp8._calls.act_fwd(None, 0, 0, q, s, None, None, None, None) is False
+    with pytest.raises(TypeError):
+        fp8._calls.bind(1, 2)
+    with pytest.raises(ValueError):
+        fp8._calls.bind(*[0] * 8)

@@ -628,6 +628,51 @@ def test_two_streams_at_once_give_the_same_results():
     assert fp8.fp8_get_status() == 0
 
 
+class _Routed:
+    """fp8._calls with its answers noted, or refusing every call."""
+
+    def __init__(self, calls, refuse):
+        self.calls, self.refuse, self.answers = calls, refuse, []
+
+    def __getattr__(self, name):
+        def call(*a):
+            ok = False if self.refuse else getattr(self.calls, name)(*a)
+            self.answers.append((name, ok))
+            return ok
+        return call
+
+
+def test_both_routes_of_a_call_give_the_same_results(monkeypatch):
+    a, b = _buffers(200, 264, 520, 5), _buffers(200, 264, 520, 5)
+    short, long = _Routed(fp8._calls, False), _Routed(fp8._calls, True)
+    for calls, buffers in ((short, a), (long, b)):
+        monkeypatch.setattr(fp8, "_calls", calls)
+        _step(buffers)
+    torch.cuda.synchronize()
+    assert all(ok for _, ok in short.answers) and len({n for n, _ in short.answers}) == 8
+    for k in OUTS:
+        assert torch.equal(a[k], b[k]), k
+
+
+def test_the_short_route_leaves_what_is_not_plain():
+    L, calls = Layer(32, 64, 128), fp8._calls
+    y, st = torch.full((32, 64), 5.0, device="cuda"), torch.cuda.Stream()
+    fwd = dict(xq=L.xq, xs=L.xs, wq=L.wq, ws=L.ws, y=y, bias=None, stream=None, rto=False)
+    for name, bad in (("xq", L.xq[:, :100]), ("xq", L.xq[None]), ("xq", L.xq.cpu()), ("xq", None), ("xs", L.xs[:100]),
+                      ("xs", L.xs.float()), ("xs", L.xs.cpu()), ("wq", L.wq.view(torch.int8)), ("wq", 3), ("y", y[:, :63]),
+                      ("y", y.double()), ("y", y.t().contiguous().t()), ("bias", torch.ones(63, device="cuda")),
+                      ("bias", torch.ones(64)), ("stream", st), ("stream", 0), ("rto", 1), ("rto", True)):
+        assert calls.linear_fwd(*(fwd | {name: bad}).values()) is False, (name, bad)
+    cast = dict(x=L.x, fmt=0, margin=0, q=L.xq.clone(), s=L.xs.clone(), qc=None, sc=None, stream=None)
+    for name, bad in (("x", L.x.double()), ("x", L.x[:1].expand(32, 128)), ("x", L.x[:, ::2]), ("fmt", 0.0), ("fmt", 2 ** 40),
+                      ("fmt", 7), ("margin", None), ("margin", -1), ("s", None), ("q", None), ("qc", L.xq), ("stream", st)):
+        assert calls.block_cast(*(cast | {name: bad}).values()) is False, (name, bad)
+    torch.cuda.synchronize()
+    assert bool((y == 5.0).all()) and calls.block_cast(*cast.values()) is True
+    assert torch.equal(cast["q"], L.xq)
+    assert fp8.fp8_get_status() == 0
+
+
 def test_calls_take_an_explicit_stream():
     L = Layer(64, 128, 256)
     torch.cuda.synchronize()
