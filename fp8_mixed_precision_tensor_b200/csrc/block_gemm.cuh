@@ -68,8 +68,8 @@ __device__ __forceinline__ void tc_mma_bs(uint32_t d, uint32_t ad, uint32_t bd, 
 
 // The MMA issuers' loops run in the whole warp with one elected lane issuing:
 // their many operands then stay in uniform registers, where the MMAs take them
-// from.  In a loop of one lane every operand is moved there for each MMA,
-// about 190 cycles a block-scaled MMA instead of its 128.
+// from.  In a loop of one lane every operand is moved there for each MMA
+// (4096^3 on the pair kernel: 50.9 us, 47.8 this way).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
@@ -135,7 +135,9 @@ __device__ __forceinline__ void store_one(const BArgs &a, size_t at, float y) {
 // exchange their partial tiles through distributed shared memory (posted
 // stores; reading the others' parts instead cost 12 us at 128 columns), and
 // each adds the S parts of its own tokens in rank order and stores them: no
-// workspace, no atomics, the same bits each time.
+// workspace, no atomics, the same bits each time.  Bound by latencies: start 3
+// us, exchange 3, a k-block of a CTA 0.3 (33 x 12288 x 4096: 9.2 us; 300 x 520 x
+// 2056 8.1; 256 x 256 x 16384 10).
 //   warp 0 TMA producer, warp 1 TMEM allocation and MMA issue, warps 2-5 epilogue.
 constexpr int kSfCols = 8;      // tensor-memory columns of one set of scales: 4 of A, 4 of B
 constexpr int kSfSets = 3;
@@ -438,7 +440,9 @@ __global__ void __launch_bounds__(kThreads)
 // that the end of the reduction needs no cluster-wide barrier (two of them and
 // the exchange took 2.7 us).
 // Bound by the weights' HBM traffic, and below about 30 MB by the latencies of
-// start, cast and exchange.
+// start, cast and exchange.  Weights in HBM: 12288 x 4096 at one token 14.7 us
+// (3.4 TB/s; 16 at 32 tokens), 12288 x 12288 28.3 (5.3), 4096 x 4096 at 16
+// tokens 8.5.
 constexpr int kTokMaxStages = 6;
 constexpr int kTokBN = 256;    // weight rows per tile
 constexpr int kTokBatch = 8;   // tokens that one cast takes
@@ -458,7 +462,7 @@ __host__ __device__ constexpr int tok_fixed(int batches) {
   return tok_groups(batches) * (4096 * batches + 512) + tok_parts(batches) + 512 + 1024;
 }
 // What is left of the SM's shared memory holds weights in flight: it is their
-// latency that bounds a CTA (16 blocks of 32 KB: 11 us with four stages).
+// latency that bounds a CTA.
 __host__ __device__ constexpr int tok_stages(int batches) {
   const int n = (232448 - tok_fixed(batches)) / (kTokStageBytes + 1024);
   return n < kTokMaxStages ? n : kTokMaxStages;
@@ -855,6 +859,11 @@ __global__ void k_bgemm_empty(const BArgs a) {
 // Whole tiles fill the clusters in waves.  Where the last wave would leave half
 // of the clusters idle, its tiles are worked as two halves of 128 columns (N =
 // 128, the CTAs loading from columns 64 apart), so that it lasts half as long.
+// Bound by the operands' way from L2 into shared memory (a k-block of the pair's
+// MMAs alone takes 0.28 us, with its loads 0.38).  4096^3 48 to 53 us (2.6 to 2.9
+// PFLOP/s), 4096 x 16384 x 4096 206, 8192 x 12288 x 12288 844 to 986 (2.5 to 2.9,
+// power-capped); eight epilogue warps with four stages took 231 us for 205 at
+// K = 16384, six stages with one staging box 61 for 52 at 4096^3.
 //   warp 0 TMA producer (both CTAs), warp 1 TMEM allocation and MMA issue
 //   (leader), warps 2-5 epilogue (both CTAs).
 constexpr int kP2Stages = 5;
