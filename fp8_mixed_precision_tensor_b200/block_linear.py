@@ -11,13 +11,45 @@ input is the 128x1 codes that its wgrad reads: one byte per element and one
 scale byte per 128.
 
 Every number is produced by the library's kernels; this module allocates the
-buffers and orders the calls.
+buffers and orders the calls.  With `stream` (a torch.cuda.Stream or its handle)
+a pass allocates and works on that stream, its outputs included; the caller
+orders it after whatever produced its arguments.
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
 from . import fp8
+
+
+def _on(stream, *args: torch.Tensor):
+    """The pass's stream as the current one; args, tensors of the caller's, are
+    in use on it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in args:
+        t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
+class _Kept:
+    """What a forward pass keeps for the backward pass, and its stream."""
+
+    def __init__(self, *tensors: torch.Tensor):
+        self.tensors, self.stream = tensors, torch.cuda.current_stream()
+
+    def take(self) -> tuple[torch.Tensor, ...]:
+        """For use on the current stream: their memory, given back on the
+        forward pass's, is not reused before that use has ended."""
+        now = torch.cuda.current_stream()
+        if now != self.stream:
+            for t in self.tensors:
+                t.record_stream(now)
+        return self.tensors
 
 
 class BlockWeight:
@@ -41,12 +73,12 @@ class BlockWeight:
 class _Cast:
     """Row and / or column blocks of a tensor."""
 
-    def __init__(self, x: torch.Tensor, fmt: int, margin: int, row: bool, col: bool, stream=None):
+    def __init__(self, x: torch.Tensor, fmt: int, margin: int, row: bool, col: bool):
         M, K = x.shape
         new = lambda outer, red: (fp8.block_codes(M, K, x.device), fp8.block_scales(outer, red, x.device))  # noqa: E731
         self.q, self.s = new(M, K) if row else (None, None)
         self.q_col, self.s_col = new(K, M) if col else (None, None)
-        fp8.fp8_block_cast(x, fmt, margin, self.q, self.s, self.q_col, self.s_col, stream=stream)
+        fp8.fp8_block_cast(x, fmt, margin, self.q, self.s, self.q_col, self.s_col)
 
 
 class BlockLinear:
@@ -64,30 +96,32 @@ class BlockLinear:
         self.kept = None
 
     def forward(self, x: torch.Tensor, keep: bool = False, stream=None) -> torch.Tensor:
-        y = torch.empty((x.shape[0], self.N), dtype=x.dtype, device=x.device)
-        w = self.weight
-        if not keep and x.shape[0] <= fp8.FP8_BLOCK_TOKENS_MAX:
-            fp8.fp8_block_linear_tokens(x, w.q, w.s, y, bias=self.bias, margin=self.margin, stream=stream)
+        with _on(stream, x):
+            y = torch.empty((x.shape[0], self.N), dtype=x.dtype, device=x.device)
+            w = self.weight
+            if not keep and x.shape[0] <= fp8.FP8_BLOCK_TOKENS_MAX:
+                fp8.fp8_block_linear_tokens(x, w.q, w.s, y, bias=self.bias, margin=self.margin)
+                return y
+            c = _Cast(x, fp8.FP8_E4M3, self.margin, True, keep)
+            fp8.fp8_block_linear_fwd(c.q, c.s, w.q, w.s, y, bias=self.bias)
+            if keep:
+                self.kept = _Kept(c.q_col, c.s_col)
             return y
-        c = _Cast(x, fp8.FP8_E4M3, self.margin, True, keep, stream)
-        fp8.fp8_block_linear_fwd(c.q, c.s, w.q, w.s, y, bias=self.bias, stream=stream)
-        if keep:
-            self.kept = (c.q_col, c.s_col)
-        return y
 
     def backward(self, dy: torch.Tensor, stream=None, rto: bool = False) -> tuple[torch.Tensor, torch.Tensor]:
         """(dx, dw) in dy's dtype (dw bfloat16 rounded to odd with rto, for a
         following FP8 gradient cast).  Uses up what forward kept."""
         if self.kept is None:
             raise RuntimeError("backward needs a forward pass with keep=True")
-        M = dy.shape[0]
-        g = _Cast(dy, self.grad_fmt, self.margin, True, True, stream)
-        dx = torch.empty((M, self.K), dtype=dy.dtype, device=dy.device)
-        dw = torch.empty((self.N, self.K), dtype=torch.bfloat16 if rto else dy.dtype, device=dy.device)
-        fp8.fp8_block_linear_dgrad(g.q, g.s, self.grad_fmt, self.weight.q, self.weight.s_col, dx, stream=stream)
-        fp8.fp8_block_linear_wgrad(g.q_col, g.s_col, self.grad_fmt, *self.kept, dw, stream=stream, rto=rto)
-        self.kept = None
-        return dx, dw
+        with _on(stream, dy):
+            M = dy.shape[0]
+            g = _Cast(dy, self.grad_fmt, self.margin, True, True)
+            dx = torch.empty((M, self.K), dtype=dy.dtype, device=dy.device)
+            dw = torch.empty((self.N, self.K), dtype=torch.bfloat16 if rto else dy.dtype, device=dy.device)
+            fp8.fp8_block_linear_dgrad(g.q, g.s, self.grad_fmt, self.weight.q, self.weight.s_col, dx)
+            fp8.fp8_block_linear_wgrad(g.q_col, g.s_col, self.grad_fmt, *self.kept.take(), dw, rto=rto)
+            self.kept = None
+            return dx, dw
 
 
 class BlockMLP:
@@ -107,39 +141,41 @@ class BlockMLP:
         self.kept = None
 
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
-        M, dev = x.shape[0], x.device
-        c = _Cast(x, fp8.FP8_E4M3, self.margin, True, True, stream)
-        h = torch.empty((M, self.F), dtype=x.dtype, device=dev)
-        fp8.fp8_block_linear_fwd(c.q, c.s, self.w1.q, self.w1.s, h, stream=stream)
-        ck, ck_s = fp8.block_codes(M, self.F, dev), fp8.block_scales(M, self.F, dev)
-        aq, a_s = fp8.block_codes(M, self.F, dev), fp8.block_scales(M, self.F, dev)
-        fp8.fp8_act_fwd(h, self.act, self.margin, ck, ck_s, aq, a_s, stream=stream)
-        y = torch.empty((M, self.N), dtype=x.dtype, device=dev)
-        fp8.fp8_block_linear_fwd(aq, a_s, self.w2.q, self.w2.s, y, stream=stream)
-        self.kept = (c.q_col, c.s_col, ck, ck_s)
-        return y
+        with _on(stream, x):
+            M, dev = x.shape[0], x.device
+            c = _Cast(x, fp8.FP8_E4M3, self.margin, True, True)
+            h = torch.empty((M, self.F), dtype=x.dtype, device=dev)
+            fp8.fp8_block_linear_fwd(c.q, c.s, self.w1.q, self.w1.s, h)
+            ck, ck_s = fp8.block_codes(M, self.F, dev), fp8.block_scales(M, self.F, dev)
+            aq, a_s = fp8.block_codes(M, self.F, dev), fp8.block_scales(M, self.F, dev)
+            fp8.fp8_act_fwd(h, self.act, self.margin, ck, ck_s, aq, a_s)
+            y = torch.empty((M, self.N), dtype=x.dtype, device=dev)
+            fp8.fp8_block_linear_fwd(aq, a_s, self.w2.q, self.w2.s, y)
+            self.kept = _Kept(c.q_col, c.s_col, ck, ck_s)
+            return y
 
     def kept_bytes(self) -> int:
         """Bytes that the forward pass keeps for the backward pass."""
-        return 0 if self.kept is None else sum(t.untyped_storage().nbytes() for t in self.kept)
+        return 0 if self.kept is None else sum(t.untyped_storage().nbytes() for t in self.kept.tensors)
 
     def backward(self, dy: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """(dx, dw1, dw2) in dy's dtype.  Uses up what forward kept."""
         if self.kept is None:
             raise RuntimeError("backward needs a forward pass")
-        xq, xs, ck, ck_s = self.kept
-        M, dev, fmt = dy.shape[0], dy.device, self.grad_fmt
-        new = lambda *shape: torch.empty(shape, dtype=dy.dtype, device=dev)  # noqa: E731
-        g = _Cast(dy, fmt, self.margin, True, True, stream)
-        da = new(M, self.F)
-        fp8.fp8_block_linear_dgrad(g.q, g.s, fmt, self.w2.q, self.w2.s_col, da, stream=stream)
-        dhq, dhs = fp8.block_codes(M, self.F, dev), fp8.block_scales(M, self.F, dev)
-        dhq_c, dhs_c = fp8.block_codes(M, self.F, dev), fp8.block_scales(self.F, M, dev)
-        aq_c, as_c = fp8.block_codes(M, self.F, dev), fp8.block_scales(self.F, M, dev)
-        fp8.fp8_act_bwd(ck, ck_s, da, self.act, fmt, self.margin, dhq, dhs, dhq_c, dhs_c, aq_c, as_c, stream=stream)
-        dw2, dx, dw1 = new(self.N, self.F), new(M, self.K), new(self.F, self.K)
-        fp8.fp8_block_linear_wgrad(g.q_col, g.s_col, fmt, aq_c, as_c, dw2, stream=stream)
-        fp8.fp8_block_linear_dgrad(dhq, dhs, fmt, self.w1.q, self.w1.s_col, dx, stream=stream)
-        fp8.fp8_block_linear_wgrad(dhq_c, dhs_c, fmt, xq, xs, dw1, stream=stream)
-        self.kept = None
-        return dx, dw1, dw2
+        with _on(stream, dy):
+            xq, xs, ck, ck_s = self.kept.take()
+            M, dev, fmt = dy.shape[0], dy.device, self.grad_fmt
+            new = lambda *shape: torch.empty(shape, dtype=dy.dtype, device=dev)  # noqa: E731
+            g = _Cast(dy, fmt, self.margin, True, True)
+            da = new(M, self.F)
+            fp8.fp8_block_linear_dgrad(g.q, g.s, fmt, self.w2.q, self.w2.s_col, da)
+            dhq, dhs = fp8.block_codes(M, self.F, dev), fp8.block_scales(M, self.F, dev)
+            dhq_c, dhs_c = fp8.block_codes(M, self.F, dev), fp8.block_scales(self.F, M, dev)
+            aq_c, as_c = fp8.block_codes(M, self.F, dev), fp8.block_scales(self.F, M, dev)
+            fp8.fp8_act_bwd(ck, ck_s, da, self.act, fmt, self.margin, dhq, dhs, dhq_c, dhs_c, aq_c, as_c)
+            dw2, dx, dw1 = new(self.N, self.F), new(M, self.K), new(self.F, self.K)
+            fp8.fp8_block_linear_wgrad(g.q_col, g.s_col, fmt, aq_c, as_c, dw2)
+            fp8.fp8_block_linear_dgrad(dhq, dhs, fmt, self.w1.q, self.w1.s_col, dx)
+            fp8.fp8_block_linear_wgrad(dhq_c, dhs_c, fmt, xq, xs, dw1)
+            self.kept = None
+            return dx, dw1, dw2

@@ -281,7 +281,11 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
 // dgrad, both in wgrad).  Ring stage: A 16 KB, B bn x 128 B; scales of both
 // (1 KB) with every fourth block.
 constexpr int kSfSlot = 1024;
-constexpr int kFewSmemBytes = 112 * 1024;  // at most: two CTAs per SM
+// At most: two CTAs per SM, whose 256 columns of tensor memory each fit it.  The
+// library's other kernels that allocate tensor memory need more shared memory
+// than is left beside one (at least 89 KB are used), so that no CTA of a cluster
+// waits for tensor memory while another holds some.
+constexpr int kFewSmemBytes = 112 * 1024;
 
 template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads)

@@ -561,6 +561,10 @@ int fp8_selftest_encode(int fmt, unsigned lo_bits, unsigned long long hi_bits, u
  * High-precision matrices have rows `ld` elements apart (ld at least the row's
  * length) and may start at any element; rows that start on 16-byte boundaries
  * are read and written with wide accesses.
+ *
+ * Outputs must not overlap inputs or one another, with two exceptions:
+ * fp8_act_fwd's a may be h, and fp8_act_bwd's dh may be da (the same pointer
+ * and row stride).
  */
 typedef struct {
   uint8_t *q;  /* dev: codes */

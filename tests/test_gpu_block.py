@@ -7,6 +7,10 @@ binary32; `red + 32` additions, each off by at most one unit (2^-23, as it may
 truncate) of a partial sum that is at most sum |a b|, then the bias add and the
 rounding to the output type.  Activations: stated at `_act_tolerance`.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -737,6 +741,103 @@ def test_block_mlp_gradients(kind):
         assert np.linalg.norm(f64(got) - ref) <= 0.005 * np.linalg.norm(ref), name
     with pytest.raises(RuntimeError):
         mlp.backward(dy)
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_modules_on_another_stream(given):
+    """A pass on a busy side stream while the current one reuses whatever
+    memory its temporaries and kept tensors would have given back to it."""
+    M, K, F = 200, 264, 520
+    x, dy = (synth.device_normal((M, n), 1.0, 40 + n, BF16, "cuda") for n in (K, F))
+    w1, w2 = (synth.device_normal(s, 0.02, 50 + s[0], BF16, "cuda") for s in ((F, K), (K, F)))
+    lin, mlp = BlockLinear(w1), BlockMLP(w1, w2, fp8.FP8_ACT_SILU)
+    dz = synth.device_normal((M, K), 1.0, 60, BF16, "cuda")
+
+    def passes(side=None):
+        out = []
+
+        def there(f, *a, **k):  # f on the side stream, behind a wait there; then memory is taken and filled here
+            if side is None:
+                return f(*a, **k)
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+            if given:
+                r = f(*a, **k, stream=side)
+            else:
+                with torch.cuda.stream(side):
+                    r = f(*a, **k)
+            for n in (M * K, M * F, M * 384, M * 640, 2 * M * F, 4096, 5120):
+                for _ in range(4):
+                    torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x55)
+            return r
+
+        out.append(there(lin.forward, x, keep=True))
+        out += there(lin.backward, dy)
+        out.append(there(lin.forward, x[:9]))
+        out.append(there(mlp.forward, x))
+        out += there(mlp.backward, dz)
+        out.append(mlp.forward(x))  # kept here, used there
+        out += there(mlp.backward, dz)
+        torch.cuda.synchronize()
+        return out
+
+    for got, want in zip(passes(torch.cuda.Stream()), passes(), strict=True):
+        assert torch.equal(got, want)
+    assert fp8.fp8_get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(500, 2056), (129, 257), (2100, 4100)])
+def test_activation_in_place(shape, dtype):
+    R, C = shape
+    h, da = (synth.device_normal(shape, s, 70 + i, dtype, "cuda") for i, s in enumerate((2.0, 1.0)))
+    q, s = fp8.block_codes(R, C), fp8.block_scales(R, C)
+    q2, s2 = fp8.block_codes(R, C), fp8.block_scales(R, C)
+    a, dh = torch.empty_like(h), torch.empty_like(da)
+    fp8.fp8_act_fwd(h, fp8.FP8_ACT_GELU_TANH, 0, q, s, a=a)
+    fp8.fp8_act_bwd(q, s, da, fp8.FP8_ACT_GELU_TANH, dh=dh)
+    fp8.fp8_act_fwd(h, fp8.FP8_ACT_GELU_TANH, 0, q2, s2, a=h)
+    fp8.fp8_act_bwd(q2, s2, da, fp8.FP8_ACT_GELU_TANH, dh=da)
+    assert torch.equal(h, a) and torch.equal(da, dh) and torch.equal(q, q2) and torch.equal(s, s2)
+
+
+def test_first_calls_of_a_process_captured():
+    """No call of the library before the capture: what it sets up once per
+    device is set up then."""
+    code = """
+import torch
+from fp8_mixed_precision_tensor_b200 import fp8
+C, S = fp8.block_codes, fp8.block_scales
+x = torch.randn(200, 300, device="cuda").to(torch.bfloat16)
+w = torch.randn(260, 300, device="cuda").to(torch.bfloat16)
+b = [C(200, 300), S(200, 300), C(260, 300), S(260, 300), S(300, 260)]
+y = torch.zeros(200, 260, device="cuda", dtype=torch.bfloat16)
+t, z = torch.zeros_like(y), torch.zeros_like(y)
+ck, cs = C(200, 260), S(200, 260)
+def work():
+    fp8.fp8_block_cast(x, 0, 0, b[0], b[1])
+    fp8.fp8_block_cast_square(w, 0, 0, b[2], b[3], b[4])
+    fp8.fp8_block_linear_fwd(b[0], b[1], b[2], b[3], y)
+    fp8.fp8_block_linear_tokens(x[:7], b[2], b[3], t[:7])
+    fp8.fp8_act_fwd(y, 2, 0, ck, cs)
+    fp8.fp8_act_bwd(ck, cs, y, 2, dh=z)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    work()
+g.replay()
+torch.cuda.synchronize()
+got = [v.clone() for v in (y, t, z)]
+work()
+torch.cuda.synchronize()
+assert all(torch.equal(u, v) for u, v in zip(got, (y, t, z))) and float(y.abs().sum()) > 0
+assert fp8.fp8_get_status() == 0
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
 
 
 def test_block_wgrad_feeds_the_adam_step():
