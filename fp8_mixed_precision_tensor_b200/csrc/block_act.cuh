@@ -108,21 +108,29 @@ __device__ __forceinline__ float2 act_grad2(float2 h, float2 r, float2 da) {
   return make_float2(side.x > 0.0f ? up.x : down.x, side.y > 0.0f ? up.y : down.y);
 }
 
-// The activation kernels work on slabs of RP rows per thread, 32 * RP rows: whole
-// tiles (RP = 4), or, where there are no more tiles than SMs and no block runs
-// along the rows, quarters of them.  A CTA then runs its code once, and the code
-// of one row per thread is a quarter as long to fetch (500 x 2056 float32:
-// forward 7.0 and 2.9 us, backward 7.1 and 3.3; 1024 x 2048 bfloat16: 5.0 and
-// 4.3, 6.3 and 4.4; 2048 x 4096: 9.8 and 13.5, 11.6 and 12.1).  (With blocks
-// along the rows, tiles of 1024 threads with two rows each gained nothing.)
+// The kernels without blocks along the rows need nothing of a tile but its
+// rows.  Their CTAs take a part of one.  RP rows per thread, 4 or 2: 128 threads
+// of the 128 * 16 / RP that a whole tile would have; CTAs this small leave and
+// are replaced one by one (4096 x 16384 bfloat16: forward 70 and 62 us in CTAs
+// of 512 and 128 threads, with codes 71 and 60).  RP = 1, 512 threads with a row
+// each, where there are no more tiles than SMs: a CTA then runs its code once,
+// and a quarter of it is fetched sooner (500 x 2056 float32: forward 7.0 and 2.9
+// us, backward 7.1 and 3.3).
 constexpr int kActThreads = 512;
-constexpr int kActStep = kActThreads / 16;  // rows between a thread's rows
+constexpr int kActStep = kActThreads / 16;  // rows between a thread's rows where a CTA has a whole tile
 template <int RP>
-constexpr int kSlabRows = kActStep * RP;
+constexpr int kPartThreads = RP == 1 ? 512 : 128;
 template <int RP>
-__device__ __forceinline__ TileAt slab_at(unsigned t, unsigned tiles_c) {
-  const unsigned r = t / tiles_c;
-  return {(int)(r * kSlabRows<RP>), (int)((t - r * tiles_c) * kTile)};
+constexpr int kParts = RP == 2 ? 8 : 4;  // of a tile
+template <int RP>
+__device__ __forceinline__ TileAt part_at(unsigned t, unsigned tiles_c) {
+  if constexpr (RP == 1) {
+    const unsigned r = t / tiles_c;
+    return {(int)(r * 32), (int)((t - r * tiles_c) * kTile)};
+  }
+  TileAt at = tile_at(t / kParts<RP>, tiles_c);
+  at.row0 += (int)(t % kParts<RP>) * 8;
+  return at;
 }
 
 struct ActFwd {
@@ -140,17 +148,17 @@ struct ActFwd {
 };
 
 // h is read once (2 B at 16 bits), one or two code bytes and / or a are written;
-// 64 % of the issue slots, 38 % of the DRAM cycles: 4096 x 16384 bfloat16 with a
-// itself 71 us (4.7 TB/s), with its codes 73 to 88.  512 threads with four rows each: act(h) of a thread's 32
+// 4096 x 16384 bfloat16 with a itself 62 us (5.4 TB/s), with its codes 60, bound
+// by the issue slots.  Four rows per thread: act(h) of a thread's 32
 // elements waits in registers for its rows' amaxes (eight rows each needed
 // 184 registers and ran at a third of the occupancy).
 template <int DT, int ACT, int RP>
-__global__ void __launch_bounds__(kActThreads, 2) k_act_fwd(const ActFwd p) {
+__global__ void __launch_bounds__(kPartThreads<RP>, 1024 / kPartThreads<RP>) k_act_fwd(const ActFwd p) {
   pdl_launch_dependents();
   pdl_wait();
   const int tiles_c = (p.cols + kTile - 1) / kTile;
   {
-    const auto [row0, col0] = slab_at<RP>(blockIdx.x, tiles_c);
+    const auto [row0, col0] = part_at<RP>(blockIdx.x, tiles_c);
     Raw8<DT> raw[RP];
     load_tile<DT>(p.h, p.ldh, p.vec_h, row0, col0, p.rows, p.cols, raw);
     cast_raw_rows<DT, FP8_E4M3>(raw, p.cq, p.cs, p.ldc, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
@@ -198,41 +206,83 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, int byte
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
+// dh alone: parts of tiles, as k_act_fwd.  float32 with two rows per thread and
+// ten CTAs per SM, 16-bit types with four and eight: 4096 x 16384 float32 91 us
+// (6.6 TB/s; four rows 101, a persistent CTA of 512 threads 139), bfloat16 72
+// (4.7; two rows 76, persistent 72).
+template <int DT>
+constexpr int kPlainRows = DT == FP8_DT_F32 ? 2 : 4;
+template <int DT, int ACT, int RP>
+__global__ void __launch_bounds__(kPartThreads<RP>, (RP == 2 ? 1280 : 1024) / kPartThreads<RP>)
+    k_act_bwd_plain(const ActBwd p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tiles_c = (p.cols + kTile - 1) / kTile, kg = (tiles_c + 3) / 4;
+  const auto [row0, col0] = part_at<RP>(blockIdx.x, tiles_c);
+  const int col = col0 + (threadIdx.x & 15) * 8, row = row0 + (threadIdx.x >> 4);
+  Raw8<DT> raw[RP];
+  uint2 q[RP];
+  uint32_t sb[RP];
+  if (row0 + kTile <= p.rows && col0 + kTile <= p.cols) {  // inside: nothing to clamp, all loads in flight at once
+    const uint8_t *c = p.cq + (size_t)row * p.ldc + col;
+#pragma unroll
+    for (int i = 0; i < RP; i++, c += Geo<RP>::kStep * p.ldc) q[i] = __ldcs(reinterpret_cast<const uint2 *>(c));
+  } else {
+#pragma unroll
+    for (int i = 0; i < RP; i++) q[i] = load_codes8(p.cq, p.ldc, row + Geo<RP>::kStep * i, col, p.rows, p.cols);
+  }
+#pragma unroll
+  for (int i = 0; i < RP; i++) sb[i] = p.cs[scale_at(min(row + Geo<RP>::kStep * i, p.rows - 1), col0 / kTile, kg)];
+  load_tile<DT>(p.da, p.ldda, p.vec_da, row0, col0, p.rows, p.cols, raw);
+  float d[RP][8];
+#pragma unroll
+  for (int i = 0; i < RP; i++) {
+    float a[8];
+    decode8<FP8_E4M3>(q[i], a);
+    unpack8<DT>(raw[i], d[i]);
+    const float s = descale_of(sb[i]);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 h = __fmul2_rn(make_float2(a[j], a[j + 1]), both(s));
+      float2 y, v, r;
+      gate2<ACT, true>(h, y, v, r);
+      const float2 g = act_grad2(h, r, make_float2(d[i][j], d[i][j + 1]));
+      d[i][j] = g.x;
+      d[i][j + 1] = g.y;
+    }
+  }
+  store_tile<DT>(p.vec_dh, p.dh_hp, p.lddh, row0, col0, p.rows, p.cols, d);
+}
+
 // Shared memory of k_act_bwd: two buffers of a tile's codes and da, each
 // thread's own elements at its own places, so that a thread waits for its own
 // copies only.
-template <int DT, int RP>
+template <int DT>
 struct ActBwdSmem {
-  static constexpr int kCodeBytes = kSlabRows<RP> * kTile;
+  static constexpr int kCodeBytes = kTile * kTile;
   static constexpr int kBuffer = kCodeBytes * (DT == FP8_DT_F32 ? 5 : 3);
   static constexpr int kBytes = 2 * kBuffer;
 };
 
-// One pass over 128x128 tiles: 1 + 2 B read, up to 3 code bytes (or 2 B of dh)
+// One pass over 128x128 tiles: 1 + 2 B read, up to 3 code bytes (and 2 B of dh)
 // written.  dh and act(h') of a thread's 32 elements stay in registers between
 // the amaxes and the encoding, which leaves room for one CTA of 16 warps per
-// SM (two where only a bfloat16 dh is wanted); the next tile's inputs are copied into
-// shared memory meanwhile.  Bound by instruction issue as much as by HBM (63 %
-// of the slots, 33 % of the DRAM cycles): 4096 x 16384 bfloat16 to dh itself 73
-// us (4.6 TB/s), to the codes of all three 130 to 158.
-// OUT: the format of dh's codes, or kActPlain where no codes are wanted.
-constexpr int kActPlain = -1;
-template <int DT, int RP, int OUT>
-constexpr int kActBwdPerSm = OUT == kActPlain && (DT == FP8_DT_BF16 || RP == 1) ? 2 : 1;
-template <int DT, int ACT, int OUT, int RP>
-__global__ void __launch_bounds__(kActThreads, kActBwdPerSm<DT, RP, OUT>) k_act_bwd(const ActBwd p) {
+// SM; the next tile's inputs are copied into shared memory meanwhile.  Bound by
+// instruction issue as much as by HBM (63 % of the slots, 33 % of the DRAM
+// cycles): 4096 x 16384 bfloat16 to the codes of all three 130 to 158 us.
+// OUT: the format of dh's codes.
+template <int DT, int ACT, int OUT>
+__global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int kVecs = Raw8<DT>::kWords / 4;
-  using Smem = ActBwdSmem<DT, RP>;
+  constexpr int RP = 4, kVecs = Raw8<DT>::kWords / 4;
+  using Smem = ActBwdSmem<DT>;
   extern __shared__ __align__(16) uint8_t act_smem[];
-  constexpr bool kCodes = OUT != kActPlain;
-  constexpr int GFMT = kCodes ? OUT : FP8_E5M2;
-  __shared__ ColScratch<4> sc[kCodes ? 2 : 1];
+  __shared__ ColScratch<RP> sc[2];
   const int tiles_c = (p.cols + kTile - 1) / kTile;
-  const unsigned tiles = (unsigned)((p.rows + kSlabRows<RP> - 1) / kSlabRows<RP>) * (unsigned)tiles_c;
+  const unsigned tiles = (unsigned)((p.rows + kTile - 1) / kTile) * (unsigned)tiles_c;
   const int kg = (tiles_c + 3) / 4;
-  const float gmax = GFMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
+  const float gmax = OUT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
   const int c8 = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   const uint32_t smem = smem_u32(act_smem);
   uint32_t sb[RP];  // scale bytes of the tile in the buffer
@@ -270,7 +320,7 @@ __global__ void __launch_bounds__(kActThreads, kActBwdPerSm<DT, RP, OUT>) k_act_
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  TileAt next = slab_at<RP>(blockIdx.x, tiles_c);  // (the grid has at most one CTA per tile)
+  TileAt next = tile_at(blockIdx.x, tiles_c);  // (the grid has at most one CTA per tile)
   prefetch(next, 0);
   int buf = 0;
   for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x, buf ^= 1) {
@@ -280,7 +330,7 @@ __global__ void __launch_bounds__(kActThreads, kActBwdPerSm<DT, RP, OUT>) k_act_
     for (int i = 0; i < RP; i++)
       sb[i] = p.cs[scale_at(min(row0 + r0 + kActStep * i, p.rows - 1), col0 / kTile, kg)];
     if (t + gridDim.x < tiles) {
-      next = slab_at<RP>(t + gridDim.x, tiles_c);
+      next = tile_at(t + gridDim.x, tiles_c);
       prefetch(next, buf ^ 1);
     } else asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -317,31 +367,27 @@ __global__ void __launch_bounds__(kActThreads, kActBwdPerSm<DT, RP, OUT>) k_act_
         const float2 g = act_grad2(h, r, make_float2(d[i][j], d[i][j + 1]));
         d[i][j] = g.x;
         d[i][j + 1] = g.y;
-        if constexpr (kCodes) {
-          const float2 v = act_value2(h, y, q);
-          a[i][j] = v.x;
-          a[i][j + 1] = v.y;
-        }
+        const float2 v = act_value2(h, y, q);
+        a[i][j] = v.x;
+        a[i][j + 1] = v.y;
       }
     }
     if (p.dh_hp) store_tile<DT>(p.vec_dh, p.dh_hp, p.lddh, row0, col0, p.rows, p.cols, d);
-    if constexpr (kCodes) {
-      // the two column reductions share their barriers
-      const bool dcols = p.dh.qt != nullptr, acols = p.aqt != nullptr;
-      if (dcols) put_tile_maxima(d, sc[0]);
-      if (acols) put_tile_maxima(a, sc[1]);
-      if (p.dh.q) cast_tile_rows<GFMT>(d, p.dh.q, p.dh.s, p.dh.ldq, row0, col0, p.rows, p.cols, gmax, p.margin);
-      if (dcols || acols) {
-        __syncthreads();
-        bool bad = false;
-        const int c = threadIdx.x & (kTile - 1);
-        if (dcols && threadIdx.x < kTile) bad = finish_column(sc[0], c, p.dh.st, row0, col0, p.rows, gmax, p.margin);
-        if (acols && threadIdx.x / kTile == 1)
-          bad = finish_column(sc[1], c, p.ast, row0, col0, p.rows, kMaxE4M3, p.margin);
-        bad = __syncthreads_or(bad);
-        if (dcols) store_tile_cols<GFMT>(d, sc[0], bad, p.dh.qt, p.dh.ldqt, row0, col0, p.rows, p.cols);
-        if (acols) store_tile_cols<FP8_E4M3>(a, sc[1], bad, p.aqt, p.ldaqt, row0, col0, p.rows, p.cols);
-      }
+    // the two column reductions share their barriers
+    const bool dcols = p.dh.qt != nullptr, acols = p.aqt != nullptr;
+    if (dcols) put_tile_maxima(d, sc[0]);
+    if (acols) put_tile_maxima(a, sc[1]);
+    if (p.dh.q) cast_tile_rows<OUT>(d, p.dh.q, p.dh.s, p.dh.ldq, row0, col0, p.rows, p.cols, gmax, p.margin);
+    if (dcols || acols) {
+      __syncthreads();
+      bool bad = false;
+      const int c = threadIdx.x & (kTile - 1);
+      if (dcols && threadIdx.x < kTile) bad = finish_column(sc[0], c, p.dh.st, row0, col0, p.rows, gmax, p.margin);
+      if (acols && threadIdx.x / kTile == 1)
+        bad = finish_column(sc[1], c, p.ast, row0, col0, p.rows, kMaxE4M3, p.margin);
+      bad = __syncthreads_or(bad);
+      if (dcols) store_tile_cols<OUT>(d, sc[0], bad, p.dh.qt, p.dh.ldqt, row0, col0, p.rows, p.cols);
+      if (acols) store_tile_cols<FP8_E4M3>(a, sc[1], bad, p.aqt, p.ldaqt, row0, col0, p.rows, p.cols);
     }
   }
 }

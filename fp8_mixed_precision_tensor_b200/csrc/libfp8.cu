@@ -863,6 +863,13 @@ unsigned tile_grid(int rows, int cols) {
 // Whether an elementwise kernel takes its form for few tiles: one CTA or less per SM.
 bool few_tiles_of(unsigned tiles, int sms) { return tiles != 0 && tiles <= (unsigned)sms; }
 
+// An activation kernel whose CTAs take parts of tiles.
+template <int RP, typename P>
+int launch_parts(void (*kernel)(P), unsigned tiles, cudaStream_t stream, const P &p) {
+  constexpr unsigned parts = block::kParts<RP>;
+  return launch_pdl(kernel, tiles <= 0x7fffffffu / parts ? tiles * parts : 0u, block::kPartThreads<RP>, 0, stream, 1, p);
+}
+
 block::CastOut cast_out(const fp8_blocks *row, const fp8_blocks *col) {
   block::CastOut o = {};
   if (row) { o.q = row->q; o.s = row->s; o.ldq = row->ld; }
@@ -1315,8 +1322,8 @@ int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int ac
     with_act(act, [&](auto f) {
       constexpr int DT = decltype(dt)::value, ACT = decltype(f)::value;
       const unsigned tiles = tile_grid(rows, cols);
-      if (few_tiles_of(tiles, d->sms)) rc = launch_pdl(block::k_act_fwd<DT, ACT, 1>, tiles * 4, block::kActThreads, 0, s, 1, p);
-      else rc = launch_pdl(block::k_act_fwd<DT, ACT, 4>, tiles, block::kActThreads, 0, s, 1, p);
+      if (few_tiles_of(tiles, d->sms)) rc = launch_parts<1>(block::k_act_fwd<DT, ACT, 1>, tiles, s, p);
+      else rc = launch_parts<4>(block::k_act_fwd<DT, ACT, 4>, tiles, s, p);
     });
   });
   return rc;
@@ -1348,21 +1355,19 @@ int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int
   with_dtype(dtype, [&](auto dt) {
     with_act(act, [&](auto f) {
       constexpr int DT = decltype(dt)::value, ACT = decltype(f)::value;
-      auto go = [&](auto out, auto rows_per_thread) {
-        constexpr int OUT = decltype(out)::value, RP = decltype(rows_per_thread)::value;
-        const auto kernel = block::k_act_bwd<DT, ACT, OUT, RP>;
-        constexpr int smem = block::ActBwdSmem<DT, RP>::kBytes;
-        if ((rc = set_smem(kernel, smem))) return;
-        const unsigned cap = (unsigned)(d->sms * block::kActBwdPerSm<DT, RP, OUT>);  // resident CTAs
-        const unsigned slabs = RP == 1 ? (rows + 31) / 32u * ((cols + 127) / 128u) : tiles;
-        rc = launch_pdl(kernel, slabs < cap ? slabs : cap, block::kActThreads, smem, s, 1, p);
-      };
-      using Plain = std::integral_constant<int, block::kActPlain>;
-      using One = std::integral_constant<int, 1>;
-      using Four = std::integral_constant<int, 4>;
-      if (dh_row || dh_col || a_col) with_fmt(fmt, [&](auto out) { go(out, Four()); });
-      else if (few_tiles_of(tiles, d->sms)) go(Plain(), One());
-      else go(Plain(), Four());
+      if (dh_row || dh_col || a_col) {
+        with_fmt(fmt, [&](auto out) {
+          const auto kernel = block::k_act_bwd<DT, ACT, decltype(out)::value>;
+          constexpr int smem = block::ActBwdSmem<DT>::kBytes;
+          if ((rc = set_smem(kernel, smem))) return;
+          const unsigned cap = (unsigned)d->sms;  // resident CTAs
+          rc = launch_pdl(kernel, tiles < cap ? tiles : cap, block::kActThreads, smem, s, 1, p);
+        });
+        return;
+      }
+      constexpr int RP = block::kPlainRows<DT>;
+      if (few_tiles_of(tiles, d->sms)) rc = launch_parts<1>(block::k_act_bwd_plain<DT, ACT, 1>, tiles, s, p);
+      else rc = launch_parts<RP>(block::k_act_bwd_plain<DT, ACT, RP>, tiles, s, p);
     });
   });
   return rc;
