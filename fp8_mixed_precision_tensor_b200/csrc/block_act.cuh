@@ -108,30 +108,8 @@ __device__ __forceinline__ float2 act_grad2(float2 h, float2 r, float2 da) {
   return make_float2(side.x > 0.0f ? up.x : down.x, side.y > 0.0f ? up.y : down.y);
 }
 
-// The kernels without blocks along the rows need nothing of a tile but its
-// rows.  Their CTAs take a part of one.  RP rows per thread, 4 or 2: 128 threads
-// of the 128 * 16 / RP that a whole tile would have; CTAs this small leave and
-// are replaced one by one (4096 x 16384 bfloat16: forward 70 and 62 us in CTAs
-// of 512 and 128 threads, with codes 71 and 60).  RP = 1, 512 threads with a row
-// each, where there are no more tiles than SMs: a CTA then runs its code once,
-// and a quarter of it is fetched sooner (500 x 2056 float32: forward 7.0 and 2.9
-// us, backward 7.1 and 3.3).
-constexpr int kActThreads = 512;
-constexpr int kActStep = kActThreads / 16;  // rows between a thread's rows where a CTA has a whole tile
-template <int RP>
-constexpr int kPartThreads = RP == 1 ? 512 : 128;
-template <int RP>
-constexpr int kParts = RP == 2 ? 8 : 4;  // of a tile
-template <int RP>
-__device__ __forceinline__ TileAt part_at(unsigned t, unsigned tiles_c) {
-  if constexpr (RP == 1) {
-    const unsigned r = t / tiles_c;
-    return {(int)(r * 32), (int)((t - r * tiles_c) * kTile)};
-  }
-  TileAt at = tile_at(t / kParts<RP>, tiles_c);
-  at.row0 += (int)(t % kParts<RP>) * 8;
-  return at;
-}
+constexpr int kActThreads = 512;            // k_act_bwd
+constexpr int kActStep = kActThreads / 16;  // rows between a thread's rows
 
 struct ActFwd {
   const void *h;

@@ -514,12 +514,51 @@ __device__ __forceinline__ void cast_raw_rows(const Raw8<DT> (&raw)[RP], uint8_t
   store_raw_rows<DT, FMT>(raw, sc, nan, q, ldq, row0, col0 + (threadIdx.x & 15) * 8, rows, cols);
 }
 
-// Cast of x [rows, cols] to 1x128 blocks and / or 128x1 blocks, x read once.
+// The kernels without blocks along the rows need nothing of a tile but its
+// rows.  Their CTAs take a part of one.  RP rows per thread, 4 or 2: 128 threads
+// of the 128 * 16 / RP that a whole tile would have; CTAs this small leave and
+// are replaced one by one (4096 x 16384 bfloat16: forward 70 and 62 us in CTAs
+// of 512 and 128 threads, with codes 71 and 60).  RP = 1, 512 threads with a row
+// each, where there are no more tiles than SMs: a CTA then runs its code once,
+// and a quarter of it is fetched sooner (500 x 2056 float32: forward 7.0 and 2.9
+// us, backward 7.1 and 3.3).
+template <int RP>
+constexpr int kPartThreads = RP == 1 ? 512 : 128;
+template <int RP>
+constexpr int kParts = RP == 2 ? 8 : 4;  // of a tile
+template <int RP>
+__device__ __forceinline__ TileAt part_at(unsigned t, unsigned tiles_c) {
+  if constexpr (RP == 1) {
+    const unsigned r = t / tiles_c;
+    return {(int)(r * 32), (int)((t - r * tiles_c) * kTile)};
+  }
+  TileAt at = tile_at(t / kParts<RP>, tiles_c);
+  at.row0 += (int)(t % kParts<RP>) * 8;
+  return at;
+}
+
+// Cast of x [rows, cols] to 1x128 blocks, 2 B read and 1 written per 16-bit
+// element: 8192 x 12288 bfloat16 52 us (5.8 TB/s), 4096 x 4096 7.8, 1003 x 4104 3.1
+// (4.4 in CTAs of a whole tile), 256 x 256 1.7 (2.3).
+template <int DT, int FMT, int RP>
+__global__ void __launch_bounds__(kPartThreads<RP>, 1024 / kPartThreads<RP>)
+    k_block_cast_rows(const void *__restrict__ x, int rows, int cols, size_t ldx, int vec, int margin,
+                      const CastOut out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const auto [row0, col0] = part_at<RP>(blockIdx.x, (cols + kTile - 1) / kTile);
+  Raw8<DT> raw[RP];
+  load_tile<DT>(x, ldx, vec, row0, col0, rows, cols, raw);
+  cast_raw_rows<DT, FMT>(raw, out.q, out.s, out.ldq, row0, col0, rows, cols, FMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2,
+                         margin);
+}
+
+// Cast of x to 128x1 blocks and, if wanted, to 1x128 blocks, x read once.
 // Each CTA takes one 128x128 tile: it sits in registers as stored (64
 // elements per thread), a row's amax is reduced over its 16 lanes, a column's
 // over the thread's 8 rows and then through shared memory.  2 B read and 1 B
-// written per direction and 16-bit element; 8192 x 12288 bfloat16 both ways 79
-// to 91 us (5.1 to 4.4 TB/s), one way 57.  Half of the issue slots and half of
+// written per direction and 16-bit element; 8192 x 12288 bfloat16 both ways 71
+// to 91 us (5.7 to 4.4 TB/s).  Half of the issue slots and half of
 // the DRAM cycles are busy: three CTAs hide a tile's latencies only in part.
 // RP = 2 (1024 threads) where there are no more tiles than SMs: a CTA then runs
 // its code once, and a quarter of it is fetched sooner (both ways, 777 x 1305 bfloat16: 6.6 and

@@ -863,11 +863,12 @@ unsigned tile_grid(int rows, int cols) {
 // Whether an elementwise kernel takes its form for few tiles: one CTA or less per SM.
 bool few_tiles_of(unsigned tiles, int sms) { return tiles != 0 && tiles <= (unsigned)sms; }
 
-// An activation kernel whose CTAs take parts of tiles.
-template <int RP, typename P>
-int launch_parts(void (*kernel)(P), unsigned tiles, cudaStream_t stream, const P &p) {
+// A kernel whose CTAs take parts of tiles.
+template <int RP, typename... P, typename... A>
+int launch_parts(void (*kernel)(P...), unsigned tiles, cudaStream_t stream, A... args) {
   constexpr unsigned parts = block::kParts<RP>;
-  return launch_pdl(kernel, tiles <= 0x7fffffffu / parts ? tiles * parts : 0u, block::kPartThreads<RP>, 0, stream, 1, p);
+  return launch_pdl(kernel, tiles <= 0x7fffffffu / parts ? tiles * parts : 0u, block::kPartThreads<RP>, 0, stream, 1,
+                    args...);
 }
 
 block::CastOut cast_out(const fp8_blocks *row, const fp8_blocks *col) {
@@ -1187,7 +1188,12 @@ int fp8_block_cast(const void *x, int dtype, int rows, int cols, size_t ldx, int
     with_fmt(fmt, [&](auto f) {
       constexpr int DT = decltype(dt)::value, FMT = decltype(f)::value;
       const int vec = (int)wide_rows(x, dtype, ldx);
-      if (few_tiles_of(tiles, d->sms))
+      const bool few = few_tiles_of(tiles, d->sms);
+      if (!col && few_tiles_of(2 * tiles, d->sms))  // (1024 x 2048 float32: 3.1 us as single rows, 2.8 as fours)
+        rc = launch_parts<1>(block::k_block_cast_rows<DT, FMT, 1>, tiles, s, x, rows, cols, ldx, vec, margin, o);
+      else if (!col)
+        rc = launch_parts<4>(block::k_block_cast_rows<DT, FMT, 4>, tiles, s, x, rows, cols, ldx, vec, margin, o);
+      else if (few)
         rc = launch_pdl(block::k_block_cast<DT, FMT, 2>, tiles, 1024, 0, s, 1, x, rows, cols, ldx, vec, margin, o);
       else
         rc = launch_pdl(block::k_block_cast<DT, FMT, 8>, tiles, block::kCastThreads, 0, s, 1, x, rows, cols, ldx, vec, margin, o);
