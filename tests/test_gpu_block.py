@@ -337,6 +337,19 @@ def test_output_types_and_pitches(shape, dtype, pad, offset):
     assert bool((buf[rest] == 3.0).all())
 
 
+@pytest.mark.parametrize("bias_dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shape", [(20, 300, 200), (300, 700, 520), (2309, 4871, 200)])
+def test_bias_types(shape, bias_dtype):
+    M, N, K = shape
+    L = Layer(M, N, K)
+    bias = torch.randn(N + 1, device="cuda").to(bias_dtype)[1:]  # (at any element's alignment)
+    ref = L.references(bias)["y"]
+    for dtype in (F32, BF16):
+        y = torch.empty((M, N), device="cuda", dtype=dtype)
+        fp8.fp8_block_linear_fwd(L.xq, L.xs, L.wq, L.ws, y, bias=bias)
+        assert_product(y, ref, (dtype, bias_dtype))
+
+
 def test_products_with_empty_sides():
     bias = torch.randn(40, device="cuda")
     e = torch.empty(0, dtype=torch.uint8, device="cuda")
