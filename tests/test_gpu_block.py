@@ -815,6 +815,39 @@ def test_activation_in_place(shape, dtype):
     assert torch.equal(h, a) and torch.equal(da, dh) and torch.equal(q, q2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("cols", [2304, 2300, 2297])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_many_tiles_as_their_rows_of_tiles(dtype, cols):
+    """The elementwise kernels' forms for many tiles against those for few,
+    which the binary64 tests cover: 128 rows at a time, the same bits."""
+    R, C, S = 1500, fp8.block_codes, fp8.block_scales
+    h, da = (dev(data(R, cols, "tiles", i), dtype) for i in range(2))
+
+    def run(h, da):
+        r = h.shape[0]
+        o = {k: C(r, cols) for k in ("row", "row2", "col", "square", "ck", "aq", "dq", "dqc", "aqc")}
+        o |= {k: S(r, cols) for k in ("row_s", "row2_s", "square_s", "ck_s", "aq_s", "dq_s")}
+        cs = [S(cols, r) for _ in range(4)]
+        o |= {k: torch.empty_like(h) for k in ("a", "dh", "dh2")}
+        fp8.fp8_block_cast(h, fp8.FP8_E4M3, 0, o["row"], o["row_s"])
+        fp8.fp8_block_cast(h, fp8.FP8_E5M2, 0, o["row2"], o["row2_s"], o["col"], cs[0])
+        fp8.fp8_block_cast_square(h, fp8.FP8_E4M3, 0, o["square"], o["square_s"], cs[1])
+        fp8.fp8_act_fwd(h, fp8.FP8_ACT_GELU_TANH, 0, o["ck"], o["ck_s"], o["aq"], o["aq_s"], o["a"])
+        fp8.fp8_act_bwd(o["ck"], o["ck_s"], da, fp8.FP8_ACT_GELU_TANH, dh=o["dh"])
+        fp8.fp8_act_bwd(o["ck"], o["ck_s"], da, fp8.FP8_ACT_GELU_TANH, fp8.FP8_E5M2, 0, o["dq"], o["dq_s"], o["dqc"],
+                        cs[2], o["aqc"], cs[3], o["dh2"])
+        return o
+
+    whole = run(h, da)
+    for r0 in range(0, R, 128):
+        part = run(h[r0:r0 + 128], da[r0:r0 + 128])
+        for k, v in part.items():
+            w = whole[k][r0:r0 + 128] if v.dim() == 2 else whole[k][r0 // 128 * v.numel():][:v.numel()]
+            bits = torch.int32 if v.dtype == F32 else torch.int16 if v.dtype in (BF16, F16) else torch.uint8
+            assert torch.equal(w.view(bits) if v.dim() == 1 else w.contiguous().view(bits), v.contiguous().view(bits)), (k, r0)
+    assert fp8.fp8_get_status() == 0
+
+
 def test_first_calls_of_a_process_captured():
     """No call of the library before the capture: what it sets up once per
     device is set up then."""
