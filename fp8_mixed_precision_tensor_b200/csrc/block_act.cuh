@@ -108,6 +108,19 @@ __device__ __forceinline__ float2 act_grad2(float2 h, float2 r, float2 da) {
   return make_float2(side.x > 0.0f ? up.x : down.x, side.y > 0.0f ? up.y : down.y);
 }
 
+// Adds 0 times a word's elements: stays 0 (of either sign) unless one is an
+// infinity or a NaN.  One FMA per word, on the pipe that is less used here.
+template <int DT>
+__device__ __forceinline__ void add_non_finite(uint32_t &t, uint32_t w) {
+  if constexpr (DT == FP8_DT_F32) asm("fma.rn.f32 %0, %1, 0f00000000, %0;" : "+r"(t) : "r"(w));
+  else if constexpr (DT == FP8_DT_BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(t) : "r"(w), "r"(0u));
+  else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(t) : "r"(w), "r"(0u));
+}
+template <int DT>
+__device__ __forceinline__ bool was_non_finite(uint32_t t) {
+  return (t & (DT == FP8_DT_F32 ? 0x7fffffffu : 0x7fff7fffu)) != 0;
+}
+
 constexpr int kActThreads = 512;            // k_act_bwd
 constexpr int kActStep = kActThreads / 16;  // rows between a thread's rows
 
@@ -184,10 +197,59 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, int byte
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
+// An infinite da (a gradient that overflowed) at h' >= 0: act' is positive
+// there, so dh is da, where act_grad2's da + da r is inf - inf for r < 0.  v is
+// h' or act(h'), which has its sign.
+__device__ __forceinline__ bool stays_infinite(float v, float da) {
+  return fabsf(da) == INFINITY && __float_as_uint(v) <= 0x7f800000u;
+}
+// That for a thread's part of a tile, v its act(h'): a rare path of its own, in
+// which da is read again (dh may take da's place, but not before the tile is
+// stored).  With the search for infinities 2 to 3 % of the pass.
+template <int DT, int RP>
+__device__ __forceinline__ void keep_infinite(const ActBwd &p, int row0, int col0, const float (&v)[RP][8],
+                                              float (&d)[RP][8]) {
+  const int row = row0 + (threadIdx.x >> 4), col = col0 + (threadIdx.x & 15) * 8;
+#pragma unroll
+  for (int i = 0; i < RP; i++) {
+    float da[8];
+    unpack8<DT>(load_raw8_single<DT>(p.da, p.ldda, row + Geo<RP>::kStep * i, col, p.rows, p.cols), da);
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      if (stays_infinite(v[i][j], da[j])) d[i][j] = da[j];
+  }
+}
+
+// dh of a thread whose da is not all finite, row by row and straight to memory
+// (each element is read before it is written: dh may take da's place).
+template <int DT, int ACT, int RP>
+__device__ __forceinline__ void act_bwd_non_finite(const ActBwd &p, int row0, int col0) {
+  const int col = col0 + (threadIdx.x & 15) * 8, kg = ((p.cols + kTile - 1) / kTile + 3) / 4;
+#pragma unroll 1
+  for (int i = 0; i < RP; i++) {
+    const int row = row0 + (threadIdx.x >> 4) + Geo<RP>::kStep * i;
+    if (row >= p.rows) break;
+    float a[8], d[8];
+    unpack8<DT>(load_raw8_single<DT>(p.da, p.ldda, row, col, p.rows, p.cols), d);
+    decode8<FP8_E4M3>(load_codes8(p.cq, p.ldc, row, col, p.rows, p.cols), a);
+    const float s = descale_of(p.cs[scale_at(row, col0 / kTile, kg)]);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 h = __fmul2_rn(make_float2(a[j], a[j + 1]), both(s)), da = make_float2(d[j], d[j + 1]);
+      float2 y, v, r;
+      gate2<ACT, true>(h, y, v, r);
+      const float2 g = act_grad2(h, r, da);
+      d[j] = stays_infinite(h.x, da.x) ? da.x : g.x;
+      d[j + 1] = stays_infinite(h.y, da.y) ? da.y : g.y;
+    }
+    store8<DT>(false, p.dh_hp, p.lddh, row, col, p.rows, p.cols, d);
+  }
+}
+
 // dh alone: parts of tiles, as k_act_fwd.  float32 with two rows per thread and
 // ten CTAs per SM, 16-bit types with four and eight: 4096 x 16384 float32 91 us
-// (6.6 TB/s; four rows 101, a persistent CTA of 512 threads 139), bfloat16 72
-// (4.7; two rows 76, persistent 72).
+// (6.6 TB/s; four rows 101, a persistent CTA of 512 threads 139), bfloat16 73
+// (4.6; two rows 76, persistent 72; without the search for infinities 72).
 template <int DT>
 constexpr int kPlainRows = DT == FP8_DT_F32 ? 2 : 4;
 template <int DT, int ACT, int RP>
@@ -212,10 +274,13 @@ __global__ void __launch_bounds__(kPartThreads<RP>, (RP == 2 ? 1280 : 1024) / kP
 #pragma unroll
   for (int i = 0; i < RP; i++) sb[i] = p.cs[scale_at(min(row + Geo<RP>::kStep * i, p.rows - 1), col0 / kTile, kg)];
   load_tile<DT>(p.da, p.ldda, p.vec_da, row0, col0, p.rows, p.cols, raw);
+  uint32_t odd = 0;
   float d[RP][8];
 #pragma unroll
   for (int i = 0; i < RP; i++) {
     float a[8];
+#pragma unroll
+    for (int j = 0; j < Raw8<DT>::kWords; j++) add_non_finite<DT>(odd, raw[i].w[j]);
     decode8<FP8_E4M3>(q[i], a);
     unpack8<DT>(raw[i], d[i]);
     const float s = descale_of(sb[i]);
@@ -229,7 +294,8 @@ __global__ void __launch_bounds__(kPartThreads<RP>, (RP == 2 ? 1280 : 1024) / kP
       d[i][j + 1] = g.y;
     }
   }
-  store_tile<DT>(p.vec_dh, p.dh_hp, p.lddh, row0, col0, p.rows, p.cols, d);
+  if (was_non_finite<DT>(odd)) act_bwd_non_finite<DT, ACT, RP>(p, row0, col0);
+  else store_tile<DT>(p.vec_dh, p.dh_hp, p.lddh, row0, col0, p.rows, p.cols, d);
 }
 
 // Shared memory of k_act_bwd: two buffers of a tile's codes and da, each
@@ -313,6 +379,7 @@ __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
     } else asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     float a[RP][8], d[RP][8];
+    uint32_t odd = 0;
     if (wide_tile(p.vec_da, col0, p.cols)) {
       const uint8_t *base = act_smem + buf * Smem::kBuffer;
 #pragma unroll
@@ -324,6 +391,8 @@ __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
           *reinterpret_cast<uint4 *>(&raw.w[4 * v]) = *reinterpret_cast<const uint4 *>(
               base + Smem::kCodeBytes + ((i * kVecs + v) * kActThreads + threadIdx.x) * 16);
         unpack8<DT>(raw, d[i]);
+#pragma unroll
+        for (int j = 0; j < Raw8<DT>::kWords; j++) add_non_finite<DT>(odd, raw.w[j]);
       }
     } else {
       Raw8<DT> raw[RP];
@@ -332,6 +401,8 @@ __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
       for (int i = 0; i < RP; i++) {
         decode8<FP8_E4M3>(load_codes8(p.cq, p.ldc, row0 + r0 + kActStep * i, col, p.rows, p.cols), a[i]);
         unpack8<DT>(raw[i], d[i]);
+#pragma unroll
+        for (int j = 0; j < Raw8<DT>::kWords; j++) add_non_finite<DT>(odd, raw[i].w[j]);
       }
     }
 #pragma unroll
@@ -350,6 +421,7 @@ __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {
         a[i][j + 1] = v.y;
       }
     }
+    if (was_non_finite<DT>(odd)) keep_infinite<DT>(p, row0, col0, a, d);
     if (p.dh_hp) store_tile<DT>(p.vec_dh, p.dh_hp, p.lddh, row0, col0, p.rows, p.cols, d);
     // the two column reductions share their barriers
     const bool dcols = p.dh.qt != nullptr, acols = p.aqt != nullptr;

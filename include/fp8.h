@@ -655,7 +655,8 @@ int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int ac
  * 1x128 / 128x1 blocks (the operands of dgrad / wgrad), and dh in dtype; and
  * a_col, E4M3 codes of the 128x1 blocks of act(h') (the following layer's
  * wgrad operand, which the forward pass then need not keep).  Outputs not
- * wanted are NULL (not all).  Codes are cast from the binary32 values.
+ * wanted are NULL (not all).  Codes are cast from the binary32 values.  An
+ * infinite da gives an infinite dh (of da's sign where act' > 0), a NaN a NaN.
  */
 int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int cols, size_t ldda, int act, int fmt,
                 int margin, const fp8_blocks *dh_row, const fp8_blocks *dh_col, const fp8_blocks *a_col, void *dh,

@@ -920,3 +920,63 @@ def test_binding_refuses_wrong_shapes_and_layouts():
         fp8.fp8_block_cast(L.x, 0, 0, L.xq.view(torch.int8), L.xs)
     with pytest.raises(fp8.FP8Error):
         fp8.fp8_block_linear_tokens(L.x.repeat(2, 1), L.wq, L.ws, torch.empty((64, 64), device="cuda"))
+
+
+@pytest.mark.parametrize("kind", list(ACTS))
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("shape", [(5, 300), (1500, 2304), (1500, 2297)])
+def test_activation_backward_of_non_finite_gradients(shape, dtype, kind):
+    """An infinite da stays infinite, of the sign of da * act'(h'), for h' of
+    either sign and 0; a NaN stays NaN; codes saturate; nothing else changes.
+    Fewer tiles than SMs, and more, of aligned rows and of odd ones."""
+    R, C = shape
+    h = torch.tensor([-2.0, -0.5, 0.0, 0.25, 0.5, 1.0, 1.5, 2.0], device="cuda").repeat(-(-C // 8))[:C].repeat(R, 1)  # exact in E4M3
+    ck = row_blocks(R, C)
+    fp8.fp8_act_fwd(h, ACTS[kind], 0, ck.q, ck.s)
+    fine = dev(data(R, C, "nfda", zeros=False), dtype)
+    da = fine.clone()
+    bad = [(1, 0, float("inf")), (2, 8, -float("inf")), (3, 16, float("nan")), (R - 1, C - 12, float("inf"))]
+    for r, c, v in bad:
+        da[r, c:c + 8] = v
+    hit = da != fine
+    named = lambda t: t.nan_to_num(nan=7.0, posinf=8.0, neginf=9.0)  # noqa: E731  (comparable)
+    out = {}
+    for fmt in FMTS:
+        for name, g in (("fine", fine), ("da", da)):
+            o = dict(dh=torch.empty_like(g), r=row_blocks(R, C), c=col_blocks(R, C), a=col_blocks(R, C))
+            fp8.fp8_act_bwd(ck.q, ck.s, g, ACTS[kind], FMTS[fmt], 0, o["r"].q, o["r"].s, o["c"].q, o["c"].s, o["a"].q,
+                            o["a"].s, o["dh"])
+            assert fp8.fp8_get_status() == (0 if name == "fine" else fp8.FP8_STATUS_NONFINITE)
+            alone, placed, spare = torch.empty_like(g), g.clone(), row_blocks(R, C)
+            fp8.fp8_act_bwd(ck.q, ck.s, g, ACTS[kind], dh=alone)
+            assert fp8.fp8_get_status() == 0
+            fp8.fp8_act_bwd(ck.q, ck.s, placed, ACTS[kind], FMTS[fmt], 0, spare.q, spare.s, dh=placed)
+            fp8.fp8_get_status()
+            for t in (alone, placed):
+                assert torch.equal(named(t), named(o["dh"]))
+            out[name] = o
+        _, d, _, tol_d = (torch.from_numpy(t).cuda() for t in act_bounds(f64(h), kind))
+        want = d * da.double()
+        got = out["da"]["dh"]
+        assert bool(want[hit].isnan().any()) and bool((want[hit] == float("inf")).any()) and bool((want[hit] == -float("inf")).any())
+        assert torch.equal(named(got[hit].double()), named(want[hit]))
+        assert torch.equal(got[~hit], out["fine"]["dh"][~hit])
+        assert torch.equal(out["da"]["a"].q, out["fine"]["a"].q) and torch.equal(out["da"]["a"].s, out["fine"]["a"].s)
+        fmax = {"e4m3": 448.0, "e5m2": 57344.0}[fmt]
+        for axis, key in ((1, "r"), (0, "c")):
+            v = {n: torch.empty((R, C), device="cuda") for n in out}
+            for n in v:
+                fp8.fp8_block_decode(out[n][key].q, out[n][key].s, FMTS[fmt], axis, v[n])
+                assert out[n][key].intact()
+            sat = want[hit].clamp(-fmax, fmax).nan_to_num(nan=7.0)
+            assert torch.equal(v["da"][hit].double().nan_to_num(nan=7.0), sat)
+            # a block with such a value has scale 1; the others are as without
+            blocks = {(r, c0 // 128 * 128) if axis else (r // 128 * 128, c0) for r, c, _ in bad for c0 in range(c, c + 8)}
+            for r0, c0 in blocks:
+                b = (slice(r0, r0 + 1), slice(c0, c0 + 128)) if axis else (slice(r0, r0 + 128), slice(c0, c0 + 1))
+                keep = ~hit[b]
+                x, tol = f64(want[b][keep]), f64(da[b][keep].abs().double() * tol_d[b][keep] + 1e-40)
+                w = f64(v["da"][b][keep])
+                assert np.all((w >= round_fp8(x - tol, fmt)) & (w <= round_fp8(x + tol, fmt)))
+                v["da"][b] = v["fine"][b] = 0.0
+            assert torch.equal(v["da"], v["fine"])
