@@ -67,7 +67,8 @@ class BlockWeight:
 
     def update(self, weight: torch.Tensor, stream=None) -> None:
         """Cast the weight anew (after an optimizer step)."""
-        fp8.fp8_block_cast_square(weight, fp8.FP8_E4M3, self.margin, self.q, self.s, self.s_col, stream=stream)
+        with _on(stream, weight, self.q, self.s, self.s_col):
+            fp8.fp8_block_cast_square(weight, fp8.FP8_E4M3, self.margin, self.q, self.s, self.s_col)
 
 
 class _Cast:

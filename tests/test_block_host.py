@@ -1,5 +1,6 @@
 """Block-scaled operators on the host: the scale order and the references the
 GPU tests use, and the calls that are refused before anything is enqueued."""
+import contextlib
 import ctypes
 
 import numpy as np
@@ -187,3 +188,41 @@ def test_short_route_leaves_host_tensors_and_wrong_arguments(fp8):
         fp8._calls.bind(1, 2)
     with pytest.raises(ValueError):
         fp8._calls.bind(*[0] * 8)
+
+
+# ---------------------------------------------------------------- modules: memory in use on a given stream
+class _Stream:
+    """In place of torch.cuda.Stream."""
+
+
+class _Tensor:
+    """A tensor of which only the streams that it is recorded on matter."""
+
+    def __init__(self, *shape):
+        self.shape, self.used = shape, set()
+
+    def record_stream(self, stream):
+        self.used.add(stream)
+
+
+@pytest.fixture
+def side(fp8, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "Stream", _Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(fp8, "fp8_block_cast_square", lambda *a, **k: None)
+    return _Stream()
+
+
+def _block_weight():
+    from fp8_mixed_precision_tensor_b200.block_linear import BlockWeight
+
+    w = object.__new__(BlockWeight)
+    w.margin, w.q, w.s, w.s_col = 0, _Tensor(4, 128), _Tensor(512), _Tensor(512)
+    return w
+
+
+def test_a_weight_update_holds_its_memory_for_its_stream(side):
+    w, new = _block_weight(), _Tensor(4, 128)
+    w.update(new, stream=side)
+    for t in (new, w.q, w.s, w.s_col):
+        assert t.used == {side}

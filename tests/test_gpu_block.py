@@ -980,3 +980,28 @@ def test_activation_backward_of_non_finite_gradients(shape, dtype, kind):
                 assert np.all((w >= round_fp8(x - tol, fmt)) & (w <= round_fp8(x + tol, fmt)))
                 v["da"][b] = v["fine"][b] = 0.0
             assert torch.equal(v["da"], v["fine"])
+
+
+def _behind_a_wait(side):
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+
+
+def _take_memory(*sizes):
+    """Whatever memory of these sizes was given back to the current stream, overwritten on it."""
+    for n in sizes:
+        for _ in range(4):
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x55)
+
+
+def test_weight_update_from_a_temporary_on_another_stream():
+    N, K = 520, 264
+    w = synth.device_normal((N, K), 0.02, 81, BF16, "cuda")
+    want, layer, side = BlockLinear(w * 2), BlockLinear(w), torch.cuda.Stream()
+    _behind_a_wait(side)
+    layer.weight.update(w * 2, stream=side)
+    _take_memory(2 * N * K)
+    torch.cuda.synchronize()
+    for k in ("q", "s", "s_col"):
+        assert torch.equal(getattr(layer.weight, k), getattr(want.weight, k)), k
