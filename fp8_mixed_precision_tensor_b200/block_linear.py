@@ -13,7 +13,8 @@ scale byte per 128.
 Every number is produced by the library's kernels; this module allocates the
 buffers and orders the calls.  With `stream` (a torch.cuda.Stream or its handle)
 a pass allocates and works on that stream, its outputs included; the caller
-orders it after whatever produced its arguments.
+orders it after whatever produced its arguments and the layer's weights.  What
+it reads may be dropped while it runs.
 """
 from __future__ import annotations
 
@@ -37,18 +38,19 @@ def _on(stream, *args: torch.Tensor):
 
 
 class _Kept:
-    """What a forward pass keeps for the backward pass, and its stream."""
+    """Tensors that outlive a pass, and the stream that their memory goes back to."""
 
     def __init__(self, *tensors: torch.Tensor):
-        self.tensors, self.stream = tensors, torch.cuda.current_stream()
+        self.tensors, self.stream = tensors, fp8._stream(None)
 
-    def take(self) -> tuple[torch.Tensor, ...]:
-        """For use on the current stream: their memory, given back on the
-        forward pass's, is not reused before that use has ended."""
-        now = torch.cuda.current_stream()
-        if now != self.stream:
-            for t in self.tensors:
-                t.record_stream(now)
+    def take(self, *beside: torch.Tensor | None) -> tuple[torch.Tensor, ...]:
+        """For use on the current stream (with `beside`, kept with them): their
+        memory is not reused before that use has ended."""
+        if fp8._stream(None) != self.stream:
+            now = torch.cuda.current_stream()
+            for t in (*self.tensors, *beside):
+                if t is not None:
+                    t.record_stream(now)
         return self.tensors
 
 
@@ -63,11 +65,13 @@ class BlockWeight:
         self.q = fp8.block_codes(N, K, dev)
         self.s = fp8.block_scales(N, K, dev)
         self.s_col = fp8.block_scales(K, N, dev)
+        self.kept = _Kept(self.q, self.s, self.s_col)
         self.update(weight)
 
     def update(self, weight: torch.Tensor, stream=None) -> None:
         """Cast the weight anew (after an optimizer step)."""
-        with _on(stream, weight, self.q, self.s, self.s_col):
+        with _on(stream, weight):
+            self.kept.take()
             fp8.fp8_block_cast_square(weight, fp8.FP8_E4M3, self.margin, self.q, self.s, self.s_col)
 
 
@@ -100,6 +104,7 @@ class BlockLinear:
         with _on(stream, x):
             y = torch.empty((x.shape[0], self.N), dtype=x.dtype, device=x.device)
             w = self.weight
+            w.kept.take(self.bias)
             if not keep and x.shape[0] <= fp8.FP8_BLOCK_TOKENS_MAX:
                 fp8.fp8_block_linear_tokens(x, w.q, w.s, y, bias=self.bias, margin=self.margin)
                 return y
@@ -116,6 +121,7 @@ class BlockLinear:
             raise RuntimeError("backward needs a forward pass with keep=True")
         with _on(stream, dy):
             M = dy.shape[0]
+            self.weight.kept.take()
             g = _Cast(dy, self.grad_fmt, self.margin, True, True)
             dx = torch.empty((M, self.K), dtype=dy.dtype, device=dy.device)
             dw = torch.empty((self.N, self.K), dtype=torch.bfloat16 if rto else dy.dtype, device=dy.device)
@@ -144,6 +150,7 @@ class BlockMLP:
     def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
         with _on(stream, x):
             M, dev = x.shape[0], x.device
+            self.w1.kept.take(), self.w2.kept.take()
             c = _Cast(x, fp8.FP8_E4M3, self.margin, True, True)
             h = torch.empty((M, self.F), dtype=x.dtype, device=dev)
             fp8.fp8_block_linear_fwd(c.q, c.s, self.w1.q, self.w1.s, h)
@@ -166,6 +173,7 @@ class BlockMLP:
         with _on(stream, dy):
             xq, xs, ck, ck_s = self.kept.take()
             M, dev, fmt = dy.shape[0], dy.device, self.grad_fmt
+            self.w1.kept.take(), self.w2.kept.take()
             new = lambda *shape: torch.empty(shape, dtype=dy.dtype, device=dev)  # noqa: E731
             g = _Cast(dy, fmt, self.margin, True, True)
             da = new(M, self.F)

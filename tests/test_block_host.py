@@ -199,7 +199,7 @@ class _Tensor:
     """A tensor of which only the streams that it is recorded on matter."""
 
     def __init__(self, *shape):
-        self.shape, self.used = shape, set()
+        self.shape, self.used, self.device, self.dtype = shape, set(), "cuda:0", torch.bfloat16
 
     def record_stream(self, stream):
         self.used.add(stream)
@@ -207,22 +207,64 @@ class _Tensor:
 
 @pytest.fixture
 def side(fp8, monkeypatch):
+    """A second stream, with the library's calls and torch's allocations left out."""
+    now = [_Stream()]
+
+    @contextlib.contextmanager
+    def on(stream):
+        now.append(stream)
+        yield
+        now.pop()
+
     monkeypatch.setattr(torch.cuda, "Stream", _Stream)
-    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
-    monkeypatch.setattr(fp8, "fp8_block_cast_square", lambda *a, **k: None)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: now[-1])
+    monkeypatch.setattr(torch, "empty", lambda shape, **k: _Tensor(*shape))
+    monkeypatch.setattr(fp8, "_stream", lambda s: id(now[-1]))
+    monkeypatch.setattr(fp8, "block_codes", lambda rows, cols, device: _Tensor(rows, cols))
+    monkeypatch.setattr(fp8, "block_scales", lambda outer, red, device: _Tensor(outer * red))
+    for name in ("fp8_block_cast_square", "fp8_block_cast", "fp8_block_linear_tokens", "fp8_block_linear_fwd",
+                 "fp8_block_linear_dgrad", "fp8_block_linear_wgrad", "fp8_act_fwd", "fp8_act_bwd"):
+        monkeypatch.setattr(fp8, name, lambda *a, **k: None)
     return _Stream()
 
 
-def _block_weight():
+def test_a_weight_update_holds_its_memory_for_its_stream(side):
     from fp8_mixed_precision_tensor_b200.block_linear import BlockWeight
 
-    w = object.__new__(BlockWeight)
-    w.margin, w.q, w.s, w.s_col = 0, _Tensor(4, 128), _Tensor(512), _Tensor(512)
-    return w
-
-
-def test_a_weight_update_holds_its_memory_for_its_stream(side):
-    w, new = _block_weight(), _Tensor(4, 128)
+    w, new = BlockWeight(_Tensor(256, 128)), _Tensor(256, 128)
     w.update(new, stream=side)
     for t in (new, w.q, w.s, w.s_col):
         assert t.used == {side}
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_passes_hold_the_layers_memory_for_their_stream(side, given):
+    from fp8_mixed_precision_tensor_b200.block_linear import BlockLinear, BlockMLP
+
+    def there(f, *a, **k):
+        if given:
+            return f(*a, **k, stream=side)
+        with torch.cuda.stream(side):
+            return f(*a, **k)
+
+    for M, keep in ((4, False), (200, False), (200, True)):
+        lin = BlockLinear(_Tensor(256, 128), _Tensor(256))
+        x = _Tensor(M, 128)
+        there(lin.forward, x, keep=keep)
+        for t in (lin.weight.q, lin.weight.s, lin.bias, *((x,) if given else ())):
+            assert t.used == {side}
+    lin = BlockLinear(_Tensor(256, 128))  # no bias; forward here, backward there
+    lin.forward(_Tensor(200, 128), keep=True)
+    kept = lin.kept.tensors
+    assert not any(t.used for t in (*kept, lin.weight.q, lin.weight.s, lin.weight.s_col))
+    there(lin.backward, _Tensor(200, 256))
+    assert all(t.used == {side} for t in (*kept, lin.weight.q, lin.weight.s_col))
+    for there_first in (True, False):
+        mlp = BlockMLP(_Tensor(256, 128), _Tensor(64, 256))
+        (there if there_first else lambda f, x: f(x))(mlp.forward, _Tensor(200, 128))
+        kept = mlp.kept.tensors
+        there(mlp.backward, _Tensor(200, 64))
+        for w in (mlp.w1, mlp.w2):
+            assert all(t.used == {side} for t in (w.q, w.s, w.s_col))
+        assert all(t.used == (set() if there_first else {side}) for t in kept)

@@ -1005,3 +1005,25 @@ def test_weight_update_from_a_temporary_on_another_stream():
     torch.cuda.synchronize()
     for k in ("q", "s", "s_col"):
         assert torch.equal(getattr(layer.weight, k), getattr(want.weight, k)), k
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_a_layer_dropped_while_its_pass_runs_on_another_stream(given):
+    M, N, K = 200, 520, 264
+    x, w1, w2 = (synth.device_normal(s, 0.5, 90 + i, BF16, "cuda") for i, s in enumerate(((M, K), (N, K), (K, N))))
+    make = {"linear": lambda: BlockLinear(w1, w1[:, 0] * 4), "tokens": lambda: BlockLinear(w1, w1[:, 0] * 4),
+            "mlp": lambda: BlockMLP(w1, w2)}
+    side = torch.cuda.Stream()
+    for kind, new in make.items():
+        a = x[:9] if kind == "tokens" else x
+        want, layer = new().forward(a), new()
+        _behind_a_wait(side)
+        if given:
+            got = layer.forward(a, stream=side)
+        else:
+            with torch.cuda.stream(side):
+                got = layer.forward(a)
+        del layer
+        _take_memory(N * 384, N * 640, K * 640, 2 * N, 4096, 5120, 512 * 5, 512 * 15, 512 * 10)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), kind
