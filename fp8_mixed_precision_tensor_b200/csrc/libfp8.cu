@@ -3,6 +3,7 @@
 // included below; this is the library's single translation unit.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -792,6 +793,11 @@ namespace {
 
 size_t dtype_bytes(int dt) { return dt == FP8_DT_F32 ? 4 : 2; }
 bool fp8_fmt(int f) { return f == FP8_E4M3 || f == FP8_E5M2; }
+// Kernels and launches round sizes up to tiles and groups of blocks in 32 bits (by 512 at the most).
+bool too_long(int a, int b, int c = 0) {
+  constexpr int kMost = INT_MAX - 1023;
+  return a > kMost || b > kMost || c > kMost;
+}
 bool valid_act(int a) { return a == FP8_ACT_GELU_TANH || a == FP8_ACT_GELU_ERF || a == FP8_ACT_SILU; }
 
 // A high-precision matrix argument: FP8_OK, or what is wrong with it.
@@ -1135,6 +1141,7 @@ int run_bgemm(const BOperand &A, const BOperand &B, const void *bias, int bias_d
   if (R < 0 || C < 0 || red < 0 || !valid_out_dtype(out_dtype) || (bias && !valid_dtype(bias_dtype)))
     return FP8_ERR_INVALID_ARG;
   if (R == 0 || C == 0) return FP8_OK;
+  if (too_long(R, C, red)) return FP8_ERR_UNSUPPORTED;
   int rc = check_matrix(out, out_dtype, C, ld_out);
   if (rc) return rc;
   if (bias && reinterpret_cast<uintptr_t>(bias) % dtype_bytes(bias_dtype)) return FP8_ERR_UNALIGNED;
@@ -1177,6 +1184,7 @@ int fp8_block_cast(const void *x, int dtype, int rows, int cols, size_t ldx, int
   if (!valid_dtype(dtype) || !fp8_fmt(fmt) || rows < 0 || cols < 0 || margin < 0 || margin > 64 || (!row && !col))
     return FP8_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return FP8_OK;
+  if (too_long(rows, cols)) return FP8_ERR_UNSUPPORTED;
   int rc = check_matrix(x, dtype, cols, ldx);
   if (rc || (row && (rc = check_blocks(row, cols))) || (col && (rc = check_blocks(col, cols)))) return rc;
   const block::CastOut o = cast_out(row, col);
@@ -1207,6 +1215,7 @@ int fp8_block_cast_square(const void *x, int dtype, int rows, int cols, size_t l
   if (!valid_dtype(dtype) || !fp8_fmt(fmt) || rows < 0 || cols < 0 || margin < 0 || margin > 64)
     return FP8_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return FP8_OK;
+  if (too_long(rows, cols)) return FP8_ERR_UNSUPPORTED;
   int rc = check_matrix(x, dtype, cols, ldx);
   if (rc || (rc = check_blocks(out, cols))) return rc;
   if (!s_col) return FP8_ERR_INVALID_ARG;
@@ -1235,6 +1244,7 @@ int fp8_block_decode(const fp8_blocks *in, int fmt, int axis, int rows, int cols
   if (!valid_dtype(dtype) || !fp8_fmt(fmt) || rows < 0 || cols < 0 || (axis != 0 && axis != 1))
     return FP8_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return FP8_OK;
+  if (too_long(rows, cols)) return FP8_ERR_UNSUPPORTED;
   int rc = check_matrix(x, dtype, cols, ldx);
   if (rc || (rc = check_blocks(in, cols))) return rc;
   DeviceInfo *d;
@@ -1267,6 +1277,7 @@ int fp8_block_linear_tokens(const void *x, int x_dtype, size_t ldx, int margin, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (M == 0 || N == 0 || K == 0)
     return run_bgemm<false, false>({nullptr, 0}, {w, 0}, bias, bias_dtype, y, y_dtype, ldy, M, N, K, s);
+  if (too_long(N, K)) return FP8_ERR_UNSUPPORTED;
   int rc = check_matrix(x, x_dtype, K, ldx);
   if (rc || (rc = check_matrix(y, y_dtype, N, ldy)) || (rc = check_blocks(w, K))) return rc;
   if (bias && reinterpret_cast<uintptr_t>(bias) % dtype_bytes(bias_dtype)) return FP8_ERR_UNALIGNED;
@@ -1310,6 +1321,7 @@ int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int ac
   if (!valid_dtype(dtype) || !valid_act(act) || rows < 0 || cols < 0 || margin < 0 || margin > 64)
     return FP8_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return FP8_OK;
+  if (too_long(rows, cols)) return FP8_ERR_UNSUPPORTED;
   int rc = check_matrix(h, dtype, cols, ldh);
   if (rc || (rc = check_blocks(ckpt, cols)) || (a_row && (rc = check_blocks(a_row, cols))) ||
       (a && (rc = check_matrix(a, dtype, cols, lda))))
@@ -1342,6 +1354,7 @@ int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int
       (!dh_row && !dh_col && !a_col && !dh))
     return FP8_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return FP8_OK;
+  if (too_long(rows, cols)) return FP8_ERR_UNSUPPORTED;
   int rc = check_matrix(da, dtype, cols, ldda);
   if (rc || (rc = check_blocks(ckpt, cols)) || (dh_row && (rc = check_blocks(dh_row, cols))) ||
       (dh_col && (rc = check_blocks(dh_col, cols))) || (a_col && (rc = check_blocks(a_col, cols))) ||
@@ -1397,7 +1410,8 @@ const char *fp8_strerror(int code) {
     case FP8_OK: return "ok";
     case FP8_ERR_INVALID_ARG: return "invalid argument";
     case FP8_ERR_UNALIGNED: return "pointer not 16-byte aligned";
-    case FP8_ERR_UNSUPPORTED: return "unsupported shape (GEMM dims must be multiples of 16)";
+    case FP8_ERR_UNSUPPORTED: return "unsupported shape (per-tensor GEMMs: dims must be multiples of 16; block-scaled calls: "
+                                  "at most 2^31 - 1024 elements a side)";
     case FP8_ERR_CUDA: return "CUDA error";
     case FP8_ERR_TIMEOUT: return "device pipeline wait timed out";
     case FP8_ERR_NONFINITE: return "non-finite amax";

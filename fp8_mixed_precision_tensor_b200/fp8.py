@@ -505,6 +505,15 @@ def _matrix(t: torch.Tensor, what: str, rows: int, cols: int, dev: int) -> int:
     return ld if rows > 1 else cols
 
 
+def _sides(shape, what: str) -> tuple[int, int]:
+    """A matrix's sides, such as a C int takes them."""
+    if len(shape) != 2:
+        raise ValueError(f"{what}: shape {tuple(shape)}, expected a matrix")
+    if max(shape) > 2 ** 31 - 1024:
+        raise ValueError(f"{what}: shape {tuple(shape)}, at most 2^31 - 1024 a side")
+    return shape
+
+
 def _hp(t: torch.Tensor, what: str) -> int:
     """Element type code of a high-precision tensor."""
     dt = _DT.get(t.dtype)
@@ -515,10 +524,8 @@ def _hp(t: torch.Tensor, what: str) -> int:
 
 def _input(t: torch.Tensor, what: str):
     """(dtype code, rows, cols, row stride, device) of a call's high-precision input."""
-    dt, dev, shape = _hp(t, what), _device(t, what), t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{what}: shape {tuple(shape)}, expected a matrix")
-    rows, cols = shape
+    dt, dev = _hp(t, what), _device(t, what)
+    rows, cols = _sides(t.shape, what)
     ld, inner = t.stride()
     if (inner != 1 and cols > 1) or (ld < cols and rows > 1):
         _bad_matrix(t, what, rows, cols, dev)
@@ -558,10 +565,8 @@ def _vector(t, what: str, n: int, dev: int):
 
 def _codes_shape(q: torch.Tensor, what: str):
     """(rows, cols, device) of a call's leading code matrix."""
-    dev, shape = _device(q, what), q.shape
-    if len(shape) != 2:
-        raise ValueError(f"{what}: shape {tuple(shape)}, expected a matrix")
-    rows, cols = shape
+    dev = _device(q, what)
+    rows, cols = _sides(q.shape, what)
     return rows, cols, dev
 
 
@@ -609,7 +614,7 @@ def fp8_block_linear_fwd(xq, xs, wq, ws, y, bias=None, stream=None, rto=False) -
     if (_calls or _load_calls()).linear_fwd(xq, xs, wq, ws, y, bias, stream, rto):
         return
     M, K, dev = _codes_shape(xq, "x")
-    N = wq.shape[0]
+    N = _sides(wq.shape, "w")[0]
     yp, ydt, ld = _out(y, "y", M, N, dev, rto)
     bp, bdt = (None, 0) if bias is None else _vector(bias, "bias", N, dev)
     _check(load_library().fp8_block_linear_fwd(_blocks(xq, xs, "x", M, K, M, K, dev),
@@ -624,7 +629,7 @@ def fp8_block_linear_tokens(x, wq, ws, y, bias=None, margin: int = 0, stream=Non
     if (_calls or _load_calls()).linear_tokens(x, wq, ws, y, bias, margin, stream, rto):
         return
     dt, M, K, ldx, dev = _input(x, "x")
-    N = wq.shape[0]
+    N = _sides(wq.shape, "w")[0]
     yp, ydt, ldy = _out(y, "y", M, N, dev, rto)
     bp, bdt = (None, 0) if bias is None else _vector(bias, "bias", N, dev)
     _check(load_library().fp8_block_linear_tokens(x.data_ptr(), dt, ldx, margin,
@@ -637,7 +642,7 @@ def fp8_block_linear_dgrad(dyq, dys, dy_fmt: int, wq, ws_col, dx, stream=None, r
     if (_calls or _load_calls()).linear_dgrad(dyq, dys, dy_fmt, wq, ws_col, dx, stream, rto):
         return
     M, N, dev = _codes_shape(dyq, "dy")
-    K = wq.shape[1]
+    K = _sides(wq.shape, "w")[1]
     xp, xdt, ld = _out(dx, "dx", M, K, dev, rto)
     _check(load_library().fp8_block_linear_dgrad(_blocks(dyq, dys, "dy", M, N, M, N, dev), dy_fmt,
                                                  _blocks(wq, ws_col, "w", N, K, K, N, dev), xp, xdt, ld, M, N, K,
@@ -649,7 +654,7 @@ def fp8_block_linear_wgrad(dyq, dys_col, dy_fmt: int, xq, xs_col, dw, stream=Non
     if (_calls or _load_calls()).linear_wgrad(dyq, dys_col, dy_fmt, xq, xs_col, dw, stream, rto):
         return
     M, N, dev = _codes_shape(dyq, "dy")
-    K = xq.shape[1]
+    K = _sides(xq.shape, "x")[1]
     wp, wdt, ld = _out(dw, "dw", N, K, dev, rto)
     _check(load_library().fp8_block_linear_wgrad(_blocks(dyq, dys_col, "dy", M, N, N, M, dev), dy_fmt,
                                                  _blocks(xq, xs_col, "x", M, K, K, M, dev), wp, wdt, ld, M, N, K,

@@ -45,7 +45,7 @@ extern "C" {
 #define FP8_OK 0
 #define FP8_ERR_INVALID_ARG 1 /* null pointer, bad enum, bad hyper-parameter */
 #define FP8_ERR_UNALIGNED 2   /* a bulk pointer is not 16-byte aligned */
-#define FP8_ERR_UNSUPPORTED 3 /* a GEMM shape the kernel cannot tile (see below) */
+#define FP8_ERR_UNSUPPORTED 3 /* a shape the kernels cannot tile (see below) */
 #define FP8_ERR_CUDA 4        /* a CUDA runtime call or kernel launch failed */
 #define FP8_ERR_TIMEOUT 5     /* device status: a pipeline wait ran out of time */
 #define FP8_ERR_NONFINITE 6   /* device status: an amax was NaN or inf */
@@ -560,7 +560,8 @@ int fp8_selftest_encode(int fmt, unsigned lo_bits, unsigned long long hi_bits, u
  * are neither read nor written).  Code and scale pointers are 16-byte aligned.
  * High-precision matrices have rows `ld` elements apart (ld at least the row's
  * length) and may start at any element; rows that start on 16-byte boundaries
- * are read and written with wide accesses.
+ * are read and written with wide accesses.  A side longer than 2^31 - 1024 is
+ * FP8_ERR_UNSUPPORTED.
  *
  * Outputs must not overlap inputs or one another, with two exceptions:
  * fp8_act_fwd's a may be h, and fp8_act_bwd's dh may be da (the same pointer

@@ -168,6 +168,47 @@ def test_activation_calls_reject_bad_arguments(lib, fp8):
     assert bwd(c=_b(fp8, FAKE + 4)) == fp8.FP8_ERR_UNALIGNED and bwd(cols=0) == fp8.FP8_OK
 
 
+@pytest.mark.parametrize("side", [2 ** 31 - 1, 2 ** 31 - 1023])
+def test_sides_near_the_end_of_an_int_are_refused(lib, fp8, side):
+    """Rounded up to a tile they would pass it."""
+    wide = _b(fp8, ld=2 ** 31)
+    calls = [lambda r, c: lib.fp8_block_cast(FAKE, 1, r, c, 2 ** 31, 0, 0, wide, None, None),
+             lambda r, c: lib.fp8_block_cast(FAKE, 1, r, c, 2 ** 31, 0, 0, None, wide, None),
+             lambda r, c: lib.fp8_block_cast_square(FAKE, 1, r, c, 2 ** 31, 0, 0, wide, FAKE, None),
+             lambda r, c: lib.fp8_block_decode(wide, 0, 1, r, c, FAKE, 1, 2 ** 31, None),
+             lambda r, c: lib.fp8_act_fwd(FAKE, 1, r, c, 2 ** 31, 0, 0, wide, None, None, 0, None),
+             lambda r, c: lib.fp8_act_bwd(wide, FAKE, 1, r, c, 2 ** 31, 0, 1, 0, wide, None, None, None, 0, None),
+             lambda n, k: lib.fp8_block_linear_tokens(FAKE, 1, 2 ** 31, 0, wide, None, 0, FAKE, 1, 2 ** 31, 4, n, k, None)]
+    for call in calls:
+        assert call(side, 64) == fp8.FP8_ERR_UNSUPPORTED and call(64, side) == fp8.FP8_ERR_UNSUPPORTED
+    for dims in ((side, 64, 64), (64, side, 64), (64, 64, side)):
+        assert lib.fp8_block_linear_fwd(wide, wide, None, 0, FAKE, 1, 2 ** 31, *dims, None) == fp8.FP8_ERR_UNSUPPORTED
+        for f in (lib.fp8_block_linear_dgrad, lib.fp8_block_linear_wgrad):
+            assert f(wide, 1, wide, FAKE, 1, 2 ** 31, *dims, None) == fp8.FP8_ERR_UNSUPPORTED
+
+
+def test_sides_that_an_int_does_not_hold_are_refused(fp8, monkeypatch):
+    """2^32 + 8 rows are not 8 rows."""
+    monkeypatch.setattr(fp8, "_device", lambda t, what: -1)
+    u8 = dict(dtype=torch.uint8, device="meta")
+    x, q, s = torch.empty((2 ** 32 + 8, 1), device="meta"), torch.empty((2 ** 32 + 8, 16), **u8), torch.empty(2 ** 34, **u8)
+    y, few = torch.empty((8, 8), device="meta"), torch.empty((8, 1), device="meta")
+    w = torch.empty((8, 16), **u8)
+    for call in (lambda: fp8.fp8_block_cast(x, 0, 0, q, s), lambda: fp8.fp8_block_cast_square(x, 0, 0, q, s, s),
+                 lambda: fp8.fp8_block_decode(q, s, 0, 1, x), lambda: fp8.fp8_act_fwd(x, 0, 0, q, s),
+                 lambda: fp8.fp8_act_bwd(q, s, x, 0, dh=x), lambda: fp8.fp8_block_linear_fwd(q, s, w, s, y),
+                 lambda: fp8.fp8_block_linear_fwd(w, s, q, s, y), lambda: fp8.fp8_block_linear_tokens(few, q, s, y),
+                 lambda: fp8.fp8_block_linear_dgrad(q, s, 1, w, s, y), lambda: fp8.fp8_block_linear_dgrad(w, s, 1, q.t(), s, y),
+                 lambda: fp8.fp8_block_linear_wgrad(q, s, 1, w, s, y), lambda: fp8.fp8_block_linear_wgrad(w, s, 1, q.t(), s, y)):
+        with pytest.raises(ValueError, match="a side"):
+            call()
+
+
+def test_the_message_of_an_unsupported_shape_names_both_rules(fp8):
+    text = fp8.fp8_strerror(fp8.FP8_ERR_UNSUPPORTED)
+    assert "multiples of 16" in text and "2^31 - 1024" in text
+
+
 def test_binding_takes_device_tensors_only(fp8):
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
     q, s = torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
