@@ -48,14 +48,15 @@ def _compile(cmd: list[str], lib: str, verbose: bool) -> None:
 def _calls_command() -> list[str]:
     import sysconfig
 
+    import torch
     from torch.utils import cpp_extension as ext
 
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(os.environ.get("NVCC", "nvcc")))))
     includes = [*ext.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     libs = ext.library_paths()
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-            *(a for d in includes for a in ("-isystem", d)), CALLS_MAIN, *(f"-L{d}" for d in libs),
-            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            f'-DFP8_TORCH_VERSION="{torch.__version__}"', *(a for d in includes for a in ("-isystem", d)), CALLS_MAIN,
+            *(f"-L{d}" for d in libs), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

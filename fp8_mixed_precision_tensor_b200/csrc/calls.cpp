@@ -320,4 +320,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&g_module); }
+// The module, with the torch whose headers it was compiled with.
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject *m = PyModule_Create(&g_module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", FP8_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

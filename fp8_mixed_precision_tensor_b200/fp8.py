@@ -13,6 +13,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 from dataclasses import dataclass
 
 import torch
@@ -90,14 +91,29 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
+class _PythonRoute:
+    """In place of _calls.so: leaves every call to the Python function."""
+
+    def __getattr__(self, name):
+        return lambda *args: False
+
+
 def _bound_calls(lib: ctypes.CDLL):
-    """_calls.so with the addresses of lib's block-scaled operators."""
-    if not os.path.exists(CALLS_PATH):
-        raise ImportError(f"_calls.so not built ({CALLS_PATH}); run python -m fp8_mixed_precision_tensor_b200.build")
-    name = __package__ + "._calls"
-    loader = importlib.machinery.ExtensionFileLoader(name, CALLS_PATH)
-    calls = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, CALLS_PATH, loader=loader))
-    loader.exec_module(calls)
+    """_calls.so with the addresses of lib's block-scaled operators; without it
+    (or with one built for another torch) the calls take the way through
+    Python, the same kernels after two to four more microseconds on the host."""
+    try:
+        name = __package__ + "._calls"
+        loader = importlib.machinery.ExtensionFileLoader(name, CALLS_PATH)
+        calls = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, CALLS_PATH, loader=loader))
+        loader.exec_module(calls)
+        built_for = getattr(calls, "torch_version", None)
+        if built_for != torch.__version__:  # tensors are laid out as its headers say
+            raise ImportError(f"built for torch {built_for}, this is {torch.__version__}")
+    except ImportError as e:
+        warnings.warn(f"_calls.so cannot be used ({e}): block-scaled calls take the longer way through Python; "
+                      "rebuild with python -m fp8_mixed_precision_tensor_b200.build --force", RuntimeWarning, stacklevel=3)
+        return _PythonRoute()
     calls.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
         "fp8_block_cast", "fp8_block_cast_square", "fp8_block_linear_fwd", "fp8_block_linear_tokens",
         "fp8_block_linear_dgrad", "fp8_block_linear_wgrad", "fp8_act_fwd", "fp8_act_bwd")))

@@ -231,6 +231,26 @@ def test_short_route_leaves_host_tensors_and_wrong_arguments(fp8):
         fp8._calls.bind(*[0] * 8)
 
 
+@pytest.mark.parametrize("how", ["missing", "no library", "another torch"])
+def test_the_library_serves_without_the_short_route(lib, fp8, monkeypatch, tmp_path, how):
+    path = tmp_path / "_calls.so"
+    if how == "no library":
+        path.write_bytes(b"not a library")
+    if how == "another torch":
+        monkeypatch.setattr(torch, "__version__", "1.0")
+    else:
+        monkeypatch.setattr(fp8, "CALLS_PATH", str(path))
+    monkeypatch.setattr(fp8, "_lib", None)
+    monkeypatch.setattr(fp8, "_calls", None)
+    with pytest.warns(RuntimeWarning, match="longer way through Python"):
+        assert fp8.fp8_strerror(0) == "ok"
+    assert fp8.fp8_adam_workspace_bytes(3) == 3 * 64
+    x, q, s = torch.zeros(4, 128), torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    assert fp8._calls.block_cast(x, 0, 0, q, s, None, None, None) is False
+    with pytest.raises(ValueError, match="device tensors"):  # the Python function's own answer
+        fp8.fp8_block_cast(x, 0, 0, q, s)
+
+
 # ---------------------------------------------------------------- modules: memory in use on a given stream
 class _Stream:
     """In place of torch.cuda.Stream."""
