@@ -1027,3 +1027,74 @@ def test_a_layer_dropped_while_its_pass_runs_on_another_stream(given):
         _take_memory(N * 384, N * 640, K * 640, 2 * N, 4096, 5120, 512 * 5, 512 * 15, 512 * 10)
         torch.cuda.synchronize()
         assert torch.equal(got, want), kind
+
+
+@pytest.mark.parametrize("kind", list(ACTS))
+@pytest.mark.parametrize("R", [1, 1500])
+def test_gradients_just_off_a_tie_keep_their_side(kind, R):
+    """For large h', act'(h') is above 1 by something far below binary32's
+    reach.  A da exactly halfway between two codes gives the one farther from
+    0, in blocks along either axis."""
+    C = 2048 if R > 1 else 128  # more tiles than SMs, or one
+    ck, cs = fp8.block_codes(R, C), fp8.block_scales(R, C)
+    fp8.fp8_act_fwd(torch.full((R, C), 24.0, device="cuda"), ACTS[kind], 0, ck, cs)  # kept as it is
+    # Every block along the rows and the columns has amax 24, scale 16: units of 1 above 8, 0.5 below.
+    # Ties to even would give 10, 12, 12, 14, 4 and 5.
+    da = torch.full((R, C), 24.0, device="cuda")
+    ties = torch.tensor([10.5, 11.5, 12.5, 13.5, 4.25, 5.25], device="cuda")
+    want = torch.tensor([11.0, 12.0, 13.0, 14.0, 4.5, 5.5], device="cuda")
+    out = da.clone()
+    for i in range(6):
+        r, sign = (0 if R == 1 else 130 + 17 * i), (1.0, -1.0)
+        for k in range(2):
+            for at in (7 + 16 * i + k, C - 21 + i + 7 * k):
+                da[r, at], out[r, at] = sign[k] * ties[i], sign[k] * want[i]
+    for dtype in (F32, BF16, F16):  # (all values are in each type)
+        q, s, qc, sc = fp8.block_codes(R, C), fp8.block_scales(R, C), fp8.block_codes(R, C), fp8.block_scales(C, R)
+        fp8.fp8_act_bwd(ck, cs, da.to(dtype), ACTS[kind], fp8.FP8_E4M3, 0, q, s, qc, sc)
+        got = torch.empty_like(da)
+        fp8.fp8_block_decode(q, s, fp8.FP8_E4M3, 1, got)
+        assert torch.equal(got, out), dtype
+        if R > 1:  # (a column of one element has a scale of its own)
+            fp8.fp8_block_decode(qc, sc, fp8.FP8_E4M3, 0, got)
+            assert torch.equal(got, out), dtype
+
+
+@pytest.mark.parametrize("cols", [2304, 2297])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_column_scales_of_many_tiles(dtype, cols):
+    """The scale bytes of blocks along the rows, from the forms for many tiles:
+    128 rows at a time the bytes of the forms for few, and 127 in the padding."""
+    from _block import scale_address
+
+    R, C, S = 1500, fp8.block_codes, fp8.block_scales
+    h, da = (dev(data(R, cols, "coltiles", i), dtype) for i in range(2))
+
+    def run(h, da):
+        r = h.shape[0]
+        q, ck, ck_s, row_s = C(r, cols), C(r, cols), S(r, cols), S(r, cols)
+        out = {k: S(cols, r).fill_(GUARD) for k in ("cast", "alone", "square", "dh", "a")}
+        fp8.fp8_block_cast(h, fp8.FP8_E5M2, 0, q, row_s, C(r, cols), out["cast"])
+        fp8.fp8_block_cast(h, fp8.FP8_E4M3, 0, q_col=q, s_col=out["alone"])
+        fp8.fp8_block_cast_square(h, fp8.FP8_E4M3, 0, q, row_s, out["square"])
+        fp8.fp8_act_fwd(h, fp8.FP8_ACT_SILU, 0, ck, ck_s)
+        fp8.fp8_act_bwd(ck, ck_s, da, fp8.FP8_ACT_SILU, fp8.FP8_E5M2, 0, dh_q_col=q, dh_s_col=out["dh"], a_q_col=C(r, cols),
+                        a_s_col=out["a"])
+        return {k: v.cpu().numpy() for k, v in out.items()}
+
+    whole, c, blocks = run(h, da), np.arange(cols), -(-R // 128)
+    for k, got in whole.items():
+        rest = np.ones(len(got), dtype=bool)
+        for b in range(blocks):
+            rest[scale_address(c, b, R)] = False
+        assert np.all(got[rest] == 127), k
+    for b in range(blocks):
+        part = run(h[b * 128:(b + 1) * 128], da[b * 128:(b + 1) * 128])
+        for k, got in whole.items():
+            assert np.array_equal(got[scale_address(c, b, R)], part[k][scale_address(c, 0, 128)]), (k, b)
+    # the few-tile forms' own bytes, of the first rows
+    x = f64(h[:128])
+    assert np.array_equal(part["cast"][scale_address(c, 0, 128)],
+                          (127 - exponents(blocks_of(f64(h[(blocks - 1) * 128:]), 128, 1), "e5m2")[0]).astype(np.uint8))
+    assert np.array_equal(whole["alone"][scale_address(c, 0, R)], (127 - exponents(blocks_of(x, 128, 1), "e4m3")[0]).astype(np.uint8))
+    assert fp8.fp8_get_status() == 0
