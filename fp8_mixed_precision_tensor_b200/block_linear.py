@@ -90,8 +90,14 @@ class BlockLinear:
     """y = x W^T (+ bias) with block-scaled FP8 operands.
 
     forward(x) with x [M, K] returns y in x's dtype; keep=True (training) keeps
-    x's 8-bit column blocks for backward(dy), which returns (dx, dw).  Without
-    keep, at most FP8_BLOCK_TOKENS_MAX tokens take the one-launch form."""
+    x's 8-bit column blocks for backward(dy), which returns (dx, dw) (the
+    bias's gradient is the sum of dy's rows, the caller's).  Without keep, at
+    most FP8_BLOCK_TOKENS_MAX tokens take the one-launch form.
+
+    Not a torch.nn.Module: no parameters, no autograd.  One pass at a time:
+    forward(keep=True) takes the place of what an earlier one kept.  With
+    several in flight (micro-batches) take `kept` from the layer after each
+    forward pass and set it again before the matching backward pass."""
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, grad_fmt: int = fp8.FP8_E5M2,
                  margin: int = 0):
@@ -136,7 +142,9 @@ class BlockMLP:
 
     Kept for the backward pass: x's column blocks and the activation's input
     as an E4M3 checkpoint, 1 byte per element each; act(h) is recomputed from
-    the checkpoint inside the pass that applies its derivative."""
+    the checkpoint inside the pass that applies its derivative.  Not a
+    torch.nn.Module, and one pass at a time, as BlockLinear; every forward pass
+    keeps."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, act: int = fp8.FP8_ACT_GELU_TANH,
                  grad_fmt: int = fp8.FP8_E5M2, margin: int = 0):

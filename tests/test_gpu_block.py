@@ -1098,3 +1098,26 @@ def test_column_scales_of_many_tiles(dtype, cols):
                           (127 - exponents(blocks_of(f64(h[(blocks - 1) * 128:]), 128, 1), "e5m2")[0]).astype(np.uint8))
     assert np.array_equal(whole["alone"][scale_address(c, 0, R)], (127 - exponents(blocks_of(x, 128, 1), "e4m3")[0]).astype(np.uint8))
     assert fp8.fp8_get_status() == 0
+
+
+def test_several_passes_in_flight():
+    """`kept` taken after each forward pass and set before its backward pass; otherwise the last pass's."""
+    M, N, K = 160, 264, 520
+    w, w2 = synth.device_normal((N, K), 0.02, 101, BF16, "cuda"), synth.device_normal((K, N), 0.02, 102, BF16, "cuda")
+    for layer in (BlockLinear(w), BlockMLP(w, w2)):
+        keep = {"keep": True} if isinstance(layer, BlockLinear) else {}
+        xs = [synth.device_normal((M + i, K), 1.0, 103 + i, BF16, "cuda") for i in range(3)]
+        dys, want, kept = [], [], []
+        for x in xs:
+            dys.append(synth.device_normal(layer.forward(x, **keep).shape, 1e-3, 110 + len(dys), BF16, "cuda"))
+            want.append(layer.backward(dys[-1]))
+        for x in xs:
+            layer.forward(x, **keep)
+            kept.append(layer.kept)
+        with pytest.raises(ValueError):
+            layer.backward(dys[0])  # another pass's: other tokens
+        for i in (1, 0, 2):
+            layer.kept = kept[i]
+            for got, ref in zip(layer.backward(dys[i]), want[i], strict=True):
+                assert torch.equal(got, ref)
+        assert layer.kept is None
