@@ -147,31 +147,27 @@ template <int DT, int ACT, int RP>
 __global__ void __launch_bounds__(kPartThreads<RP>, 1024 / kPartThreads<RP>) k_act_fwd(const ActFwd p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int tiles_c = (p.cols + kTile - 1) / kTile;
-  {
-    const auto [row0, col0] = part_at<RP>(blockIdx.x, tiles_c);
-    Raw8<DT> raw[RP];
-    load_tile<DT>(p.h, p.ldh, p.vec_h, row0, col0, p.rows, p.cols, raw);
-    cast_raw_rows<DT, FP8_E4M3>(raw, p.cq, p.cs, p.ldc, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
-    if (p.aq || p.a) {
-      float f[RP][8];
+  const auto [row0, col0] = part_at<RP>(blockIdx.x, (p.cols + kTile - 1) / kTile);
+  Raw8<DT> raw[RP];
+  load_tile<DT>(p.h, p.ldh, p.vec_h, row0, col0, p.rows, p.cols, raw);
+  cast_raw_rows<DT, FP8_E4M3>(raw, p.cq, p.cs, p.ldc, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
+  if (!p.aq && !p.a) return;
+  float f[RP][8];
 #pragma unroll
-      for (int i = 0; i < RP; i++) {
-        unpack8<DT>(raw[i], f[i]);
+  for (int i = 0; i < RP; i++) {
+    unpack8<DT>(raw[i], f[i]);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float2 h = make_float2(f[i][j], f[i][j + 1]);
-          float2 y, q, r;
-          gate2<ACT, false>(h, y, q, r);
-          const float2 a = act_value2(h, y, q);
-          f[i][j] = a.x;
-          f[i][j + 1] = a.y;
-        }
-      }
-      if (p.a) store_tile<DT>(p.vec_a, p.a, p.lda, row0, col0, p.rows, p.cols, f);
-      if (p.aq) cast_tile_rows<FP8_E4M3>(f, p.aq, p.as, p.lda_q, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
+    for (int j = 0; j < 8; j += 2) {
+      const float2 h = make_float2(f[i][j], f[i][j + 1]);
+      float2 y, q, r;
+      gate2<ACT, false>(h, y, q, r);
+      const float2 a = act_value2(h, y, q);
+      f[i][j] = a.x;
+      f[i][j + 1] = a.y;
     }
   }
+  if (p.a) store_tile<DT>(p.vec_a, p.a, p.lda, row0, col0, p.rows, p.cols, f);
+  if (p.aq) cast_tile_rows<FP8_E4M3>(f, p.aq, p.as, p.lda_q, row0, col0, p.rows, p.cols, kMaxE4M3, p.margin);
 }
 
 struct ActBwd {

@@ -367,41 +367,39 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncwarp();
   } else if (warp == 1) {
-    {
-      const bool elected = elect_one();
-      const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0), b_d0 = (uint32_t)operand_desc<B_MN>(base + BM * BK, 0);
-      constexpr uint32_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4, b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
-      const uint32_t st_d = args.stage_bytes >> 4, sf_tmem = tmem_base + args.bn;
-      int stage = 0, set = kSfSets - 1;
-      uint32_t phase = 0;
-      bool ok = true, issued_any = false;
-      for (int kb = kb0; kb < kb1; kb++) {
-        if (!warp_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
-        if (kb == kb0 || (kb & 3) == 0) {
-          set = set == kSfSets - 1 ? 0 : set + 1;
-          if (elected) {
-            tc_cp_scales(sf_tmem + set * kSfCols, scale_desc(sf0 + stage * kSfSlot));
-            tc_cp_scales(sf_tmem + set * kSfCols + 4, scale_desc(sf0 + stage * kSfSlot + 512));
-          }
-        }
-        const uint32_t sfa = sf_tmem + set * kSfCols, so = (uint32_t)stage * st_d;
-        const uint32_t idesc = with_scale_ids(args.idesc, kb);
+    const bool elected = elect_one();
+    const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0), b_d0 = (uint32_t)operand_desc<B_MN>(base + BM * BK, 0);
+    constexpr uint32_t a_ks = A_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4, b_ks = B_MN ? (UMMA_K * 128) >> 4 : UMMA_K >> 4;
+    const uint32_t st_d = args.stage_bytes >> 4, sf_tmem = tmem_base + args.bn;
+    int stage = 0, set = kSfSets - 1;
+    uint32_t phase = 0;
+    bool ok = true, issued_any = false;
+    for (int kb = kb0; kb < kb1; kb++) {
+      if (!warp_ready(full_bar(stage), phase, abort_flag)) { ok = false; break; }
+      if (kb == kb0 || (kb & 3) == 0) {
+        set = set == kSfSets - 1 ? 0 : set + 1;
         if (elected) {
-#pragma unroll
-          for (int ks = 0; ks < BK / UMMA_K; ks++)
-            tc_mma_bs(tmem_base, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfa + 4,
-                      (kb != kb0 || ks != 0) ? 1u : 0u);
-          tc_commit(empty_bar(stage));
+          tc_cp_scales(sf_tmem + set * kSfCols, scale_desc(sf0 + stage * kSfSlot));
+          tc_cp_scales(sf_tmem + set * kSfCols + 4, scale_desc(sf0 + stage * kSfSlot + 512));
         }
-        issued_any = true;
-        if (++stage == S) { stage = 0; phase ^= 1u; }
       }
-      if (ok) {
-        if (elected) tc_commit(tfull_bar);
-      } else if (issued_any) {
-        if (elected) tc_commit(drain_bar);
-        mbar_wait_drain(drain_bar, 0);
+      const uint32_t sfa = sf_tmem + set * kSfCols, so = (uint32_t)stage * st_d;
+      const uint32_t idesc = with_scale_ids(args.idesc, kb);
+      if (elected) {
+#pragma unroll
+        for (int ks = 0; ks < BK / UMMA_K; ks++)
+          tc_mma_bs(tmem_base, a_d0 + so + ks * a_ks, b_d0 + so + ks * b_ks, args.desc_hi, idesc, sfa, sfa + 4,
+                    (kb != kb0 || ks != 0) ? 1u : 0u);
+        tc_commit(empty_bar(stage));
       }
+      issued_any = true;
+      if (++stage == S) { stage = 0; phase ^= 1u; }
+    }
+    if (ok) {
+      if (elected) tc_commit(tfull_bar);
+    } else if (issued_any) {
+      if (elected) tc_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0);
     }
     __syncwarp();
   } else {

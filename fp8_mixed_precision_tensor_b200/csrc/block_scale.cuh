@@ -28,8 +28,6 @@
 namespace fp8lib {
 namespace block {
 
-constexpr int kBlock = 128;
-
 __host__ __device__ inline size_t scale_groups(int outer, int red) {
   const size_t rb = ((size_t)outer + 127) / 128, kb = ((size_t)red + 127) / 128;
   return rb * ((kb + 3) / 4);
@@ -296,13 +294,7 @@ __device__ __forceinline__ void put_scale(uint8_t *s, int r, int b, int kblocks,
     for (int j = (b & 3) + 1; j < 4; j++) p[j - (b & 3)] = 127;
 }
 
-__device__ __forceinline__ uint32_t max16(uint32_t v) {  // over the 16 lanes of a row
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
-// Where a cast writes: 1x128 blocks (q, s), 128x1 blocks (qt, st); either q may be null.
+// Where a cast writes: 1x128 blocks (q, s), 128x1 blocks (qt, st).
 struct CastOut {
   uint8_t *q, *s;
   uint8_t *qt, *st;
@@ -570,51 +562,43 @@ __global__ void __launch_bounds__(Geo<RP>::kThreads, RP == 2 ? 1 : DT == FP8_DT_
   pdl_wait();
   __shared__ ColScratch<RP> sc;
   const float fmax = FMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
-  const int tiles_c = (cols + kTile - 1) / kTile;
-  const int c8 = threadIdx.x & 15;
-  {
-    const auto [row0, col0] = tile_at(blockIdx.x, tiles_c);
-    const int col = col0 + c8 * 8;
-    Raw8<DT> raw[RP];
-    load_tile<DT>(x, ldx, vec, row0, col0, rows, cols, raw);
-    if (out.qt) {  // the column maxima go out first: their barriers overlap the row side
-      uint32_t w[Raw8<DT>::kWords], m[8];
+  const auto [row0, col0] = tile_at(blockIdx.x, (cols + kTile - 1) / kTile);
+  Raw8<DT> raw[RP];
+  load_tile<DT>(x, ldx, vec, row0, col0, rows, cols, raw);
+  // the column maxima go out first: their barriers overlap the row side
+  uint32_t w[Raw8<DT>::kWords], m[8];
 #pragma unroll
-      for (int j = 0; j < Raw8<DT>::kWords; j++) {
-        w[j] = 0;
+  for (int j = 0; j < Raw8<DT>::kWords; j++) {
+    w[j] = 0;
 #pragma unroll
-        for (int i = 0; i < RP; i++) w[j] = max_words<DT>(w[j], raw[i].w[j]);
-        if constexpr (DT == FP8_DT_F32) {
-          m[j] = w[j];
-        } else {
-          m[2 * j] = widen_abs<DT>(w[j] & 0xffffu);
-          m[2 * j + 1] = widen_abs<DT>(w[j] >> 16);
-        }
-      }
-      put_column_maxima(sc, m);
-    }
-    if (out.q) cast_raw_rows<DT, FMT>(raw, out.q, out.s, out.ldq, row0, col0, rows, cols, fmax, margin);
-    if (out.qt) {
-      float2 s[4];
-      const bool bad = column_scales(sc, out.st, row0, col0, rows, fmax, margin, s);
-      uint2 o[RP];
-#pragma unroll
-      for (int i = 0; i < RP; i++) {
-        float f[8];
-        unpack8<DT>(raw[i], f);
-        o[i] = enc8<FMT>(f, s);
-      }
-      if (bad) {
-#pragma unroll
-        for (int i = 0; i < RP; i++) {
-          float f[8];
-          unpack8<DT>(raw[i], f);
-          o[i] = enc8_any<FMT>(f, s);
-        }
-      }
-      store_codes(out.qt, out.ldqt, row0, col, rows, cols, o);
+    for (int i = 0; i < RP; i++) w[j] = max_words<DT>(w[j], raw[i].w[j]);
+    if constexpr (DT == FP8_DT_F32) {
+      m[j] = w[j];
+    } else {
+      m[2 * j] = widen_abs<DT>(w[j] & 0xffffu);
+      m[2 * j + 1] = widen_abs<DT>(w[j] >> 16);
     }
   }
+  put_column_maxima(sc, m);
+  if (out.q) cast_raw_rows<DT, FMT>(raw, out.q, out.s, out.ldq, row0, col0, rows, cols, fmax, margin);
+  float2 s[4];
+  const bool bad = column_scales(sc, out.st, row0, col0, rows, fmax, margin, s);
+  uint2 o[RP];
+#pragma unroll
+  for (int i = 0; i < RP; i++) {
+    float f[8];
+    unpack8<DT>(raw[i], f);
+    o[i] = enc8<FMT>(f, s);
+  }
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < RP; i++) {
+      float f[8];
+      unpack8<DT>(raw[i], f);
+      o[i] = enc8_any<FMT>(f, s);
+    }
+  }
+  store_codes(out.qt, out.ldqt, row0, col0 + (threadIdx.x & 15) * 8, rows, cols, o);
 }
 
 // Cast of x to 128x128 blocks: one set of codes, the block's scale repeated
@@ -630,29 +614,25 @@ __global__ void __launch_bounds__(Geo<RP>::kThreads, RP == 2 ? 1 : DT == FP8_DT_
   __shared__ uint32_t red[32];
   const float fmax = FMT == FP8_E4M3 ? kMaxE4M3 : kMaxE5M2;
   const int tiles_c = (cols + kTile - 1) / kTile, tiles_r = (rows + kTile - 1) / kTile;
-  const int c8 = threadIdx.x & 15;
-  {
-    const auto [row0, col0] = tile_at(blockIdx.x, tiles_c);
-    const int col = col0 + c8 * 8;
-    Raw8<DT> raw[RP];
-    load_tile<DT>(x, ldx, vec, row0, col0, rows, cols, raw);
-    uint32_t w = 0;
+  const auto [row0, col0] = tile_at(blockIdx.x, tiles_c);
+  Raw8<DT> raw[RP];
+  load_tile<DT>(x, ldx, vec, row0, col0, rows, cols, raw);
+  uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < RP; i++)
+  for (int i = 0; i < RP; i++)
 #pragma unroll
-      for (int j = 0; j < Raw8<DT>::kWords; j++) w = max_words<DT>(w, raw[i].w[j]);
-    const uint32_t m = block_max_u32(word_abs<DT>(w), red);
-    const int k = block_exponent(m, fmax, margin);
-    if (threadIdx.x < kTile) {
-      const int r = row0 + threadIdx.x, c = col0 + threadIdx.x;
-      put_scale(out.s, r, col0 / kTile, tiles_c, r < rows ? k : 0);
-      put_scale(out.st, c, row0 / kTile, tiles_r, c < cols ? k : 0);
-    }
-    float sc[RP];
-#pragma unroll
-    for (int i = 0; i < RP; i++) sc[i] = pow2f(k);
-    store_raw_rows<DT, FMT>(raw, sc, m >= 0x7f800000u, out.q, out.ldq, row0, col, rows, cols);
+    for (int j = 0; j < Raw8<DT>::kWords; j++) w = max_words<DT>(w, raw[i].w[j]);
+  const uint32_t m = block_max_u32(word_abs<DT>(w), red);
+  const int k = block_exponent(m, fmax, margin);
+  if (threadIdx.x < kTile) {
+    const int r = row0 + threadIdx.x, c = col0 + threadIdx.x;
+    put_scale(out.s, r, col0 / kTile, tiles_c, r < rows ? k : 0);
+    put_scale(out.st, c, row0 / kTile, tiles_r, c < cols ? k : 0);
   }
+  float sc[RP];
+#pragma unroll
+  for (int i = 0; i < RP; i++) sc[i] = pow2f(k);
+  store_raw_rows<DT, FMT>(raw, sc, m >= 0x7f800000u, out.q, out.ldq, row0, col0 + (threadIdx.x & 15) * 8, rows, cols);
 }
 
 // Eight codes at (row, col), 0 outside [rows, cols).
