@@ -996,7 +996,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto sffree_bar = [&](int b) { return bar0 + 8u * (2 * kP2Stages + 2 + b); };
   const uint32_t tempty_bar = bar0 + 8u * (2 * kP2Stages + 4);
   const uint32_t drain_bar = bar0 + 8u * (2 * kP2Stages + 5);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (bar0 - base) + 8 * (2 * kP2Stages + 6));
+  const uint32_t alloc_bar = bar0 + 8u * (2 * kP2Stages + 6);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base_ptr + (bar0 - base) + 8 * (2 * kP2Stages + 7));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1031,6 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(tempty_bar, 8);  // leader: 4 epilogue warps x 2 CTAs
     mbar_init(drain_bar, 1);
+    mbar_init(alloc_bar, 2);   // leader: the issuing warps of both CTAs
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_desc(&tmA);
@@ -1039,20 +1041,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmSB);
     if (args.vec_out) tma_prefetch_desc(&tmOut);
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(512u)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  }
-  tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised before any cross-CTA signal
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
-  // Not before the allocation: a dependent CTA that took tensor memory first
-  // and then waited for this kernel would wait for good.
-  pdl_launch_dependents();
+  // Tensor memory is taken when the stream's previous kernel has ended (by warp
+  // 1, beside the first loads), given back by both CTAs before either leaves,
+  // and the right to allocate with it.  A pair that allocated while CTAs of the
+  // previous kernels still came and went on its SMs, gave up the right at once
+  // and left without waiting for each other, once in some 10^7 pairs stood still
+  // for good: one CTA held its columns, the other waited for its own on an SM on
+  // which nothing else ran.  (1024^3 6.3 us then, 6.6 now; 2048^3 10.8 both ways.)
   pdl_wait();
+  constexpr uint32_t tmem_base = 0;  // where all 512 columns begin
 
   if (warp == 0) {
     // ------------------------------------------------------------ producers (both CTAs, one thread)
@@ -1087,7 +1085,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (leader)
+    // ------------------------------------------------------------ tensor memory, MMA issuer (leader)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    // Not before the allocation: a dependent CTA that took tensor memory first
+    // and then waited for this kernel would wait for good.
+    pdl_launch_dependents();
+    tc_fence_before();
+    if (lane == 0) mbar_arrive_remote(map_to_rank(alloc_bar, 0));
     if (leader) {
       const bool elected = elect_one();
       const uint32_t a_d0 = (uint32_t)operand_desc<A_MN>(base, 0);
@@ -1097,7 +1103,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t st_d = kPairStageBytes >> 4;
       int stage = 0, n = 0;
       uint32_t phase = 0, group = 0;
-      bool ok = true, issued_any = false;
+      bool ok = warp_ready(alloc_bar, 0, abort_flag), issued_any = false;
+      tc_fence_after();
       for (int tile = pair; tile < num_items && ok; tile += num_pairs, n++) {
         if (n > 0 && !warp_ready(tempty_bar, (uint32_t)(n - 1) & 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
@@ -1223,8 +1230,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // the leader's MMAs no longer read this CTA's smem / TMEM
   if (warp == 1) {
     tc_fence_after();
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u) : "memory");
   }
+  __syncwarp();
+  cluster_sync();  // neither CTA leaves before both have given their columns back
 }
 
 }  // namespace bgemm

@@ -1121,3 +1121,42 @@ def test_several_passes_in_flight():
             for got, ref in zip(layer.backward(dys[i]), want[i], strict=True):
                 assert torch.equal(got, ref)
         assert layer.kept is None
+
+
+def test_pairs_take_and_give_back_tensor_memory_many_times():
+    """Products on CTA pairs among other kernels of the stream, without a pause
+    and some millions of pairs long: a pair that waits for its tensor memory
+    for good would show once in about ten million.  In a process of its own,
+    so that it could be ended."""
+    code = """
+import torch
+from fp8_mixed_precision_tensor_b200 import fp8, synth
+C, S = fp8.block_codes, fp8.block_scales
+M, K, N = 2720, 167, 656
+x, w, dy = (synth.device_normal(s, v, 7, torch.bfloat16, "cuda") for s, v in (((M, K), 1.0), ((N, K), 0.02), ((M, N), 1e-3)))
+xq, xs, gq, gs, ck, cs = C(M, K), S(M, K), C(M, N), S(M, N), C(M, N), S(M, N)
+xqc, xsc, gqc, gsc, aq, a_s = C(M, K), S(K, M), C(M, N), S(N, M), C(M, N), S(M, N)
+wq, ws, wsc, w2, w2s, w2c = C(N, K), S(N, K), S(K, N), C(K, N), S(K, N), S(N, K)
+y, z, dx, dw = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((M, N), (M, K), (M, K), (N, K)))
+fp8.fp8_block_cast_square(w, 0, 0, wq, ws, wsc)
+fp8.fp8_block_cast_square(w.t().contiguous(), 0, 0, w2, w2s, w2c)
+def step():
+    fp8.fp8_block_cast(x, 0, 0, xq, xs, xqc, xsc)
+    fp8.fp8_block_linear_fwd(xq, xs, wq, ws, y)
+    fp8.fp8_act_fwd(y, 1, 0, ck, cs, aq, a_s)
+    fp8.fp8_block_linear_fwd(aq, a_s, w2, w2s, z)
+    fp8.fp8_block_cast(dy, 1, 0, gq, gs, gqc, gsc)
+    fp8.fp8_block_linear_wgrad(gqc, gsc, 1, xqc, xsc, dw)
+    fp8.fp8_block_linear_dgrad(gq, gs, 1, wq, wsc, dx)
+step()
+first = [t.clone() for t in (y, z, dx, dw)]
+for _ in range(40):
+    for _ in range(1000):
+        step()
+    torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, (y, z, dx, dw))) and fp8.fp8_get_status() == 0
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
