@@ -627,7 +627,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"((uint32_t)kPairTmemCols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised before any cross-CTA signal
@@ -736,11 +735,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   cluster_sync();  // the leader's MMAs no longer read this CTA's smem / TMEM
   if (warp == 1) {
+    // The right to allocate goes with the columns, and both CTAs leave together: a
+    // pair that gave it up at once and did not wait for its peer has been seen
+    // to wait for its columns for good (k_bgemm2 has the account).
     tc_fence_after();
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                  "r"((uint32_t)kPairTmemCols)
                  : "memory");
   }
+  __syncwarp();
+  cluster_sync();
 }
 
 
@@ -814,7 +819,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(512u)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   cluster_sync();
@@ -1045,9 +1049,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");  // as k_gemm2
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u)
                  : "memory");
   }
+  __syncwarp();
+  cluster_sync();
 }
 
 }  // namespace gemm
