@@ -38,7 +38,8 @@ namespace block {
 // These kernels were bound by the ALU pipe (minima, selects, logic: half the
 // rate of FMA), so the arithmetic is on the packed binary32 instructions and
 // the rest as little as it can be: 43 -> 24 instructions per element forward,
-// 63 -> 42 backward (4096 x 16384 bfloat16: 107 -> 91 us, 200 -> 164).
+// 63 -> 42 backward, a sixth of the time then.  The erf form calls erfcf for
+// every element and takes twice as long (times beside the kernels).
 // ex2.approx and rcp.approx are within 2 units in the last place, and the
 // argument's rounding adds about |u| units to exp(-u); exp(-u) below 2^-126
 // counts as 0.
@@ -139,8 +140,8 @@ struct ActFwd {
 };
 
 // h is read once (2 B at 16 bits), one or two code bytes and / or a are written;
-// 4096 x 16384 bfloat16 with a itself 62 us (5.4 TB/s), with its codes 60, bound
-// by the issue slots.  Four rows per thread: act(h) of a thread's 32
+// 4096 x 16384 bfloat16 with a itself 63 us (5.4 TB/s; SiLU 62, GELU by erf 145),
+// with its codes 61 (59, 149), bound by the issue slots (66 and 73 % busy).  Four rows per thread: act(h) of a thread's 32
 // elements waits in registers for its rows' amaxes (eight rows each needed
 // 184 registers and ran at a third of the occupancy).
 template <int DT, int ACT, int RP>
@@ -245,7 +246,8 @@ __device__ __forceinline__ void act_bwd_non_finite(const ActBwd &p, int row0, in
 // dh alone: parts of tiles, as k_act_fwd.  float32 with two rows per thread and
 // ten CTAs per SM, 16-bit types with four and eight: 4096 x 16384 float32 91 us
 // (6.6 TB/s; four rows 101, a persistent CTA of 512 threads 139), bfloat16 73
-// (4.6; two rows 76, persistent 72; without the search for infinities 72).
+// (4.6; SiLU 69, GELU by erf 156; two rows 76, persistent 72; without the search
+// for infinities 72), 73 % of the issue slots busy.
 template <int DT>
 constexpr int kPlainRows = DT == FP8_DT_F32 ? 2 : 4;
 template <int DT, int ACT, int RP>
@@ -308,8 +310,10 @@ struct ActBwdSmem {
 // written.  dh and act(h') of a thread's 32 elements stay in registers between
 // the amaxes and the encoding, which leaves room for one CTA of 16 warps per
 // SM; the next tile's inputs are copied into shared memory meanwhile.  Bound by
-// instruction issue as much as by HBM (63 % of the slots, 33 % of the DRAM
-// cycles): 4096 x 16384 bfloat16 to the codes of all three 130 to 158 us.
+// latency (one CTA, two barriers a tile) and instruction issue (62 % of the
+// slots, 31 % of the DRAM cycles): 4096 x 16384 bfloat16 to the codes of all
+// three 130 us, up to 158 in a long run (SiLU 126, GELU by erf 221; float32 176,
+// 168, 262).
 // OUT: the format of dh's codes.
 template <int DT, int ACT, int OUT>
 __global__ void __launch_bounds__(kActThreads, 1) k_act_bwd(const ActBwd p) {

@@ -136,8 +136,9 @@ __device__ __forceinline__ void store_one(const BArgs &a, size_t at, float y) {
 // stores; reading the others' parts instead cost 12 us at 128 columns), and
 // each adds the S parts of its own tokens in rank order and stores them: no
 // workspace, no atomics, the same bits each time.  Bound by latencies: start 3
-// us, exchange 3, a k-block of a CTA 0.3 (33 x 12288 x 4096: 9.2 us; 300 x 520 x
-// 2056 8.1; 256 x 256 x 16384 10).
+// us, exchange 3, a k-block of a CTA 0.3 (operands in L2: 33 x 12288 x 4096 9.6
+// us, 300 x 520 x 2056 7.9, 256 x 256 x 16384 10; weights from HBM: 33 x 12288 x
+// 4096 13.6).
 //   warp 0 TMA producer, warp 1 TMEM allocation and MMA issue, warps 2-5 epilogue.
 constexpr int kSfCols = 8;      // tensor-memory columns of one set of scales: 4 of A, 4 of B
 constexpr int kSfSets = 3;
@@ -442,9 +443,9 @@ __global__ void __launch_bounds__(kThreads)
 // that the end of the reduction needs no cluster-wide barrier (two of them and
 // the exchange took 2.7 us).
 // Bound by the weights' HBM traffic, and below about 30 MB by the latencies of
-// start, cast and exchange.  Weights in HBM: 12288 x 4096 at one token 14.7 us
-// (3.4 TB/s; 16 at 32 tokens), 12288 x 12288 28.3 (5.3), 4096 x 4096 at 16
-// tokens 8.5.
+// start, cast and exchange.  Weights from HBM: 12288 x 4096 at one token 14.7 us
+// (3.4 TB/s; 16 at 32 tokens; cast and k_bgemm in two launches 15), 12288 x 12288
+// 28 to 30 (5 TB/s), 4096 x 4096 at 16 tokens 8.4.  In L2 12288 x 4096 takes 11.6.
 constexpr int kTokMaxStages = 6;
 constexpr int kTokBN = 256;    // weight rows per tile
 constexpr int kTokBatch = 8;   // tokens that one cast takes

@@ -756,7 +756,11 @@ __device__ __forceinline__ void store_tile(bool vec, void *out, size_t ld, int r
 }
 
 // Decode of blocked codes: x = dec(q) * 2^(byte - 127).  COLS: 128x1 blocks
-// (scales of the transposed order), else 1x128 (or square) blocks.
+// (scales of the transposed order), else 1x128 (or square) blocks.  1 B read and
+// 2 written: 8192 x 12288 to bfloat16 70 us (4.3 TB/s; two thirds of the issue
+// slots busy, with a 64-bit division per eight elements), from 128x1 blocks 152,
+// where each element has a scale byte of its own to fetch.  No product and no
+// pass of a layer goes through it.
 template <int DT, int FMT, bool COLS>
 __global__ void __launch_bounds__(kCastThreads)
     k_block_decode(const uint8_t *__restrict__ q, const uint8_t *__restrict__ s, int rows, int cols, size_t ldq,
