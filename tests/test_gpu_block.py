@@ -1160,3 +1160,36 @@ print("ok")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
+
+
+def test_products_read_what_the_kernels_before_them_have_just_written():
+    """The few-token form brings x and weights into L2 before the kernel in
+    front of it has ended; operands that change from call to call, without a
+    pause, give what they give with a pause after every kernel."""
+    M, N, K, n = 24, 2304, 2048, 40
+    C, S = fp8.block_codes, fp8.block_scales
+    hs = [synth.device_normal((M, K), 1.0, 200 + i, BF16, "cuda") for i in range(n)]
+    w32 = [synth.device_normal((N, K), 0.02, 300 + i, BF16, "cuda") for i in range(4)]
+    ck, cs, x, wq, ws, wsc = C(M, K), S(M, K), torch.empty_like(hs[0]), C(N, K), S(N, K), S(K, N)
+    xq, xs = C(M, K), S(M, K)
+    got = {}
+    for pause in (False, True):
+        ys = [torch.empty((M, N), dtype=BF16, device="cuda") for _ in range(3 * n)]
+        wait = torch.cuda.synchronize if pause else (lambda: None)
+        for _ in range(5):
+            for i in range(n):
+                for f in (lambda: fp8.fp8_block_cast_square(w32[i % 4], 0, 0, wq, ws, wsc),
+                          lambda: fp8.fp8_act_fwd(hs[i], fp8.FP8_ACT_SILU, 0, ck, cs, a=x),
+                          lambda: fp8.fp8_block_linear_tokens(x, wq, ws, ys[3 * i]),
+                          lambda: fp8.fp8_block_decode(ck, cs, fp8.FP8_E4M3, 1, x),
+                          lambda: fp8.fp8_block_linear_tokens(x, wq, ws, ys[3 * i + 1]),
+                          lambda: fp8.fp8_block_cast(x, fp8.FP8_E4M3, 0, xq, xs),
+                          lambda: fp8.fp8_block_linear_fwd(xq, xs, wq, ws, ys[3 * i + 2])):
+                    f()
+                    wait()
+        torch.cuda.synchronize()
+        got[pause] = ys
+    for a, b in zip(got[False], got[True]):
+        assert torch.equal(a, b)
+    assert len({float(y.float().sum()) for y in got[True]}) > n
+    assert fp8.fp8_get_status() == 0
