@@ -26,11 +26,15 @@ CALLS_PATH = os.path.join(_HERE, "_calls.so")
 FP8_OK, FP8_ERR_INVALID_ARG, FP8_ERR_UNALIGNED, FP8_ERR_UNSUPPORTED = 0, 1, 2, 3
 FP8_ERR_CUDA, FP8_ERR_TIMEOUT, FP8_ERR_NONFINITE = 4, 5, 6
 FP8_STATUS_NONFINITE, FP8_STATUS_TIMEOUT, FP8_STATUS_INTERNAL, FP8_STATUS_BAD_MU = 1, 2, 4, 8
+FP8_STATUS_BAD_INDEX = 16
 FP8_DT_F32, FP8_DT_BF16, FP8_DT_F16 = 0, 1, 2
 FP8_DT_BF16_RTO = 3  # GEMM outputs only: bfloat16 rounded to odd, for a following FP8 cast
 FP8_E4M3, FP8_E5M2, FP8_F16S = 0, 1, 2
 FP8_ACT_GELU_TANH, FP8_ACT_GELU_ERF, FP8_ACT_SILU = 0, 1, 2
 FP8_BLOCK_TOKENS_MAX = 32
+FP8_NORM_NONE, FP8_NORM_RMS, FP8_NORM_LAYER = 0, 1, 2
+FP8_NORM_COLS_MAX, FP8_TOP_MAX, FP8_DISTILL_MAX, FP8_DISTILL_COLS_MAX = 32768, 32, 1024, 1048576
+FP8_DISTILL_TOP, FP8_DISTILL_TAIL = 0, 1
 
 _DT = {torch.float32: FP8_DT_F32, torch.bfloat16: FP8_DT_BF16, torch.float16: FP8_DT_F16}
 
@@ -44,6 +48,8 @@ SYMBOLS = ("fp8_amax", "fp8_compute_scale", "fp8_cast", "fp8_scale_cast", "fp8_a
            "fp8_block_scale_bytes", "fp8_block_cast", "fp8_block_cast_square", "fp8_block_decode",
            "fp8_block_linear_fwd", "fp8_block_linear_tokens", "fp8_block_linear_dgrad", "fp8_block_linear_wgrad",
            "fp8_act_fwd", "fp8_act_bwd",
+           "fp8_norm_workspace_bytes", "fp8_norm_fwd", "fp8_norm_bwd", "fp8_logprob_fwd", "fp8_logprob_bwd",
+           "fp8_distill_fwd", "fp8_distill_bwd",
            "fp8_selftest_wait_timeout", "fp8_selftest_step_reciprocal", "fp8_selftest_encode", "fp8_get_status", "fp8_strerror")
 
 
@@ -76,6 +82,22 @@ class _MuRule(ctypes.Structure):
 
 class _Blocks(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("ld", ctypes.c_size_t)]
+
+
+class _Vec(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("dtype", ctypes.c_int)]
+
+
+class _NormParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int),
+                ("pre", ctypes.c_int), ("post", ctypes.c_int), ("w", _Vec), ("b", _Vec), ("post_w", _Vec),
+                ("post_b", _Vec), ("gate", _Vec), ("gate_rows", ctypes.c_int), ("ld_gate", ctypes.c_size_t),
+                ("res_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class _NormGrads(ctypes.Structure):
+    _fields_ = [("w", _Vec), ("b", _Vec), ("post_w", _Vec), ("post_b", _Vec), ("gate", _Vec),
+                ("ld_gate", ctypes.c_size_t)]
 
 
 class _HParams(ctypes.Structure):
@@ -166,13 +188,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp8_block_linear_wgrad.argtypes = [b, i, b, p, i, sz, i, i, i, p]
     lib.fp8_act_fwd.argtypes = [p, i, i, i, sz, i, i, b, b, p, sz, p]
     lib.fp8_act_bwd.argtypes = [b, p, i, i, i, sz, i, i, i, b, b, b, p, sz, p]
+    n = ctypes.POINTER(_NormParams)
+    lib.fp8_norm_workspace_bytes.argtypes, lib.fp8_norm_workspace_bytes.restype = [i, i, i], sz
+    lib.fp8_norm_fwd.argtypes = [n, p, sz, p, sz, p, sz, p, p, sz, i, b, b, p]
+    lib.fp8_norm_bwd.argtypes = [n, p, sz, p, sz, p, sz, p, sz, p, p, sz, p, sz, ctypes.POINTER(_NormGrads), p, sz, p]
+    lib.fp8_logprob_fwd.argtypes = [p, i, i, i, sz, f, p, i, p, p, i, p, p, p, p]
+    lib.fp8_logprob_bwd.argtypes = [p, i, i, i, sz, f, p, i, p, p, p, i, i, b, b, p, sz, p]
+    lib.fp8_distill_fwd.argtypes = [p, i, i, i, sz, f, i, i, p, i, p, i, p, p, p, p, p]
+    lib.fp8_distill_bwd.argtypes = [p, i, i, i, sz, f, i, p, p, p, p, i, i, b, b, p, sz, p]
     lib.fp8_selftest_wait_timeout.argtypes = [ctypes.c_uint, p]
     lib.fp8_selftest_step_reciprocal.argtypes = [ctypes.c_uint, ctypes.c_ulonglong, p, p, p]
     lib.fp8_selftest_encode.argtypes = [i, ctypes.c_uint, ctypes.c_ulonglong, p, p, p]
     lib.fp8_get_status.argtypes = [ctypes.POINTER(ctypes.c_uint), p]
     lib.fp8_strerror.argtypes, lib.fp8_strerror.restype = [i], ctypes.c_char_p
     for name in SYMBOLS:
-        if name not in ("fp8_adam_workspace_bytes", "fp8_block_scale_bytes", "fp8_strerror"):
+        if name not in ("fp8_adam_workspace_bytes", "fp8_block_scale_bytes", "fp8_norm_workspace_bytes", "fp8_strerror"):
             getattr(lib, name).restype = i
     _calls = _bound_calls(lib)
     _lib = lib
@@ -715,6 +745,183 @@ def fp8_act_bwd(ckpt_q, ckpt_s, da, act: int, fmt: int = FP8_E5M2, margin: int =
                                       _blocks(dh_q_col, dh_s_col, "dh column blocks", rows, cols, cols, rows, dev),
                                       _blocks(a_q_col, a_s_col, "a column blocks", rows, cols, cols, rows, dev),
                                       hp, lddh, _stream(stream)), "fp8_act_bwd")
+
+
+# ---------------------------------------------------------------- norms with gate and residual
+def _optional(t, what: str, rows: int, cols: int, dev: int, dtype) -> tuple[int | None, int]:
+    """(pointer, row stride) of an optional [rows, cols] matrix of this type."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    return t.data_ptr(), _matrix(t, what, rows, cols, dev)
+
+
+def _vec(t, what: str, n: int, dev: int) -> _Vec:
+    return _Vec(None, 0) if t is None else _Vec(*_vector(t, what, n, dev))
+
+
+def _gate(t, what: str, rows: int, cols: int, dev: int) -> tuple[_Vec, int, int]:
+    """A gate of [cols] or [gates, cols] (each for rows / gates rows): (vector, its rows, row stride)."""
+    if t is None:
+        return _Vec(None, 0), max(rows, 1), cols
+    if t.dim() == 1:
+        return _vec(t, what, cols, dev), max(rows, 1), cols
+    dt = _hp(t, what)
+    gates = _sides(t.shape, what)[0]
+    if gates < 1 or rows % gates:
+        raise ValueError(f"{what}: {gates} rows for {rows} rows of the matrix")
+    return _Vec(t.data_ptr(), dt), max(rows // gates, 1), _matrix(t, what, gates, cols, dev)
+
+
+def _f32(t, what: str, shape: tuple, dev: int, dtype=torch.float32) -> int | None:
+    """Pointer of an optional contiguous tensor of this shape."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{what}: {shape} contiguous elements on cuda:{dev} expected, got {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def fp8_norm_workspace_bytes(rows: int, cols: int, gate_rows: int | None = None) -> int:
+    """Bytes of workspace that fp8_norm_bwd needs for gradients of parameters;
+    gate_rows: rows of the matrix to one row of the gate (all of them)."""
+    return load_library().fp8_norm_workspace_bytes(rows, cols, rows if gate_rows is None else gate_rows)
+
+
+def _norm_params(lead, res, dev, rows, cols, pre, post, w, b, post_w, post_b, gate, res_scale, eps):
+    g, gate_rows, ldg = _gate(gate, "gate", rows, cols, dev)
+    return _NormParams(rows, cols, _hp(lead, "h, x"), _hp(res, "r"), pre, post, _vec(w, "w", cols, dev),
+                       _vec(b, "b", cols, dev), _vec(post_w, "post_w", cols, dev), _vec(post_b, "post_b", cols, dev), g,
+                       gate_rows, ldg, res_scale, eps)
+
+
+def fp8_norm_fwd(h, r, r_out, stats, *, pre: int = FP8_NORM_RMS, post: int = FP8_NORM_NONE, w=None, b=None, post_w=None,
+                 post_b=None, gate=None, res_scale: float = 1.0, eps: float = 1e-5, margin: int = 0, x=None, x_q=None,
+                 x_s=None, x_q_col=None, x_s_col=None, stream=None) -> None:
+    """r_out = res_scale * r + gate * u with u = post_norm(h) or h, and the
+    pre-norm of r_out as x (h's dtype), as E4M3 codes of its 1x128 blocks (x_q,
+    x_s) and of its 128x1 blocks (x_q_col, x_s_col).  r and r_out are h's dtype
+    or float32.  h may be None (r_out is res_scale * r, and may be None for a
+    scale of 1); x then gives the dtype, or else r.  gate: [cols], or [gates, cols], each
+    row for rows / gates rows.  stats: [rows, 4] float32 for the backward pass,
+    or None."""
+    rt, rows, cols, ldr, dev = _input(r, "r")
+    lead = h if h is not None else x if x is not None else r
+    p = _norm_params(lead, r, dev, rows, cols, pre, post, w, b, post_w, post_b, gate, res_scale, eps)
+    _check(load_library().fp8_norm_fwd(
+        p, *_optional(h, "h", rows, cols, dev, lead.dtype), r.data_ptr(), ldr,
+        *_optional(r_out, "r_out", rows, cols, dev, r.dtype), _f32(stats, "stats", (rows, 4), dev),
+        *_optional(x, "x", rows, cols, dev, lead.dtype), margin,
+        _blocks(x_q, x_s, "x row blocks", rows, cols, rows, cols, dev),
+        _blocks(x_q_col, x_s_col, "x column blocks", rows, cols, cols, rows, dev), _stream(stream)), "fp8_norm_fwd")
+
+
+def fp8_norm_bwd(dx, dr_out, h, r_out, stats, *, pre: int = FP8_NORM_RMS, post: int = FP8_NORM_NONE, w=None,
+                 post_w=None, post_b=None, gate=None, res_scale: float = 1.0, dh=None, dr=None, dw=None, db=None,
+                 dpost_w=None, dpost_b=None, dgate=None, workspace=None, stream=None) -> None:
+    """Gradients of fp8_norm_fwd from dx (None without a pre-norm) and dr_out
+    (the gradient of r_out from what follows, or None): dh, dr and those of the
+    parameters (each in its own dtype), any of them.  workspace: uint8, at least
+    fp8_norm_workspace_bytes(rows, cols, rows // gates), where a parameter's
+    gradient is wanted."""
+    lead = next((t for t in (dx, dh, h) if t is not None), None)
+    res = next((t for t in (r_out, dr_out, dr) if t is not None), None)
+    first = lead if lead is not None else res
+    if first is None:
+        raise ValueError("a gradient is needed: dx or dr_out")
+    _, rows, cols, _, dev = _input(first, "dx" if dx is not None else "dr_out")
+    lead, res = first if lead is None else lead, first if res is None else res
+    p = _norm_params(lead, res, dev, rows, cols, pre, post, w, None, post_w, post_b, gate, res_scale, 0.0)
+    g, _, ldg = _gate(dgate, "dgate", rows, cols, dev)
+    if dgate is not None and (gate is None or dgate.shape != gate.shape):
+        raise ValueError("dgate has gate's shape")
+    grads = _NormGrads(_vec(dw, "dw", cols, dev), _vec(db, "db", cols, dev), _vec(dpost_w, "dpost_w", cols, dev),
+                       _vec(dpost_b, "dpost_b", cols, dev), g, ldg)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace: contiguous memory on cuda:{dev} expected")
+    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(load_library().fp8_norm_bwd(
+        p, *_optional(dx, "dx", rows, cols, dev, lead.dtype), *_optional(dr_out, "dr_out", rows, cols, dev, res.dtype),
+        *_optional(h, "h", rows, cols, dev, lead.dtype), *_optional(r_out, "r_out", rows, cols, dev, res.dtype),
+        _f32(stats, "stats", (rows, 4), dev), *_optional(dh, "dh", rows, cols, dev, lead.dtype),
+        *_optional(dr, "dr", rows, cols, dev, res.dtype), grads, *ws, _stream(stream)), "fp8_norm_bwd")
+
+
+# ---------------------------------------------------------------- log probabilities, distillation
+def _indices(t, what: str, shape: tuple, dev: int) -> tuple[int | None, int]:
+    """(pointer, bytes of an index) of optional int32 or int64 indices."""
+    if t is None:
+        return None, 0
+    if t.dtype is not torch.int64 and t.dtype is not torch.int32:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected int32 or int64")
+    return _f32(t, what, shape, dev, t.dtype), t.element_size()
+
+
+def fp8_logprob_fwd(logits, tokens, logp, stats, *, inv_temp: float = 1.0, entropy=None, top_logp=None, top_ids=None,
+                    stream=None) -> None:
+    """logp [rows] of the tokens [rows] (int32 or int64; negative: absent, logp
+    0) under softmax(inv_temp * logits); optionally entropy [rows], and the
+    largest log probabilities top_logp [rows, n] with their places top_ids
+    (int32), ties to the lowest.  tokens and logp may be None.  stats: [rows, 4]
+    float32 for the backward pass, or None."""
+    dt, rows, cols, ld, dev = _input(logits, "logits")
+    top = 0 if top_logp is None else _sides(top_logp.shape, "top_logp")[1]
+    _check(load_library().fp8_logprob_fwd(
+        logits.data_ptr(), dt, rows, cols, ld, inv_temp, *_indices(tokens, "tokens", (rows,), dev),
+        _f32(logp, "logp", (rows,), dev), _f32(entropy, "entropy", (rows,), dev), top,
+        _f32(top_logp, "top_logp", (rows, top), dev), _f32(top_ids, "top_ids", (rows, top), dev, torch.int32),
+        _f32(stats, "stats", (rows, 4), dev), _stream(stream)), "fp8_logprob_fwd")
+
+
+def fp8_logprob_bwd(logits, tokens, stats, dlogp, *, inv_temp: float = 1.0, dentropy=None, fmt: int = FP8_E5M2,
+                    margin: int = 0, d_q=None, d_s=None, d_q_col=None, d_s_col=None, dlogits=None, stream=None) -> None:
+    """The gradient of the logits from dlogp [rows] and dentropy [rows] (either
+    may be None): codes of its 1x128 blocks (d_q, d_s) and 128x1 blocks (d_q_col,
+    d_s_col), and itself in the logits' dtype (dlogits, which may be logits); any
+    of them.  dentropy needs a forward pass that computed the entropy."""
+    dt, rows, cols, ld, dev = _input(logits, "logits")
+    _check(load_library().fp8_logprob_bwd(
+        logits.data_ptr(), dt, rows, cols, ld, inv_temp, *_indices(tokens, "tokens", (rows,), dev),
+        _f32(stats, "stats", (rows, 4), dev), _f32(dlogp, "dlogp", (rows,), dev),
+        _f32(dentropy, "dentropy", (rows,), dev), fmt, margin,
+        _blocks(d_q, d_s, "row blocks", rows, cols, rows, cols, dev),
+        _blocks(d_q_col, d_s_col, "column blocks", rows, cols, cols, rows, dev),
+        *_optional(dlogits, "dlogits", rows, cols, dev, logits.dtype), _stream(stream)), "fp8_logprob_bwd")
+
+
+def fp8_distill_fwd(logits, ids, values, loss, stats, list_ids, list_q, *, form: int = FP8_DISTILL_TOP,
+                    inv_temp: float = 1.0, stream=None) -> None:
+    """loss [rows], the divergence of the student's softmax(inv_temp * logits)
+    from a teacher of which each row's outcomes ids [rows, n] (int32 or int64;
+    negative: absent) with values [rows, n] are kept: its logits
+    (FP8_DISTILL_TOP) or its log probabilities (FP8_DISTILL_TAIL, the rest one
+    more outcome).  stats [rows, 4] float32, list_ids [rows, n] int32 and list_q
+    [rows, n] float32 are written for the backward pass."""
+    dt, rows, cols, ld, dev = _input(logits, "logits")
+    n = _sides(values.shape, "values")[1]
+    vdt = _hp(values, "values")
+    _check(load_library().fp8_distill_fwd(
+        logits.data_ptr(), dt, rows, cols, ld, inv_temp, form, n, *_indices(ids, "ids", (rows, n), dev),
+        _f32(values, "values", (rows, n), dev, values.dtype), vdt, _f32(loss, "loss", (rows,), dev),
+        _f32(stats, "stats", (rows, 4), dev), _f32(list_ids, "list_ids", (rows, n), dev, torch.int32),
+        _f32(list_q, "list_q", (rows, n), dev), _stream(stream)), "fp8_distill_fwd")
+
+
+def fp8_distill_bwd(logits, list_ids, list_q, stats, dloss, *, inv_temp: float = 1.0, fmt: int = FP8_E5M2,
+                    margin: int = 0, d_q=None, d_s=None, d_q_col=None, d_s_col=None, dlogits=None, stream=None) -> None:
+    """The gradient of the logits from dloss [rows], with outputs as fp8_logprob_bwd."""
+    dt, rows, cols, ld, dev = _input(logits, "logits")
+    n = _sides(list_q.shape, "list_q")[1]
+    _check(load_library().fp8_distill_bwd(
+        logits.data_ptr(), dt, rows, cols, ld, inv_temp, n, _f32(list_ids, "list_ids", (rows, n), dev, torch.int32),
+        _f32(list_q, "list_q", (rows, n), dev), _f32(stats, "stats", (rows, 4), dev),
+        _f32(dloss, "dloss", (rows,), dev), fmt, margin,
+        _blocks(d_q, d_s, "row blocks", rows, cols, rows, cols, dev),
+        _blocks(d_q_col, d_s_col, "column blocks", rows, cols, cols, rows, dev),
+        *_optional(dlogits, "dlogits", rows, cols, dev, logits.dtype), _stream(stream)), "fp8_distill_bwd")
 
 
 def fp8_selftest_wait_timeout(limit_us: int, stream=None) -> None:

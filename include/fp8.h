@@ -55,6 +55,7 @@ extern "C" {
 #define FP8_STATUS_TIMEOUT 2u
 #define FP8_STATUS_INTERNAL 4u /* a kernel's own consistency check failed */
 #define FP8_STATUS_BAD_MU 8u   /* a device mu was not a power of two in [2^-32, 2^32]; 1 was used */
+#define FP8_STATUS_BAD_INDEX 16u /* a token or list entry at or beyond the vocabulary; it counted as absent */
 
 /* ---- element types of high-precision tensors -------------------------- */
 #define FP8_DT_F32 0
@@ -662,6 +663,157 @@ int fp8_act_fwd(const void *h, int dtype, int rows, int cols, size_t ldh, int ac
 int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int cols, size_t ldda, int act, int fmt,
                 int margin, const fp8_blocks *dh_row, const fp8_blocks *dh_col, const fp8_blocks *a_col, void *dh,
                 size_t lddh, void *stream);
+
+/*
+ * The passes between and behind the linear layers.  Matrices, codes and scales
+ * as above; float32 outputs and statistics are contiguous.  Outputs must not
+ * overlap inputs or one another, except where a call names it.  Every sum and
+ * statistic is taken in binary32 in an order that depends on the sizes only:
+ * the same inputs give the same bits.
+ *
+ * A vector of parameters: `p` dev, contiguous elements of `dtype`, or NULL.
+ */
+typedef struct {
+  void *p;
+  int dtype;
+} fp8_vector;
+
+/*
+ * Norms before and after a sublayer with its gate and residual scale, on
+ * [rows, cols] with cols <= FP8_NORM_COLS_MAX:
+ *     u    = post_norm(h), or h
+ *     r'   = res_scale * r + gate * u          rounded to res_dtype
+ *     x    = pre_norm(r')                      the norm of r' as stored
+ *     norm(v) = (v - mean) * rstd * w + b,     rstd = 1 / sqrt(mean((v - mean)^2) + eps)
+ * with mean = 0 for FP8_NORM_RMS.
+ *   dtype      of h, x, dx, dh;  res_dtype  of r, r', their gradients: dtype or FP8_DT_F32
+ *   pre, post  FP8_NORM_NONE, FP8_NORM_RMS or FP8_NORM_LAYER
+ *   w, b       of the pre norm;  post_w, post_b  of the post norm; NULL: 1 and 0
+ *   gate       one row of cols elements for every gate_rows rows (row i takes
+ *              gate row i / gate_rows; gate_rows >= rows: one for all), gate
+ *              rows ld_gate elements apart; NULL: 1
+ */
+#define FP8_NORM_NONE 0
+#define FP8_NORM_RMS 1
+#define FP8_NORM_LAYER 2
+#define FP8_NORM_COLS_MAX 32768
+typedef struct {
+  int rows, cols;
+  int dtype, res_dtype;
+  int pre, post;
+  fp8_vector w, b, post_w, post_b, gate;
+  int gate_rows;
+  size_t ld_gate;
+  float res_scale, eps;
+} fp8_norm_params;
+
+/*
+ * fp8_norm_fwd -- r' (r_out) and any of: x in dtype; x_row / x_col, E4M3 codes
+ * of x's 1x128 / 128x1 blocks (cast from the binary32 values: the operands of
+ * the next forward product and of its wgrad).  h NULL: the sublayer's output is
+ * absent (u = 0; post is FP8_NORM_NONE and gate NULL then).  r_out may be NULL
+ * where h is NULL and res_scale 1 (r' is r).  stats: [rows, 4] floats (mean and
+ * rstd of the post norm, then of the pre norm; 0 and 1 without one), what the
+ * backward pass needs beside h and r', or NULL (then no x_col).  r_out may be
+ * r, and x may be h (the same pointer and row stride).  rows == 0 or cols == 0
+ * is a no-op.
+ */
+int fp8_norm_fwd(const fp8_norm_params *p, const void *h, size_t ldh, const void *r, size_t ldr, void *r_out,
+                 size_t ldr_out, float *stats, void *x, size_t ldx, int margin, const fp8_blocks *x_row,
+                 const fp8_blocks *x_col, void *stream);
+
+/* Gradients of the parameters: sums over the rows (over each gate row's rows
+ * for gate, `gate` rows ld_gate elements apart), each in its own type; NULL
+ * where not wanted. */
+typedef struct {
+  fp8_vector w, b, post_w, post_b, gate;
+  size_t ld_gate;
+} fp8_norm_grads;
+
+/*
+ * fp8_norm_bwd -- from dx (of dtype; NULL with pre FP8_NORM_NONE) and dr_out
+ * (of res_dtype, the gradient of r' from what follows, or NULL for none), and
+ * the forward pass's h, r' and stats:  dh (of dtype), dr (of res_dtype) and the
+ * parameters' gradients, each wanted or NULL.  dh may be dx or h, dr may be
+ * dr_out (the same pointer and row stride).  workspace: dev, 16-byte aligned,
+ * fp8_norm_workspace_bytes(rows, cols, gate_rows) bytes, contents of no
+ * meaning before and after (needed where a parameter's gradient is wanted);
+ * calls whose work overlaps on the GPU need one each.  rows == 0 gives
+ * gradients of 0 for the parameters.
+ */
+size_t fp8_norm_workspace_bytes(int rows, int cols, int gate_rows);
+int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const void *dr_out, size_t lddr_out,
+                 const void *h, size_t ldh, const void *r_out, size_t ldr_out, const float *stats, void *dh,
+                 size_t lddh, void *dr, size_t lddr, const fp8_norm_grads *grads, void *workspace, size_t ws_bytes,
+                 void *stream);
+
+/*
+ * Log probabilities of given tokens.  With s = inv_temp * logits (inv_temp > 0)
+ * and p = softmax(s) of each row of [rows, cols]:
+ *
+ * fp8_logprob_fwd -- logp[i] = log p of token tokens[i]; entropy[i] = -sum p
+ * log p; the `top` (<= FP8_TOP_MAX, <= cols) largest logits in order, ties to
+ * the lowest index (a NaN before all else): their log probabilities top_logp
+ * and places top_ids, [rows, top].  tokens: int32 or int64 (token_bytes 4 or
+ * 8).  A negative token is absent: logp 0; so is one at or beyond cols, which
+ * sets FP8_STATUS_BAD_INDEX.  A row whose every logit is -inf has no
+ * distribution: log probabilities -inf, entropy 0, no gradient.  A row with a
+ * NaN or +inf gives NaN.  stats: [rows, 4] floats for the backward pass (the
+ * largest logit, 1 / sum exp(s - its s), the log of that sum, the entropy), or
+ * NULL.  logp with tokens, entropy, top_logp with top_ids: each wanted or NULL.
+ */
+#define FP8_TOP_MAX 32
+int fp8_logprob_fwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, const void *tokens,
+                    int token_bytes, float *logp, float *entropy, int top, float *top_logp, int *top_ids,
+                    float *stats, void *stream);
+
+/*
+ * fp8_logprob_bwd -- the gradient of the logits from those of logp and of the
+ * entropy ([rows] floats; dlogp with tokens, either may be NULL, not both):
+ *     d[i,j] = inv_temp * (dlogp[i] * ([j == token] - p) - dentropy[i] * p * (log p + entropy[i]))
+ * in any of: d_row / d_col, codes of fmt of its 1x128 / 128x1 blocks (cast from
+ * the binary32 values: the operands of dgrad / wgrad), and dlogits in dtype,
+ * which may be logits (the same pointer and row stride).  stats with the
+ * entropy must come from a forward call that computed it (entropy not NULL).
+ */
+int fp8_logprob_bwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, const void *tokens,
+                    int token_bytes, const float *stats, const float *dlogp, const float *dentropy, int fmt, int margin,
+                    const fp8_blocks *d_row, const fp8_blocks *d_col, void *dlogits, size_t ld_d, void *stream);
+
+/*
+ * Distillation from a teacher of which each row's `top` (<= FP8_DISTILL_MAX)
+ * largest outcomes are kept: ids (int32 or int64, id_bytes 4 or 8) and values
+ * (of value_dtype), [rows, top] contiguous, in any order.
+ *   FP8_DISTILL_TOP   values are the teacher's logits; q = softmax(inv_temp * values)
+ *       loss = sum q (log q - log p)
+ *   FP8_DISTILL_TAIL  values are its log probabilities (at the temperature); q = exp(values), and
+ *       all that is not listed is one outcome: q' = max(0, 1 - sum q), p' = sum of the unlisted p
+ *       loss = sum q (log q - log p) + q' (log q' - log p')      (without the last where p' = 0)
+ * p the student's softmax(inv_temp * logits) over all cols.  An entry is absent
+ * where its id is negative, at or beyond cols (FP8_STATUS_BAD_INDEX), listed
+ * before in the row, or its value -inf; a row with nothing listed has loss 0
+ * and no gradient.  A row whose every logit is -inf: loss +inf, no gradient.
+ * cols <= FP8_DISTILL_COLS_MAX.
+ *
+ * fp8_distill_fwd also writes what the backward pass needs: stats [rows, 4]
+ * (the largest logit, 1 / sum exp, and the factors of p for listed and for
+ * unlisted outcomes), and the list in the order of the ids: list_ids, list_q
+ * [rows, top] (absent entries last, 2^31 - 1).
+ *
+ * fp8_distill_bwd -- from dloss [rows], the gradient of the logits as
+ * fp8_logprob_bwd:  d = inv_temp * dloss * (p * factor - q).
+ */
+#define FP8_DISTILL_TOP 0
+#define FP8_DISTILL_TAIL 1
+#define FP8_DISTILL_MAX 1024
+#define FP8_DISTILL_COLS_MAX 1048576
+int fp8_distill_fwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, int form, int top,
+                    const void *ids, int id_bytes, const void *values, int value_dtype, float *loss, float *stats,
+                    int *list_ids, float *list_q, void *stream);
+int fp8_distill_bwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, int top,
+                    const int *list_ids, const float *list_q, const float *stats, const float *dloss, int fmt,
+                    int margin, const fp8_blocks *d_row, const fp8_blocks *d_col, void *dlogits, size_t ld_d,
+                    void *stream);
 
 /* Human-readable message of a status code (static string). */
 const char *fp8_strerror(int code);
