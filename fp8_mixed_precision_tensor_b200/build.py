@@ -10,18 +10,19 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libfp8.so")
-MAIN = os.path.join(HERE, "csrc", "libfp8.cu")
+UNITS = [os.path.join(HERE, "csrc", f) for f in ("libfp8.cu", "passes.cu")]
 CALLS = os.path.join(HERE, "_calls.so")
 CALLS_MAIN = os.path.join(HERE, "csrc", "calls.cpp")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
 ]
 
 
@@ -34,6 +35,22 @@ def stale(lib: str, srcs: list[str]) -> bool:
         return True
     t = os.path.getmtime(lib)
     return any(os.path.getmtime(s) > t for s in srcs)
+
+
+def _compile_units(verbose: bool) -> None:
+    """The translation units side by side, then the library from them."""
+    nvcc = os.environ.get("NVCC", "nvcc")
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, os.path.basename(u) + ".o") for u in UNITS]
+        commands = [[nvcc, *NVCC_FLAGS, "-c", u, "-o", o] for u, o in zip(UNITS, objects)]
+        if verbose:
+            print("\n".join(" ".join(c) for c in commands), flush=True)
+        running = [subprocess.Popen(c) for c in commands]
+        codes = [r.wait() for r in running]
+        for c, cmd in zip(codes, commands):
+            if c:
+                raise subprocess.CalledProcessError(c, cmd)
+        _compile([nvcc, *NVCC_FLAGS, "-shared", *objects], LIB, verbose)
 
 
 def _compile(cmd: list[str], lib: str, verbose: bool) -> None:
@@ -61,7 +78,7 @@ def _calls_command() -> list[str]:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or stale(LIB, sources()):
-        _compile([os.environ.get("NVCC", "nvcc"), *NVCC_FLAGS, MAIN], LIB, verbose)
+        _compile_units(verbose)
     if force or stale(CALLS, [CALLS_MAIN, os.path.join(ROOT, "include", "fp8.h")]):
         _compile(_calls_command(), CALLS, verbose)
     return LIB

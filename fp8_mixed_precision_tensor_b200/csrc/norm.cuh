@@ -25,12 +25,37 @@ namespace norm {
 
 using block::Raw8;
 
-// A row belongs to a group of T threads (a multiple of 32) in each of C CTAs
-// (a cluster); a thread holds NV vectors of eight neighbouring columns.
-constexpr int kGroupThreads = 512;       // the most threads of a row in one CTA
-constexpr int kFwdThreads = 256;         // a CTA takes several narrow rows, up to this many threads
-constexpr int kBwdThreads = 512;
-constexpr int kBwdCols = 8 * kBwdThreads;  // columns of a CTA in the backward pass
+// A row belongs to a group of T threads (a multiple of 32) of a CTA; a thread
+// holds NV chunks of eight columns.  A CTA takes as many narrow rows at a time
+// as it has threads for, and row after row while it lives.
+constexpr int kThreads = 256;      // of a CTA, but for the widest rows
+constexpr int kMostThreads = 512;
+constexpr int kMostWarps = kMostThreads / 32;
+constexpr int kStagedCols = 12288;  // the widest staged rows: 384 threads, 168 registers each
+template <int NV, int MODE>
+constexpr int kCtaThreads = NV < 4 ? kThreads : MODE == 0 ? kStagedCols / 32 : kMostThreads;
+
+// How rows are read and written.
+//   kStaged  eight neighbouring columns a chunk, in 16-byte pieces; the next
+//            row's are copied into the thread's own part of shared memory while
+//            it works on the present one (no barriers: nobody else reads them)
+//   kDirect  rows that start anywhere: the lanes of a warp take neighbouring
+//            columns, and element by element from memory, twice where two
+//            passes need them
+enum { kStaged = 0, kDirect = 1 };
+
+// The chunk v of a thread, and whether it lies in the row (kStaged: all of it).
+struct Place {
+  int cols, t, T;
+  template <int MODE>
+  __device__ __forceinline__ int col(int v, int j) const {
+    return MODE == kStaged ? (v * T + t) * 8 + j : (v * T + (t & ~31)) * 8 + 32 * j + (t & 31);
+  }
+  template <int MODE>
+  __device__ __forceinline__ bool has(int v, int j) const {
+    return col<MODE>(v, MODE == kStaged ? 0 : j) < cols;
+  }
+};
 
 struct Vec {
   const void *p;
@@ -90,12 +115,15 @@ __device__ __forceinline__ void store_param(Vec v, size_t i, float x) {
   else reinterpret_cast<__half *>(const_cast<void *>(v.p))[i] = __float2half_rn(x);
 }
 
-// A row's eight elements at column c; 0 behind the row's end.
-template <int DT>
-__device__ __forceinline__ Raw8<DT> load_row8(const void *base, size_t ld, bool wide, int row, int rows, int c,
-                                              int cols) {
-  return wide ? block::load_raw8_wide<DT>(base, ld, row, c, rows, cols)
-              : block::load_raw8_single<DT>(base, ld, row, c, rows, cols);
+
+template <int MODE>
+__device__ __forceinline__ void load_params(Vec v, size_t off, const Place &at, int chunk, float fill, float (&f)[8]) {
+  if constexpr (MODE == kStaged) {
+    load_param8(v, off, at.col<MODE>(chunk, 0), at.cols, fill, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] = at.has<MODE>(chunk, j) ? param_at(v, off + at.col<MODE>(chunk, j), fill) : fill;
+  }
 }
 
 template <int DT>
@@ -105,105 +133,223 @@ __device__ __forceinline__ float as_stored(float x) {
   else return __half2float(__float2half_rn(x));
 }
 
-// Sums over the threads of a row.  Two buffers in turn: one barrier a sum.
-struct RowSum {
-  float (*slots)[2][128];  // shared memory: [2 buffers][2 sums][warps of the row's CTAs]
-  int group, warps;        // this row's group in the CTA, its warps
-  unsigned ctas, rank;     // CTAs of the row
-  int buf;
+template <int DT>
+constexpr int kPieces = DT == FP8_DT_F32 ? 2 : 1;  // of 16 bytes in a chunk
 
-  __device__ __forceinline__ void wait() const {
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(warps * 32) : "memory");
+// A matrix's chunks of one row.  `slot`: this matrix's part of the CTA's shared
+// memory, [chunk][piece][thread] of 16 bytes.
+template <int DT, int MODE>
+struct Rows {
+  const uint8_t *p;
+  size_t ld;  // bytes
+  uint8_t *slot;
+  int threads, tid;
+
+  __device__ __forceinline__ void fetch(const Place &at, int v, int row) const {
+    if constexpr (MODE == kStaged) {
+      if (!at.has<MODE>(v, 0)) return;
+      const uint8_t *src = p + (size_t)row * ld + (size_t)at.col<MODE>(v, 0) * (DT == FP8_DT_F32 ? 4 : 2);
+#pragma unroll
+      for (int i = 0; i < kPieces<DT>; i++)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         smem_u32(slot + (size_t)((v * kPieces<DT> + i) * threads + tid) * 16)),
+                     "l"(src + 16 * i)
+                     : "memory");
+    }
   }
-
-  template <int N>
-  __device__ __forceinline__ void operator()(float (&v)[N]) {
-    static_assert(N <= 2, "slots");
+  __device__ __forceinline__ void get(const Place &at, int v, int row, float (&f)[8]) const {
+    if constexpr (MODE == kStaged) {
+      Raw8<DT> r;
 #pragma unroll
-    for (int n = 0; n < N; n++)
-#pragma unroll
-      for (int b = 16; b > 0; b /= 2) v[n] += __shfl_xor_sync(0xffffffffu, v[n], b);
-    if (warps == 1 && ctas == 1) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (ctas == 1) {
-      const int at = group * warps;
-      if (lane == 0) {
-#pragma unroll
-        for (int n = 0; n < N; n++) slots[buf][n][at + warp] = v[n];
+      for (int i = 0; i < kPieces<DT>; i++) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(slot + (size_t)((v * kPieces<DT> + i) * threads + tid) * 16);
+        r.w[4 * i] = w.x, r.w[4 * i + 1] = w.y, r.w[4 * i + 2] = w.z, r.w[4 * i + 3] = w.w;
       }
-      wait();
-#pragma unroll
-      for (int n = 0; n < N; n++) v[n] = lane < warps ? slots[buf][n][at + lane] : 0.0f;
-#pragma unroll
-      for (int n = 0; n < N; n++)
-#pragma unroll
-        for (int b = 8; b > 0; b /= 2) v[n] += __shfl_xor_sync(0xffffffffu, v[n], b);
+      block::unpack8<DT>(r, f);
     } else {
-      // every CTA of the cluster gets every warp's sum
-      if ((unsigned)lane < ctas) {
+      const uint8_t *src = p + (size_t)row * ld;
 #pragma unroll
-        for (int n = 0; n < N; n++) {
-          uint32_t there;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                       : "=r"(there)
-                       : "r"(smem_u32(&slots[buf][n][rank * warps + warp])), "r"(lane));
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there), "f"(v[n]) : "memory");
-        }
-      }
-      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-#pragma unroll
-      for (int n = 0; n < N; n++) {
-        v[n] = 0.0f;
-        for (int i = lane; i < (int)ctas * warps; i += 32) v[n] += slots[buf][n][i];
-#pragma unroll
-        for (int b = 16; b > 0; b /= 2) v[n] += __shfl_xor_sync(0xffffffffu, v[n], b);
+      for (int j = 0; j < 8; j++) {
+        const int c = min(at.col<MODE>(v, j), at.cols - 1);
+        if constexpr (DT == FP8_DT_F32) f[j] = reinterpret_cast<const float *>(src)[c];
+        else if constexpr (DT == FP8_DT_BF16) f[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(src)[c]);
+        else f[j] = __half2float(reinterpret_cast<const __half *>(src)[c]);
       }
     }
-#pragma unroll
-    for (int n = 0; n < N; n++) v[n] = __shfl_sync(0xffffffffu, v[n], 0);
-    buf ^= 1;
   }
 };
 
-__device__ __forceinline__ RowSum row_sum(float (*slots)[2][128], unsigned ctas) {
-  RowSum s;
-  s.slots = slots;
-  s.group = threadIdx.y;
-  s.warps = blockDim.x >> 5;
-  s.ctas = ctas;
-  s.rank = ctas > 1 ? blockIdx.x % ctas : 0;
-  s.buf = 0;
-  if (ctas > 1)  // the other CTAs' shared memory is there
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  return s;
+template <int DT, int MODE>
+__device__ __forceinline__ void put_row(void *out, size_t ld, const Place &at, int v, int row, const float (&f)[8]) {
+  if constexpr (MODE == kStaged) {
+    if (!at.has<MODE>(v, 0)) return;
+    constexpr int esz = DT == FP8_DT_F32 ? 4 : 2;
+    uint4 w[DT == FP8_DT_F32 ? 2 : 1];
+    block::pack8<DT>(f, w);
+    uint4 *q = reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(out) + ((size_t)row * ld + at.col<MODE>(v, 0)) * esz);
+    __stcs(q, w[0]);
+    if constexpr (DT == FP8_DT_F32) __stcs(q + 1, w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      if (at.has<MODE>(v, j)) {
+        const size_t i = (size_t)row * ld + at.col<MODE>(v, j);
+        if constexpr (DT == FP8_DT_F32) reinterpret_cast<float *>(out)[i] = f[j];
+        else if constexpr (DT == FP8_DT_BF16) reinterpret_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(f[j]);
+        else reinterpret_cast<__half *>(out)[i] = __float2half_rn(f[j]);
+      }
+  }
 }
 
-// mean and rstd of a row whose NV x 8 elements a thread holds in v (n[i] of the
-// eight are columns of the row).
-template <int NV>
-__device__ __forceinline__ float2 row_stats(const float (&v)[NV][8], const int (&n)[NV], int kind, int cols, float eps,
-                                            RowSum &sum) {
-  float mean = 0.0f;
-  const float inv = 1.0f / (float)cols;
-  if (kind == FP8_NORM_LAYER) {
-    float t[1] = {0.0f};
+// Zero outside the row.
+template <int MODE>
+__device__ __forceinline__ void mask(const Place &at, int v, float (&f)[8]) {
+  if constexpr (MODE == kStaged) {
+    if (!at.has<MODE>(v, 0)) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) f[j] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j++) f[j] = at.has<MODE>(v, j) ? f[j] : 0.0f;
+  }
+}
+
+// Eight floats of a thread in shared memory, its own: [half][thread] of 16 bytes
+// for each chunk.
+__device__ __forceinline__ void put8(float *s, int threads, int tid, int v, const float (&f)[8]) {
+  float4 *p = reinterpret_cast<float4 *>(s) + (size_t)v * 2 * threads + tid;
+  p[0] = make_float4(f[0], f[1], f[2], f[3]);
+  p[threads] = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void get8(const float *s, int threads, int tid, int v, float (&f)[8]) {
+  const float4 *p = reinterpret_cast<const float4 *>(s) + (size_t)v * 2 * threads + tid;
+  const float4 a = p[0], b = p[threads];
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// What the warps of a row's group tell one another: up to 8 numbers each, two
+// buffers in turn, so that one barrier serves an exchange.
+struct Exchange {
+  float (*slots)[8][kMostWarps];  // shared memory [2][8][warps of the CTA]
+  int group, warps, buf;
+
+  __device__ __forceinline__ void put(int n, float x) { slots[buf][n][group * warps + (threadIdx.x >> 5)] = x; }
+  __device__ __forceinline__ void wait() const {
+    if (warps > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(warps * 32) : "memory");
+    else __syncwarp();
+  }
+  __device__ __forceinline__ float get(int n, int w) const { return slots[buf][n][group * warps + w]; }
+  __device__ __forceinline__ float sum(int n) const {
+    float s = 0.0f;
+    if ((warps & 3) == 0) {  // (rows of 1024 columns and more)
+      for (int w = 0; w < warps; w += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(&slots[buf][n][group * warps + w]);
+        s += (q.x + q.y) + (q.z + q.w);
+      }
+    } else {
+      for (int w = 0; w < warps; w++) s += get(n, w);
+    }
+    return s;
+  }
+  __device__ __forceinline__ void next() { buf ^= 1; }
+};
+
+// Sums over a warp of N numbers a thread, in halves: a step gives half of the
+// numbers away and takes the other half's share, until each lane adds up one.
+// Lane l then has the sum of number l / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4 || N == 8, "halved down to one");
+  const int lane = threadIdx.x & 31;
+  int bit = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2, bit /= 2) {
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      const float send = (lane & bit) ? v[i] : v[i + n], keep = (lane & bit) ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+    }
+  }
+#pragma unroll
+  for (; bit > 0; bit /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+  return v[0];
+}
+
+// The sums over a row of N numbers a thread, to every thread.
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], Exchange &x) {
+  const float s = warp_sums(v);
+  const int lane = threadIdx.x & 31;
+  if (x.warps == 1) {
+#pragma unroll
+    for (int n = 0; n < N; n++) v[n] = __shfl_sync(0xffffffffu, s, n * (32 / N));
+    return;
+  }
+  if (lane % (32 / N) == 0) x.put(lane / (32 / N), s);
+  x.wait();
+#pragma unroll
+  for (int n = 0; n < N; n++) v[n] = x.sum(n);
+  x.next();
+}
+
+// mean and rstd of a row of which a thread holds v, zero outside the row.  A
+// layer norm's warps take the squares about their own mean, and those are joined
+// about the row's (Chan, Golub, LeVeque), so that one exchange gives both and an
+// offset costs no digits.
+template <int MODE, int NV>
+__device__ __forceinline__ float2 row_stats(const float (&v)[NV][8], const Place &at, int kind, float inv, float eps,
+                                            Exchange &x) {
+  if (kind == FP8_NORM_RMS) {
+    float q[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; i++)
 #pragma unroll
-      for (int j = 0; j < 8; j++) t[0] += j < n[i] ? v[i][j] : 0.0f;
-    sum(t);
-    mean = t[0] * inv;
+      for (int j = 0; j < 8; j++) q[0] = fmaf(v[i][j], v[i][j], q[0]);
+    row_sums(q, x);
+    return make_float2(0.0f, rsqrtf(fmaf(q[0], inv, eps)));
   }
-  float q[1] = {0.0f};
+  // columns of a warp: 256 a chunk
+  auto count = [&](int w) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; i++) n += max(0, min(256, at.cols - (i * at.T + w * 32) * 8));
+    return n;
+  };
+  float s[1] = {0.0f}, q[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < NV; i++)
+#pragma unroll
+    for (int j = 0; j < 8; j++) s[0] += v[i][j];
+  const int own = count((int)threadIdx.x >> 5);
+  const float total = warp_sums(s), mean_w = own ? total / (float)own : 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; i++)
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const float d = j < n[i] ? v[i][j] - mean : 0.0f;
+      const float d = at.has<MODE>(i, j) ? v[i][j] - mean_w : 0.0f;
       q[0] = fmaf(d, d, q[0]);
     }
-  sum(q);
-  return make_float2(mean, rsqrtf(fmaf(q[0], inv, eps)));
+  const float sq = warp_sums(q);
+  if (x.warps == 1) return make_float2(mean_w, rsqrtf(fmaf(sq, inv, eps)));
+  if ((threadIdx.x & 31) == 0) {
+    x.put(0, total);
+    x.put(1, sq);
+    x.put(2, mean_w);
+  }
+  x.wait();
+  const float mean = x.sum(0) * inv;
+  float m2 = 0.0f;
+  for (int w = 0; w < x.warps; w++) {
+    const float d = x.get(2, w) - mean;
+    m2 += fmaf((float)count(w) * d, d, x.get(1, w));
+  }
+  x.next();
+  return make_float2(mean, rsqrtf(fmaf(m2, inv, eps)));
+}
+
+__device__ __forceinline__ Exchange exchange(float (*slots)[8][kMostWarps]) {
+  return {slots, (int)threadIdx.y, (int)(blockDim.x >> 5), 0};
 }
 
 // r' = a r + g u takes each product rounded: 0.9f is not 0.9, but 0.9f * 10
@@ -222,102 +368,214 @@ struct Fwd {
   size_t ldg;
   float alpha, eps;
   int margin;
-  int wide_h, wide_r, wide_ro, wide_x;
 };
 
-// The codes of a thread's eight elements of a row's 1x128 block (16 lanes hold
-// one), its scale, and, with the last row, the padding of its scales.
-__device__ __forceinline__ void store_block8(const Fwd &p, int row, int c, const float (&v)[8]) {
-  float a = 0.0f;
+
+// Scale bytes of rows behind the last one, up to a whole group of 128.
+__device__ __forceinline__ void pad_scales(const Fwd &p, int blk, int kblocks, int l, int step) {
+  for (int r = p.rows + l; r < (p.rows + 127) / 128 * 128; r += step) block::put_scale(p.xs, r, blk, kblocks, 0);
+}
+
+// The codes of a thread's chunk of a row's 1x128 blocks with their scales, and
+// with the last row the padding of these.
+template <int MODE>
+__device__ __forceinline__ void put_codes(const Fwd &p, const Place &at, int v, int row, const float (&f)[8]) {
+  const int lane = threadIdx.x & 31, kblocks = (p.cols + 127) / 128;
+  uint8_t *q = p.xq + (size_t)row * p.ldxq;
+  if constexpr (MODE == kStaged) {  // 16 lanes a block
+    float a = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) a = block::absmax2(a, v[j], v[j + 1]);
-  uint32_t m = __float_as_uint(a);
+    for (int j = 0; j < 8; j += 2) a = block::absmax2(a, f[j], f[j + 1]);
+    uint32_t m = __float_as_uint(a);
 #pragma unroll
-  for (int b = 8; b > 0; b /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, b));
-  const int k = block::block_exponent(m, kMaxE4M3, p.margin), l = threadIdx.x & 15;
-  const int kblocks = (p.cols + 127) / 128, blk = c >> 7;
-  if (blk < kblocks) {
-    if (l == 0) block::put_scale(p.xs, row, blk, kblocks, k);
-    if (row == p.rows - 1)
-      for (int r = p.rows + l; r < (p.rows + 127) / 128 * 128; r += 16) block::put_scale(p.xs, r, blk, kblocks, 0);
-  }
-  float2 s[4];
-  block::spread_scale(pow2f(k), s);
-  const uint2 o = m >= 0x7f800000u ? block::enc8_any<FP8_E4M3>(v, s) : block::enc8<FP8_E4M3>(v, s);
-  uint8_t *q = p.xq + (size_t)row * p.ldxq + c;
-  if (c + 8 <= p.cols) {
-    __stcs(reinterpret_cast<uint2 *>(q), o);
-  } else if (c < p.cols) {
-    for (int j = 0; j < p.cols - c; j++) q[j] = (uint8_t)((j < 4 ? o.x : o.y) >> (8 * (j & 3)));
+    for (int b = 8; b > 0; b /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, b));
+    const int k = block::block_exponent(m, kMaxE4M3, p.margin), blk = at.col<MODE>(v, 0) >> 7, l = lane & 15;
+    if (blk < kblocks) {
+      if (l == 0) block::put_scale(p.xs, row, blk, kblocks, k);
+      if (row == p.rows - 1) pad_scales(p, blk, kblocks, l, 16);
+    }
+    float2 s[4];
+    block::spread_scale(pow2f(k), s);
+    const uint2 o = m >= 0x7f800000u ? block::enc8_any<FP8_E4M3>(f, s) : block::enc8<FP8_E4M3>(f, s);
+    if (at.has<MODE>(v, 0)) __stcs(reinterpret_cast<uint2 *>(q + at.col<MODE>(v, 0)), o);
+  } else {  // a warp has two: elements 0 to 3 and 4 to 7 of its lanes
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const float a = block::absmax2(block::absmax2(0.0f, f[4 * h], f[4 * h + 1]), f[4 * h + 2], f[4 * h + 3]);
+      const uint32_t m = warp_max_u32(__float_as_uint(a));
+      const int k = block::block_exponent(m, kMaxE4M3, p.margin);
+      const int blk = at.col<MODE>(v, 4 * h) >> 7;
+      if (blk < kblocks) {
+        if (lane == 0) block::put_scale(p.xs, row, blk, kblocks, k);
+        if (row == p.rows - 1) pad_scales(p, blk, kblocks, lane, 32);
+      }
+      const float s = pow2f(k);
+      const uint32_t o = enc4<FP8_E4M3>(f[4 * h] * s, f[4 * h + 1] * s, f[4 * h + 2] * s, f[4 * h + 3] * s);
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        if (at.has<MODE>(v, 4 * h + j)) q[at.col<MODE>(v, 4 * h + j)] = (uint8_t)(o >> (8 * j));
+    }
   }
 }
 
-template <int DT, int RT, int NV>
-__global__ void __launch_bounds__(kGroupThreads) k_norm_fwd(const Fwd p, unsigned ctas) {
+// Shared memory of a CTA: the staged rows, then the parameters of each thread's
+// columns as it needs them for every row.
+struct FwdSmem {
+  int stage, w, b, gw, gb, bytes;  // offsets; -1: absent.  gw, gb: the gate times the post norm's w and b
+};
+template <int DT, int RT>
+__host__ __device__ inline FwdSmem fwd_smem(int chunks, bool h, bool w, bool b, bool gw, bool gb, int mode) {
+  FwdSmem s;
+  int at = mode == kStaged ? chunks * 16 * ((h ? kPieces<DT> : 0) + kPieces<RT>) : 0;
+  auto take = [&](bool on) {
+    const int o = on && mode == kStaged ? at : -1;
+    at += o >= 0 ? chunks * 32 : 0;
+    return o;
+  };
+  s.stage = 0;
+  s.w = take(w), s.b = take(b), s.gw = take(gw), s.gb = take(gb);
+  s.bytes = at;
+  return s;
+}
+
+// POST: whether there is a post norm (kDirect goes by p.post).
+template <int DT, int RT, bool POST, int NV, int MODE>
+__global__ void __launch_bounds__(kCtaThreads<NV, MODE>, NV == 4 ? 1 : 4) k_norm_fwd(const Fwd p) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float slots[2][2][128];
-  RowSum sum = row_sum(slots, ctas);
-  const unsigned stride = gridDim.x / ctas * blockDim.y;
-  int c[NV], n[NV];
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  __shared__ __align__(16) float slots[2][8][kMostWarps];
+  Exchange ex = exchange(slots);
+  const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const Place at = {p.cols, (int)threadIdx.x, (int)blockDim.x};
+  const bool post = MODE == kStaged ? POST : p.post != FP8_NORM_NONE;
+  const bool scaled = p.g.p || (post && p.pw.p), shifted = post && p.pb.p;
+  const FwdSmem lay = fwd_smem<DT, RT>(NV * threads, p.h, p.w.p, p.b.p, scaled, shifted, MODE);
+  float *const w_s = reinterpret_cast<float *>(norm_smem + lay.w), *const b_s = reinterpret_cast<float *>(norm_smem + lay.b);
+  float *const gw_s = reinterpret_cast<float *>(norm_smem + lay.gw), *const gb_s = reinterpret_cast<float *>(norm_smem + lay.gb);
+  const Rows<RT, MODE> R = {static_cast<const uint8_t *>(p.r), p.ldr * (RT == FP8_DT_F32 ? 4 : 2), norm_smem, threads, tid};
+  const Rows<DT, MODE> H = {static_cast<const uint8_t *>(p.h), p.ldh * (DT == FP8_DT_F32 ? 4 : 2),
+                            norm_smem + NV * threads * 16 * kPieces<RT>, threads, tid};
+  const unsigned stride = gridDim.x * blockDim.y;
+  unsigned next = blockIdx.x * blockDim.y + threadIdx.y;
+  auto fetch = [&](int v, unsigned row) {
+    if (row >= (unsigned)p.rows) return;
+    if (p.h) H.fetch(at, v, (int)row);
+    R.fetch(at, v, (int)row);
+  };
 #pragma unroll
-  for (int i = 0; i < NV; i++) {
-    c[i] = (int)((sum.rank * NV + i) * blockDim.x + threadIdx.x) * 8;
-    n[i] = max(0, min(8, p.cols - c[i]));
-  }
-  for (unsigned at = blockIdx.x / ctas * blockDim.y + threadIdx.y; at < (unsigned)p.rows; at += stride) {
-    const int row = (int)at;
-    float v[NV][8], y[NV][8];
-    if (p.h) {
+  for (int v = 0; v < NV; v++) fetch(v, next);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  if constexpr (MODE == kStaged) {
 #pragma unroll
-      for (int i = 0; i < NV; i++) block::unpack8<DT>(load_row8<DT>(p.h, p.ldh, p.wide_h, row, p.rows, c[i], p.cols), v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; i++)
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[i][j] = 0.0f;
+    for (int v = 0; v < NV; v++) {
+      float f[8];
+      if (p.w.p) load_params<MODE>(p.w, 0, at, v, 1.0f, f), put8(w_s, threads, tid, v, f);
+      if (p.b.p) load_params<MODE>(p.b, 0, at, v, 0.0f, f), put8(b_s, threads, tid, v, f);
     }
+  }
+  // the gate's row times the post norm's w and b
+  auto gate_params = [&](int v, int gate, float (&gw)[8], float (&gb)[8]) {
+    load_params<MODE>(p.g, (size_t)gate * p.ldg, at, v, 1.0f, gw);
+    if (shifted) {
+      load_params<MODE>(p.pb, 0, at, v, 0.0f, gb);
 #pragma unroll
-    for (int i = 0; i < NV; i++) block::unpack8<RT>(load_row8<RT>(p.r, p.ldr, p.wide_r, row, p.rows, c[i], p.cols), y[i]);
-    float2 s1 = make_float2(0.0f, 1.0f), s2 = make_float2(0.0f, 1.0f);
-    if (p.post != FP8_NORM_NONE) {
-      s1 = row_stats(v, n, p.post, p.cols, p.eps, sum);
+      for (int j = 0; j < 8; j++) gb[j] *= gw[j];
+    }
+    if (post) {
+      float f[8];
+      load_params<MODE>(p.pw, 0, at, v, 1.0f, f);
 #pragma unroll
-      for (int i = 0; i < NV; i++) {
-        float w[8], b[8];
-        load_param8(p.pw, 0, c[i], p.cols, 1.0f, w);
-        load_param8(p.pb, 0, c[i], p.cols, 0.0f, b);
+      for (int j = 0; j < 8; j++) gw[j] *= f[j];
+    }
+  };
+  const float inv = 1.0f / (float)p.cols;
+  int gate = -1;
+  for (; next < (unsigned)p.rows; next += stride) {
+    const int row = (int)next;
+    const int now = p.g.p ? row / p.gate_rows : 0;
+    if (MODE == kStaged && (scaled || shifted) && now != gate) {  // (a thread's own part: nobody else waits for it)
+      gate = now;
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[i][j] = fmaf((v[i][j] - s1.x) * s1.y, w[j], b[j]);
+      for (int v = 0; v < NV; v++) {
+        float gw[8], gb[8];
+        gate_params(v, now, gw, gb);
+        if (scaled) put8(gw_s, threads, tid, v, gw);
+        if (shifted) put8(gb_s, threads, tid, v, gb);
       }
     }
-    const size_t gate_at = p.g.p ? (size_t)(row / p.gate_rows) * p.ldg : 0;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    float y[NV][8];
+    float2 s1 = make_float2(0.0f, 1.0f), s2 = make_float2(0.0f, 1.0f);
+    if (post) {
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-      float g[8];
-      load_param8(p.g, gate_at, c[i], p.cols, 1.0f, g);
-#pragma unroll
-      for (int j = 0; j < 8; j++)
-        y[i][j] = j < n[i] ? as_stored<RT>(__fadd_rn(__fmul_rn(p.alpha, y[i][j]), __fmul_rn(g[j], v[i][j]))) : 0.0f;
-      if (p.r_out) block::store8<RT>(p.wide_ro, p.r_out, p.ldro, row, c[i], p.rows, p.cols, y[i]);
+      for (int v = 0; v < NV; v++) {
+        H.get(at, v, row, y[v]);
+        mask<MODE>(at, v, y[v]);
+      }
+      s1 = row_stats<MODE, NV>(y, at, p.post, inv, p.eps, ex);
     }
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+      float u[8], f[8];
+      if (post) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) u[j] = (y[v][j] - s1.x) * s1.y;
+      } else if (p.h) {
+        H.get(at, v, row, u);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) u[j] = 0.0f;
+      }
+      float gb[8];
+      if (MODE == kDirect) gate_params(v, now, f, gb);
+      if (scaled) {
+        if (MODE == kStaged) get8(gw_s, threads, tid, v, f);
+#pragma unroll
+        for (int j = 0; j < 8; j++) u[j] = __fmul_rn(u[j], f[j]);
+      }
+      if (shifted) {
+        if (MODE == kStaged) get8(gb_s, threads, tid, v, gb);
+#pragma unroll
+        for (int j = 0; j < 8; j++) u[j] += gb[j];
+      }
+      R.get(at, v, row, f);
+      fetch(v, next + stride);  // (what the chunk had has been read)
+#pragma unroll
+      for (int j = 0; j < 8; j++) y[v][j] = as_stored<RT>(__fadd_rn(__fmul_rn(p.alpha, f[j]), u[j]));
+      mask<MODE>(at, v, y[v]);
+      if (p.r_out) put_row<RT, MODE>(p.r_out, p.ldro, at, v, row, y[v]);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     if (p.pre != FP8_NORM_NONE) {
-      s2 = row_stats(y, n, p.pre, p.cols, p.eps, sum);
+      s2 = row_stats<MODE, NV>(y, at, p.pre, inv, p.eps, ex);
       if (p.x || p.xq) {
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-          float w[8], b[8];
-          load_param8(p.w, 0, c[i], p.cols, 1.0f, w);
-          load_param8(p.b, 0, c[i], p.cols, 0.0f, b);
+        for (int v = 0; v < NV; v++) {
+          float f[8];
 #pragma unroll
-          for (int j = 0; j < 8; j++) v[i][j] = j < n[i] ? fmaf((y[i][j] - s2.x) * s2.y, w[j], b[j]) : 0.0f;
-          if (p.x) block::store8<DT>(p.wide_x, p.x, p.ldx, row, c[i], p.rows, p.cols, v[i]);
-          if (p.xq) store_block8(p, row, c[i], v[i]);
+          for (int j = 0; j < 8; j++) y[v][j] = (y[v][j] - s2.x) * s2.y;
+          if (p.w.p) {
+            if (MODE == kStaged) get8(w_s, threads, tid, v, f);
+            else load_params<MODE>(p.w, 0, at, v, 1.0f, f);
+#pragma unroll
+            for (int j = 0; j < 8; j++) y[v][j] = __fmul_rn(y[v][j], f[j]);
+          }
+          if (p.b.p) {
+            if (MODE == kStaged) get8(b_s, threads, tid, v, f);
+            else load_params<MODE>(p.b, 0, at, v, 0.0f, f);
+#pragma unroll
+            for (int j = 0; j < 8; j++) y[v][j] = __fadd_rn(y[v][j], f[j]);
+          }
+          if (p.x) put_row<DT, MODE>(p.x, p.ldx, at, v, row, y[v]);
+          if (p.xq) {
+            mask<MODE>(at, v, y[v]);
+            put_codes<MODE>(p, at, v, row, y[v]);
+          }
         }
       }
     }
-    if (p.stats && sum.rank == 0 && threadIdx.x == 0)
-      reinterpret_cast<float4 *>(p.stats)[row] = make_float4(s1.x, s1.y, s2.x, s2.y);
+    if (p.stats && threadIdx.x == 0) reinterpret_cast<float4 *>(p.stats)[row] = make_float4(s1.x, s1.y, s2.x, s2.y);
   }
 }
 
@@ -355,7 +613,7 @@ __global__ void __launch_bounds__(512, 2) k_norm_cols(const Cols p) {
     block::unpack8<RT>(raw[i], f[i]);
 #pragma unroll
     for (int j = 0; j < 8; j++)
-      f[i][j] = row < p.rows && col + j < p.cols ? fmaf((f[i][j] - s.z) * s.w, w[j], b[j]) : 0.0f;
+      f[i][j] = row < p.rows && col + j < p.cols ? __fadd_rn(__fmul_rn((f[i][j] - s.z) * s.w, w[j]), b[j]) : 0.0f;
   }
   block::put_tile_maxima(f, sc);
   __syncthreads();
@@ -367,33 +625,42 @@ __global__ void __launch_bounds__(512, 2) k_norm_cols(const Cols p) {
 }
 
 // ---------------------------------------------------------------- backward
-// The rows are dealt out in units, each within one gate row; a cluster takes
+// The rows are dealt out in units, each within one gate row; a CTA takes
 // neighbouring units.  Its sums over rows stay in registers: dw2 and db2 until
 // it ends, A and C until its unit does.
+//
+// dh needs means of q = G g w1, and G needs means of dx w2: two exchanges, one
+// waiting for the other.  But G is linear in its means: with H = dr' + rho2 dx w2,
+//   q = gw H - gw rho2 (m0 + n2 m1)
+//   mean(q)    = mean(gw H)    - rho2 (m0 mean(gw)    + m1 mean(gw n2))
+//   mean(q n1) = mean(gw n1 H) - rho2 (m0 mean(gw n1) + m1 mean(gw n1 n2))
+// so one pass over the row gives all of them in one exchange, and a second one
+// (from shared memory) writes everything.
 struct Plan {
-  int ctas;                // per row
-  int threads, groups;     // of a CTA
+  int chunks, threads, groups;         // NV; of a CTA: threads of a row, rows at a time
   int gate_rows, unit_rows, per_gate;  // rows of a gate row and of a unit, units per gate row
   long long units;
-  int clusters;
+  int ctas;
 };
 
-constexpr int kMostClusters = 148;  // (a CTA of 512 threads on every SM of a B200)
+constexpr int kSms = 148;
+
+inline int padded(int cols) { return (cols + 7) / 8 * 8; }  // of a partial sum
 
 inline Plan plan_of(int rows, int cols, int gate_rows) {
   Plan p = {};
-  p.ctas = (cols + kBwdCols - 1) / kBwdCols;
-  const int vecs = ((cols + 7) / 8 + p.ctas - 1) / p.ctas;
-  p.threads = (vecs + 31) / 32 * 32;
-  p.groups = p.ctas > 1 ? 1 : kBwdThreads / p.threads;
+  const int vecs = (cols + 7) / 8;
+  p.chunks = vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : 4;
+  p.threads = (vecs + 32 * p.chunks - 1) / (32 * p.chunks) * 32;
+  p.groups = p.threads < kThreads ? kThreads / p.threads : 1;
   p.gate_rows = gate_rows < rows ? gate_rows : rows;
-  const int most = kMostClusters / p.ctas;
+  const int most = p.threads > kThreads ? kSms : 2 * kSms;
   p.unit_rows = rows / most + (rows % most != 0);
   if (p.unit_rows < p.groups) p.unit_rows = p.groups;
   if (rows == 0) return p;
   p.per_gate = p.gate_rows / p.unit_rows + (p.gate_rows % p.unit_rows != 0);
   p.units = ((long long)rows + p.gate_rows - 1) / p.gate_rows * p.per_gate;
-  p.clusters = (int)(p.units < most ? p.units : most);
+  p.ctas = (int)(p.units < most ? p.units : most);
   return p;
 }
 
@@ -406,214 +673,404 @@ struct Bwd {
   Vec w, pw, g;
   size_t ldg;
   float alpha;
-  int wide_dx, wide_dro, wide_h, wide_ro, wide_dh, wide_dr;
-  float *ef, *ac;  // partial sums [cluster][2][cols] and [unit][2][cols], or null
+  float *ef, *ac;  // partial sums [CTA][2][padded cols] and [unit][2][padded cols], or null
   int gate_rows, unit_rows, per_gate;
   long long units;
 };
 
+
+struct BwdSmem {
+  int w, gw, comb, bytes;
+};
+template <int DT, int RT>
+__host__ __device__ inline BwdSmem bwd_smem(int chunks, bool h, bool dro, bool pre, bool scaled, bool groups, int mode) {
+  BwdSmem s;
+  int at = mode == kStaged ? chunks * 16 * ((h ? kPieces<DT> : 0) + (dro ? kPieces<RT> : 0) + (pre ? kPieces<DT> + kPieces<RT> : 0)) : 0;
+  auto take = [&](bool on) {
+    const int o = on && mode == kStaged ? at : -1;
+    at += o >= 0 ? chunks * 32 : 0;
+    return o;
+  };
+  s.w = take(pre), s.gw = take(scaled);
+  s.comb = groups ? at : -1;
+  at += groups ? kThreads * 32 : 0;
+  s.bytes = at;
+  return s;
+}
+
 // Adds up the groups of a CTA and writes one partial sum.
-__device__ __forceinline__ void flush(float (&a)[8], float *comb, float *out, int c, int cols) {
-  const int t = threadIdx.x, T = blockDim.x;
-  if (blockDim.y > 1) {
+template <int MODE, int NV>
+__device__ __forceinline__ void flush(float (&a)[8], float *comb, float *out, const Place &at, int v, int threads, int tid) {
+  if (NV == 1 && blockDim.y > 1) {  // (rows of several chunks have a CTA to themselves)
     __syncthreads();
-    float4 *at = reinterpret_cast<float4 *>(comb) + (threadIdx.y * T + t) * 2;
-    at[0] = make_float4(a[0], a[1], a[2], a[3]);
-    at[1] = make_float4(a[4], a[5], a[6], a[7]);
+    put8(comb, threads, tid, 0, a);
     __syncthreads();
     if (threadIdx.y == 0) {
       for (int y = 1; y < (int)blockDim.y; y++) {
-        const float *q = comb + (y * T + t) * 8;
+        float f[8];
+        get8(comb, threads, y * blockDim.x + threadIdx.x, 0, f);
 #pragma unroll
-        for (int j = 0; j < 8; j++) a[j] += q[j];
+        for (int j = 0; j < 8; j++) a[j] += f[j];
       }
     }
   }
   if (threadIdx.y == 0) {
+    if constexpr (MODE == kStaged) {
+      if (at.has<MODE>(v, 0)) {
+        float4 *o = reinterpret_cast<float4 *>(out + at.col<MODE>(v, 0));
+        o[0] = make_float4(a[0], a[1], a[2], a[3]);
+        o[1] = make_float4(a[4], a[5], a[6], a[7]);
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (c + j < cols) out[c + j] = a[j];
+      for (int j = 0; j < 8; j++)
+        if (at.has<MODE>(v, j)) out[at.col<MODE>(v, j)] = a[j];
+    }
   }
 #pragma unroll
   for (int j = 0; j < 8; j++) a[j] = 0.0f;
 }
 
-template <int DT, int RT>
-__global__ void __launch_bounds__(kBwdThreads, 1) k_norm_bwd(const Bwd p, unsigned ctas) {
+// POST: whether there is a post norm; BIAS: whether sums of dx and of G are
+// wanted (gradients of b, of post_b, and of a gate behind post_b).  kDirect goes
+// by p.post, and takes the sums.
+template <int DT, int RT, bool POST, bool BIAS, int NV, int MODE>
+__global__ void __launch_bounds__(kCtaThreads<NV, MODE>, NV == 4 ? 1 : 2) k_norm_bwd(const Bwd p) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float slots[2][2][128];
-  __shared__ __align__(16) float comb[kBwdThreads * 8];
-  RowSum sum = row_sum(slots, ctas);
-  const int c = (int)(sum.rank * blockDim.x + threadIdx.x) * 8, n = max(0, min(8, p.cols - c));
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  __shared__ __align__(16) float slots[2][8][kMostWarps];
+  Exchange ex = exchange(slots);
+  const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
+  const Place at = {p.cols, (int)threadIdx.x, (int)blockDim.x};
+  const bool post = MODE == kStaged ? POST : p.post != FP8_NORM_NONE;
+  const bool pre = p.pre != FP8_NORM_NONE, scaled = p.h && (p.g.p || (post && p.pw.p));
+  const BwdSmem lay = bwd_smem<DT, RT>(NV * threads, p.h, p.dro, pre, scaled, blockDim.y > 1, MODE);
+  float *const w_s = reinterpret_cast<float *>(norm_smem + lay.w), *const gw_s = reinterpret_cast<float *>(norm_smem + lay.gw);
+  float *const comb = reinterpret_cast<float *>(norm_smem + lay.comb);
+  uint8_t *slot = norm_smem;
+  auto take = [&](bool on, int pieces) {
+    uint8_t *s = slot;
+    slot += on ? NV * threads * 16 * pieces : 0;
+    return s;
+  };
+  constexpr size_t de = DT == FP8_DT_F32 ? 4 : 2, re = RT == FP8_DT_F32 ? 4 : 2;
+  const Rows<DT, MODE> DX = {static_cast<const uint8_t *>(p.dx), p.lddx * de, take(pre, kPieces<DT>), threads, tid};
+  const Rows<RT, MODE> RO = {static_cast<const uint8_t *>(p.ro), p.ldro * re, take(pre, kPieces<RT>), threads, tid};
+  const Rows<RT, MODE> DRO = {static_cast<const uint8_t *>(p.dro), p.lddro * re, take(p.dro, kPieces<RT>), threads, tid};
+  const Rows<DT, MODE> H = {static_cast<const uint8_t *>(p.h), p.ldh * de, take(p.h, kPieces<DT>), threads, tid};
+  auto fetch = [&](int v, int row) {
+    if (pre) {
+      DX.fetch(at, v, row);
+      RO.fetch(at, v, row);
+    }
+    if (p.dro) DRO.fetch(at, v, row);
+    if (p.h) H.fetch(at, v, row);
+  };
   const float inv = 1.0f / (float)p.cols;
-  const unsigned cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
-  const long long u0 = p.units * cluster / clusters, u1 = p.units * (cluster + 1) / clusters;
-  float w2[8], E[8], F[8], A[8], C[8];
-  load_param8(p.w, 0, c, p.cols, 1.0f, w2);
+  const size_t ld_sum = (size_t)(p.cols + 7) / 8 * 8;
+  const long long u0 = p.units * blockIdx.x / gridDim.x, u1 = p.units * (blockIdx.x + 1) / gridDim.x;
+  float E[NV][8], F[NV][8], A[NV][8], C[NV][8];
 #pragma unroll
-  for (int j = 0; j < 8; j++) E[j] = F[j] = A[j] = C[j] = 0.0f;
+  for (int v = 0; v < NV; v++)
+#pragma unroll
+    for (int j = 0; j < 8; j++) E[v][j] = F[v][j] = A[v][j] = C[v][j] = 0.0f;
+  // the rows of unit u
+  struct Span {
+    long long first, last;
+  };
+  auto rows_of = [&](long long u) -> Span {
+    const long long gate = u / p.per_gate, first = gate * p.gate_rows;
+    const long long end = min(first + p.gate_rows, (long long)p.rows);
+    const long long r0 = first + (u - gate * p.per_gate) * p.unit_rows;
+    return {r0, min(r0 + p.unit_rows, end)};
+  };
+  float4 s_next = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+  auto fetch_first = [&](long long u) {
+    if (u >= u1) return;
+    const Span s = rows_of(u);
+    const long long row = s.first + threadIdx.y;
+    if (row >= s.last) return;
+#pragma unroll
+    for (int v = 0; v < NV; v++) fetch(v, (int)row);
+    if (p.stats) s_next = __ldg(reinterpret_cast<const float4 *>(p.stats) + row);
+  };
+  fetch_first(u0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  if (MODE == kStaged && pre) {
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+      float f[8];
+      load_params<MODE>(p.w, 0, at, v, 1.0f, f);
+      put8(w_s, threads, tid, v, f);
+    }
+  }
+  auto weight = [&](int v, float (&f)[8]) {
+    if (MODE == kStaged) get8(w_s, threads, tid, v, f);
+    else load_params<MODE>(p.w, 0, at, v, 1.0f, f);
+  };
+  // the gate's row times the post norm's w
+  auto gate_params = [&](int v, int gate, float (&g)[8]) {
+    load_params<MODE>(p.g, (size_t)gate * p.ldg, at, v, 1.0f, g);
+    if (post) {
+      float f[8];
+      load_params<MODE>(p.pw, 0, at, v, 1.0f, f);
+#pragma unroll
+      for (int j = 0; j < 8; j++) g[j] *= f[j];
+    }
+  };
+  int gate_now = -1;
   for (long long u = u0; u < u1; u++) {
     const int gate = (int)(u / p.per_gate);
-    const int first = gate * p.gate_rows, last = (int)min((long long)first + p.gate_rows, (long long)p.rows);
-    const long long r0 = first + (u - (long long)gate * p.per_gate) * p.unit_rows;
-    const int r1 = (int)min(r0 + p.unit_rows, (long long)last);
-    float gw[8];
-    load_param8(p.g, (size_t)gate * p.ldg, c, p.cols, 1.0f, gw);
-    if (p.post != FP8_NORM_NONE) {
-      float pw[8];
-      load_param8(p.pw, 0, c, p.cols, 1.0f, pw);
+    const Span span = rows_of(u);
+    if (MODE == kStaged && scaled && gate != gate_now) {
+      gate_now = gate;
 #pragma unroll
-      for (int j = 0; j < 8; j++) gw[j] *= pw[j];
+      for (int v = 0; v < NV; v++) {
+        float g[8];
+        gate_params(v, gate, g);
+        put8(gw_s, threads, tid, v, g);
+      }
     }
-    for (long long row_ = r0 + threadIdx.y; row_ < r1; row_ += blockDim.y) {
-      const int row = (int)row_;
-      const float4 s = __ldg(reinterpret_cast<const float4 *>(p.stats) + row);
-      float G[8], t[8], v[8];
-      if (p.dro) {
-        block::unpack8<RT>(load_row8<RT>(p.dro, p.lddro, p.wide_dro, row, p.rows, c, p.cols), G);
-      } else {
+    auto gate_weight = [&](int v, float (&f)[8]) {
+      if (MODE == kStaged) get8(gw_s, threads, tid, v, f);
+      else gate_params(v, gate, f);
+    };
+    for (long long r = span.first + threadIdx.y; r < span.last; r += blockDim.y) {
+      const int row = (int)r;
+      const float4 s = s_next;
+      const bool more = r + blockDim.y < span.last;
+      if (more && p.stats) s_next = __ldg(reinterpret_cast<const float4 *>(p.stats) + row + blockDim.y);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      float m0 = 0.0f, m1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+      if (pre || post) {
+        float k[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll(NV == 4 ? 1 : NV)
+        for (int v = 0; v < NV; v++) {
+          float t[8], n2[8];
+          if (pre) {
+            float w[8];
+            DX.get(at, v, row, t);
+            RO.get(at, v, row, n2);
+            weight(v, w);
+            mask<MODE>(at, v, t);
+            mask<MODE>(at, v, n2);
 #pragma unroll
-        for (int j = 0; j < 8; j++) G[j] = 0.0f;
-      }
-      if (p.pre != FP8_NORM_NONE) {
-        block::unpack8<DT>(load_row8<DT>(p.dx, p.lddx, p.wide_dx, row, p.rows, c, p.cols), t);
-        block::unpack8<RT>(load_row8<RT>(p.ro, p.ldro, p.wide_ro, row, p.rows, c, p.cols), v);
-        float m[2] = {0.0f, 0.0f};
+            for (int j = 0; j < 8; j++) {
+              n2[j] = (n2[j] - s.z) * s.w;
+              t[j] *= w[j];
+              k[0] = fmaf(t[j], n2[j], k[0]);
+              k[1] += t[j];
+            }
+          } else {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          v[j] = (v[j] - s.z) * s.w;  // n2
-          E[j] = fmaf(t[j], v[j], E[j]);
-          F[j] += t[j];
-          t[j] *= w2[j];
-          m[0] += t[j];
-          m[1] = fmaf(t[j], v[j], m[1]);
-        }
-        sum(m);
-        const float m0 = p.pre == FP8_NORM_LAYER ? m[0] * inv : 0.0f, m1 = m[1] * inv;
-#pragma unroll
-        for (int j = 0; j < 8; j++) G[j] = j < n ? fmaf(s.w, t[j] - m0 - v[j] * m1, G[j]) : 0.0f;
-      }
-      if (p.dr) {
-#pragma unroll
-        for (int j = 0; j < 8; j++) t[j] = p.alpha * G[j];
-        block::store8<RT>(p.wide_dr, p.dr, p.lddr, row, c, p.rows, p.cols, t);
-      }
-      if (p.h) {
-        block::unpack8<DT>(load_row8<DT>(p.h, p.ldh, p.wide_h, row, p.rows, c, p.cols), v);
-        if (p.post != FP8_NORM_NONE) {
-          float m[2] = {0.0f, 0.0f};
-#pragma unroll
-          for (int j = 0; j < 8; j++) {
-            v[j] = (v[j] - s.x) * s.y;  // n1
-            t[j] = G[j] * gw[j];
-            m[0] += t[j];
-            m[1] = fmaf(t[j], v[j], m[1]);
+            for (int j = 0; j < 8; j++) t[j] = n2[j] = 0.0f;
           }
-          sum(m);
-          const float m0 = p.post == FP8_NORM_LAYER ? m[0] * inv : 0.0f, m1 = m[1] * inv;
+          if (post) {
+            float q[8], n1[8], h[8];
+            if (p.dro) {
+              DRO.get(at, v, row, h);
+            } else {
 #pragma unroll
-          for (int j = 0; j < 8; j++) t[j] = s.y * (t[j] - m0 - v[j] * m1);
+              for (int j = 0; j < 8; j++) h[j] = 0.0f;
+            }
+            H.get(at, v, row, n1);
+            if (scaled) {
+              gate_weight(v, q);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; j++) q[j] = 1.0f;
+            }
+            mask<MODE>(at, v, q);
+            mask<MODE>(at, v, h);
+            mask<MODE>(at, v, n1);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              n1[j] = (n1[j] - s.x) * s.y;
+              const float qh = q[j] * fmaf(s.w, t[j], h[j]), qn = q[j] * n1[j];
+              k[2] = fmaf(qh, n1[j], k[2]);
+              k[3] = fmaf(qn, n2[j], k[3]);
+              k[4] += qh;
+              k[5] = fmaf(q[j], n2[j], k[5]);
+              k[6] += qn;
+              k[7] += q[j];
+            }
+          }
+        }
+        if (post) {
+          if (p.pre == FP8_NORM_LAYER || p.post == FP8_NORM_LAYER) {
+            row_sums(k, ex);
+          } else {
+            float few[4] = {k[0], k[1], k[2], k[3]};
+            row_sums(few, ex);
+            k[0] = few[0], k[2] = few[2], k[3] = few[3];
+          }
+        } else {
+          float few[2] = {k[0], k[1]};
+          row_sums(few, ex);
+          k[0] = few[0], k[1] = few[1];
+        }
+        m1 = k[0] * inv;
+        if (p.pre == FP8_NORM_LAYER) m0 = k[1] * inv;
+        if (post) {
+          t1 = (k[2] - s.w * fmaf(m0, k[6], m1 * k[3])) * inv;
+          if (p.post == FP8_NORM_LAYER) t0 = (k[4] - s.w * fmaf(m0, k[7], m1 * k[5])) * inv;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < NV; v++) {
+        float G[8], t[8], n[8];
+        if (p.dro) {
+          DRO.get(at, v, row, G);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; j++) t[j] = G[j] * gw[j];
+          for (int j = 0; j < 8; j++) G[j] = 0.0f;
         }
-        if (p.dh) block::store8<DT>(p.wide_dh, p.dh, p.lddh, row, c, p.rows, p.cols, t);
+        if (pre) {
+          float w[8];
+          DX.get(at, v, row, t);
+          RO.get(at, v, row, n);
+          weight(v, w);
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-          A[j] = fmaf(G[j], v[j], A[j]);
-          C[j] += G[j];
+          for (int j = 0; j < 8; j++) {
+            n[j] = (n[j] - s.z) * s.w;
+            E[v][j] = fmaf(t[j], n[j], E[v][j]);
+            if (BIAS) F[v][j] += t[j];
+            G[j] = fmaf(s.w, fmaf(t[j], w[j], -m0) - n[j] * m1, G[j]);
+          }
+        }
+        if (p.h) H.get(at, v, row, n);
+        if (MODE == kStaged && more) fetch(v, row + (int)blockDim.y);  // (what the chunk had has been read)
+        if (p.dr) {
+#pragma unroll
+          for (int j = 0; j < 8; j++) t[j] = p.alpha * G[j];
+          put_row<RT, MODE>(p.dr, p.lddr, at, v, row, t);
+        }
+        if (p.h) {
+          if (scaled) {
+            gate_weight(v, t);
+#pragma unroll
+            for (int j = 0; j < 8; j++) t[j] *= G[j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) t[j] = G[j];
+          }
+          if (post) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              n[j] = (n[j] - s.x) * s.y;
+              t[j] = s.y * (t[j] - t0 - n[j] * t1);
+            }
+          }
+          if (p.dh) put_row<DT, MODE>(p.dh, p.lddh, at, v, row, t);
+          if (p.ac) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+              A[v][j] = fmaf(G[j], n[j], A[v][j]);
+              if (BIAS) C[v][j] += G[j];
+            }
+          }
         }
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    fetch_first(u + 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
     if (p.ac) {
-      flush(A, comb, p.ac + (size_t)(2 * u) * p.cols, c, p.cols);
-      flush(C, comb, p.ac + (size_t)(2 * u + 1) * p.cols, c, p.cols);
+#pragma unroll
+      for (int v = 0; v < NV; v++) {
+        flush<MODE, NV>(A[v], comb, p.ac + (size_t)(2 * u) * ld_sum, at, v, threads, tid);
+        if (BIAS) flush<MODE, NV>(C[v], comb, p.ac + (size_t)(2 * u + 1) * ld_sum, at, v, threads, tid);
+      }
     }
   }
   if (p.ef) {
-    flush(E, comb, p.ef + (size_t)(2 * cluster) * p.cols, c, p.cols);
-    flush(F, comb, p.ef + (size_t)(2 * cluster + 1) * p.cols, c, p.cols);
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+      flush<MODE, NV>(E[v], comb, p.ef + (size_t)(2 * blockIdx.x) * ld_sum, at, v, threads, tid);
+      if (BIAS) flush<MODE, NV>(F[v], comb, p.ef + (size_t)(2 * blockIdx.x + 1) * ld_sum, at, v, threads, tid);
+    }
   }
 }
 
 struct Params {
   const float *ef, *ac;
-  int cols, clusters, gates, per_gate, post;
+  int cols, ctas, gates, per_gate;
+  bool post, bias;
   Vec pw, pb, g;
   size_t ldg;
   Vec dw, db, dpw, dpb, dg;  // outputs
   size_t lddg;
+  int col_blocks;
 };
 
-constexpr int kParamLanes = 16;
+constexpr int kParamLanes = 32;
 
-// Adds up v over the lanes (threadIdx.y) of each column, in their order.
-__device__ __forceinline__ float lane_sum(float v, float (&sh)[kParamLanes][33]) {
-  __syncthreads();
-  sh[threadIdx.y][threadIdx.x] = v;
-  __syncthreads();
-  float s = 0.0f;
-#pragma unroll
-  for (int y = 0; y < kParamLanes; y++) s += sh[y][threadIdx.x];
-  return s;
-}
-
-// The parameters' gradients from the partial sums: 32 columns a CTA.
+// The parameters' gradients from the partial sums: a CTA takes 32 columns of
+// one job (the pre norm's, the post norm's, or one gate row's), its lanes
+// (threadIdx.y) every 32nd partial sum.
 __global__ void __launch_bounds__(32 * kParamLanes) k_norm_params(const Params p) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ float sh[kParamLanes][33];
-  const int c = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
+  __shared__ float sh[2][kParamLanes][33];
+  const int job = (int)(blockIdx.x / p.col_blocks) - 2, c = (int)(blockIdx.x % p.col_blocks) * 32 + threadIdx.x;
+  const int y = threadIdx.y;
+  const size_t ld = (size_t)(p.cols + 7) / 8 * 8;
   const bool in = c < p.cols;
-  if (p.dw.p || p.db.p) {
-    float e = 0.0f, f = 0.0f;
+  float a = 0.0f, b = 0.0f;
+  if (job == -2) {
+    if (!p.dw.p && !p.db.p) return;
     if (in) {
-      for (int i = y; i < p.clusters; i += kParamLanes) {
-        e += p.ef[(size_t)(2 * i) * p.cols + c];
-        f += p.ef[(size_t)(2 * i + 1) * p.cols + c];
+#pragma unroll 4
+      for (int i = y; i < p.ctas; i += kParamLanes) {
+        a += p.ef[2 * i * ld + c];
+        if (p.bias) b += p.ef[(2 * i + 1) * ld + c];
       }
     }
-    e = lane_sum(e, sh);
-    f = lane_sum(f, sh);
-    if (in && y == 0) {
-      store_param(p.dw, c, e);
-      store_param(p.db, c, f);
-    }
-  }
-  if (!p.dg.p && !p.dpw.p && !p.dpb.p) return;
-  const float pw = in && p.post != FP8_NORM_NONE ? param_at(p.pw, c, 1.0f) : 1.0f;
-  const float pb = in && p.post != FP8_NORM_NONE ? param_at(p.pb, c, 0.0f) : 0.0f;
-  // few gate rows: the lanes share each one's units; many: each lane takes whole gate rows
-  const bool share = p.gates < kParamLanes;
-  float wsum = 0.0f, bsum = 0.0f;
-  for (int s = share ? 0 : y; s < p.gates; s += share ? 1 : kParamLanes) {
-    float a = 0.0f, k = 0.0f;
+  } else if (job == -1) {
+    if (!p.dpw.p && !p.dpb.p) return;
+    const long long units = (long long)p.gates * p.per_gate;
     if (in) {
-      for (long long i = share ? y : 0; i < p.per_gate; i += share ? kParamLanes : 1) {
-        const size_t u = (size_t)s * p.per_gate + i;
-        a += p.ac[2 * u * p.cols + c];
-        k += p.ac[(2 * u + 1) * p.cols + c];
+#pragma unroll 4
+      for (long long i = y; i < units; i += kParamLanes) {
+        const float g = param_at(p.g, (size_t)(i / p.per_gate) * p.ldg + c, 1.0f);
+        a = fmaf(g, p.ac[2 * i * ld + c], a);
+        if (p.bias) b = fmaf(g, p.ac[(2 * i + 1) * ld + c], b);
       }
     }
-    if (share) {
-      a = lane_sum(a, sh);
-      k = lane_sum(k, sh);
-    }
+  } else {
+    if (!p.dg.p) return;
     if (in) {
-      const float g = param_at(p.g, (size_t)s * p.ldg + c, 1.0f);
-      wsum = fmaf(g, a, wsum);
-      bsum = fmaf(g, k, bsum);
-      if (!share || y == 0) store_param(p.dg, (size_t)s * p.lddg + c, fmaf(pw, a, pb * k));
+#pragma unroll 4
+      for (int i = y; i < p.per_gate; i += kParamLanes) {
+        const size_t u = (size_t)job * p.per_gate + i;
+        a += p.ac[2 * u * ld + c];
+        if (p.bias) b += p.ac[(2 * u + 1) * ld + c];
+      }
     }
   }
-  if (!share) {
-    wsum = lane_sum(wsum, sh);
-    bsum = lane_sum(bsum, sh);
+  sh[0][y][threadIdx.x] = a;
+  sh[1][y][threadIdx.x] = b;
+  __syncthreads();
+  if (y > 1) return;
+  a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kParamLanes; i++) a += sh[y][i][threadIdx.x];  // in their order
+  // the first lane has the sums with the normed value, the second the plain ones
+  if (job < 0) {
+    if (in) store_param(job == -2 ? (y == 0 ? p.dw : p.db) : (y == 0 ? p.dpw : p.dpb), c, a);
+    return;
   }
-  if (in && y == 0) {
-    store_param(p.dpw, c, wsum);
-    store_param(p.dpb, c, bsum);
+  if (y == 1) {
+    if (!p.post || !p.pb.p) return;
+    // dg = w1 A + b1 C: C by way of shared memory, behind what the first lane reads
+    sh[1][0][threadIdx.x] = a;
+  }
+  asm volatile("bar.sync 1, %0;" ::"r"(p.post && p.pb.p ? 64 : 32) : "memory");
+  if (y == 0 && in) {
+    if (p.post) a *= param_at(p.pw, c, 1.0f);
+    if (p.post && p.pb.p) a = fmaf(param_at(p.pb, c, 0.0f), sh[1][0][threadIdx.x], a);
+    store_param(p.dg, (size_t)job * p.lddg + c, a);
   }
 }
 

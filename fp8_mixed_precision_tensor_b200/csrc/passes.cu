@@ -1,0 +1,448 @@
+// passes.cu -- the C ABI of include/fp8.h's passes between and behind the linear
+// layers: norms with gate and residual, log probabilities, distillation.
+//
+// A translation unit of its own, compiled beside libfp8.cu.  Its copies of what
+// the shared headers define (kernels, the device status word) have names of
+// their own; fp8_get_status reads both status words.
+#define fp8lib fp8lib_passes
+
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "../../include/fp8.h"
+#include "host.cuh"
+#include "loss.cuh"
+#include "norm.cuh"
+
+using namespace fp8lib;
+
+namespace {
+
+// SMs of the current device, looked up once.
+int sm_count(int *out) {
+  static std::mutex mu;
+  static int sms[64] = {0};
+  int dev;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return FP8_ERR_CUDA;
+  *out = sms[dev];
+  return FP8_OK;
+}
+
+// A vector of parameters, or a matrix with cols elements a row: FP8_OK, or what is wrong with it.
+int check_vector(const fp8_vector &v) {
+  if (!v.p) return FP8_OK;
+  if (!valid_dtype(v.dtype)) return FP8_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(v.p) % dtype_bytes(v.dtype) ? FP8_ERR_UNALIGNED : FP8_OK;
+}
+norm::Vec vec_of(const fp8_vector &v) { return {v.p, v.dtype}; }
+
+bool norm_kind(int k) { return k == FP8_NORM_NONE || k == FP8_NORM_RMS || k == FP8_NORM_LAYER; }
+
+int check_norm(const fp8_norm_params *p, bool h) {
+  if (!p || !valid_dtype(p->dtype) || (p->res_dtype != p->dtype && p->res_dtype != FP8_DT_F32) || p->rows < 0 ||
+      p->cols < 0 || !norm_kind(p->pre) || !norm_kind(p->post) || !(p->eps >= 0.0f) || !isfinite(p->eps) ||
+      !isfinite(p->res_scale) || (!h && p->rows && (p->post != FP8_NORM_NONE || p->gate.p)))
+    return FP8_ERR_INVALID_ARG;
+  int rc;
+  for (const fp8_vector *v : {&p->w, &p->b, &p->post_w, &p->post_b, &p->gate})
+    if ((rc = check_vector(*v))) return rc;
+  if (p->gate.p && (p->gate_rows < 1 || p->ld_gate < (size_t)p->cols)) return FP8_ERR_INVALID_ARG;
+  if (p->cols > FP8_NORM_COLS_MAX || too_long(p->rows, p->cols)) return FP8_ERR_UNSUPPORTED;
+  return FP8_OK;
+}
+
+bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Whether a matrix, where there is one, is read and written in whole groups of eight.
+bool whole_groups(const void *p, int dtype, size_t ld, int cols) { return !p || (wide_rows(p, dtype, ld) && cols % 8 == 0); }
+
+template <typename F>
+void with_chunks(int chunks, F f) {
+  if (chunks == 1) f(std::integral_constant<int, 1>());
+  else if (chunks == 2) f(std::integral_constant<int, 2>());
+  else f(std::integral_constant<int, 4>());
+}
+constexpr int kMostSmem = 232448 - 2048;  // of a CTA, beside a kernel's own 2 KB
+
+template <typename F>
+void with_norm_types(int dt, int rt, F f) {
+  with_dtype(dt, [&](auto d) {
+    constexpr int DT = decltype(d)::value;
+    if (rt == dt) f(d, d);
+    else if constexpr (DT != FP8_DT_F32) f(d, std::integral_constant<int, FP8_DT_F32>());
+  });
+}
+
+int gate_rows_of(const fp8_norm_params *p) { return p->gate.p && p->gate_rows < p->rows ? p->gate_rows : p->rows; }
+
+struct LossArgs {
+  const void *logits;
+  int dtype, rows, cols;
+  size_t ld;
+  float inv_temp;
+};
+int check_loss(const LossArgs &a) {
+  if (!valid_dtype(a.dtype) || a.rows < 0 || a.cols < 0 || !(a.inv_temp > 0.0f) || !isfinite(a.inv_temp))
+    return FP8_ERR_INVALID_ARG;
+  if (a.rows == 0 || a.cols == 0) return FP8_OK;
+  if (too_long(a.rows, a.cols)) return FP8_ERR_UNSUPPORTED;
+  return check_matrix(a.logits, a.dtype, a.cols, a.ld);
+}
+bool index_bytes(int b) { return b == 4 || b == 8; }
+
+// CTAs that share a row, and their threads.
+struct LossGrid {
+  unsigned ctas, threads;
+  int vecs;  // 16-byte vectors of a CTA, at the most
+};
+LossGrid loss_grid(int rows, int cols, int dtype, int sms, unsigned least) {
+  const int elems = dtype == FP8_DT_F32 ? 4 : 8, vecs = cols / elems;
+  LossGrid g = {1, 0, 0};
+  while (g.ctas < 8 && (long long)rows * g.ctas * 2 <= sms && vecs / (int)(2 * g.ctas) >= 512) g.ctas *= 2;
+  g.vecs = (vecs + (int)g.ctas - 1) / (int)g.ctas;
+  const unsigned most = (long long)rows * g.ctas >= 2LL * sms ? 256u : 1024u;
+  g.threads = least;
+  while (g.threads < most && (int)g.threads * 2 <= g.vecs) g.threads *= 2;
+  return g;
+}
+
+template <int DT, int MODE, bool ENT>
+int launch_loss_fwd(const loss::Fwd &p, const LossGrid &g, size_t smem, cudaStream_t s) {
+  const auto kernel = loss::k_loss_fwd<DT, MODE, ENT>;
+  if ((long long)p.rows * g.ctas > INT_MAX) return FP8_ERR_UNSUPPORTED;
+  int rc;
+  if (smem > 48 * 1024 && (rc = set_smem(kernel, (int)smem))) return rc;
+  return launch_pdl(kernel, (unsigned)p.rows * g.ctas, g.threads, smem, s, g.ctas, p, g.ctas);
+}
+
+template <bool LIST>
+int launch_loss_bwd(const loss::Bwd &p, int dtype, int fmt, cudaStream_t s) {
+  int rc = FP8_OK;
+  with_dtype(dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (p.out.q || p.out.qt) {
+      with_fmt(fmt, [&](auto f) {
+        rc = launch_pdl(loss::k_loss_bwd_tiles<DT, LIST, decltype(f)::value>, tile_grid(p.rows, p.cols), 512, 0, s, 1, p);
+      });
+      return;
+    }
+    constexpr int share = loss::kBwdThreads * loss::kBwdVecs;
+    const long long vecs = p.cols / loss::kElems<DT>, chunks = vecs ? (vecs + share - 1) / share : 1;
+    if (chunks * p.rows > INT_MAX) {
+      rc = FP8_ERR_UNSUPPORTED;
+      return;
+    }
+    rc = launch_pdl(loss::k_loss_bwd_rows<DT, LIST>, (unsigned)(chunks * p.rows), loss::kBwdThreads, 0, s, 1, p,
+                    (unsigned)chunks);
+  });
+  return rc;
+}
+
+// The outputs of a gradient of the logits, and the factors that both have.
+int loss_outputs(loss::Bwd &p, const LossArgs &a, const float *stats, int fmt, int margin, const fp8_blocks *row,
+                 const fp8_blocks *col, void *d, size_t ldd) {
+  if (!fp8_fmt(fmt) || margin < 0 || margin > 64) return FP8_ERR_INVALID_ARG;
+  int rc = check_loss(a);
+  if (rc || a.rows == 0 || a.cols == 0) return rc;
+  if ((!row && !col && !d) || !stats) return FP8_ERR_INVALID_ARG;
+  if ((row && (rc = check_blocks(row, a.cols))) || (col && (rc = check_blocks(col, a.cols))) ||
+      (d && (rc = check_matrix(d, a.dtype, a.cols, ldd))))
+    return rc;
+  if (!aligned16(stats)) return FP8_ERR_UNALIGNED;
+  const size_t e = dtype_bytes(a.dtype);
+  p.z = static_cast<const uint8_t *>(a.logits);
+  p.ld = a.ld * e;
+  p.rows = a.rows;
+  p.cols = a.cols;
+  p.beta = a.inv_temp;
+  p.stats = stats;
+  p.d = static_cast<uint8_t *>(d);
+  p.ldd = ldd * e;
+  p.margin = margin;
+  p.vec_z = wide_rows(a.logits, a.dtype, a.ld);
+  p.vec_d = wide_rows(d, a.dtype, ldd);
+  p.out = cast_out(row, col);
+  return FP8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8_norm_fwd(const fp8_norm_params *p, const void *h, size_t ldh, const void *r, size_t ldr, void *r_out,
+                 size_t ldr_out, float *stats, void *x, size_t ldx, int margin, const fp8_blocks *x_row,
+                 const fp8_blocks *x_col, void *stream) {
+  int rc = check_norm(p, h != nullptr);
+  if (rc) return rc;
+  if (margin < 0 || margin > 64) return FP8_ERR_INVALID_ARG;
+  const int rows = p->rows, cols = p->cols;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  if ((p->pre == FP8_NORM_NONE && (x || x_row || x_col)) || (x_col && !stats) ||
+      (!r_out && (h || p->res_scale != 1.0f)) || (!r_out && !x && !x_row && !x_col && !stats))
+    return FP8_ERR_INVALID_ARG;
+  if ((h && (rc = check_matrix(h, p->dtype, cols, ldh))) || (rc = check_matrix(r, p->res_dtype, cols, ldr)) ||
+      (r_out && (rc = check_matrix(r_out, p->res_dtype, cols, ldr_out))) ||
+      (x && (rc = check_matrix(x, p->dtype, cols, ldx))) || (x_row && (rc = check_blocks(x_row, cols))) ||
+      (x_col && (rc = check_blocks(x_col, cols))))
+    return rc;
+  if (!aligned16(stats)) return FP8_ERR_UNALIGNED;
+  norm::Fwd a = {};
+  a.h = h, a.r = r, a.r_out = r_out, a.x = x, a.stats = stats;
+  a.ldh = ldh, a.ldr = ldr, a.ldro = ldr_out, a.ldx = ldx;
+  if (x_row) a.xq = x_row->q, a.xs = x_row->s, a.ldxq = x_row->ld;
+  a.rows = rows, a.cols = cols, a.pre = p->pre, a.post = p->post;
+  a.w = vec_of(p->w), a.b = vec_of(p->b), a.pw = vec_of(p->post_w), a.pb = vec_of(p->post_b), a.g = vec_of(p->gate);
+  a.gate_rows = p->gate.p ? p->gate_rows : rows;
+  a.ldg = p->ld_gate;
+  a.alpha = p->res_scale, a.eps = p->eps, a.margin = margin;
+  const bool whole = whole_groups(h, p->dtype, ldh, cols) && whole_groups(r, p->res_dtype, ldr, cols) &&
+                     whole_groups(r_out, p->res_dtype, ldr_out, cols) && whole_groups(x, p->dtype, ldx, cols);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int sms;
+  if ((rc = sm_count(&sms))) return rc;
+  const norm::Plan plan = norm::plan_of(rows, cols, rows);
+  const bool post = p->post != FP8_NORM_NONE;
+  with_norm_types(p->dtype, p->res_dtype, [&](auto dt, auto rt) {
+    constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
+    with_chunks(plan.chunks, [&](auto nv) {
+      constexpr int NV = decltype(nv)::value;
+      const int threads = plan.threads * plan.groups;
+      auto launch = [&](auto kernel, int mode) {
+        const int smem = norm::fwd_smem<DT, RT>(NV * threads, h, a.w.p, a.b.p, a.g.p || (post && a.pw.p), post && a.pb.p,
+                                                mode).bytes;
+        if (smem > kMostSmem) return FP8_ERR_UNSUPPORTED;
+        if (int e = set_smem(kernel, smem)) return e;
+        // as many CTAs as stay resident (64 registers a thread, 128 with four chunks) share the rows out
+        const int by_regs = 65536 / (threads * (NV == 4 ? 128 : 64)), by_smem = 232448 / (smem + 2048);
+        const unsigned most = (unsigned)(sms * (by_regs < by_smem ? by_regs : by_smem));
+        const unsigned need = ((unsigned)rows + (unsigned)plan.groups - 1) / (unsigned)plan.groups;
+        return launch_pdl(kernel, need < most ? need : most, dim3(plan.threads, plan.groups), smem, s, 1, a);
+      };
+      rc = FP8_ERR_UNSUPPORTED;
+      if (whole && cols <= norm::kStagedCols) {
+        if (post) rc = launch(norm::k_norm_fwd<DT, RT, true, NV, norm::kStaged>, norm::kStaged);
+        else rc = launch(norm::k_norm_fwd<DT, RT, false, NV, norm::kStaged>, norm::kStaged);
+      }
+      if (rc == FP8_ERR_UNSUPPORTED)
+        rc = launch(norm::k_norm_fwd<DT, RT, true, NV == 1 ? 1 : 4, norm::kDirect>, norm::kDirect);
+    });
+    if (rc || !x_col) return;
+    norm::Cols c = {};
+    c.r = r_out ? r_out : r;
+    c.ldr = r_out ? ldr_out : ldr;
+    c.stats = stats;
+    c.w = a.w, c.b = a.b;
+    c.rows = rows, c.cols = cols, c.margin = margin, c.vec = wide_rows(c.r, p->res_dtype, c.ldr);
+    c.qt = x_col->q, c.st = x_col->s, c.ldqt = x_col->ld;
+    rc = launch_pdl(norm::k_norm_cols<RT>, tile_grid(rows, cols), 512, 0, s, 1, c);
+  });
+  return rc;
+}
+
+size_t fp8_norm_workspace_bytes(int rows, int cols, int gate_rows) {
+  if (rows <= 0 || cols <= 0 || cols > FP8_NORM_COLS_MAX || gate_rows <= 0) return 0;
+  const norm::Plan plan = norm::plan_of(rows, cols, gate_rows);
+  return ((size_t)plan.ctas + (size_t)plan.units) * 2 * (size_t)norm::padded(cols) * sizeof(float);
+}
+
+int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const void *dr_out, size_t lddr_out,
+                 const void *h, size_t ldh, const void *r_out, size_t ldr_out, const float *stats, void *dh,
+                 size_t lddh, void *dr, size_t lddr, const fp8_norm_grads *grads, void *workspace, size_t ws_bytes,
+                 void *stream) {
+  int rc = check_norm(p, h != nullptr);
+  if (rc) return rc;
+  const fp8_norm_grads none = {};
+  const fp8_norm_grads &g = grads ? *grads : none;
+  for (const fp8_vector *v : {&g.w, &g.b, &g.post_w, &g.post_b, &g.gate})
+    if ((rc = check_vector(*v))) return rc;
+  const int rows = p->rows, cols = p->cols;
+  const bool pre = p->pre != FP8_NORM_NONE, post = p->post != FP8_NORM_NONE;
+  const bool of_pre = g.w.p || g.b.p, of_post = g.post_w.p || g.post_b.p || g.gate.p;
+  // (matrices without rows have no address)
+  if ((rows && (pre != (dx != nullptr) || (!h && (dh || of_post)) || (!dh && !dr && !of_pre && !of_post))) ||
+      (!pre && of_pre) || (!post && (g.post_w.p || g.post_b.p)) || (g.gate.p && !p->gate.p) ||
+      (g.gate.p && g.ld_gate < (size_t)cols))
+    return FP8_ERR_INVALID_ARG;
+  if (cols == 0) return FP8_OK;
+  if (rows && ((pre && ((rc = check_matrix(dx, p->dtype, cols, lddx)) || (rc = check_matrix(r_out, p->res_dtype, cols, ldr_out)))) ||
+               (dr_out && (rc = check_matrix(dr_out, p->res_dtype, cols, lddr_out))) ||
+               (h && (rc = check_matrix(h, p->dtype, cols, ldh))) || (dh && (rc = check_matrix(dh, p->dtype, cols, lddh))) ||
+               (dr && (rc = check_matrix(dr, p->res_dtype, cols, lddr)))))
+    return rc;
+  if (rows && (pre || post) && !stats) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(stats) || !aligned16(workspace)) return FP8_ERR_UNALIGNED;
+  const norm::Plan plan = norm::plan_of(rows, cols, gate_rows_of(p));
+  const bool sums = of_pre || of_post;
+  const bool bias = g.b.p || g.post_b.p || (g.gate.p && post && p->post_b.p);  // plain sums of dx or G
+  if (sums && rows && (!workspace || ws_bytes < fp8_norm_workspace_bytes(rows, cols, gate_rows_of(p))))
+    return FP8_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  norm::Bwd a = {};
+  float *ws = static_cast<float *>(workspace);
+  if (rows) {
+    a.dx = dx, a.dro = dr_out, a.h = h, a.ro = r_out, a.stats = stats, a.dh = dh, a.dr = dr;
+    a.lddx = lddx, a.lddro = lddr_out, a.ldh = ldh, a.ldro = ldr_out, a.lddh = lddh, a.lddr = lddr;
+    a.rows = rows, a.cols = cols, a.pre = p->pre, a.post = p->post;
+    a.w = vec_of(p->w), a.pw = vec_of(p->post_w), a.g = vec_of(p->gate);
+    a.ldg = p->ld_gate;
+    a.alpha = p->res_scale;
+    const bool whole = whole_groups(dx, p->dtype, lddx, cols) && whole_groups(dr_out, p->res_dtype, lddr_out, cols) &&
+                       whole_groups(h, p->dtype, ldh, cols) && whole_groups(pre ? r_out : nullptr, p->res_dtype, ldr_out, cols) &&
+                       whole_groups(dh, p->dtype, lddh, cols) && whole_groups(dr, p->res_dtype, lddr, cols);
+    a.ef = of_pre ? ws : nullptr;
+    a.ac = of_post ? ws + (size_t)plan.ctas * 2 * norm::padded(cols) : nullptr;
+    a.gate_rows = plan.gate_rows, a.unit_rows = plan.unit_rows, a.per_gate = plan.per_gate, a.units = plan.units;
+    with_norm_types(p->dtype, p->res_dtype, [&](auto dt, auto rt) {
+      constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
+      with_chunks(plan.chunks, [&](auto nv) {
+        constexpr int NV = decltype(nv)::value;
+        const int threads = plan.threads * plan.groups;
+        auto launch = [&](auto kernel, int mode) {
+          const int smem = norm::bwd_smem<DT, RT>(NV * threads, h, dr_out, pre, h && (a.g.p || (post && a.pw.p)),
+                                                  plan.groups > 1, mode).bytes;
+          if (smem > kMostSmem) return FP8_ERR_UNSUPPORTED;
+          if (int e = set_smem(kernel, smem)) return e;
+          return launch_pdl(kernel, (unsigned)plan.ctas, dim3(plan.threads, plan.groups), smem, s, 1, a);
+        };
+        rc = FP8_ERR_UNSUPPORTED;
+        if (whole && cols <= norm::kStagedCols)
+          with_bool(post, [&](auto has_post) {
+            with_bool(bias || NV == 4, [&](auto has_bias) {
+              constexpr bool kBias = decltype(has_bias)::value || NV == 4;
+              rc = launch(norm::k_norm_bwd<DT, RT, decltype(has_post)::value, kBias, NV, norm::kStaged>, norm::kStaged);
+            });
+          });
+        if (rc == FP8_ERR_UNSUPPORTED)
+          rc = launch(norm::k_norm_bwd<DT, RT, true, true, NV == 1 ? 1 : 4, norm::kDirect>, norm::kDirect);
+      });
+    });
+    if (rc) return rc;
+  }
+  if (!sums) return FP8_OK;
+  norm::Params q = {};
+  q.ef = ws, q.ac = ws + (size_t)plan.ctas * 2 * norm::padded(cols);
+  q.cols = cols, q.ctas = plan.ctas, q.per_gate = rows ? plan.per_gate : 1;
+  q.post = post, q.bias = bias;
+  q.gates = rows ? (int)(plan.units / plan.per_gate) : 0;
+  q.pw = vec_of(p->post_w), q.pb = vec_of(p->post_b), q.g = vec_of(p->gate), q.ldg = p->ld_gate;
+  q.dw = vec_of(g.w), q.db = vec_of(g.b), q.dpw = vec_of(g.post_w), q.dpb = vec_of(g.post_b), q.dg = vec_of(g.gate);
+  q.lddg = g.ld_gate;
+  q.col_blocks = (cols + 31) / 32;
+  const long long jobs = 2 + (g.gate.p ? (long long)q.gates : 0);
+  if (jobs * q.col_blocks > INT_MAX) return FP8_ERR_UNSUPPORTED;
+  return launch_pdl(norm::k_norm_params, (unsigned)(jobs * q.col_blocks), dim3(32, norm::kParamLanes), 0, s, 1, q);
+}
+
+int fp8_logprob_fwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, const void *tokens,
+                    int token_bytes, float *logp, float *entropy, int top, float *top_logp, int *top_ids,
+                    float *stats, void *stream) {
+  const LossArgs a = {logits, dtype, rows, cols, ld, inv_temp};
+  int rc = check_loss(a);
+  if (rc) return rc;
+  if (top < 0 || top > FP8_TOP_MAX) return FP8_ERR_INVALID_ARG;
+  if (rows == 0) return FP8_OK;  // (tensors without rows have no address)
+  if ((logp != nullptr) != (tokens != nullptr) || (tokens && !index_bytes(token_bytes)) ||
+      (top > 0) != (top_logp != nullptr) || (top > 0) != (top_ids != nullptr) || (!logp && !entropy && !top && !stats))
+    return FP8_ERR_INVALID_ARG;
+  if (cols == 0 || top > cols) return FP8_ERR_INVALID_ARG;
+  if (!aligned16(stats) || (tokens && !aligned_to(tokens, token_bytes)) || !aligned_to(logp, 4) || !aligned_to(entropy, 4) ||
+      !aligned_to(top_logp, 4) || !aligned_to(top_ids, 4))
+    return FP8_ERR_UNALIGNED;
+  int sms;
+  if ((rc = sm_count(&sms))) return rc;
+  loss::Fwd p = {};
+  p.z = static_cast<const uint8_t *>(logits);
+  p.ld = ld * dtype_bytes(dtype);
+  p.rows = rows, p.cols = cols, p.beta = inv_temp;
+  p.tokens = tokens, p.token_bytes = token_bytes, p.top = top;
+  p.logp = logp, p.entropy = entropy, p.top_logp = top_logp, p.top_ids = top_ids, p.stats = stats;
+  const LossGrid g = loss_grid(rows, cols, dtype, sms, 128);
+  const size_t smem = top ? sizeof(loss::TopScratch) : 0;
+  with_dtype(dtype, [&](auto dt) {
+    with_bool(entropy != nullptr, [&](auto ent) {
+      rc = launch_loss_fwd<decltype(dt)::value, loss::kLogprob, decltype(ent)::value>(p, g, smem,
+                                                                                     static_cast<cudaStream_t>(stream));
+    });
+  });
+  return rc;
+}
+
+int fp8_logprob_bwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, const void *tokens,
+                    int token_bytes, const float *stats, const float *dlogp, const float *dentropy, int fmt, int margin,
+                    const fp8_blocks *d_row, const fp8_blocks *d_col, void *dlogits, size_t ld_d, void *stream) {
+  const LossArgs a = {logits, dtype, rows, cols, ld, inv_temp};
+  if (rows > 0 && ((dlogp != nullptr) != (tokens != nullptr) || (!dlogp && !dentropy) || (tokens && !index_bytes(token_bytes))))
+    return FP8_ERR_INVALID_ARG;
+  loss::Bwd p = {};
+  int rc = loss_outputs(p, a, stats, fmt, margin, d_row, d_col, dlogits, ld_d);
+  if (rc || rows == 0 || cols == 0) return rc;
+  if ((tokens && !aligned_to(tokens, token_bytes)) || !aligned_to(dlogp, 4) || !aligned_to(dentropy, 4))
+    return FP8_ERR_UNALIGNED;
+  p.tokens = tokens, p.token_bytes = token_bytes, p.g = dlogp, p.g_ent = dentropy;
+  return launch_loss_bwd<false>(p, dtype, fmt, static_cast<cudaStream_t>(stream));
+}
+
+int fp8_distill_fwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, int form, int top,
+                    const void *ids, int id_bytes, const void *values, int value_dtype, float *loss, float *stats,
+                    int *list_ids, float *list_q, void *stream) {
+  const LossArgs a = {logits, dtype, rows, cols, ld, inv_temp};
+  int rc = check_loss(a);
+  if (rc) return rc;
+  if ((form != FP8_DISTILL_TOP && form != FP8_DISTILL_TAIL) || top < 1 || top > FP8_DISTILL_MAX || !index_bytes(id_bytes) ||
+      !valid_dtype(value_dtype))
+    return FP8_ERR_INVALID_ARG;
+  if (rows == 0) return FP8_OK;
+  if (cols == 0 || !ids || !values || !loss || !stats || !list_ids || !list_q) return FP8_ERR_INVALID_ARG;
+  if (cols > FP8_DISTILL_COLS_MAX) return FP8_ERR_UNSUPPORTED;
+  if (!aligned16(stats) || !aligned_to(ids, id_bytes) || !aligned_to(values, dtype_bytes(value_dtype)) ||
+      !aligned_to(loss, 4) || !aligned_to(list_ids, 4) || !aligned_to(list_q, 4))
+    return FP8_ERR_UNALIGNED;
+  int sms;
+  if ((rc = sm_count(&sms))) return rc;
+  loss::Fwd p = {};
+  p.z = static_cast<const uint8_t *>(logits);
+  p.ld = ld * dtype_bytes(dtype);
+  p.rows = rows, p.cols = cols, p.beta = inv_temp;
+  p.top = top, p.ids = ids, p.id_bytes = id_bytes, p.values = values, p.value_dt = value_dtype;
+  p.loss = loss, p.stats = stats, p.list_ids = list_ids, p.list_q = list_q;
+  const LossGrid g = loss_grid(rows, cols, dtype, sms, 256);
+  const size_t marks = form == FP8_DISTILL_TAIL ? ((size_t)g.vecs * (16 / dtype_bytes(dtype)) + 31) / 32 * 4 : 0;
+  const size_t smem = sizeof(loss::ListScratch) + marks;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  with_dtype(dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    rc = form == FP8_DISTILL_TOP ? launch_loss_fwd<DT, loss::kListTop, false>(p, g, smem, s)
+                                 : launch_loss_fwd<DT, loss::kListTail, false>(p, g, smem, s);
+  });
+  return rc;
+}
+
+int fp8_distill_bwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, int top,
+                    const int *list_ids, const float *list_q, const float *stats, const float *dloss, int fmt,
+                    int margin, const fp8_blocks *d_row, const fp8_blocks *d_col, void *dlogits, size_t ld_d,
+                    void *stream) {
+  const LossArgs a = {logits, dtype, rows, cols, ld, inv_temp};
+  if (top < 1 || top > FP8_DISTILL_MAX || (rows > 0 && (!list_ids || !list_q || !dloss))) return FP8_ERR_INVALID_ARG;
+  loss::Bwd p = {};
+  int rc = loss_outputs(p, a, stats, fmt, margin, d_row, d_col, dlogits, ld_d);
+  if (rc || rows == 0 || cols == 0) return rc;
+  if (cols > FP8_DISTILL_COLS_MAX) return FP8_ERR_UNSUPPORTED;
+  if (!aligned_to(list_ids, 4) || !aligned_to(list_q, 4) || !aligned_to(dloss, 4)) return FP8_ERR_UNALIGNED;
+  p.g = dloss, p.K = top, p.list_ids = list_ids, p.list_q = list_q;
+  return launch_loss_bwd<true>(p, dtype, fmt, static_cast<cudaStream_t>(stream));
+}
+
+// Reads and clears this unit's status word on the stream; the caller waits for it.
+int passes_take_status(unsigned *host_out, cudaStream_t s) {
+  k_take_status<<<1, 1, 0, s>>>();
+  if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
+  return cuda_rc(cudaMemcpyFromSymbolAsync(host_out, g_status_taken, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s));
+}
+
+}  // extern "C"

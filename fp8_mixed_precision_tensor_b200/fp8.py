@@ -33,7 +33,7 @@ FP8_E4M3, FP8_E5M2, FP8_F16S = 0, 1, 2
 FP8_ACT_GELU_TANH, FP8_ACT_GELU_ERF, FP8_ACT_SILU = 0, 1, 2
 FP8_BLOCK_TOKENS_MAX = 32
 FP8_NORM_NONE, FP8_NORM_RMS, FP8_NORM_LAYER = 0, 1, 2
-FP8_NORM_COLS_MAX, FP8_TOP_MAX, FP8_DISTILL_MAX, FP8_DISTILL_COLS_MAX = 32768, 32, 1024, 1048576
+FP8_NORM_COLS_MAX, FP8_TOP_MAX, FP8_DISTILL_MAX, FP8_DISTILL_COLS_MAX = 16384, 32, 1024, 1048576
 FP8_DISTILL_TOP, FP8_DISTILL_TAIL = 0, 1
 
 _DT = {torch.float32: FP8_DT_F32, torch.bfloat16: FP8_DT_BF16, torch.float16: FP8_DT_F16}

@@ -696,7 +696,7 @@ typedef struct {
 #define FP8_NORM_NONE 0
 #define FP8_NORM_RMS 1
 #define FP8_NORM_LAYER 2
-#define FP8_NORM_COLS_MAX 32768
+#define FP8_NORM_COLS_MAX 16384
 typedef struct {
   int rows, cols;
   int dtype, res_dtype;
