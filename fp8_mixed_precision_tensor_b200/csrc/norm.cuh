@@ -23,83 +23,96 @@
 namespace fp8lib {
 namespace norm {
 
-using block::Raw8;
-
-// A row belongs to a group of T threads (a multiple of 32) of a CTA; a thread
-// holds NV chunks of eight columns.  A CTA takes as many narrow rows at a time
-// as it has threads for, and row after row while it lives.
+// A row belongs to a group of threads (a multiple of 32) of a CTA; a thread holds
+// 8 CK of its columns, CK = 1, 2 or 4, as NV chunks of CW neighbouring ones: 8,
+// or 4 where the residual is binary32, so that a warp reads and writes whole
+// sectors of every matrix (chunks of 8 binary32 numbers in 16-byte pieces cost
+// each sector twice: 46 instead of 36 us for 4096 x 4096 forward).  A CTA takes
+// as many narrow rows at a time as it has threads for, and row after row while
+// it lives.
 constexpr int kThreads = 256;      // of a CTA, but for the widest rows
 constexpr int kMostThreads = 512;
 constexpr int kMostWarps = kMostThreads / 32;
 constexpr int kStagedCols = 12288;  // the widest staged rows: 384 threads, 168 registers each
-template <int NV, int MODE>
-constexpr int kCtaThreads = NV < 4 ? kThreads : MODE == 0 ? kStagedCols / 32 : kMostThreads;
+template <int CK, int MODE>
+constexpr int kCtaThreads = CK < 4 ? kThreads : MODE == 0 ? kStagedCols / 32 : kMostThreads;
+// Whether the parameters are in shared memory (unaligned wide rows read them each time).
+__host__ __device__ constexpr bool held(int CK, int mode) { return mode == 0 || CK == 1; }
+template <int RT>
+constexpr int kWidth = RT == FP8_DT_F32 ? 4 : 8;  // CW
 
 // How rows are read and written.
-//   kStaged  eight neighbouring columns a chunk, in 16-byte pieces; the next
-//            row's are copied into the thread's own part of shared memory while
-//            it works on the present one (no barriers: nobody else reads them)
+//   kStaged  the next row's chunks are copied into the thread's own part of
+//            shared memory while it works on the present one (no barriers:
+//            nobody else reads them)
 //   kDirect  rows that start anywhere: the lanes of a warp take neighbouring
 //            columns, and element by element from memory, twice where two
 //            passes need them
 enum { kStaged = 0, kDirect = 1 };
 
 // The chunk v of a thread, and whether it lies in the row (kStaged: all of it).
+// width: threads from one chunk's columns to the next one's; lanes: from one
+// chunk's place in shared memory to the next one's (a constant, but for the
+// widest rows: a CTA has 256 threads, in one row or several).
+template <int CK, int CW, int MODE>
 struct Place {
-  int cols, t, T;
-  template <int MODE>
+  static constexpr int NV = CK * 8 / CW;
+  int cols, t;
+  __device__ __forceinline__ int width() const { return CK == 2 ? kThreads : (int)blockDim.x; }
+  __device__ __forceinline__ int lanes() const { return CK == 4 ? (int)blockDim.x : kThreads; }
   __device__ __forceinline__ int col(int v, int j) const {
-    return MODE == kStaged ? (v * T + t) * 8 + j : (v * T + (t & ~31)) * 8 + 32 * j + (t & 31);
+    return MODE == kStaged ? (v * width() + t) * CW + j : (v * width() + (t & ~31)) * CW + 32 * j + (t & 31);
   }
-  template <int MODE>
-  __device__ __forceinline__ bool has(int v, int j) const {
-    return col<MODE>(v, MODE == kStaged ? 0 : j) < cols;
-  }
+  __device__ __forceinline__ bool has(int v, int j) const { return col(v, MODE == kStaged ? 0 : j) < cols; }
+  // Whether the thread works on its chunk v.  Staged chunks outside the row are
+  // skipped whole (by a branch that only a row's last warp splits at).
+  __device__ __forceinline__ bool mine(int v) const { return MODE == kDirect || has(v, 0); }
 };
+
+// A chunk's elements as they are stored, 8 or 16 bytes.
+template <int DT, int CW>
+struct __align__(CW == 8 || DT == FP8_DT_F32 ? 16 : 8) Raw {
+  static constexpr int kWords = DT == FP8_DT_F32 ? CW : CW / 2;
+  static_assert(kWords <= 4, "one piece");
+  uint32_t w[kWords];
+};
+template <int DT, int CW>
+__device__ __forceinline__ void unpack(const Raw<DT, CW> &r, float (&f)[CW]) {
+#pragma unroll
+  for (int i = 0; i < Raw<DT, CW>::kWords; i++) {
+    if constexpr (DT == FP8_DT_F32) {
+      f[i] = __uint_as_float(r.w[i]);
+    } else if constexpr (DT == FP8_DT_BF16) {
+      f[2 * i] = __uint_as_float(r.w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+    } else {
+      const float2 h = h2f2(r.w[i]);
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    }
+  }
+}
+template <int DT, int CW>
+__device__ __forceinline__ Raw<DT, CW> pack(const float (&f)[CW]) {
+  Raw<DT, CW> r;
+#pragma unroll
+  for (int i = 0; i < Raw<DT, CW>::kWords; i++) {
+    if constexpr (DT == FP8_DT_F32) {
+      r.w[i] = __float_as_uint(f[i]);
+    } else if constexpr (DT == FP8_DT_BF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      r.w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    } else {
+      r.w[i] = f16x2(f[2 * i], f[2 * i + 1]);
+    }
+  }
+  return r;
+}
 
 struct Vec {
   const void *p;
   int dt;
 };
-
-// Eight parameters at column c (a multiple of 8); `fill` where there are none.
-__device__ __forceinline__ void load_param8(Vec v, size_t off, int c, int cols, float fill, float (&f)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; j++) f[j] = fill;
-  if (!v.p || c >= cols) return;
-  if (v.dt == FP8_DT_F32) {
-    const float *p = reinterpret_cast<const float *>(v.p) + off + c;
-    if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-      const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (c + j < cols) f[j] = __ldg(p + j);
-    return;
-  }
-  const uint16_t *p = reinterpret_cast<const uint16_t *>(v.p) + off + c;
-  Raw8<FP8_DT_BF16> r;
-  if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
-  } else {
-    uint32_t e[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) e[j] = c + j < cols ? __ldg(p + j) : 0u;
-#pragma unroll
-    for (int j = 0; j < 4; j++) r.w[j] = e[2 * j] | (e[2 * j + 1] << 16);
-  }
-  if (v.dt == FP8_DT_BF16) {
-    block::unpack8<FP8_DT_BF16>(r, f);
-  } else {
-    Raw8<FP8_DT_F16> h;
-#pragma unroll
-    for (int j = 0; j < 4; j++) h.w[j] = r.w[j];
-    block::unpack8<FP8_DT_F16>(h, f);
-  }
-}
 
 __device__ __forceinline__ float param_at(Vec v, size_t i, float fill) {
   if (!v.p) return fill;
@@ -116,116 +129,242 @@ __device__ __forceinline__ void store_param(Vec v, size_t i, float x) {
 }
 
 
-template <int MODE>
-__device__ __forceinline__ void load_params(Vec v, size_t off, const Place &at, int chunk, float fill, float (&f)[8]) {
-  if constexpr (MODE == kStaged) {
-    load_param8(v, off, at.col<MODE>(chunk, 0), at.cols, fill, f);
-  } else {
+// A chunk's parameters; `fill` where there are none.
+template <int DT, int CW>
+__device__ __forceinline__ bool load_vector(const void *p, size_t i, float (&f)[CW]) {
+  using R = Raw<DT == FP8_DT_F32 ? FP8_DT_F32 : DT, DT == FP8_DT_F32 ? 4 : CW>;
+  const uint8_t *q = reinterpret_cast<const uint8_t *>(p) + i * (DT == FP8_DT_F32 ? 4 : 2);
+  if (reinterpret_cast<uintptr_t>(q) % alignof(R)) return false;
+  if constexpr (DT == FP8_DT_F32) {
 #pragma unroll
-    for (int j = 0; j < 8; j++) f[j] = at.has<MODE>(chunk, j) ? param_at(v, off + at.col<MODE>(chunk, j), fill) : fill;
+    for (int h = 0; h < CW / 4; h++) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(q) + h);
+      f[4 * h] = v.x, f[4 * h + 1] = v.y, f[4 * h + 2] = v.z, f[4 * h + 3] = v.w;
+    }
+  } else {
+    R r;
+    if constexpr (CW == 8) *reinterpret_cast<uint4 *>(r.w) = __ldg(reinterpret_cast<const uint4 *>(q));
+    else *reinterpret_cast<uint2 *>(r.w) = __ldg(reinterpret_cast<const uint2 *>(q));
+    unpack<DT, CW>(r, f);
   }
+  return true;
+}
+template <int CK, int CW, int MODE>
+__device__ __forceinline__ void load_params(Vec v, size_t off, const Place<CK, CW, MODE> &at, int chunk, float fill,
+                                            float (&f)[CW]) {
+#pragma unroll
+  for (int j = 0; j < CW; j++) f[j] = fill;
+  if (!v.p) return;
+  if constexpr (MODE == kStaged) {
+    if (!at.has(chunk, 0)) return;
+    const size_t i = off + at.col(chunk, 0);
+    if (v.dt == FP8_DT_F32 ? load_vector<FP8_DT_F32, CW>(v.p, i, f)
+                           : v.dt == FP8_DT_BF16 ? load_vector<FP8_DT_BF16, CW>(v.p, i, f) : load_vector<FP8_DT_F16, CW>(v.p, i, f))
+      return;
+  }
+#pragma unroll
+  for (int j = 0; j < CW; j++)
+    if (at.has(chunk, j)) f[j] = param_at(v, off + at.col(chunk, j), fill);
+}
+
+// Eight parameters at column c.
+__device__ __forceinline__ void load_eight(Vec v, int c, int cols, float fill, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j++) f[j] = fill;
+  if (!v.p || c >= cols) return;
+  if (c + 8 <= cols && (v.dt == FP8_DT_F32 ? load_vector<FP8_DT_F32, 8>(v.p, c, f)
+                                           : v.dt == FP8_DT_BF16 ? load_vector<FP8_DT_BF16, 8>(v.p, c, f)
+                                                                 : load_vector<FP8_DT_F16, 8>(v.p, c, f)))
+    return;
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    if (c + j < cols) f[j] = param_at(v, c + j, fill);
 }
 
 template <int DT>
-__device__ __forceinline__ float as_stored(float x) {
-  if constexpr (DT == FP8_DT_F32) return x;
-  else if constexpr (DT == FP8_DT_BF16) return __bfloat162float(__float2bfloat16_rn(x));
-  else return __half2float(__float2half_rn(x));
+constexpr int kBytes = DT == FP8_DT_F32 ? 4 : 2;  // of an element
+
+// Keeps a value in a register that the compiler would else fetch or work out
+// again for every row.
+template <typename V>
+__device__ __forceinline__ void keep(V &v) {
+  if constexpr (sizeof(V) == 8) asm volatile("" : "+l"(v));
+  else asm volatile("" : "+r"(v));
 }
 
-template <int DT>
-constexpr int kPieces = DT == FP8_DT_F32 ? 2 : 1;  // of 16 bytes in a chunk
-
-// A matrix's chunks of one row.  `slot`: this matrix's part of the CTA's shared
-// memory, [chunk][piece][thread] of 16 bytes.
-template <int DT, int MODE>
-struct Rows {
-  const uint8_t *p;
+// A matrix whose rows a thread reads, one after another.  kStaged: `p` is the
+// thread's place in the row that is fetched next, and shared memory has
+// [chunk][thread] of a chunk's bytes, `slot` the thread's place in the first;
+// kDirect: the present row.
+template <int DT, int CK, int CW, int MODE>
+struct In {
+  static constexpr int kChunk = sizeof(Raw<DT, CW>);
+  const uint8_t *base;
   size_t ld;  // bytes
   uint8_t *slot;
-  int threads, tid;
+  const uint8_t *p;
+  long long step;
 
-  __device__ __forceinline__ void fetch(const Place &at, int v, int row) const {
+  __device__ __forceinline__ In(const void *m, size_t ld_elems, uint8_t *part, unsigned rows_apart)
+      : base(static_cast<const uint8_t *>(m)), ld(ld_elems * kBytes<DT>),
+        slot(part + (threadIdx.y * blockDim.x + threadIdx.x) * kChunk), p(nullptr), step((long long)ld * rows_apart) {
+    keep(step);
+  }
+  __device__ __forceinline__ void seek(const Place<CK, CW, MODE> &at, long long row) {
+    p = base + row * ld + (MODE == kStaged ? at.t * kChunk : 0);
+  }
+  __device__ __forceinline__ void advance() { p += step; }
+  __device__ __forceinline__ void fetch(const Place<CK, CW, MODE> &at, int v) const {
     if constexpr (MODE == kStaged) {
-      if (!at.has<MODE>(v, 0)) return;
-      const uint8_t *src = p + (size_t)row * ld + (size_t)at.col<MODE>(v, 0) * (DT == FP8_DT_F32 ? 4 : 2);
-#pragma unroll
-      for (int i = 0; i < kPieces<DT>; i++)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                         smem_u32(slot + (size_t)((v * kPieces<DT> + i) * threads + tid) * 16)),
-                     "l"(src + 16 * i)
-                     : "memory");
+      const uint32_t to = smem_u32(slot + v * at.lanes() * kChunk);
+      const uint8_t *src = p + v * at.width() * kChunk;
+      if constexpr (kChunk == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+      else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(src) : "memory");
     }
   }
-  __device__ __forceinline__ void get(const Place &at, int v, int row, float (&f)[8]) const {
+  __device__ __forceinline__ void get(const Place<CK, CW, MODE> &at, int v, float (&f)[CW]) const {
     if constexpr (MODE == kStaged) {
-      Raw8<DT> r;
-#pragma unroll
-      for (int i = 0; i < kPieces<DT>; i++) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(slot + (size_t)((v * kPieces<DT> + i) * threads + tid) * 16);
-        r.w[4 * i] = w.x, r.w[4 * i + 1] = w.y, r.w[4 * i + 2] = w.z, r.w[4 * i + 3] = w.w;
-      }
-      block::unpack8<DT>(r, f);
+      unpack<DT, CW>(*reinterpret_cast<const Raw<DT, CW> *>(slot + v * at.lanes() * kChunk), f);
     } else {
-      const uint8_t *src = p + (size_t)row * ld;
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const int c = min(at.col<MODE>(v, j), at.cols - 1);
-        if constexpr (DT == FP8_DT_F32) f[j] = reinterpret_cast<const float *>(src)[c];
-        else if constexpr (DT == FP8_DT_BF16) f[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(src)[c]);
-        else f[j] = __half2float(reinterpret_cast<const __half *>(src)[c]);
+      for (int j = 0; j < CW; j++) {
+        const int c = min(at.col(v, j), at.cols - 1);
+        if constexpr (DT == FP8_DT_F32) f[j] = reinterpret_cast<const float *>(p)[c];
+        else if constexpr (DT == FP8_DT_BF16) f[j] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[c]);
+        else f[j] = __half2float(reinterpret_cast<const __half *>(p)[c]);
       }
     }
   }
 };
 
-template <int DT, int MODE>
-__device__ __forceinline__ void put_row(void *out, size_t ld, const Place &at, int v, int row, const float (&f)[8]) {
-  if constexpr (MODE == kStaged) {
-    if (!at.has<MODE>(v, 0)) return;
-    constexpr int esz = DT == FP8_DT_F32 ? 4 : 2;
-    uint4 w[DT == FP8_DT_F32 ? 2 : 1];
-    block::pack8<DT>(f, w);
-    uint4 *q = reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(out) + ((size_t)row * ld + at.col<MODE>(v, 0)) * esz);
-    __stcs(q, w[0]);
-    if constexpr (DT == FP8_DT_F32) __stcs(q + 1, w[1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (at.has<MODE>(v, j)) {
-        const size_t i = (size_t)row * ld + at.col<MODE>(v, j);
-        if constexpr (DT == FP8_DT_F32) reinterpret_cast<float *>(out)[i] = f[j];
-        else if constexpr (DT == FP8_DT_BF16) reinterpret_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(f[j]);
-        else reinterpret_cast<__half *>(out)[i] = __float2half_rn(f[j]);
-      }
-  }
-}
+// A matrix whose rows a thread writes; put() leaves in f what was stored.
+template <int DT, int CK, int CW, int MODE>
+struct Out {
+  static constexpr int kChunk = sizeof(Raw<DT, CW>);
+  uint8_t *base;
+  size_t ld;
+  uint8_t *p;
+  long long step;
 
-// Zero outside the row.
-template <int MODE>
-__device__ __forceinline__ void mask(const Place &at, int v, float (&f)[8]) {
-  if constexpr (MODE == kStaged) {
-    if (!at.has<MODE>(v, 0)) {
+  __device__ __forceinline__ Out(void *m, size_t ld_elems, unsigned rows_apart)
+      : base(static_cast<uint8_t *>(m)), ld(ld_elems * kBytes<DT>), p(nullptr), step((long long)ld * rows_apart) {
+    keep(step);
+  }
+  __device__ __forceinline__ void seek(const Place<CK, CW, MODE> &at, long long row) {
+    p = base + row * ld + (MODE == kStaged ? at.t * kChunk : 0);
+  }
+  __device__ __forceinline__ void advance() { p += step; }
+  __device__ __forceinline__ void put(const Place<CK, CW, MODE> &at, int v, float (&f)[CW], bool store = true) const {
+    const Raw<DT, CW> r = pack<DT, CW>(f);
+    if constexpr (DT != FP8_DT_F32) unpack<DT, CW>(r, f);
+    if (!store) return;
+    if constexpr (MODE == kStaged) {
+      uint8_t *q = p + v * at.width() * kChunk;
+      if constexpr (kChunk == 16) __stcs(reinterpret_cast<uint4 *>(q), *reinterpret_cast<const uint4 *>(r.w));
+      else __stcs(reinterpret_cast<uint2 *>(q), *reinterpret_cast<const uint2 *>(r.w));
+    } else {
 #pragma unroll
-      for (int j = 0; j < 8; j++) f[j] = 0.0f;
+      for (int j = 0; j < CW; j++)
+        if (at.has(v, j)) {
+          const int c = at.col(v, j);
+          if constexpr (DT == FP8_DT_F32) reinterpret_cast<uint32_t *>(p)[c] = r.w[j];
+          else reinterpret_cast<uint16_t *>(p)[c] = (uint16_t)(r.w[j >> 1] >> (16 * (j & 1)));
+        }
     }
-  } else {
+  }
+};
+
+template <int CW>
+__device__ __forceinline__ void zero(float (&f)[CW]) {
 #pragma unroll
-    for (int j = 0; j < 8; j++) f[j] = at.has<MODE>(v, j) ? f[j] : 0.0f;
+  for (int j = 0; j < CW; j++) f[j] = 0.0f;
+}
+// Zero outside the row (kDirect).
+template <int CK, int CW, int MODE>
+__device__ __forceinline__ void mask(const Place<CK, CW, MODE> &at, int v, float (&f)[CW]) {
+  if constexpr (MODE == kDirect) {
+#pragma unroll
+    for (int j = 0; j < CW; j++) f[j] = at.has(v, j) ? f[j] : 0.0f;
   }
 }
 
-// Eight floats of a thread in shared memory, its own: [half][thread] of 16 bytes
-// for each chunk.
-__device__ __forceinline__ void put8(float *s, int threads, int tid, int v, const float (&f)[8]) {
-  float4 *p = reinterpret_cast<float4 *>(s) + (size_t)v * 2 * threads + tid;
-  p[0] = make_float4(f[0], f[1], f[2], f[3]);
-  p[threads] = make_float4(f[4], f[5], f[6], f[7]);
+// A chunk at a time on the packed binary32 instructions.
+template <int CW>
+__device__ __forceinline__ float2 pair(const float (&a)[CW], int j) {
+  return make_float2(a[j], a[j + 1]);
 }
-__device__ __forceinline__ void get8(const float *s, int threads, int tid, int v, float (&f)[8]) {
-  const float4 *p = reinterpret_cast<const float4 *>(s) + (size_t)v * 2 * threads + tid;
-  const float4 a = p[0], b = p[threads];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+template <int CW, typename F>
+__device__ __forceinline__ void pairs(float (&o)[CW], F f) {
+#pragma unroll
+  for (int j = 0; j < CW; j += 2) {
+    const float2 r = f(j);
+    o[j] = r.x;
+    o[j + 1] = r.y;
+  }
+}
+template <int CW>
+__device__ __forceinline__ void mul(float (&o)[CW], const float (&a)[CW], const float (&b)[CW]) {
+  pairs(o, [&](int j) { return __fmul2_rn(pair(a, j), pair(b, j)); });
+}
+template <int CW>
+__device__ __forceinline__ void mul(float (&o)[CW], const float (&a)[CW], float s) {
+  pairs(o, [&](int j) { return __fmul2_rn(pair(a, j), both(s)); });
+}
+template <int CW>
+__device__ __forceinline__ void add(float (&o)[CW], const float (&a)[CW], const float (&b)[CW]) {
+  pairs(o, [&](int j) { return __fadd2_rn(pair(a, j), pair(b, j)); });
+}
+template <int CW>
+__device__ __forceinline__ void add(float (&o)[CW], const float (&a)[CW], float s) {
+  pairs(o, [&](int j) { return __fadd2_rn(pair(a, j), both(s)); });
+}
+// o = a b + c
+template <int CW>
+__device__ __forceinline__ void fma8(float (&o)[CW], const float (&a)[CW], const float (&b)[CW], const float (&c)[CW]) {
+  pairs(o, [&](int j) { return __ffma2_rn(pair(a, j), pair(b, j), pair(c, j)); });
+}
+template <int CW>
+__device__ __forceinline__ void fma8(float (&o)[CW], const float (&a)[CW], float s, const float (&c)[CW]) {
+  pairs(o, [&](int j) { return __ffma2_rn(pair(a, j), both(s), pair(c, j)); });
+}
+template <int CW>
+__device__ __forceinline__ void fma8(float (&o)[CW], const float (&a)[CW], const float (&b)[CW], float s) {
+  pairs(o, [&](int j) { return __ffma2_rn(pair(a, j), pair(b, j), both(s)); });
+}
+// (v - mean) rstd: the difference first, so that a large mean costs no digits of it
+template <int CW>
+__device__ __forceinline__ void normed(float (&o)[CW], const float (&a)[CW], float mean, float rstd) {
+  add(o, a, -mean);
+  mul(o, o, rstd);
+}
+// s += sum of a b, in two halves
+template <int CW>
+__device__ __forceinline__ void dot(float2 &s, const float (&a)[CW], const float (&b)[CW]) {
+#pragma unroll
+  for (int j = 0; j < CW; j += 2) s = __ffma2_rn(pair(a, j), pair(b, j), s);
+}
+template <int CW>
+__device__ __forceinline__ void plus(float2 &s, const float (&a)[CW]) {
+#pragma unroll
+  for (int j = 0; j < CW; j += 2) s = __fadd2_rn(s, pair(a, j));
+}
+
+// A chunk of floats of a thread in shared memory, its own: [16 bytes of the
+// chunk][thread] for each chunk, s the thread's place in the first.
+template <int CW>
+__device__ __forceinline__ void put_own(uint8_t *s, int v, int width, const float (&f)[CW]) {
+  float4 *p = reinterpret_cast<float4 *>(s) + v * (CW / 4) * width;
+#pragma unroll
+  for (int h = 0; h < CW / 4; h++) p[h * width] = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+}
+template <int CW>
+__device__ __forceinline__ void get_own(const uint8_t *s, int v, int width, float (&f)[CW]) {
+  const float4 *p = reinterpret_cast<const float4 *>(s) + v * (CW / 4) * width;
+#pragma unroll
+  for (int h = 0; h < CW / 4; h++) {
+    const float4 a = p[h * width];
+    f[4 * h] = a.x, f[4 * h + 1] = a.y, f[4 * h + 2] = a.z, f[4 * h + 3] = a.w;
+  }
 }
 
 // What the warps of a row's group tell one another: up to 8 numbers each, two
@@ -241,8 +380,15 @@ struct Exchange {
   }
   __device__ __forceinline__ float get(int n, int w) const { return slots[buf][n][group * warps + w]; }
   __device__ __forceinline__ float sum(int n) const {
+    if (warps == 8) {  // (most rows: 256 threads)
+      const float4 *q = reinterpret_cast<const float4 *>(slots[buf][n]);
+      const float4 a = q[0], b = q[1];
+      const float2 s = __fadd2_rn(__fadd2_rn(make_float2(a.x, a.y), make_float2(a.z, a.w)),
+                                  __fadd2_rn(make_float2(b.x, b.y), make_float2(b.z, b.w)));
+      return s.x + s.y;
+    }
     float s = 0.0f;
-    if ((warps & 3) == 0) {  // (rows of 1024 columns and more)
+    if ((warps & 3) == 0) {
       for (int w = 0; w < warps; w += 4) {
         const float4 q = *reinterpret_cast<const float4 *>(&slots[buf][n][group * warps + w]);
         s += (q.x + q.y) + (q.z + q.w);
@@ -297,40 +443,41 @@ __device__ __forceinline__ void row_sums(float (&v)[N], Exchange &x) {
 // layer norm's warps take the squares about their own mean, and those are joined
 // about the row's (Chan, Golub, LeVeque), so that one exchange gives both and an
 // offset costs no digits.
-template <int MODE, int NV>
-__device__ __forceinline__ float2 row_stats(const float (&v)[NV][8], const Place &at, int kind, float inv, float eps,
+template <int CK, int CW, int MODE, int NV>
+__device__ __forceinline__ float2 row_stats(const float (&v)[NV][CW], const Place<CK, CW, MODE> &at, int kind, float inv, float eps,
                                             Exchange &x) {
+  float2 s = both(0.0f);
   if (kind == FP8_NORM_RMS) {
-    float q[1] = {0.0f};
 #pragma unroll
-    for (int i = 0; i < NV; i++)
-#pragma unroll
-      for (int j = 0; j < 8; j++) q[0] = fmaf(v[i][j], v[i][j], q[0]);
+    for (int i = 0; i < NV; i++) dot(s, v[i], v[i]);
+    float q[1] = {s.x + s.y};
     row_sums(q, x);
     return make_float2(0.0f, rsqrtf(fmaf(q[0], inv, eps)));
   }
-  // columns of a warp: 256 a chunk
+  // columns of a warp: 32 chunks each time
   auto count = [&](int w) {
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < NV; i++) n += max(0, min(256, at.cols - (i * at.T + w * 32) * 8));
+    for (int i = 0; i < NV; i++) n += max(0, min(32 * CW, at.cols - (i * at.width() + w * 32) * CW));
     return n;
   };
-  float s[1] = {0.0f}, q[1] = {0.0f};
 #pragma unroll
-  for (int i = 0; i < NV; i++)
-#pragma unroll
-    for (int j = 0; j < 8; j++) s[0] += v[i][j];
+  for (int i = 0; i < NV; i++) plus(s, v[i]);
+  float one[1] = {s.x + s.y};
   const int own = count((int)threadIdx.x >> 5);
-  const float total = warp_sums(s), mean_w = own ? total / (float)own : 0.0f;
+  const float total = warp_sums(one), mean_w = own ? total / (float)own : 0.0f;
+  s = both(0.0f);
 #pragma unroll
-  for (int i = 0; i < NV; i++)
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const float d = at.has<MODE>(i, j) ? v[i][j] - mean_w : 0.0f;
-      q[0] = fmaf(d, d, q[0]);
+  for (int i = 0; i < NV; i++) {
+    if (at.mine(i)) {
+      float d[CW];
+      add(d, v[i], -mean_w);
+      mask(at, i, d);
+      dot(s, d, d);
     }
-  const float sq = warp_sums(q);
+  }
+  one[0] = s.x + s.y;
+  const float sq = warp_sums(one);
   if (x.warps == 1) return make_float2(mean_w, rsqrtf(fmaf(sq, inv, eps)));
   if ((threadIdx.x & 31) == 0) {
     x.put(0, total);
@@ -339,11 +486,16 @@ __device__ __forceinline__ float2 row_stats(const float (&v)[NV][8], const Place
   }
   x.wait();
   const float mean = x.sum(0) * inv;
+  // lane w joins warp w
+  const int lane = threadIdx.x & 31;
   float m2 = 0.0f;
-  for (int w = 0; w < x.warps; w++) {
-    const float d = x.get(2, w) - mean;
-    m2 += fmaf((float)count(w) * d, d, x.get(1, w));
+  if (lane < x.warps) {
+    const float d = x.get(2, lane) - mean;
+    m2 = fmaf((float)count(lane) * d, d, x.get(1, lane));
   }
+#pragma unroll
+  for (int b = kMostWarps / 2; b > 0; b /= 2) m2 += __shfl_xor_sync(0xffffffffu, m2, b);
+  m2 = __shfl_sync(0xffffffffu, m2, 0);
   x.next();
   return make_float2(mean, rsqrtf(fmaf(m2, inv, eps)));
 }
@@ -378,42 +530,44 @@ __device__ __forceinline__ void pad_scales(const Fwd &p, int blk, int kblocks, i
 
 // The codes of a thread's chunk of a row's 1x128 blocks with their scales, and
 // with the last row the padding of these.
-template <int MODE>
-__device__ __forceinline__ void put_codes(const Fwd &p, const Place &at, int v, int row, const float (&f)[8]) {
+template <int CK, int CW, int MODE>
+__device__ __forceinline__ void put_codes(const Fwd &p, const Place<CK, CW, MODE> &at, int v, int row, const float (&f)[CW]) {
   const int lane = threadIdx.x & 31, kblocks = (p.cols + 127) / 128;
   uint8_t *q = p.xq + (size_t)row * p.ldxq;
-  if constexpr (MODE == kStaged) {  // 16 lanes a block
+  // lanes l, l + 1 ... of `step` hold a block blk with this amax
+  auto scale = [&](uint32_t m, int blk, int l, int step) {
+    const int k = block::block_exponent(m, kMaxE4M3, p.margin);
+    if (blk < kblocks) {
+      if (l == 0) block::put_scale(p.xs, row, blk, kblocks, k);
+      if (row == p.rows - 1) pad_scales(p, blk, kblocks, l, step);
+    }
+    return pow2f(k);
+  };
+  if constexpr (MODE == kStaged && CW == 8) {  // 16 lanes a block
     float a = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; j += 2) a = block::absmax2(a, f[j], f[j + 1]);
     uint32_t m = __float_as_uint(a);
 #pragma unroll
     for (int b = 8; b > 0; b /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, b));
-    const int k = block::block_exponent(m, kMaxE4M3, p.margin), blk = at.col<MODE>(v, 0) >> 7, l = lane & 15;
-    if (blk < kblocks) {
-      if (l == 0) block::put_scale(p.xs, row, blk, kblocks, k);
-      if (row == p.rows - 1) pad_scales(p, blk, kblocks, l, 16);
-    }
     float2 s[4];
-    block::spread_scale(pow2f(k), s);
+    block::spread_scale(scale(m, at.col(v, 0) >> 7, lane & 15, 16), s);
     const uint2 o = m >= 0x7f800000u ? block::enc8_any<FP8_E4M3>(f, s) : block::enc8<FP8_E4M3>(f, s);
-    if (at.has<MODE>(v, 0)) __stcs(reinterpret_cast<uint2 *>(q + at.col<MODE>(v, 0)), o);
-  } else {  // a warp has two: elements 0 to 3 and 4 to 7 of its lanes
+    if (at.has(v, 0)) __stcs(reinterpret_cast<uint2 *>(q + at.col(v, 0)), o);
+  } else {  // a warp a block: four elements of its lanes
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const float a = block::absmax2(block::absmax2(0.0f, f[4 * h], f[4 * h + 1]), f[4 * h + 2], f[4 * h + 3]);
+    for (int h = 0; h < CW; h += 4) {
+      const float a = block::absmax2(block::absmax2(0.0f, f[h], f[h + 1]), f[h + 2], f[h + 3]);
       const uint32_t m = warp_max_u32(__float_as_uint(a));
-      const int k = block::block_exponent(m, kMaxE4M3, p.margin);
-      const int blk = at.col<MODE>(v, 4 * h) >> 7;
-      if (blk < kblocks) {
-        if (lane == 0) block::put_scale(p.xs, row, blk, kblocks, k);
-        if (row == p.rows - 1) pad_scales(p, blk, kblocks, lane, 32);
-      }
-      const float s = pow2f(k);
-      const uint32_t o = enc4<FP8_E4M3>(f[4 * h] * s, f[4 * h + 1] * s, f[4 * h + 2] * s, f[4 * h + 3] * s);
+      const float s = scale(m, at.col(v, h) >> 7, lane, 32);
+      const uint32_t o = enc4<FP8_E4M3>(f[h] * s, f[h + 1] * s, f[h + 2] * s, f[h + 3] * s);
+      if constexpr (MODE == kStaged) {
+        if (at.has(v, 0)) __stcs(reinterpret_cast<uint32_t *>(q + at.col(v, 0)), o);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; j++)
-        if (at.has<MODE>(v, 4 * h + j)) q[at.col<MODE>(v, 4 * h + j)] = (uint8_t)(o >> (8 * j));
+        for (int j = 0; j < 4; j++)
+          if (at.has(v, h + j)) q[at.col(v, h + j)] = (uint8_t)(o >> (8 * j));
+      }
     }
   }
 }
@@ -423,13 +577,14 @@ __device__ __forceinline__ void put_codes(const Fwd &p, const Place &at, int v, 
 struct FwdSmem {
   int stage, w, b, gw, gb, bytes;  // offsets; -1: absent.  gw, gb: the gate times the post norm's w and b
 };
+// of `columns` columns
 template <int DT, int RT>
-__host__ __device__ inline FwdSmem fwd_smem(int chunks, bool h, bool w, bool b, bool gw, bool gb, int mode) {
+__host__ __device__ inline FwdSmem fwd_smem(int columns, bool h, bool w, bool b, bool gw, bool gb, int mode, bool held) {
   FwdSmem s;
-  int at = mode == kStaged ? chunks * 16 * ((h ? kPieces<DT> : 0) + kPieces<RT>) : 0;
+  int at = mode == kStaged ? columns * ((h ? kBytes<DT> : 0) + kBytes<RT>) : 0;
   auto take = [&](bool on) {
-    const int o = on && mode == kStaged ? at : -1;
-    at += o >= 0 ? chunks * 32 : 0;
+    const int o = on && held ? at : -1;
+    at += o >= 0 ? columns * 4 : 0;
     return o;
   };
   s.stage = 0;
@@ -438,143 +593,172 @@ __host__ __device__ inline FwdSmem fwd_smem(int chunks, bool h, bool w, bool b, 
   return s;
 }
 
-// POST: whether there is a post norm (kDirect goes by p.post).
-template <int DT, int RT, bool POST, int NV, int MODE>
-__global__ void __launch_bounds__(kCtaThreads<NV, MODE>, NV == 4 ? 1 : 4) k_norm_fwd(const Fwd p) {
+// FULL: h, r', x in its type, both norms' w and no codes, the common call, with
+// nothing left to ask for each chunk; POST: whether there is a post norm.  Else
+// both are asked for at run time.
+template <int DT, int RT, bool FULL, bool POST, int CK, int MODE>
+__global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK == 4 ? 1 : 3) k_norm_fwd(const Fwd p) {
+  constexpr int CW = kWidth<RT>, NV = CK * 8 / CW;
+  constexpr bool kHeld = held(CK, MODE);
   pdl_launch_dependents();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t norm_smem[];
   __shared__ __align__(16) float slots[2][8][kMostWarps];
   Exchange ex = exchange(slots);
-  const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
-  const Place at = {p.cols, (int)threadIdx.x, (int)blockDim.x};
-  const bool post = MODE == kStaged ? POST : p.post != FP8_NORM_NONE;
-  const bool scaled = p.g.p || (post && p.pw.p), shifted = post && p.pb.p;
-  const FwdSmem lay = fwd_smem<DT, RT>(NV * threads, p.h, p.w.p, p.b.p, scaled, shifted, MODE);
-  float *const w_s = reinterpret_cast<float *>(norm_smem + lay.w), *const b_s = reinterpret_cast<float *>(norm_smem + lay.b);
-  float *const gw_s = reinterpret_cast<float *>(norm_smem + lay.gw), *const gb_s = reinterpret_cast<float *>(norm_smem + lay.gb);
-  const Rows<RT, MODE> R = {static_cast<const uint8_t *>(p.r), p.ldr * (RT == FP8_DT_F32 ? 4 : 2), norm_smem, threads, tid};
-  const Rows<DT, MODE> H = {static_cast<const uint8_t *>(p.h), p.ldh * (DT == FP8_DT_F32 ? 4 : 2),
-                            norm_smem + NV * threads * 16 * kPieces<RT>, threads, tid};
+  const Place<CK, CW, MODE> at = {p.cols, (int)threadIdx.x};
+  const int W = at.lanes();
+  uint8_t *const own = norm_smem + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+  const bool post = FULL ? POST : p.post != FP8_NORM_NONE;
+  enum { kH = 1, kRout = 2, kX = 4, kXq = 8, kW = 16, kB = 32, kScaled = 64, kShifted = 128, kPre = 256 };
+  int has = (p.h ? kH : 0) | (p.r_out ? kRout : 0) | (p.x ? kX : 0) | (p.xq ? kXq : 0) | (p.w.p ? kW : 0) | (p.b.p ? kB : 0) |
+            (p.g.p || (post && p.pw.p) ? kScaled : 0) | (post && p.pb.p ? kShifted : 0) | (p.pre != FP8_NORM_NONE ? kPre : 0);
+  constexpr int kKnown = FULL ? kH | kRout | kX | kXq | kW | kPre | (POST ? kScaled : kShifted) : 0;  // bits known here ...
+  constexpr int kSet = FULL ? kH | kRout | kX | kW | kPre | (POST ? kScaled : 0) : 0;                 // ... and those that are set
+  auto on = [&](int bit) { return (kKnown & bit) ? (kSet & bit) != 0 : (has & bit) != 0; };
+  const FwdSmem lay = fwd_smem<DT, RT>(8 * CK * W, on(kH), on(kW), on(kB), on(kScaled), on(kShifted), MODE, kHeld);
+  uint8_t *const w_s = own + lay.w, *const b_s = own + lay.b, *const gw_s = own + lay.gw, *const gb_s = own + lay.gb;
   const unsigned stride = gridDim.x * blockDim.y;
   unsigned next = blockIdx.x * blockDim.y + threadIdx.y;
-  auto fetch = [&](int v, unsigned row) {
-    if (row >= (unsigned)p.rows) return;
-    if (p.h) H.fetch(at, v, (int)row);
-    R.fetch(at, v, (int)row);
-  };
+  In<RT, CK, CW, MODE> R(p.r, p.ldr, norm_smem, stride);
+  In<DT, CK, CW, MODE> H(p.h, p.ldh, norm_smem + 8 * CK * W * kBytes<RT>, stride);
+  Out<RT, CK, CW, MODE> Ro(p.r_out, p.ldro, stride);
+  Out<DT, CK, CW, MODE> X(p.x, p.ldx, stride);
+  R.seek(at, next), H.seek(at, next), Ro.seek(at, next), X.seek(at, next);
+  if (next < (unsigned)p.rows) {
 #pragma unroll
-  for (int v = 0; v < NV; v++) fetch(v, next);
+    for (int v = 0; v < NV; v++)
+      if (at.mine(v)) {
+        if (on(kH)) H.fetch(at, v);
+        R.fetch(at, v);
+      }
+  }
+  if (MODE == kStaged) R.advance(), H.advance();  // (the row behind)
   asm volatile("cp.async.commit_group;" ::: "memory");
-  if constexpr (MODE == kStaged) {
-#pragma unroll
-    for (int v = 0; v < NV; v++) {
-      float f[8];
-      if (p.w.p) load_params<MODE>(p.w, 0, at, v, 1.0f, f), put8(w_s, threads, tid, v, f);
-      if (p.b.p) load_params<MODE>(p.b, 0, at, v, 0.0f, f), put8(b_s, threads, tid, v, f);
+  if constexpr (kHeld) {
+#pragma unroll 1
+    for (int v = 0; v < NV; v++) {  // (code that runs once: its fetch counts)
+      float f[CW];
+      if (on(kW)) load_params(p.w, 0, at, v, 1.0f, f), put_own(w_s, v, W, f);
+      if (on(kB)) load_params(p.b, 0, at, v, 0.0f, f), put_own(b_s, v, W, f);
     }
   }
+  keep(has);
   // the gate's row times the post norm's w and b
-  auto gate_params = [&](int v, int gate, float (&gw)[8], float (&gb)[8]) {
-    load_params<MODE>(p.g, (size_t)gate * p.ldg, at, v, 1.0f, gw);
-    if (shifted) {
-      load_params<MODE>(p.pb, 0, at, v, 0.0f, gb);
-#pragma unroll
-      for (int j = 0; j < 8; j++) gb[j] *= gw[j];
+  auto gate_params = [&](int v, int gate, float (&gw)[CW], float (&gb)[CW]) {
+    load_params(p.g, (size_t)gate * p.ldg, at, v, 1.0f, gw);
+    if (on(kShifted)) {
+      load_params(p.pb, 0, at, v, 0.0f, gb);
+      mul(gb, gb, gw);
     }
     if (post) {
-      float f[8];
-      load_params<MODE>(p.pw, 0, at, v, 1.0f, f);
-#pragma unroll
-      for (int j = 0; j < 8; j++) gw[j] *= f[j];
+      float f[CW];
+      load_params(p.pw, 0, at, v, 1.0f, f);
+      mul(gw, gw, f);
     }
   };
-  const float inv = 1.0f / (float)p.cols;
-  int gate = -1;
-  for (; next < (unsigned)p.rows; next += stride) {
+  float inv = 1.0f / (float)p.cols, alpha = p.alpha, eps = p.eps;
+  int inv_bits = __float_as_int(inv);
+  keep(inv_bits);
+  inv = __int_as_float(inv_bits);
+  unsigned rows = (unsigned)p.rows;
+  keep(rows);
+  unsigned now = 0, gate_end = 0;  // the row's gate row, and the first row behind its rows
+  for (; next < rows; next += stride) {
     const int row = (int)next;
-    const int now = p.g.p ? row / p.gate_rows : 0;
-    if (MODE == kStaged && (scaled || shifted) && now != gate) {  // (a thread's own part: nobody else waits for it)
-      gate = now;
-#pragma unroll
-      for (int v = 0; v < NV; v++) {
-        float gw[8], gb[8];
-        gate_params(v, now, gw, gb);
-        if (scaled) put8(gw_s, threads, tid, v, gw);
-        if (shifted) put8(gb_s, threads, tid, v, gb);
+    if ((on(kScaled) || on(kShifted)) && next >= gate_end) {
+      now = next / (unsigned)p.gate_rows;
+      gate_end = (now + 1) * (unsigned)p.gate_rows;
+      if (gate_end < now) gate_end = 0xffffffffu;
+      if constexpr (kHeld) {  // (a thread's own part: nobody else waits for it)
+#pragma unroll 1
+        for (int v = 0; v < NV; v++) {
+          float gw[CW], gb[CW];
+          gate_params(v, (int)now, gw, gb);
+          if (on(kScaled)) put_own(gw_s, v, W, gw);
+          if (on(kShifted)) put_own(gb_s, v, W, gb);
+        }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    float y[NV][8];
+    float y[NV][CW];
     float2 s1 = make_float2(0.0f, 1.0f), s2 = make_float2(0.0f, 1.0f);
     if (post) {
 #pragma unroll
       for (int v = 0; v < NV; v++) {
-        H.get(at, v, row, y[v]);
-        mask<MODE>(at, v, y[v]);
+        if (at.mine(v)) {
+          H.get(at, v, y[v]);
+          mask(at, v, y[v]);
+        } else {
+          zero(y[v]);
+        }
       }
-      s1 = row_stats<MODE, NV>(y, at, p.post, inv, p.eps, ex);
+      s1 = row_stats(y, at, p.post, inv, eps, ex);
     }
+    const bool more = next + stride < rows && next + stride > next;
 #pragma unroll
     for (int v = 0; v < NV; v++) {
-      float u[8], f[8];
-      if (post) {
-#pragma unroll
-        for (int j = 0; j < 8; j++) u[j] = (y[v][j] - s1.x) * s1.y;
-      } else if (p.h) {
-        H.get(at, v, row, u);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) u[j] = 0.0f;
+      if (!at.mine(v)) {
+        zero(y[v]);
+        continue;
       }
-      float gb[8];
-      if (MODE == kDirect) gate_params(v, now, f, gb);
-      if (scaled) {
-        if (MODE == kStaged) get8(gw_s, threads, tid, v, f);
-#pragma unroll
-        for (int j = 0; j < 8; j++) u[j] = __fmul_rn(u[j], f[j]);
+      float f[CW], gb[CW];
+      if (post) normed(y[v], y[v], s1.x, s1.y);
+      else if (on(kH)) H.get(at, v, y[v]);
+      else zero(y[v]);
+      if (!kHeld) gate_params(v, (int)now, f, gb);
+      if (on(kScaled)) {
+        if (kHeld) get_own(gw_s, v, W, f);
+        mul(y[v], y[v], f);
       }
-      if (shifted) {
-        if (MODE == kStaged) get8(gb_s, threads, tid, v, gb);
-#pragma unroll
-        for (int j = 0; j < 8; j++) u[j] += gb[j];
+      if (on(kShifted)) {
+        if (kHeld) get_own(gb_s, v, W, gb);
+        add(y[v], y[v], gb);
       }
-      R.get(at, v, row, f);
-      fetch(v, next + stride);  // (what the chunk had has been read)
-#pragma unroll
-      for (int j = 0; j < 8; j++) y[v][j] = as_stored<RT>(__fadd_rn(__fmul_rn(p.alpha, f[j]), u[j]));
-      mask<MODE>(at, v, y[v]);
-      if (p.r_out) put_row<RT, MODE>(p.r_out, p.ldro, at, v, row, y[v]);
+      R.get(at, v, f);
+      if (MODE == kStaged && more) {  // (what the chunk had has been read)
+        if (on(kH)) H.fetch(at, v);
+        R.fetch(at, v);
+      }
+      mul(f, f, alpha);
+      add(y[v], f, y[v]);
+      Ro.put(at, v, y[v], on(kRout));
+      mask(at, v, y[v]);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    if (p.pre != FP8_NORM_NONE) {
-      s2 = row_stats<MODE, NV>(y, at, p.pre, inv, p.eps, ex);
-      if (p.x || p.xq) {
+    R.advance(), H.advance(), Ro.advance();
+    if (on(kPre)) {
+      s2 = row_stats(y, at, p.pre, inv, eps, ex);
+      if (on(kX) || on(kXq)) {
 #pragma unroll
         for (int v = 0; v < NV; v++) {
-          float f[8];
+          if (at.mine(v)) {
+            float f[CW];
+            normed(y[v], y[v], s2.x, s2.y);
+            if (on(kW)) {
+              if (kHeld) get_own(w_s, v, W, f);
+              else load_params(p.w, 0, at, v, 1.0f, f);
+              mul(y[v], y[v], f);
+            }
+            if (on(kB)) {
+              if (kHeld) get_own(b_s, v, W, f);
+              else load_params(p.b, 0, at, v, 0.0f, f);
+              add(y[v], y[v], f);
+            }
+            if (on(kX)) {
+              float f2[CW];
 #pragma unroll
-          for (int j = 0; j < 8; j++) y[v][j] = (y[v][j] - s2.x) * s2.y;
-          if (p.w.p) {
-            if (MODE == kStaged) get8(w_s, threads, tid, v, f);
-            else load_params<MODE>(p.w, 0, at, v, 1.0f, f);
-#pragma unroll
-            for (int j = 0; j < 8; j++) y[v][j] = __fmul_rn(y[v][j], f[j]);
+              for (int j = 0; j < CW; j++) f2[j] = y[v][j];
+              X.put(at, v, f2);
+            }
           }
-          if (p.b.p) {
-            if (MODE == kStaged) get8(b_s, threads, tid, v, f);
-            else load_params<MODE>(p.b, 0, at, v, 0.0f, f);
-#pragma unroll
-            for (int j = 0; j < 8; j++) y[v][j] = __fadd_rn(y[v][j], f[j]);
-          }
-          if (p.x) put_row<DT, MODE>(p.x, p.ldx, at, v, row, y[v]);
-          if (p.xq) {
-            mask<MODE>(at, v, y[v]);
-            put_codes<MODE>(p, at, v, row, y[v]);
+          if (on(kXq)) {
+            mask(at, v, y[v]);
+            put_codes(p, at, v, row, y[v]);
           }
         }
       }
     }
+    X.advance();
     if (p.stats && threadIdx.x == 0) reinterpret_cast<float4 *>(p.stats)[row] = make_float4(s1.x, s1.y, s2.x, s2.y);
   }
 }
@@ -601,11 +785,11 @@ __global__ void __launch_bounds__(512, 2) k_norm_cols(const Cols p) {
   const int tiles_c = (p.cols + block::kTile - 1) / block::kTile;
   const auto [row0, col0] = block::tile_at(blockIdx.x, tiles_c);
   const int col = col0 + (threadIdx.x & 15) * 8;
-  Raw8<RT> raw[RP];
+  block::Raw8<RT> raw[RP];
   block::load_tile<RT>(p.r, p.ldr, p.vec, row0, col0, p.rows, p.cols, raw);
   float w[8], b[8], f[RP][8];
-  load_param8(p.w, 0, col, p.cols, 1.0f, w);
-  load_param8(p.b, 0, col, p.cols, 0.0f, b);
+  load_eight(p.w, col, p.cols, 1.0f, w);
+  load_eight(p.b, col, p.cols, 0.0f, b);
 #pragma unroll
   for (int i = 0; i < RP; i++) {
     const int row = row0 + (threadIdx.x >> 4) + i * G::kStep;
@@ -651,7 +835,7 @@ inline Plan plan_of(int rows, int cols, int gate_rows) {
   Plan p = {};
   const int vecs = (cols + 7) / 8;
   p.chunks = vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : 4;
-  p.threads = (vecs + 32 * p.chunks - 1) / (32 * p.chunks) * 32;
+  p.threads = p.chunks == 2 ? kThreads : (vecs + 32 * p.chunks - 1) / (32 * p.chunks) * 32;
   p.groups = p.threads < kThreads ? kThreads / p.threads : 1;
   p.gate_rows = gate_rows < rows ? gate_rows : rows;
   const int most = p.threads > kThreads ? kSms : 2 * kSms;
@@ -683,12 +867,12 @@ struct BwdSmem {
   int w, gw, comb, bytes;
 };
 template <int DT, int RT>
-__host__ __device__ inline BwdSmem bwd_smem(int chunks, bool h, bool dro, bool pre, bool scaled, bool groups, int mode) {
+__host__ __device__ inline BwdSmem bwd_smem(int columns, bool h, bool dro, bool pre, bool scaled, bool groups, int mode, bool held) {
   BwdSmem s;
-  int at = mode == kStaged ? chunks * 16 * ((h ? kPieces<DT> : 0) + (dro ? kPieces<RT> : 0) + (pre ? kPieces<DT> + kPieces<RT> : 0)) : 0;
+  int at = mode == kStaged ? columns * ((h ? kBytes<DT> : 0) + (dro ? kBytes<RT> : 0) + (pre ? kBytes<DT> + kBytes<RT> : 0)) : 0;
   auto take = [&](bool on) {
-    const int o = on && mode == kStaged ? at : -1;
-    at += o >= 0 ? chunks * 32 : 0;
+    const int o = on && held ? at : -1;
+    at += o >= 0 ? columns * 4 : 0;
     return o;
   };
   s.w = take(pre), s.gw = take(scaled);
@@ -699,82 +883,98 @@ __host__ __device__ inline BwdSmem bwd_smem(int chunks, bool h, bool dro, bool p
 }
 
 // Adds up the groups of a CTA and writes one partial sum.
-template <int MODE, int NV>
-__device__ __forceinline__ void flush(float (&a)[8], float *comb, float *out, const Place &at, int v, int threads, int tid) {
-  if (NV == 1 && blockDim.y > 1) {  // (rows of several chunks have a CTA to themselves)
+template <int CK, int CW, int MODE>
+__device__ __forceinline__ void flush(float (&a)[CW], uint8_t *comb, float *out, const Place<CK, CW, MODE> &at, int v) {
+  if (CK == 1 && blockDim.y > 1) {  // (rows of several chunks have a CTA to themselves)
+    uint8_t *own = comb + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
     __syncthreads();
-    put8(comb, threads, tid, 0, a);
+    put_own(own, 0, kThreads, a);
     __syncthreads();
     if (threadIdx.y == 0) {
       for (int y = 1; y < (int)blockDim.y; y++) {
-        float f[8];
-        get8(comb, threads, y * blockDim.x + threadIdx.x, 0, f);
-#pragma unroll
-        for (int j = 0; j < 8; j++) a[j] += f[j];
+        float f[CW];
+        get_own(own + y * blockDim.x * 16, 0, kThreads, f);
+        add(a, a, f);
       }
     }
   }
   if (threadIdx.y == 0) {
     if constexpr (MODE == kStaged) {
-      if (at.has<MODE>(v, 0)) {
-        float4 *o = reinterpret_cast<float4 *>(out + at.col<MODE>(v, 0));
-        o[0] = make_float4(a[0], a[1], a[2], a[3]);
-        o[1] = make_float4(a[4], a[5], a[6], a[7]);
+      if (at.has(v, 0)) {
+        float4 *o = reinterpret_cast<float4 *>(out + at.col(v, 0));
+#pragma unroll
+        for (int h = 0; h < CW / 4; h++) o[h] = make_float4(a[4 * h], a[4 * h + 1], a[4 * h + 2], a[4 * h + 3]);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; j++)
-        if (at.has<MODE>(v, j)) out[at.col<MODE>(v, j)] = a[j];
+      for (int j = 0; j < CW; j++)
+        if (at.has(v, j)) out[at.col(v, j)] = a[j];
     }
   }
 #pragma unroll
-  for (int j = 0; j < 8; j++) a[j] = 0.0f;
+  for (int j = 0; j < CW; j++) a[j] = 0.0f;
 }
 
-// POST: whether there is a post norm; BIAS: whether sums of dx and of G are
-// wanted (gradients of b, of post_b, and of a gate behind post_b).  kDirect goes
-// by p.post, and takes the sums.
-template <int DT, int RT, bool POST, bool BIAS, int NV, int MODE>
-__global__ void __launch_bounds__(kCtaThreads<NV, MODE>, NV == 4 ? 1 : 2) k_norm_bwd(const Bwd p) {
+// BIAS: whether sums of dx and of G are wanted (gradients of b, of post_b, and
+// of a gate behind post_b).  FULL: dx, dr', h, both outputs and the post norm's
+// w, the common call; POST: whether there is a post norm.  Else asked for at run
+// time.
+template <int DT, int RT, bool FULL, bool POST, bool BIAS, int CK, int MODE>
+__global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK == 4 ? 1 : 2) k_norm_bwd(const Bwd p) {
+  constexpr int CW = kWidth<RT>, NV = CK * 8 / CW;
+  constexpr bool kHeld = held(CK, MODE);
   pdl_launch_dependents();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t norm_smem[];
   __shared__ __align__(16) float slots[2][8][kMostWarps];
   Exchange ex = exchange(slots);
-  const int threads = blockDim.x * blockDim.y, tid = threadIdx.y * blockDim.x + threadIdx.x;
-  const Place at = {p.cols, (int)threadIdx.x, (int)blockDim.x};
-  const bool post = MODE == kStaged ? POST : p.post != FP8_NORM_NONE;
-  const bool pre = p.pre != FP8_NORM_NONE, scaled = p.h && (p.g.p || (post && p.pw.p));
-  const BwdSmem lay = bwd_smem<DT, RT>(NV * threads, p.h, p.dro, pre, scaled, blockDim.y > 1, MODE);
-  float *const w_s = reinterpret_cast<float *>(norm_smem + lay.w), *const gw_s = reinterpret_cast<float *>(norm_smem + lay.gw);
-  float *const comb = reinterpret_cast<float *>(norm_smem + lay.comb);
-  uint8_t *slot = norm_smem;
-  auto take = [&](bool on, int pieces) {
-    uint8_t *s = slot;
-    slot += on ? NV * threads * 16 * pieces : 0;
+  const Place<CK, CW, MODE> at = {p.cols, (int)threadIdx.x};
+  const int W = at.lanes();
+  const bool post = FULL ? POST : p.post != FP8_NORM_NONE;
+  enum { kH = 1, kDro = 2, kDr = 4, kDh = 8, kAc = 16, kScaled = 32, kPre = 64, kLayer = 128, kPreLayer = 256, kPostLayer = 512,
+         kStats = 1024 };
+  int has = (p.h ? kH : 0) | (p.dro ? kDro : 0) | (p.dr ? kDr : 0) | (p.dh ? kDh : 0) | (p.ac ? kAc : 0) |
+            (p.h && (p.g.p || (post && p.pw.p)) ? kScaled : 0) | (p.pre != FP8_NORM_NONE ? kPre : 0) |
+            (p.pre == FP8_NORM_LAYER ? kPreLayer | kLayer : 0) | (p.post == FP8_NORM_LAYER ? kPostLayer | kLayer : 0) |
+            (p.stats ? kStats : 0);
+  constexpr int kKnown = FULL ? kH | kDro | kDr | kDh | kPre | kStats | (POST ? kScaled : kPostLayer) : 0;  // bits known here ...
+  constexpr int kSet = FULL ? kH | kDro | kDr | kDh | kPre | kStats | (POST ? kScaled : 0) : 0;             // ... and set
+  auto on = [&](int bit) { return (kKnown & bit) ? (kSet & bit) != 0 : (has & bit) != 0; };
+  const BwdSmem lay = bwd_smem<DT, RT>(8 * CK * W, on(kH), on(kDro), on(kPre), on(kScaled), blockDim.y > 1, MODE, kHeld);
+  uint8_t *const own = norm_smem + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+  uint8_t *const w_s = own + lay.w, *const gw_s = own + lay.gw, *const comb = norm_smem + lay.comb;
+  uint8_t *part = norm_smem;
+  auto take = [&](bool on, int bytes) {
+    uint8_t *s = part;
+    part += on ? 8 * CK * W * bytes : 0;
     return s;
   };
-  constexpr size_t de = DT == FP8_DT_F32 ? 4 : 2, re = RT == FP8_DT_F32 ? 4 : 2;
-  const Rows<DT, MODE> DX = {static_cast<const uint8_t *>(p.dx), p.lddx * de, take(pre, kPieces<DT>), threads, tid};
-  const Rows<RT, MODE> RO = {static_cast<const uint8_t *>(p.ro), p.ldro * re, take(pre, kPieces<RT>), threads, tid};
-  const Rows<RT, MODE> DRO = {static_cast<const uint8_t *>(p.dro), p.lddro * re, take(p.dro, kPieces<RT>), threads, tid};
-  const Rows<DT, MODE> H = {static_cast<const uint8_t *>(p.h), p.ldh * de, take(p.h, kPieces<DT>), threads, tid};
-  auto fetch = [&](int v, int row) {
-    if (pre) {
-      DX.fetch(at, v, row);
-      RO.fetch(at, v, row);
+  const unsigned apart = blockDim.y;
+  In<DT, CK, CW, MODE> DX(p.dx, p.lddx, take(on(kPre), kBytes<DT>), apart);
+  In<RT, CK, CW, MODE> RO(p.ro, p.ldro, take(on(kPre), kBytes<RT>), apart);
+  In<RT, CK, CW, MODE> DRO(p.dro, p.lddro, take(on(kDro), kBytes<RT>), apart);
+  In<DT, CK, CW, MODE> H(p.h, p.ldh, take(on(kH), kBytes<DT>), apart);
+  Out<RT, CK, CW, MODE> DR(p.dr, p.lddr, apart);
+  Out<DT, CK, CW, MODE> DH(p.dh, p.lddh, apart);
+  keep(has);
+  auto fetch = [&](int v) {
+    if (!at.mine(v)) return;
+    if (on(kPre)) {
+      DX.fetch(at, v);
+      RO.fetch(at, v);
     }
-    if (p.dro) DRO.fetch(at, v, row);
-    if (p.h) H.fetch(at, v, row);
+    if (on(kDro)) DRO.fetch(at, v);
+    if (on(kH)) H.fetch(at, v);
   };
-  const float inv = 1.0f / (float)p.cols;
+  auto advance_in = [&] { DX.advance(), RO.advance(), DRO.advance(), H.advance(); };
+  const float inv = 1.0f / (float)p.cols, alpha = p.alpha;
   const size_t ld_sum = (size_t)(p.cols + 7) / 8 * 8;
   const long long u0 = p.units * blockIdx.x / gridDim.x, u1 = p.units * (blockIdx.x + 1) / gridDim.x;
-  float E[NV][8], F[NV][8], A[NV][8], C[NV][8];
+  float E[NV][CW], F[NV][CW], A[NV][CW], C[NV][CW];
 #pragma unroll
   for (int v = 0; v < NV; v++)
 #pragma unroll
-    for (int j = 0; j < 8; j++) E[v][j] = F[v][j] = A[v][j] = C[v][j] = 0.0f;
+    for (int j = 0; j < CW; j++) E[v][j] = F[v][j] = A[v][j] = C[v][j] = 0.0f;
   // the rows of unit u
   struct Span {
     long long first, last;
@@ -786,209 +986,203 @@ __global__ void __launch_bounds__(kCtaThreads<NV, MODE>, NV == 4 ? 1 : 2) k_norm
     return {r0, min(r0 + p.unit_rows, end)};
   };
   float4 s_next = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+  // the first row of unit u for this group: its loads, and the pointers behind it
   auto fetch_first = [&](long long u) {
     if (u >= u1) return;
     const Span s = rows_of(u);
     const long long row = s.first + threadIdx.y;
-    if (row >= s.last) return;
+    DX.seek(at, row), RO.seek(at, row), DRO.seek(at, row), H.seek(at, row);
+    if (row < s.last) {
 #pragma unroll
-    for (int v = 0; v < NV; v++) fetch(v, (int)row);
-    if (p.stats) s_next = __ldg(reinterpret_cast<const float4 *>(p.stats) + row);
+      for (int v = 0; v < NV; v++) fetch(v);
+      if (on(kStats)) s_next = __ldg(reinterpret_cast<const float4 *>(p.stats) + row);
+    }
+    if (MODE == kStaged) advance_in();
   };
   fetch_first(u0);
   asm volatile("cp.async.commit_group;" ::: "memory");
-  if (MODE == kStaged && pre) {
-#pragma unroll
+  if (kHeld && on(kPre)) {
+#pragma unroll 1
     for (int v = 0; v < NV; v++) {
-      float f[8];
-      load_params<MODE>(p.w, 0, at, v, 1.0f, f);
-      put8(w_s, threads, tid, v, f);
+      float f[CW];
+      load_params(p.w, 0, at, v, 1.0f, f);
+      put_own(w_s, v, W, f);
     }
   }
-  auto weight = [&](int v, float (&f)[8]) {
-    if (MODE == kStaged) get8(w_s, threads, tid, v, f);
-    else load_params<MODE>(p.w, 0, at, v, 1.0f, f);
+  auto weight = [&](int v, float (&f)[CW]) {
+    if (kHeld) get_own(w_s, v, W, f);
+    else load_params(p.w, 0, at, v, 1.0f, f);
   };
   // the gate's row times the post norm's w
-  auto gate_params = [&](int v, int gate, float (&g)[8]) {
-    load_params<MODE>(p.g, (size_t)gate * p.ldg, at, v, 1.0f, g);
+  auto gate_params = [&](int v, int gate, float (&g)[CW]) {
+    load_params(p.g, (size_t)gate * p.ldg, at, v, 1.0f, g);
     if (post) {
-      float f[8];
-      load_params<MODE>(p.pw, 0, at, v, 1.0f, f);
+      float f[CW];
+      load_params(p.pw, 0, at, v, 1.0f, f);
 #pragma unroll
-      for (int j = 0; j < 8; j++) g[j] *= f[j];
+      for (int j = 0; j < CW; j++) g[j] *= f[j];
     }
   };
   int gate_now = -1;
   for (long long u = u0; u < u1; u++) {
     const int gate = (int)(u / p.per_gate);
     const Span span = rows_of(u);
-    if (MODE == kStaged && scaled && gate != gate_now) {
+    if (kHeld && (on(kScaled)) && gate != gate_now) {
       gate_now = gate;
-#pragma unroll
+#pragma unroll 1
       for (int v = 0; v < NV; v++) {
-        float g[8];
+        float g[CW];
         gate_params(v, gate, g);
-        put8(gw_s, threads, tid, v, g);
+        put_own(gw_s, v, W, g);
       }
     }
-    auto gate_weight = [&](int v, float (&f)[8]) {
-      if (MODE == kStaged) get8(gw_s, threads, tid, v, f);
+    auto gate_weight = [&](int v, float (&f)[CW]) {
+      if (kHeld) get_own(gw_s, v, W, f);
       else gate_params(v, gate, f);
     };
-    for (long long r = span.first + threadIdx.y; r < span.last; r += blockDim.y) {
-      const int row = (int)r;
+    const long long row0 = span.first + threadIdx.y;
+    DR.seek(at, row0), DH.seek(at, row0);
+    for (int row = (int)row0, left = (int)(span.last - row0); left > 0; row += apart, left -= apart) {
       const float4 s = s_next;
-      const bool more = r + blockDim.y < span.last;
-      if (more && p.stats) s_next = __ldg(reinterpret_cast<const float4 *>(p.stats) + row + blockDim.y);
+      const bool more = left > (int)apart;
+      if (more && (on(kStats))) s_next = __ldg(reinterpret_cast<const float4 *>(p.stats) + row + apart);
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       float m0 = 0.0f, m1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+      const bool pre = on(kPre), layer = on(kLayer);
       if (pre || post) {
-        float k[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll(NV == 4 ? 1 : NV)
+        float2 k[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) k[i] = both(0.0f);
+#pragma unroll(CK == 4 ? 1 : NV)
         for (int v = 0; v < NV; v++) {
-          float t[8], n2[8];
+          if (!at.mine(v)) continue;
+          float t[CW], n2[CW];
           if (pre) {
-            float w[8];
-            DX.get(at, v, row, t);
-            RO.get(at, v, row, n2);
+            float w[CW];
+            DX.get(at, v, t);
+            RO.get(at, v, n2);
             weight(v, w);
-            mask<MODE>(at, v, t);
-            mask<MODE>(at, v, n2);
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-              n2[j] = (n2[j] - s.z) * s.w;
-              t[j] *= w[j];
-              k[0] = fmaf(t[j], n2[j], k[0]);
-              k[1] += t[j];
-            }
+            mask(at, v, t);
+            normed(n2, n2, s.z, s.w);
+            mul(t, t, w);
+            dot(k[0], t, n2);
+            if (layer) plus(k[1], t);
           } else {
-#pragma unroll
-            for (int j = 0; j < 8; j++) t[j] = n2[j] = 0.0f;
+            zero(t);
+            zero(n2);
           }
           if (post) {
-            float q[8], n1[8], h[8];
-            if (p.dro) {
-              DRO.get(at, v, row, h);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; j++) h[j] = 0.0f;
-            }
-            H.get(at, v, row, n1);
-            if (scaled) {
+            float q[CW], n1[CW], h[CW];
+            if (on(kDro)) DRO.get(at, v, h);
+            else zero(h);
+            H.get(at, v, n1);
+            fma8(h, t, s.w, h);
+            normed(n1, n1, s.x, s.y);
+            if (on(kScaled)) {
               gate_weight(v, q);
             } else {
 #pragma unroll
-              for (int j = 0; j < 8; j++) q[j] = 1.0f;
+              for (int j = 0; j < CW; j++) q[j] = 1.0f;
             }
-            mask<MODE>(at, v, q);
-            mask<MODE>(at, v, h);
-            mask<MODE>(at, v, n1);
+            mask(at, v, q);
+            mul(h, q, h);    // gw H
+            dot(k[2], h, n1);
+            if (layer) {
+              plus(k[4], h);
+              plus(k[7], q);
+              dot(k[5], q, n2);
+            }
+            mul(q, q, n1);  // gw n1
+            dot(k[3], q, n2);
+            if (layer) plus(k[6], q);
+          }
+        }
+        float c[8];
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-              n1[j] = (n1[j] - s.x) * s.y;
-              const float qh = q[j] * fmaf(s.w, t[j], h[j]), qn = q[j] * n1[j];
-              k[2] = fmaf(qh, n1[j], k[2]);
-              k[3] = fmaf(qn, n2[j], k[3]);
-              k[4] += qh;
-              k[5] = fmaf(q[j], n2[j], k[5]);
-              k[6] += qn;
-              k[7] += q[j];
-            }
-          }
-        }
-        if (post) {
-          if (p.pre == FP8_NORM_LAYER || p.post == FP8_NORM_LAYER) {
-            row_sums(k, ex);
-          } else {
-            float few[4] = {k[0], k[1], k[2], k[3]};
-            row_sums(few, ex);
-            k[0] = few[0], k[2] = few[2], k[3] = few[3];
-          }
-        } else {
-          float few[2] = {k[0], k[1]};
+        for (int i = 0; i < 8; i++) c[i] = k[i].x + k[i].y;
+        if (post && layer) {
+          row_sums(c, ex);
+        } else if (post) {
+          float few[4] = {c[0], c[2], c[3], 0.0f};
           row_sums(few, ex);
-          k[0] = few[0], k[1] = few[1];
+          c[0] = few[0], c[2] = few[1], c[3] = few[2];
+        } else if (layer) {
+          float few[2] = {c[0], c[1]};
+          row_sums(few, ex);
+          c[0] = few[0], c[1] = few[1];
+        } else {
+          float one[1] = {c[0]};
+          row_sums(one, ex);
+          c[0] = one[0];
         }
-        m1 = k[0] * inv;
-        if (p.pre == FP8_NORM_LAYER) m0 = k[1] * inv;
+        m1 = c[0] * inv;
+        if (on(kPreLayer)) m0 = c[1] * inv;
         if (post) {
-          t1 = (k[2] - s.w * fmaf(m0, k[6], m1 * k[3])) * inv;
-          if (p.post == FP8_NORM_LAYER) t0 = (k[4] - s.w * fmaf(m0, k[7], m1 * k[5])) * inv;
+          t1 = (c[2] - s.w * fmaf(m0, c[6], m1 * c[3])) * inv;
+          if (on(kPostLayer)) t0 = (c[4] - s.w * fmaf(m0, c[7], m1 * c[5])) * inv;
         }
       }
 #pragma unroll
       for (int v = 0; v < NV; v++) {
-        float G[8], t[8], n[8];
-        if (p.dro) {
-          DRO.get(at, v, row, G);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; j++) G[j] = 0.0f;
-        }
+        if (!at.mine(v)) continue;
+        float G[CW], t[CW], n[CW];
+        if (on(kDro)) DRO.get(at, v, G);
+        else zero(G);
         if (pre) {
-          float w[8];
-          DX.get(at, v, row, t);
-          RO.get(at, v, row, n);
+          float w[CW];
+          DX.get(at, v, t);
+          RO.get(at, v, n);
           weight(v, w);
-#pragma unroll
-          for (int j = 0; j < 8; j++) {
-            n[j] = (n[j] - s.z) * s.w;
-            E[v][j] = fmaf(t[j], n[j], E[v][j]);
-            if (BIAS) F[v][j] += t[j];
-            G[j] = fmaf(s.w, fmaf(t[j], w[j], -m0) - n[j] * m1, G[j]);
+          normed(n, n, s.z, s.w);
+          fma8(E[v], t, n, E[v]);
+          if (BIAS) add(F[v], F[v], t);
+          fma8(t, t, w, -m0);
+          fma8(t, n, -m1, t);
+          fma8(G, t, s.w, G);
+        }
+        if (on(kH)) H.get(at, v, n);
+        if (MODE == kStaged && more) fetch(v);  // (what the chunk had has been read)
+        if (on(kDr)) {
+          mul(t, G, alpha);
+          DR.put(at, v, t);
+        }
+        if (on(kH)) {
+          if (post) normed(n, n, s.x, s.y);
+          if (on(kAc)) {
+            fma8(A[v], G, n, A[v]);
+            if (BIAS) add(C[v], C[v], G);
           }
-        }
-        if (p.h) H.get(at, v, row, n);
-        if (MODE == kStaged && more) fetch(v, row + (int)blockDim.y);  // (what the chunk had has been read)
-        if (p.dr) {
-#pragma unroll
-          for (int j = 0; j < 8; j++) t[j] = p.alpha * G[j];
-          put_row<RT, MODE>(p.dr, p.lddr, at, v, row, t);
-        }
-        if (p.h) {
-          if (scaled) {
+          if (on(kScaled)) {
             gate_weight(v, t);
-#pragma unroll
-            for (int j = 0; j < 8; j++) t[j] *= G[j];
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; j++) t[j] = G[j];
+            mul(G, G, t);
           }
           if (post) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-              n[j] = (n[j] - s.x) * s.y;
-              t[j] = s.y * (t[j] - t0 - n[j] * t1);
-            }
+            add(G, G, -t0);
+            fma8(G, n, -t1, G);
+            mul(G, G, s.y);
           }
-          if (p.dh) put_row<DT, MODE>(p.dh, p.lddh, at, v, row, t);
-          if (p.ac) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-              A[v][j] = fmaf(G[j], n[j], A[v][j]);
-              if (BIAS) C[v][j] += G[j];
-            }
-          }
+          if (on(kDh)) DH.put(at, v, G);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
+      advance_in();
+      DR.advance(), DH.advance();
     }
     fetch_first(u + 1);
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (p.ac) {
 #pragma unroll
       for (int v = 0; v < NV; v++) {
-        flush<MODE, NV>(A[v], comb, p.ac + (size_t)(2 * u) * ld_sum, at, v, threads, tid);
-        if (BIAS) flush<MODE, NV>(C[v], comb, p.ac + (size_t)(2 * u + 1) * ld_sum, at, v, threads, tid);
+        flush(A[v], comb, p.ac + (size_t)(2 * u) * ld_sum, at, v);
+        if (BIAS) flush(C[v], comb, p.ac + (size_t)(2 * u + 1) * ld_sum, at, v);
       }
     }
   }
   if (p.ef) {
 #pragma unroll
     for (int v = 0; v < NV; v++) {
-      flush<MODE, NV>(E[v], comb, p.ef + (size_t)(2 * blockIdx.x) * ld_sum, at, v, threads, tid);
-      if (BIAS) flush<MODE, NV>(F[v], comb, p.ef + (size_t)(2 * blockIdx.x + 1) * ld_sum, at, v, threads, tid);
+      flush(E[v], comb, p.ef + (size_t)(2 * blockIdx.x) * ld_sum, at, v);
+      if (BIAS) flush(F[v], comb, p.ef + (size_t)(2 * blockIdx.x + 1) * ld_sum, at, v);
     }
   }
 }

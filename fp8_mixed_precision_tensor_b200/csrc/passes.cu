@@ -210,27 +210,31 @@ int fp8_norm_fwd(const fp8_norm_params *p, const void *h, size_t ldh, const void
   const bool post = p->post != FP8_NORM_NONE;
   with_norm_types(p->dtype, p->res_dtype, [&](auto dt, auto rt) {
     constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-    with_chunks(plan.chunks, [&](auto nv) {
-      constexpr int NV = decltype(nv)::value;
+    with_chunks(plan.chunks, [&](auto ck) {
+      constexpr int CK = decltype(ck)::value;
       const int threads = plan.threads * plan.groups;
       auto launch = [&](auto kernel, int mode) {
-        const int smem = norm::fwd_smem<DT, RT>(NV * threads, h, a.w.p, a.b.p, a.g.p || (post && a.pw.p), post && a.pb.p,
-                                                mode).bytes;
+        const int columns = 8 * CK * (CK == 4 ? plan.threads : norm::kThreads);
+        const int smem = norm::fwd_smem<DT, RT>(columns, h, a.w.p, a.b.p, a.g.p || (post && a.pw.p), post && a.pb.p,
+                                                mode, norm::held(CK, mode)).bytes;
         if (smem > kMostSmem) return FP8_ERR_UNSUPPORTED;
         if (int e = set_smem(kernel, smem)) return e;
-        // as many CTAs as stay resident (64 registers a thread, 128 with four chunks) share the rows out
-        const int by_regs = 65536 / (threads * (NV == 4 ? 128 : 64)), by_smem = 232448 / (smem + 2048);
-        const unsigned most = (unsigned)(sms * (by_regs < by_smem ? by_regs : by_smem));
+        // as many CTAs as stay resident (80 registers a thread, 168 with four chunks) share the rows out
+        const int by_regs = 65536 / (threads * (CK == 4 ? 168 : 80)), by_smem = 232448 / (smem + 2048);
+        const int resident = by_regs < by_smem ? by_regs : by_smem;
+        const unsigned most = (unsigned)(sms * (resident > 1 ? resident : 1));
         const unsigned need = ((unsigned)rows + (unsigned)plan.groups - 1) / (unsigned)plan.groups;
         return launch_pdl(kernel, need < most ? need : most, dim3(plan.threads, plan.groups), smem, s, 1, a);
       };
       rc = FP8_ERR_UNSUPPORTED;
       if (whole && cols <= norm::kStagedCols) {
-        if (post) rc = launch(norm::k_norm_fwd<DT, RT, true, NV, norm::kStaged>, norm::kStaged);
-        else rc = launch(norm::k_norm_fwd<DT, RT, false, NV, norm::kStaged>, norm::kStaged);
+        const bool full = h && r_out && x && !x_row && a.w.p && (!post || a.pw.p);
+        if (full && post) rc = launch(norm::k_norm_fwd<DT, RT, true, true, CK, norm::kStaged>, norm::kStaged);
+        else if (full) rc = launch(norm::k_norm_fwd<DT, RT, true, false, CK, norm::kStaged>, norm::kStaged);
+        else rc = launch(norm::k_norm_fwd<DT, RT, false, false, CK, norm::kStaged>, norm::kStaged);
       }
       if (rc == FP8_ERR_UNSUPPORTED)
-        rc = launch(norm::k_norm_fwd<DT, RT, true, NV == 1 ? 1 : 4, norm::kDirect>, norm::kDirect);
+        rc = launch(norm::k_norm_fwd<DT, RT, false, false, CK == 1 ? 1 : 4, norm::kDirect>, norm::kDirect);
     });
     if (rc || !x_col) return;
     norm::Cols c = {};
@@ -300,26 +304,30 @@ int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const vo
     a.gate_rows = plan.gate_rows, a.unit_rows = plan.unit_rows, a.per_gate = plan.per_gate, a.units = plan.units;
     with_norm_types(p->dtype, p->res_dtype, [&](auto dt, auto rt) {
       constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-      with_chunks(plan.chunks, [&](auto nv) {
-        constexpr int NV = decltype(nv)::value;
-        const int threads = plan.threads * plan.groups;
+      with_chunks(plan.chunks, [&](auto ck) {
+        constexpr int CK = decltype(ck)::value;
         auto launch = [&](auto kernel, int mode) {
-          const int smem = norm::bwd_smem<DT, RT>(NV * threads, h, dr_out, pre, h && (a.g.p || (post && a.pw.p)),
-                                                  plan.groups > 1, mode).bytes;
+          const int columns = 8 * CK * (CK == 4 ? plan.threads : norm::kThreads);
+          const int smem = norm::bwd_smem<DT, RT>(columns, h, dr_out, pre, h && (a.g.p || (post && a.pw.p)),
+                                                  plan.groups > 1, mode, norm::held(CK, mode)).bytes;
           if (smem > kMostSmem) return FP8_ERR_UNSUPPORTED;
           if (int e = set_smem(kernel, smem)) return e;
           return launch_pdl(kernel, (unsigned)plan.ctas, dim3(plan.threads, plan.groups), smem, s, 1, a);
         };
         rc = FP8_ERR_UNSUPPORTED;
-        if (whole && cols <= norm::kStagedCols)
-          with_bool(post, [&](auto has_post) {
-            with_bool(bias || NV == 4, [&](auto has_bias) {
-              constexpr bool kBias = decltype(has_bias)::value || NV == 4;
-              rc = launch(norm::k_norm_bwd<DT, RT, decltype(has_post)::value, kBias, NV, norm::kStaged>, norm::kStaged);
+        if (whole && cols <= norm::kStagedCols) {
+          if (pre && dr_out && h && dh && dr && (!post || a.pw.p))
+            with_bool(post, [&](auto has_post) {
+              with_bool(bias || CK == 4, [&](auto has_bias) {
+                constexpr bool kBias = decltype(has_bias)::value || CK == 4;
+                rc = launch(norm::k_norm_bwd<DT, RT, true, decltype(has_post)::value, kBias, CK, norm::kStaged>, norm::kStaged);
+              });
             });
-          });
+          else
+            rc = launch(norm::k_norm_bwd<DT, RT, false, false, true, CK, norm::kStaged>, norm::kStaged);
+        }
         if (rc == FP8_ERR_UNSUPPORTED)
-          rc = launch(norm::k_norm_bwd<DT, RT, true, true, NV == 1 ? 1 : 4, norm::kDirect>, norm::kDirect);
+          rc = launch(norm::k_norm_bwd<DT, RT, false, false, true, CK == 1 ? 1 : 4, norm::kDirect>, norm::kDirect);
       });
     });
     if (rc) return rc;

@@ -92,8 +92,9 @@ def test_norm_workspace_is_that_of_the_partial_sums(fp8):
         for cols in (1, 64, 4096, 4097, 12288, 16384):
             for gate_rows in (1, 3, rows, 10 * rows):
                 n = need(rows, cols, gate_rows)
-                sums = n // (2 * cols * 4)
-                assert n == sums * 2 * cols * 4 and 2 <= sums <= 3 * 2 * 148 + -(-rows // gate_rows) + 1
+                line = 2 * (-(-cols // 8) * 8) * 4  # whole groups of eight
+                sums = n // line
+                assert n == sums * line and 2 <= sums <= 3 * 2 * 148 + -(-rows // gate_rows) + 1
 
 
 def test_losses_reject_bad_arguments(fp8):
