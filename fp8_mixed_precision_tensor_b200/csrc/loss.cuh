@@ -149,18 +149,6 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
   for (int b = 16; b > 0; b /= 2) v += __shfl_xor_sync(0xffffffffu, v, b);
   return __shfl_sync(0xffffffffu, v, 0);
 }
-__device__ __forceinline__ float block_max(float v, float *red) {
-#pragma unroll
-  for (int b = 16; b > 0; b /= 2) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, b));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = (threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : kNone;
-#pragma unroll
-  for (int b = 16; b > 0; b /= 2) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, b));
-  return __shfl_sync(0xffffffffu, v, 0);
-}
-
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -192,24 +180,64 @@ __device__ __forceinline__ Range range_of(const uint8_t *row, int cols, unsigned
   return r;
 }
 
-// Calls f(column, logit) for every element of the range that this thread owns.
-template <int DT, typename F>
-__device__ __forceinline__ void each_own(const Range &r, F f) {
-  const int t = threadIdx.x;
-  if (t < r.head) f(t, load_one<DT>(r.row, t));
-  for (int v = r.v0 + t; v < r.v1; v += blockDim.x) {
-    float x[kElems<DT>];
-    unpack<DT>(__ldg(reinterpret_cast<const uint4 *>(r.body) + v), x);
-#pragma unroll
-    for (int j = 0; j < kElems<DT>; j++) f(r.s.head + v * kElems<DT> + j, x[j]);
+// The larger of a vector's elements; a NaN anywhere stays one.
+template <int DT>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (DT == FP8_DT_F32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else if constexpr (DT == FP8_DT_BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ float widest(uint32_t w) {
+  if constexpr (DT == FP8_DT_F32) return __uint_as_float(w);
+  else if constexpr (DT == FP8_DT_BF16) return max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else {
+    const float2 v = h2f2(w);
+    return max_nan(v.x, v.y);
   }
-  const int c = r.s.head + r.s.vecs * kElems<DT> + t - r.head;
-  if (t >= r.head && t < r.head + r.tail) f(c, load_one<DT>(r.row, c));
+}
+template <int DT>
+constexpr uint32_t kMinusInf = DT == FP8_DT_F32 ? 0xff800000u : DT == FP8_DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+
+// Calls f(column, logit) for the elements of the range that this thread owns and
+// whose key reaches `least`.
+template <int DT, typename F>
+__device__ __forceinline__ void each_own(const Range &r, uint32_t least, F f) {
+  const int t = threadIdx.x, T = blockDim.x;
+  if (t < r.head + r.tail) {
+    const int c = t < r.head ? t : r.s.head + r.s.vecs * kElems<DT> + t - r.head;
+    const float x = load_one<DT>(r.row, c);
+    if (order_key(x) >= least) f(c, x);
+  }
+#pragma unroll 1
+  for (int v = r.v0 + t; v < r.v1; v += 4 * T) {
+    uint4 w[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) w[u] = __ldcg(reinterpret_cast<const uint4 *>(r.body) + min(v + u * T, r.v1 - 1));
+    uint32_t pass = 0;
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const float x = widest<DT>(max_word<DT>(max_word<DT>(w[u].x, w[u].y), max_word<DT>(w[u].z, w[u].w)));
+      if (v + u * T < r.v1 && order_key(x) >= least) pass |= 1u << u;
+    }
+    while (pass) {
+      const int u = __ffs(pass) - 1, c = r.s.head + (v + u * T) * kElems<DT>;
+      pass &= pass - 1;
+      const uint4 q = u == 0 ? w[0] : u == 1 ? w[1] : u == 2 ? w[2] : w[3];
+      float x[kElems<DT>];
+      unpack<DT>(q, x);
+#pragma unroll
+      for (int j = 0; j < kElems<DT>; j++)
+        if (order_key(x[j]) >= least) f(c + j, x[j]);
+    }
+  }
 }
 
-struct TopScratch {
+struct __align__(16) TopScratch {
   unsigned long long list[kCandidates];  // (key, ~column): larger is earlier
-  uint32_t group[32];
+  uint32_t group[64];
   int above, equal, ties;
   uint32_t bound;
   unsigned long long best[kTop];
@@ -220,22 +248,29 @@ __device__ __forceinline__ unsigned long long candidate(uint32_t key, int col) {
   return (unsigned long long)key << 32 | (uint32_t)~col;
 }
 
-// The `top` first candidates of a list of n, in order, to out (0: none).
+// The `top` first candidates of a list of n, in order, to out (0: none).  Eight
+// lanes count together how many come before a candidate.
 __device__ __forceinline__ void rank_list(const unsigned long long *list, int n, int top, unsigned long long *out) {
+  constexpr int G = 8;
+  const int g = threadIdx.x % G, rows = blockDim.x / G;
   for (int i = threadIdx.x; i < top; i += blockDim.x) out[i] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const unsigned long long c = list[i];
+  for (int i0 = 0; i0 < n; i0 += rows) {
+    const int i = i0 + threadIdx.x / G;
+    const unsigned long long c = i < n ? list[i] : 0ull;
     int before = 0;
-    for (int j = 0; j < n && before < top; j++) before += list[j] > c;
-    if (before < top && c) out[before] = c;
+#pragma unroll 4
+    for (int j = g; j < n; j += G) before += list[j] > c;
+#pragma unroll
+    for (int b = G / 2; b > 0; b /= 2) before += __shfl_xor_sync(0xffffffffu, before, b);
+    if (g == 0 && before < top && c) out[before] = c;
   }
   __syncthreads();
 }
 
 // The `top` largest logits of the CTA's range, in order, to sh.best.  `most` is
-// the thread's own largest.  The top-th largest maximum of 32 groups of threads
-// is a bound that at least `top` elements reach; few others do, and only threads
+// the thread's own largest.  The top-th largest maximum of 64 groups of
+// threads is a bound that at least `top` elements reach; few others do, and only threads
 // that own one read their elements again.  Where many are equal to the bound (a
 // masked vocabulary) those of the lowest columns are taken in order; where too
 // many lie above it the bound is raised by bisection.
@@ -243,27 +278,30 @@ template <int DT>
 __device__ void top_of_range(const Range &r, float most, bool any, int top, TopScratch &sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const uint32_t own = any ? order_key(most) : 0u;
-  const int per = warps;  // threads of a group: blockDim.x / 32, a power of two
+  constexpr int groups = 64;
+  const int per = blockDim.x / groups;  // (128 threads or more: 2 to 16, powers of two)
   uint32_t g = own;
   for (int b = per / 2; b > 0; b /= 2) g = max(g, __shfl_xor_sync(0xffffffffu, g, b));
   if (threadIdx.x % per == 0) sh.group[threadIdx.x / per] = g;
   if (threadIdx.x == 0) sh.above = sh.equal = 0;
   __syncthreads();
-  if (warp == 0) {
-    const uint32_t k = sh.group[lane];
-    int before = 0;
-    for (int j = 0; j < 32; j++) {
-      const uint32_t o = __shfl_sync(0xffffffffu, k, j);
-      before += o > k || (o == k && j < lane);
+  if (threadIdx.x < groups) {
+    const uint32_t k = sh.group[threadIdx.x];
+    int more = 0, same = 0;  // groups above this one's maximum, and at it
+#pragma unroll 4
+    for (int j = 0; j < groups; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4 *>(&sh.group[j]);
+      more += (o.x > k) + (o.y > k) + (o.z > k) + (o.w > k);
+      same += (o.x == k) + (o.y == k) + (o.z == k) + (o.w == k);
     }
-    if (before == top - 1) sh.bound = k;
+    if (more < top && more + same >= top) sh.bound = k;
   }
   __syncthreads();
   uint32_t bound = sh.bound;
   // candidates above the bound from the front, equal ones from the back
   auto collect = [&] {
     if (own >= bound)
-      each_own<DT>(r, [&](int c, float z) {
+      each_own<DT>(r, bound, [&](int c, float z) {
         const uint32_t k = order_key(z);
         if (k > bound) {
           const int i = atomicAdd(&sh.above, 1);
@@ -285,7 +323,7 @@ __device__ void top_of_range(const Range &r, float most, bool any, int top, TopS
       if (threadIdx.x == 0) sh.ties = 0;
       __syncthreads();
       int count = 0;
-      if (own >= mid) each_own<DT>(r, [&](int, float z) { count += order_key(z) >= mid; });
+      if (own >= mid) each_own<DT>(r, mid, [&](int, float) { count++; });
       if (count) atomicAdd(&sh.ties, count);
       __syncthreads();
       if (sh.ties >= top) lo = mid;
@@ -337,85 +375,180 @@ __device__ void top_of_range(const Range &r, float most, bool any, int top, TopS
   rank_list(sh.list, n, top, sh.best);
 }
 
-struct ListScratch {
+struct __align__(16) ListScratch {
   int id[FP8_DISTILL_MAX];
+  float v[FP8_DISTILL_MAX];
 };
 
-// Running softmax of a row's elements and, for kListTail, of the unlisted ones
-// alone (`marks`: a bit for each element of the body, by its place there).
-template <int DT, int MODE, bool ENT>
-__device__ __forceinline__ Part stream_row(const Range &r, float c2, const uint8_t *marks, uint32_t edge_marks,
-                                           float &most, bool &any) {
-  float m = kNone, S = 0.0f, W = 0.0f, L = 0.0f;  // L: of the listed ones
-  float largest = -INFINITY;
-  bool got = false;
-  // n elements; bits: which of them are listed
-  auto add = [&](const float *x, int n, uint32_t bits) {
-    float t = x[0];
-#pragma unroll
-    for (int j = 1; j < n; j++) t = max_nan(t, x[j]);
+// What a thread has seen: S and W about m; L the listed ones' part (kListTail).
+template <int MODE, bool ENT>
+struct Running {
+  float m = kNone, W = 0.0f, L = 0.0f, largest = -INFINITY;
+  float2 S = make_float2(0.0f, 0.0f), W2 = make_float2(0.0f, 0.0f);
+  bool any = false;
+
+  // m grows to include t
+  __device__ __forceinline__ void raise(float t, float c2) {
     if constexpr (MODE == kLogprob) largest = max_nan(largest, t);
+    any = true;
     const float m1 = max_nan(m, t);
     float d = (m - m1) * c2;
     if constexpr (ENT) {
       d = max_nan(d, -1000.0f);
-      W = fmaf(S, d, W);
+      W2 = __ffma2_rn(S, both(d), W2);
     }
     const float down = ex2(d);
-    S *= down;
+    S = __fmul2_rn(S, both(down));
     if constexpr (MODE == kListTail) L *= down;
-    if constexpr (ENT) W *= down;
+    if constexpr (ENT) W2 = __fmul2_rn(W2, both(down));
     m = m1;
-#pragma unroll
-    for (int j = 0; j < n; j++) {
-      float a = (x[j] - m) * c2;
+  }
+  // n elements, none above m
+  template <int N>
+  __device__ __forceinline__ void add(const float (&x)[N], float c2) {
+    if constexpr (N == 1) {
+      float a = (x[0] - m) * c2;
       if constexpr (ENT) a = max_nan(a, -1000.0f);
       const float e = ex2(a);
-      if constexpr (MODE == kListTail) {
-        if (bits >> j & 1) L += e;
-        else S += e;
-      } else {
-        S += e;
+      S.x += e;
+      if constexpr (ENT) W2.x = fmaf(e, a, W2.x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; j += 2) {
+        float2 a = __fmul2_rn(__fadd2_rn(make_float2(x[j], x[j + 1]), both(-m)), both(c2));
+        if constexpr (ENT) a = make_float2(max_nan(a.x, -1000.0f), max_nan(a.y, -1000.0f));
+        const float2 e = make_float2(ex2(a.x), ex2(a.y));
+        S = __fadd2_rn(S, e);
+        if constexpr (ENT) W2 = __ffma2_rn(e, a, W2);
       }
-      if constexpr (ENT) W = fmaf(e, a, W);
     }
-    got = true;
-  };
-  const int t = threadIdx.x;
-  if (t < r.head + r.tail) {
-    const float x[1] = {load_one<DT>(r.row, t < r.head ? t : r.s.head + r.s.vecs * kElems<DT> + t - r.head)};
-    add(x, 1, edge_marks >> (t < r.head ? t : 16 + t - r.head) & 1);
   }
-  for (int v = r.v0 + t; v < r.v1; v += blockDim.x) {
-    float x[kElems<DT>];
-    unpack<DT>(__ldg(reinterpret_cast<const uint4 *>(r.body) + v), x);
-    uint32_t bits = 0;
-    if constexpr (MODE == kListTail) {
-      const int at = (v - r.v0) * kElems<DT>;
-      bits = marks[at >> 3] >> (at & 7);
-    }
-    add(x, kElems<DT>, bits);
-  }
-  most = largest;
-  any = got;
-  // (a thread that has seen only -inf has m = kNone: its parts are 0)
-  return {m, S, W, L};
+  // a listed element
+  __device__ __forceinline__ void add_listed(float x, float c2) { L += ex2((x - m) * c2); }
+};
+
+// Where element e of a CTA's body has its bit: a thread's kRun vectors of one
+// step stand side by side, so that it asks once for all of them.
+constexpr int kRun = 4;
+template <int DT>
+__device__ __forceinline__ int mark_at(int e) {
+  const int v = e / kElems<DT>, T = blockDim.x, step = v / (kRun * T), in = v - step * kRun * T;
+  return (step * T + in % T) * (kRun * kElems<DT>) + in / T * kElems<DT> + e % kElems<DT>;
+}
+template <int DT>
+__host__ __device__ inline size_t mark_bytes(int vecs, int threads) {
+  return (size_t)((vecs + kRun * threads - 1) / (kRun * threads)) * threads * (kRun * kElems<DT> / 8);
 }
 
-// The parts of several threads or CTAs joined.  W is in units of log 2.
-template <int MODE, bool ENT>
-__device__ __forceinline__ Part join_block(Part p, float c2, float *red) {
-  const float m = block_max(p.m, red);
-  float d = (p.m - m) * c2;
-  if constexpr (ENT) {
-    d = max_nan(d, -1000.0f);
-    p.W = fmaf(p.S, d, p.W);
+// Running softmax of a row's elements and, for kListTail, of the unlisted ones
+// alone (`marks`: a bit for each element, see mark_at).  Four
+// vectors at a time: their loads are in flight together, and m is raised once.
+// Per element of a 16-bit row: one exponential (16 a cycle and SM: 46 us for
+// 4096 x 50304), some four other instructions.
+template <int DT, int MODE, bool ENT>
+__device__ __forceinline__ Running<MODE, ENT> stream_row(const Range &r, float c2, const uint8_t *marks, uint32_t edge_marks) {
+  constexpr int E = kElems<DT>;
+  Running<MODE, ENT> s;
+  const int t = threadIdx.x, T = blockDim.x;
+  if (t < r.head + r.tail) {
+    const float x[1] = {load_one<DT>(r.row, t < r.head ? t : r.s.head + r.s.vecs * E + t - r.head)};
+    s.raise(x[0], c2);
+    if (MODE == kListTail && (edge_marks >> (t < r.head ? t : 16 + t - r.head) & 1)) s.add_listed(x[0], c2);
+    else s.add(x, c2);
   }
-  const float down = ex2(d);
-  Part o = {m, block_sum(p.S * down, red), 0.0f, 0.0f};
-  if constexpr (ENT) o.W = block_sum(p.W * down, red);
-  if constexpr (MODE == kListTail) o.rest = block_sum(p.rest * down, red);
-  return o;
+  const uint4 *body = reinterpret_cast<const uint4 *>(r.body);
+  const uint32_t none = kMinusInf<DT>;
+  int step = t;
+  for (int v = r.v0 + t; v < r.v1; v += kRun * T, step += T) {
+    uint4 w[kRun];
+    bool skip = false;  // runs with listed elements are left to add_marked
+    if constexpr (MODE == kListTail)
+      skip = (E == 8 ? reinterpret_cast<const uint32_t *>(marks)[step] : (uint32_t)reinterpret_cast<const uint16_t *>(marks)[step]) != 0;
+#pragma unroll
+    for (int u = 0; u < kRun; u++) {
+      w[u] = make_uint4(none, none, none, none);
+      if (!skip && v + u * T < r.v1) w[u] = __ldcg(body + v + u * T);
+    }
+    uint32_t k = w[0].x;
+#pragma unroll
+    for (int u = 0; u < kRun; u++)
+      k = max_word<DT>(max_word<DT>(max_word<DT>(max_word<DT>(k, w[u].x), w[u].y), w[u].z), w[u].w);
+    s.raise(widest<DT>(k), c2);
+#pragma unroll
+    for (int u = 0; u < kRun; u++) {
+      float x[E];
+      unpack<DT>(w[u], x);
+      s.add(x, c2);
+    }
+  }
+  // (a thread that has seen only -inf has m = kNone, and its sums are 0)
+  return s;
+}
+
+// The run of element e of the body, which is listed, if none before it in the
+// run is: lane g of G takes every G-th of its vectors.  (Tested inside the
+// stream, two of three steps of a warp took the slow way: 142 us for 4096 x
+// 50304 with 64 entries a row.)
+template <int DT, bool ENT>
+__device__ __forceinline__ void add_marked(Running<kListTail, ENT> &s, const Range &r, float c2, const uint8_t *marks, int e,
+                                           int g, int G) {
+  constexpr int E = kElems<DT>, kBits = kRun * E;
+  const int T = blockDim.x, b = mark_at<DT>(e), run = b / kBits;
+  const uint32_t bits = E == 8 ? reinterpret_cast<const uint32_t *>(marks)[run]
+                               : (uint32_t)reinterpret_cast<const uint16_t *>(marks)[run];
+  if (bits & ((1u << (b % kBits)) - 1)) return;
+#pragma unroll 1
+  for (int u = g; u < kRun; u += G) {
+    const int v = r.v0 + run / T * (kRun * T) + u * T + run % T;
+    if (v >= r.v1) break;
+    const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(r.body) + v);
+    s.raise(widest<DT>(max_word<DT>(max_word<DT>(w.x, w.y), max_word<DT>(w.z, w.w))), c2);
+    float x[E];
+    unpack<DT>(w, x);
+#pragma unroll
+    for (int j = 0; j < E; j++) {
+      const float x1[1] = {x[j]};
+      if (bits >> (u * E + j) & 1) s.add_listed(x[j], c2);
+      else s.add(x1, c2);
+    }
+  }
+}
+
+// Parts about their own m joined about the largest.  W is in units of log 2.
+__device__ __forceinline__ Part about(Part p, float m, float c2) {
+  const float d = max_nan((p.m - m) * c2, -1000.0f), down = ex2(d);
+  return {m, p.S * down, fmaf(p.S, d, p.W) * down, p.rest * down};
+}
+
+// The CTA's part, to every thread: the warps by shuffles, then one exchange.
+template <int MODE, bool ENT>
+__device__ __forceinline__ Part join_block(const Running<MODE, ENT> &s, float c2, Part *warps) {
+  float m = s.m;
+#pragma unroll
+  for (int b = 16; b > 0; b /= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, b));
+  Part p = about({s.m, s.S.x + s.S.y, s.W2.x + s.W2.y, s.L}, m, c2);
+#pragma unroll
+  for (int b = 16; b > 0; b /= 2) {
+    p.S += __shfl_xor_sync(0xffffffffu, p.S, b);
+    if constexpr (ENT) p.W += __shfl_xor_sync(0xffffffffu, p.W, b);
+    if constexpr (MODE == kListTail) p.rest += __shfl_xor_sync(0xffffffffu, p.rest, b);
+  }
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = p;
+  __syncthreads();
+  // each warp joins all of them, a lane a part
+  const int lane = threadIdx.x & 31;
+  p = lane < (int)(blockDim.x >> 5) ? warps[lane] : Part{kNone, 0.0f, 0.0f, 0.0f};
+  m = p.m;
+#pragma unroll
+  for (int b = 16; b > 0; b /= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, b));
+  p = about(p, m, c2);
+#pragma unroll
+  for (int b = 16; b > 0; b /= 2) {
+    p.S += __shfl_xor_sync(0xffffffffu, p.S, b);
+    if constexpr (ENT) p.W += __shfl_xor_sync(0xffffffffu, p.W, b);
+    if constexpr (MODE == kListTail) p.rest += __shfl_xor_sync(0xffffffffu, p.rest, b);
+  }
+  return p;
 }
 
 template <int DT, int MODE, bool ENT>
@@ -424,7 +557,7 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
   pdl_wait();
   extern __shared__ __align__(16) uint8_t loss_smem[];
   __shared__ float red[32];
-  __shared__ Part parts[8];
+  __shared__ __align__(16) Part parts[8], warp_parts[32];
   __shared__ uint32_t edge_bits;
   const unsigned rank = ctas > 1 ? blockIdx.x % ctas : 0;
   const int row = (int)(blockIdx.x / ctas);
@@ -433,87 +566,118 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
   const float c2 = p.beta * kLog2e;
   ListScratch &list = *reinterpret_cast<ListScratch *>(loss_smem);
   uint8_t *marks = loss_smem + sizeof(ListScratch);
-  float q_sum = 0.0f, top_value = 0.0f, mine_v[4], mine_q[4];
+  // an entry belongs to the first of G lanes, which look at the list together; a thread has at most four
+  const int K = MODE == kLogprob ? 0 : p.top, K4 = (K + 3) / 4;
+  const int G = K * 4 <= (int)blockDim.x ? 4 : K * 2 <= (int)blockDim.x ? 2 : 1;
+  const int lead = threadIdx.x % G == 0, first = threadIdx.x / G, apart = blockDim.x / G;
+  float top_value = 0.0f, mine_v[4], mine_q[4];
   int mine_id[4], mine_at[4];
   if constexpr (MODE != kLogprob) {
-    // the list by id: an entry's place is the number of entries that come before it
-    const int K = p.top;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int k = threadIdx.x + i * blockDim.x;
-      mine_id[i] = kAbsent;
-      mine_v[i] = -INFINITY;
-      mine_at[i] = 0;
+    for (int k = threadIdx.x; k < K4 * 4; k += blockDim.x) {
+      int id = kAbsent;
+      float v = -INFINITY;
       if (k < K) {
         const size_t at = (size_t)row * K + k;
-        const long long id = index_at(p.ids, p.id_bytes, at);
-        if (id >= p.cols) atomicOr(&g_status, FP8_STATUS_BAD_INDEX);
+        const long long i = index_at(p.ids, p.id_bytes, at);
+        if (i >= p.cols) atomicOr(&g_status, FP8_STATUS_BAD_INDEX);
         if (p.value_dt == FP8_DT_F32) {
-          mine_v[i] = reinterpret_cast<const float *>(p.values)[at];
+          v = reinterpret_cast<const float *>(p.values)[at];
         } else {
           const uint16_t h = reinterpret_cast<const uint16_t *>(p.values)[at];
-          mine_v[i] = p.value_dt == FP8_DT_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+          v = p.value_dt == FP8_DT_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
         }
-        if (id >= 0 && id < p.cols && mine_v[i] != -INFINITY) mine_id[i] = (int)id;
-        list.id[k] = mine_id[i];
+        if (i >= 0 && i < p.cols && v != -INFINITY) id = (int)i;
+        else v = -INFINITY;
       }
+      list.id[k] = id;
+      list.v[k] = v;
     }
     if (MODE == kListTail) {
-      const int bytes = ((r.v1 - r.v0) * kElems<DT> + 7) / 8;
-      for (int i = threadIdx.x; i < (bytes + 3) / 4; i += blockDim.x) reinterpret_cast<uint32_t *>(marks)[i] = 0;
+      const int words = (int)mark_bytes<DT>(r.v1 - r.v0, blockDim.x) / 4;  // (128 threads or more: whole words)
+      for (int i = threadIdx.x; i < words; i += blockDim.x) reinterpret_cast<uint32_t *>(marks)[i] = 0;
       if (threadIdx.x == 0) edge_bits = 0;
     }
     __syncthreads();
+    // an entry's place by id is the number of entries that come before it; the same id earlier in the list: listed again
+    float v_max = kNone, q_sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const int k = threadIdx.x + i * blockDim.x;
-      bool again = false;
-      if (k < K && mine_id[i] != kAbsent)
-        for (int j = 0; j < k; j++) again |= list.id[j] == mine_id[i];
-      if (again) mine_id[i] = kAbsent;
-    }
-    __syncthreads();
-    float v_max = kNone;
+      const int k = first + i * apart;
+      mine_id[i] = kAbsent;
+      mine_v[i] = -INFINITY;
+      mine_at[i] = -1;
+      if (i * apart >= K) continue;  // (the same for all lanes)
+      const int id = k < K ? list.id[k] : kAbsent;
+      int before = 0, again = 0;
+      for (int j = threadIdx.x % G; j < K4; j += G) {
+        const int4 o = reinterpret_cast<const int4 *>(list.id)[j];
+        const int e[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int k = threadIdx.x + i * blockDim.x;
-      if (k < K) list.id[k] = mine_id[i];
-      if (mine_id[i] == kAbsent) mine_v[i] = -INFINITY;
-      v_max = max_nan(v_max, mine_v[i]);
-      if (MODE == kListTail && mine_id[i] != kAbsent) {
-        const int e = mine_id[i] - r.s.head, body = r.s.vecs * kElems<DT>;
+        for (int n = 0; n < 4; n++) {
+          const int same = e[n] == id && 4 * j + n < k;
+          again += same;
+          before += (e[n] < id) + same;
+        }
+        if (MODE == kListTop && i == 0) {
+          const float4 v = reinterpret_cast<const float4 *>(list.v)[j];
+          v_max = max_nan(max_nan(max_nan(max_nan(v_max, v.x), v.y), v.z), v.w);
+        }
+      }
+      for (int b = G / 2; b > 0; b /= 2) {
+        before += __shfl_xor_sync(0xffffffffu, before, b);
+        again += __shfl_xor_sync(0xffffffffu, again, b);
+        if (MODE == kListTop && i == 0) v_max = max_nan(v_max, __shfl_xor_sync(0xffffffffu, v_max, b));
+      }
+      if (MODE == kListTop) top_value = v_max;
+      if (!lead || k >= K) continue;
+      mine_at[i] = before;
+      mine_id[i] = id;
+      mine_q[i] = 0.0f;
+      if (id == kAbsent) continue;
+      if (again) {
+        mine_q[i] = -1.0f;  // stands behind the first one and counts for nothing
+        continue;
+      }
+      mine_v[i] = list.v[k];
+      mine_q[i] = expf(MODE == kListTop ? (mine_v[i] - top_value) * p.beta : mine_v[i]);
+      q_sum += mine_q[i];
+      if (MODE == kListTail) {
+        const int e = id - r.s.head, body = r.s.vecs * kElems<DT>;
         if (e >= 0 && e < body) {
-          const int b = e - r.v0 * kElems<DT>;
-          if (b >= 0 && e < r.v1 * kElems<DT>) atomicOr(reinterpret_cast<uint32_t *>(marks) + (b >> 5), 1u << (b & 31));
+          if (e >= r.v0 * kElems<DT> && e < r.v1 * kElems<DT>) {
+            const int b = mark_at<DT>(e - r.v0 * kElems<DT>);
+            atomicOr(reinterpret_cast<uint32_t *>(marks) + (b >> 5), 1u << (b & 31));
+          }
         } else {
-          atomicOr(&edge_bits, 1u << (e < 0 ? mine_id[i] : 16 + e - body));
+          atomicOr(&edge_bits, 1u << (e < 0 ? id : 16 + e - body));
         }
       }
     }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int k = threadIdx.x + i * blockDim.x;
-      if (k < K)
-        for (int j = 0; j < K; j++) {
-          const int o = list.id[j];
-          mine_at[i] += o < mine_id[i] || (o == mine_id[i] && j < k);
-        }
-    }
-    if (MODE == kListTop) top_value = block_max(v_max, red);
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      mine_q[i] = expf(MODE == kListTop ? (mine_v[i] - top_value) * p.beta : mine_v[i]);
-      q_sum += mine_q[i];
-    }
-    q_sum = block_sum(q_sum, red);  // (its barriers also publish the marks)
+    for (int b = 16; b > 0; b /= 2) q_sum += __shfl_xor_sync(0xffffffffu, q_sum, b);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = q_sum;
+    if (MODE == kListTail) __syncthreads();  // the marks (red is read behind the next exchange)
   }
-  float most;
-  bool any;
-  Part own = stream_row<DT, MODE, ENT>(r, c2, marks, MODE == kListTail ? edge_bits : 0u, most, any);
-  Part all = join_block<MODE, ENT>(own, c2, red);
+  Running<MODE, ENT> own = stream_row<DT, MODE, ENT>(r, c2, marks, MODE == kListTail ? edge_bits : 0u);
+  if constexpr (MODE == kListTail) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if (i * apart >= K) continue;
+      const int lead_lane = (threadIdx.x & 31) / G * G;
+      const bool counts = mine_at[i] >= 0 && mine_id[i] != kAbsent && !(mine_q[i] < 0.0f);
+      const int id = __shfl_sync(0xffffffffu, counts ? mine_id[i] : kAbsent, lead_lane);
+      const int e = id - r.s.head - r.v0 * kElems<DT>;
+      if (id != kAbsent && e >= 0 && e < (r.v1 - r.v0) * kElems<DT>)
+        add_marked<DT, ENT>(own, r, c2, marks, e, threadIdx.x % G, G);
+    }
+  }
+  Part all = join_block<MODE, ENT>(own, c2, warp_parts);
+  float q_sum = 0.0f;
+  if constexpr (MODE != kLogprob) {
+    for (int w = 0; w < (int)(blockDim.x >> 5); w++) q_sum += red[w];
+  }
   TopScratch &top = *reinterpret_cast<TopScratch *>(loss_smem);
-  if (MODE == kLogprob && p.top) top_of_range<DT>(r, most, any, p.top, top);
+  if (MODE == kLogprob && p.top) top_of_range<DT>(r, own.largest, own.any, p.top, top);
   if (ctas > 1) {
     if (threadIdx.x == 0) parts[rank] = all;
     cluster_wait();
@@ -542,11 +706,10 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
     for (unsigned i = 0; i < ctas; i++) m = max_nan(m, parts[i].m);
     all = {m, 0.0f, 0.0f, 0.0f};
     for (unsigned i = 0; i < ctas; i++) {
-      Part o = parts[i];
-      const float d = max_nan((o.m - m) * c2, -1000.0f), down = ex2(d);
-      all.W += fmaf(o.S, d, o.W) * down;
-      all.S += o.S * down;
-      all.rest += o.rest * down;
+      const Part o = about(parts[i], m, c2);
+      all.W += o.W;
+      all.S += o.S;
+      all.rest += o.rest;
     }
     if (MODE == kLogprob && p.top) rank_list(top.list, (int)ctas * p.top, p.top, top.best);
   }
@@ -571,23 +734,19 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
       p.top_logp[(size_t)row * p.top + i] = none ? -INFINITY : p.beta * (key_value((uint32_t)(c >> 32)) - all.m) - log_S;
     }
   } else {
-    const int K = p.top;
     const float log_q_sum = logf(q_sum), q_scale = MODE == kListTop && q_sum > 0.0f ? 1.0f / q_sum : 1.0f;
     float l = 0.0f;
-    if (rank == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int k = threadIdx.x + i * blockDim.x;
-        if (k >= K) break;
-        const float q = mine_q[i] * q_scale;
-        if (mine_id[i] != kAbsent && q != 0.0f) {
-          const float lq = MODE == kListTop ? (mine_v[i] - top_value) * p.beta - log_q_sum : mine_v[i];
-          const float lp = none ? -INFINITY : p.beta * (load_one<DT>(z, mine_id[i]) - all.m) - log_S;
-          l = fmaf(q, lq - lp, l);
-        }
-        p.list_ids[(size_t)row * K + mine_at[i]] = mine_id[i];
-        p.list_q[(size_t)row * K + mine_at[i]] = q;
+    for (int i = 0; i < 4; i++) {
+      if (mine_at[i] < 0) continue;
+      const float q = mine_q[i] < 0.0f ? mine_q[i] : mine_q[i] * q_scale;
+      if (mine_id[i] != kAbsent && !(mine_q[i] <= 0.0f)) {
+        const float lq = MODE == kListTop ? (mine_v[i] - top_value) * p.beta - log_q_sum : mine_v[i];
+        const float lp = none ? -INFINITY : p.beta * (load_one<DT>(z, mine_id[i]) - all.m) - log_S;
+        l = fmaf(q, lq - lp, l);
       }
+      p.list_ids[(size_t)row * K + mine_at[i]] = mine_id[i];
+      p.list_q[(size_t)row * K + mine_at[i]] = q;
     }
     l = block_sum(l, red);
     float listed = q_sum > 0.0f ? 1.0f : 0.0f, unlisted = listed;
@@ -701,8 +860,11 @@ __global__ void __launch_bounds__(kBwdThreads) k_loss_bwd_rows(const Bwd p, unsi
       if (k < p.K) {
         const int c = __ldg(p.list_ids + (size_t)row * p.K + k);
         if (c < p.cols && ((c >= c0 && c < c1) || (chunk == 0 && c >= last))) {
-          listed_at[i] = c;
-          listed[i] = fmaf(ex2(scaled(load_one<DT>(z, c), r.m, c2)), r.kl, -r.gt * __ldg(p.list_q + (size_t)row * p.K + k));
+          const float q = __ldg(p.list_q + (size_t)row * p.K + k);
+          if (!(q < 0.0f)) {  // (not listed again)
+            listed_at[i] = c;
+            listed[i] = fmaf(ex2(scaled(load_one<DT>(z, c), r.m, c2)), r.kl, -r.gt * q);
+          }
         }
       }
     }
@@ -747,31 +909,35 @@ __global__ void __launch_bounds__(kBwdThreads) k_loss_bwd_rows(const Bwd p, unsi
   }
 }
 
-// Codes of d, and d itself where wanted: tiles of block_scale.cuh.
-template <int DT, bool LIST, int OUT>
+// Codes of d, and d itself where wanted: tiles of block_scale.cuh.  The 16 lanes
+// of a tile's row share RP rows: lane i works out the i-th one's factors (and
+// which of the tile's columns are listed) while the tile's loads are in flight,
+// and passes them on by shuffles; no barrier before the column maxima.
+enum { kToken = 0, kTokenEntropy = 1, kListed = 2 };
+
+template <int DT, int KIND, int OUT>
 __global__ void __launch_bounds__(512, 2) k_loss_bwd_tiles(const Bwd p) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int RP = 4;
+  constexpr bool LIST = KIND == kListed;
   using G = block::Geo<RP>;
   __shared__ block::ColScratch<RP> sc;
-  __shared__ __align__(16) uint32_t marks[LIST ? block::kTile : 1][4];
-  __shared__ int places[LIST ? block::kTile : 1];
   constexpr int esz = kSize<DT>;
   const int tiles_c = (p.cols + block::kTile - 1) / block::kTile;
   const auto [row0, col0] = block::tile_at(blockIdx.x, tiles_c);
-  const int c8 = threadIdx.x & 15, col = col0 + c8 * 8, r0 = threadIdx.x >> 4;
+  const int c8 = threadIdx.x & 15, col = col0 + c8 * 8, r0 = row0 + (threadIdx.x >> 4);
   Raw8<DT> raw[RP];
   block::load_tile<DT>(p.z, p.ld / esz, p.vec_z, row0, col0, p.rows, p.cols, raw);
-  if constexpr (LIST) {
-    // the list entries of each row in this tile: marked, and where the first one stands
-    if (threadIdx.x < block::kTile) {
-      const int row = row0 + threadIdx.x;
-      uint32_t m[4] = {0, 0, 0, 0};
-      int lo = 0;
-      if (row < p.rows) {
+  RowTerms own = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, -1};  // rows behind the last: 0
+  uint32_t marks[4] = {0, 0, 0, 0};                    // listed columns of the tile
+  {
+    const int row = r0 + c8 * G::kStep;
+    if (c8 < RP && row < p.rows) {
+      own = row_terms<LIST>(p, row);
+      if constexpr (LIST) {
         const int *ids = p.list_ids + (size_t)row * p.K;
-        int hi = p.K;
+        int lo = 0, hi = p.K;
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
           if (__ldg(ids + mid) < col0) lo = mid + 1;
@@ -782,44 +948,72 @@ __global__ void __launch_bounds__(512, 2) k_loss_bwd_tiles(const Bwd p) {
           if (b >= block::kTile) break;
 #pragma unroll
           for (int w = 0; w < 4; w++)
-            if (b >> 5 == w) m[w] |= 1u << (b & 31);
+            if (b >> 5 == w) marks[w] |= 1u << (b & 31);
         }
+        own.token = lo;  // the first entry there
+      } else if (own.token >= 0) {
+        own.token -= col0;
       }
-      *reinterpret_cast<uint4 *>(marks[threadIdx.x]) = make_uint4(m[0], m[1], m[2], m[3]);
-      places[threadIdx.x] = lo;
     }
-    __syncthreads();
   }
   const float c2 = p.beta * kLog2e;
+  const int lane0 = threadIdx.x & 16;
   float f[RP][8];
 #pragma unroll
   for (int i = 0; i < RP; i++) {
-    const int row = row0 + r0 + i * G::kStep;
+    const float m = __shfl_sync(0xffffffffu, own.m, lane0 + i), k0 = __shfl_sync(0xffffffffu, own.k0, lane0 + i);
+    const float gt = __shfl_sync(0xffffffffu, own.gt, lane0 + i);
+    const int token = __shfl_sync(0xffffffffu, own.token, lane0 + i);
+    float k1 = 0.0f;
+    if constexpr (KIND == kTokenEntropy) k1 = __shfl_sync(0xffffffffu, own.k1, lane0 + i);
     block::unpack8<DT>(raw[i], f[i]);
-    if (row >= p.rows) {
+    float2 e[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      float2 a = __fmul2_rn(__fadd2_rn(make_float2(f[i][2 * j], f[i][2 * j + 1]), both(-m)), both(c2));
+      if constexpr (KIND == kTokenEntropy) a = make_float2(max_nan(a.x, -1000.0f), max_nan(a.y, -1000.0f));
+      e[j] = make_float2(ex2(a.x), ex2(a.y));
+      float2 g;
+      if constexpr (KIND == kTokenEntropy) g = __fmul2_rn(e[j], __ffma2_rn(both(k1), a, both(k0)));
+      else g = __fmul2_rn(e[j], both(k0));
+      f[i][2 * j] = g.x;
+      f[i][2 * j + 1] = g.y;
+    }
+    if constexpr (LIST) {
+      const float kl = __shfl_sync(0xffffffffu, own.kl, lane0 + i);
+      uint32_t bits = 0;
+#pragma unroll
+      for (int w = 0; w < 4; w++) {
+        const uint32_t word = __shfl_sync(0xffffffffu, marks[w], lane0 + i);
+        if (c8 >> 2 == w) bits = word >> ((c8 & 3) * 8) & 0xffu;
+      }
+      if (bits) {  // rare: the list's entries of these columns
+        const size_t at = (size_t)(r0 + i * G::kStep) * p.K;
+        int k = token;
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+          if (bits >> j & 1) {
+            while (__ldg(p.list_ids + at + k) != col + j) k++;  // (marked, so it is there)
+            const float ej = j & 1 ? e[j >> 1].y : e[j >> 1].x;
+            f[i][j] = fmaf(ej, kl, -gt * __ldg(p.list_q + at + k));
+          }
+      }
+    } else {
+      const int at = token - c8 * 8;
+      if (token >= 0 && (unsigned)at < 8u) {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+          if (j == at) f[i][j] += gt;
+      }
+    }
+    if (col + 8 > p.cols) {  // the row's end
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+        if (col + j >= p.cols) f[i][j] = 0.0f;
+    }
+    if (r0 + i * G::kStep >= p.rows) {  // NaN here would spoil a column's scale: the clamped load is of another row
 #pragma unroll
       for (int j = 0; j < 8; j++) f[i][j] = 0.0f;
-      continue;
-    }
-    const RowTerms r = row_terms<LIST>(p, row);
-    uint32_t bits = 0;
-    if constexpr (LIST) bits = marks[row - row0][c8 >> 2] >> ((c8 & 3) * 8) & 0xffu;
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const float a = scaled(f[i][j], r.m, c2), e = ex2(a);
-      float g = e * fmaf(r.k1, a, r.k0);
-      if (!LIST && col + j == r.token) g += r.gt;
-      if (LIST && (bits >> j & 1)) {
-        int k = places[row - row0];
-#pragma unroll
-        for (int w = 0; w < 4; w++) {
-          const uint32_t m = marks[row - row0][w];
-          const int first = c8 * 8 + j - w * 32;  // bits of this word that come before
-          k += first >= 32 ? __popc(m) : first > 0 ? __popc(m & ((1u << first) - 1)) : 0;
-        }
-        g = fmaf(e, r.kl, -r.gt * __ldg(p.list_q + (size_t)row * p.K + k));
-      }
-      f[i][j] = col + j < p.cols ? g : 0.0f;
     }
   }
   if (p.d) block::store_tile<DT>(p.vec_d, p.d, p.ldd / esz, row0, col0, p.rows, p.cols, f);

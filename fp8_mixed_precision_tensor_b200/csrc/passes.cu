@@ -106,7 +106,8 @@ LossGrid loss_grid(int rows, int cols, int dtype, int sms, unsigned least) {
   LossGrid g = {1, 0, 0};
   while (g.ctas < 8 && (long long)rows * g.ctas * 2 <= sms && vecs / (int)(2 * g.ctas) >= 512) g.ctas *= 2;
   g.vecs = (vecs + (int)g.ctas - 1) / (int)g.ctas;
-  const unsigned most = (long long)rows * g.ctas >= 2LL * sms ? 256u : 1024u;
+  const long long all = (long long)rows * g.ctas;
+  const unsigned most = all <= sms ? 1024u : all <= 2LL * sms ? 512u : 256u;  // a CTA of 1024 threads fills an SM
   g.threads = least;
   while (g.threads < most && (int)g.threads * 2 <= g.vecs) g.threads *= 2;
   return g;
@@ -128,7 +129,10 @@ int launch_loss_bwd(const loss::Bwd &p, int dtype, int fmt, cudaStream_t s) {
     constexpr int DT = decltype(dt)::value;
     if (p.out.q || p.out.qt) {
       with_fmt(fmt, [&](auto f) {
-        rc = launch_pdl(loss::k_loss_bwd_tiles<DT, LIST, decltype(f)::value>, tile_grid(p.rows, p.cols), 512, 0, s, 1, p);
+        constexpr int OUT = decltype(f)::value, KIND = LIST ? loss::kListed : loss::kToken;
+        const auto kernel = !LIST && p.g_ent ? loss::k_loss_bwd_tiles<DT, loss::kTokenEntropy, OUT>
+                                             : loss::k_loss_bwd_tiles<DT, KIND, OUT>;
+        rc = launch_pdl(kernel, tile_grid(p.rows, p.cols), 512, 0, s, 1, p);
       });
       return;
     }
@@ -420,7 +424,9 @@ int fp8_distill_fwd(const void *logits, int dtype, int rows, int cols, size_t ld
   p.top = top, p.ids = ids, p.id_bytes = id_bytes, p.values = values, p.value_dt = value_dtype;
   p.loss = loss, p.stats = stats, p.list_ids = list_ids, p.list_q = list_q;
   const LossGrid g = loss_grid(rows, cols, dtype, sms, 256);
-  const size_t marks = form == FP8_DISTILL_TAIL ? ((size_t)g.vecs * (16 / dtype_bytes(dtype)) + 31) / 32 * 4 : 0;
+  const size_t marks = form != FP8_DISTILL_TAIL  ? 0
+                       : dtype == FP8_DT_F32     ? loss::mark_bytes<FP8_DT_F32>(g.vecs, (int)g.threads)
+                                                 : loss::mark_bytes<FP8_DT_BF16>(g.vecs, (int)g.threads);
   const size_t smem = sizeof(loss::ListScratch) + marks;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   with_dtype(dtype, [&](auto dt) {

@@ -798,7 +798,8 @@ int fp8_logprob_bwd(const void *logits, int dtype, int rows, int cols, size_t ld
  * fp8_distill_fwd also writes what the backward pass needs: stats [rows, 4]
  * (the largest logit, 1 / sum exp, and the factors of p for listed and for
  * unlisted outcomes), and the list in the order of the ids: list_ids, list_q
- * [rows, top] (absent entries last, 2^31 - 1).
+ * [rows, top] (absent entries last, 2^31 - 1; an entry that was listed before
+ * stands behind the first one, its q -1).
  *
  * fp8_distill_bwd -- from dloss [rows], the gradient of the logits as
  * fp8_logprob_bwd:  d = inv_temp * dloss * (p * factor - q).
