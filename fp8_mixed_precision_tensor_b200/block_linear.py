@@ -75,22 +75,46 @@ class BlockWeight:
             fp8.fp8_block_cast_square(weight, fp8.FP8_E4M3, self.margin, self.q, self.s, self.s_col)
 
 
-class _Cast:
-    """Row and / or column blocks of a tensor."""
+class BlockCodes:
+    """Row blocks (q, s) and / or column blocks (q_col, s_col) of a [rows, cols]
+    tensor of this dtype: what a layer takes in place of the tensor itself where
+    the pass before it (BlockNorm) writes them."""
 
-    def __init__(self, x: torch.Tensor, fmt: int, margin: int, row: bool, col: bool):
-        M, K = x.shape
-        new = lambda outer, red: (fp8.block_codes(M, K, x.device), fp8.block_scales(outer, red, x.device))  # noqa: E731
+    def __init__(self, shape, dtype: torch.dtype, device, row: bool, col: bool):
+        M, K = self.shape = tuple(shape)
+        self.dtype, self.device = dtype, device
+        new = lambda outer, red: (fp8.block_codes(M, K, device), fp8.block_scales(outer, red, device))  # noqa: E731
         self.q, self.s = new(M, K) if row else (None, None)
         self.q_col, self.s_col = new(K, M) if col else (None, None)
+
+    def record_stream(self, stream) -> None:
+        for t in (self.q, self.s, self.q_col, self.s_col):
+            if t is not None:
+                t.record_stream(stream)
+
+
+class _Cast(BlockCodes):
+    """A tensor cast to such blocks."""
+
+    def __init__(self, x: torch.Tensor, fmt: int, margin: int, row: bool, col: bool):
+        super().__init__(x.shape, x.dtype, x.device, row, col)
         fp8.fp8_block_cast(x, fmt, margin, self.q, self.s, self.q_col, self.s_col)
+
+
+def _operand(x: torch.Tensor | BlockCodes, margin: int, col: bool) -> BlockCodes:
+    """x's E4M3 row blocks, and its column blocks where a backward pass needs them."""
+    if not isinstance(x, BlockCodes):
+        return _Cast(x, fp8.FP8_E4M3, margin, True, col)
+    if x.q is None or (col and x.q_col is None):
+        raise ValueError("codes of the rows are needed, and of the columns for a backward pass")
+    return x
 
 
 class BlockLinear:
     """y = x W^T (+ bias) with block-scaled FP8 operands.
 
-    forward(x) with x [M, K] returns y in x's dtype; keep=True (training) keeps
-    x's 8-bit column blocks for backward(dy), which returns (dx, dw) (the
+    forward(x) with x [M, K] (or its BlockCodes) returns y in x's dtype;
+    keep=True (training) keeps x's 8-bit column blocks for backward(dy), which returns (dx, dw) (the
     bias's gradient is the sum of dy's rows, the caller's).  Without keep, at
     most FP8_BLOCK_TOKENS_MAX tokens take the one-launch form.
 
@@ -106,15 +130,15 @@ class BlockLinear:
         self.bias, self.grad_fmt, self.margin = bias, grad_fmt, margin
         self.kept = None
 
-    def forward(self, x: torch.Tensor, keep: bool = False, stream=None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor | BlockCodes, keep: bool = False, stream=None) -> torch.Tensor:
         with _on(stream, x):
             y = torch.empty((x.shape[0], self.N), dtype=x.dtype, device=x.device)
             w = self.weight
             w.kept.take(self.bias)
-            if not keep and x.shape[0] <= fp8.FP8_BLOCK_TOKENS_MAX:
+            if not keep and x.shape[0] <= fp8.FP8_BLOCK_TOKENS_MAX and not isinstance(x, BlockCodes):
                 fp8.fp8_block_linear_tokens(x, w.q, w.s, y, bias=self.bias, margin=self.margin)
                 return y
-            c = _Cast(x, fp8.FP8_E4M3, self.margin, True, keep)
+            c = _operand(x, self.margin, keep)
             fp8.fp8_block_linear_fwd(c.q, c.s, w.q, w.s, y, bias=self.bias)
             if keep:
                 self.kept = _Kept(c.q_col, c.s_col)
@@ -155,11 +179,11 @@ class BlockMLP:
         self.act, self.grad_fmt, self.margin = act, grad_fmt, margin
         self.kept = None
 
-    def forward(self, x: torch.Tensor, stream=None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor | BlockCodes, stream=None) -> torch.Tensor:
         with _on(stream, x):
             M, dev = x.shape[0], x.device
             self.w1.kept.take(), self.w2.kept.take()
-            c = _Cast(x, fp8.FP8_E4M3, self.margin, True, True)
+            c = _operand(x, self.margin, True)
             h = torch.empty((M, self.F), dtype=x.dtype, device=dev)
             fp8.fp8_block_linear_fwd(c.q, c.s, self.w1.q, self.w1.s, h)
             ck, ck_s = fp8.block_codes(M, self.F, dev), fp8.block_scales(M, self.F, dev)
@@ -196,3 +220,166 @@ class BlockMLP:
             fp8.fp8_block_linear_wgrad(dhq_c, dhs_c, fmt, xq, xs, dw1)
             self.kept = None
             return dx, dw1, dw2
+
+
+class BlockNorm:
+    """What stands between two sublayers: r' = res_scale r + gate u with u the
+    sublayer's output h or its norm, and x, the norm of r' for the next sublayer.
+
+    forward(h, r) returns (r', x); with codes=True x is its BlockCodes, written
+    by the norm itself, for BlockLinear, BlockMLP or BlockHead (with keep=True
+    the column blocks of their weight gradient too).  h may be None (a norm
+    alone).  keep=True keeps h, r' and each row's statistics for
+    backward(dx, dr), which returns (dh, dr, grads): dr is the gradient of r' from
+    what follows, or None, and grads has the gradient of each parameter given, in
+    its dtype, by name.
+
+    Not a torch.nn.Module, and one pass at a time, as BlockLinear."""
+
+    def __init__(self, w: torch.Tensor | None, b: torch.Tensor | None = None, pre: int = fp8.FP8_NORM_RMS,
+                 post: int = fp8.FP8_NORM_NONE, post_w: torch.Tensor | None = None, post_b: torch.Tensor | None = None,
+                 gate: torch.Tensor | None = None, res_scale: float = 1.0, eps: float = 1e-5, margin: int = 0):
+        self.params = {"w": w, "b": b, "post_w": post_w, "post_b": post_b, "gate": gate}
+        self.pre, self.post, self.res_scale, self.eps, self.margin = pre, post, float(res_scale), float(eps), margin
+        self.kept = None
+
+    def _in_use(self) -> None:
+        """The parameters on the pass's stream."""
+        now = torch.cuda.current_stream()
+        for t in self.params.values():
+            if t is not None:
+                t.record_stream(now)
+
+    def forward(self, h: torch.Tensor | None, r: torch.Tensor, codes: bool = False, keep: bool = False,
+                stream=None) -> tuple[torch.Tensor, torch.Tensor | BlockCodes]:
+        with _on(stream, *(t for t in (h, r) if t is not None)):
+            if stream is not None:
+                self._in_use()
+            M, D = r.shape
+            dtype = r.dtype if h is None else h.dtype
+            r_out = torch.empty_like(r, memory_format=torch.contiguous_format)
+            stats = torch.empty((M, 4), dtype=torch.float32, device=r.device) if keep else None
+            out = {}
+            if codes:
+                x = BlockCodes((M, D), dtype, r.device, True, keep)
+                out = {"x_q": x.q, "x_s": x.s, "x_q_col": x.q_col, "x_s_col": x.s_col}
+            else:
+                x = out["x"] = torch.empty((M, D), dtype=dtype, device=r.device)
+            fp8.fp8_norm_fwd(h, r, r_out, stats, pre=self.pre, post=self.post, res_scale=self.res_scale, eps=self.eps,
+                             margin=self.margin, **self.params, **out)
+            if keep:
+                self.kept = (h is not None, _Kept(*((h,) if h is not None else ()), r_out, stats))
+            return r_out, x
+
+    def backward(self, dx: torch.Tensor, dr: torch.Tensor | None = None,
+                 stream=None) -> tuple[torch.Tensor | None, torch.Tensor, dict[str, torch.Tensor]]:
+        if self.kept is None:
+            raise RuntimeError("backward needs a forward pass with keep=True")
+        with _on(stream, *(t for t in (dx, dr) if t is not None)):
+            if stream is not None:
+                self._in_use()
+            had, kept = self.kept
+            *h, r_out, stats = kept.take()
+            M, D = r_out.shape
+            gate = self.params["gate"]
+            need = fp8.fp8_norm_workspace_bytes(M, D, M // gate.shape[0] if gate is not None and gate.dim() == 2 and M else M)
+            work = torch.empty(need, dtype=torch.uint8, device=dx.device) if need else None
+            new = lambda like: torch.empty(like.shape, dtype=like.dtype, device=dx.device)  # noqa: E731
+            dh, dr_in = new(h[0]) if had else None, new(r_out)
+            grads = {k: new(t) for k, t in self.params.items() if t is not None}
+            given = {k: t for k, t in self.params.items() if k != "b"}
+            fp8.fp8_norm_bwd(dx, dr, h[0] if had else None, r_out, stats, pre=self.pre, post=self.post,
+                             res_scale=self.res_scale, **given, dh=dh, dr=dr_in, workspace=work,
+                             **{"d" + k: t for k, t in grads.items()})
+            self.kept = None
+            return dh, dr_in, grads
+
+
+class BlockHead:
+    """The last linear layer, logits = x W^T with W [V, K], and what is computed
+    from its logits: log probabilities of tokens, or the divergence from a
+    teacher's top logits.  The gradient of the logits is only ever written as the
+    8-bit codes that the layer's own dgrad and wgrad read.
+
+    log_probs(x, tokens) and distill(x, ids, values) take x [M, K] or its
+    BlockCodes; keep=True keeps the logits and x's column blocks for backward(g),
+    g the gradient of what was returned for each row, which returns (dx, dw) in
+    x's dtype.
+
+    Not a torch.nn.Module, and one pass at a time, as BlockLinear."""
+
+    def __init__(self, weight: torch.Tensor, grad_fmt: int = fp8.FP8_E5M2, margin: int = 0,
+                 logits_dtype: torch.dtype | None = None):
+        self.N, self.K = weight.shape
+        self.weight = BlockWeight(weight, margin)
+        self.grad_fmt, self.margin, self.logits_dtype = grad_fmt, margin, logits_dtype
+        self.kept = None
+
+    def _logits(self, x: torch.Tensor | BlockCodes, keep: bool) -> tuple[torch.Tensor, tuple]:
+        w = self.weight
+        w.kept.take()
+        logits = torch.empty((x.shape[0], self.N), dtype=self.logits_dtype or x.dtype, device=x.device)
+        if not keep and x.shape[0] <= fp8.FP8_BLOCK_TOKENS_MAX and not isinstance(x, BlockCodes):
+            fp8.fp8_block_linear_tokens(x, w.q, w.s, logits, margin=self.margin)
+            return logits, ()
+        c = _operand(x, self.margin, keep)
+        fp8.fp8_block_linear_fwd(c.q, c.s, w.q, w.s, logits)
+        return logits, (c.q_col, c.s_col)
+
+    def log_probs(self, x: torch.Tensor | BlockCodes, tokens: torch.Tensor, inv_temp: float = 1.0, entropy: bool = False,
+                  top: int = 0, keep: bool = False, stream=None) -> dict[str, torch.Tensor]:
+        """{"logp": [M]} and, where asked for, "entropy" [M], "top_logp" and "top_ids" [M, top]."""
+        with _on(stream, x, tokens):
+            logits, cols = self._logits(x, keep)
+            M, dev = logits.shape[0], logits.device
+            f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+            out = {"logp": f32(M)}
+            if entropy:
+                out["entropy"] = f32(M)
+            if top:
+                out |= {"top_logp": f32(M, top), "top_ids": torch.empty((M, top), dtype=torch.int32, device=dev)}
+            stats = f32(M, 4) if keep else None
+            more = {k: v for k, v in out.items() if k != "logp"}
+            fp8.fp8_logprob_fwd(logits, tokens, out["logp"], stats, inv_temp=float(inv_temp), **more)
+            if keep:
+                self.kept = ("entropy" if entropy else "logp", x.dtype, float(inv_temp), _Kept(*cols, logits, stats, tokens))
+            return out
+
+    def distill(self, x: torch.Tensor | BlockCodes, ids: torch.Tensor, values: torch.Tensor,
+                form: int = fp8.FP8_DISTILL_TOP, inv_temp: float = 1.0, keep: bool = False, stream=None) -> torch.Tensor:
+        """The divergence of each row, [M]."""
+        with _on(stream, x, ids, values):
+            logits, cols = self._logits(x, keep)
+            M, dev = logits.shape[0], logits.device
+            f32 = lambda *s: torch.empty(s, dtype=torch.float32, device=dev)  # noqa: E731
+            loss, stats, list_q = f32(M), f32(M, 4), f32(*ids.shape)
+            list_ids = torch.empty(ids.shape, dtype=torch.int32, device=dev)
+            fp8.fp8_distill_fwd(logits, ids, values, loss, stats, list_ids, list_q, form=form, inv_temp=float(inv_temp))
+            if keep:
+                self.kept = ("distill", x.dtype, float(inv_temp), _Kept(*cols, logits, stats, list_ids, list_q))
+            return loss
+
+    def backward(self, g: torch.Tensor, dentropy: torch.Tensor | None = None,
+                 stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+        """(dx, dw).  dentropy: the gradient of the entropies, which log_probs then computed.  Uses up what was kept."""
+        if self.kept is None:
+            raise RuntimeError("backward needs log_probs or distill with keep=True")
+        kind, dtype, inv_temp, kept = self.kept
+        if dentropy is not None and kind != "entropy":
+            raise ValueError("dentropy needs log_probs with entropy=True")
+        with _on(stream, *(t for t in (g, dentropy) if t is not None)):
+            xq, xs, logits, stats, *rest = kept.take()
+            w, fmt = self.weight, self.grad_fmt
+            w.kept.take()
+            d = BlockCodes(logits.shape, logits.dtype, logits.device, True, True)
+            out = dict(inv_temp=inv_temp, fmt=fmt, margin=self.margin, d_q=d.q, d_s=d.s, d_q_col=d.q_col, d_s_col=d.s_col)
+            if kind != "distill":
+                fp8.fp8_logprob_bwd(logits, rest[0], stats, g, dentropy=dentropy, **out)
+            else:
+                fp8.fp8_distill_bwd(logits, *rest, stats, g, **out)
+            dx = torch.empty((logits.shape[0], self.K), dtype=dtype, device=logits.device)
+            dw = torch.empty((self.N, self.K), dtype=dtype, device=logits.device)
+            fp8.fp8_block_linear_dgrad(d.q, d.s, fmt, w.q, w.s_col, dx)
+            fp8.fp8_block_linear_wgrad(d.q_col, d.s_col, fmt, xq, xs, dw)
+            self.kept = None
+            return dx, dw

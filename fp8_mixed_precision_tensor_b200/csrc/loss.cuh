@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
       }
       if (ENT && p.entropy) p.entropy[row] = ent;
       if (p.stats)
-        reinterpret_cast<float4 *>(p.stats)[row] = make_float4(all.m, none ? 0.0f : 1.0f / S, none ? 0.0f : log_S, ent);
+        reinterpret_cast<float4 *>(p.stats)[row] = make_float4(all.m, none ? 0.0f : 1.0f / S, none ? 0.0f : log_S, ENT ? ent : NAN);  // (an entropy's gradient needs one)
     }
     for (int i = threadIdx.x; i < p.top; i += blockDim.x) {
       const unsigned long long c = top.best[i];
@@ -809,7 +809,7 @@ __device__ __forceinline__ RowTerms row_terms(const Bwd &p, int row) {
     const float g = none || r.token < 0 ? 0.0f : p.beta * __ldg(p.g + row);
     const float ge = none || !p.g_ent ? 0.0f : p.beta * __ldg(p.g_ent + row);
     r.gt = g;
-    r.k0 = -(g + ge * (s.w - s.z)) * s.y;
+    r.k0 = -(p.g_ent && !none ? g + ge * (s.w - s.z) : g) * s.y;
     r.k1 = -ge * 0.69314718055994531f * s.y;
     r.kl = 0.0f;
   }

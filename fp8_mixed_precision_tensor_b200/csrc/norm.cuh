@@ -310,6 +310,13 @@ template <int CW>
 __device__ __forceinline__ void mul(float (&o)[CW], const float (&a)[CW], float s) {
   pairs(o, [&](int j) { return __fmul2_rn(pair(a, j), both(s)); });
 }
+// o = s a + b with the product rounded: on single numbers, since packed products
+// and sums are made one on the way, whatever rounding they ask for.
+template <int CW>
+__device__ __forceinline__ void scale_add(float (&o)[CW], float s, const float (&a)[CW], const float (&b)[CW]) {
+#pragma unroll
+  for (int j = 0; j < CW; j++) o[j] = __fadd_rn(__fmul_rn(s, a[j]), b[j]);
+}
 template <int CW>
 __device__ __forceinline__ void add(float (&o)[CW], const float (&a)[CW], const float (&b)[CW]) {
   pairs(o, [&](int j) { return __fadd2_rn(pair(a, j), pair(b, j)); });
@@ -719,8 +726,7 @@ __global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK == 4 ? 1 : 3) k_norm
         if (on(kH)) H.fetch(at, v);
         R.fetch(at, v);
       }
-      mul(f, f, alpha);
-      add(y[v], f, y[v]);
+      scale_add(y[v], alpha, f, y[v]);
       Ro.put(at, v, y[v], on(kRout));
       mask(at, v, y[v]);
     }

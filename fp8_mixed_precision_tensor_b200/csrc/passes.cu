@@ -107,7 +107,7 @@ LossGrid loss_grid(int rows, int cols, int dtype, int sms, unsigned least) {
   while (g.ctas < 8 && (long long)rows * g.ctas * 2 <= sms && vecs / (int)(2 * g.ctas) >= 512) g.ctas *= 2;
   g.vecs = (vecs + (int)g.ctas - 1) / (int)g.ctas;
   const long long all = (long long)rows * g.ctas;
-  const unsigned most = all <= sms ? 1024u : all <= 2LL * sms ? 512u : 256u;  // a CTA of 1024 threads fills an SM
+  const unsigned most = all <= sms ? 1024u : all <= 2LL * sms ? 512u : all <= 4LL * sms ? 256u : 128u;  // (a CTA of 1024 threads fills an SM)
   g.threads = least;
   while (g.threads < most && (int)g.threads * 2 <= g.vecs) g.threads *= 2;
   return g;
@@ -423,7 +423,7 @@ int fp8_distill_fwd(const void *logits, int dtype, int rows, int cols, size_t ld
   p.rows = rows, p.cols = cols, p.beta = inv_temp;
   p.top = top, p.ids = ids, p.id_bytes = id_bytes, p.values = values, p.value_dt = value_dtype;
   p.loss = loss, p.stats = stats, p.list_ids = list_ids, p.list_q = list_q;
-  const LossGrid g = loss_grid(rows, cols, dtype, sms, 256);
+  const LossGrid g = loss_grid(rows, cols, dtype, sms, top > 512 ? 256 : 128);
   const size_t marks = form != FP8_DISTILL_TAIL  ? 0
                        : dtype == FP8_DT_F32     ? loss::mark_bytes<FP8_DT_F32>(g.vecs, (int)g.threads)
                                                  : loss::mark_bytes<FP8_DT_BF16>(g.vecs, (int)g.threads);

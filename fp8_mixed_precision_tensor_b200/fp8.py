@@ -139,6 +139,8 @@ def _bound_calls(lib: ctypes.CDLL):
     calls.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
         "fp8_block_cast", "fp8_block_cast_square", "fp8_block_linear_fwd", "fp8_block_linear_tokens",
         "fp8_block_linear_dgrad", "fp8_block_linear_wgrad", "fp8_act_fwd", "fp8_act_bwd")))
+    calls.bind_passes(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+        "fp8_norm_fwd", "fp8_norm_bwd", "fp8_logprob_fwd", "fp8_logprob_bwd", "fp8_distill_fwd", "fp8_distill_bwd")))
     return calls
 
 
@@ -808,6 +810,9 @@ def fp8_norm_fwd(h, r, r_out, stats, *, pre: int = FP8_NORM_RMS, post: int = FP8
     scale of 1); x then gives the dtype, or else r.  gate: [cols], or [gates, cols], each
     row for rows / gates rows.  stats: [rows, 4] float32 for the backward pass,
     or None."""
+    if (_calls or _load_calls()).norm_fwd(h, r, r_out, stats, pre, post, w, b, post_w, post_b, gate, res_scale, eps, margin,
+                                          x, x_q, x_s, x_q_col, x_s_col, stream):
+        return
     rt, rows, cols, ldr, dev = _input(r, "r")
     lead = h if h is not None else x if x is not None else r
     p = _norm_params(lead, r, dev, rows, cols, pre, post, w, b, post_w, post_b, gate, res_scale, eps)
@@ -827,6 +832,9 @@ def fp8_norm_bwd(dx, dr_out, h, r_out, stats, *, pre: int = FP8_NORM_RMS, post: 
     parameters (each in its own dtype), any of them.  workspace: uint8, at least
     fp8_norm_workspace_bytes(rows, cols, rows // gates), where a parameter's
     gradient is wanted."""
+    if (_calls or _load_calls()).norm_bwd(dx, dr_out, h, r_out, stats, pre, post, w, post_w, post_b, gate, res_scale, dh, dr,
+                                          dw, db, dpost_w, dpost_b, dgate, workspace, stream):
+        return
     lead = next((t for t in (dx, dh, h) if t is not None), None)
     res = next((t for t in (r_out, dr_out, dr) if t is not None), None)
     first = lead if lead is not None else res
@@ -867,6 +875,8 @@ def fp8_logprob_fwd(logits, tokens, logp, stats, *, inv_temp: float = 1.0, entro
     largest log probabilities top_logp [rows, n] with their places top_ids
     (int32), ties to the lowest.  tokens and logp may be None.  stats: [rows, 4]
     float32 for the backward pass, or None."""
+    if (_calls or _load_calls()).logprob_fwd(logits, tokens, logp, stats, inv_temp, entropy, top_logp, top_ids, stream):
+        return
     dt, rows, cols, ld, dev = _input(logits, "logits")
     top = 0 if top_logp is None else _sides(top_logp.shape, "top_logp")[1]
     _check(load_library().fp8_logprob_fwd(
@@ -882,6 +892,9 @@ def fp8_logprob_bwd(logits, tokens, stats, dlogp, *, inv_temp: float = 1.0, dent
     may be None): codes of its 1x128 blocks (d_q, d_s) and 128x1 blocks (d_q_col,
     d_s_col), and itself in the logits' dtype (dlogits, which may be logits); any
     of them.  dentropy needs a forward pass that computed the entropy."""
+    if (_calls or _load_calls()).logprob_bwd(logits, tokens, stats, dlogp, inv_temp, dentropy, fmt, margin, d_q, d_s, d_q_col,
+                                             d_s_col, dlogits, stream):
+        return
     dt, rows, cols, ld, dev = _input(logits, "logits")
     _check(load_library().fp8_logprob_bwd(
         logits.data_ptr(), dt, rows, cols, ld, inv_temp, *_indices(tokens, "tokens", (rows,), dev),
@@ -900,6 +913,8 @@ def fp8_distill_fwd(logits, ids, values, loss, stats, list_ids, list_q, *, form:
     (FP8_DISTILL_TOP) or its log probabilities (FP8_DISTILL_TAIL, the rest one
     more outcome).  stats [rows, 4] float32, list_ids [rows, n] int32 and list_q
     [rows, n] float32 are written for the backward pass."""
+    if (_calls or _load_calls()).distill_fwd(logits, ids, values, loss, stats, list_ids, list_q, form, inv_temp, stream):
+        return
     dt, rows, cols, ld, dev = _input(logits, "logits")
     n = _sides(values.shape, "values")[1]
     vdt = _hp(values, "values")
@@ -913,6 +928,9 @@ def fp8_distill_fwd(logits, ids, values, loss, stats, list_ids, list_q, *, form:
 def fp8_distill_bwd(logits, list_ids, list_q, stats, dloss, *, inv_temp: float = 1.0, fmt: int = FP8_E5M2,
                     margin: int = 0, d_q=None, d_s=None, d_q_col=None, d_s_col=None, dlogits=None, stream=None) -> None:
     """The gradient of the logits from dloss [rows], with outputs as fp8_logprob_bwd."""
+    if (_calls or _load_calls()).distill_bwd(logits, list_ids, list_q, stats, dloss, inv_temp, fmt, margin, d_q, d_s, d_q_col,
+                                             d_s_col, dlogits, stream):
+        return
     dt, rows, cols, ld, dev = _input(logits, "logits")
     n = _sides(list_q.shape, "list_q")[1]
     _check(load_library().fp8_distill_bwd(

@@ -773,8 +773,9 @@ int fp8_logprob_fwd(const void *logits, int dtype, int rows, int cols, size_t ld
  *     d[i,j] = inv_temp * (dlogp[i] * ([j == token] - p) - dentropy[i] * p * (log p + entropy[i]))
  * in any of: d_row / d_col, codes of fmt of its 1x128 / 128x1 blocks (cast from
  * the binary32 values: the operands of dgrad / wgrad), and dlogits in dtype,
- * which may be logits (the same pointer and row stride).  stats with the
- * entropy must come from a forward call that computed it (entropy not NULL).
+ * which may be logits (the same pointer and row stride).  dentropy needs the
+ * stats of a forward call that computed the entropy (entropy not NULL); with
+ * others the gradient is NaN.
  */
 int fp8_logprob_bwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, const void *tokens,
                     int token_bytes, const float *stats, const float *dlogp, const float *dentropy, int fmt, int margin,

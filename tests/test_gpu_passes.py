@@ -149,6 +149,18 @@ def test_norm_parameters_of_other_types_and_a_strided_gate():
     assert not dgate[:, :384].any() and not dgate[:, 768:].any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("cols", [264, 1001, 4096])
+def test_norm_residual_takes_its_scale_as_written(cols, dtype):
+    """0.9f is not 0.9, but 0.9f * 10 rounds to 9: sums halfway between two 16-bit numbers go to the even one."""
+    g = rng(cols, str(dtype))
+    r = torch.randint(-2000, 2000, (50, cols), device="cuda", generator=g).to(dtype)
+    h = torch.randint(-2000, 2000, (50, cols), device="cuda", generator=g).to(dtype) / 8
+    r_out = torch.empty_like(r)
+    fp8.fp8_norm_fwd(h, r, r_out, None, pre=KIND["none"], res_scale=0.9)
+    assert torch.equal(r_out, (r.float() * 0.9 + h.float()).to(dtype))
+
+
 def test_norm_in_place():
     for dtype, res in ((BF16, BF16), (F16, F32)):
         h, r, p, dx, dr_out = norm_inputs(40, 1096, dtype, res, "rms", "rms", "channel")
