@@ -24,7 +24,7 @@ namespace fp8lib {
 namespace norm {
 
 // A row belongs to a group of threads (a multiple of 32) of a CTA; a thread holds
-// 8 CK of its columns, CK = 1, 2 or 4, as NV chunks of CW neighbouring ones: 8,
+// 8, 16 or 32 of its columns, as NV chunks of CW neighbouring ones: 8,
 // or 4 where the residual is binary32, so that a warp reads and writes whole
 // sectors of every matrix (chunks of 8 binary32 numbers in 16-byte pieces cost
 // each sector twice: 46 instead of 36 us for 4096 x 4096 forward).  A CTA takes
@@ -34,8 +34,13 @@ constexpr int kThreads = 256;      // of a CTA, but for the widest rows
 constexpr int kMostThreads = 512;
 constexpr int kMostWarps = kMostThreads / 32;
 constexpr int kStagedCols = 12288;  // the widest staged rows: 384 threads, 168 registers each
+// How wide a row is: CK = 1 and 2, so many groups of eight columns a thread in
+// CTAs of 256; 3, two of them in 512 threads (8192 columns; as four in 256
+// threads, 8 warps an SM, 2048 rows took 51 and 150 us for 41 and 96); 4, four of
+// them in up to 384 (or 512, kDirect).
+__host__ __device__ constexpr int eights(int CK) { return CK == 3 ? 2 : CK; }
 template <int CK, int MODE>
-constexpr int kCtaThreads = CK < 4 ? kThreads : MODE == 0 ? kStagedCols / 32 : kMostThreads;
+constexpr int kCtaThreads = CK < 3 ? kThreads : CK == 3 ? kMostThreads : MODE == 0 ? kStagedCols / 32 : kMostThreads;
 // Whether the parameters are in shared memory (unaligned wide rows read them each time).
 __host__ __device__ constexpr bool held(int CK, int mode) { return mode == 0 || CK == 1; }
 template <int RT>
@@ -56,10 +61,9 @@ enum { kStaged = 0, kDirect = 1 };
 // widest rows: a CTA has 256 threads, in one row or several).
 template <int CK, int CW, int MODE>
 struct Place {
-  static constexpr int NV = CK * 8 / CW;
   int cols, t;
-  __device__ __forceinline__ int width() const { return CK == 2 ? kThreads : (int)blockDim.x; }
-  __device__ __forceinline__ int lanes() const { return CK == 4 ? (int)blockDim.x : kThreads; }
+  __device__ __forceinline__ int width() const { return CK == 2 || CK == 3 ? kCtaThreads<CK, MODE> : (int)blockDim.x; }
+  __device__ __forceinline__ int lanes() const { return CK == 4 ? (int)blockDim.x : kCtaThreads<CK, MODE>; }
   __device__ __forceinline__ int col(int v, int j) const {
     return MODE == kStaged ? (v * width() + t) * CW + j : (v * width() + (t & ~31)) * CW + 32 * j + (t & 31);
   }
@@ -600,12 +604,12 @@ __host__ __device__ inline FwdSmem fwd_smem(int columns, bool h, bool w, bool b,
   return s;
 }
 
-// FULL: h, r', x in its type, both norms' w and no codes, the common call, with
-// nothing left to ask for each chunk; POST: whether there is a post norm.  Else
-// both are asked for at run time.
-template <int DT, int RT, bool FULL, bool POST, int CK, int MODE>
-__global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK == 4 ? 1 : 3) k_norm_fwd(const Fwd p) {
-  constexpr int CW = kWidth<RT>, NV = CK * 8 / CW;
+// FULL: h, r', both norms' w, and x in its type (1) or as codes of its rows (2),
+// the common calls, with little left to ask for each chunk; POST: whether there
+// is a post norm.  0: all asked for at run time.
+template <int DT, int RT, int FULL, bool POST, int CK, int MODE>
+__global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK >= 3 ? 1 : 3) k_norm_fwd(const Fwd p) {
+  constexpr int CW = kWidth<RT>, NV = eights(CK) * 8 / CW;
   constexpr bool kHeld = held(CK, MODE);
   pdl_launch_dependents();
   pdl_wait();
@@ -620,14 +624,14 @@ __global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK == 4 ? 1 : 3) k_norm
   int has = (p.h ? kH : 0) | (p.r_out ? kRout : 0) | (p.x ? kX : 0) | (p.xq ? kXq : 0) | (p.w.p ? kW : 0) | (p.b.p ? kB : 0) |
             (p.g.p || (post && p.pw.p) ? kScaled : 0) | (post && p.pb.p ? kShifted : 0) | (p.pre != FP8_NORM_NONE ? kPre : 0);
   constexpr int kKnown = FULL ? kH | kRout | kX | kXq | kW | kPre | (POST ? kScaled : kShifted) : 0;  // bits known here ...
-  constexpr int kSet = FULL ? kH | kRout | kX | kW | kPre | (POST ? kScaled : 0) : 0;                 // ... and those that are set
+  constexpr int kSet = FULL ? kH | kRout | (FULL == 1 ? kX : kXq) | kW | kPre | (POST ? kScaled : 0) : 0;  // ... and set
   auto on = [&](int bit) { return (kKnown & bit) ? (kSet & bit) != 0 : (has & bit) != 0; };
-  const FwdSmem lay = fwd_smem<DT, RT>(8 * CK * W, on(kH), on(kW), on(kB), on(kScaled), on(kShifted), MODE, kHeld);
+  const FwdSmem lay = fwd_smem<DT, RT>(8 * eights(CK) * W, on(kH), on(kW), on(kB), on(kScaled), on(kShifted), MODE, kHeld);
   uint8_t *const w_s = own + lay.w, *const b_s = own + lay.b, *const gw_s = own + lay.gw, *const gb_s = own + lay.gb;
   const unsigned stride = gridDim.x * blockDim.y;
   unsigned next = blockIdx.x * blockDim.y + threadIdx.y;
   In<RT, CK, CW, MODE> R(p.r, p.ldr, norm_smem, stride);
-  In<DT, CK, CW, MODE> H(p.h, p.ldh, norm_smem + 8 * CK * W * kBytes<RT>, stride);
+  In<DT, CK, CW, MODE> H(p.h, p.ldh, norm_smem + 8 * eights(CK) * W * kBytes<RT>, stride);
   Out<RT, CK, CW, MODE> Ro(p.r_out, p.ldro, stride);
   Out<DT, CK, CW, MODE> X(p.x, p.ldx, stride);
   R.seek(at, next), H.seek(at, next), Ro.seek(at, next), X.seek(at, next);
@@ -827,7 +831,7 @@ __global__ void __launch_bounds__(512, 2) k_norm_cols(const Cols p) {
 // so one pass over the row gives all of them in one exchange, and a second one
 // (from shared memory) writes everything.
 struct Plan {
-  int chunks, threads, groups;         // NV; of a CTA: threads of a row, rows at a time
+  int kind, threads, groups;           // CK; of a CTA: threads of a row, rows at a time
   int gate_rows, unit_rows, per_gate;  // rows of a gate row and of a unit, units per gate row
   long long units;
   int ctas;
@@ -840,8 +844,8 @@ inline int padded(int cols) { return (cols + 7) / 8 * 8; }  // of a partial sum
 inline Plan plan_of(int rows, int cols, int gate_rows) {
   Plan p = {};
   const int vecs = (cols + 7) / 8;
-  p.chunks = vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : 4;
-  p.threads = p.chunks == 2 ? kThreads : (vecs + 32 * p.chunks - 1) / (32 * p.chunks) * 32;
+  p.kind = vecs <= kThreads ? 1 : vecs <= 2 * kThreads ? 2 : vecs <= 2 * kMostThreads ? 3 : 4;
+  p.threads = p.kind == 2 ? kThreads : p.kind == 3 ? kMostThreads : (vecs + 32 * p.kind - 1) / (32 * p.kind) * 32;
   p.groups = p.threads < kThreads ? kThreads / p.threads : 1;
   p.gate_rows = gate_rows < rows ? gate_rows : rows;
   const int most = p.threads > kThreads ? kSms : 2 * kSms;
@@ -926,8 +930,8 @@ __device__ __forceinline__ void flush(float (&a)[CW], uint8_t *comb, float *out,
 // w, the common call; POST: whether there is a post norm.  Else asked for at run
 // time.
 template <int DT, int RT, bool FULL, bool POST, bool BIAS, int CK, int MODE>
-__global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK == 4 ? 1 : 2) k_norm_bwd(const Bwd p) {
-  constexpr int CW = kWidth<RT>, NV = CK * 8 / CW;
+__global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK >= 3 ? 1 : 2) k_norm_bwd(const Bwd p) {
+  constexpr int CW = kWidth<RT>, NV = eights(CK) * 8 / CW;
   constexpr bool kHeld = held(CK, MODE);
   pdl_launch_dependents();
   pdl_wait();
@@ -946,13 +950,13 @@ __global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK == 4 ? 1 : 2) k_norm
   constexpr int kKnown = FULL ? kH | kDro | kDr | kDh | kPre | kStats | (POST ? kScaled : kPostLayer) : 0;  // bits known here ...
   constexpr int kSet = FULL ? kH | kDro | kDr | kDh | kPre | kStats | (POST ? kScaled : 0) : 0;             // ... and set
   auto on = [&](int bit) { return (kKnown & bit) ? (kSet & bit) != 0 : (has & bit) != 0; };
-  const BwdSmem lay = bwd_smem<DT, RT>(8 * CK * W, on(kH), on(kDro), on(kPre), on(kScaled), blockDim.y > 1, MODE, kHeld);
+  const BwdSmem lay = bwd_smem<DT, RT>(8 * eights(CK) * W, on(kH), on(kDro), on(kPre), on(kScaled), blockDim.y > 1, MODE, kHeld);
   uint8_t *const own = norm_smem + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
   uint8_t *const w_s = own + lay.w, *const gw_s = own + lay.gw, *const comb = norm_smem + lay.comb;
   uint8_t *part = norm_smem;
   auto take = [&](bool on, int bytes) {
     uint8_t *s = part;
-    part += on ? 8 * CK * W * bytes : 0;
+    part += on ? 8 * eights(CK) * W * bytes : 0;
     return s;
   };
   const unsigned apart = blockDim.y;

@@ -63,9 +63,10 @@ bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p)
 bool whole_groups(const void *p, int dtype, size_t ld, int cols) { return !p || (wide_rows(p, dtype, ld) && cols % 8 == 0); }
 
 template <typename F>
-void with_chunks(int chunks, F f) {
-  if (chunks == 1) f(std::integral_constant<int, 1>());
-  else if (chunks == 2) f(std::integral_constant<int, 2>());
+void with_kind(int kind, F f) {
+  if (kind == 1) f(std::integral_constant<int, 1>());
+  else if (kind == 2) f(std::integral_constant<int, 2>());
+  else if (kind == 3) f(std::integral_constant<int, 3>());
   else f(std::integral_constant<int, 4>());
 }
 constexpr int kMostSmem = 232448 - 2048;  // of a CTA, beside a kernel's own 2 KB
@@ -214,17 +215,17 @@ int fp8_norm_fwd(const fp8_norm_params *p, const void *h, size_t ldh, const void
   const bool post = p->post != FP8_NORM_NONE;
   with_norm_types(p->dtype, p->res_dtype, [&](auto dt, auto rt) {
     constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-    with_chunks(plan.chunks, [&](auto ck) {
+    with_kind(plan.kind, [&](auto ck) {
       constexpr int CK = decltype(ck)::value;
       const int threads = plan.threads * plan.groups;
       auto launch = [&](auto kernel, int mode) {
-        const int columns = 8 * CK * (CK == 4 ? plan.threads : norm::kThreads);
+        const int columns = 8 * norm::eights(CK) * (CK == 4 ? plan.threads : norm::kCtaThreads<CK, norm::kStaged>);
         const int smem = norm::fwd_smem<DT, RT>(columns, h, a.w.p, a.b.p, a.g.p || (post && a.pw.p), post && a.pb.p,
                                                 mode, norm::held(CK, mode)).bytes;
         if (smem > kMostSmem) return FP8_ERR_UNSUPPORTED;
         if (int e = set_smem(kernel, smem)) return e;
-        // as many CTAs as stay resident (80 registers a thread, 168 with four chunks) share the rows out
-        const int by_regs = 65536 / (threads * (CK == 4 ? 168 : 80)), by_smem = 232448 / (smem + 2048);
+        // as many CTAs as stay resident (80 registers a thread, 128 or 168 in the widest rows) share the rows out
+        const int by_regs = 65536 / (threads * (CK == 4 ? 168 : CK == 3 ? 128 : 80)), by_smem = 232448 / (smem + 2048);
         const int resident = by_regs < by_smem ? by_regs : by_smem;
         const unsigned most = (unsigned)(sms * (resident > 1 ? resident : 1));
         const unsigned need = ((unsigned)rows + (unsigned)plan.groups - 1) / (unsigned)plan.groups;
@@ -232,13 +233,16 @@ int fp8_norm_fwd(const fp8_norm_params *p, const void *h, size_t ldh, const void
       };
       rc = FP8_ERR_UNSUPPORTED;
       if (whole && cols <= norm::kStagedCols) {
-        const bool full = h && r_out && x && !x_row && a.w.p && (!post || a.pw.p);
-        if (full && post) rc = launch(norm::k_norm_fwd<DT, RT, true, true, CK, norm::kStaged>, norm::kStaged);
-        else if (full) rc = launch(norm::k_norm_fwd<DT, RT, true, false, CK, norm::kStaged>, norm::kStaged);
-        else rc = launch(norm::k_norm_fwd<DT, RT, false, false, CK, norm::kStaged>, norm::kStaged);
+        const bool full = h && r_out && a.w.p && (!post || a.pw.p);
+        with_bool(post, [&](auto has_post) {
+          constexpr bool POST = decltype(has_post)::value;
+          if (full && x && !x_row) rc = launch(norm::k_norm_fwd<DT, RT, 1, POST, CK, norm::kStaged>, norm::kStaged);
+          else if (full && x_row && !x) rc = launch(norm::k_norm_fwd<DT, RT, 2, POST, CK, norm::kStaged>, norm::kStaged);
+          else rc = launch(norm::k_norm_fwd<DT, RT, 0, false, CK, norm::kStaged>, norm::kStaged);
+        });
       }
       if (rc == FP8_ERR_UNSUPPORTED)
-        rc = launch(norm::k_norm_fwd<DT, RT, false, false, CK == 1 ? 1 : 4, norm::kDirect>, norm::kDirect);
+        rc = launch(norm::k_norm_fwd<DT, RT, 0, false, CK == 1 ? 1 : 4, norm::kDirect>, norm::kDirect);
     });
     if (rc || !x_col) return;
     norm::Cols c = {};
@@ -308,10 +312,10 @@ int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const vo
     a.gate_rows = plan.gate_rows, a.unit_rows = plan.unit_rows, a.per_gate = plan.per_gate, a.units = plan.units;
     with_norm_types(p->dtype, p->res_dtype, [&](auto dt, auto rt) {
       constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-      with_chunks(plan.chunks, [&](auto ck) {
+      with_kind(plan.kind, [&](auto ck) {
         constexpr int CK = decltype(ck)::value;
         auto launch = [&](auto kernel, int mode) {
-          const int columns = 8 * CK * (CK == 4 ? plan.threads : norm::kThreads);
+          const int columns = 8 * norm::eights(CK) * (CK == 4 ? plan.threads : norm::kCtaThreads<CK, norm::kStaged>);
           const int smem = norm::bwd_smem<DT, RT>(columns, h, dr_out, pre, h && (a.g.p || (post && a.pw.p)),
                                                   plan.groups > 1, mode, norm::held(CK, mode)).bytes;
           if (smem > kMostSmem) return FP8_ERR_UNSUPPORTED;
@@ -322,8 +326,8 @@ int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const vo
         if (whole && cols <= norm::kStagedCols) {
           if (pre && dr_out && h && dh && dr && (!post || a.pw.p))
             with_bool(post, [&](auto has_post) {
-              with_bool(bias || CK == 4, [&](auto has_bias) {
-                constexpr bool kBias = decltype(has_bias)::value || CK == 4;
+              with_bool(bias || CK >= 3, [&](auto has_bias) {
+                constexpr bool kBias = decltype(has_bias)::value || CK >= 3;
                 rc = launch(norm::k_norm_bwd<DT, RT, true, decltype(has_post)::value, kBias, CK, norm::kStaged>, norm::kStaged);
               });
             });
