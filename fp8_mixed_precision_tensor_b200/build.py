@@ -15,7 +15,7 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libfp8.so")
-UNITS = [os.path.join(HERE, "csrc", f) for f in ("libfp8.cu", "passes.cu")]
+UNITS = [os.path.join(HERE, "csrc", f) for f in ("libfp8.cu", "passes.cu", "norm_bwd.cu")]
 CALLS = os.path.join(HERE, "_calls.so")
 CALLS_MAIN = os.path.join(HERE, "csrc", "calls.cpp")
 

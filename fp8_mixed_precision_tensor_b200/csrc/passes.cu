@@ -1,5 +1,6 @@
 // passes.cu -- the C ABI of include/fp8.h's passes between and behind the linear
-// layers: norms with gate and residual, log probabilities, distillation.
+// layers: norms with gate and residual (their backward pass: norm_bwd.cu), log
+// probabilities, distillation.
 //
 // A translation unit of its own, compiled beside libfp8.cu.  Its copies of what
 // the shared headers define (kernels, the device status word) have names of
@@ -17,6 +18,7 @@
 #include "host.cuh"
 #include "loss.cuh"
 #include "norm.cuh"
+#include "norm_host.cuh"
 
 using namespace fp8lib;
 
@@ -33,54 +35,6 @@ int sm_count(int *out) {
   *out = sms[dev];
   return FP8_OK;
 }
-
-// A vector of parameters, or a matrix with cols elements a row: FP8_OK, or what is wrong with it.
-int check_vector(const fp8_vector &v) {
-  if (!v.p) return FP8_OK;
-  if (!valid_dtype(v.dtype)) return FP8_ERR_INVALID_ARG;
-  return reinterpret_cast<uintptr_t>(v.p) % dtype_bytes(v.dtype) ? FP8_ERR_UNALIGNED : FP8_OK;
-}
-norm::Vec vec_of(const fp8_vector &v) { return {v.p, v.dtype}; }
-
-bool norm_kind(int k) { return k == FP8_NORM_NONE || k == FP8_NORM_RMS || k == FP8_NORM_LAYER; }
-
-int check_norm(const fp8_norm_params *p, bool h) {
-  if (!p || !valid_dtype(p->dtype) || (p->res_dtype != p->dtype && p->res_dtype != FP8_DT_F32) || p->rows < 0 ||
-      p->cols < 0 || !norm_kind(p->pre) || !norm_kind(p->post) || !(p->eps >= 0.0f) || !isfinite(p->eps) ||
-      !isfinite(p->res_scale) || (!h && p->rows && (p->post != FP8_NORM_NONE || p->gate.p)))
-    return FP8_ERR_INVALID_ARG;
-  int rc;
-  for (const fp8_vector *v : {&p->w, &p->b, &p->post_w, &p->post_b, &p->gate})
-    if ((rc = check_vector(*v))) return rc;
-  if (p->gate.p && (p->gate_rows < 1 || p->ld_gate < (size_t)p->cols)) return FP8_ERR_INVALID_ARG;
-  if (p->cols > FP8_NORM_COLS_MAX || too_long(p->rows, p->cols)) return FP8_ERR_UNSUPPORTED;
-  return FP8_OK;
-}
-
-bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-// Whether a matrix, where there is one, is read and written in whole groups of eight.
-bool whole_groups(const void *p, int dtype, size_t ld, int cols) { return !p || (wide_rows(p, dtype, ld) && cols % 8 == 0); }
-
-template <typename F>
-void with_kind(int kind, F f) {
-  if (kind == 1) f(std::integral_constant<int, 1>());
-  else if (kind == 2) f(std::integral_constant<int, 2>());
-  else if (kind == 3) f(std::integral_constant<int, 3>());
-  else f(std::integral_constant<int, 4>());
-}
-constexpr int kMostSmem = 232448 - 2048;  // of a CTA, beside a kernel's own 2 KB
-
-template <typename F>
-void with_norm_types(int dt, int rt, F f) {
-  with_dtype(dt, [&](auto d) {
-    constexpr int DT = decltype(d)::value;
-    if (rt == dt) f(d, d);
-    else if constexpr (DT != FP8_DT_F32) f(d, std::integral_constant<int, FP8_DT_F32>());
-  });
-}
-
-int gate_rows_of(const fp8_norm_params *p) { return p->gate.p && p->gate_rows < p->rows ? p->gate_rows : p->rows; }
 
 struct LossArgs {
   const void *logits;
@@ -255,104 +209,6 @@ int fp8_norm_fwd(const fp8_norm_params *p, const void *h, size_t ldh, const void
     rc = launch_pdl(norm::k_norm_cols<RT>, tile_grid(rows, cols), 512, 0, s, 1, c);
   });
   return rc;
-}
-
-size_t fp8_norm_workspace_bytes(int rows, int cols, int gate_rows) {
-  if (rows <= 0 || cols <= 0 || cols > FP8_NORM_COLS_MAX || gate_rows <= 0) return 0;
-  const norm::Plan plan = norm::plan_of(rows, cols, gate_rows);
-  return ((size_t)plan.ctas + (size_t)plan.units) * 2 * (size_t)norm::padded(cols) * sizeof(float);
-}
-
-int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const void *dr_out, size_t lddr_out,
-                 const void *h, size_t ldh, const void *r_out, size_t ldr_out, const float *stats, void *dh,
-                 size_t lddh, void *dr, size_t lddr, const fp8_norm_grads *grads, void *workspace, size_t ws_bytes,
-                 void *stream) {
-  int rc = check_norm(p, h != nullptr);
-  if (rc) return rc;
-  const fp8_norm_grads none = {};
-  const fp8_norm_grads &g = grads ? *grads : none;
-  for (const fp8_vector *v : {&g.w, &g.b, &g.post_w, &g.post_b, &g.gate})
-    if ((rc = check_vector(*v))) return rc;
-  const int rows = p->rows, cols = p->cols;
-  const bool pre = p->pre != FP8_NORM_NONE, post = p->post != FP8_NORM_NONE;
-  const bool of_pre = g.w.p || g.b.p, of_post = g.post_w.p || g.post_b.p || g.gate.p;
-  // (matrices without rows have no address)
-  if ((rows && (pre != (dx != nullptr) || (!h && (dh || of_post)) || (!dh && !dr && !of_pre && !of_post))) ||
-      (!pre && of_pre) || (!post && (g.post_w.p || g.post_b.p)) || (g.gate.p && !p->gate.p) ||
-      (g.gate.p && g.ld_gate < (size_t)cols))
-    return FP8_ERR_INVALID_ARG;
-  if (cols == 0) return FP8_OK;
-  if (rows && ((pre && ((rc = check_matrix(dx, p->dtype, cols, lddx)) || (rc = check_matrix(r_out, p->res_dtype, cols, ldr_out)))) ||
-               (dr_out && (rc = check_matrix(dr_out, p->res_dtype, cols, lddr_out))) ||
-               (h && (rc = check_matrix(h, p->dtype, cols, ldh))) || (dh && (rc = check_matrix(dh, p->dtype, cols, lddh))) ||
-               (dr && (rc = check_matrix(dr, p->res_dtype, cols, lddr)))))
-    return rc;
-  if (rows && (pre || post) && !stats) return FP8_ERR_INVALID_ARG;
-  if (!aligned16(stats) || !aligned16(workspace)) return FP8_ERR_UNALIGNED;
-  const norm::Plan plan = norm::plan_of(rows, cols, gate_rows_of(p));
-  const bool sums = of_pre || of_post;
-  const bool bias = g.b.p || g.post_b.p || (g.gate.p && post && p->post_b.p);  // plain sums of dx or G
-  if (sums && rows && (!workspace || ws_bytes < fp8_norm_workspace_bytes(rows, cols, gate_rows_of(p))))
-    return FP8_ERR_INVALID_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  norm::Bwd a = {};
-  float *ws = static_cast<float *>(workspace);
-  if (rows) {
-    a.dx = dx, a.dro = dr_out, a.h = h, a.ro = r_out, a.stats = stats, a.dh = dh, a.dr = dr;
-    a.lddx = lddx, a.lddro = lddr_out, a.ldh = ldh, a.ldro = ldr_out, a.lddh = lddh, a.lddr = lddr;
-    a.rows = rows, a.cols = cols, a.pre = p->pre, a.post = p->post;
-    a.w = vec_of(p->w), a.pw = vec_of(p->post_w), a.g = vec_of(p->gate);
-    a.ldg = p->ld_gate;
-    a.alpha = p->res_scale;
-    const bool whole = whole_groups(dx, p->dtype, lddx, cols) && whole_groups(dr_out, p->res_dtype, lddr_out, cols) &&
-                       whole_groups(h, p->dtype, ldh, cols) && whole_groups(pre ? r_out : nullptr, p->res_dtype, ldr_out, cols) &&
-                       whole_groups(dh, p->dtype, lddh, cols) && whole_groups(dr, p->res_dtype, lddr, cols);
-    a.ef = of_pre ? ws : nullptr;
-    a.ac = of_post ? ws + (size_t)plan.ctas * 2 * norm::padded(cols) : nullptr;
-    a.gate_rows = plan.gate_rows, a.unit_rows = plan.unit_rows, a.per_gate = plan.per_gate, a.units = plan.units;
-    with_norm_types(p->dtype, p->res_dtype, [&](auto dt, auto rt) {
-      constexpr int DT = decltype(dt)::value, RT = decltype(rt)::value;
-      with_kind(plan.kind, [&](auto ck) {
-        constexpr int CK = decltype(ck)::value;
-        auto launch = [&](auto kernel, int mode) {
-          const int columns = 8 * norm::eights(CK) * (CK == 4 ? plan.threads : norm::kCtaThreads<CK, norm::kStaged>);
-          const int smem = norm::bwd_smem<DT, RT>(columns, h, dr_out, pre, h && (a.g.p || (post && a.pw.p)),
-                                                  plan.groups > 1, mode, norm::held(CK, mode)).bytes;
-          if (smem > kMostSmem) return FP8_ERR_UNSUPPORTED;
-          if (int e = set_smem(kernel, smem)) return e;
-          return launch_pdl(kernel, (unsigned)plan.ctas, dim3(plan.threads, plan.groups), smem, s, 1, a);
-        };
-        rc = FP8_ERR_UNSUPPORTED;
-        if (whole && cols <= norm::kStagedCols) {
-          if (pre && dr_out && h && dh && dr && (!post || a.pw.p))
-            with_bool(post, [&](auto has_post) {
-              with_bool(bias || CK >= 3, [&](auto has_bias) {
-                constexpr bool kBias = decltype(has_bias)::value || CK >= 3;
-                rc = launch(norm::k_norm_bwd<DT, RT, true, decltype(has_post)::value, kBias, CK, norm::kStaged>, norm::kStaged);
-              });
-            });
-          else
-            rc = launch(norm::k_norm_bwd<DT, RT, false, false, true, CK, norm::kStaged>, norm::kStaged);
-        }
-        if (rc == FP8_ERR_UNSUPPORTED)
-          rc = launch(norm::k_norm_bwd<DT, RT, false, false, true, CK == 1 ? 1 : 4, norm::kDirect>, norm::kDirect);
-      });
-    });
-    if (rc) return rc;
-  }
-  if (!sums) return FP8_OK;
-  norm::Params q = {};
-  q.ef = ws, q.ac = ws + (size_t)plan.ctas * 2 * norm::padded(cols);
-  q.cols = cols, q.ctas = plan.ctas, q.per_gate = rows ? plan.per_gate : 1;
-  q.post = post, q.bias = bias;
-  q.gates = rows ? (int)(plan.units / plan.per_gate) : 0;
-  q.pw = vec_of(p->post_w), q.pb = vec_of(p->post_b), q.g = vec_of(p->gate), q.ldg = p->ld_gate;
-  q.dw = vec_of(g.w), q.db = vec_of(g.b), q.dpw = vec_of(g.post_w), q.dpb = vec_of(g.post_b), q.dg = vec_of(g.gate);
-  q.lddg = g.ld_gate;
-  q.col_blocks = (cols + 31) / 32;
-  const long long jobs = 2 + (g.gate.p ? (long long)q.gates : 0);
-  if (jobs * q.col_blocks > INT_MAX) return FP8_ERR_UNSUPPORTED;
-  return launch_pdl(norm::k_norm_params, (unsigned)(jobs * q.col_blocks), dim3(32, norm::kParamLanes), 0, s, 1, q);
 }
 
 int fp8_logprob_fwd(const void *logits, int dtype, int rows, int cols, size_t ld, float inv_temp, const void *tokens,

@@ -668,8 +668,8 @@ int fp8_act_bwd(const fp8_blocks *ckpt, const void *da, int dtype, int rows, int
  * The passes between and behind the linear layers.  Matrices, codes and scales
  * as above; float32 outputs and statistics are contiguous.  Outputs must not
  * overlap inputs or one another, except where a call names it.  Every sum and
- * statistic is taken in binary32 in an order that depends on the sizes only:
- * the same inputs give the same bits.
+ * statistic is taken in binary32 in an order that depends on sizes, pitches and
+ * alignment only: the same call on the same inputs gives the same bits.
  *
  * A vector of parameters: `p` dev, contiguous elements of `dtype`, or NULL.
  */
