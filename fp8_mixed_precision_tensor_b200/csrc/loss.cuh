@@ -551,6 +551,10 @@ __device__ __forceinline__ Part join_block(const Running<MODE, ENT> &s, float c2
   return p;
 }
 
+// One row a CTA (128 threads where there are many rows: 4096 x 50304 bfloat16 77
+// us in CTAs of 256, 73 so, 5.7 TB/s; with the entropy 80, lists of 64: 88, in
+// the tail form 95), or a cluster's where there are few (one row of 50304 4.2
+// us, with 20 alternatives 10).  Bound by the exponential unit beside HBM.
 template <int DT, int MODE, bool ENT>
 __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
   pdl_launch_dependents();
@@ -819,6 +823,8 @@ __device__ __forceinline__ RowTerms row_terms(const Bwd &p, int row) {
 __device__ __forceinline__ float scaled(float z, float m, float c2) { return max_nan((z - m) * c2, -1000.0f); }
 
 // d itself: one row's chunk a CTA, in 16-byte vectors wherever the row starts.
+// HBM-bound: 4096 x 50304 bfloat16 120 us (6.9 TB/s; rows of 50257 the same;
+// with lists of 64 139, their entries written behind the rest).
 constexpr int kBwdThreads = 256;
 constexpr int kBwdVecs = 4;  // vectors of a thread
 template <int DT, bool LIST>
@@ -912,7 +918,10 @@ __global__ void __launch_bounds__(kBwdThreads) k_loss_bwd_rows(const Bwd p, unsi
 // Codes of d, and d itself where wanted: tiles of block_scale.cuh.  The 16 lanes
 // of a tile's row share RP rows: lane i works out the i-th one's factors (and
 // which of the tile's columns are listed) while the tile's loads are in flight,
-// and passes them on by shuffles; no barrier before the column maxima.
+// and passes them on by shuffles; no barrier before the column maxima.  4096 x
+// 50304 bfloat16 210 us (3.9 TB/s of logits read and codes written), with lists
+// 311, 2048 x 50304 float32 115; half of the issue slots busy, two CTAs of 16
+// warps an SM between two barriers.
 enum { kToken = 0, kTokenEntropy = 1, kListed = 2 };
 
 template <int DT, int KIND, int OUT>

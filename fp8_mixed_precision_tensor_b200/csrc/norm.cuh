@@ -27,7 +27,7 @@ namespace norm {
 // 8, 16 or 32 of its columns, as NV chunks of CW neighbouring ones: 8,
 // or 4 where the residual is binary32, so that a warp reads and writes whole
 // sectors of every matrix (chunks of 8 binary32 numbers in 16-byte pieces cost
-// each sector twice: 46 instead of 36 us for 4096 x 4096 forward).  A CTA takes
+// each sector twice: 46 instead of 40 us for 4096 x 4096 forward).  A CTA takes
 // as many narrow rows at a time as it has threads for, and row after row while
 // it lives.
 constexpr int kThreads = 256;      // of a CTA, but for the widest rows
@@ -36,7 +36,7 @@ constexpr int kMostWarps = kMostThreads / 32;
 constexpr int kStagedCols = 12288;  // the widest staged rows: 384 threads, 168 registers each
 // How wide a row is: CK = 1 and 2, so many groups of eight columns a thread in
 // CTAs of 256; 3, two of them in 512 threads (8192 columns; as four in 256
-// threads, 8 warps an SM, 2048 rows took 51 and 150 us for 41 and 96); 4, four of
+// threads, 8 warps an SM, 2048 rows took 51 and 150 us for 47 and 91); 4, four of
 // them in up to 384 (or 512, kDirect).
 __host__ __device__ constexpr int eights(int CK) { return CK == 3 ? 2 : CK; }
 template <int CK, int MODE>
@@ -604,6 +604,13 @@ __host__ __device__ inline FwdSmem fwd_smem(int columns, bool h, bool w, bool b,
   return s;
 }
 
+// One pass: h and r read, r' and x written.  A row's chunks stay in registers
+// between its exchanges; the next row's are on their way into shared memory.
+// 8192 x 12288 bfloat16, layer norm 128 us (6.3 TB/s; codes of the rows 187);
+// 4096 x 4096 bfloat16 22 (6.0), with a float32 residual, both norms and a gate
+// 40 (5.1), there bound by the latency of copies, shared memory and shuffles at
+// 24 warps an SM (47 % of the issue slots busy); one token 3.1.
+//
 // FULL: h, r', both norms' w, and x in its type (1) or as codes of its rows (2),
 // the common calls, with little left to ask for each chunk; POST: whether there
 // is a post norm.  0: all asked for at run time.
@@ -774,7 +781,9 @@ __global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK >= 3 ? 1 : 3) k_norm
 }
 
 // x again from r' and its statistics, as codes of 128x1 blocks: tiles of
-// block_scale.cuh.  2 B (or 4) read and 1 written per element.
+// block_scale.cuh.  2 B (or 4) read and 1 written per element: 8192 x 12288
+// bfloat16 86 us (3.5 TB/s), 4096 x 4096 16; as k_block_cast two barriers a tile,
+// which two CTAs of 16 warps hide in part.
 struct Cols {
   const void *r;
   size_t ldr;
@@ -925,6 +934,12 @@ __device__ __forceinline__ void flush(float (&a)[CW], uint8_t *comb, float *out,
   for (int j = 0; j < CW; j++) a[j] = 0.0f;
 }
 
+// dx, dr', r' and h read, dr and dh written: 8192 x 12288 bfloat16 278 us without
+// the parameters' gradients (4.4 TB/s) and 286 with, 4096 x 4096 with a float32
+// residual and both norms 59 and 68 (5.1 TB/s).  Bound by the copies of one row
+// in flight beside 12 to 16 warps: the sums over rows take the registers, and the
+// staged row with the parameters the shared memory, that a second row would need.
+//
 // BIAS: whether sums of dx and of G are wanted (gradients of b, of post_b, and
 // of a gate behind post_b).  FULL: dx, dr', h, both outputs and the post norm's
 // w, the common call; POST: whether there is a post norm.  Else asked for at run
@@ -1212,7 +1227,8 @@ constexpr int kParamLanes = 32;
 
 // The parameters' gradients from the partial sums: a CTA takes 32 columns of
 // one job (the pre norm's, the post norm's, or one gate row's), its lanes
-// (threadIdx.y) every 32nd partial sum.
+// (threadIdx.y) every 32nd partial sum.  Two or three microseconds behind the
+// kernel above, and 4 to 8 in all with the sums' stores and loads.
 __global__ void __launch_bounds__(32 * kParamLanes) k_norm_params(const Params p) {
   pdl_launch_dependents();
   pdl_wait();
