@@ -403,6 +403,7 @@ PyObject *norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g.post_w = vector_of(a[16], s.cols, call), g.post_b = vector_of(a[17], s.cols, call);
     int gate_rows;
     g.gate = gate_of(a[18], s, call, gate_rows, g.ld_gate);
+    if (g.gate.p) g.gates = tensor(a[18]).dim() == 1 ? 1 : (int)tensor(a[18]).size(0);
     need(!g.gate.p || (p.gate.p && tensor(a[18]).sizes() == tensor(a[10]).sizes()));
     void *ws = nullptr;
     size_t bytes = 0;

@@ -38,7 +38,7 @@ int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const vo
   // (matrices without rows have no address)
   if ((rows && (pre != (dx != nullptr) || (!h && (dh || of_post)) || (!dh && !dr && !of_pre && !of_post))) ||
       (!pre && of_pre) || (!post && (g.post_w.p || g.post_b.p)) || (g.gate.p && !p->gate.p) ||
-      (g.gate.p && g.ld_gate < (size_t)cols))
+      (g.gate.p && (g.ld_gate < (size_t)cols || g.gates < 0)))
     return FP8_ERR_INVALID_ARG;
   if (cols == 0) return FP8_OK;
   if (rows && ((pre && ((rc = check_matrix(dx, p->dtype, cols, lddx)) || (rc = check_matrix(r_out, p->res_dtype, cols, ldr_out)))) ||
@@ -102,9 +102,9 @@ int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const vo
   if (!sums) return FP8_OK;
   norm::Params q = {};
   q.ef = ws, q.ac = ws + (size_t)plan.ctas * 2 * norm::padded(cols);
-  q.cols = cols, q.ctas = plan.ctas, q.per_gate = rows ? plan.per_gate : 1;
+  q.cols = cols, q.ctas = plan.ctas, q.per_gate = plan.per_gate;
   q.post = post, q.bias = bias;
-  q.gates = rows ? (int)(plan.units / plan.per_gate) : 0;
+  q.gates = rows ? (int)(plan.units / plan.per_gate) : g.gates > 1 ? g.gates : 1;  // (no rows: no partial sums, 0 each)
   q.pw = vec_of(p->post_w), q.pb = vec_of(p->post_b), q.g = vec_of(p->gate), q.ldg = p->ld_gate;
   q.dw = vec_of(g.w), q.db = vec_of(g.b), q.dpw = vec_of(g.post_w), q.dpb = vec_of(g.post_b), q.dg = vec_of(g.gate);
   q.lddg = g.ld_gate;

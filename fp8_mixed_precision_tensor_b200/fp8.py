@@ -97,7 +97,7 @@ class _NormParams(ctypes.Structure):
 
 class _NormGrads(ctypes.Structure):
     _fields_ = [("w", _Vec), ("b", _Vec), ("post_w", _Vec), ("post_b", _Vec), ("gate", _Vec),
-                ("ld_gate", ctypes.c_size_t)]
+                ("ld_gate", ctypes.c_size_t), ("gates", ctypes.c_int)]
 
 
 class _HParams(ctypes.Structure):
@@ -831,7 +831,7 @@ def fp8_norm_bwd(dx, dr_out, h, r_out, stats, *, pre: int = FP8_NORM_RMS, post: 
     (the gradient of r_out from what follows, or None): dh, dr and those of the
     parameters (each in its own dtype), any of them.  workspace: uint8, at least
     fp8_norm_workspace_bytes(rows, cols, rows // gates), where a parameter's
-    gradient is wanted."""
+    gradient is wanted.  No rows: parameters' gradients of 0."""
     if (_calls or _load_calls()).norm_bwd(dx, dr_out, h, r_out, stats, pre, post, w, post_w, post_b, gate, res_scale, dh, dr,
                                           dw, db, dpost_w, dpost_b, dgate, workspace, stream):
         return
@@ -847,7 +847,7 @@ def fp8_norm_bwd(dx, dr_out, h, r_out, stats, *, pre: int = FP8_NORM_RMS, post: 
     if dgate is not None and (gate is None or dgate.shape != gate.shape):
         raise ValueError("dgate has gate's shape")
     grads = _NormGrads(_vec(dw, "dw", cols, dev), _vec(db, "db", cols, dev), _vec(dpost_w, "dpost_w", cols, dev),
-                       _vec(dpost_b, "dpost_b", cols, dev), g, ldg)
+                       _vec(dpost_b, "dpost_b", cols, dev), g, ldg, 1 if dgate is None or dgate.dim() == 1 else dgate.shape[0])
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         raise ValueError(f"workspace: contiguous memory on cuda:{dev} expected")
     ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())

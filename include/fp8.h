@@ -724,10 +724,12 @@ int fp8_norm_fwd(const fp8_norm_params *p, const void *h, size_t ldh, const void
 
 /* Gradients of the parameters: sums over the rows (over each gate row's rows
  * for gate, `gate` rows ld_gate elements apart), each in its own type; NULL
- * where not wanted. */
+ * where not wanted.  gates: how many rows `gate` has, read only where there are
+ * no rows to tell (0 counts as 1). */
 typedef struct {
   fp8_vector w, b, post_w, post_b, gate;
   size_t ld_gate;
+  int gates;
 } fp8_norm_grads;
 
 /*
@@ -739,7 +741,7 @@ typedef struct {
  * fp8_norm_workspace_bytes(rows, cols, gate_rows) bytes, contents of no
  * meaning before and after (needed where a parameter's gradient is wanted);
  * calls whose work overlaps on the GPU need one each.  rows == 0 gives
- * gradients of 0 for the parameters.
+ * gradients of 0 for the parameters, the grads' `gates` rows of gate among them.
  */
 size_t fp8_norm_workspace_bytes(int rows, int cols, int gate_rows);
 int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const void *dr_out, size_t lddr_out,
