@@ -73,7 +73,8 @@ int launch_loss_fwd(const loss::Fwd &p, const LossGrid &g, size_t smem, cudaStre
   const auto kernel = loss::k_loss_fwd<DT, MODE, ENT>;
   if ((long long)p.rows * g.ctas > INT_MAX) return FP8_ERR_UNSUPPORTED;
   int rc;
-  if (smem > 48 * 1024 && (rc = set_smem(kernel, (int)smem))) return rc;
+  // (what a launch has unasked, 48 KB, holds the kernel's own shared memory too)
+  if (smem > 48 * 1024 - kOwnSmem && (rc = set_smem(kernel, (int)smem))) return rc;
   return launch_pdl(kernel, (unsigned)p.rows * g.ctas, g.threads, smem, s, g.ctas, p, g.ctas);
 }
 

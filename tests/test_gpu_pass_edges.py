@@ -4,7 +4,8 @@ import torch
 
 from fp8_mixed_precision_tensor_b200 import fp8
 from fp8_mixed_precision_tensor_b200.block_linear import BlockNorm
-from test_gpu_passes import BF16, F32, GUARD, KIND, Strided
+from test_gpu_passes import BF16, F16, F32, GUARD, KIND, Strided, normal, rng, run_distill
+
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +50,14 @@ def test_a_norm_that_got_no_tokens(shape):
     dh, dr, grads = norm.backward(h, h)
     assert dh.shape == dr.shape == (0, 64) and grads["gate"].shape == shape
     assert all(not g.any() for g in grads.values())
+
+
+@pytest.mark.parametrize("cols", [300000, 327680])
+def test_a_tail_whose_marks_end_just_below_48_kb(cols):
+    """8 KB for the list and 40 for the marks, beside what the kernel has of its own."""
+    g = rng("marks", cols)
+    z = Strided(75, cols, F16, values=normal(g, 75, cols, std=2.0))
+    ids = torch.stack([torch.randperm(cols, device="cuda", generator=g)[:16] for _ in range(75)])
+    values = torch.log_softmax(normal(g, 75, 17), 1)[:, :16].contiguous()
+    run_distill(z, ids, values, g, "tail", 1.0)
+    assert fp8.fp8_get_status() == 0
