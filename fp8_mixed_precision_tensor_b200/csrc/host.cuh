@@ -22,6 +22,16 @@ int set_smem(K kernel, int bytes) {
   return cuda_rc(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
 }
 
+constexpr int kOwnSmem = 2048;                // of a pass's kernel beside what a launch gives it, at the most
+constexpr int kMostSmem = 232448 - kOwnSmem;  // of a launch
+// Lets a kernel's launches take up to kMostSmem.  The limit is the kernel's, not
+// a launch's: set to what one call needs it would refuse another thread's call
+// between that one's setting and its launch.
+template <typename K>
+int allow_smem(K kernel) {
+  return set_smem(kernel, kMostSmem);
+}
+
 bool valid_dtype(int dt) { return dt == FP8_DT_F32 || dt == FP8_DT_BF16 || dt == FP8_DT_F16; }
 
 size_t dtype_bytes(int dt) { return dt == FP8_DT_F32 ? 4 : 2; }

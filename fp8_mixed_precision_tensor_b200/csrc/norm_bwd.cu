@@ -78,7 +78,7 @@ int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const vo
           const int smem = norm::bwd_smem<DT, RT>(columns, h, dr_out, pre, h && (a.g.p || (post && a.pw.p)),
                                                   plan.groups > 1, mode, norm::held(CK, mode)).bytes;
           if (smem > kMostSmem) return FP8_ERR_UNSUPPORTED;
-          if (int e = set_smem(kernel, smem)) return e;
+          if (int e = allow_smem(kernel)) return e;
           return launch_pdl(kernel, (unsigned)plan.ctas, dim3(plan.threads, plan.groups), smem, s, 1, a);
         };
         rc = FP8_ERR_UNSUPPORTED;

@@ -45,8 +45,6 @@ void with_kind(int kind, F f) {
   else if (kind == 3) f(std::integral_constant<int, 3>());
   else f(std::integral_constant<int, 4>());
 }
-constexpr int kOwnSmem = 2048;               // of a kernel beside what a launch gives it, at the most
-constexpr int kMostSmem = 232448 - kOwnSmem;  // of a launch
 
 template <typename F>
 void with_norm_types(int dt, int rt, F f) {

@@ -74,7 +74,7 @@ int launch_loss_fwd(const loss::Fwd &p, const LossGrid &g, size_t smem, cudaStre
   if ((long long)p.rows * g.ctas > INT_MAX) return FP8_ERR_UNSUPPORTED;
   int rc;
   // (what a launch has unasked, 48 KB, holds the kernel's own shared memory too)
-  if (smem > 48 * 1024 - kOwnSmem && (rc = set_smem(kernel, (int)smem))) return rc;
+  if (smem > 48 * 1024 - kOwnSmem && (rc = allow_smem(kernel))) return rc;
   return launch_pdl(kernel, (unsigned)p.rows * g.ctas, g.threads, smem, s, g.ctas, p, g.ctas);
 }
 
@@ -178,7 +178,7 @@ int fp8_norm_fwd(const fp8_norm_params *p, const void *h, size_t ldh, const void
         const int smem = norm::fwd_smem<DT, RT>(columns, h, a.w.p, a.b.p, a.g.p || (post && a.pw.p), post && a.pb.p,
                                                 mode, norm::held(CK, mode)).bytes;
         if (smem > kMostSmem) return FP8_ERR_UNSUPPORTED;
-        if (int e = set_smem(kernel, smem)) return e;
+        if (int e = allow_smem(kernel)) return e;
         // as many CTAs as stay resident (80 registers a thread, 128 or 168 in the widest rows) share the rows out
         const int by_regs = 65536 / (threads * (CK == 4 ? 168 : CK == 3 ? 128 : 80)), by_smem = 232448 / (smem + 2048);
         const int resident = by_regs < by_smem ? by_regs : by_smem;
