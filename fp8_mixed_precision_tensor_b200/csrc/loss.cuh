@@ -604,6 +604,14 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
     __syncthreads();
     // an entry's place by id is the number of entries that come before it; the same id earlier in the list: listed again
     float v_max = kNone, q_sum = 0.0f;
+    int dropped = 0;  // whether one of the thread's entries is listed again
+    auto larger = [&](int j) {
+      const float4 v = reinterpret_cast<const float4 *>(list.v)[j];
+      v_max = max_nan(max_nan(max_nan(max_nan(v_max, v.x), v.y), v.z), v.w);
+    };
+    auto to_group = [&] {
+      for (int b = G / 2; b > 0; b /= 2) v_max = max_nan(v_max, __shfl_xor_sync(0xffffffffu, v_max, b));
+    };
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int k = first + i * apart;
@@ -622,17 +630,13 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
           again += same;
           before += (e[n] < id) + same;
         }
-        if (MODE == kListTop && i == 0) {
-          const float4 v = reinterpret_cast<const float4 *>(list.v)[j];
-          v_max = max_nan(max_nan(max_nan(max_nan(v_max, v.x), v.y), v.z), v.w);
-        }
+        if (MODE == kListTop && i == 0) larger(j);
       }
       for (int b = G / 2; b > 0; b /= 2) {
         before += __shfl_xor_sync(0xffffffffu, before, b);
         again += __shfl_xor_sync(0xffffffffu, again, b);
-        if (MODE == kListTop && i == 0) v_max = max_nan(v_max, __shfl_xor_sync(0xffffffffu, v_max, b));
       }
-      if (MODE == kListTop) top_value = v_max;
+      if (MODE == kListTop && i == 0) to_group();
       if (!lead || k >= K) continue;
       mine_at[i] = before;
       mine_id[i] = id;
@@ -640,11 +644,14 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
       if (id == kAbsent) continue;
       if (again) {
         mine_q[i] = -1.0f;  // stands behind the first one and counts for nothing
+        dropped = 1;
         continue;
       }
       mine_v[i] = list.v[k];
-      mine_q[i] = expf(MODE == kListTop ? (mine_v[i] - top_value) * p.beta : mine_v[i]);
-      q_sum += mine_q[i];
+      if (MODE == kListTail) {
+        mine_q[i] = expf(mine_v[i]);
+        q_sum += mine_q[i];
+      }
       if (MODE == kListTail) {
         const int e = id - r.s.head, body = r.s.vecs * kElems<DT>;
         if (e >= 0 && e < body) {
@@ -655,6 +662,24 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
         } else {
           atomicOr(&edge_bits, 1u << (e < 0 ? id : 16 + e - body));
         }
+      }
+    }
+    if constexpr (MODE == kListTop) {
+      if (__syncthreads_or(dropped)) {  // rare: the largest value among those that count
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (mine_id[i] != kAbsent && mine_q[i] < 0.0f) list.v[first + i * apart] = -INFINITY;
+        __syncthreads();
+        v_max = kNone;
+        for (int j = threadIdx.x % G; j < K4; j += G) larger(j);
+        to_group();
+      }
+      top_value = v_max;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if (mine_id[i] == kAbsent || mine_q[i] < 0.0f) continue;
+        mine_q[i] = expf((mine_v[i] - top_value) * p.beta);
+        q_sum += mine_q[i];
       }
     }
 #pragma unroll

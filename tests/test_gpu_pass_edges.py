@@ -139,3 +139,22 @@ def test_tails_of_two_vocabularies_side_by_side():
     torch.cuda.synchronize()
     assert codes_of(calls, 2000) == [{0}] * len(calls)
     assert all(torch.equal(a, b) for o, w in zip(outs, want) for a, b in zip(o[4:], w))
+
+
+# ---------------------------------------------------------------- lists
+@pytest.mark.parametrize("form", ["top", "tail"])
+def test_an_entry_listed_again_with_a_larger_value_counts_for_nothing(form):
+    """The first of them counts, also where the value of another is the largest of the list by far."""
+    g = rng("again", form)
+    z = Strided(6, 700, F32, values=normal(g, 6, 700, std=2.0))
+    ids = torch.stack([torch.randperm(700, device="cuda", generator=g)[:9] for _ in range(6)])
+    values = normal(g, 6, 9, std=1.0) - 4.0
+    for row, (at, of, v) in enumerate(((3, 0, 300.0), (8, 2, 120.0), (1, 0, 2e4), (5, 4, 88.0), (2, 1, float("nan")))):
+        ids[row, at], values[row, at] = ids[row, of].item(), v
+    if form == "tail":
+        values = torch.where(values.isnan(), values, values.clamp_max(-3.0))
+    values_of_reference = torch.where(values.isnan(), 0.0, values)  # (of the entry that does not count)
+    loss, stats, li, lq = run_distill(z, ids, values_of_reference, rng("w", form), form, 1.0)
+    more = [torch.empty_like(t) for t in (loss, stats, li, lq)]
+    fp8.fp8_distill_fwd(z.t, ids, values, *more, form=FORM[form])
+    assert all(torch.equal(a, b) for a, b in zip(more, (loss, stats, li, lq)))
