@@ -11,8 +11,7 @@
 //
 //   d logp_t   / d z_j = beta ([j = t] - p_j)
 //   d entropy  / d z_j = -beta p_j (log p_j + entropy)
-//   distillation:  beta (p_j factor - q_j)
-#pragma once
+//   distillation:  beta (p Q - q) of listed outcomes, beta p (Q - q' / p') of the others
 
 #include "block_scale.cuh"
 #include "pipeline.cuh"
@@ -134,7 +133,8 @@ struct Fwd {
 enum { kLogprob = 0, kListTop = 1, kListTail = 2 };
 
 struct Part {  // of a row: what one CTA has seen
-  float m, S, W, rest;
+  float m, S;
+  float W, L;  // kListTail: the listed ones' m and S
 };
 
 // Sum over the CTA in a fixed order; every thread gets it.
@@ -380,10 +380,13 @@ struct __align__(16) ListScratch {
   float v[FP8_DISTILL_MAX];
 };
 
-// What a thread has seen: S and W about m; L the listed ones' part (kListTail).
+// What a thread has seen: S and W about m.  kListTail: of the unlisted ones; L
+// of the listed ones, about a largest of their own, ml.  (About one m for both,
+// the unlisted sum is 0 in binary32 where the listed ones lie 88 or more above,
+// and its logarithm and its share of the gradient are lost.)
 template <int MODE, bool ENT>
 struct Running {
-  float m = kNone, W = 0.0f, L = 0.0f, largest = -INFINITY;
+  float m = kNone, ml = kNone, L = 0.0f, largest = -INFINITY;
   float2 S = make_float2(0.0f, 0.0f), W2 = make_float2(0.0f, 0.0f);
   bool any = false;
 
@@ -399,7 +402,6 @@ struct Running {
     }
     const float down = ex2(d);
     S = __fmul2_rn(S, both(down));
-    if constexpr (MODE == kListTail) L *= down;
     if constexpr (ENT) W2 = __fmul2_rn(W2, both(down));
     m = m1;
   }
@@ -424,7 +426,11 @@ struct Running {
     }
   }
   // a listed element
-  __device__ __forceinline__ void add_listed(float x, float c2) { L += ex2((x - m) * c2); }
+  __device__ __forceinline__ void add_listed(float x, float c2) {
+    const float m1 = max_nan(ml, x);
+    L = fmaf(L, ex2((ml - m1) * c2), ex2((x - m1) * c2));
+    ml = m1;
+  }
 };
 
 // Where element e of a CTA's body has its bit: a thread's kRun vectors of one
@@ -440,8 +446,8 @@ __host__ __device__ inline size_t mark_bytes(int vecs, int threads) {
   return (size_t)((vecs + kRun * threads - 1) / (kRun * threads)) * threads * (kRun * kElems<DT> / 8);
 }
 
-// Running softmax of a row's elements and, for kListTail, of the unlisted ones
-// alone (`marks`: a bit for each element, see mark_at).  Four
+// Running softmax of a row's elements, for kListTail of the unlisted ones alone
+// (`marks`: a bit for each element, see mark_at).  Four
 // vectors at a time: their loads are in flight together, and m is raised once.
 // Per element of a 16-bit row: one exponential (16 a cycle and SM: 46 us for
 // 4096 x 50304), some four other instructions.
@@ -452,9 +458,10 @@ __device__ __forceinline__ Running<MODE, ENT> stream_row(const Range &r, float c
   const int t = threadIdx.x, T = blockDim.x;
   if (t < r.head + r.tail) {
     const float x[1] = {load_one<DT>(r.row, t < r.head ? t : r.s.head + r.s.vecs * E + t - r.head)};
-    s.raise(x[0], c2);
-    if (MODE == kListTail && (edge_marks >> (t < r.head ? t : 16 + t - r.head) & 1)) s.add_listed(x[0], c2);
-    else s.add(x, c2);
+    if (!(MODE == kListTail && (edge_marks >> (t < r.head ? t : 16 + t - r.head) & 1))) {
+      s.raise(x[0], c2);
+      s.add(x, c2);
+    }
   }
   const uint4 *body = reinterpret_cast<const uint4 *>(r.body);
   const uint32_t none = kMinusInf<DT>;
@@ -485,8 +492,8 @@ __device__ __forceinline__ Running<MODE, ENT> stream_row(const Range &r, float c
   return s;
 }
 
-// The run of element e of the body, which is listed, if none before it in the
-// run is: lane g of G takes every G-th of its vectors.  (Tested inside the
+// The unlisted ones of the run of element e of the body, which is listed, if none
+// before it in the run is: lane g of G takes every G-th of its vectors.  (Tested inside the
 // stream, two of three steps of a warp took the slow way: 142 us for 4096 x
 // 50304 with 64 entries a row.)
 template <int DT, bool ENT>
@@ -502,53 +509,55 @@ __device__ __forceinline__ void add_marked(Running<kListTail, ENT> &s, const Ran
     const int v = r.v0 + run / T * (kRun * T) + u * T + run % T;
     if (v >= r.v1) break;
     const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(r.body) + v);
-    s.raise(widest<DT>(max_word<DT>(max_word<DT>(w.x, w.y), max_word<DT>(w.z, w.w))), c2);
-    float x[E];
+    float x[E], most = -INFINITY;
     unpack<DT>(w, x);
 #pragma unroll
     for (int j = 0; j < E; j++) {
-      const float x1[1] = {x[j]};
-      if (bits >> (u * E + j) & 1) s.add_listed(x[j], c2);
-      else s.add(x1, c2);
+      if (bits >> (u * E + j) & 1) x[j] = -INFINITY;
+      most = max_nan(most, x[j]);
     }
+    s.raise(most, c2);
+    s.add(x, c2);
   }
 }
 
 // Parts about their own m joined about the largest.  W is in units of log 2.
-__device__ __forceinline__ Part about(Part p, float m, float c2) {
+template <int MODE>
+__device__ __forceinline__ Part about(Part p, float m, float ml, float c2) {
   const float d = max_nan((p.m - m) * c2, -1000.0f), down = ex2(d);
-  return {m, p.S * down, fmaf(p.S, d, p.W) * down, p.rest * down};
+  if constexpr (MODE == kListTail) return {m, p.S * down, ml, p.L * ex2((p.W - ml) * c2)};
+  return {m, p.S * down, fmaf(p.S, d, p.W) * down, 0.0f};
+}
+
+// Joins the lanes' parts.
+template <int MODE, bool ENT>
+__device__ __forceinline__ Part join_lanes(Part p, float c2) {
+  float m = p.m, ml = p.W;
+#pragma unroll
+  for (int b = 16; b > 0; b /= 2) {
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, b));
+    if constexpr (MODE == kListTail) ml = max_nan(ml, __shfl_xor_sync(0xffffffffu, ml, b));
+  }
+  p = about<MODE>(p, m, ml, c2);
+#pragma unroll
+  for (int b = 16; b > 0; b /= 2) {
+    p.S += __shfl_xor_sync(0xffffffffu, p.S, b);
+    if constexpr (ENT) p.W += __shfl_xor_sync(0xffffffffu, p.W, b);
+    if constexpr (MODE == kListTail) p.L += __shfl_xor_sync(0xffffffffu, p.L, b);
+  }
+  return p;
 }
 
 // The CTA's part, to every thread: the warps by shuffles, then one exchange.
 template <int MODE, bool ENT>
 __device__ __forceinline__ Part join_block(const Running<MODE, ENT> &s, float c2, Part *warps) {
-  float m = s.m;
-#pragma unroll
-  for (int b = 16; b > 0; b /= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, b));
-  Part p = about({s.m, s.S.x + s.S.y, s.W2.x + s.W2.y, s.L}, m, c2);
-#pragma unroll
-  for (int b = 16; b > 0; b /= 2) {
-    p.S += __shfl_xor_sync(0xffffffffu, p.S, b);
-    if constexpr (ENT) p.W += __shfl_xor_sync(0xffffffffu, p.W, b);
-    if constexpr (MODE == kListTail) p.rest += __shfl_xor_sync(0xffffffffu, p.rest, b);
-  }
+  Part p = join_lanes<MODE, ENT>({s.m, s.S.x + s.S.y, MODE == kListTail ? s.ml : s.W2.x + s.W2.y, s.L}, c2);
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = p;
   __syncthreads();
   // each warp joins all of them, a lane a part
   const int lane = threadIdx.x & 31;
-  p = lane < (int)(blockDim.x >> 5) ? warps[lane] : Part{kNone, 0.0f, 0.0f, 0.0f};
-  m = p.m;
-#pragma unroll
-  for (int b = 16; b > 0; b /= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, b));
-  p = about(p, m, c2);
-#pragma unroll
-  for (int b = 16; b > 0; b /= 2) {
-    p.S += __shfl_xor_sync(0xffffffffu, p.S, b);
-    if constexpr (ENT) p.W += __shfl_xor_sync(0xffffffffu, p.W, b);
-    if constexpr (MODE == kListTail) p.rest += __shfl_xor_sync(0xffffffffu, p.rest, b);
-  }
-  return p;
+  p = lane < (int)(blockDim.x >> 5) ? warps[lane] : Part{kNone, 0.0f, MODE == kListTail ? kNone : 0.0f, 0.0f};
+  return join_lanes<MODE, ENT>(p, c2);
 }
 
 // One row a CTA (128 threads where there are many rows: 4096 x 50304 bfloat16 77
@@ -694,6 +703,7 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
       if (i * apart >= K) continue;
       const int lead_lane = (threadIdx.x & 31) / G * G;
       const bool counts = mine_at[i] >= 0 && mine_id[i] != kAbsent && !(mine_q[i] < 0.0f);
+      if (counts && rank == 0) own.add_listed(load_one<DT>(z, mine_id[i]), c2);
       const int id = __shfl_sync(0xffffffffu, counts ? mine_id[i] : kAbsent, lead_lane);
       const int e = id - r.s.head - r.v0 * kElems<DT>;
       if (id != kAbsent && e >= 0 && e < (r.v1 - r.v0) * kElems<DT>)
@@ -715,7 +725,7 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
       const uint32_t there = cluster_at(smem_u32(&parts[threadIdx.x]), threadIdx.x);
       Part o;
       asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(o.m), "=f"(o.S), "=f"(o.W), "=f"(o.rest)
+                   : "=f"(o.m), "=f"(o.S), "=f"(o.W), "=f"(o.L)
                    : "r"(there)
                    : "memory");
       parts[threadIdx.x] = o;
@@ -733,17 +743,19 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
     __syncthreads();
     float m = kNone;
     for (unsigned i = 0; i < ctas; i++) m = max_nan(m, parts[i].m);
-    all = {m, 0.0f, 0.0f, 0.0f};
+    all = {m, 0.0f, MODE == kListTail ? parts[0].W : 0.0f, parts[0].L};  // (the first CTA has all listed ones)
     for (unsigned i = 0; i < ctas; i++) {
-      const Part o = about(parts[i], m, c2);
-      all.W += o.W;
+      const Part o = about<MODE>(parts[i], m, parts[i].W, c2);
+      if (MODE != kListTail) all.W += o.W;
       all.S += o.S;
-      all.rest += o.rest;
     }
     if (MODE == kLogprob && p.top) rank_list(top.list, (int)ctas * p.top, p.top, top.best);
   }
   constexpr float kLn2 = 0.69314718055994531f;
-  const float S = MODE == kListTail ? all.S + all.rest : all.S;  // (rest: of the listed ones here)
+  // the row's m and S, and those of the unlisted ones, which are `down` of it about its m
+  const float m_row = MODE == kListTail ? max_nan(all.m, all.W) : all.m;
+  const float down = MODE == kListTail ? ex2((all.m - m_row) * c2) : 1.0f;
+  const float S = MODE == kListTail ? fmaf(all.S, down, all.L * ex2((all.W - m_row) * c2)) : all.S;
   const bool none = S == 0.0f;
   const float log_S = logf(S);  // -inf for none
   if constexpr (MODE == kLogprob) {
@@ -771,25 +783,29 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
       const float q = mine_q[i] < 0.0f ? mine_q[i] : mine_q[i] * q_scale;
       if (mine_id[i] != kAbsent && !(mine_q[i] <= 0.0f)) {
         const float lq = MODE == kListTop ? (mine_v[i] - top_value) * p.beta - log_q_sum : mine_v[i];
-        const float lp = none ? -INFINITY : p.beta * (load_one<DT>(z, mine_id[i]) - all.m) - log_S;
+        const float lp = none ? -INFINITY : p.beta * (load_one<DT>(z, mine_id[i]) - m_row) - log_S;
         l = fmaf(q, lq - lp, l);
       }
       p.list_ids[(size_t)row * K + mine_at[i]] = mine_id[i];
       p.list_q[(size_t)row * K + mine_at[i]] = q;
     }
     l = block_sum(l, red);
-    float listed = q_sum > 0.0f ? 1.0f : 0.0f, unlisted = listed;
-    if (q_sum != q_sum) listed = unlisted = q_sum;
+    // factors of e^(s - s_m): of a listed outcome about the row's m, of an unlisted one about theirs
+    float whole = q_sum > 0.0f ? 1.0f : 0.0f, rest = 0.0f;
+    if (q_sum != q_sum) whole = q_sum;
     if (MODE == kListTail) {
       const float q_rest = fmaxf(0.0f, 1.0f - q_sum);
-      const bool there = q_rest > 0.0f && all.S > 0.0f;
-      listed = q_sum + (there ? q_rest : 0.0f);
-      unlisted = listed - (there ? q_rest * (S / all.S) : 0.0f);
-      if (there) l += q_rest * (logf(q_rest) - (logf(all.S) - log_S));
+      whole = q_sum;
+      if (q_rest > 0.0f && all.S > 0.0f) {
+        whole += q_rest;
+        rest = q_rest / all.S;  // (S >= 1: their largest one)
+        l += q_rest * (logf(q_rest) - (fmaf(p.beta, all.m - m_row, logf(all.S)) - log_S));
+      }
     }
     if (threadIdx.x == 0) {
       p.loss[row] = l;
-      reinterpret_cast<float4 *>(p.stats)[row] = make_float4(all.m, none ? 0.0f : 1.0f / S, listed, unlisted);
+      const float listed = none ? 0.0f : whole / S;
+      reinterpret_cast<float4 *>(p.stats)[row] = make_float4(m_row, listed, all.m, none ? 0.0f : fmaf(listed, down, -rest));
     }
   }
 }
@@ -814,9 +830,9 @@ struct Bwd {
 };
 
 // A row's factors: with a = (z - m) c2 and e = 2^a, d = e (k0 + k1 a), plus gt
-// at the token; of a listed outcome e kl - gt q.
+// at the token; of a listed outcome, e about ml, e kl - gt q.
 struct RowTerms {
-  float m, k0, k1, kl, gt;
+  float m, k0, k1, ml, kl, gt;
   int token;
 };
 
@@ -824,16 +840,19 @@ template <bool LIST>
 __device__ __forceinline__ RowTerms row_terms(const Bwd &p, int row) {
   const float4 s = __ldg(reinterpret_cast<const float4 *>(p.stats) + row);
   RowTerms r;
-  r.m = s.x;
-  const bool none = s.y == 0.0f;  // no distribution: no gradient
+  const bool none = s.y == 0.0f;  // no distribution (or nothing listed): no gradient
   if constexpr (LIST) {
     const float g = none ? 0.0f : p.beta * __ldg(p.g + row);
-    r.k0 = g * s.w * s.y;
-    r.kl = g * s.z * s.y;
+    r.m = s.z;
+    r.k0 = g * s.w;
+    r.ml = s.x;
+    r.kl = g * s.y;
     r.k1 = 0.0f;
     r.gt = g;
     r.token = -1;
   } else {
+    r.m = s.x;
+    r.ml = 0.0f;
     r.token = p.g ? token_at(p.tokens, p.token_bytes, row, p.cols) : -1;
     const float g = none || r.token < 0 ? 0.0f : p.beta * __ldg(p.g + row);
     const float ge = none || !p.g_ent ? 0.0f : p.beta * __ldg(p.g_ent + row);
@@ -894,7 +913,7 @@ __global__ void __launch_bounds__(kBwdThreads) k_loss_bwd_rows(const Bwd p, unsi
           const float q = __ldg(p.list_q + (size_t)row * p.K + k);
           if (!(q < 0.0f)) {  // (not listed again)
             listed_at[i] = c;
-            listed[i] = fmaf(ex2(scaled(load_one<DT>(z, c), r.m, c2)), r.kl, -r.gt * q);
+            listed[i] = fmaf(ex2(scaled(load_one<DT>(z, c), r.ml, c2)), r.kl, -r.gt * q);
           }
         }
       }
@@ -963,7 +982,7 @@ __global__ void __launch_bounds__(512, 2) k_loss_bwd_tiles(const Bwd p) {
   const int c8 = threadIdx.x & 15, col = col0 + c8 * 8, r0 = row0 + (threadIdx.x >> 4);
   Raw8<DT> raw[RP];
   block::load_tile<DT>(p.z, p.ld / esz, p.vec_z, row0, col0, p.rows, p.cols, raw);
-  RowTerms own = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, -1};  // rows behind the last: 0
+  RowTerms own = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, -1};  // rows behind the last: 0
   uint32_t marks[4] = {0, 0, 0, 0};                    // listed columns of the tile
   {
     const int row = r0 + c8 * G::kStep;
@@ -1014,7 +1033,7 @@ __global__ void __launch_bounds__(512, 2) k_loss_bwd_tiles(const Bwd p) {
       f[i][2 * j + 1] = g.y;
     }
     if constexpr (LIST) {
-      const float kl = __shfl_sync(0xffffffffu, own.kl, lane0 + i);
+      const float ml = __shfl_sync(0xffffffffu, own.ml, lane0 + i), kl = __shfl_sync(0xffffffffu, own.kl, lane0 + i);
       uint32_t bits = 0;
 #pragma unroll
       for (int w = 0; w < 4; w++) {
@@ -1024,12 +1043,13 @@ __global__ void __launch_bounds__(512, 2) k_loss_bwd_tiles(const Bwd p) {
       if (bits) {  // rare: the list's entries of these columns
         const size_t at = (size_t)(r0 + i * G::kStep) * p.K;
         int k = token;
+        float x[8];
+        block::unpack8<DT>(raw[i], x);
 #pragma unroll
         for (int j = 0; j < 8; j++)
           if (bits >> j & 1) {
             while (__ldg(p.list_ids + at + k) != col + j) k++;  // (marked, so it is there)
-            const float ej = j & 1 ? e[j >> 1].y : e[j >> 1].x;
-            f[i][j] = fmaf(ej, kl, -gt * __ldg(p.list_q + at + k));
+            f[i][j] = fmaf(ex2(scaled(x[j], ml, c2)), kl, -gt * __ldg(p.list_q + at + k));
           }
       }
     } else {

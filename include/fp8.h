@@ -799,13 +799,14 @@ int fp8_logprob_bwd(const void *logits, int dtype, int rows, int cols, size_t ld
  * cols <= FP8_DISTILL_COLS_MAX.
  *
  * fp8_distill_fwd also writes what the backward pass needs: stats [rows, 4]
- * (the largest logit, 1 / sum exp, and the factors of p for listed and for
- * unlisted outcomes), and the list in the order of the ids: list_ids, list_q
+ * (the largest logit and the factor of exp(s - its s) for listed outcomes, the
+ * largest of the others and their factor), and the list in the order of the ids: list_ids, list_q
  * [rows, top] (absent entries last, 2^31 - 1; an entry that was listed before
  * stands behind the first one, its q -1).
  *
  * fp8_distill_bwd -- from dloss [rows], the gradient of the logits as
- * fp8_logprob_bwd:  d = inv_temp * dloss * (p * factor - q).
+ * fp8_logprob_bwd:  d = inv_temp * dloss * (p Q - q) of a listed outcome, p (Q - q' / p')
+ * of another, Q the sum of q and q' (1 in the form "top", which has no q').
  */
 #define FP8_DISTILL_TOP 0
 #define FP8_DISTILL_TAIL 1

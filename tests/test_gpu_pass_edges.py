@@ -7,7 +7,7 @@ import torch
 
 from fp8_mixed_precision_tensor_b200 import fp8
 from fp8_mixed_precision_tensor_b200.block_linear import BlockNorm
-from test_gpu_passes import BF16, F16, F32, FORM, GUARD, KIND, Strided, normal, rng, run_distill
+from test_gpu_passes import BF16, F16, F32, FORM, GUARD, KIND, Strided, check_gradient_codes, normal, rng, run_distill
 
 
 pytestmark = pytest.mark.gpu
@@ -158,3 +158,78 @@ def test_an_entry_listed_again_with_a_larger_value_counts_for_nothing(form):
     more = [torch.empty_like(t) for t in (loss, stats, li, lq)]
     fp8.fp8_distill_fwd(z.t, ids, values, *more, form=FORM[form])
     assert all(torch.equal(a, b) for a, b in zip(more, (loss, stats, li, lq)))
+
+
+def far_student(rows, cols, K, dtype, gaps, inv_temp=1.0):
+    """Logits whose listed ones lie a gap above all others, and a teacher that gives the others a quarter."""
+    g = rng("far", rows, cols, K, str(dtype), inv_temp)
+    z = normal(g, rows, cols, std=1.5)
+    ids = torch.stack([torch.randperm(cols, device="cuda", generator=g)[:K] for _ in range(rows)])
+    gap = torch.tensor([gaps[i % len(gaps)] for i in range(rows)], device="cuda")[:, None]
+    z.scatter_add_(1, ids, (gap / inv_temp).expand(-1, K))
+    values = torch.log(0.75 * torch.softmax(normal(g, rows, K), 1))
+    return Strided(rows, cols, dtype, values=z), values, ids, g
+
+
+GAPS = (0.0, 30.0, 80.0, 84.0, 86.0, 87.0, 87.5, 88.0, 89.0, 95.0, 103.0, 120.0, 300.0, 600.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("rows,cols,K", [(14, 515, 5), (14, 50257, 64), (200, 2056, 33), (28, 77, 70)])
+def test_a_student_that_is_sure_of_what_is_listed(rows, cols, K, dtype):
+    """The rest's term and gradient where its probability is below what binary32 holds: -log p' is of the gap's size."""
+    z, values, ids, g = far_student(rows, cols, K, dtype, GAPS)
+    run_distill(z, ids, values, g, "tail", 1.0)
+    z, values, ids, g = far_student(rows, cols, K, dtype, GAPS, 4.0)
+    run_distill(z, ids, values, g, "tail", 4.0)
+    assert fp8.fp8_get_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradient_codes_of_a_sure_student(dtype):
+    z, values, ids, g = far_student(150, 700, 20, dtype, GAPS)
+    loss, stats = torch.empty(150, device="cuda"), torch.empty(150, 4, device="cuda")
+    li, lq = torch.empty(150, 20, dtype=torch.int32, device="cuda"), torch.empty(150, 20, device="cuda")
+    fp8.fp8_distill_fwd(z.t, ids, values, loss, stats, li, lq, form=FORM["tail"])
+    w = torch.randn(150, device="cuda", generator=g)
+    check_gradient_codes(lambda dt, **out: fp8.fp8_distill_bwd(z.t.to(dt), li, lq, stats, w, **out), 150, 700, dtype, "e5m2")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_student_that_excludes_all_that_is_not_listed(dtype):
+    """Masked to -inf: p' is 0, and the rest has no term; masked by a large number it has one."""
+    for mask in (-float("inf"), -1e4, -60000.0):
+        g = rng("mask", mask, str(dtype))
+        z = torch.full((5, 900), mask, device="cuda")
+        ids = torch.stack([torch.randperm(900, device="cuda", generator=g)[:6] for _ in range(5)])
+        z.scatter_(1, ids, normal(g, 5, 6))
+        values = torch.log(0.9 * torch.softmax(normal(g, 5, 6), 1))
+        s = Strided(5, 900, dtype, values=z)
+        loss = torch.empty(5, device="cuda")
+        stats, li, lq = torch.empty(5, 4, device="cuda"), torch.empty(5, 6, dtype=torch.int32, device="cuda"), torch.empty(5, 6, device="cuda")
+        fp8.fp8_distill_fwd(s.t, ids, values, loss, stats, li, lq, form=FORM["tail"])
+        zl = s.t.gather(1, ids).double()
+        lp, q = torch.log_softmax(zl, 1), values.double().exp()  # (the others' e^-10000 is nothing to the sum)
+        want = (q * (values.double() - lp)).sum(1)
+        if mask > -float("inf"):
+            rest = 1.0 - q.sum(1)
+            lp_rest = mask_of(s.t, ids) + torch.tensor(894.0, device="cuda", dtype=torch.float64).log() - torch.logsumexp(zl, 1)
+            want = want + rest * (rest.log() - lp_rest)
+        # each product and sum rounded: some 20 units of what is added up, and 1 - sum q off by 8 units of 1
+        size = 20 * (want.abs() + 10) + (8 * abs(mask) if mask > -float("inf") else 0)
+        assert bool(((loss.double() - want).abs() <= 2.0 ** -24 * size).all()), mask
+        d = torch.empty(5, 900, device="cuda")
+        fp8.fp8_distill_bwd(s.t.float(), li, lq, stats, torch.ones(5, device="cuda"), dlogits=d)
+        assert bool(d.isfinite().all())
+        whole = 1.0 if mask > -float("inf") else float(q.sum(1)[0])
+        rest = 0.0 if mask == -float("inf") else 0.1
+        listed = torch.zeros(5, 900, dtype=torch.bool, device="cuda").scatter_(1, ids, True)
+        out = d.masked_fill(listed, 0.0).double().sum(1)  # the rest's share of the gradient: -q' in all
+        assert bool((out + rest).abs().max() <= 64 * 2.0 ** -24), mask
+        got = d.double().gather(1, ids)
+        assert bool((got - (lp.exp() * whole - q)).abs().max() <= 64 * 2.0 ** -24), mask
+
+
+def mask_of(z, ids):
+    """The masked logits' value, as stored."""
+    return z.masked_fill(torch.zeros_like(z, dtype=torch.bool).scatter_(1, ids, True), -float("inf")).amax(1).double()
