@@ -1048,8 +1048,8 @@ __global__ void __launch_bounds__(512, 2) k_loss_bwd_tiles(const Bwd p) {
 #pragma unroll
         for (int j = 0; j < 8; j++)
           if (bits >> j & 1) {
-            while (__ldg(p.list_ids + at + k) != col + j) k++;  // (marked, so it is there)
-            f[i][j] = fmaf(ex2(scaled(x[j], ml, c2)), kl, -gt * __ldg(p.list_q + at + k));
+            while (k < p.K && __ldg(p.list_ids + at + k) != col + j) k++;
+            if (k < p.K) f[i][j] = fmaf(ex2(scaled(x[j], ml, c2)), kl, -gt * __ldg(p.list_q + at + k));  // (as in every list in order)
           }
       }
     } else {

@@ -807,6 +807,8 @@ int fp8_logprob_bwd(const void *logits, int dtype, int rows, int cols, size_t ld
  * fp8_distill_bwd -- from dloss [rows], the gradient of the logits as
  * fp8_logprob_bwd:  d = inv_temp * dloss * (p Q - q) of a listed outcome, p (Q - q' / p')
  * of another, Q the sum of q and q' (1 in the form "top", which has no q').
+ * The list is that of the forward call: one in another order gives a gradient of
+ * no meaning.
  */
 #define FP8_DISTILL_TOP 0
 #define FP8_DISTILL_TAIL 1

@@ -233,3 +233,33 @@ def test_a_student_that_excludes_all_that_is_not_listed(dtype):
 def mask_of(z, ids):
     """The masked logits' value, as stored."""
     return z.masked_fill(torch.zeros_like(z, dtype=torch.bool).scatter_(1, ids, True), -float("inf")).amax(1).double()
+
+
+# ---------------------------------------------------------------- unsorted
+@pytest.mark.parametrize("codes", [False, True])
+def test_a_list_in_another_order_is_read_inside_its_bounds(codes):
+    """The last rows' entries in falling order, and numbers that are no columns: nothing beyond the list is looked at, and
+    rows whose list is in order have their gradient."""
+    g = rng("order")
+    rows, cols, K = 140, 300, 40
+    z = normal(g, rows, cols)
+    ids = torch.stack([torch.randperm(cols, device="cuda", generator=g)[:K] for _ in range(rows)])
+    loss, stats, li, lq = (torch.empty(rows, device="cuda"), torch.empty(rows, 4, device="cuda"),
+                           torch.empty(rows, K, dtype=torch.int32, device="cuda"), torch.empty(rows, K, device="cuda"))
+    fp8.fp8_distill_fwd(z, ids, normal(g, rows, K), loss, stats, li, lq)
+    other = li.clone()
+    other[70:] = li[70:].flip(1)
+    other[-1] = torch.tensor([-2 ** 31, -1, 2 ** 31 - 1, cols] * (K // 4), dtype=torch.int32, device="cuda")
+    w = torch.randn(rows, device="cuda", generator=g)
+
+    def values(ids_):
+        if not codes:
+            d = torch.empty_like(z)
+            fp8.fp8_distill_bwd(z, ids_, lq, stats, w, dlogits=d)
+            return d[:64]
+        q, s = fp8.block_codes(rows, cols, "cuda"), fp8.block_scales(rows, cols, "cuda")
+        fp8.fp8_distill_bwd(z, ids_, lq, stats, w, d_q=q, d_s=s)
+        return q[:64]
+
+    assert torch.equal(values(other), values(li))
+    assert fp8.fp8_get_status() == 0
