@@ -239,6 +239,10 @@ class BlockNorm:
     def __init__(self, w: torch.Tensor | None, b: torch.Tensor | None = None, pre: int = fp8.FP8_NORM_RMS,
                  post: int = fp8.FP8_NORM_NONE, post_w: torch.Tensor | None = None, post_b: torch.Tensor | None = None,
                  gate: torch.Tensor | None = None, res_scale: float = 1.0, eps: float = 1e-5, margin: int = 0):
+        if pre == fp8.FP8_NORM_NONE:
+            raise ValueError("pre: the norm that gives x is needed")
+        if post == fp8.FP8_NORM_NONE and (post_w is not None or post_b is not None):
+            raise ValueError("post_w and post_b belong to a post norm: post is FP8_NORM_NONE")
         self.params = {"w": w, "b": b, "post_w": post_w, "post_b": post_b, "gate": gate}
         self.pre, self.post, self.res_scale, self.eps, self.margin = pre, post, float(res_scale), float(eps), margin
         self.kept = None

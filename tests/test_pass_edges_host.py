@@ -1,6 +1,9 @@
 """Norms, log probabilities and distillation at their edges: what is refused on the host."""
 import ctypes
 
+import pytest
+import torch
+
 from test_passes_host import FAKE, fp8, norm_params  # noqa: F401
 
 
@@ -11,3 +14,16 @@ def test_a_gate_gradient_of_fewer_than_no_rows_is_refused(fp8):  # noqa: F811
     p = norm_params(fp8, rows=0, gate=V(FAKE, 0))
     args = (None, 256, None, 256, None, 256, None, 256, None, None, 256, None, 256, ctypes.byref(g), None, 0, None)
     assert lib.fp8_norm_bwd(ctypes.byref(p), *args) == fp8.FP8_ERR_INVALID_ARG
+
+
+def test_a_norm_layer_refuses_parameters_of_a_norm_that_it_lacks(fp8):  # noqa: F811
+    """Its forward pass would leave them out and its backward pass, asked for their gradients, fail."""
+    from fp8_mixed_precision_tensor_b200.block_linear import BlockNorm
+
+    w = torch.ones(8)
+    for kw in (dict(post_w=w), dict(post_b=w), dict(post_w=w, post=fp8.FP8_NORM_NONE)):
+        with pytest.raises(ValueError, match="post norm"):
+            BlockNorm(w, **kw)
+    with pytest.raises(ValueError, match="pre"):
+        BlockNorm(w, pre=fp8.FP8_NORM_NONE)
+    BlockNorm(w, post=fp8.FP8_NORM_RMS, post_w=w)
