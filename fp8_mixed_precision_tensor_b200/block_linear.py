@@ -229,7 +229,8 @@ class BlockNorm:
     forward(h, r) returns (r', x); with codes=True x is its BlockCodes, written
     by the norm itself, for BlockLinear, BlockMLP or BlockHead (with keep=True
     the column blocks of their weight gradient too).  h may be None (a norm
-    alone).  keep=True keeps h, r' and each row's statistics for
+    alone); dtype then gives x's, r's own by default (a model of 16-bit layers
+    with a float32 residual starts so).  keep=True keeps h, r' and each row's statistics for
     backward(dx, dr), which returns (dh, dr, grads): dr is the gradient of r' from
     what follows, or None, and grads has the gradient of each parameter given, in
     its dtype, by name.
@@ -254,13 +255,17 @@ class BlockNorm:
             if t is not None:
                 t.record_stream(now)
 
-    def forward(self, h: torch.Tensor | None, r: torch.Tensor, codes: bool = False, keep: bool = False,
-                stream=None) -> tuple[torch.Tensor, torch.Tensor | BlockCodes]:
+    def forward(self, h: torch.Tensor | None, r: torch.Tensor, codes: bool = False, keep: bool = False, stream=None,
+                dtype: torch.dtype | None = None) -> tuple[torch.Tensor, torch.Tensor | BlockCodes]:
+        of = r if h is None else h
+        if dtype is None:
+            dtype = of.dtype
+        elif dtype != of.dtype and not (h is None and r.dtype is torch.float32):
+            raise ValueError(f"dtype {dtype}: x has h's, or beside a float32 residual without h another")
         with _on(stream, *(t for t in (h, r) if t is not None)):
             if stream is not None:
                 self._in_use()
             M, D = r.shape
-            dtype = r.dtype if h is None else h.dtype
             r_out = torch.empty_like(r, memory_format=torch.contiguous_format)
             stats = torch.empty((M, 4), dtype=torch.float32, device=r.device) if keep else None
             out = {}

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 from fp8_mixed_precision_tensor_b200 import fp8
-from fp8_mixed_precision_tensor_b200.block_linear import BlockNorm
+from fp8_mixed_precision_tensor_b200.block_linear import BlockLinear, BlockNorm
+from test_gpu_block import row_blocks
 from test_gpu_passes import BF16, F16, F32, FORM, GUARD, KIND, Strided, check_gradient_codes, normal, rng, run_distill
 
 
@@ -53,6 +54,38 @@ def test_a_norm_that_got_no_tokens(shape):
     dh, dr, grads = norm.backward(h, h)
     assert dh.shape == dr.shape == (0, 64) and grads["gate"].shape == shape
     assert all(not g.any() for g in grads.values())
+
+
+# ---------------------------------------------------------------- a float32 residual
+def test_the_first_norm_of_a_float32_residual_writes_for_16_bit_layers():
+    """A norm alone: x and its codes are those of the call, the layer behind it gives its type, and the residual's
+    gradient has the residual's."""
+    g = rng("first")
+    r, w = normal(g, 70, 256), torch.ones(256, device="cuda", dtype=BF16)
+    norm, lin = BlockNorm(w), BlockLinear(normal(g, 128, 256, std=0.05, dtype=BF16))
+    want, stats, x32 = torch.empty(70, 256, device="cuda", dtype=BF16), torch.empty(70, 4, device="cuda"), torch.empty_like(r)
+    fp8.fp8_norm_fwd(None, r, None, stats, w=w, x=want)
+    fp8.fp8_norm_fwd(None, r, None, None, w=w, x=x32)
+    r_out, x = norm.forward(None, r, dtype=BF16)
+    assert torch.equal(x, want) and torch.equal(r_out, r)
+    r_out, x = norm.forward(None, r, codes=True, keep=True, dtype=BF16)
+    c = row_blocks(70, 256)
+    fp8.fp8_block_cast(x32, fp8.FP8_E4M3, 0, c.q, c.s, None, None)
+    assert x.dtype is BF16 and torch.equal(x.q, c.q) and torch.equal(x.s, c.s)
+    y = lin.forward(x, keep=True)
+    dx, dw = lin.backward(torch.ones_like(y))
+    assert y.dtype is dx.dtype is dw.dtype is BF16
+    none, dr, grads = norm.backward(dx, r)
+    d = torch.empty_like(r)
+    fp8.fp8_norm_bwd(dx, r, None, r, stats, w=w, dr=d)
+    assert none is None and torch.equal(dr, d) and grads["w"].dtype is BF16
+
+
+@pytest.mark.parametrize("h,r,dtype", [(BF16, F32, F32), (BF16, BF16, F32), (None, BF16, F32), (None, BF16, F16)])
+def test_a_norm_gives_x_in_no_other_type(h, r, dtype):
+    e = lambda t: None if t is None else torch.zeros(2, 8, device="cuda", dtype=t)  # noqa: E731
+    with pytest.raises(ValueError, match="dtype"):
+        BlockNorm(torch.ones(8, device="cuda")).forward(e(h), e(r), dtype=dtype)
 
 
 @pytest.mark.parametrize("cols", [300000, 327680])
