@@ -857,7 +857,7 @@ __device__ __forceinline__ RowTerms row_terms(const Bwd &p, int row) {
     const float g = none || r.token < 0 ? 0.0f : p.beta * __ldg(p.g + row);
     const float ge = none || !p.g_ent ? 0.0f : p.beta * __ldg(p.g_ent + row);
     r.gt = g;
-    r.k0 = -(p.g_ent && !none ? g + ge * (s.w - s.z) : g) * s.y;
+    r.k0 = (0.0f - (p.g_ent && !none ? g + ge * (s.w - s.z) : g)) * s.y;  // (+0 where there is no gradient)
     r.k1 = -ge * 0.69314718055994531f * s.y;
     r.kl = 0.0f;
   }
@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(kBwdThreads) k_loss_bwd_rows(const Bwd p, unsi
   }
   auto grad = [&](float x, int c) {
     const float a = scaled(x, r.m, c2);
-    float g = ex2(a) * fmaf(r.k1, a, r.k0);
+    float g = ex2(a) * (LIST ? r.k0 : fmaf(r.k1, a, r.k0));
     if (!LIST && c == r.token) g += r.gt;
     return g;
   };

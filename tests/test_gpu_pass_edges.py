@@ -296,3 +296,30 @@ def test_a_list_in_another_order_is_read_inside_its_bounds(codes):
 
     assert torch.equal(values(other), values(li))
     assert fp8.fp8_get_status() == 0
+
+
+# ---------------------------------------------------------------- zeros
+@pytest.mark.parametrize("loss", ["logprob", "entropy", "top", "tail"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_without_a_gradient_are_zeros_of_one_sign(loss, dtype):
+    """No token, or nothing listed: the codes are the casts of the gradient there too, to the sign of a zero."""
+    rows, cols, K = 140, 300, 5
+    g = rng("zeros", loss)
+    z = normal(g, rows, cols, std=2.0, dtype=dtype)
+    none = torch.arange(rows, device="cuda") % 3 == 1
+    first, stats, w = torch.empty(rows, device="cuda"), torch.empty(rows, 4, device="cuda"), torch.randn(rows, device="cuda", generator=g)
+    if loss in ("logprob", "entropy"):
+        tokens = torch.where(none, -1, torch.randint(0, cols, (rows,), device="cuda", generator=g))
+        ent = torch.empty(rows, device="cuda") if loss == "entropy" else None
+        fp8.fp8_logprob_fwd(z, tokens, first, stats, entropy=ent)
+        went = None if ent is None else torch.where(none, 0.0, w)
+        call = lambda dt, **out: fp8.fp8_logprob_bwd(z.to(dt), tokens, stats, w, dentropy=went, **out)  # noqa: E731
+    else:
+        ids = torch.stack([torch.randperm(cols, device="cuda", generator=g)[:K] for _ in range(rows)]).masked_fill(none[:, None], -1)
+        li, lq = torch.empty(rows, K, dtype=torch.int32, device="cuda"), torch.empty(rows, K, device="cuda")
+        fp8.fp8_distill_fwd(z, ids, normal(g, rows, K) - 3.0, first, stats, li, lq, form=FORM[loss])
+        call = lambda dt, **out: fp8.fp8_distill_bwd(z.to(dt), li, lq, stats, w, **out)  # noqa: E731
+    d = torch.empty(rows, cols, device="cuda")
+    call(F32, dlogits=d)
+    assert not d[none].any() and bool((first[none] == 0).all())
+    check_gradient_codes(call, rows, cols, dtype, "e5m2")
