@@ -425,11 +425,11 @@ struct Running {
       }
     }
   }
-  // a listed element
-  __device__ __forceinline__ void add_listed(float x, float c2) {
-    const float m1 = max_nan(ml, x);
-    L = fmaf(L, ex2((ml - m1) * c2), ex2((x - m1) * c2));
-    ml = m1;
+  // the thread's listed elements; -inf for none
+  __device__ __forceinline__ void add_listed(const float (&x)[4], float c2) {
+    ml = max_nan(max_nan(max_nan(max_nan(ml, x[0]), x[1]), x[2]), x[3]);
+#pragma unroll
+    for (int i = 0; i < 4; i++) L += ex2((x[i] - ml) * c2);
   }
 };
 
@@ -697,18 +697,24 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
     if (MODE == kListTail) __syncthreads();  // the marks (red is read behind the next exchange)
   }
   Running<MODE, ENT> own = stream_row<DT, MODE, ENT>(r, c2, marks, MODE == kListTail ? edge_bits : 0u);
+  float mine_z[4];  // the listed logits
   if constexpr (MODE == kListTail) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      mine_z[i] = -INFINITY;
+      if (mine_id[i] != kAbsent && !(mine_q[i] < 0.0f) && rank == 0) mine_z[i] = load_one<DT>(z, mine_id[i]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       if (i * apart >= K) continue;
       const int lead_lane = (threadIdx.x & 31) / G * G;
       const bool counts = mine_at[i] >= 0 && mine_id[i] != kAbsent && !(mine_q[i] < 0.0f);
-      if (counts && rank == 0) own.add_listed(load_one<DT>(z, mine_id[i]), c2);
       const int id = __shfl_sync(0xffffffffu, counts ? mine_id[i] : kAbsent, lead_lane);
       const int e = id - r.s.head - r.v0 * kElems<DT>;
       if (id != kAbsent && e >= 0 && e < (r.v1 - r.v0) * kElems<DT>)
         add_marked<DT, ENT>(own, r, c2, marks, e, threadIdx.x % G, G);
     }
+    own.add_listed(mine_z, c2);
   }
   Part all = join_block<MODE, ENT>(own, c2, warp_parts);
   float q_sum = 0.0f;
@@ -783,7 +789,7 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
       const float q = mine_q[i] < 0.0f ? mine_q[i] : mine_q[i] * q_scale;
       if (mine_id[i] != kAbsent && !(mine_q[i] <= 0.0f)) {
         const float lq = MODE == kListTop ? (mine_v[i] - top_value) * p.beta - log_q_sum : mine_v[i];
-        const float lp = none ? -INFINITY : p.beta * (load_one<DT>(z, mine_id[i]) - m_row) - log_S;
+        const float lp = none ? -INFINITY : p.beta * ((MODE == kListTail ? mine_z[i] : load_one<DT>(z, mine_id[i])) - m_row) - log_S;
         l = fmaf(q, lq - lp, l);
       }
       p.list_ids[(size_t)row * K + mine_at[i]] = mine_id[i];
@@ -1033,7 +1039,7 @@ __global__ void __launch_bounds__(512, 2) k_loss_bwd_tiles(const Bwd p) {
       f[i][2 * j + 1] = g.y;
     }
     if constexpr (LIST) {
-      const float ml = __shfl_sync(0xffffffffu, own.ml, lane0 + i), kl = __shfl_sync(0xffffffffu, own.kl, lane0 + i);
+      const float kl = __shfl_sync(0xffffffffu, own.kl, lane0 + i);
       uint32_t bits = 0;
 #pragma unroll
       for (int w = 0; w < 4; w++) {
@@ -1041,16 +1047,21 @@ __global__ void __launch_bounds__(512, 2) k_loss_bwd_tiles(const Bwd p) {
         if (c8 >> 2 == w) bits = word >> ((c8 & 3) * 8) & 0xffu;
       }
       if (bits) {  // rare: the list's entries of these columns
-        const size_t at = (size_t)(r0 + i * G::kStep) * p.K;
+        const int row = r0 + i * G::kStep;
+        const size_t at = (size_t)row * p.K;
+        const uint8_t *z = p.z + (size_t)row * p.ld;  // read again (d, which may take its place, is written below)
+        const float ml = __ldg(p.stats + 4 * (size_t)row);
         int k = token;
-        float x[8];
-        block::unpack8<DT>(raw[i], x);
+#pragma unroll 1
+        for (uint32_t left = bits; left; left &= left - 1) {
+          const int j = __ffs(left) - 1;
+          while (k < p.K && __ldg(p.list_ids + at + k) != col + j) k++;
+          if (k == p.K) break;  // (in no list in order)
+          const float v = fmaf(ex2(scaled(load_one<DT>(z, col + j), ml, c2)), kl, -gt * __ldg(p.list_q + at + k));
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-          if (bits >> j & 1) {
-            while (k < p.K && __ldg(p.list_ids + at + k) != col + j) k++;
-            if (k < p.K) f[i][j] = fmaf(ex2(scaled(x[j], ml, c2)), kl, -gt * __ldg(p.list_q + at + k));  // (as in every list in order)
-          }
+          for (int n = 0; n < 8; n++)
+            if (n == j) f[i][n] = v;
+        }
       }
     } else {
       const int at = token - c8 * 8;
