@@ -43,7 +43,7 @@ struct LossArgs {
   float inv_temp;
 };
 int check_loss(const LossArgs &a) {
-  if (!valid_dtype(a.dtype) || a.rows < 0 || a.cols < 0 || !(a.inv_temp > 0.0f) || !isfinite(a.inv_temp))
+  if (!valid_dtype(a.dtype) || a.rows < 0 || a.cols < 0 || !(a.inv_temp > 0.0f) || !isfinite(a.inv_temp * loss::kLog2e))
     return FP8_ERR_INVALID_ARG;
   if (a.rows == 0 || a.cols == 0) return FP8_OK;
   if (too_long(a.rows, a.cols)) return FP8_ERR_UNSUPPORTED;

@@ -750,8 +750,8 @@ int fp8_norm_bwd(const fp8_norm_params *p, const void *dx, size_t lddx, const vo
                  void *stream);
 
 /*
- * Log probabilities of given tokens.  With s = inv_temp * logits (inv_temp > 0)
- * and p = softmax(s) of each row of [rows, cols]:
+ * Log probabilities of given tokens.  With s = inv_temp * logits (inv_temp > 0,
+ * and inv_temp / log 2 a binary32 number) and p = softmax(s) of each row of [rows, cols]:
  *
  * fp8_logprob_fwd -- logp[i] = log p of token tokens[i]; entropy[i] = -sum p
  * log p; the `top` (<= FP8_TOP_MAX, <= cols) largest logits in order, ties to
