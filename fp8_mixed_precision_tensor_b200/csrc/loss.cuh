@@ -12,6 +12,7 @@
 //   d logp_t   / d z_j = beta ([j = t] - p_j)
 //   d entropy  / d z_j = -beta p_j (log p_j + entropy)
 //   distillation:  beta (p Q - q) of listed outcomes, beta p (Q - q' / p') of the others
+#pragma once
 
 #include "block_scale.cuh"
 #include "pipeline.cuh"
