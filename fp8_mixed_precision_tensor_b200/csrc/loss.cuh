@@ -806,7 +806,9 @@ __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
       if (q_rest > 0.0f && all.S > 0.0f) {
         whole += q_rest;
         rest = q_rest / all.S;  // (S >= 1: their largest one)
-        l += q_rest * (logf(q_rest) - (fmaf(p.beta, all.m - m_row, logf(all.S)) - log_S));
+        // p' itself where binary32 holds it (the logarithms of S and of its part are rounded at their own size)
+        const float p_rest = all.S * down / S;
+        l = fmaf(q_rest, p_rest > 1e-30f ? logf(q_rest / p_rest) : logf(q_rest) - (fmaf(p.beta, all.m - m_row, logf(all.S)) - log_S), l);
       }
     }
     if (threadIdx.x == 0) {

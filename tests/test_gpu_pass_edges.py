@@ -268,6 +268,24 @@ def mask_of(z, ids):
     return z.masked_fill(torch.zeros_like(z, dtype=torch.bool).scatter_(1, ids, True), -float("inf")).amax(1).double()
 
 
+@pytest.mark.parametrize("rows", [3, 200])
+def test_a_rest_that_student_and_teacher_agree_about(rows):
+    """One rare outcome listed: the loss is q' log(q' / p'), both almost 1.  q', p' and their ratio have four roundings,
+    the sum one and the logarithm one; the listed term is 10^-4 of what it would need to count."""
+    g = rng("agree", rows)
+    z = normal(g, rows, 30000, std=0.1)
+    ids = torch.randint(0, 30000, (rows, 1), device="cuda", generator=g)
+    lp = torch.log_softmax(z.double(), 1)
+    values = (lp.gather(1, ids) + 0.1).float()
+    loss, stats = torch.empty(rows, device="cuda"), torch.empty(rows, 4, device="cuda")
+    fp8.fp8_distill_fwd(z, ids, values, loss, stats, torch.empty(rows, 1, dtype=torch.int32, device="cuda"),
+                        torch.empty(rows, 1, device="cuda"), form=FORM["tail"])
+    lq = values.double()
+    q, p = lq.exp()[:, 0], lp.gather(1, ids).exp()[:, 0]
+    want = (q * (lq - lp.gather(1, ids))[:, 0]) + (1 - q) * ((1 - q) / (1 - p)).log()
+    assert bool(((loss.double() - want).abs() <= 6 * 2.0 ** -24).all())
+
+
 # ---------------------------------------------------------------- unsorted
 @pytest.mark.parametrize("codes", [False, True])
 def test_a_list_in_another_order_is_read_inside_its_bounds(codes):
