@@ -311,7 +311,9 @@ class BlockHead:
     8-bit codes that the layer's own dgrad and wgrad read.
 
     log_probs(x, tokens) and distill(x, ids, values) take x [M, K] or its
-    BlockCodes; keep=True keeps the logits and x's column blocks for backward(g),
+    BlockCodes.  The logits are stored in x's dtype, and what is computed from them
+    carries that rounding (half a step of bfloat16 at a logit of 20 is 0.06),
+    unless logits_dtype asks for another (float32).  keep=True keeps the logits and x's column blocks for backward(g),
     g the gradient of what was returned for each row, which returns (dx, dw) in
     x's dtype.
 

@@ -562,9 +562,11 @@ __device__ __forceinline__ Part join_block(const Running<MODE, ENT> &s, float c2
 }
 
 // One row a CTA (128 threads where there are many rows: 4096 x 50304 bfloat16 77
-// us in CTAs of 256, 73 so, 5.7 TB/s; with the entropy 80, lists of 64: 88, in
-// the tail form 95), or a cluster's where there are few (one row of 50304 4.2
-// us, with 20 alternatives 10).  Bound by the exponential unit beside HBM.
+// us in CTAs of 256, 72 so, 5.7 TB/s; with the entropy 75, lists of 64: 84, in
+// the tail form 94), or a cluster's where there are few (one row of 50304 4.7
+// us, with 20 alternatives 10).  Neither HBM (59 % busy) nor the exponential unit
+// (69 %) is full: warps wait for loads, four vectors each in flight, at 27 warps
+// an SM.
 template <int DT, int MODE, bool ENT>
 __global__ void __launch_bounds__(1024) k_loss_fwd(const Fwd p, unsigned ctas) {
   pdl_launch_dependents();
@@ -876,8 +878,10 @@ __device__ __forceinline__ RowTerms row_terms(const Bwd &p, int row) {
 __device__ __forceinline__ float scaled(float z, float m, float c2) { return max_nan((z - m) * c2, -1000.0f); }
 
 // d itself: one row's chunk a CTA, in 16-byte vectors wherever the row starts.
-// HBM-bound: 4096 x 50304 bfloat16 120 us (6.9 TB/s; rows of 50257 the same;
-// with lists of 64 139, their entries written behind the rest).
+// HBM-bound: 4096 x 50304 bfloat16 121 us (rows of 50257 the same; with lists of
+// 64 138 to 141, their entries written behind the rest).  That is 6.8 TB/s of
+// logits and gradient, above the copy rate: a part of either is still in L2 from
+// the call before, or stays there.
 constexpr int kBwdThreads = 256;
 constexpr int kBwdVecs = 4;  // vectors of a thread
 template <int DT, bool LIST>
@@ -972,9 +976,10 @@ __global__ void __launch_bounds__(kBwdThreads) k_loss_bwd_rows(const Bwd p, unsi
 // of a tile's row share RP rows: lane i works out the i-th one's factors (and
 // which of the tile's columns are listed) while the tile's loads are in flight,
 // and passes them on by shuffles; no barrier before the column maxima.  4096 x
-// 50304 bfloat16 210 us (3.9 TB/s of logits read and codes written), with lists
-// 311, 2048 x 50304 float32 115; half of the issue slots busy, two CTAs of 16
-// warps an SM between two barriers.
+// 50304 bfloat16 211 us (3.9 TB/s of logits read and codes written), with lists
+// 302 (each tile row searches its list anew), rows of 50257 294 and 385 (element
+// loads), 2048 x 50304 float32 116 and 173.  65 % of the issue slots are busy, two
+// CTAs of 16 warps an SM between two barriers.
 enum { kToken = 0, kTokenEntropy = 1, kListed = 2 };
 
 template <int DT, int KIND, int OUT>

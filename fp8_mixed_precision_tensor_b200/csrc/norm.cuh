@@ -33,7 +33,14 @@ namespace norm {
 constexpr int kThreads = 256;      // of a CTA, but for the widest rows
 constexpr int kMostThreads = 512;
 constexpr int kMostWarps = kMostThreads / 32;
-constexpr int kStagedCols = 12288;  // the widest staged rows: 384 threads, 168 registers each
+// The widest staged rows: 384 threads, 168 registers each.  The parameters stand
+// beside the staged row as 4 bytes a column each, and where both do not fit the
+// row is read directly.  Of 16 bits: forward with both norms' biases from 11265
+// columns on (10241 with a binary32 residual), backward with a binary32 residual
+// and a gate or post norm from 11265; of binary32: forward with both biases from
+// 9217, with one and a gate or post norm from 11265, backward from 11265 (9217
+// with a gate or post norm).
+constexpr int kStagedCols = 12288;
 // How wide a row is: CK = 1 and 2, so many groups of eight columns a thread in
 // CTAs of 256; 3, two of them in 512 threads (8192 columns; as four in 256
 // threads, 8 warps an SM, 2048 rows took 51 and 150 us for 47 and 91); 4, four of
@@ -53,6 +60,12 @@ constexpr int kWidth = RT == FP8_DT_F32 ? 4 : 8;  // CW
 //   kDirect  rows that start anywhere: the lanes of a warp take neighbouring
 //            columns, and element by element from memory, twice where two
 //            passes need them
+//            (and rows too wide to be staged).  No row is in flight while another
+//            is worked on, and above 2048 columns a thread takes 32 of them, also
+//            those behind the row's end: 4096 rows of 2051, 4099 and 8195
+//            bfloat16, an RMS norm, 122, 212 and 372 us forward, 240, 486 and 749
+//            backward; of 16384 447 and 895; of 12288 backward with a binary32
+//            residual, both norms and a gate 1.7 ms, spilling 1.1 KB a thread.
 enum { kStaged = 0, kDirect = 1 };
 
 // The chunk v of a thread, and whether it lies in the row (kStaged: all of it).
@@ -606,10 +619,11 @@ __host__ __device__ inline FwdSmem fwd_smem(int columns, bool h, bool w, bool b,
 
 // One pass: h and r read, r' and x written.  A row's chunks stay in registers
 // between its exchanges; the next row's are on their way into shared memory.
-// 8192 x 12288 bfloat16, layer norm 128 us (6.3 TB/s; codes of the rows 187);
+// 8192 x 12288 bfloat16, layer norm 129 us (6.2 TB/s; codes of the rows 189: one
+// CTA of 12 warps hides a row's four rounds of shuffles and encoding alone);
 // 4096 x 4096 bfloat16 22 (6.0), with a float32 residual, both norms and a gate
-// 40 (5.1), there bound by the latency of copies, shared memory and shuffles at
-// 24 warps an SM (47 % of the issue slots busy); one token 3.1.
+// 40 (5.0; codes 47), there bound by the latency of copies, shared memory and
+// shuffles at 24 warps an SM (47 % of the issue slots busy); one token 3.1.
 //
 // FULL: h, r', both norms' w, and x in its type (1) or as codes of its rows (2),
 // the common calls, with little left to ask for each chunk; POST: whether there
@@ -782,8 +796,9 @@ __global__ void __launch_bounds__(kCtaThreads<CK, MODE>, CK >= 3 ? 1 : 3) k_norm
 
 // x again from r' and its statistics, as codes of 128x1 blocks: tiles of
 // block_scale.cuh.  2 B (or 4) read and 1 written per element: 8192 x 12288
-// bfloat16 86 us (3.5 TB/s), 4096 x 4096 16; as k_block_cast two barriers a tile,
-// which two CTAs of 16 warps hide in part.
+// bfloat16 85 us (3.5 TB/s), 4096 x 4096 16, with a float32 residual 22; as
+// k_block_cast two barriers a tile, which two CTAs of 16 warps hide in part
+// (63 % of the issue slots busy).
 struct Cols {
   const void *r;
   size_t ldr;
@@ -935,10 +950,12 @@ __device__ __forceinline__ void flush(float (&a)[CW], uint8_t *comb, float *out,
 }
 
 // dx, dr', r' and h read, dr and dh written: 8192 x 12288 bfloat16 278 us without
-// the parameters' gradients (4.4 TB/s) and 286 with, 4096 x 4096 with a float32
-// residual and both norms 59 and 68 (5.1 TB/s).  Bound by the copies of one row
-// in flight beside 12 to 16 warps: the sums over rows take the registers, and the
-// staged row with the parameters the shared memory, that a second row would need.
+// the parameters' gradients (4.4 TB/s) and 286 to 292 with, 4096 x 4096 with a
+// float32 residual and both norms 59 and 69 (5.1 TB/s), 2048 x 8192 91.  Bound by
+// the copies of one row in flight beside 12 to 16 warps.  Registers: a thread
+// holds all four sums of its columns whether they are wanted or not (A and C are
+// asked for at run time, F is there at CK >= 3); of 12288 columns they take 128 of
+// 168, and without a gate and a post norm 64 of these stay 0 while 248 bytes spill.
 //
 // BIAS: whether sums of dx and of G are wanted (gradients of b, of post_b, and
 // of a gate behind post_b).  FULL: dx, dr', h, both outputs and the post norm's

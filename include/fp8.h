@@ -738,7 +738,9 @@ typedef struct {
  * the forward pass's h, r' and stats:  dh (of dtype), dr (of res_dtype) and the
  * parameters' gradients, each wanted or NULL.  dh may be dx or h, dr may be
  * dr_out (the same pointer and row stride).  workspace: dev, 16-byte aligned,
- * fp8_norm_workspace_bytes(rows, cols, gate_rows) bytes, contents of no
+ * fp8_norm_workspace_bytes(rows, cols, gate_rows) bytes (two binary32 rows for
+ * each of some 300 shares of the rows, and for each gate row: a gate row for every
+ * row of the matrix asks for twice the matrix in binary32), contents of no
  * meaning before and after (needed where a parameter's gradient is wanted);
  * calls whose work overlaps on the GPU need one each.  rows == 0 gives
  * gradients of 0 for the parameters, the grads' `gates` rows of gate among them.
