@@ -260,8 +260,8 @@ class BlockNorm:
         of = r if h is None else h
         if dtype is None:
             dtype = of.dtype
-        elif dtype != of.dtype and not (h is None and r.dtype is torch.float32):
-            raise ValueError(f"dtype {dtype}: x has h's, or beside a float32 residual without h another")
+        elif dtype != of.dtype and not (h is None and r.dtype is torch.float32 and dtype in (torch.bfloat16, torch.float16)):
+            raise ValueError(f"dtype {dtype}: x has h's, or beside a float32 residual without h a 16-bit one")
         with _on(stream, *(t for t in (h, r) if t is not None)):
             if stream is not None:
                 self._in_use()

@@ -81,7 +81,7 @@ def test_the_first_norm_of_a_float32_residual_writes_for_16_bit_layers():
     assert none is None and torch.equal(dr, d) and grads["w"].dtype is BF16
 
 
-@pytest.mark.parametrize("h,r,dtype", [(BF16, F32, F32), (BF16, BF16, F32), (None, BF16, F32), (None, BF16, F16)])
+@pytest.mark.parametrize("h,r,dtype", [(BF16, F32, F32), (BF16, BF16, F32), (None, BF16, F32), (None, BF16, F16), (None, F32, torch.float64)])
 def test_a_norm_gives_x_in_no_other_type(h, r, dtype):
     e = lambda t: None if t is None else torch.zeros(2, 8, device="cuda", dtype=t)  # noqa: E731
     with pytest.raises(ValueError, match="dtype"):
